@@ -185,6 +185,13 @@ typedef uint16_t gdn_bf16; /* bfloat16 bit pattern */
 #define GDN_STATUS_BAD_ROW 4u  /* gdn_move_rows got a row index outside its
                                   cohort; that pair was not copied */
 
+#define GDN_STATUS_NO_PAGES 8u /* gdn_kv_plan found no page, or no place for
+                                  its tokens, for a row */
+#define GDN_STATUS_BAD_INDEX 16u /* a cache call met a page, slot or position
+                                  outside its bounds; it was skipped */
+#define GDN_STATUS_BAD_LEN 32u /* a cache call met a row whose length, pages or
+                                  new tokens are outside their bounds */
+
 #define GDN_MAX_LAYERS 256     /* layers one gdn_commit call may group */
 
 typedef struct gdn_dims {
@@ -445,6 +452,147 @@ int gdn_move_rows(const gdn_dims *src_dims, const gdn_dims *dst_dims, int mode, 
 size_t gdn_accept_workspace_bytes(int B, int T, int V);
 int gdn_accept_greedy(int B, int T, int V, const gdn_bf16 *logits, const int32_t *draft, const uint8_t *active,
                       int32_t *keep, int32_t *next, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- a paged 4-bit key/value cache for the attention layers --------------------
+ * The hybrid models of the three pages have attention layers next to the GDN
+ * layers, with a KV cache that is trimmed on rewind ("perf(qwen): full-context
+ * MTP draft prefill and replay-free rewind", Summary; "Add request-owned
+ * eight-way MTP serving for Qwen 35B", section 2: a ragged physical cache with
+ * per-row committed offsets).  These calls keep such a cache for the same
+ * cohort: its lengths are the committed `offsets` that gdn_commit advances, so
+ * a rejected draft needs no call at all; the next cycle's plan gives its pages
+ * back or reuses them.  One cycle of an attention layer:
+ *   gdn_kv_plan (once for all layers) -> gdn_kv4_append -> gdn_kv4_attend
+ *
+ * Cache of one layer: uint8 [n_pages][H_kv][record], a page holds `page`
+ * tokens, and a head's record in it is
+ *   K codes [page][d/2] | V codes [page][d/2]
+ *   | K entries [page][d/64][2] fp16 | V entries [page][d/64][2] fp16
+ * Byte i of a token's codes holds channel 2i (low four bits) and 2i+1.  Channel
+ * c belongs to group (c / 8) mod (d / 64) of its token and stands for
+ * base + step * code, with the group's entry (step, base).
+ * Slot s is place s mod page of page s / page.  Supported: d in {64, 128, 256},
+ * page in {16, 32, 64}, H_q a multiple of H_kv with H_q / H_kv <= 64,
+ * B <= 65535, max_pages <= 2^20, n_pages * page < 2^31.
+ */
+typedef struct gdn_kv4_dims {
+  int32_t B;         /* rows */
+  int32_t H_q;       /* query heads, a multiple of H_kv */
+  int32_t H_kv;      /* key/value heads; query head h reads head h * H_kv / H_q */
+  int32_t d;         /* head size */
+  int32_t page;      /* tokens per page */
+  int32_t max_pages; /* columns of the block table: a row holds max_pages * page tokens at most */
+  int32_t n_pages;   /* pages of the cache */
+} gdn_kv4_dims;
+
+#define GDN_ROPE_HALF 0  /* a pair is channels (i, i + rot/2) */
+#define GDN_ROPE_PAIRS 1 /* a pair is channels (2i, 2i+1) */
+
+/*
+ * Bytes of one page (all kv heads) of one layer's cache; 0 for invalid
+ * dimensions.  (The pages describe no such call.)
+ */
+size_t gdn_kv4_page_bytes(const gdn_kv4_dims *dims);
+
+/*
+ * Block tables, slots and positions of a cycle's new tokens, from the rows'
+ * committed lengths ("Add request-owned eight-way MTP serving for Qwen 35B",
+ * section 2: per-row committed offsets over a ragged physical cache).  Row b
+ * gets a_b = active[b] ? max(add[b], 0) : 0 new tokens at positions
+ * lens[b] .. lens[b] + a_b - 1 and holds ceil((lens[b] + a_b) / page) pages
+ * afterwards:
+ *  1. rows that hold more give their last pages back: pushed on the free
+ *     stack in row order, each row's in column order; their table cells get -1;
+ *  2. rows that hold fewer take pages from the stack's end, in row order.  The
+ *     first row that does not fit (too few pages, or in the packed layout no
+ *     place for its tokens among the N) and every row after it that adds
+ *     tokens or needs pages gets none (a_b = 0, GDN_STATUS_NO_PAGES).
+ * A finished row is one with lens = 0 and add = 0: all its pages go back.  A
+ * row with a negative length, with more pages than max_pages, or with a_b > T
+ * in the fixed layout keeps what it holds and gets no tokens
+ * (GDN_STATUS_BAD_LEN).
+ *  T          > 0: row b's tokens stand at b*T (the layout of gdn_conv_verify;
+ *             N >= B*T); 0: packed one row after the other
+ *  lens, add  [B] int32 (lens is typically `offsets`); active [B] uint8
+ *  held       [B] int32 in/out, pages the row holds
+ *  table      [B][max_pages] int32 in/out, the row's pages in order
+ *  free_list  [n_pages] int32 in/out, free_count [1] int32 in/out: the stack
+ *  q_start    [B+1] int32 out, first token of each row; q_count [B] int32 out, a_b
+ *  kv_len     [B] int32 out, lens[b] + a_b
+ *  slots, positions  [N] int32 out; -1 where no row has the token
+ * B = 0 writes nothing.  The result is the same on every run.
+ */
+int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, const int32_t *add,
+                const uint8_t *active, int32_t *held, int32_t *table, int32_t *free_list, int32_t *free_count,
+                int32_t *q_start, int32_t *q_count, int32_t *kv_len, int32_t *slots, int32_t *positions,
+                void *stream);
+
+/*
+ * Rotate q and k by positions of several axes and write k and v into the cache
+ * at their slots.  (The pages describe no such call; the attention layers of
+ * the models they serve need it.)  Pair i < rot/2 of a token n turns by the
+ * angle whose cosine and sine stand in rope[positions[axis[i]][n]][i]; build
+ * the table in 64 bits and round it once.  The channels from rot on are kept.
+ * Codes are formed from the rotated fp32 keys: per group base = fp16(min), step =
+ * fp16((max - min) / 15), code = clamp(round((y - base) / step), 0, 15).
+ * Magnitudes over 65504 are held there; a group with an infinity or NaN reads
+ * back as NaN.
+ *  q, k, v    bf16, token n at n * stride elements (stride a multiple of 8, at
+ *             least heads * d), its heads densely packed: slices of one fused
+ *             projection serve
+ *  positions  [n_axes][N] int32 in [0, max_pos)
+ *  rope       [max_pos][rot/2][2] fp32 (cos, sin); not read if rot = 0
+ *  axis       HOST array [rot/2], the axis of each pair, < n_axes
+ *  slots      [N] int32; a token with a negative slot is rotated, not cached
+ *  q_out      [N][H_q][d] bf16 (may be q itself where q is dense)
+ * rot: a multiple of 16, 0 <= rot <= d; style GDN_ROPE_HALF or GDN_ROPE_PAIRS.
+ * A token with a slot or, where its slot is not negative, a position outside
+ * the bounds is not cached and such a position does not turn (GDN_STATUS_BAD_INDEX).
+ * Two tokens with one slot race.
+ */
+int gdn_kv4_append(const gdn_kv4_dims *dims, int N, const gdn_bf16 *q, long long q_stride, const gdn_bf16 *k,
+                   long long k_stride, const gdn_bf16 *v, long long v_stride, const int32_t *positions, int n_axes,
+                   const float *rope, int max_pos, int rot, const uint8_t *axis, int style, const int32_t *slots,
+                   void *pages, gdn_bf16 *q_out, void *stream);
+
+/*
+ * The keys and values that the cache stands for at the given slots, rounded
+ * once to bf16: k, v [N][H_kv][d]; zeros for a negative slot or one outside
+ * the cache (GDN_STATUS_BAD_INDEX).  (The pages describe no such call; it
+ * serves moves to a cache of another kind, and checks.)
+ */
+int gdn_kv4_read(const gdn_kv4_dims *dims, int N, const int32_t *slots, const void *pages, gdn_bf16 *k,
+                 gdn_bf16 *v, void *stream);
+
+/*
+ * Bytes of workspace gdn_kv4_attend needs for N tokens with at most max_q a
+ * row; 0 for invalid arguments.  (The pages describe no such call.)
+ */
+size_t gdn_kv4_attend_workspace_bytes(const gdn_kv4_dims *dims, int N, int max_q);
+
+/*
+ * Causal attention of the new tokens over the cache (the attention layers of
+ * "perf(qwen): full-context MTP draft prefill and replay-free rewind",
+ * Summary: their cache is trimmed on rewind, here by kv_len).  Query i of row b
+ * is token q_start[b] + i, i < q_count[b]; it sits at position
+ * kv_len[b] - q_count[b] + i and sees every cached key at its own position or
+ * before it: o = sum_t softmax_t(scale * q . k_t) v_t.  Tokens of a row's span
+ * [q_start[b], q_start[b+1]) from q_count[b] on, and queries that see no key,
+ * get zeros; tokens in no span are not written.  Keys behind a query's
+ * position and places that no row holds are never used, whatever they hold.
+ *  q, out     [N][H_q][d] bf16 (rotated queries; out may not overlap q)
+ *  table, q_start, q_count, kv_len  as gdn_kv_plan leaves them
+ *  max_q      the largest span of a row (the host's bound; 1 for plain decoding)
+ *  ws         gdn_kv4_attend_workspace_bytes, 256-byte aligned, zero-filled
+ *             once before its first use (each call leaves it ready for the
+ *             next); one call at a time may use it
+ * A row with kv_len outside [0, max_pages * page] is cut to that range, a span
+ * longer than max_q to max_q (GDN_STATUS_BAD_LEN); a page outside the cache
+ * leaves that row's outputs unspecified (GDN_STATUS_BAD_INDEX).
+ */
+int gdn_kv4_attend(const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages,
+                   const int32_t *table, const int32_t *q_start, const int32_t *q_count, const int32_t *kv_len,
+                   float scale, gdn_bf16 *out, void *ws, size_t ws_bytes, void *stream);
 
 /* ---- test hook ---------------------------------------------------------------
  * gdn_conv_verify at d = 128 (RECOMPUTE or DEFERRED) with its failure path

@@ -19,6 +19,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "gdn_common.cuh"
+#include "kv4.cuh"
 
 using namespace gdn;
 
@@ -479,6 +480,195 @@ __attribute__((visibility("default"))) int gdn_move_rows(
   if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   cudaError_t e = launch_move_rows(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gdn_move_rows launch");
+  return ok();
+}
+
+// ---- paged 4-bit key/value cache ---------------------------------------------
+namespace {
+
+constexpr int kMaxCacheTokens = 1 << 24;  // tokens of one call
+
+int check_kv4(const gdn_kv4_dims *d) {
+  if (!d) return fail(GDN_ERR_INVALID_ARG, "dims is NULL");
+  if (d->B < 0 || d->B > 65535) return fail(GDN_ERR_UNSUPPORTED, "B=%d outside [0, 65535]", d->B);
+  if (d->H_kv < 1 || d->H_q < 1 || d->H_q % d->H_kv != 0 || d->H_q / d->H_kv > 64 || d->H_q > 65535)
+    return fail(GDN_ERR_UNSUPPORTED, "need H_q (%d) a multiple of H_kv (%d), at most 64 times it and at most 65535",
+                d->H_q, d->H_kv);
+  if (d->d != 64 && d->d != 128 && d->d != 256)
+    return fail(GDN_ERR_UNSUPPORTED, "need d in {64, 128, 256} (got %d)", d->d);
+  if (d->page != 16 && d->page != 32 && d->page != 64)
+    return fail(GDN_ERR_UNSUPPORTED, "need page in {16, 32, 64} (got %d)", d->page);
+  if (d->max_pages < 1 || d->max_pages > (1 << 20))
+    return fail(GDN_ERR_UNSUPPORTED, "max_pages=%d outside [1, 2^20]", d->max_pages);
+  if (d->n_pages < 1 || (long long)d->n_pages * d->page >= (1LL << 31))
+    return fail(GDN_ERR_UNSUPPORTED, "need n_pages (%d) >= 1 and n_pages * page < 2^31", d->n_pages);
+  return GDN_OK;
+}
+
+int check_tokens(int N) {
+  if (N < 0 || N > kMaxCacheTokens) return fail(GDN_ERR_UNSUPPORTED, "N=%d outside [0, %d]", N, kMaxCacheTokens);
+  return GDN_OK;
+}
+
+int log2_page(const gdn_kv4_dims *d) { return d->page == 16 ? 4 : d->page == 32 ? 5 : 6; }
+
+Kv4Geom geom_of(const gdn_kv4_dims *d) {
+  return Kv4Geom{d->B, d->H_q, d->H_kv, d->d, log2_page(d), d->max_pages, d->n_pages};
+}
+
+}  // namespace
+
+__attribute__((visibility("default"))) size_t gdn_kv4_page_bytes(const gdn_kv4_dims *dims) {
+  if (check_kv4(dims) != GDN_OK) return 0;
+  return size_t(dims->H_kv) * kv4_record_bytes(dims->d, dims->page);
+}
+
+__attribute__((visibility("default"))) int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens,
+                                                       const int32_t *add, const uint8_t *active, int32_t *held,
+                                                       int32_t *table, int32_t *free_list, int32_t *free_count,
+                                                       int32_t *q_start, int32_t *q_count, int32_t *kv_len,
+                                                       int32_t *slots, int32_t *positions, void *stream) {
+  NvtxRange range("gdn_kv_plan");
+  int rc = check_kv4(dims);
+  if (rc) return rc;
+  if ((rc = check_tokens(N))) return rc;
+  if (T < 0 || (T > 0 && (long long)dims->B * T > N))
+    return fail(GDN_ERR_INVALID_ARG, "plan: need T >= 0 and, where T > 0, N (%d) >= B * T (%d * %d)", N, dims->B, T);
+  if (dims->B == 0) return ok();
+  GDN_NEED_PTR(lens, 4);
+  GDN_NEED_PTR(add, 4);
+  GDN_NEED_PTR(active, 1);
+  GDN_NEED_PTR(held, 4);
+  GDN_NEED_PTR(table, 4);
+  GDN_NEED_PTR(free_list, 4);
+  GDN_NEED_PTR(free_count, 4);
+  GDN_NEED_PTR(q_start, 4);
+  GDN_NEED_PTR(q_count, 4);
+  GDN_NEED_PTR(kv_len, 4);
+  if (N > 0) {
+    GDN_NEED_PTR(slots, 4);
+    GDN_NEED_PTR(positions, 4);
+  }
+  KvPlanParams p{};
+  p.lens = lens, p.add = add, p.active = active;
+  p.held = held, p.table = table, p.free_list = free_list, p.free_count = free_count;
+  p.q_start = q_start, p.q_count = q_count, p.kv_len = kv_len, p.slots = slots, p.positions = positions;
+  p.B = dims->B, p.T = T, p.N = N;
+  p.log2P = log2_page(dims), p.max_pages = dims->max_pages, p.n_pages = dims->n_pages;
+  p.status = status_word_address();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  cudaError_t e = launch_kv_plan(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv_plan launch");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int gdn_kv4_append(
+    const gdn_kv4_dims *dims, int N, const gdn_bf16 *q, long long q_stride, const gdn_bf16 *k, long long k_stride,
+    const gdn_bf16 *v, long long v_stride, const int32_t *positions, int n_axes, const float *rope, int max_pos,
+    int rot, const uint8_t *axis, int style, const int32_t *slots, void *pages, gdn_bf16 *q_out, void *stream) {
+  NvtxRange range("gdn_kv4_append");
+  int rc = check_kv4(dims);
+  if (rc) return rc;
+  if ((rc = check_tokens(N))) return rc;
+  if (rot < 0 || rot > dims->d || rot % 16 != 0)
+    return fail(GDN_ERR_UNSUPPORTED, "append: need rot (%d) a multiple of 16 in [0, d]", rot);
+  if (style != GDN_ROPE_HALF && style != GDN_ROPE_PAIRS)
+    return fail(GDN_ERR_INVALID_ARG, "append: style must be GDN_ROPE_HALF or GDN_ROPE_PAIRS (got %d)", style);
+  const long long wq = (long long)dims->H_q * dims->d, wk = (long long)dims->H_kv * dims->d;
+  if (q_stride < wq || k_stride < wk || v_stride < wk || q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return fail(GDN_ERR_INVALID_ARG,
+                "append: token strides (%lld, %lld, %lld) must be multiples of 8 and at least heads * d", q_stride,
+                k_stride, v_stride);
+  if (N == 0) return ok();
+  GDN_NEED_PTR(q, 16);
+  GDN_NEED_PTR(k, 16);
+  GDN_NEED_PTR(v, 16);
+  GDN_NEED_PTR(slots, 4);
+  GDN_NEED_PTR(pages, 16);
+  GDN_NEED_PTR(q_out, 16);
+  Kv4AppendParams p{};
+  if (rot > 0) {
+    GDN_NEED_PTR(positions, 4);
+    GDN_NEED_PTR(rope, 8);
+    if (!axis) return fail(GDN_ERR_INVALID_ARG, "axis is NULL");
+    if (n_axes < 1 || max_pos < 1)
+      return fail(GDN_ERR_INVALID_ARG, "append: n_axes=%d and max_pos=%d must be positive", n_axes, max_pos);
+    for (int i = 0; i < rot / 2; ++i) {
+      if (axis[i] >= n_axes)
+        return fail(GDN_ERR_INVALID_ARG, "append: axis[%d]=%d outside [0, %d)", i, int(axis[i]), n_axes);
+      p.axis[i] = axis[i];
+    }
+  }
+  p.q = q, p.k = k, p.v = v, p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
+  p.positions = positions, p.rope = reinterpret_cast<const float2 *>(rope), p.slots = slots;
+  p.pages = static_cast<uint8_t *>(pages), p.q_out = q_out;
+  p.N = N, p.H_q = dims->H_q, p.H_kv = dims->H_kv, p.rot = rot, p.max_pos = max_pos, p.n_axes = n_axes;
+  p.pairs = style == GDN_ROPE_PAIRS;
+  p.log2P = log2_page(dims), p.n_pages = dims->n_pages;
+  p.status = status_word_address();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  cudaError_t e = launch_kv4_append(p, dims->d, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv4_append launch");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int gdn_kv4_read(const gdn_kv4_dims *dims, int N, const int32_t *slots,
+                                                        const void *pages, gdn_bf16 *k, gdn_bf16 *v, void *stream) {
+  NvtxRange range("gdn_kv4_read");
+  int rc = check_kv4(dims);
+  if (rc) return rc;
+  if ((rc = check_tokens(N))) return rc;
+  if (N == 0) return ok();
+  GDN_NEED_PTR(slots, 4);
+  GDN_NEED_PTR(pages, 16);
+  GDN_NEED_PTR(k, 16);
+  GDN_NEED_PTR(v, 16);
+  Kv4ReadParams p{};
+  p.slots = slots, p.pages = static_cast<const uint8_t *>(pages), p.k = k, p.v = v;
+  p.N = N, p.H_kv = dims->H_kv, p.log2P = log2_page(dims), p.n_pages = dims->n_pages;
+  p.status = status_word_address();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  cudaError_t e = launch_kv4_read(p, dims->d, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv4_read launch");
+  return ok();
+}
+
+__attribute__((visibility("default"))) size_t gdn_kv4_attend_workspace_bytes(const gdn_kv4_dims *dims, int N,
+                                                                             int max_q) {
+  if (check_kv4(dims) != GDN_OK || check_tokens(N) != GDN_OK || max_q < 1 || max_q > kMaxPrefillLen) return 0;
+  return kv4_attend_workspace_bytes(geom_of(dims), N, max_q);
+}
+
+__attribute__((visibility("default"))) int gdn_kv4_attend(
+    const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages, const int32_t *table,
+    const int32_t *q_start, const int32_t *q_count, const int32_t *kv_len, float scale, gdn_bf16 *out, void *ws,
+    size_t ws_bytes, void *stream) {
+  NvtxRange range("gdn_kv4_attend");
+  int rc = check_kv4(dims);
+  if (rc) return rc;
+  if ((rc = check_tokens(N))) return rc;
+  if (max_q < 1 || max_q > kMaxPrefillLen)
+    return fail(GDN_ERR_UNSUPPORTED, "attend: max_q=%d outside [1, %d]", max_q, kMaxPrefillLen);
+  if (!std::isfinite(scale)) return fail(GDN_ERR_INVALID_ARG, "attend: scale must be finite");
+  if (dims->B == 0 || N == 0) return ok();
+  GDN_NEED_PTR(q, 16);
+  GDN_NEED_PTR(pages, 16);
+  GDN_NEED_PTR(table, 4);
+  GDN_NEED_PTR(q_start, 4);
+  GDN_NEED_PTR(q_count, 4);
+  GDN_NEED_PTR(kv_len, 4);
+  GDN_NEED_PTR(out, 16);
+  GDN_NEED_PTR(ws, 256);
+  const size_t need = kv4_attend_workspace_bytes(geom_of(dims), N, max_q);
+  if (ws_bytes < need) return fail(GDN_ERR_WORKSPACE, "attend workspace has %zu bytes, needs %zu", ws_bytes, need);
+  Kv4AttendParams p{};
+  p.q = q, p.pages = static_cast<const uint8_t *>(pages), p.table = table;
+  p.q_start = q_start, p.q_count = q_count, p.kv_len = kv_len, p.out = out, p.ws = ws;
+  p.scale = scale, p.N = N, p.max_q = max_q, p.g = geom_of(dims);
+  p.status = status_word_address();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  cudaError_t e = launch_kv4_attend(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv4_attend launch");
   return ok();
 }
 

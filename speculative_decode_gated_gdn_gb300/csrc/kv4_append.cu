@@ -1,0 +1,270 @@
+// kv4_append.cu -- rotary positions with several axes on q and k, and k and v
+// into the paged 4-bit cache; and the cache's tokens back in bf16.
+//
+// Rotation: pair i of a token turns by the angle whose (cos, sin) the caller's
+// fp32 table holds at [positions[axis[i]]][i].  The table, and not an angle
+// formed here, keeps far positions exact: an fp32 product pos * frequency is
+// off by 0.06 rad at a million.  Products and sums are rounded one by one
+// (no fused multiply-add), so that a value next to a border between two codes
+// falls on the side the plain formula puts it.
+//
+// Quantisation, per token, head and group of 64 channels (kv4.cuh):
+//   base = fp16(min), step = fp16((max - min) / 15)
+//   code = clamp(round_half_even((y - base) / step), 0, 15), 0 where step is 0
+// from the fp32 rotated value; min, max and the step are exact or rounded once
+// in fp32 before fp16.  A group that holds an infinity or NaN reads back as
+// NaN; magnitudes over 65504 are held at 65504.
+//
+// Both kernels move each byte once and are bound by HBM: 8 channels a lane
+// (16 bytes of bf16, one 32-bit word of codes), a head on D / 8 lanes, the
+// loads of several heads in flight per lane.
+#include <cuda_fp16.h>
+
+#include "kv4.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr float kHalfMax = 65504.f;
+
+__device__ __forceinline__ uint4 ld_stream_u4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Quantise the lane's 8 channels with the 8 lanes of its group (lanes equal
+// modulo W within the head) and write codes and, from the group's first lane,
+// the entry.
+template <int D>
+__device__ __forceinline__ void store_codes(const float (&y)[8], uint8_t *codes, uint8_t *entries, int chunk, bool store) {
+  constexpr int W = D / 64;
+  float mn = y[0], mx = y[0];
+  bool fine = fabsf(y[0]) <= 3.402823466e38f;
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    mn = fminf(mn, y[e]), mx = fmaxf(mx, y[e]);
+    fine = fine && fabsf(y[e]) <= 3.402823466e38f;
+  }
+  int ok = fine;
+#pragma unroll
+  for (int o = W; o < 8 * W; o <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    ok &= __shfl_xor_sync(0xffffffffu, ok, o);
+  }
+  __half base = __float2half_rn(fminf(fmaxf(mn, -kHalfMax), kHalfMax));
+  __half step = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(mx, mn), 15.f), kHalfMax));
+  if (!ok) base = step = __ushort_as_half(0x7e00);
+  const float b = __half2float(base), s = __half2float(step);
+  uint32_t word = 0;
+  if (ok && s > 0.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(y[e], b), s)), 0.f), 15.f);
+      word |= uint32_t(c) << (4 * e);
+    }
+  }
+  if (!store) return;
+  reinterpret_cast<uint32_t *>(codes)[chunk] = word;
+  if (chunk < W)
+    reinterpret_cast<uint32_t *>(entries)[chunk] = uint32_t(__half_as_ushort(step)) | uint32_t(__half_as_ushort(base)) << 16;
+}
+
+// One token a warp sub-group: D / 8 lanes hold a head, the warp's 32 / (D / 8)
+// heads at a time; blockIdx.y splits the heads of a token where tokens are few.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4AppendParams p, const int splits) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH, W = D / 64;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunk = lane % LPH, sub = lane / LPH;
+  const int n = blockIdx.x * (kAppendThreads / 32) + warp;
+  pdl_wait();
+  pdl_trigger();
+  if (n >= p.N) return;  // whole warps
+  const int P = 1 << p.log2P;
+  const int slot = p.slots[n];
+  bool write = slot >= 0;
+  if (write && (slot >> p.log2P) >= p.n_pages) {
+    write = false;
+    if (lane == 0) atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+  }
+  // the lane's angles: it holds channels [8 chunk, 8 chunk + 8)
+  const int half = p.rot >> 1;
+  const bool turned = 8 * chunk < p.rot;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = 1.f, sn[e] = 0.f;
+    if (turned) {
+      const int c = 8 * chunk + e;
+      const int i = p.pairs ? c >> 1 : (c < half ? c : c - half);
+      const int pos = p.positions[size_t(p.axis[i]) * p.N + n];
+      if (pos >= 0 && pos < p.max_pos) {
+        const float2 t = __ldg(p.rope + size_t(pos) * half + i);
+        cs[e] = t.x, sn[e] = t.y;
+      } else if (slot >= 0) {
+        write = false;
+        atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+      }
+    }
+  }
+  write = __all_sync(0xffffffffu, write);
+  const int page = write ? slot >> p.log2P : 0, off = write ? slot & (P - 1) : 0;
+  const int heads = p.H_q + 2 * p.H_kv;
+  const int per = (heads + splits - 1) / splits;
+  const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
+  const int partner = lane + (p.pairs || !turned ? 0 : (8 * chunk < half ? half / 8 : -half / 8));
+  const float sign = 8 * chunk < half ? -1.f : 1.f;
+  for (int hb = h0; hb < h1; hb += HPW) {
+    const int h = hb + sub;
+    const bool in = h < h1;
+    const int kind = h < p.H_q ? 0 : h < p.H_q + p.H_kv ? 1 : 2;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (in) {
+      const uint16_t *src = kind == 0   ? p.q + n * p.q_stride + size_t(h) * D
+                            : kind == 1 ? p.k + n * p.k_stride + size_t(h - p.H_q) * D
+                                        : p.v + n * p.v_stride + size_t(h - p.H_q - p.H_kv) * D;
+      raw = ld_stream_u4(src + 8 * chunk);
+    }
+    float y[8];
+    unpack8(raw, y);
+    if (p.rot) {  // every lane takes part in the exchange
+      if (p.pairs) {
+        if (turned && kind < 2) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float a = y[e], b = y[e + 1];
+            y[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+            y[e + 1] = __fadd_rn(__fmul_rn(b, cs[e + 1]), __fmul_rn(a, sn[e + 1]));
+          }
+        }
+      } else {
+        uint4 o;
+        o.x = __shfl_sync(0xffffffffu, raw.x, partner);
+        o.y = __shfl_sync(0xffffffffu, raw.y, partner);
+        o.z = __shfl_sync(0xffffffffu, raw.z, partner);
+        o.w = __shfl_sync(0xffffffffu, raw.w, partner);
+        if (turned && kind < 2) {
+          float z[8];
+          unpack8(o, z);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), sign * __fmul_rn(z[e], sn[e]));
+        }
+      }
+    }
+    if (in && kind == 0)
+      *reinterpret_cast<uint4 *>(p.q_out + (size_t(n) * p.H_q + h) * D + 8 * chunk) = pack8(y);
+    // the groups' exchanges need every lane of a head, so the whole warp goes in
+    if (__any_sync(0xffffffffu, in && kind > 0)) {
+      const int hk = kind == 1 ? h - p.H_q : h - p.H_q - p.H_kv;
+      const bool store = in && kind > 0 && write;
+      uint8_t *rec = p.pages + (size_t(page) * p.H_kv + (store ? hk : 0)) * kv4_record_bytes(D, P);
+      const int w = kind == 2;
+      store_codes<D>(y, rec + w * kv4_code_bytes(D, P) + off * (D / 2),
+                     rec + 2 * kv4_code_bytes(D, P) + w * kv4_entry_bytes(D, P) + off * (W * 4), chunk, store);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(const Kv4ReadParams p) {
+  constexpr int LPH = D / 8, W = D / 64;
+  pdl_wait();
+  pdl_trigger();
+  const long long item = (blockIdx.x * (long long)kAppendThreads + threadIdx.x) / LPH;  // (token, head, K or V)
+  const int chunk = threadIdx.x % LPH;
+  const long long th = item >> 1;
+  if (th >= (long long)p.N * p.H_kv) return;
+  const int w = int(item & 1), n = int(th / p.H_kv), h = int(th % p.H_kv);
+  const int P = 1 << p.log2P;
+  const int slot = p.slots[n];
+  bool in = slot >= 0;
+  if (in && (slot >> p.log2P) >= p.n_pages) {
+    in = false;
+    atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+  }
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = 0.f;
+  if (in) {
+    const int off = slot & (P - 1);
+    const uint8_t *rec = p.pages + (size_t(slot >> p.log2P) * p.H_kv + h) * kv4_record_bytes(D, P);
+    const uint32_t word = *reinterpret_cast<const uint32_t *>(rec + w * kv4_code_bytes(D, P) + off * (D / 2) + 4 * chunk);
+    const uint32_t entry = *reinterpret_cast<const uint32_t *>(rec + 2 * kv4_code_bytes(D, P) + w * kv4_entry_bytes(D, P) +
+                                                               (off * W + chunk % W) * 4);
+    const float s = __half2float(__ushort_as_half(uint16_t(entry))), b = __half2float(__ushort_as_half(uint16_t(entry >> 16)));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(s, float((word >> (4 * e)) & 15u), b);  // s * code is exact in fp32
+  }
+  uint16_t *dst = (w ? p.v : p.k) + (size_t(n) * p.H_kv + h) * D + 8 * chunk;
+  *reinterpret_cast<uint4 *>(dst) = pack8(y);
+}
+
+template <int D>
+cudaError_t launch_append(const Kv4AppendParams &p, cudaStream_t s) {
+  // heads split until a few thousand warps are there, while each keeps a load
+  const int heads = p.H_q + 2 * p.H_kv, at_a_time = 32 / (D / 8);
+  int splits = 1;
+  while (splits < (heads + at_a_time - 1) / at_a_time && (long long)p.N * splits < 2432) splits *= 2;
+  if (splits > heads) splits = heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.N + kAppendThreads / 32 - 1) / (kAppendThreads / 32), splits);
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_append_kernel<D>, p, splits);
+}
+
+template <int D>
+cudaError_t launch_read(const Kv4ReadParams &p, cudaStream_t s) {
+  const long long threads = (long long)p.N * p.H_kv * 2 * (D / 8);
+  return launch_pdl(kv4_read_kernel<D>, dim3(unsigned((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const Kv4AppendParams &p, int D, cudaStream_t s) {
+  switch (D) {
+    case 64: return launch_append<64>(p, s);
+    case 128: return launch_append<128>(p, s);
+    default: return launch_append<256>(p, s);
+  }
+}
+
+cudaError_t launch_kv4_read(const Kv4ReadParams &p, int D, cudaStream_t s) {
+  switch (D) {
+    case 64: return launch_read<64>(p, s);
+    case 128: return launch_read<128>(p, s);
+    default: return launch_read<256>(p, s);
+  }
+}
+
+}  // namespace gdn

@@ -30,13 +30,19 @@ GDN_VERIFY_OVERLAP_STATE = 0x200
 GDN_STATUS_TIMEOUT = 2
 GDN_STATUS_BAD_KEEP = 1
 GDN_STATUS_BAD_ROW = 4
+GDN_STATUS_NO_PAGES = 8
+GDN_STATUS_BAD_INDEX = 16
+GDN_STATUS_BAD_LEN = 32
+GDN_ROPE_HALF = 0
+GDN_ROPE_PAIRS = 1
 GDN_MAX_LAYERS = 256
 GDN_NOALLOC_WS_BYTES = 4 << 20
 
 EXPORTS = ("gdn_version", "gdn_last_error", "gdn_layer_workspace_bytes", "gdn_conv_verify",
            "gdn_commit", "gdn_prefill_workspace_bytes", "gdn_prefill_chunked", "gdn_get_status",
            "gdn_conv_verify_noalloc", "gdn_flush", "gdn_accept_workspace_bytes", "gdn_accept_greedy",
-           "gdn_conv_verify_gated", "gdn_move_rows", "gdn_test_verify_timeout")
+           "gdn_conv_verify_gated", "gdn_move_rows", "gdn_kv4_page_bytes", "gdn_kv_plan", "gdn_kv4_append",
+           "gdn_kv4_read", "gdn_kv4_attend_workspace_bytes", "gdn_kv4_attend", "gdn_test_verify_timeout")
 
 
 class GdnError(RuntimeError):
@@ -58,6 +64,17 @@ def dims(B, T, H_k, H_v, d, T_max=None, width=4, act=GDN_ACT_SILU) -> gdn_dims:
 def dims_of(geom) -> gdn_dims:
     """gdn_dims from a synth.Geometry."""
     return dims(geom.B, geom.T, geom.H_k, geom.H_v, geom.d, geom.tmax, geom.width, geom.act)
+
+
+class gdn_kv4_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H_q", "H_kv", "d", "page", "max_pages", "n_pages")]
+
+
+def kv4_dims(B, H_q, H_kv, d, page, max_pages, n_pages) -> gdn_kv4_dims:
+    """gdn_kv4_dims of a paged 4-bit cache: B rows, H_q query heads over H_kv
+    key/value heads of size d, pages of `page` tokens, a block table of
+    max_pages columns, n_pages pages."""
+    return gdn_kv4_dims(B, H_q, H_kv, d, page, max_pages, n_pages)
 
 
 _P = ctypes.c_void_p
@@ -100,6 +117,19 @@ def _declare(lib):
     lib.gdn_accept_workspace_bytes.argtypes = [ctypes.c_int] * 3
     lib.gdn_accept_greedy.restype = ctypes.c_int
     lib.gdn_accept_greedy.argtypes = [ctypes.c_int] * 3 + [_P] * 6 + [ctypes.c_size_t, _P]
+    K, I, LL = ctypes.POINTER(gdn_kv4_dims), ctypes.c_int, ctypes.c_longlong
+    lib.gdn_kv4_page_bytes.restype = ctypes.c_size_t
+    lib.gdn_kv4_page_bytes.argtypes = [K]
+    lib.gdn_kv_plan.restype = ctypes.c_int
+    lib.gdn_kv_plan.argtypes = [K, I, I] + [_P] * 13
+    lib.gdn_kv4_append.restype = ctypes.c_int
+    lib.gdn_kv4_append.argtypes = [K, I, _P, LL, _P, LL, _P, LL, _P, I, _P, I, I, ctypes.c_char_p, I, _P, _P, _P, _P]
+    lib.gdn_kv4_read.restype = ctypes.c_int
+    lib.gdn_kv4_read.argtypes = [K, I] + [_P] * 5
+    lib.gdn_kv4_attend_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_kv4_attend_workspace_bytes.argtypes = [K, I, I]
+    lib.gdn_kv4_attend.restype = ctypes.c_int
+    lib.gdn_kv4_attend.argtypes = [K, I, I] + [_P] * 6 + [ctypes.c_float, _P, _P, ctypes.c_size_t, _P]
 
 
 def library_path() -> str:
@@ -329,6 +359,129 @@ def gdn_accept_greedy(logits, draft, active, keep, nxt, ws, stream=None):
                                   _ptr(nxt, "next", torch.int32), _ptr(ws, "ws"),
                                   ws.numel() * ws.element_size(), _stream(stream))
     _check(rc, "gdn_accept_greedy")
+
+
+def gdn_kv4_page_bytes(kd: gdn_kv4_dims) -> int:
+    """Bytes of one page (all kv heads) of one layer's cache (0 for invalid dims)."""
+    return int(load().gdn_kv4_page_bytes(ctypes.byref(kd)))
+
+
+def _tokens(t, what, heads, d):
+    """Pointer and token stride of a [N][heads][d] bf16 tensor whose heads are
+    densely packed (a slice of a fused projection serves)."""
+    torch = _t()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{what}: expected [N][{heads}][{d}], got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and heads > 1):
+        raise ValueError(f"{what}: a token's heads must be densely packed")
+    return t.data_ptr(), (s0 if t.shape[0] > 1 else max(heads * d, 8))
+
+
+def _count(t, what, n):
+    if t.numel() != n:
+        raise ValueError(f"{what}: expected {n} elements, got {t.numel()}")
+
+
+def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, free_count, q_start, q_count, kv_len,
+                slots, positions, T=0, stream=None):
+    """Block table, slots and positions of a cycle's new tokens (gdn.h,
+    gdn_kv_plan): int32 CUDA tensors, active uint8; N = slots.numel().  T > 0
+    puts row b's tokens at b*T, T = 0 packs them."""
+    torch = _t()
+    i32, B = torch.int32, kd.B
+    for t, what, n in ((lens, "lens", B), (add, "add", B), (active, "active", B), (held, "held", B),
+                       (table, "table", B * kd.max_pages), (free_list, "free_list", kd.n_pages),
+                       (free_count, "free_count", 1), (q_start, "q_start", B + 1), (q_count, "q_count", B),
+                       (kv_len, "kv_len", B), (positions, "positions", slots.numel())):
+        _count(t, what, n)
+    rc = load().gdn_kv_plan(
+        ctypes.byref(kd), T, slots.numel(), _ptr(lens, "lens", i32), _ptr(add, "add", i32),
+        _ptr(active, "active", torch.uint8), _ptr(held, "held", i32), _ptr(table, "table", i32),
+        _ptr(free_list, "free_list", i32), _ptr(free_count, "free_count", i32), _ptr(q_start, "q_start", i32),
+        _ptr(q_count, "q_count", i32), _ptr(kv_len, "kv_len", i32), _ptr(slots, "slots", i32),
+        _ptr(positions, "positions", i32), _stream(stream))
+    _check(rc, "gdn_kv_plan")
+
+
+def _cache(kd, pages):
+    """Pointer of a cache; it may be larger than its dims say, never smaller."""
+    need = kd.n_pages * gdn_kv4_page_bytes(kd)
+    p = _ptr(pages, "pages", _t().uint8)
+    if pages.numel() < need:
+        raise ValueError(f"pages: {pages.numel()} bytes, needs {need}")
+    return p
+
+
+def gdn_kv4_append(kd: gdn_kv4_dims, q, k, v, positions, rope, axis, slots, pages, q_out, style=GDN_ROPE_HALF,
+                   stream=None):
+    """Rotate q and k, write k and v into the cache (gdn.h, gdn_kv4_append).
+    q [N][H_q][d], k and v [N][H_kv][d] bf16 (token stride free), positions
+    [axes][N] int32, rope [max_pos][rot/2][2] fp32 (None: no rotation), axis:
+    bytes, the axis of each pair, slots [N] int32, pages uint8, q_out
+    [N][H_q][d] bf16."""
+    torch = _t()
+    qp, qs = _tokens(q, "q", kd.H_q, kd.d)
+    kp, ks = _tokens(k, "k", kd.H_kv, kd.d)
+    vp, vs = _tokens(v, "v", kd.H_kv, kd.d)
+    N = q.shape[0]
+    if k.shape[0] != N or v.shape[0] != N:
+        raise ValueError("q, k and v must have the same number of tokens")
+    _count(slots, "slots", N)
+    _count(q_out, "q_out", N * kd.H_q * kd.d)
+    rot, max_pos, n_axes = 0, 0, 0
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2:
+            raise ValueError("rope: expected [max_pos][rot/2][2]")
+        if positions.dim() != 2 or positions.shape[1] != N:
+            raise ValueError("positions: expected [axes][N]")
+        max_pos, rot, n_axes = rope.shape[0], 2 * rope.shape[1], positions.shape[0]
+        if len(axis) != rot // 2:
+            raise ValueError(f"axis: expected {rot // 2} bytes, got {len(axis)}")
+    rc = load().gdn_kv4_append(
+        ctypes.byref(kd), N, qp, qs, kp, ks, vp, vs, _ptr(positions, "positions", torch.int32) if rot else None,
+        n_axes, _ptr(rope, "rope", torch.float32), max_pos, rot, axis if rot else None, style,
+        _ptr(slots, "slots", torch.int32), _cache(kd, pages), _ptr(q_out, "q_out", torch.bfloat16), _stream(stream))
+    _check(rc, "gdn_kv4_append")
+
+
+def gdn_kv4_read(kd: gdn_kv4_dims, slots, pages, k, v, stream=None):
+    """The cached keys and values at the given slots in bf16 (gdn.h,
+    gdn_kv4_read): k and v [N][H_kv][d] bf16, written."""
+    torch = _t()
+    N = slots.numel()
+    _count(k, "k", N * kd.H_kv * kd.d)
+    _count(v, "v", N * kd.H_kv * kd.d)
+    rc = load().gdn_kv4_read(ctypes.byref(kd), N, _ptr(slots, "slots", torch.int32), _cache(kd, pages),
+                             _ptr(k, "k", torch.bfloat16), _ptr(v, "v", torch.bfloat16), _stream(stream))
+    _check(rc, "gdn_kv4_read")
+
+
+def gdn_kv4_attend_workspace_bytes(kd: gdn_kv4_dims, N: int, max_q: int) -> int:
+    """Bytes of workspace gdn_kv4_attend needs (0 for invalid arguments)."""
+    return int(load().gdn_kv4_attend_workspace_bytes(ctypes.byref(kd), N, max_q))
+
+
+def gdn_kv4_attend(kd: gdn_kv4_dims, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q, stream=None):
+    """Causal attention of the new tokens over the cache (gdn.h,
+    gdn_kv4_attend): q and out [N][H_q][d] bf16, pages uint8, table, q_start,
+    q_count, kv_len as gdn_kv_plan leaves them, ws zero-filled once."""
+    torch = _t()
+    i32, B = torch.int32, kd.B
+    N = q.shape[0]
+    for t, what, n in ((q, "q", N * kd.H_q * kd.d), (out, "out", N * kd.H_q * kd.d),
+                       (table, "table", B * kd.max_pages), (q_start, "q_start", B + 1), (q_count, "q_count", B),
+                       (kv_len, "kv_len", B)):
+        _count(t, what, n)
+    rc = load().gdn_kv4_attend(
+        ctypes.byref(kd), N, max_q, _ptr(q, "q", torch.bfloat16), _cache(kd, pages), _ptr(table, "table", i32),
+        _ptr(q_start, "q_start", i32), _ptr(q_count, "q_count", i32), _ptr(kv_len, "kv_len", i32), scale,
+        _ptr(out, "out", torch.bfloat16), _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
+    _check(rc, "gdn_kv4_attend")
 
 
 def gdn_get_status(clear: bool = False) -> int:
