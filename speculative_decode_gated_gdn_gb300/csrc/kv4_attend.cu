@@ -1,45 +1,63 @@
 // kv4_attend.cu -- choice of the cache attention's form, and its workspace.
 #include <atomic>
 
-#include "kv4_attend.cuh"
+#include "kv4_attend_tc.cuh"
 
 namespace gdn {
 
 namespace {
 
-// CTAs of the persistent grid at most: the workspace has room for the parts of
+// CTAs of the persistent grids at most: the workspace has room for the parts of
 // so many, on whichever device it is used.
-constexpr int kAttMaxCtas = 320;
+constexpr int kMaxSms = 160;
 
-int att_ctas() {
+int att_sms() {
   static std::atomic<int> cached[64];  // per device, 0 until looked up
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 2 * 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
   n = cached[dev].load(std::memory_order_relaxed);
   if (!n) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    n = 2 * n < kAttMaxCtas ? 2 * n : kAttMaxCtas;
+    n = n < kMaxSms ? n : kMaxSms;
     cached[dev].store(n, std::memory_order_relaxed);
   }
   return n;
 }
 
+// More query rows a kv head than one 16-row tile: the tensor-core form, which
+// shares every formed key among up to 128 rows.
+bool att_many_rows(const Kv4Geom &g, int max_q) { return (long long)max_q * (g.H_q / g.H_kv) > kAttRows; }
+
 }  // namespace
 
-size_t kv4_attend_workspace_bytes(const Kv4Geom &g, int, int) {
+size_t kv4_attend_workspace_bytes(const Kv4Geom &g, int, int max_q) {
+  if (att_many_rows(g, max_q)) {
+    switch (g.D) {
+      case 64: return att_tc_ws<64>(kMaxSms);
+      case 128: return att_tc_ws<128>(kMaxSms);
+      default: return att_tc_ws<256>(kMaxSms);
+    }
+  }
   switch (g.D) {
-    case 64: return att_mma_ws<64>(kAttMaxCtas);
-    case 128: return att_mma_ws<128>(kAttMaxCtas);
-    default: return att_mma_ws<256>(kAttMaxCtas);
+    case 64: return att_mma_ws<64>(2 * kMaxSms);
+    case 128: return att_mma_ws<128>(2 * kMaxSms);
+    default: return att_mma_ws<256>(2 * kMaxSms);
   }
 }
 
 cudaError_t launch_kv4_attend(const Kv4AttendParams &p, cudaStream_t s) {
-  const int ctas = att_ctas();
+  const int sms = att_sms();
+  if (att_many_rows(p.g, p.max_q)) {
+    switch (p.g.D) {
+      case 64: return launch_att_tc_64(p, sms, s);
+      case 128: return launch_att_tc_128(p, sms, s);
+      default: return launch_att_tc_256(p, sms, s);
+    }
+  }
   switch (p.g.D) {
-    case 64: return launch_att_mma_64(p, ctas, s);
-    case 128: return launch_att_mma_128(p, ctas, s);
-    default: return launch_att_mma_256(p, ctas, s);
+    case 64: return launch_att_mma_64(p, 2 * sms, s);
+    case 128: return launch_att_mma_128(p, 2 * sms, s);
+    default: return launch_att_mma_256(p, 2 * sms, s);
   }
 }
 
