@@ -3,15 +3,24 @@
 //
 // A unit is (row b, kv head, tile of TT = floor(128 / G) whole tokens): up to
 // 128 query rows share every key that is formed.  Per tile of NK keys:
-//   dequant  4 warps form K [NK][D] and V^T [D][NK] in fp16 (each value rounded
-//            once) in shared memory, K-major with the 128-byte swizzle;
+//   copies   one warp brings the tile's codes and entries into a ring of four;
+//   dequant  4 warps form K [NK][D] and 4 form V^T [D][NK] in fp16 (each value
+//            rounded once) in shared memory, K-major with the 128-byte swizzle;
 //   scores   S = Q K^T, Q in tensor memory as the A operand;
 //   softmax  4 warps, a thread a row: running maximum and sum in fp32; P goes
-//            back to tensor memory in fp16 over S;
+//            back to tensor memory in fp16;
 //   output   O += P V, P from tensor memory; O is rescaled only when a
 //            probability passes 2^14.
-// The channel order inside 8 channels is 0 4 1 5 2 6 3 7 in Q and K alike (a
-// product does not see it): the order in which masks take codes out of a word.
+// A product does not see the order of its inner dimension, nor O's columns the
+// order they are kept in, so both follow what shared memory likes:
+//  - inside 8 channels 0 4 1 5 2 6 3 7 (the order masks take codes out of a word);
+//  - the words of a key as tc_unit() lays them, so that the threads that read a
+//    key side by side store into different banks;
+//  - channel 8 w + e of V in row e (D / 8) + w, for the same reason.
+// The loops over a tile are kept short in code (a chunk of 32 scores, a word of
+// codes at a time): unrolled whole, the roles' code passed what the SM's
+// instruction caches hold, and every instruction waited for its fetch (5.5 us a
+// tile of 64 keys at D = 256).
 //
 // What bounds it: the tensor cores where rows are many (4 * 128 * NK * D
 // operations a tile), the dequant's instructions where a tile's rows are few.
@@ -28,14 +37,17 @@
 namespace gdn {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 288;  // warps 0-3 softmax, 4-7 dequant, 8 products
+constexpr int kTcThreads = 448;  // warps 0-3 softmax, 4-7 K, 8-11 V, 12 products, 13 copies
+constexpr int kTcRing = 4;       // tiles of codes in flight
 
 template <int D>
 struct TcShape {
   static constexpr int W = D / 64;
   static constexpr int NK = D == 256 ? 64 : 128;  // keys of a tile
   static constexpr int kKBytes = NK * D * 2;      // K or V of a tile
-  static constexpr int kSmem = 4 * kKBytes + 1024;
+  static constexpr int kCodes = NK * D / 2, kEntries = NK * W * 4;
+  static constexpr int kRaw = 2 * (kCodes + kEntries);  // a tile as it comes
+  static constexpr int kSmem = 4 * kKBytes + kTcRing * kRaw + 1024;
   // tensor memory columns: O [D], S two buffers [NK], Q [D / 2], P [NK / 2].
   // At D = 256 there is no room for P of its own: it lies over its S.
   static constexpr bool kOver = D == 256;
@@ -61,6 +73,32 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// As mbar_wait_spin, kept small: the roles wait in many places.
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
 // Loads of 32 columns without the wait.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -80,6 +118,25 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld4_async(uint32_t taddr, float (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st4_async(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Where the word 4 c + q of a key (channels 8 (4 c + q) ..) stands among its
+// 16-byte units: the 8 threads that store at a time hold 4 rows x 2 c (D = 64),
+// 2 rows x 4 c or 1 row x 8 c, and the swizzle xors the row into the unit.
+template <int D>
+__host__ __device__ constexpr int tc_unit(int c, int q) {
+  return D == 64 ? 4 * c + q : D == 128 ? (q >> 1) * 8 + 2 * c + (q & 1) : 8 * q + c;
 }
 
 // One row's part of the line.
@@ -200,6 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   using S = TcShape<D>;
   constexpr int W = S::W, NK = S::NK;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t raw_full[kTcRing], raw_empty[kTcRing];
   __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done, q_full, joined, drained;
   __shared__ uint32_t s_tmem;
   __shared__ long long s_warp[kTcThreads / 32];
@@ -208,9 +266,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   __shared__ uint32_t s_bad[2][NK / 32][W];  // keys of a V tile with a value that is not finite, per group
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *ring = smem + 4 * S::kKBytes;
   const int G = p.g.H_q / p.g.H_kv, Hkv = p.g.H_kv, TT = kTcRows / G;
   const int P = 1 << p.g.log2P;
   if (tid == 0) {
+    for (int i = 0; i < kTcRing; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128), mbar_init(&v_full[i], 128);
       mbar_init(&k_empty[i], 1), mbar_init(&v_empty[i], 1);
@@ -289,7 +349,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   __syncthreads();
   TcWalk<D> walk(p, TT, at, stop, int(s_place[0]), int(s_place[4]), int(s_place[2]), int(s_place[3]));
 
-  if (warp == 8) tmem_alloc(&s_tmem, S::kCols);
+  if (warp == 12) tmem_alloc(&s_tmem, S::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -298,228 +358,231 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   // a bounded wait; false (for good) once any wait of the CTA has run out
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (*dead) return false;
-    if (mbar_wait_spin(bar, parity, kWaitLimit)) return true;
+    if (tc_wait(bar, parity)) return true;
     *dead = 1;
     atomicOr(p.status, GDN_STATUS_TIMEOUT);
     return false;
   };
   auto wait_warp = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
-  if (warp == 8) {
-    // ---- products ---------------------------------------------------------------------
+  if (warp == 13) {
+    // ---- copies -------------------------------------------------------------------------
+    const int pt = min(P, NK), n_sub = NK / pt;  // tokens of a copy, pages of a tile
+    uint32_t it = 0;
+    bool ok = true;
+    for (; ok && !walk.done(); walk.next()) {
+      const int lim = tc_limit(walk.row, walk.tile, TT);
+      const int32_t *table = p.table + size_t(walk.b) * p.g.max_pages;
+      // lane l: piece l % 4 (K, V codes, K, V entries) of page l / 4
+      const int piece = lane & 3, sub = lane >> 2;
+      auto page_of = [&](int st) -> int {
+        const int t = st * NK + sub * pt;
+        return sub < n_sub && st < walk.st1 && t < lim ? table[t >> p.g.log2P] : -2;
+      };
+      int next = page_of(walk.st0);
+      for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
+        const uint32_t slot = it % kTcRing;
+        int page = next;
+        next = page_of(st + 1);
+        if (page != -2 && (page < 0 || page >= p.g.n_pages)) {
+          page = -2;
+          atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+        }
+        ok = wait_warp(&raw_empty[slot], (it / kTcRing & 1) ^ 1);
+        if (!ok) break;
+        const uint32_t pages = __popc(__ballot_sync(0xffffffffu, page >= 0 && piece == 0));
+        if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], pages * 2 * pt * (D / 2 + W * 4));
+        __syncwarp();
+        if (page >= 0) {
+          const int off = (st * NK + sub * pt) & (P - 1);
+          const uint8_t *rec = p.pages + (size_t(page) * Hkv + walk.hk) * kv4_record_bytes(D, P);
+          const uint8_t *src = rec + (piece & 1) * (piece < 2 ? kv4_code_bytes(D, P) : kv4_entry_bytes(D, P)) +
+                               (piece < 2 ? off * (D / 2) : 2 * kv4_code_bytes(D, P) + off * W * 4);
+          uint8_t *dst = ring + slot * S::kRaw + (piece & 1) * (piece < 2 ? S::kCodes : S::kEntries) +
+                         (piece < 2 ? sub * pt * (D / 2) : 2 * S::kCodes + sub * pt * W * 4);
+          bulk_g2s(dst, src, piece < 2 ? pt * D / 2 : pt * W * 4, &raw_full[slot]);
+        }
+      }
+    }
+    // nothing is in flight when the CTA ends: every copy is waited for by its
+    // readers, or here after a wait that ran out
+    if (!ok)
+      for (uint32_t k = it < kTcRing ? 0 : it - kTcRing; k < it; ++k)
+        tc_wait(&raw_full[k % kTcRing], k / kTcRing & 1);
+  } else if (warp == 12) {
+    // ---- products -----------------------------------------------------------------------
     if (lane == 0) {
       const uint32_t idesc_s = umma_idesc_f16(kTcRows, NK), idesc_o = umma_idesc_f16(kTcRows, D);
       const uint32_t sb = smem_u32(smem);
-      uint32_t it = 0, unit = 0;
+      uint32_t base = 0, unit = 0;  // tiles before this unit
       bool ok = true;
-      auto scores = [&](uint32_t i) {
-        const uint32_t buf = i & 1, ph = (i >> 1) & 1;
-        ok = ok && wait(&k_full[buf], ph);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t kb = sb + buf * S::kKBytes;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_f16_ts(tmem + S::kColS + buf * NK, tmem + S::kColQ + ks * 8,
-                      umma_desc_sw128(kb + (ks >> 2) * (NK * 128) + (ks & 3) * 32), idesc_s, ks > 0);
-        umma_commit(&k_empty[buf]);
-        umma_commit(&s_full[buf]);
-      };
       for (; ok && !walk.done(); walk.next(), ++unit) {
         ok = wait(&q_full, unit & 1);
-        tc_fence_after();
         const int n = walk.st1 - walk.st0;
-        if (ok) scores(it);
-        for (int i = 0; ok && i < n; ++i, ++it) {
-          // the next tile's scores run while this tile's softmax does.  Their
-          // buffer's scores were read before the last product was let go; a P
-          // lying over them is used up only when that product is done
-          if (i + 1 < n) {
-            if (S::kOver && i > 0) ok = ok && wait(&pv_done, (it - 1) & 1);
-            scores(it + 1);
-          }
-          const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-          ok = ok && wait(&v_full[buf], ph) && wait(&p_full[buf], ph);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t vb = sb + 2 * S::kKBytes + buf * S::kKBytes;
+        // scores of tile i, then the output of tile i - 1: a tile's scores run
+        // while the softmax of the one before does
+#pragma unroll 1
+        for (int i = 0; ok && i <= n; ++i) {
+          if (i < n) {
+            const uint32_t it = base + i, buf = it & 1;
+            // the buffer's scores were read before the product of two tiles ago
+            // was let go; a P lying over them is used up only when it is done
+            if (S::kOver && i > 1) ok = wait(&pv_done, (it - 2) & 1);
+            ok = ok && wait(&k_full[buf], (it >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kb = umma_desc_sw128(sb + buf * S::kKBytes);
 #pragma unroll
-          for (int ks = 0; ks < NK / 16; ++ks)
-            umma_f16_ts(tmem, tmem + S::col_p(buf) + ks * 8, umma_desc_sw128(vb + (ks >> 2) * (D * 128) + (ks & 3) * 32),
-                        idesc_o, i > 0 || ks > 0);
-          umma_commit(&v_empty[buf]);
-          umma_commit(&pv_done);
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_f16_ts(tmem + S::kColS + buf * NK, tmem + S::kColQ + ks * 8,
+                          kb + (((ks >> 2) * (NK * 128) + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+            umma_commit(&k_empty[buf]);
+            umma_commit(&s_full[buf]);
+          }
+          if (i > 0) {
+            const uint32_t it = base + i - 1, buf = it & 1, ph = (it >> 1) & 1;
+            ok = wait(&v_full[buf], ph) && wait(&p_full[buf], ph);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vb = umma_desc_sw128(sb + (2 + buf) * S::kKBytes);
+#pragma unroll
+            for (int ks = 0; ks < NK / 16; ++ks)
+              umma_f16_ts(tmem, tmem + S::col_p(buf) + ks * 8, vb + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4), idesc_o,
+                          i > 1 || ks > 0);
+            umma_commit(&v_empty[buf]);
+            umma_commit(&pv_done);
+          }
         }
+        base += n;
       }
       if (!ok) {  // a wait ran out: the products in flight end before the CTA does
         umma_commit(&drained);
-        mbar_wait_spin(&drained, 0, kWaitLimit);
+        tc_wait(&drained, 0);
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
-    // ---- dequant -------------------------------------------------------------------------
-    const int dw = warp - 4;
-    constexpr int KC = NK * D / 32 / 128;      // 16-byte chunks of K codes a thread
-    constexpr int CB = D == 64 ? 1 : 2;        // words of V codes a thread and key
-    constexpr int kChunks = D / 32;            // chunks of a key
-    // K: row r = 8 * group + lane % 8, chunk; V: 8 keys, CB words
-    uint32_t it = 0, had0[CB], had1[CB];  // what the thread noted in each buffer
-#pragma unroll
-    for (int x = 0; x < CB; ++x) had0[x] = had1[x] = 0;
+  } else if (warp >= 8) {
+    // ---- V^T: 8 keys of one word (8 channels) at a time, 16 bytes of 8 rows ------------------
+    const int vt = tid - 256;
+    constexpr int kWords = D / 8, kTasks = NK / 8 * kWords / 128;
+    uint32_t had = 0;  // bit 16 buf + i: the thread noted keys of task i in the buffer
+    uint32_t it = 0;
     bool ok = true;
     for (; ok && !walk.done(); walk.next()) {
-      const int32_t *table = p.table + size_t(walk.b) * p.g.max_pages;
       const int lim = tc_limit(walk.row, walk.tile, TT);
-      const size_t rec_bytes = kv4_record_bytes(D, P);
-      const uint8_t *heads = p.pages + size_t(walk.hk) * rec_bytes;
-      const size_t page_bytes = size_t(Hkv) * rec_bytes;
-      // lane l holds the page of keys [16 l, 16 l + 16) of a tile
-      auto pages_of = [&](int st) -> int {
-        const int t = st * NK + 16 * lane;
-        int pg = -1;
-        if (lane < NK / 16 && st < walk.st1 && t < lim) {
-          pg = table[t >> p.g.log2P];
-          if (pg < 0 || pg >= p.g.n_pages) {
-            pg = -1;
-            atomicOr(p.status, GDN_STATUS_BAD_INDEX);
-          }
-        }
-        return pg;
-      };
-      uint4 kr[KC];
-      uint32_t ke[KC][W];
-      uint32_t vr[8][CB], ve[8][CB];
-      const int vkey = (dw & (NK / 64 - 1)) * 64 + (lane & 7) * 8;                       // first of the thread's 8 keys
-      const int vword = ((dw / (NK / 64)) * 4 + (lane >> 3)) * CB;                       // first of its words
-      auto load = [&](int st, int pg) {
-#pragma unroll
-        for (int i = 0; i < KC; ++i) {
-          const int idx = (i * 4 + dw) * 4 + (lane >> 3);  // (8-row group, chunk)
-          const int r = (idx / kChunks) * 8 + (lane & 7), chunk = idx % kChunks;
-          const int page = __shfl_sync(0xffffffffu, pg, r >> 4);
-          const int t = st * NK + r, off = t & (P - 1);
-          kr[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int g = 0; g < W; ++g) ke[i][g] = 0;
-          if (page >= 0 && t < lim) {
-            const uint8_t *rec = heads + size_t(page) * page_bytes;
-            kr[i] = __ldg(reinterpret_cast<const uint4 *>(rec + off * (D / 2) + chunk * 16));
-            const uint8_t *e = rec + 2 * kv4_code_bytes(D, P) + off * (4 * W);
-            if (W == 4) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4 *>(e));
-              ke[i][0] = x.x, ke[i][1 % W] = x.y, ke[i][2 % W] = x.z, ke[i][3 % W] = x.w;
-            } else if (W == 2) {
-              const uint2 x = __ldg(reinterpret_cast<const uint2 *>(e));
-              ke[i][0] = x.x, ke[i][1 % W] = x.y;
-            } else {
-              ke[i][0] = __ldg(reinterpret_cast<const uint32_t *>(e));
-            }
-          }
-        }
-        const int page = __shfl_sync(0xffffffffu, pg, vkey >> 4);
-        const uint8_t *rec = heads + size_t(page < 0 ? 0 : page) * page_bytes;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int t = st * NK + vkey + k, off = t & (P - 1);
-#pragma unroll
-          for (int x = 0; x < CB; ++x) vr[k][x] = ve[k][x] = 0;
-          if (page >= 0 && t < lim) {
-            const uint8_t *cp = rec + kv4_code_bytes(D, P) + off * (D / 2) + vword * 4;
-            const uint8_t *e = rec + 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P) + (off * W + vword % W) * 4;
-            if (CB == 2) {
-              const uint2 a = __ldg(reinterpret_cast<const uint2 *>(cp));
-              const uint2 d = __ldg(reinterpret_cast<const uint2 *>(e));
-              vr[k][0] = a.x, vr[k][CB - 1] = a.y, ve[k][0] = d.x, ve[k][CB - 1] = d.y;
-            } else {
-              vr[k][0] = __ldg(reinterpret_cast<const uint32_t *>(cp)), ve[k][0] = __ldg(reinterpret_cast<const uint32_t *>(e));
-            }
-          }
-        }
-      };
-      __syncwarp();
-      load(walk.st0, pages_of(walk.st0));
-      int pg_next = pages_of(walk.st0 + 1);
+#pragma unroll 1
       for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
-        const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-        // ---- K: the thread's 16-byte chunks as 4 rows of 16 bytes
-        ok = wait_warp(&k_empty[buf], ph ^ 1);
-        uint8_t *kb = smem + buf * S::kKBytes;
+        const uint32_t buf = it & 1, slot = it % kTcRing;
+        ok = wait_warp(&v_empty[buf], ((it >> 1) & 1) ^ 1) && wait_warp(&raw_full[slot], it / kTcRing & 1);
+        if (!ok) break;
+        const uint8_t *raw = ring + slot * S::kRaw;
+        uint8_t *vb = smem + (2 + buf) * S::kKBytes;
+        uint32_t noted = 0;
+#pragma unroll 1
+        for (int i = 0; i < kTasks; ++i) {
+          const int id = i * 128 + vt, word = id % kWords, chunk = id / kWords;  // keys [8 chunk, 8 chunk + 8)
+          // rows of two neighbouring chunks lie in the same banks: the odd ones
+          // read their key pairs the other way round
+          const int swap = D == 256 ? 0 : chunk & 1;
+          const uint8_t *cp = raw + S::kCodes + chunk * 8 * (D / 2) + word * 4;
+          const uint8_t *ep = raw + 2 * S::kCodes + S::kEntries + (chunk * 8 * W + word % W) * 4;
+          uint32_t c[8], e[8];
 #pragma unroll
-        for (int i = 0; i < KC; ++i) {
-          const int idx = (i * 4 + dw) * 4 + (lane >> 3);
-          const int r = (idx / kChunks) * 8 + (lane & 7), chunk = idx % kChunks;
-          const uint32_t wd[4] = {kr[i].x, kr[i].y, kr[i].z, kr[i].w};
+          for (int k = 0; k < 8; ++k) {
+            c[k] = *reinterpret_cast<const uint32_t *>(cp + (k ^ swap) * (D / 2));
+            e[k] = *reinterpret_cast<const uint32_t *>(ep + (k ^ swap) * (W * 4));
+          }
+          const int left = lim - st * NK - chunk * 8;  // keys that the row has
+          if (left < 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if ((k ^ swap) >= left) e[k] = 0;
+          }
+          // values that are not finite are left out here and put back by the rows
+          // that see their key: the thread of the group's first word notes them
+          uint32_t odd = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) odd |= ((e[k] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+          const bool was = had >> (buf * 16 + i) & 1u;
+          if (odd || was) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (att_not_finite(e[k])) bad |= 1u << (k ^ swap), e[k] = 0;
+            if (word < W) {
+              uint32_t *flag = &s_bad[buf][chunk >> 2][word];
+              atomicAnd(flag, ~(0xffu << ((chunk & 3) * 8)));
+              if (bad) atomicOr(flag, bad << ((chunk & 3) * 8)), noted |= 1u << i;
+            }
+          }
+          const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
+          uint32_t es[4], eb[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            es[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel0);
+            eb[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel1);
+          }
+          uint8_t *dst = vb + (chunk >> 3) * (D * 128) + word * 128 + (((chunk ^ word) & 7) << 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t x[4], y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = __byte_perm(c[2 * k], c[2 * k + 1], half ? sel1 : sel0), y[k] = x[k] >> 8;
+            *reinterpret_cast<uint4 *>(dst + (4 * half + 0) * (kWords * 128)) =
+                make_uint4(att_even(x[0], es[0], eb[0]), att_even(x[1], es[1], eb[1]), att_even(x[2], es[2], eb[2]), att_even(x[3], es[3], eb[3]));
+            *reinterpret_cast<uint4 *>(dst + (4 * half + 1) * (kWords * 128)) =
+                make_uint4(att_odd(x[0], es[0], eb[0]), att_odd(x[1], es[1], eb[1]), att_odd(x[2], es[2], eb[2]), att_odd(x[3], es[3], eb[3]));
+            *reinterpret_cast<uint4 *>(dst + (4 * half + 2) * (kWords * 128)) =
+                make_uint4(att_even(y[0], es[0], eb[0]), att_even(y[1], es[1], eb[1]), att_even(y[2], es[2], eb[2]), att_even(y[3], es[3], eb[3]));
+            *reinterpret_cast<uint4 *>(dst + (4 * half + 3) * (kWords * 128)) =
+                make_uint4(att_odd(y[0], es[0], eb[0]), att_odd(y[1], es[1], eb[1]), att_odd(y[2], es[2], eb[2]), att_odd(y[3], es[3], eb[3]));
+          }
+        }
+        had = (had & ~(0xffffu << (buf * 16))) | noted << (buf * 16);
+        fence_proxy_async_shared();
+        mbar_arrive(&v_full[buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[slot]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- K: 4 words (32 channels) of a key at a time ----------------------------------------
+    const int kt = tid - 128;
+    constexpr int kChunks = D / 32, kTasks = NK * kChunks / 128;
+    uint32_t it = 0;
+    bool ok = true;
+    for (; ok && !walk.done(); walk.next()) {
+#pragma unroll 1
+      for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
+        const uint32_t buf = it & 1, slot = it % kTcRing;
+        ok = wait_warp(&k_empty[buf], ((it >> 1) & 1) ^ 1) && wait_warp(&raw_full[slot], it / kTcRing & 1);
+        if (!ok) break;
+        const uint8_t *raw = ring + slot * S::kRaw;
+        uint8_t *kb = smem + buf * S::kKBytes;
+#pragma unroll 2
+        for (int i = 0; i < kTasks; ++i) {
+          const int id = i * 128 + kt, c = id % kChunks, r = id / kChunks;
+          const uint4 x4 = *reinterpret_cast<const uint4 *>(raw + r * (D / 2) + c * 16);
+          uint32_t e[W];
+          att_words<W>(e, raw + 2 * S::kCodes + r * (W * 4));
+          const uint32_t wd[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t e = ke[i][q % W];
-            const uint32_t step = __byte_perm(e, e, 0x1010), base = __byte_perm(e, e, 0x3232);
+            const uint32_t step = __byte_perm(e[q % W], e[q % W], 0x1010), off = __byte_perm(e[q % W], e[q % W], 0x3232);
             const uint32_t x = wd[q], y = x >> 8;
-            const uint4 o = make_uint4(att_even(x, step, base), att_odd(x, step, base), att_even(y, step, base), att_odd(y, step, base));
-            const int u = chunk * 4 + q;  // 8-channel unit of the key
-            *reinterpret_cast<uint4 *>(kb + (u >> 3) * (NK * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = o;
+            const int u = tc_unit<D>(c, q);
+            *reinterpret_cast<uint4 *>(kb + (u >> 3) * (NK * 128) + r * 128 + (((u ^ r) & 7) << 4)) =
+                make_uint4(att_even(x, step, off), att_odd(x, step, off), att_even(y, step, off), att_odd(y, step, off));
           }
         }
         fence_proxy_async_shared();
         mbar_arrive(&k_full[buf]);
-        // ---- V^T: the thread's 8 keys as 16 bytes of each channel's row
-        ok = ok && wait_warp(&v_empty[buf], ph ^ 1);
-        uint8_t *vb = smem + 2 * S::kKBytes + buf * S::kKBytes;
-        // values that are not finite are left out here and put back by the rows
-        // that see their key: one thread notes each (key, group)
-#pragma unroll
-        for (int x = 0; x < CB; ++x) {
-          uint32_t bad = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (att_not_finite(ve[k][x])) bad |= 1u << k, ve[k][x] = 0;
-          if (vword + x < W) {
-            uint32_t &had = buf ? had1[x] : had0[x];
-            if (had | bad) {
-              uint32_t *flag = &s_bad[buf][vkey >> 5][(vword + x) % W];
-              atomicAnd(flag, ~(0xffu << (vkey & 31)));
-              if (bad) atomicOr(flag, bad << (vkey & 31));
-            }
-            had = bad;
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < CB; ++x) {
-          uint32_t es[4], eb[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            es[k] = __byte_perm(ve[2 * k][x], ve[2 * k + 1][x], 0x5410);
-            eb[k] = __byte_perm(ve[2 * k][x], ve[2 * k + 1][x], 0x7632);
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t lo[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) lo[k] = __byte_perm(vr[2 * k][x], vr[2 * k + 1][x], half ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t o[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t y = e >= 2 ? lo[k] >> 8 : lo[k];
-                o[k] = e & 1 ? att_odd(y, es[k], eb[k]) : att_even(y, es[k], eb[k]);
-              }
-              const int ch = (vword + x) * 8 + half * 4 + e;
-              *reinterpret_cast<uint4 *>(vb + (vkey >> 6) * (D * 128) + ch * 128 + ((((vkey & 63) >> 3) ^ (ch & 7)) << 4)) =
-                  make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          }
-        }
-        fence_proxy_async_shared();
-        mbar_arrive(&v_full[buf]);
-        if (st + 1 < walk.st1) {
-          load(st + 1, pg_next);
-          pg_next = pages_of(st + 2);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[slot]);
       }
     }
   } else {
-    // ---- softmax: thread = query row ----------------------------------------------------------
+    // ---- softmax: thread = query row --------------------------------------------------------
     const uint32_t lane_base = tmem + (uint32_t(warp * 32) << 16);
     float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
     uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
@@ -546,23 +609,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           for (int e = 0; e < 4; ++e) mx = max(mx, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         }
         const int e = min(max(int(mx >> 7), 20), 240);
-        const float up = __uint_as_float(uint32_t(264 - e) << 23);
-        f = (1.f / up) * (p.scale * 1.4426950408889634f);
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
+        float up = __uint_as_float(uint32_t(264 - e) << 23);
+        // the factor of a score is kept positive: the maximum is taken before it
+        f = p.scale != 0.f ? (1.f / up) * fabsf(p.scale * 1.4426950408889634f) : 1.f;
+        up = p.scale > 0.f ? up : p.scale < 0.f ? -up : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
           uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 x = live ? __ldg(src + 4 * u + k) : make_uint4(0, 0, 0, 0);
+          for (int q = 0; q < 4; ++q) {
+            const uint4 x = live ? __ldg(src + 4 * c + q) : make_uint4(0, 0, 0, 0);
             const uint32_t a[4] = {x.x, x.y, x.z, x.w};
             float y[8];
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               y[2 * h] = __uint_as_float(a[h] << 16) * up, y[2 * h + 1] = __uint_as_float(a[h] & 0xffff0000u) * up;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) w[4 * k + h] = pack_h2(y[h], y[h + 4]);
+            for (int h = 0; h < 4; ++h) w[4 * q + h] = pack_h2(y[h], y[h + 4]);
           }
-          tmem_st16_async(lane_base + S::kColQ + 16 * u, w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            tmem_st4_async(lane_base + S::kColQ + 4 * tc_unit<D>(c, q), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -570,36 +637,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       }
       float m = -INFINITY, l = 0.f;
       uint32_t nan = 0;
+#pragma unroll 1
       for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
         const uint32_t buf = it & 1, ph = (it >> 1) & 1;
         ok = wait_warp(&s_full[buf], ph);
         if (!ok) break;
         tc_fence_after();
-        uint32_t raw[NK / 32][32];
-#pragma unroll
-        for (int q = 0; q < NK / 32; ++q) tmem_ld32_async(lane_base + S::kColS + buf * NK + 32 * q, raw[q]);
-        tmem_wait_ld();
-        float x = -INFINITY;
+        const uint32_t sc = lane_base + S::kColS + buf * NK;
         const int t0 = st * NK;
-        if (t0 + NK > lim_min) {
-#pragma unroll
-          for (int q = 0; q < NK / 32; ++q)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float s = t0 + 32 * q + k < lim ? __uint_as_float(raw[q][k]) * f : -INFINITY;
-              raw[q][k] = __float_as_uint(s);
-              x = fmaxf(x, s);
-            }
-        } else {
-#pragma unroll
-          for (int q = 0; q < NK / 32; ++q)
+        const bool cut = t0 + NK > lim_min;
+        float x = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < NK / 64; ++q) {
+          uint32_t a[32], b[32];
+          tmem_ld32_async(sc + 64 * q, a);
+          tmem_ld32_async(sc + 64 * q + 32, b);
+          tmem_wait_ld();
+          if (cut) {
+            const int left = lim - t0 - 64 * q;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const float s = __uint_as_float(raw[q][k]) * f;
-              raw[q][k] = __float_as_uint(s);
-              x = fmaxf(x, s);
+              if (k >= left) a[k] = 0xff800000u;
+              if (32 + k >= left) b[k] = 0xff800000u;
             }
+          }
+          float xs[4] = {x, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 32; ++k) xs[k & 3] = max3(xs[k & 3], __uint_as_float(a[k]), __uint_as_float(b[k]));
+          x = fmaxf(max3(xs[0], xs[1], xs[2]), xs[3]);
         }
+        x *= f;
         float a = 1.f;
         const bool move = x > m + 14.f;
         if (move) {
@@ -608,55 +675,75 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           m = n;
           l *= a;
         }
-        if (__any_sync(0xffffffffu, move) && st > walk.st0) {
-          // the product that is still adding to O has to be done first
-          ok = wait_warp(&pv_done, (it - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32_async(lane_base + 32 * q, o);
-            tmem_wait_ld();
-            float y[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * a;
-            tmem_st32_async(lane_base + 32 * q, y);
+        if (st > walk.st0) {
+          const bool any = __any_sync(0xffffffffu, move);
+          // the last product has to be done before O is rescaled, or its P written over
+          if (any || !S::kOver) {
+            ok = wait_warp(&pv_done, (it - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
           }
-          tmem_wait_st();
+          if (any) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[32];
+              tmem_ld32_async(lane_base + 32 * q, o);
+              tmem_wait_ld();
+              float y[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * a;
+              tmem_st32_async(lane_base + 32 * q, y);
+            }
+          }
         }
         const float r0 = m == -INFINITY ? 0.f : m;
-        uint32_t w[NK / 32][16];
+        const F2 ff = f2(f, f), rr = f2(-r0, -r0);
+        F2 ls[2] = {f2(l, 0.f), f2(0.f, 0.f)};
+        // P's 16 columns of a chunk lie over scores that are read already
+#pragma unroll 1
+        for (int q = 0; q < NK / 32; ++q) {
+          uint32_t b[32], w[16];
+          tmem_ld32_async(sc + 32 * q, b);
+          tmem_wait_ld();
+          if (cut) {
+            const int left = lim - t0 - 32 * q;
 #pragma unroll
-        for (int q = 0; q < NK / 32; ++q)
+            for (int k = 0; k < 32; ++k)
+              if (k >= left) b[k] = 0xff800000u;
+          }
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float pa = ex2(__uint_as_float(raw[q][2 * k]) - r0), pb = ex2(__uint_as_float(raw[q][2 * k + 1]) - r0);
-            l += pa + pb;
-            w[q][k] = pack_h2(pa, pb);
+            float pa, pb;
+            f2_get(f2_fma(f2(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1])), ff, rr), pa, pb);
+            pa = ex2(pa), pb = ex2(pb);
+            ls[k & 1] = f2_add(ls[k & 1], f2(pa, pb));
+            w[k] = pack_h2(pa, pb);
           }
-        if (!S::kOver && st > walk.st0) {  // the last product has read its P
-          ok = wait_warp(&pv_done, (it - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
+          tmem_st16_async(lane_base + S::col_p(buf) + 16 * q, w);
         }
-#pragma unroll
-        for (int q = 0; q < NK / 32; ++q) tmem_st16_async(lane_base + S::col_p(buf) + 16 * q, w[q]);
+        {
+          float la, lb;
+          f2_get(f2_add(ls[0], ls[1]), la, lb);
+          l = la + lb;
+        }
         tmem_wait_st();
         tc_fence_before();
         // values that are not finite reach the rows that see their key
         ok = wait_warp(&v_full[buf], ph);
         if (!ok) break;
+        {
+          uint32_t any = 0;
 #pragma unroll
-        for (int q = 0; q < NK / 32; ++q)
-#pragma unroll
-          for (int g = 0; g < W; ++g) {
-            const uint32_t bad = *reinterpret_cast<volatile uint32_t *>(&s_bad[buf][q][g]);
-            if (bad) {
-              const int n = lim - t0 - 32 * q;
-              if (n > 0 && (bad & (n >= 32 ? 0xffffffffu : (1u << n) - 1))) nan |= 1u << g;
+          for (int k = 0; k < NK / 32 * W; ++k) any |= *reinterpret_cast<volatile uint32_t *>(&s_bad[buf][0][0] + k);
+          if (any) {
+#pragma unroll 1
+            for (int k = 0; k < NK / 32 * W; ++k) {
+              const uint32_t bad = *reinterpret_cast<volatile uint32_t *>(&s_bad[buf][0][0] + k);
+              const int n = lim - t0 - 32 * (k / W);
+              if (n > 0 && (bad & (n >= 32 ? 0xffffffffu : (1u << n) - 1))) nan |= 1u << (k % W);
             }
           }
+        }
         mbar_arrive(&p_full[buf]);
       }
       if (!ok) break;
@@ -664,25 +751,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       ok = wait_warp(&pv_done, (it - 1) & 1);
       if (!ok) break;
       tc_fence_after();
+      constexpr int kWords = D / 8;  // column e kWords + w of O is channel 8 w + e
       const bool whole = walk.st0 == 0 && walk.st1 == walk.stages;
       bool last = whole;
       long long c_first = 0, c_last = 0;
+      auto part_of = [&](long long k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>() + r; };
       if (!whole) {
         c_first = ((walk.unit_first + 1) * ctas - 1) / total;
         c_last = ((walk.unit_first + walk.stages) * ctas - 1) / total;
-        float *part = parts + (size_t(c) * 2 + (c == c_first ? 1 : 0)) * tc_part_floats<D>();
+        float *part = part_of(c);
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t o[32];
           tmem_ld32_async(lane_base + 32 * q, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int g = ((32 * q + k) / 8) % W;
-            part[size_t(32 * q + k) * kTcRows + r] = nan >> g & 1 ? __uint_as_float(0x7fc00000u) : __uint_as_float(o[k]);
-          }
+          for (int k = 0; k < 32; ++k)
+            part[size_t(32 * q + k) * kTcRows] = nan >> ((32 * q + k) % kWords % W) & 1 ? __uint_as_float(0x7fc00000u) : __uint_as_float(o[k]);
         }
-        part[size_t(D) * kTcRows + r] = m, part[size_t(D + 1) * kTcRows + r] = l;
+        part[size_t(D) * kTcRows] = m, part[size_t(D + 1) * kTcRows] = l;
         __threadfence();
         mbar_arrive(&joined);
         ok = wait_warp(&joined, joins++ & 1);
@@ -704,47 +791,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         float M = m, Ls = l;
         if (!whole) {
           M = -INFINITY, Ls = 0.f;
-          for (long long k = c_first; k <= c_last; ++k)
-            M = fmaxf(M, __ldcg(parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>() + size_t(D) * kTcRows + r));
+          for (long long k = c_first; k <= c_last; ++k) M = fmaxf(M, __ldcg(part_of(k) + size_t(D) * kTcRows));
           for (long long k = c_first; k <= c_last; ++k) {
-            const float *src = parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>() + r;
-            const float mk = __ldcg(src + size_t(D) * kTcRows), lk = __ldcg(src + size_t(D + 1) * kTcRows);
+            const float mk = __ldcg(part_of(k) + size_t(D) * kTcRows), lk = __ldcg(part_of(k) + size_t(D + 1) * kTcRows);
             Ls = fmaf(lk, lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M), Ls);
           }
         }
-        const float v = Ls > 0.f ? 1.f / Ls : Ls;
+        const float v = Ls > 0.f ? 1.f / Ls : Ls;  // no key: 0; NaN stays
         uint16_t *dst = p.out + (size_t(tok) * p.g.H_q + head) * D;
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          float y[32];
+        for (int w = 0; w < kWords; w += 4) {  // 4 words of 8 channels
+          float y[8][4];
           if (whole) {
-            uint32_t o[32];
-            tmem_ld32_async(lane_base + 32 * q, o);
-            tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              y[k] = nan >> (((32 * q + k) / 8) % W) & 1 ? __uint_as_float(0x7fc00000u) : __uint_as_float(o[k]);
+            for (int e = 0; e < 8; ++e) tmem_ld4_async(lane_base + e * kWords + w, y[e]);
+            tmem_wait_ld();
+            if (nan)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (nan >> (k % W) & 1)
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e][k] = __uint_as_float(0x7fc00000u);
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = 0.f;
+            for (int e = 0; e < 8; ++e) y[e][0] = y[e][1] = y[e][2] = y[e][3] = 0.f;
+#pragma unroll 1
             for (long long kc = c_first; kc <= c_last; ++kc) {
-              const float *src = parts + (size_t(kc) * 2 + (kc == c_first ? 1 : 0)) * tc_part_floats<D>() + r;
+              const float *src = part_of(kc);
               const float mk = __ldcg(src + size_t(D) * kTcRows), lk = __ldcg(src + size_t(D + 1) * kTcRows);
               const float ck = lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = fmaf(__ldcg(src + size_t(32 * q + k) * kTcRows), ck, y[k]);
+              for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[e][k] = fmaf(__ldcg(src + size_t(e * kWords + w + k) * kTcRows), ck, y[e][k]);
             }
           }
           if (in) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+              uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(y[8 * k + 2 * e] * v, y[8 * k + 2 * e + 1] * v);
-                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * e][k] * v, y[2 * e + 1][k] * v);
+                h[e] = *reinterpret_cast<const uint32_t *>(&b2);
               }
-              *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(dst + 8 * (w + k)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
         }
@@ -755,7 +846,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, S::kCols);
+  if (warp == 12) tmem_dealloc(tmem, S::kCols);
 }
 
 template <int D>
