@@ -107,6 +107,21 @@ __device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ush
 // of a lane differ in the parity of their place (shared-memory banks).
 __device__ __forceinline__ int att_key(int c) { return c ^ ((c >> 1) & 1); }
 
+// As mbar_wait_spin, kept small: the roles wait in many places.
+__device__ __forceinline__ bool att_wait(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
 // W consecutive 32-bit words of shared memory.
 template <int W>
 __device__ __forceinline__ void att_words(uint32_t (&w)[W], const uint8_t *p) {
@@ -393,7 +408,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
     int slot = 0;
     for (int st = st0 + warp; st < st_hi; st += kAttWarps) {
       if (st < issued) {  // once a wait has run out nothing more is issued, and what is in flight still waited for
-        if (!mbar_wait_spin(&s_full[warp][slot], (phases >> slot) & 1, kWaitLimit)) {
+        if (!att_wait(&s_full[warp][slot], (phases >> slot) & 1)) {
           dead = true;
           atomicOr(p.status, GDN_STATUS_TIMEOUT);
         }

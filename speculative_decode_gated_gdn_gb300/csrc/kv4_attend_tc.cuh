@@ -7,8 +7,9 @@
 //   dequant  4 warps form K [NK][D] and 4 form V^T [D][NK] in fp16 (each value
 //            rounded once) in shared memory, K-major with the 128-byte swizzle;
 //   scores   S = Q K^T, Q in tensor memory as the A operand;
-//   softmax  4 warps, a thread a row: running maximum and sum in fp32; P goes
-//            back to tensor memory in fp16;
+//   softmax  two groups of 4 warps take the tiles in turn, a thread a row:
+//            running maximum and sum in fp32, the reference handed from tile to
+//            tile; P goes back to tensor memory in fp16, over its scores;
 //   output   O += P V, P from tensor memory; O is rescaled only when a
 //            probability passes 2^14.
 // A product does not see the order of its inner dimension, nor O's columns the
@@ -37,8 +38,9 @@
 namespace gdn {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 448;  // warps 0-3 softmax, 4-7 K, 8-11 V, 12 products, 13 copies
+constexpr int kTcThreads = 608;  // warps 0-7 softmax, 8-11 K, 12-15 V, 16 products, 17 copies, 18 units
 constexpr int kTcRing = 4;       // tiles of codes in flight
+constexpr int kTcUnits = 4;      // units handed out ahead
 
 template <int D>
 struct TcShape {
@@ -48,13 +50,10 @@ struct TcShape {
   static constexpr int kCodes = NK * D / 2, kEntries = NK * W * 4;
   static constexpr int kRaw = 2 * (kCodes + kEntries);  // a tile as it comes
   static constexpr int kSmem = 4 * kKBytes + kTcRing * kRaw + 1024;
-  // tensor memory columns: O [D], S two buffers [NK], Q [D / 2], P [NK / 2].
-  // At D = 256 there is no room for P of its own: it lies over its S.
-  static constexpr bool kOver = D == 256;
-  static constexpr int kColS = D, kColQ = D + 2 * NK, kColP = kOver ? kColS : kColQ + D / 2;
+  // tensor memory columns: O [D], S two buffers [NK] with P over them, Q [D / 2]
+  static constexpr int kColS = D, kColQ = D + 2 * NK;
   static constexpr int kCols = 512;
-  static_assert(kColQ + D / 2 + (kOver ? 0 : NK / 2) <= kCols, "tensor memory");
-  static __device__ __forceinline__ uint32_t col_p(uint32_t buf) { return kColP + (kOver ? buf * NK : 0); }
+  static_assert(kColQ + D / 2 <= kCols, "tensor memory");
 };
 
 template <int D>
@@ -82,21 +81,6 @@ __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
-}
-
-// As mbar_wait_spin, kept small: the roles wait in many places.
-__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
 }
 
 // Loads of 32 columns without the wait.
@@ -165,105 +149,131 @@ __device__ __forceinline__ TcRow tc_row(const Kv4AttendParams &p, int b, int TT,
 
 // Keys that the last query of tile t sees, and its tiles of keys (1 at least:
 // a unit without keys still writes its zeros).
-__device__ __forceinline__ int tc_limit(const TcRow &r, int t, int TT) {
+template <typename Row>
+__device__ __forceinline__ int tc_limit(const Row &r, int t, int TT) {
   return r.count > t * TT ? max(0, r.len - r.count + min((t + 1) * TT, r.count)) : 0;
 }
-template <int NK>
-__device__ __forceinline__ int tc_stages(const TcRow &r, int t, int TT) {
+template <int NK, typename Row>
+__device__ __forceinline__ int tc_stages(const Row &r, int t, int TT) {
   return max(1, (tc_limit(r, t, TT) + NK - 1) / NK);
 }
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0 (the Euclid-like descent of
-// lattice points under a line).
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long s = 0;
-  while (n > 0) {
-    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m, b %= m;
-    const long long y = a * n + b;
-    if (y < m) break;
-    n = y / m, b = y % m;
-    const long long t = m;
-    m = a, a = t;
-  }
-  return s;
-}
-
-// Tiles of keys of all query tiles of a row (one head).
+// Tiles of keys of all query tiles of a row (one head).  Query tile t of the
+// full ones takes ceil((base + (t + 1) TT) / NK): with NK a power of two its
+// fractions repeat every `per` tiles, so whole periods come from a formula.
 template <int NK>
-__device__ inline long long tc_row_stages(const TcRow &r, int TT) {
-  if (r.tiles <= 8) {
-    long long s = 0;
-    for (int t = 0; t < r.tiles; ++t) s += tc_stages<NK>(r, t, TT);
-    return s;
-  }
+__device__ __noinline__ long long tc_row_stages(const TcRow r, int TT) {
   const int live = (r.count + TT - 1) / TT;  // tiles with a query
-  long long s = r.tiles - live;
-  int first = 0;  // tiles whose queries see no key count as one
   const int base = r.len - r.count;
-  while (first < live && base + min((first + 1) * TT, r.count) <= 0) {
-    // jump: base + (t + 1) TT > 0
-    const int t = min(live, max(first + 1, -base / TT));
-    s += t - first;
-    first = t;
-  }
-  if (first < live) {
-    // full tiles first .. live - 2: ceil((base + (t + 1) TT) / NK), and the last
-    const int n = live - 1 - first;
-    if (n > 0) s += floor_sum(n, NK, TT, (long long)base + (long long)(first + 1) * TT + NK - 1);
-    s += tc_stages<NK>(r, live - 1, TT);
-  }
+  long long s = r.tiles - live;
+  // tiles whose queries see no key count as one
+  int first = 0;
+  if (base < 0) first = min(live, -base / TT);
+  s += first;
+  const int n = live - first;
+  if (n <= 0) return s;
+  int per = NK;
+  while (per > 1 && ((per >> 1) * TT) % NK == 0) per >>= 1;
+  const int full = (n - 1) / per;  // the last tile may be short: left to the loop
+  const int b0 = base + (first + 1) * TT + NK - 1, rise = per * TT / NK;
+  long long one = 0;
+#pragma unroll 1
+  for (int j = 0; j < per && full; ++j) one += (b0 + j * TT) / NK;
+  s += full * one + (long long)rise * per * ((long long)full * (full - 1) / 2);
+#pragma unroll 1
+  for (int t = first + full * per; t < live; ++t) s += tc_stages<NK>(r, t, TT);
   return s;
 }
 
-// A thread's walk over its CTA's piece of the line.
-template <int D>
-struct TcWalk {
-  static constexpr int NK = TcShape<D>::NK;
-  const Kv4AttendParams &p;
-  int TT;
-  long long at, stop, unit_first;
-  int b, hk, tile, st0, st1, stages;
-  TcRow row;
-  __device__ TcWalk(const Kv4AttendParams &q, int tt, long long at_, long long stop_, int b_, int hk_, int tile_, int st_)
-      : p(q), TT(tt), at(at_), stop(stop_), b(b_), hk(hk_), tile(tile_), st0(st_), st1(0) {
-    row = tc_row(p, b, TT, false);
-    open();
-  }
-  __device__ void open() {
-    stages = tc_stages<NK>(row, tile, TT);
-    unit_first = at - st0;
-    st1 = int(min((long long)stages, st0 + (stop - at)));
-  }
-  __device__ bool done() const { return at >= stop; }
-  __device__ void next() {
-    at += st1 - st0;
-    if (at >= stop) return;
-    st0 = 0;
-    if (++tile == row.tiles) {
-      tile = 0;
-      if (++hk == p.g.H_kv) {
-        hk = 0;
-        do row = tc_row(p, ++b, TT, false);
-        while (row.tiles == 0);
-      }
-    }
-    open();
-  }
+// A unit, or the part of one that a CTA has: tiles of keys [st0, st1) of stages.
+struct TcUnit {
+  int b, hk, tile, st0, st1, stages;  // st1 = 0: there are no more
+  int start, span, count, len;
+  long long first;                    // the unit's place in the line
 };
+
+// One thread of the warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// S[BUF] = Q K[BUF]^T; kv: the descriptor of the first K buffer.
+template <int D, int BUF>
+__device__ __forceinline__ void tc_scores(uint64_t kv) {
+  using S = TcShape<D>;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    umma_f16_ts(S::kColS + BUF * S::NK, S::kColQ + ks * 8,
+                kv + ((BUF * S::kKBytes + (ks >> 2) * (S::NK * 128) + (ks & 3) * 32) >> 4), umma_idesc_f16(kTcRows, S::NK), ks > 0);
+}
+
+// O (+)= P V[BUF].
+template <int D, int BUF>
+__device__ __forceinline__ void tc_output(uint64_t kv, bool acc) {
+  using S = TcShape<D>;
+#pragma unroll
+  for (int ks = 0; ks < S::NK / 16; ++ks)
+    umma_f16_ts(0, S::kColS + BUF * S::NK + ks * 8,
+                kv + (((2 + BUF) * S::kKBytes + (ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4), umma_idesc_f16(kTcRows, D),
+                acc || ks > 0);
+}
+
+// The rest of a wait that did not end at once; out of line to keep the roles'
+// code small.
+static __device__ __noinline__ bool tc_wait_slow(uint64_t *bar, uint32_t parity, volatile int *dead, uint32_t *status) {
+  bool ok = false;
+  if (!*dead) {
+    ok = att_wait(bar, parity);
+    if (!ok && !*dead) {
+      *dead = 1;
+      atomicOr(status, GDN_STATUS_TIMEOUT);
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Exclusive prefix of v over the CTA, and the sum.
+static __device__ __noinline__ long long tc_scan(long long v, long long *s_warp, long long *sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll 1
+  for (int i = 0; i < kTcThreads / 32; ++i) {
+    if (i == warp) before = all;
+    all += s_warp[i];
+  }
+  *sum = all;
+  return before + x - v;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_constant__ Kv4AttendParams p) {
   using S = TcShape<D>;
   constexpr int W = S::W, NK = S::NK;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t raw_full[kTcRing], raw_empty[kTcRing];
-  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done, q_full, joined, drained;
+  __shared__ uint64_t raw_full[kTcRing], raw_empty[kTcRing], unit_full[kTcUnits], unit_empty[kTcUnits];
+  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], m_full[2];
+  __shared__ uint64_t pv_done, q_full, joined, drained;
+  __shared__ TcUnit s_unit[kTcUnits];
   __shared__ uint32_t s_tmem;
   __shared__ long long s_warp[kTcThreads / 32];
-  __shared__ long long s_place[5];
+  __shared__ long long s_place[4];
+  __shared__ float s_ref[kTcRows], s_sum[2][kTcRows], s_own[2][kTcRows];
+  __shared__ uint32_t s_nan[2 * kTcRows];
   __shared__ int s_flag, s_dead;
-  __shared__ uint32_t s_bad[2][NK / 32][W];  // keys of a V tile with a value that is not finite, per group
+  // keys of a V tile with a value that is not finite, per group; of four tiles,
+  // since the rows look two tiles later
+  __shared__ __align__(16) uint32_t s_bad[4][NK / 32 * W];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *ring = smem + 4 * S::kKBytes;
@@ -271,116 +281,136 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   const int P = 1 << p.g.log2P;
   if (tid == 0) {
     for (int i = 0; i < kTcRing; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 8);
+    for (int i = 0; i < kTcUnits; ++i) mbar_init(&unit_full[i], 1), mbar_init(&unit_empty[i], 18);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128), mbar_init(&v_full[i], 128);
       mbar_init(&k_empty[i], 1), mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128);
+      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&m_full[i], 128);
     }
-    mbar_init(&pv_done, 1), mbar_init(&q_full, 128), mbar_init(&joined, 128), mbar_init(&drained, 1);
+    mbar_init(&pv_done, 1), mbar_init(&q_full, 256), mbar_init(&joined, 256), mbar_init(&drained, 1);
     s_dead = 0;
     fence_mbar_init();
   }
-  for (int i = tid; i < 2 * (NK / 32) * W; i += kTcThreads) (&s_bad[0][0][0])[i] = 0;
+  for (int i = tid; i < 4 * (NK / 32) * W; i += kTcThreads) (&s_bad[0][0])[i] = 0;
   pdl_wait();
   pdl_trigger();
 
   // ---- this CTA's piece of the line --------------------------------------------------
-  auto block_sum = [&](long long v) -> long long {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (lane == 0) s_warp[warp] = v;
-    __syncthreads();
-    long long t = 0;
-    for (int i = 0; i < kTcThreads / 32; ++i) t += s_warp[i];
-    return t;
-  };
-  // exclusive prefix of v over the CTA
-  auto block_before = [&](long long v) -> long long {
-    long long x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += u;
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    long long t = x - v;
-    for (int i = 0; i < warp; ++i) t += s_warp[i];
-    return t;
-  };
-  long long mine = 0;
+  long long total = 0, mine = 0;
+#pragma unroll 1
   for (int b = tid; b < p.g.B; b += kTcThreads) mine += tc_row_stages<NK>(tc_row(p, b, TT, blockIdx.x == 0), TT);
-  const long long total = block_sum(mine) * Hkv;
+  tc_scan(mine, s_warp, &total);
+  total *= Hkv;
   const long long ctas = min((long long)gridDim.x, total);
   const long long c = blockIdx.x;
   if (c >= ctas) return;
-  const long long at = total * c / ctas, stop = total * (c + 1) / ctas;
-  {
+  const long long at0 = total * c / ctas, stop = total * (c + 1) / ctas;
+  // the row, and in it the query tile, that hold at0: the same search twice
+  long long want = at0;
+  int b_at = 0, hk_at = 0, t_at = 0, st_at = 0;
+  TcRow row_at{};
+#pragma unroll 1
+  for (int level = 0; level < 2; ++level) {
+    const int n = level ? row_at.tiles : p.g.B;
     long long before0 = 0;
-    for (int b0 = 0; b0 < p.g.B; b0 += kTcThreads) {
-      const long long v = b0 + tid < p.g.B ? tc_row_stages<NK>(tc_row(p, b0 + tid, TT, false), TT) * Hkv : 0;
-      const long long before = before0 + block_before(v);
-      if (tid == 0) s_place[0] = -1;
-      __syncthreads();
-      if (at >= before && at < before + v) s_place[0] = b0 + tid, s_place[1] = before;
-      before0 += block_sum(v);
-      if (s_place[0] >= 0) break;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kTcThreads) {
+      const int i = i0 + tid;
+      long long v = 0, sum;
+      if (i < n) v = level ? tc_stages<NK>(row_at, i, TT) : tc_row_stages<NK>(tc_row(p, i, TT, false), TT) * Hkv;
+      const long long before = before0 + tc_scan(v, s_warp, &sum);
+      if (want >= before && want < before + v) s_place[0] = i, s_place[1] = want - before, s_place[2] = v;
+      before0 += sum;
+      if (want < before0) break;  // the same for every thread
     }
-    const int b = int(s_place[0]);
-    const TcRow row = tc_row(p, b, TT, false);
-    const long long head = tc_row_stages<NK>(row, TT), in_row = at - s_place[1];
-    const int hk = int(in_row / head);
-    const long long x = in_row - hk * head;
-    before0 = 0;
-    for (int t0 = 0; t0 < row.tiles; t0 += kTcThreads) {
-      const long long v = t0 + tid < row.tiles ? tc_stages<NK>(row, t0 + tid, TT) : 0;
-      const long long before = before0 + block_before(v);
-      __syncthreads();
-      if (tid == 0) s_place[2] = -1;
-      __syncthreads();
-      if (x >= before && x < before + v) s_place[2] = t0 + tid, s_place[3] = x - before;
-      before0 += block_sum(v);
-      if (s_place[2] >= 0) break;
+    __syncthreads();
+    if (level == 0) {
+      b_at = int(s_place[0]);
+      row_at = tc_row(p, b_at, TT, false);
+      const long long head = s_place[2] / Hkv;
+      hk_at = int(s_place[1] / head);
+      want = s_place[1] - hk_at * head;
+    } else {
+      t_at = int(s_place[0]), st_at = int(s_place[1]);
     }
-    s_place[4] = hk;  // the same value from every thread
+    __syncthreads();
   }
-  __syncthreads();
-  TcWalk<D> walk(p, TT, at, stop, int(s_place[0]), int(s_place[4]), int(s_place[2]), int(s_place[3]));
 
-  if (warp == 12) tmem_alloc(&s_tmem, S::kCols);
+  if (warp == 16) tmem_alloc(&s_tmem, S::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  volatile int *dead = &s_dead;
-  // a bounded wait; false (for good) once any wait of the CTA has run out
-  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (*dead) return false;
-    if (tc_wait(bar, parity)) return true;
-    *dead = 1;
-    atomicOr(p.status, GDN_STATUS_TIMEOUT);
-    return false;
+  // a bounded wait of the whole warp; false once any wait of the CTA has run out
+  auto wait_warp = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return tc_wait_slow(bar, parity, &s_dead, p.status);
   };
-  auto wait_warp = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+  uint32_t un = 0;  // units taken so far
+  // the next unit, for a role's warp; false when there is none or a wait ran out
+  auto next_unit = [&](bool ok) -> bool {
+    const uint32_t i = un % kTcUnits;
+    if (un > 0) {  // the last one is done with
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[(un - 1) % kTcUnits]);
+    }
+    if (!ok || !wait_warp(&unit_full[i], un / kTcUnits & 1)) return false;
+    ++un;
+    return s_unit[i].st1 > 0;
+  };
+  auto unit = [&]() -> const TcUnit & { return s_unit[(un - 1) % kTcUnits]; };
 
-  if (warp == 13) {
+  if (warp == 18) {
+    // ---- units ------------------------------------------------------------------------------
+    long long at = at0;
+    int b = b_at, hk = hk_at, t = t_at, st0 = st_at;
+    TcRow row = row_at;
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t k = 0; ok; ++k) {
+      ok = wait_warp(&unit_empty[k % kTcUnits], (k / kTcUnits & 1) ^ 1);
+      if (!ok) break;
+      const bool more = at < stop;
+      int st1 = 0;
+      if (lane == 0) {
+        TcUnit u{};
+        if (more) {
+          u.stages = tc_stages<NK>(row, t, TT);
+          u.st0 = st0, u.st1 = st1 = int(min((long long)u.stages, st0 + (stop - at)));
+          u.first = at - st0;
+          u.b = b, u.hk = hk, u.tile = t, u.start = row.start, u.span = row.span, u.count = row.count, u.len = row.len;
+        }
+        s_unit[k % kTcUnits] = u;
+        mbar_arrive(&unit_full[k % kTcUnits]);
+      }
+      if (!more) break;
+      at += __shfl_sync(0xffffffffu, st1, 0) - st0;
+      st0 = 0;
+      if (at < stop && ++t == row.tiles) {
+        t = 0;
+        if (++hk == Hkv) {
+          hk = 0;
+          do row = tc_row(p, ++b, TT, false);
+          while (row.tiles == 0);
+        }
+      }
+    }
+  } else if (warp == 17) {
     // ---- copies -------------------------------------------------------------------------
     const int pt = min(P, NK), n_sub = NK / pt;  // tokens of a copy, pages of a tile
     uint32_t it = 0;
     bool ok = true;
-    for (; ok && !walk.done(); walk.next()) {
-      const int lim = tc_limit(walk.row, walk.tile, TT);
-      const int32_t *table = p.table + size_t(walk.b) * p.g.max_pages;
+    while (next_unit(ok)) {
+      const TcUnit u = unit();
+      const int lim = tc_limit(u, u.tile, TT);
+      const int32_t *table = p.table + size_t(u.b) * p.g.max_pages;
       // lane l: piece l % 4 (K, V codes, K, V entries) of page l / 4
       const int piece = lane & 3, sub = lane >> 2;
       auto page_of = [&](int st) -> int {
         const int t = st * NK + sub * pt;
-        return sub < n_sub && st < walk.st1 && t < lim ? table[t >> p.g.log2P] : -2;
+        return sub < n_sub && st < u.st1 && t < lim ? table[t >> p.g.log2P] : -2;
       };
-      int next = page_of(walk.st0);
-      for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
+      int next = page_of(u.st0);
+      for (int st = u.st0; ok && st < u.st1; ++st, ++it) {
         const uint32_t slot = it % kTcRing;
         int page = next;
         next = page_of(st + 1);
@@ -395,7 +425,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         __syncwarp();
         if (page >= 0) {
           const int off = (st * NK + sub * pt) & (P - 1);
-          const uint8_t *rec = p.pages + (size_t(page) * Hkv + walk.hk) * kv4_record_bytes(D, P);
+          const uint8_t *rec = p.pages + (size_t(page) * Hkv + u.hk) * kv4_record_bytes(D, P);
           const uint8_t *src = rec + (piece & 1) * (piece < 2 ? kv4_code_bytes(D, P) : kv4_entry_bytes(D, P)) +
                                (piece < 2 ? off * (D / 2) : 2 * kv4_code_bytes(D, P) + off * W * 4);
           uint8_t *dst = ring + slot * S::kRaw + (piece & 1) * (piece < 2 ? S::kCodes : S::kEntries) +
@@ -408,70 +438,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     // readers, or here after a wait that ran out
     if (!ok)
       for (uint32_t k = it < kTcRing ? 0 : it - kTcRing; k < it; ++k)
-        tc_wait(&raw_full[k % kTcRing], k / kTcRing & 1);
-  } else if (warp == 12) {
+        att_wait(&raw_full[k % kTcRing], k / kTcRing & 1);
+  } else if (warp == 16) {
     // ---- products -----------------------------------------------------------------------
-    if (lane == 0) {
-      const uint32_t idesc_s = umma_idesc_f16(kTcRows, NK), idesc_o = umma_idesc_f16(kTcRows, D);
-      const uint32_t sb = smem_u32(smem);
-      uint32_t base = 0, unit = 0;  // tiles before this unit
-      bool ok = true;
-      for (; ok && !walk.done(); walk.next(), ++unit) {
-        ok = wait(&q_full, unit & 1);
-        const int n = walk.st1 - walk.st0;
-        // scores of tile i, then the output of tile i - 1: a tile's scores run
-        // while the softmax of the one before does
+    // The whole warp waits, one elected thread issues; the operands'
+    // addresses are constants of each buffer's own code, so that they stand in
+    // uniform registers (moved there one by one, they made a product of 32
+    // cycles take 90 to issue).
+    const uint64_t kv = umma_desc_sw128(smem_u32(smem));
+    uint32_t base = 0, units = 0;  // tiles and units before this one
+    bool ok = true;
+    while (next_unit(ok)) {
+      ok = wait_warp(&q_full, units++ & 1);
+      const int n = unit().st1 - unit().st0;
+      // scores of tile i, then the output of tile i - 1
 #pragma unroll 1
-        for (int i = 0; ok && i <= n; ++i) {
-          if (i < n) {
-            const uint32_t it = base + i, buf = it & 1;
-            // the buffer's scores were read before the product of two tiles ago
-            // was let go; a P lying over them is used up only when it is done
-            if (S::kOver && i > 1) ok = wait(&pv_done, (it - 2) & 1);
-            ok = ok && wait(&k_full[buf], (it >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t kb = umma_desc_sw128(sb + buf * S::kKBytes);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              umma_f16_ts(tmem + S::kColS + buf * NK, tmem + S::kColQ + ks * 8,
-                          kb + (((ks >> 2) * (NK * 128) + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i < n) {
+          const uint32_t it = base + i, buf = it & 1;
+          // the P of two tiles ago that lies over them is used up
+          if (i > 1) ok = wait_warp(&pv_done, (it - 2) & 1);
+          ok = ok && wait_warp(&k_full[buf], (it >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (buf) tc_scores<D, 1>(kv);
+            else tc_scores<D, 0>(kv);
             umma_commit(&k_empty[buf]);
             umma_commit(&s_full[buf]);
           }
-          if (i > 0) {
-            const uint32_t it = base + i - 1, buf = it & 1, ph = (it >> 1) & 1;
-            ok = wait(&v_full[buf], ph) && wait(&p_full[buf], ph);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t vb = umma_desc_sw128(sb + (2 + buf) * S::kKBytes);
-#pragma unroll
-            for (int ks = 0; ks < NK / 16; ++ks)
-              umma_f16_ts(tmem, tmem + S::col_p(buf) + ks * 8, vb + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4), idesc_o,
-                          i > 1 || ks > 0);
+          __syncwarp();
+        }
+        if (i > 0) {
+          const uint32_t it = base + i - 1, buf = it & 1, ph = (it >> 1) & 1;
+          ok = wait_warp(&v_full[buf], ph) && wait_warp(&p_full[buf], ph);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (buf) tc_output<D, 1>(kv, i > 1);
+            else tc_output<D, 0>(kv, i > 1);
             umma_commit(&v_empty[buf]);
             umma_commit(&pv_done);
           }
+          __syncwarp();
         }
-        base += n;
       }
-      if (!ok) {  // a wait ran out: the products in flight end before the CTA does
-        umma_commit(&drained);
-        tc_wait(&drained, 0);
-      }
+      base += n;
     }
-    __syncwarp();
-  } else if (warp >= 8) {
+    if (!ok) {  // a wait ran out: the products in flight end before the CTA does
+      if (elect_one()) umma_commit(&drained);
+      __syncwarp();
+      att_wait(&drained, 0);
+    }
+  } else if (warp >= 12) {
     // ---- V^T: 8 keys of one word (8 channels) at a time, 16 bytes of 8 rows ------------------
-    const int vt = tid - 256;
+    const int vt = tid - 384;
     constexpr int kWords = D / 8, kTasks = NK / 8 * kWords / 128;
-    uint32_t had = 0;  // bit 16 buf + i: the thread noted keys of task i in the buffer
+    uint32_t had = 0;  // bit kTasks * (tile % 4) + i: the thread noted keys of task i
     uint32_t it = 0;
     bool ok = true;
-    for (; ok && !walk.done(); walk.next()) {
-      const int lim = tc_limit(walk.row, walk.tile, TT);
+    while (next_unit(ok)) {
+      const int lim = tc_limit(unit(), unit().tile, TT), st1 = unit().st1;
 #pragma unroll 1
-      for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
+      for (int st = unit().st0; ok && st < st1; ++st, ++it) {
         const uint32_t buf = it & 1, slot = it % kTcRing;
         ok = wait_warp(&v_empty[buf], ((it >> 1) & 1) ^ 1) && wait_warp(&raw_full[slot], it / kTcRing & 1);
         if (!ok) break;
@@ -503,14 +532,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           uint32_t odd = 0;
 #pragma unroll
           for (int k = 0; k < 8; ++k) odd |= ((e[k] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-          const bool was = had >> (buf * 16 + i) & 1u;
+          const bool was = had >> ((it & 3) * kTasks + i) & 1u;
           if (odd || was) {
             uint32_t bad = 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (att_not_finite(e[k])) bad |= 1u << (k ^ swap), e[k] = 0;
             if (word < W) {
-              uint32_t *flag = &s_bad[buf][chunk >> 2][word];
+              uint32_t *flag = &s_bad[it & 3][(chunk >> 2) * W + word];
               atomicAnd(flag, ~(0xffu << ((chunk & 3) * 8)));
               if (bad) atomicOr(flag, bad << ((chunk & 3) * 8)), noted |= 1u << i;
             }
@@ -523,7 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
             eb[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel1);
           }
           uint8_t *dst = vb + (chunk >> 3) * (D * 128) + word * 128 + (((chunk ^ word) & 7) << 4);
-#pragma unroll
+#pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             uint32_t x[4], y[4];
 #pragma unroll
@@ -538,28 +567,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
                 make_uint4(att_odd(y[0], es[0], eb[0]), att_odd(y[1], es[1], eb[1]), att_odd(y[2], es[2], eb[2]), att_odd(y[3], es[3], eb[3]));
           }
         }
-        had = (had & ~(0xffffu << (buf * 16))) | noted << (buf * 16);
+        had = (had & ~(((1u << kTasks) - 1) << ((it & 3) * kTasks))) | noted << ((it & 3) * kTasks);
         fence_proxy_async_shared();
         mbar_arrive(&v_full[buf]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&raw_empty[slot]);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ---- K: 4 words (32 channels) of a key at a time ----------------------------------------
-    const int kt = tid - 128;
+    const int kt = tid - 256;
     constexpr int kChunks = D / 32, kTasks = NK * kChunks / 128;
     uint32_t it = 0;
     bool ok = true;
-    for (; ok && !walk.done(); walk.next()) {
+    while (next_unit(ok)) {
+      const int st1 = unit().st1;
 #pragma unroll 1
-      for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
+      for (int st = unit().st0; ok && st < st1; ++st, ++it) {
         const uint32_t buf = it & 1, slot = it % kTcRing;
         ok = wait_warp(&k_empty[buf], ((it >> 1) & 1) ^ 1) && wait_warp(&raw_full[slot], it / kTcRing & 1);
         if (!ok) break;
         const uint8_t *raw = ring + slot * S::kRaw;
         uint8_t *kb = smem + buf * S::kKBytes;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < kTasks; ++i) {
           const int id = i * 128 + kt, c = id % kChunks, r = id / kChunks;
           const uint4 x4 = *reinterpret_cast<const uint4 *>(raw + r * (D / 2) + c * 16);
@@ -582,54 +612,64 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       }
     }
   } else {
-    // ---- softmax: thread = query row --------------------------------------------------------
-    const uint32_t lane_base = tmem + (uint32_t(warp * 32) << 16);
+    // ---- softmax: thread = query row, groups of 4 warps by the tile's parity -------------------
+    const uint32_t wg = warp >> 2;
+    const int r = tid & 127;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    constexpr int kWords = D / 8;  // column e kWords + w of O is channel 8 w + e
     float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
     uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
-    uint32_t it = 0, joins = 0;
+    uint32_t base = 0, joins = 0;
     bool ok = true;
-    for (; ok && !walk.done(); walk.next()) {
-      const TcRow &row = walk.row;
-      const int r = tid, i = walk.tile * TT + r / G, head = walk.hk * G + r % G;
-      const bool in = r < TT * G && i < row.span, live = in && i < row.count;
-      const int tok = row.start + i;
-      const int tile_lim = tc_limit(row, walk.tile, TT);
-      const int lim = live ? max(0, row.len - row.count + i + 1) : in ? 0 : tile_lim;
+    while (next_unit(ok)) {
+      const int st0 = unit().st0, n = unit().st1 - st0;
+      const int i = unit().tile * TT + r / G, head = unit().hk * G + r % G;
+      const bool in = r < TT * G && i < unit().span, live = in && i < unit().count;
+      const int tok = unit().start + i;
+      const int tile_lim = tc_limit(unit(), unit().tile, TT);
+      const int lim = live ? max(0, unit().len - unit().count + i + 1) : in ? 0 : tile_lim;
       const int lim_min = __reduce_min_sync(0xffffffffu, lim);
-      // ---- Q: scaled by a power of two to [2^10, 2^11), fp16, into tensor memory
-      float f;
+      // ---- Q as fp16 into tensor memory, half of a row's words a group.  Rows whose
+      // largest magnitude is far from 1 are scaled by a power of two (exactly).
+      float f = fabsf(p.scale) * 1.4426950408889634f;
       {
+        // the factor of a score is kept positive: the maximum is taken before it
+        const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
+        if (p.scale == 0.f) f = 1.f;
         const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(live ? tok : 0) * p.g.H_q + (live ? head : 0)) * D);
         uint32_t mx = 0;
-#pragma unroll 4
-        for (int u = 0; u < D / 8; ++u) {
-          const uint4 x = live ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = max(mx, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-        }
-        const int e = min(max(int(mx >> 7), 20), 240);
-        float up = __uint_as_float(uint32_t(264 - e) << 23);
-        // the factor of a score is kept positive: the maximum is taken before it
-        f = p.scale != 0.f ? (1.f / up) * fabsf(p.scale * 1.4426950408889634f) : 1.f;
-        up = p.scale > 0.f ? up : p.scale < 0.f ? -up : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t w[16];
+        for (int h = 0; h < 2; ++h) {  // the group's own half last: it stays in registers
+          uint4 x[D / 16];
+          const int half = wg ^ h ^ 1;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 x = live ? __ldg(src + 4 * c + q) : make_uint4(0, 0, 0, 0);
-            const uint32_t a[4] = {x.x, x.y, x.z, x.w};
-            float y[8];
+          for (int k = 0; k < D / 16; ++k) x[k] = live ? __ldg(src + half * (D / 16) + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-              y[2 * h] = __uint_as_float(a[h] << 16) * up, y[2 * h + 1] = __uint_as_float(a[h] & 0xffff0000u) * up;
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-            for (int h = 0; h < 4; ++h) w[4 * q + h] = pack_h2(y[h], y[h + 4]);
+            for (int e = 0; e < 4; ++e) mx = max(mx, max(a[e] & 0x7fffu, (a[e] >> 16) & 0x7fffu));
+          }
+          if (h == 0) continue;
+          const int e = int(mx >> 7);
+          float up = sign;
+          if (mx != 0 && (e < 127 - 6 || e > 127 + 13)) {
+            const int k = min(max(e, 20), 240);
+            const float s2 = __uint_as_float(uint32_t(264 - k) << 23);
+            up *= s2;
+            f *= 1.f / s2;
           }
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            tmem_st4_async(lane_base + S::kColQ + 4 * tc_unit<D>(c, q), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            float y[8];
+#pragma unroll
+            for (int h2 = 0; h2 < 4; ++h2)
+              y[2 * h2] = __uint_as_float(a[h2] << 16) * up, y[2 * h2 + 1] = __uint_as_float(a[h2] & 0xffff0000u) * up;
+            const int word = half * (D / 16) + k;
+            tmem_st4_async(lane_base + S::kColQ + 4 * tc_unit<D>(word >> 2, word & 3), pack_h2(y[0], y[4]), pack_h2(y[1], y[5]),
+                           pack_h2(y[2], y[6]), pack_h2(y[3], y[7]));
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -637,65 +677,84 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       }
       float m = -INFINITY, l = 0.f;
       uint32_t nan = 0;
+      // values that are not finite reach the rows that see their key
+      auto look = [&](int k) {  // tile k of the unit
+        const uint32_t *bad = s_bad[(base + k) & 3];
+        uint32_t any = 0;
+#pragma unroll
+        for (int g = 0; g < NK / 32 * W; g += 4) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(bad + g);
+          any |= x.x | x.y | x.z | x.w;
+        }
+        if (any) {
 #pragma unroll 1
-      for (int st = walk.st0; ok && st < walk.st1; ++st, ++it) {
-        const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-        ok = wait_warp(&s_full[buf], ph);
+          for (int g = 0; g < NK / 32 * W; ++g) {
+            const int left = lim - (st0 + k) * NK - 32 * (g / W);
+            if (left > 0 && (bad[g] & (left >= 32 ? 0xffffffffu : (1u << left) - 1))) nan |= 1u << (g % W);
+          }
+        }
+      };
+#pragma unroll 1
+      for (int k = (base ^ wg) & 1; ok && k < n; k += 2) {
+        const uint32_t it = base + k, ph = (it >> 1) & 1;  // it & 1 == wg
+        ok = wait_warp(&s_full[wg], ph);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sc = lane_base + S::kColS + buf * NK;
-        const int t0 = st * NK;
+        const uint32_t sc = lane_base + S::kColS + wg * NK;
+        const int t0 = (st0 + k) * NK;
         const bool cut = t0 + NK > lim_min;
         float x = -INFINITY;
 #pragma unroll 1
-        for (int q = 0; q < NK / 64; ++q) {
-          uint32_t a[32], b[32];
-          tmem_ld32_async(sc + 64 * q, a);
-          tmem_ld32_async(sc + 64 * q + 32, b);
+        for (int q = 0; q < NK / 32; ++q) {
+          uint32_t a[32];
+          tmem_ld32_async(sc + 32 * q, a);
           tmem_wait_ld();
           if (cut) {
-            const int left = lim - t0 - 64 * q;
+            const int left = lim - t0 - 32 * q;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (k >= left) a[k] = 0xff800000u;
-              if (32 + k >= left) b[k] = 0xff800000u;
-            }
+            for (int e = 0; e < 32; ++e)
+              if (e >= left) a[e] = 0xff800000u;
           }
           float xs[4] = {x, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 32; ++k) xs[k & 3] = max3(xs[k & 3], __uint_as_float(a[k]), __uint_as_float(b[k]));
+          for (int e = 0; e < 32; e += 2) xs[(e >> 1) & 3] = max3(xs[(e >> 1) & 3], __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
           x = fmaxf(max3(xs[0], xs[1], xs[2]), xs[3]);
         }
         x *= f;
-        float a = 1.f;
+        // the reference as the tile before left it
+        const float own = m;
+        if (k > 0) {
+          ok = wait_warp(&m_full[wg ^ 1], ((it - 1) >> 1) & 1);
+          if (!ok) break;
+          m = s_ref[r];
+        }
         const bool move = x > m + 14.f;
+        float a = 1.f;
         if (move) {
-          const float n = fmaxf(m, x - 6.f);
-          a = m == -INFINITY ? 0.f : ex2(m - n);
-          m = n;
-          l *= a;
+          const float to = fmaxf(m, x - 6.f);
+          a = m == -INFINITY ? 0.f : ex2(m - to);
+          m = to;
         }
-        if (st > walk.st0) {
-          const bool any = __any_sync(0xffffffffu, move);
-          // the last product has to be done before O is rescaled, or its P written over
-          if (any || !S::kOver) {
-            ok = wait_warp(&pv_done, (it - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (any) {
+        if (own != m) l *= own == -INFINITY ? 0.f : ex2(own - m);
+        if (k > 0 && __any_sync(0xffffffffu, move)) {
+          ok = wait_warp(&pv_done, (it - 1) & 1);  // every product before this tile's is in O
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32_async(lane_base + 32 * q, o);
-              tmem_wait_ld();
-              float y[32];
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32_async(lane_base + 32 * q, o);
+            tmem_wait_ld();
+            float y[32];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = __uint_as_float(o[k]) * a;
-              tmem_st32_async(lane_base + 32 * q, y);
-            }
+            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * a;
+            tmem_st32_async(lane_base + 32 * q, y);
           }
+          tmem_wait_st();
         }
+        s_ref[r] = m;
+        tc_fence_before();
+        mbar_arrive(&m_full[wg]);
         const float r0 = m == -INFINITY ? 0.f : m;
         const F2 ff = f2(f, f), rr = f2(-r0, -r0);
         F2 ls[2] = {f2(l, 0.f), f2(0.f, 0.f)};
@@ -708,68 +767,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           if (cut) {
             const int left = lim - t0 - 32 * q;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k >= left) b[k] = 0xff800000u;
+            for (int e = 0; e < 32; ++e)
+              if (e >= left) b[e] = 0xff800000u;
           }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int e = 0; e < 16; ++e) {
             float pa, pb;
-            f2_get(f2_fma(f2(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1])), ff, rr), pa, pb);
+            f2_get(f2_fma(f2(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])), ff, rr), pa, pb);
             pa = ex2(pa), pb = ex2(pb);
-            ls[k & 1] = f2_add(ls[k & 1], f2(pa, pb));
-            w[k] = pack_h2(pa, pb);
+            ls[e & 1] = f2_add(ls[e & 1], f2(pa, pb));
+            w[e] = pack_h2(pa, pb);
           }
-          tmem_st16_async(lane_base + S::col_p(buf) + 16 * q, w);
+          tmem_st16_async(sc + 16 * q, w);
         }
         {
           float la, lb;
           f2_get(f2_add(ls[0], ls[1]), la, lb);
           l = la + lb;
         }
+        // the scores of this tile were let go after the values of two tiles ago
+        if (k > 1) look(k - 2);
         tmem_wait_st();
         tc_fence_before();
-        // values that are not finite reach the rows that see their key
-        ok = wait_warp(&v_full[buf], ph);
-        if (!ok) break;
-        {
-          uint32_t any = 0;
-#pragma unroll
-          for (int k = 0; k < NK / 32 * W; ++k) any |= *reinterpret_cast<volatile uint32_t *>(&s_bad[buf][0][0] + k);
-          if (any) {
-#pragma unroll 1
-            for (int k = 0; k < NK / 32 * W; ++k) {
-              const uint32_t bad = *reinterpret_cast<volatile uint32_t *>(&s_bad[buf][0][0] + k);
-              const int n = lim - t0 - 32 * (k / W);
-              if (n > 0 && (bad & (n >= 32 ? 0xffffffffu : (1u << n) - 1))) nan |= 1u << (k % W);
-            }
-          }
-        }
-        mbar_arrive(&p_full[buf]);
+        mbar_arrive(&p_full[wg]);
       }
       if (!ok) break;
-      // ---- the unit's rows, or a part of them ------------------------------------------
-      ok = wait_warp(&pv_done, (it - 1) & 1);
+      // ---- the unit's rows, or a part of them: half of the words a group -----------------
+      const uint32_t last_it = base + n - 1;
+      ok = wait_warp(&pv_done, last_it & 1);
       if (!ok) break;
       tc_fence_after();
-      constexpr int kWords = D / 8;  // column e kWords + w of O is channel 8 w + e
-      const bool whole = walk.st0 == 0 && walk.st1 == walk.stages;
+      if (n > 1 && ((base + n - 2) & 1) == wg) look(n - 2);
+      if ((last_it & 1) == wg) look(n - 1);
+      s_sum[wg][r] = l, s_own[wg][r] = m;
+      s_nan[wg * kTcRows + r] = nan;
+      mbar_arrive(&joined);
+      ok = wait_warp(&joined, joins++ & 1);
+      if (!ok) break;
+      nan |= s_nan[(wg ^ 1) * kTcRows + r];
+      {
+        const float mo = s_own[wg ^ 1][r], lo = s_sum[wg ^ 1][r];
+        const float M = fmaxf(m, mo);  // the later tile's reference
+        const float ca = m == M ? 1.f : ex2(m - M), cb = mo == M ? 1.f : ex2(mo - M);
+        l = (l != l || m != -INFINITY ? l * ca : 0.f) + (lo != lo || mo != -INFINITY ? lo * cb : 0.f);
+        m = M;
+      }
+      const bool whole = st0 == 0 && n == unit().stages;
       bool last = whole;
       long long c_first = 0, c_last = 0;
       auto part_of = [&](long long k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>() + r; };
       if (!whole) {
-        c_first = ((walk.unit_first + 1) * ctas - 1) / total;
-        c_last = ((walk.unit_first + walk.stages) * ctas - 1) / total;
+        c_first = ((unit().first + 1) * ctas - 1) / total;
+        c_last = ((unit().first + unit().stages) * ctas - 1) / total;
         float *part = part_of(c);
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
+        for (int q = wg * (D / 64); q < (wg + 1) * (D / 64); ++q) {
           uint32_t o[32];
           tmem_ld32_async(lane_base + 32 * q, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            part[size_t(32 * q + k) * kTcRows] = nan >> ((32 * q + k) % kWords % W) & 1 ? __uint_as_float(0x7fc00000u) : __uint_as_float(o[k]);
+          for (int e = 0; e < 32; ++e)
+            part[size_t(32 * q + e) * kTcRows] = nan >> ((32 * q + e) % kWords % W) & 1 ? __uint_as_float(0x7fc00000u) : __uint_as_float(o[e]);
         }
-        part[size_t(D) * kTcRows] = m, part[size_t(D + 1) * kTcRows] = l;
+        if (wg == 0) part[size_t(D) * kTcRows] = m, part[size_t(D + 1) * kTcRows] = l;
         __threadfence();
         mbar_arrive(&joined);
         ok = wait_warp(&joined, joins++ & 1);
@@ -791,7 +851,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         float M = m, Ls = l;
         if (!whole) {
           M = -INFINITY, Ls = 0.f;
+#pragma unroll 1
           for (long long k = c_first; k <= c_last; ++k) M = fmaxf(M, __ldcg(part_of(k) + size_t(D) * kTcRows));
+#pragma unroll 1
           for (long long k = c_first; k <= c_last; ++k) {
             const float mk = __ldcg(part_of(k) + size_t(D) * kTcRows), lk = __ldcg(part_of(k) + size_t(D + 1) * kTcRows);
             Ls = fmaf(lk, lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M), Ls);
@@ -800,7 +862,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         const float v = Ls > 0.f ? 1.f / Ls : Ls;  // no key: 0; NaN stays
         uint16_t *dst = p.out + (size_t(tok) * p.g.H_q + head) * D;
 #pragma unroll 1
-        for (int w = 0; w < kWords; w += 4) {  // 4 words of 8 channels
+        for (int w = wg * (kWords / 2); w < (wg + 1) * (kWords / 2); w += 4) {  // 4 words of 8 channels
           float y[8][4];
           if (whole) {
 #pragma unroll
@@ -840,13 +902,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           }
         }
       }
+      base += n;
       tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, S::kCols);
+  if (warp == 16) tmem_dealloc(s_tmem, S::kCols);
 }
 
 template <int D>
