@@ -286,34 +286,49 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
     const int lim_min = __reduce_min_sync(0xffffffffu, min(lim0, lim1));
     const int st_hi = min(st1, (lim_max + ST - 1) / ST);
 
-    // ---- copies: 4 pieces (K, V codes, K, V entries) of up to 4 pages a stage -------
-    const int pt = min(P, ST), n_sub = ST / pt;
-    const int piece = lane & 3, sub = lane >> 2;
+    // ---- copies: a page is one copy, as it lies in memory (copies are taken one in
+    // about 70 cycles whatever their size); half of a page is four pieces ---------------
+    const bool half_page = P > ST;
+    const int n_sub = half_page ? 4 : ST >> p.g.log2P;
     const int32_t *table = p.table + size_t(b) * p.g.max_pages;
+    const uint32_t rec_bytes = kv4_record_bytes(D, P);
+    const uint8_t *head_pages = p.pages + size_t(hk) * rec_bytes;
     auto page_of = [&](int st) -> int {
-      const int t = st * ST + sub * pt;
-      return sub < n_sub && t < lim_max && st < st_hi ? table[t >> p.g.log2P] : -2;
+      const int t = st * ST + (half_page ? 0 : lane << p.g.log2P);
+      return lane < n_sub && t < lim_max && st < st_hi ? table[t >> p.g.log2P] : -2;
     };
     auto issue = [&](int st, int slot, int page) {
-      const int t = st * ST + sub * pt;
       bool ok = page != -2;
       if (ok && (page < 0 || page >= p.g.n_pages)) {
         ok = false;
         atomicOr(p.status, GDN_STATUS_BAD_INDEX);
       }
-      const int bytes = piece < 2 ? pt * D / 2 : pt * W * 4;
-      const uint32_t lanes = __ballot_sync(0xffffffffu, ok && piece == 0);
-      if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][slot], __popc(lanes) * 2 * pt * (D / 2 + W * 4));
+      const uint32_t pages = __popc(__ballot_sync(0xffffffffu, ok));
+      if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][slot], half_page ? (pages ? uint32_t(S::kStage) : 0u) : pages * rec_bytes);
       __syncwarp();
       if (ok) {
-        const uint8_t *rec = p.pages + (size_t(page) * Hkv + hk) * kv4_record_bytes(D, P);
-        const int off = t & (P - 1);
-        const uint8_t *src = rec + (piece & 1) * (piece < 2 ? kv4_code_bytes(D, P) : kv4_entry_bytes(D, P)) +
-                             (piece < 2 ? off * (D / 2) : 2 * kv4_code_bytes(D, P) + off * W * 4);
-        uint8_t *dst = ring + slot * S::kStage + (piece & 1) * (piece < 2 ? S::kCodes : S::kEntries) +
-                       (piece < 2 ? sub * pt * (D / 2) : 2 * S::kCodes + sub * pt * W * 4);
-        bulk_g2s(dst, src, bytes, &s_full[warp][slot]);
+        const uint8_t *rec = head_pages + size_t(page) * (Hkv * size_t(rec_bytes));
+        uint8_t *dst = ring + slot * S::kStage;
+        if (half_page) {  // K, V codes, K, V entries by lanes 0 .. 3
+          const int off = (st * ST) & (P - 1);
+          const bool codes = lane < 2, second = lane & 1;
+          bulk_g2s(dst + (codes ? second * S::kCodes : 2 * S::kCodes + second * S::kEntries),
+                   rec + (codes ? second * kv4_code_bytes(D, P) + off * (D / 2)
+                                : 2 * kv4_code_bytes(D, P) + second * kv4_entry_bytes(D, P) + off * W * 4),
+                   codes ? S::kCodes : S::kEntries, &s_full[warp][slot]);
+        } else {
+          bulk_g2s(dst + lane * rec_bytes, rec, rec_bytes, &s_full[warp][slot]);
+        }
       }
+    };
+    // places of a stage's keys: `pt` keys (a page, or the half of one) a record
+    const int log2pt = min(p.g.log2P, ST == 32 ? 5 : 6), pt = 1 << log2pt;
+    const int rec_c = pt * (D / 2), rec_e = pt * (W * 4), rec_s = 2 * (rec_c + rec_e);
+    auto code_at = [&](const uint8_t *stage, int which, int key) {
+      return stage + (key >> log2pt) * rec_s + which * rec_c + (key & (pt - 1)) * (D / 2);
+    };
+    auto entry_at = [&](const uint8_t *stage, int which, int key) {
+      return stage + (key >> log2pt) * rec_s + 2 * rec_c + which * rec_e + (key & (pt - 1)) * (W * 4);
     };
     int next = page_of(st0 + warp);
     int issued = st0 + warp;  // next stage to issue
@@ -416,7 +431,6 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
         phases ^= 1u << slot;
       }
       const uint8_t *stage = ring + slot * S::kStage;
-      const uint8_t *kc = stage, *vc = stage + S::kCodes, *ke = stage + 2 * S::kCodes, *ve = ke + S::kEntries;
       const int t_base = st * ST;
 
       // ---- scores ------------------------------------------------------------------
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
         float acc[W][4];
 #pragma unroll
         for (int g = 0; g < W; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-        const uint8_t *kr = kc + (8 * u + att_key(n)) * (D / 2);
+        const uint8_t *kr = code_at(stage, 0, 8 * u + att_key(n));
         uint32_t word[D / 32];
         if (D == 64) {
           const uint2 x = *reinterpret_cast<const uint2 *>(kr + 8 * j);
@@ -447,8 +461,8 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
                    y & 0x00f000f0u);
         }
         uint32_t x0[W], x1[W];
-        att_words<W>(x0, ke + (8 * u + att_key(2 * j)) * (4 * W));
-        att_words<W>(x1, ke + (8 * u + att_key(2 * j + 1)) * (4 * W));
+        att_words<W>(x0, entry_at(stage, 0, 8 * u + att_key(2 * j)));
+        att_words<W>(x1, entry_at(stage, 0, 8 * u + att_key(2 * j + 1)));
         F2 r0 = f2(0.f, 0.f), r1 = f2(0.f, 0.f);
 #pragma unroll
         for (int g = 0; g < W; ++g) {
@@ -517,8 +531,8 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
           a[2 * half + 1] = pack_h2(p10, p11);
           const int ka = 8 * u + att_key(2 * j), kb = 8 * u + att_key(2 * j + 1);
           uint32_t wa[W], wb[W];
-          att_words<W>(wa, ve + ka * (4 * W));
-          att_words<W>(wb, ve + kb * (4 * W));
+          att_words<W>(wa, entry_at(stage, 1, ka));
+          att_words<W>(wb, entry_at(stage, 1, kb));
           if (cut) {
             // a value that one query sees and another does not must not reach
             // the other as 0 * NaN: it is left out and remembered by the row
@@ -538,11 +552,10 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
           }
         }
         uint32_t w0[W], w1[W], w2[W], w3[W];
-        const uint8_t *vr = vc + n * (4 * W);
-        att_words<W>(w0, vr + (16 * h + att_key(2 * j)) * (D / 2));
-        att_words<W>(w1, vr + (16 * h + att_key(2 * j + 1)) * (D / 2));
-        att_words<W>(w2, vr + (16 * h + 8 + att_key(2 * j)) * (D / 2));
-        att_words<W>(w3, vr + (16 * h + 8 + att_key(2 * j + 1)) * (D / 2));
+        att_words<W>(w0, code_at(stage, 1, 16 * h + att_key(2 * j)) + n * (4 * W));
+        att_words<W>(w1, code_at(stage, 1, 16 * h + att_key(2 * j + 1)) + n * (4 * W));
+        att_words<W>(w2, code_at(stage, 1, 16 * h + 8 + att_key(2 * j)) + n * (4 * W));
+        att_words<W>(w3, code_at(stage, 1, 16 * h + 8 + att_key(2 * j + 1)) + n * (4 * W));
 #pragma unroll
         for (int g = 0; g < W; ++g) {
 #pragma unroll

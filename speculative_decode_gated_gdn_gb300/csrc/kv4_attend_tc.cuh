@@ -47,8 +47,7 @@ struct TcShape {
   static constexpr int W = D / 64;
   static constexpr int NK = D == 256 ? 64 : 128;  // keys of a tile
   static constexpr int kKBytes = NK * D * 2;      // K or V of a tile
-  static constexpr int kCodes = NK * D / 2, kEntries = NK * W * 4;
-  static constexpr int kRaw = 2 * (kCodes + kEntries);  // a tile as it comes
+  static constexpr int kRaw = 2 * (NK * D / 2 + NK * W * 4);  // a tile as it comes: its pages' records
   static constexpr int kSmem = 4 * kKBytes + kTcRing * kRaw + 1024;
   // tensor memory columns: O [D], S two buffers [NK] with P over them, Q [D / 2]
   static constexpr int kColS = D, kColQ = D + 2 * NK;
@@ -396,21 +395,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     }
   } else if (warp == 17) {
     // ---- copies -------------------------------------------------------------------------
-    const int pt = min(P, NK), n_sub = NK / pt;  // tokens of a copy, pages of a tile
+    // A page is one copy, as it lies in memory: copies are taken one in about 70
+    // cycles whatever their size, so 32 pieces of eight small pages took 2250
+    // cycles a tile.
+    const int n_sub = NK >> p.g.log2P;  // pages of a tile
+    const uint32_t rec_bytes = kv4_record_bytes(D, P);
     uint32_t it = 0;
     bool ok = true;
     while (next_unit(ok)) {
-      const TcUnit u = unit();
-      const int lim = tc_limit(u, u.tile, TT);
-      const int32_t *table = p.table + size_t(u.b) * p.g.max_pages;
-      // lane l: piece l % 4 (K, V codes, K, V entries) of page l / 4
-      const int piece = lane & 3, sub = lane >> 2;
-      auto page_of = [&](int st) -> int {
-        const int t = st * NK + sub * pt;
-        return sub < n_sub && st < u.st1 && t < lim ? table[t >> p.g.log2P] : -2;
+      const int lim = tc_limit(unit(), unit().tile, TT), st1 = unit().st1;
+      const int32_t *table = p.table + size_t(unit().b) * p.g.max_pages;
+      const uint8_t *head = p.pages + size_t(unit().hk) * rec_bytes;
+      auto page_of = [&](int st) -> int {  // lane l: page l of the tile
+        const int t = st * NK + (lane << p.g.log2P);
+        return lane < n_sub && st < st1 && t < lim ? table[t >> p.g.log2P] : -2;
       };
-      int next = page_of(u.st0);
-      for (int st = u.st0; ok && st < u.st1; ++st, ++it) {
+      int next = page_of(unit().st0);
+#pragma unroll 1
+      for (int st = unit().st0; ok && st < st1; ++st, ++it) {
         const uint32_t slot = it % kTcRing;
         int page = next;
         next = page_of(st + 1);
@@ -420,18 +422,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         }
         ok = wait_warp(&raw_empty[slot], (it / kTcRing & 1) ^ 1);
         if (!ok) break;
-        const uint32_t pages = __popc(__ballot_sync(0xffffffffu, page >= 0 && piece == 0));
-        if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], pages * 2 * pt * (D / 2 + W * 4));
+        const uint32_t pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], pages * rec_bytes);
         __syncwarp();
-        if (page >= 0) {
-          const int off = (st * NK + sub * pt) & (P - 1);
-          const uint8_t *rec = p.pages + (size_t(page) * Hkv + u.hk) * kv4_record_bytes(D, P);
-          const uint8_t *src = rec + (piece & 1) * (piece < 2 ? kv4_code_bytes(D, P) : kv4_entry_bytes(D, P)) +
-                               (piece < 2 ? off * (D / 2) : 2 * kv4_code_bytes(D, P) + off * W * 4);
-          uint8_t *dst = ring + slot * S::kRaw + (piece & 1) * (piece < 2 ? S::kCodes : S::kEntries) +
-                         (piece < 2 ? sub * pt * (D / 2) : 2 * S::kCodes + sub * pt * W * 4);
-          bulk_g2s(dst, src, piece < 2 ? pt * D / 2 : pt * W * 4, &raw_full[slot]);
-        }
+        if (page >= 0)
+          bulk_g2s(ring + slot * S::kRaw + lane * rec_bytes, head + size_t(page) * (Hkv * size_t(rec_bytes)), rec_bytes, &raw_full[slot]);
       }
     }
     // nothing is in flight when the CTA ends: every copy is waited for by its
@@ -513,8 +508,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           // rows of two neighbouring chunks lie in the same banks: the odd ones
           // read their key pairs the other way round
           const int swap = D == 256 ? 0 : chunk & 1;
-          const uint8_t *cp = raw + S::kCodes + chunk * 8 * (D / 2) + word * 4;
-          const uint8_t *ep = raw + 2 * S::kCodes + S::kEntries + (chunk * 8 * W + word % W) * 4;
+          const uint8_t *rec = raw + (chunk >> (p.g.log2P - 3)) * kv4_record_bytes(D, P);
+          const int off = (chunk * 8) & (P - 1);
+          const uint8_t *cp = rec + kv4_code_bytes(D, P) + off * (D / 2) + word * 4;
+          const uint8_t *ep = rec + 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P) + (off * W + word % W) * 4;
           uint32_t c[8], e[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -592,9 +589,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
 #pragma unroll 1
         for (int i = 0; i < kTasks; ++i) {
           const int id = i * 128 + kt, c = id % kChunks, r = id / kChunks;
-          const uint4 x4 = *reinterpret_cast<const uint4 *>(raw + r * (D / 2) + c * 16);
+          const uint8_t *rec = raw + (r >> p.g.log2P) * kv4_record_bytes(D, P);
+          const int off = r & (P - 1);
+          const uint4 x4 = *reinterpret_cast<const uint4 *>(rec + off * (D / 2) + c * 16);
           uint32_t e[W];
-          att_words<W>(e, raw + 2 * S::kCodes + r * (W * 4));
+          att_words<W>(e, rec + 2 * kv4_code_bytes(D, P) + off * (W * 4));
           const uint32_t wd[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
