@@ -41,6 +41,10 @@ constexpr int kTcRows = 128;
 constexpr int kTcThreads = 608;  // warps 0-7 softmax, 8-11 K, 12-15 V, 16 products, 17 copies, 18 units
 constexpr int kTcRing = 4;       // tiles of codes in flight
 constexpr int kTcUnits = 4;      // units handed out ahead
+// What a unit costs besides its tiles of keys (queries in, outputs out), in
+// tiles: its place on the line is that much longer, so that the pieces of the
+// CTAs that have many short units are not the last to end.
+constexpr int kTcUnitCost = 6;
 
 template <int D>
 struct TcShape {
@@ -127,7 +131,7 @@ struct TcRow {
   int start, span, count, len, tiles;
 };
 
-__device__ __forceinline__ TcRow tc_row(const Kv4AttendParams &p, int b, int TT, bool report) {
+static __device__ __noinline__ TcRow tc_row(const Kv4AttendParams &p, int b, int TT, bool report) {
   TcRow r;
   r.start = p.q_start[b];
   int span = p.q_start[b + 1] - r.start;
@@ -157,14 +161,14 @@ __device__ __forceinline__ int tc_stages(const Row &r, int t, int TT) {
   return max(1, (tc_limit(r, t, TT) + NK - 1) / NK);
 }
 
-// Tiles of keys of all query tiles of a row (one head).  Query tile t of the
-// full ones takes ceil((base + (t + 1) TT) / NK): with NK a power of two its
+// Places on the line of all query tiles of a row (one head): the tiles of keys,
+// and kTcUnitCost each.  Query tile t of the full ones takes ceil((base + (t + 1) TT) / NK): with NK a power of two its
 // fractions repeat every `per` tiles, so whole periods come from a formula.
 template <int NK>
 __device__ __noinline__ long long tc_row_stages(const TcRow r, int TT) {
   const int live = (r.count + TT - 1) / TT;  // tiles with a query
   const int base = r.len - r.count;
-  long long s = r.tiles - live;
+  long long s = (long long)r.tiles * kTcUnitCost + r.tiles - live;
   // tiles whose queries see no key count as one
   int first = 0;
   if (base < 0) first = min(live, -base / TT);
@@ -245,11 +249,11 @@ static __device__ __noinline__ long long tc_scan(long long v, long long *s_warp,
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  long long before = 0, all = 0;
+  long long before = lane < warp ? s_warp[lane] : 0, all = lane < kTcThreads / 32 ? s_warp[lane] : 0;
 #pragma unroll 1
-  for (int i = 0; i < kTcThreads / 32; ++i) {
-    if (i == warp) before = all;
-    all += s_warp[i];
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
   }
   *sum = all;
   return before + x - v;
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   __shared__ TcUnit s_unit[kTcUnits];
   __shared__ uint32_t s_tmem;
   __shared__ long long s_warp[kTcThreads / 32];
-  __shared__ long long s_place[4];
+  __shared__ long long s_place[2];
   __shared__ float s_ref[kTcRows], s_sum[2][kTcRows], s_own[2][kTcRows];
   __shared__ uint32_t s_nan[2 * kTcRows];
   __shared__ int s_flag, s_dead;
@@ -300,10 +304,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   for (int b = tid; b < p.g.B; b += kTcThreads) mine += tc_row_stages<NK>(tc_row(p, b, TT, blockIdx.x == 0), TT);
   tc_scan(mine, s_warp, &total);
   total *= Hkv;
-  const long long ctas = min((long long)gridDim.x, total);
-  const long long c = blockIdx.x;
+  // a piece is worth its fixed costs, or there are fewer
+  const int ctas = int(min((long long)gridDim.x, (total + kTcUnitCost + 1) / (kTcUnitCost + 2)));
+  const int c = blockIdx.x;
   if (c >= ctas) return;
-  const long long at0 = total * c / ctas, stop = total * (c + 1) / ctas;
+  // pieces of `per` places, the first `more` of one more
+  const long long per = total / ctas;
+  const int more = int(total - per * ctas);
+  const long long at0 = per * c + min(c, more), stop = at0 + per + (c < more);
+  auto cta_of = [&](long long x) -> int {
+    const long long y = x - more * (per + 1);
+    return int(y < 0 ? x / (per + 1) : more + y / per);
+  };
   // the row, and in it the query tile, that hold at0: the same search twice
   long long want = at0;
   int b_at = 0, hk_at = 0, t_at = 0, st_at = 0;
@@ -316,9 +328,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     for (int i0 = 0; i0 < n; i0 += kTcThreads) {
       const int i = i0 + tid;
       long long v = 0, sum;
-      if (i < n) v = level ? tc_stages<NK>(row_at, i, TT) : tc_row_stages<NK>(tc_row(p, i, TT, false), TT) * Hkv;
+      if (i < n) v = level ? tc_stages<NK>(row_at, i, TT) + kTcUnitCost : tc_row_stages<NK>(tc_row(p, i, TT, false), TT) * Hkv;
       const long long before = before0 + tc_scan(v, s_warp, &sum);
-      if (want >= before && want < before + v) s_place[0] = i, s_place[1] = want - before, s_place[2] = v;
+      if (want >= before && want < before + v) s_place[0] = i, s_place[1] = want - before;
       before0 += sum;
       if (want < before0) break;  // the same for every thread
     }
@@ -326,9 +338,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     if (level == 0) {
       b_at = int(s_place[0]);
       row_at = tc_row(p, b_at, TT, false);
-      const long long head = s_place[2] / Hkv;
-      hk_at = int(s_place[1] / head);
-      want = s_place[1] - hk_at * head;
+      const long long head = tc_row_stages<NK>(row_at, TT);
+      want = s_place[1];
+      while (want >= head) want -= head, ++hk_at;
     } else {
       t_at = int(s_place[0]), st_at = int(s_place[1]);
     }
@@ -361,29 +373,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   if (warp == 18) {
     // ---- units ------------------------------------------------------------------------------
     long long at = at0;
-    int b = b_at, hk = hk_at, t = t_at, st0 = st_at;
+    int b = b_at, hk = hk_at, t = t_at, place = st_at;  // place in the unit, of stages + kTcUnitCost
     TcRow row = row_at;
     bool ok = true;
+    uint32_t k = 0;
 #pragma unroll 1
-    for (uint32_t k = 0; ok; ++k) {
-      ok = wait_warp(&unit_empty[k % kTcUnits], (k / kTcUnits & 1) ^ 1);
-      if (!ok) break;
-      const bool more = at < stop;
-      int st1 = 0;
-      if (lane == 0) {
-        TcUnit u{};
-        if (more) {
-          u.stages = tc_stages<NK>(row, t, TT);
-          u.st0 = st0, u.st1 = st1 = int(min((long long)u.stages, st0 + (stop - at)));
-          u.first = at - st0;
-          u.b = b, u.hk = hk, u.tile = t, u.start = row.start, u.span = row.span, u.count = row.count, u.len = row.len;
-        }
-        s_unit[k % kTcUnits] = u;
-        mbar_arrive(&unit_full[k % kTcUnits]);
+    while (ok) {
+      const bool more_units = at < stop;
+      int stages = 0, end = 0;
+      if (more_units) {
+        stages = tc_stages<NK>(row, t, TT);
+        end = int(min((long long)stages + kTcUnitCost, place + (stop - at)));
       }
-      if (!more) break;
-      at += __shfl_sync(0xffffffffu, st1, 0) - st0;
-      st0 = 0;
+      // a piece that ends in a unit's fixed part has none of its tiles
+      if (!more_units || end > kTcUnitCost) {
+        ok = wait_warp(&unit_empty[k % kTcUnits], (k / kTcUnits & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          TcUnit u{};
+          if (more_units) {
+            u.stages = stages, u.st0 = max(0, place - kTcUnitCost), u.st1 = end - kTcUnitCost;
+            u.first = at - place;
+            u.b = b, u.hk = hk, u.tile = t, u.start = row.start, u.span = row.span, u.count = row.count, u.len = row.len;
+          }
+          s_unit[k % kTcUnits] = u;
+          mbar_arrive(&unit_full[k % kTcUnits]);
+        }
+        ++k;
+      }
+      if (!more_units) break;
+      at += end - place;
+      place = 0;
       if (at < stop && ++t == row.tiles) {
         t = 0;
         if (++hk == Hkv) {
@@ -813,11 +833,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       }
       const bool whole = st0 == 0 && n == unit().stages;
       bool last = whole;
-      long long c_first = 0, c_last = 0;
-      auto part_of = [&](long long k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>() + r; };
+      int c_first = 0, c_last = 0;
+      auto part_of = [&](int k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>() + r; };
       if (!whole) {
-        c_first = ((unit().first + 1) * ctas - 1) / total;
-        c_last = ((unit().first + unit().stages) * ctas - 1) / total;
+        c_first = cta_of(unit().first + kTcUnitCost);
+        c_last = cta_of(unit().first + unit().stages + kTcUnitCost - 1);
         float *part = part_of(c);
 #pragma unroll 1
         for (int q = wg * (D / 64); q < (wg + 1) * (D / 64); ++q) {
@@ -851,9 +871,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (!whole) {
           M = -INFINITY, Ls = 0.f;
 #pragma unroll 1
-          for (long long k = c_first; k <= c_last; ++k) M = fmaxf(M, __ldcg(part_of(k) + size_t(D) * kTcRows));
+          for (int k = c_first; k <= c_last; ++k) M = fmaxf(M, __ldcg(part_of(k) + size_t(D) * kTcRows));
 #pragma unroll 1
-          for (long long k = c_first; k <= c_last; ++k) {
+          for (int k = c_first; k <= c_last; ++k) {
             const float mk = __ldcg(part_of(k) + size_t(D) * kTcRows), lk = __ldcg(part_of(k) + size_t(D + 1) * kTcRows);
             Ls = fmaf(lk, lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M), Ls);
           }
@@ -877,7 +897,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e][0] = y[e][1] = y[e][2] = y[e][3] = 0.f;
 #pragma unroll 1
-            for (long long kc = c_first; kc <= c_last; ++kc) {
+            for (int kc = c_first; kc <= c_last; ++kc) {
               const float *src = part_of(kc);
               const float mk = __ldcg(src + size_t(D) * kTcRows), lk = __ldcg(src + size_t(D + 1) * kTcRows);
               const float ck = lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M);
