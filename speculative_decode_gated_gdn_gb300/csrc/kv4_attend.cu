@@ -26,7 +26,7 @@ int att_sms() {
 
 // More query rows a kv head than one 16-row tile: the tensor-core form, which
 // shares every formed key among up to 128 rows.
-bool att_many_rows(const Kv4Geom &g, int max_q) { return (long long)max_q * (g.H_q / g.H_kv) > kAttRows; }
+bool att_many_rows(const Kv4Geom &g, int max_q) { return (long long)max_q * (g.H_q / g.H_kv) > kAttMaxRows; }
 
 }  // namespace
 
@@ -39,9 +39,9 @@ size_t kv4_attend_workspace_bytes(const Kv4Geom &g, int, int max_q) {
     }
   }
   switch (g.D) {
-    case 64: return att_mma_ws<64>(2 * kMaxSms);
-    case 128: return att_mma_ws<128>(2 * kMaxSms);
-    default: return att_mma_ws<256>(2 * kMaxSms);
+    case 64: return att_mma_ws<64, 16>(kMaxSms);
+    case 128: return att_mma_ws<128, 16>(kMaxSms);
+    default: return att_mma_ws<256, 16>(kMaxSms);
   }
 }
 
@@ -54,10 +54,11 @@ cudaError_t launch_kv4_attend(const Kv4AttendParams &p, cudaStream_t s) {
       default: return launch_att_tc_256(p, sms, s);
     }
   }
+  const int rows = (long long)p.max_q * (p.g.H_q / p.g.H_kv) <= 8 ? 8 : 16;
   switch (p.g.D) {
-    case 64: return launch_att_mma_64(p, 2 * sms, s);
-    case 128: return launch_att_mma_128(p, 2 * sms, s);
-    default: return launch_att_mma_256(p, 2 * sms, s);
+    case 64: return launch_att_mma_64(p, rows, sms, s);
+    case 128: return launch_att_mma_128(p, rows, sms, s);
+    default: return launch_att_mma_256(p, rows, sms, s);
   }
 }
 

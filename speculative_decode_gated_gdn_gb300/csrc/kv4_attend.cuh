@@ -1,7 +1,7 @@
 // kv4_attend.cuh -- causal attention of a few query rows over the paged 4-bit
 // cache: one pass over the keys, the codes as matrix operands.
 //
-// A unit is (row b, kv head, tile of 16 query rows); a query row is one
+// A unit is (row b, kv head, tile of R = 8 or 16 query rows); a query row is one
 // (token, head of the group), so the group's heads and a row's draft positions
 // share every byte that is read.  A warp takes stages of ST keys:
 //   scores   mma m16n8k16 (fp16, fp32 accumulators) of Q with the keys' codes.
@@ -16,19 +16,21 @@
 //            out exactly (1024 + code, less 1024, or 1024 + 16 code, / 16 - 64),
 //            then base + step * code in one fused multiply-add; P is rounded
 //            once to fp16, at most 2^14 and exact to 2^-11 down to 2^-20 of
-//            the largest.
+//            the largest.  With R = 8 the values are the first operand and P the
+//            second, which takes half the products and accumulators.
 // q is scaled per row by a power of two before fp16, exactly.
 //
 // What bounds it: HBM for single tokens and drafts (144 bytes a token and
 // head pair at D = 128), with the instructions that unpack 2 x D codes a token
-// close behind; hence the AND-only unpacking of the keys and packed fp32
-// arithmetic.
+// close behind; hence the AND-only unpacking of the keys, packed fp32
+// arithmetic and as many warps as the registers allow.
 //
 // The keys' stages of all units form one line, which the CTAs of a persistent
-// grid cut into equal pieces; the warps of a CTA take its stages in turn, each
-// with its own ring of bulk copies, and join in shared memory.  A unit cut
-// between CTAs is joined by whichever of them finishes last, in the order of
-// the pieces, so the result does not depend on timing.
+// grid (one an SM) cut into equal pieces; the warps of a CTA take its stages in
+// turn, each with its own ring of bulk copies, and join in shared memory while
+// the next unit's first stages are on their way.  A unit cut between CTAs is
+// joined by whichever of them finishes last, in the order of the pieces, so the
+// result does not depend on timing.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -37,27 +39,37 @@
 
 namespace gdn {
 
-constexpr int kAttWarps = 4;
-constexpr int kAttThreads = 32 * kAttWarps;
-constexpr int kAttRows = 16;
-
-template <int D>
+template <int D, int R>
 struct AttShape {
   static constexpr int W = D / 64;               // groups of a head
-  static constexpr int ST = D == 256 ? 32 : 64;  // keys of a stage
+  static constexpr int ST = D == 64 ? 64 : 32;   // keys of a stage
   static constexpr int NT = ST / 8;              // key tiles of a stage
+  // warps of a CTA, as many as the registers of a thread allow
+  static constexpr int NW = D == 256 ? (R == 8 ? 12 : 8) : D == 128 ? (R == 8 ? 16 : 12) : 16;
+  static constexpr int kThreads = 32 * NW;
   static constexpr int kCodes = ST * D / 2, kEntries = ST * W * 4;
   static constexpr int kStage = 2 * (kCodes + kEntries);
-  static constexpr int kSlots = 3;               // stages of a warp's ring
-  static constexpr int kPart = 16 * D;           // floats of a partial output
+  static constexpr int kSlots = (224 * 1024 / kStage) / NW;  // stages of a warp's ring
+  static constexpr int X = R / 4;                // accumulators of a lane and channel tile
+  static constexpr int kRegs = D / 8 * X;        // accumulators of a lane
+  static constexpr int kScratch = (kRegs * 128 + kStage - 1) / kStage;  // slots a warp's part takes in the join
+  static constexpr int kAhead = kSlots - kScratch;                      // slots the next unit may fill before it
+  static constexpr int kRegsSlot = kRegs / kScratch;                    // accumulators a slot takes
+  static constexpr int kQuads = kRegs / 4 * 32;  // items of the join: 4 channels of a query row
+  static constexpr int kPart = kRegs * 32;       // floats of a part
   static constexpr int kRing = kSlots * kStage;
-  static constexpr int kSmem = kAttWarps * kRing + 128;
-  static_assert(kRing >= kPart * 4, "the join reuses the ring");
+  static constexpr int kSmem = NW * kRing + 128;
+  static_assert(kAhead >= 1 && kRegs % kScratch == 0 && kRegsSlot * 128 <= kStage, "ring");
+  // accumulator of channel tile 8 g + e: R = 16: one tile of 8 channels a product,
+  // x the four values; R = 8: two tiles a product, x the two rows
+  static __host__ __device__ constexpr int reg(int t, int x) { return R == 16 ? 4 * t + x : (t >> 1) * 4 + 2 * (t & 1) + x; }
 };
 
-// Partial results in the workspace: two per CTA, [16 D] outputs then m, l [16].
-template <int D>
-__host__ __device__ constexpr size_t att_part_floats() { return AttShape<D>::kPart + 32; }
+constexpr int kAttMaxRows = 16;
+
+// Floats of a part in the workspace: outputs, then maximum and sum of 16 rows.
+template <int D, int R>
+__host__ __device__ constexpr size_t att_part_floats() { return AttShape<D, R>::kPart + 32; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -84,6 +96,17 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
 __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
   F2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
 
@@ -164,7 +187,7 @@ struct AttRow {
   int tiles, stages;            // query tiles; stages of each
 };
 
-template <int D>
+template <int D, int R>
 __device__ __forceinline__ AttRow att_row(const Kv4AttendParams &p, int b, bool report) {
   AttRow r;
   r.start = p.q_start[b];
@@ -181,20 +204,54 @@ __device__ __forceinline__ AttRow att_row(const Kv4AttendParams &p, int b, bool 
   }
   r.span = span, r.count = count, r.len = min(max(len, 0), cap);
   const int G = p.g.H_q / p.g.H_kv;
-  r.tiles = int(((long long)span * G + kAttRows - 1) / kAttRows);
-  r.stages = count > 0 ? max(1, (r.len + AttShape<D>::ST - 1) / AttShape<D>::ST) : 1;
+  r.tiles = int(((long long)span * G + R - 1) / R);
+  r.stages = count > 0 ? max(1, (r.len + AttShape<D, R>::ST - 1) / AttShape<D, R>::ST) : 1;
   return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_constant__ Kv4AttendParams p) {
-  using S = AttShape<D>;
-  constexpr int W = S::W, ST = S::ST, NT = S::NT;
+// Exclusive prefix of v over a CTA of NW warps, and the sum.
+template <int NW>
+__device__ __forceinline__ long long att_scan(long long v, long long *s_warp, long long *sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  long long before = lane < warp ? s_warp[lane] : 0, all = lane < NW ? s_warp[lane] : 0;
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  *sum = all;
+  return before + x - v;
+}
+
+// A unit, or the part of one that a CTA has: stages [st0, st1) of `stages`, of
+// which those below st_hi hold keys that a query sees.
+struct AttPiece {
+  int b, hk, tile, st0, st1, stages, st_hi, lim_max;
+  int more;             // another piece follows
+  long long first, end; // the unit's first place on the line, the place behind the piece
+  AttRow row;
+};
+
+template <int D, int R>
+__global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(const __grid_constant__ Kv4AttendParams p) {
+  using S = AttShape<D, R>;
+  constexpr int W = S::W, ST = S::ST, NT = S::NT, NW = S::NW, X = S::X;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t s_full[kAttWarps][S::kSlots];
-  __shared__ float s_m[kAttWarps][kAttRows], s_l[kAttWarps][kAttRows];
-  __shared__ long long s_scan[kAttThreads];
+  __shared__ uint64_t s_full[NW][S::kSlots];
+  __shared__ float s_m[NW][R], s_l[NW][R];
+  __shared__ int s_scr[NW];
+  __shared__ long long s_warp[NW];
   __shared__ long long s_place[2];
+  __shared__ AttPiece s_piece[2];
   __shared__ int s_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = lane >> 2, j = lane & 3;
@@ -207,221 +264,227 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
   pdl_trigger();
 
   // ---- this CTA's piece of the line ----------------------------------------------
-  long long mine = 0;
-  for (int b = tid; b < p.g.B; b += kAttThreads) {
-    const AttRow r = att_row<D>(p, b, blockIdx.x == 0);
+  long long mine = 0, total;
+#pragma unroll 1
+  for (int b = tid; b < p.g.B; b += S::kThreads) {
+    const AttRow r = att_row<D, R>(p, b, blockIdx.x == 0);
     mine += (long long)r.tiles * r.stages;
   }
-  s_scan[tid] = mine;
-  __syncthreads();
-  long long total = 0;
-  for (int i = 0; i < min(kAttThreads, p.g.B); ++i) total += s_scan[i];
+  att_scan<NW>(mine, s_warp, &total);
   total *= Hkv;
   if (total == 0) return;
   // a CTA wants a stage for each warp at least
-  const long long ctas = min((long long)gridDim.x, (total + kAttWarps - 1) / kAttWarps);
-  const long long c = blockIdx.x;
+  const int ctas = int(min((long long)gridDim.x, (total + NW - 1) / NW));
+  const int c = blockIdx.x;
   if (c >= ctas) return;
-  long long at = total * c / ctas;
-  const long long stop = total * (c + 1) / ctas;
+  // pieces of `per` stages, the first `more` of one more
+  const long long per = total / ctas;
+  const int more = int(total - per * ctas);
+  const long long at = per * c + min(c, more), stop = at + per + (c < more);
+  auto cta_of = [&](long long x) -> int {
+    const long long y = x - more * (per + 1);
+    return int(y < 0 ? x / (per + 1) : more + y / per);
+  };
   // the row that holds `at`
-  int b = 0;
-  long long row0 = 0;
-  for (int b0 = 0; b0 < p.g.B; b0 += kAttThreads) {
-    __syncthreads();
-    long long v = 0;
+  long long before0 = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.g.B; b0 += S::kThreads) {
+    long long v = 0, sum;
     if (b0 + tid < p.g.B) {
-      const AttRow r = att_row<D>(p, b0 + tid, false);
+      const AttRow r = att_row<D, R>(p, b0 + tid, false);
       v = (long long)r.tiles * r.stages * Hkv;
     }
-    s_scan[tid] = v;
-    if (tid == 0) s_place[0] = -1;
-    __syncthreads();
-    long long before = row0, all = 0;
-    for (int i = 0; i < min(kAttThreads, p.g.B - b0); ++i) {
-      const long long x = s_scan[i];
-      if (i < tid) before += x;
-      all += x;
-    }
-    if (at >= before && at < before + v) s_place[0] = b0 + tid, s_place[1] = before;
-    __syncthreads();
-    if (s_place[0] >= 0) {
-      b = int(s_place[0]), row0 = s_place[1];
-      break;
-    }
-    row0 += all;
+    const long long before = before0 + att_scan<NW>(v, s_warp, &sum);
+    if (at >= before && at < before + v) s_place[0] = b0 + tid, s_place[1] = at - before;
+    before0 += sum;
+    if (at < before0) break;
   }
+  __syncthreads();
 
   uint8_t *ring = smem + warp * S::kRing;
-  float *join = reinterpret_cast<float *>(ring);
   float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
   uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
-  uint32_t phases = 0;  // parity of each ring slot
-  bool dead = false;    // a copy never came: nothing more is waited for
-  AttRow row = att_row<D>(p, b, false);
+  uint32_t phases = 0;      // parity of each ring slot
+  int slot = 0, in = 0;     // next slot to read and to fill
+  bool dead = false;        // a copy never came: nothing more is issued
 
-  while (at < stop) {
-    while (at >= row0 + (long long)row.tiles * row.stages * Hkv) {
-      row0 += (long long)row.tiles * row.stages * Hkv;
-      row = att_row<D>(p, ++b, false);
+  // a piece's extent and limits, from its rows' queries
+  auto close = [&](AttPiece &u, long long from) {
+    u.stages = u.row.stages;
+    u.st1 = int(min((long long)u.stages, u.st0 + (stop - from)));
+    u.first = from - u.st0, u.end = from + (u.st1 - u.st0), u.more = u.end < stop;
+    const int first = u.tile * R / G;
+    const int last = min(((u.tile + 1) * R - 1) / G, u.row.count - 1);
+    u.lim_max = last >= first ? max(0, u.row.len - u.row.count + last + 1) : 0;
+    u.st_hi = min(u.st1, (u.lim_max + ST - 1) / ST);
+  };
+  if (tid == 0) {
+    AttPiece u;
+    u.b = int(s_place[0]);
+    u.row = att_row<D, R>(p, u.b, false);
+    const int x = int(s_place[1] / u.row.stages);
+    u.st0 = int(s_place[1] - (long long)x * u.row.stages);
+    u.hk = x / u.row.tiles, u.tile = x - u.hk * u.row.tiles;
+    close(u, at);
+    s_piece[0] = u;
+  }
+  __syncthreads();
+  uint32_t turn = 0;  // s_piece[turn & 1] is the current piece
+
+  // ---- copies: a page is one copy, as it lies in memory (copies are taken one in
+  // about 70 cycles whatever their size); half of a page is four pieces ---------------
+  const bool half_page = P > ST;
+  const int n_sub = half_page ? 4 : ST >> p.g.log2P;
+  const uint32_t rec_bytes = kv4_record_bytes(D, P);
+  auto page_of = [&](const AttPiece &u, int st) -> int {
+    const int t = st * ST + (half_page ? 0 : lane << p.g.log2P);
+    return lane < n_sub && t < u.lim_max && st < u.st_hi ? p.table[size_t(u.b) * p.g.max_pages + (t >> p.g.log2P)] : -2;
+  };
+  auto issue = [&](const AttPiece &u, int st, int page) {
+    bool ok = page != -2;
+    if (ok && (page < 0 || page >= p.g.n_pages)) {
+      ok = false;
+      atomicOr(p.status, GDN_STATUS_BAD_INDEX);
     }
-    const long long in_row = at - row0;
-    const int unit = int(in_row / row.stages), st0 = int(in_row - (long long)unit * row.stages);
-    const int hk = unit / row.tiles, tile = unit - hk * row.tiles;
-    const long long unit_first = at - st0, unit_end = unit_first + row.stages;
-    const int st1 = int(min((long long)row.stages, st0 + (stop - at)));
+    const uint32_t pages = __popc(__ballot_sync(0xffffffffu, ok));
+    uint64_t *bar = &s_full[warp][in];
+    if (lane == 0) mbar_arrive_expect_tx(bar, half_page ? (pages ? uint32_t(S::kStage) : 0u) : pages * rec_bytes);
+    __syncwarp();
+    if (ok) {
+      const uint8_t *rec = p.pages + (size_t(page) * Hkv + u.hk) * rec_bytes;
+      uint8_t *dst = ring + in * S::kStage;
+      if (half_page) {  // K, V codes, K, V entries by lanes 0 .. 3
+        const int off = (st * ST) & (P - 1);
+        const bool codes = lane < 2, second = lane & 1;
+        bulk_g2s(dst + (codes ? second * S::kCodes : 2 * S::kCodes + second * S::kEntries),
+                 rec + (codes ? second * kv4_code_bytes(D, P) + off * (D / 2)
+                              : 2 * kv4_code_bytes(D, P) + second * kv4_entry_bytes(D, P) + off * W * 4),
+                 codes ? S::kCodes : S::kEntries, bar);
+      } else {
+        bulk_g2s(dst + lane * rec_bytes, rec, rec_bytes, bar);
+      }
+    }
+    in = in + 1 == S::kSlots ? 0 : in + 1;
+  };
+  // places of a stage's keys: `pt` keys (a page, or the half of one) a record
+  const int log2pt = min(p.g.log2P, ST == 32 ? 5 : 6), pt = 1 << log2pt;
+  const int rec_c = pt * (D / 2), rec_e = pt * (W * 4), rec_s = 2 * (rec_c + rec_e);
+  auto code_at = [&](const uint8_t *stage, int which, int key) {
+    return stage + (key >> log2pt) * rec_s + which * rec_c + (key & (pt - 1)) * (D / 2);
+  };
+  auto entry_at = [&](const uint8_t *stage, int which, int key) {
+    return stage + (key >> log2pt) * rec_s + 2 * rec_c + which * rec_e + (key & (pt - 1)) * (W * 4);
+  };
 
-    // ---- the tile's queries ----------------------------------------------------
-    const int R0 = tile * kAttRows + n, R1 = R0 + 8;
+  int issued = s_piece[0].st0 + warp;  // next stage of the piece to issue
+  int next = page_of(s_piece[0], issued);
+  auto fill = [&](const AttPiece &u, int most) {  // up to `most` stages
+#pragma unroll 1
+    for (int i = 0; i < most && issued < u.st_hi && !dead; ++i) {
+      const int page = next;
+      next = page_of(u, issued + NW);
+      issue(u, issued, page);
+      issued += NW;
+    }
+  };
+  fill(s_piece[0], S::kSlots);
+
+  for (;;) {
+    const AttPiece &cur = s_piece[turn & 1];
+    const int lim_max = cur.lim_max, st_hi = cur.st_hi;
+    // ---- the tile's queries: rows n and (R = 16) n + 8 ---------------------------------
+    const AttRow row = cur.row;
+    const int R0 = cur.tile * R + n, R1 = R0 + 8;
     const int i0 = R0 / G, i1 = R1 / G;
-    const int tok0 = row.start + i0, tok1 = row.start + i1;
-    const bool in0 = i0 < row.span, in1 = i1 < row.span;
-    const int head0 = hk * G + R0 - i0 * G, head1 = hk * G + R1 - i1 * G;
-    // keys that the row's query sees; rows past the span follow the others
+    const bool in0 = i0 < row.span, in1 = R == 16 && i1 < row.span;
     const bool live0 = in0 && i0 < row.count, live1 = in1 && i1 < row.count;
-    int lim0 = live0 ? max(0, row.len - row.count + i0 + 1) : 0, lim1 = live1 ? max(0, row.len - row.count + i1 + 1) : 0;
-    const int lim_max = __reduce_max_sync(0xffffffffu, max(lim0, lim1));
-    if (!in0) lim0 = lim_max;
-    if (!in1) lim1 = lim_max;
+    // keys that the row's query sees; rows past the span follow the others
+    const int lim0 = live0 ? max(0, row.len - row.count + i0 + 1) : in0 ? 0 : lim_max;
+    const int lim1 = live1 ? max(0, row.len - row.count + i1 + 1) : in1 ? 0 : lim_max;
     const int lim_min = __reduce_min_sync(0xffffffffu, min(lim0, lim1));
-    const int st_hi = min(st1, (lim_max + ST - 1) / ST);
-
-    // ---- copies: a page is one copy, as it lies in memory (copies are taken one in
-    // about 70 cycles whatever their size); half of a page is four pieces ---------------
-    const bool half_page = P > ST;
-    const int n_sub = half_page ? 4 : ST >> p.g.log2P;
-    const int32_t *table = p.table + size_t(b) * p.g.max_pages;
-    const uint32_t rec_bytes = kv4_record_bytes(D, P);
-    const uint8_t *head_pages = p.pages + size_t(hk) * rec_bytes;
-    auto page_of = [&](int st) -> int {
-      const int t = st * ST + (half_page ? 0 : lane << p.g.log2P);
-      return lane < n_sub && t < lim_max && st < st_hi ? table[t >> p.g.log2P] : -2;
-    };
-    auto issue = [&](int st, int slot, int page) {
-      bool ok = page != -2;
-      if (ok && (page < 0 || page >= p.g.n_pages)) {
-        ok = false;
-        atomicOr(p.status, GDN_STATUS_BAD_INDEX);
-      }
-      const uint32_t pages = __popc(__ballot_sync(0xffffffffu, ok));
-      if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][slot], half_page ? (pages ? uint32_t(S::kStage) : 0u) : pages * rec_bytes);
-      __syncwarp();
-      if (ok) {
-        const uint8_t *rec = head_pages + size_t(page) * (Hkv * size_t(rec_bytes));
-        uint8_t *dst = ring + slot * S::kStage;
-        if (half_page) {  // K, V codes, K, V entries by lanes 0 .. 3
-          const int off = (st * ST) & (P - 1);
-          const bool codes = lane < 2, second = lane & 1;
-          bulk_g2s(dst + (codes ? second * S::kCodes : 2 * S::kCodes + second * S::kEntries),
-                   rec + (codes ? second * kv4_code_bytes(D, P) + off * (D / 2)
-                                : 2 * kv4_code_bytes(D, P) + second * kv4_entry_bytes(D, P) + off * W * 4),
-                   codes ? S::kCodes : S::kEntries, &s_full[warp][slot]);
-        } else {
-          bulk_g2s(dst + lane * rec_bytes, rec, rec_bytes, &s_full[warp][slot]);
-        }
-      }
-    };
-    // places of a stage's keys: `pt` keys (a page, or the half of one) a record
-    const int log2pt = min(p.g.log2P, ST == 32 ? 5 : 6), pt = 1 << log2pt;
-    const int rec_c = pt * (D / 2), rec_e = pt * (W * 4), rec_s = 2 * (rec_c + rec_e);
-    auto code_at = [&](const uint8_t *stage, int which, int key) {
-      return stage + (key >> log2pt) * rec_s + which * rec_c + (key & (pt - 1)) * (D / 2);
-    };
-    auto entry_at = [&](const uint8_t *stage, int which, int key) {
-      return stage + (key >> log2pt) * rec_s + 2 * rec_c + which * rec_e + (key & (pt - 1)) * (W * 4);
-    };
-    int next = page_of(st0 + warp);
-    int issued = st0 + warp;  // next stage to issue
-    int slot_in = 0;
-#pragma unroll
-    for (int i = 0; i < S::kSlots; ++i) {
-      if (issued < st_hi && !dead) {
-        const int page = next;
-        next = page_of(issued + kAttWarps);
-        issue(issued, slot_in, page);
-        issued += kAttWarps;
-        slot_in = slot_in + 1 == S::kSlots ? 0 : slot_in + 1;
-      }
-    }
 
     // ---- Q as fp16 fragments, scaled by a power of two per row -------------------------
-    uint32_t qa[D / 16][4];
+    uint32_t qa[D / 16][R / 4];  // rows n (, n + 8) of columns 0-7, then of columns 8-15
     float qs0[W], qs1[W];
-    float f0, f1;
-    {
-      uint32_t mx0 = 0, mx1 = 0;
-      uint4 raw0[D / 32], raw1[D / 32];
-      const uint16_t *src0 = p.q + (size_t(tok0) * p.g.H_q + head0) * D;
-      const uint16_t *src1 = p.q + (size_t(tok1) * p.g.H_q + head1) * D;
+    float f0 = fabsf(p.scale) * 1.4426950408889634f * 16777216.f, f1 = f0;  // 2^24 of the subnormal codes
+    // the factor of a score is kept positive: the maximum is taken before it
+    const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
+    if (p.scale == 0.f) f0 = f1 = 1.f;
+#pragma unroll
+    for (int h = 0; h < R / 8; ++h) {
+      const bool live = h ? live1 : live0;
+      const int tok = row.start + (h ? i1 : i0), head = cur.hk * G + (h ? R1 - i1 * G : R0 - i0 * G);
+      const uint16_t *src = p.q + (size_t(live ? tok : 0) * p.g.H_q + (live ? head : 0)) * D;
+      uint4 raw[D / 32];
+      uint32_t mx = 0;
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
-        // word w of the lane: channels 8 * (4 * (w / WL) ... ) as the keys' words below
+        // word w of the lane: the channels of the keys' words below
         const int ch = D == 64 ? 16 * j + 8 * w : 128 * (w >> 2) + 32 * j + 8 * (w & 3);
-        raw0[w] = live0 ? *reinterpret_cast<const uint4 *>(src0 + ch) : make_uint4(0, 0, 0, 0);
-        raw1[w] = live1 ? *reinterpret_cast<const uint4 *>(src1 + ch) : make_uint4(0, 0, 0, 0);
+        raw[w] = live ? *reinterpret_cast<const uint4 *>(src + ch) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
-        const uint32_t a[4] = {raw0[w].x, raw0[w].y, raw0[w].z, raw0[w].w};
-        const uint32_t d[4] = {raw1[w].x, raw1[w].y, raw1[w].z, raw1[w].w};
+        const uint32_t a[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          mx0 = max(mx0, max(a[e] & 0x7fffu, (a[e] >> 16) & 0x7fffu));
-          mx1 = max(mx1, max(d[e] & 0x7fffu, (d[e] >> 16) & 0x7fffu));
-        }
+        for (int e = 0; e < 4; ++e) mx = max(mx, max(a[e] & 0x7fffu, (a[e] >> 16) & 0x7fffu));
       }
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        mx0 = max(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = max(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-      }
-      // the largest magnitude goes to [2^10, 2^11); exponents kept where both
-      // powers of two are normal numbers
-      const int e0 = min(max(int(mx0 >> 7), 20), 240), e1 = min(max(int(mx1 >> 7), 20), 240);
-      const float up0 = __uint_as_float(uint32_t(264 - e0) << 23), up1 = __uint_as_float(uint32_t(264 - e1) << 23);
-      // back to the score in base 2: 1 / up, 2^24 of the subnormal codes, scale * log2(e)
-      f0 = (1.f / up0) * (p.scale * 1.4426950408889634f) * 16777216.f;
-      f1 = (1.f / up1) * (p.scale * 1.4426950408889634f) * 16777216.f;
+      for (int o = 1; o < 4; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // the largest magnitude goes to [2^10, 2^11)
+      const int e = min(max(int(mx >> 7), 20), 240);
+      const float s2 = __uint_as_float(uint32_t(264 - e) << 23), up = s2 * sign;
+      (h ? f1 : f0) *= 1.f / s2;
+      float qs[W];
 #pragma unroll
-      for (int g = 0; g < W; ++g) qs0[g] = qs1[g] = 0.f;
+      for (int g = 0; g < W; ++g) qs[g] = 0.f;
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
-        const int g = D == 64 ? 0 : w % W;
-        float x[8], y[8];
-        const uint32_t a[4] = {raw0[w].x, raw0[w].y, raw0[w].z, raw0[w].w};
-        const uint32_t d[4] = {raw1[w].x, raw1[w].y, raw1[w].z, raw1[w].w};
+        float x[8];
+        const uint32_t a[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = __uint_as_float(a[e] << 16) * up0, x[2 * e + 1] = __uint_as_float(a[e] & 0xffff0000u) * up0;
-          y[2 * e] = __uint_as_float(d[e] << 16) * up1, y[2 * e + 1] = __uint_as_float(d[e] & 0xffff0000u) * up1;
-        }
+        for (int k = 0; k < 4; ++k)
+          x[2 * k] = __uint_as_float(a[k] << 16) * up, x[2 * k + 1] = __uint_as_float(a[k] & 0xffff0000u) * up;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qs0[g] += x[e], qs1[g] += y[e];
+        for (int k = 0; k < 8; ++k) qs[w % W] += x[k];
         // step 2w: columns (0, 4) and (1, 5) / 16; step 2w + 1: (2, 6) and (3, 7) / 16
-        qa[2 * w][0] = pack_h2(x[0], x[4]), qa[2 * w][1] = pack_h2(y[0], y[4]);
-        qa[2 * w][2] = pack_h2(x[1] * 0.0625f, x[5] * 0.0625f), qa[2 * w][3] = pack_h2(y[1] * 0.0625f, y[5] * 0.0625f);
-        qa[2 * w + 1][0] = pack_h2(x[2], x[6]), qa[2 * w + 1][1] = pack_h2(y[2], y[6]);
-        qa[2 * w + 1][2] = pack_h2(x[3] * 0.0625f, x[7] * 0.0625f), qa[2 * w + 1][3] = pack_h2(y[3] * 0.0625f, y[7] * 0.0625f);
+        qa[2 * w][h] = pack_h2(x[0], x[4]), qa[2 * w][R / 8 + h] = pack_h2(x[1] * 0.0625f, x[5] * 0.0625f);
+        qa[2 * w + 1][h] = pack_h2(x[2], x[6]), qa[2 * w + 1][R / 8 + h] = pack_h2(x[3] * 0.0625f, x[7] * 0.0625f);
       }
 #pragma unroll
       for (int g = 0; g < W; ++g) {
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          qs0[g] += __shfl_xor_sync(0xffffffffu, qs0[g], o);
-          qs1[g] += __shfl_xor_sync(0xffffffffu, qs1[g], o);
-        }
-        qs0[g] *= 5.9604644775390625e-08f, qs1[g] *= 5.9604644775390625e-08f;  // 2^-24, as the codes
+        for (int o = 1; o < 4; o <<= 1) qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], o);
+        (h ? qs1 : qs0)[g] = qs[g] * 5.9604644775390625e-08f;  // 2^-24, as the codes
       }
     }
 
-    float o_acc[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.f;
-    uint32_t nan0 = 0, nan1 = 0;  // groups in which the row has seen a value that is not finite
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // the piece after this one, by the warp with the fewest stages
+    if (cur.more && tid == S::kThreads - 1) {
+      AttPiece u = cur;
+      u.st0 = 0;
+      if (++u.tile == u.row.tiles) {
+        u.tile = 0;
+        if (++u.hk == Hkv) {
+          u.hk = 0;
+          do u.row = att_row<D, R>(p, ++u.b, false);
+          while (u.row.tiles == 0);
+        }
+      }
+      close(u, cur.end);
+      s_piece[(turn & 1) ^ 1] = u;
+    }
+    __syncthreads();
 
-    int slot = 0;
-    for (int st = st0 + warp; st < st_hi; st += kAttWarps) {
+    float o_acc[S::kRegs / 4][4];
+#pragma unroll
+    for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.f;
+    uint32_t nan0 = 0, nan1 = 0;  // groups in which the row has seen a value that is not finite
+    float m0 = -INFINITY, m1 = -INFINITY;
+    F2 l0 = f2(0.f, 0.f), l1 = f2(0.f, 0.f);
+
+#pragma unroll 1
+    for (int st = cur.st0 + warp; st < st_hi; st += NW) {
       if (st < issued) {  // once a wait has run out nothing more is issued, and what is in flight still waited for
         if (!att_wait(&s_full[warp][slot], (phases >> slot) & 1)) {
           dead = true;
@@ -432,9 +495,11 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
       }
       const uint8_t *stage = ring + slot * S::kStage;
       const int t_base = st * ST;
+      const bool cut = t_base + ST > lim_min;  // some query does not see all of the stage
 
-      // ---- scores ------------------------------------------------------------------
-      float s[NT][4];
+      // ---- scores, and their maximum ----------------------------------------------
+      float s[NT][X];
+      float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         float acc[W][4];
@@ -454,81 +519,78 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-          const int g = D == 64 ? 0 : w % W;
           const uint32_t x = word[w], y = x >> 8;
-          mma16816(acc[g], qa[2 * w][0], qa[2 * w][1], qa[2 * w][2], qa[2 * w][3], x & 0x000f000fu, x & 0x00f000f0u);
-          mma16816(acc[g], qa[2 * w + 1][0], qa[2 * w + 1][1], qa[2 * w + 1][2], qa[2 * w + 1][3], y & 0x000f000fu,
-                   y & 0x00f000f0u);
+          if (R == 16) {
+            mma16816(acc[w % W], qa[2 * w][0], qa[2 * w][1], qa[2 * w][2 % X], qa[2 * w][3 % X], x & 0x000f000fu, x & 0x00f000f0u);
+            mma16816(acc[w % W], qa[2 * w + 1][0], qa[2 * w + 1][1], qa[2 * w + 1][2 % X], qa[2 * w + 1][3 % X], y & 0x000f000fu,
+                     y & 0x00f000f0u);
+          } else {
+            mma16816(acc[w % W], qa[2 * w][0], 0u, qa[2 * w][1], 0u, x & 0x000f000fu, x & 0x00f000f0u);
+            mma16816(acc[w % W], qa[2 * w + 1][0], 0u, qa[2 * w + 1][1], 0u, y & 0x000f000fu, y & 0x00f000f0u);
+          }
         }
-        uint32_t x0[W], x1[W];
-        att_words<W>(x0, entry_at(stage, 0, 8 * u + att_key(2 * j)));
-        att_words<W>(x1, entry_at(stage, 0, 8 * u + att_key(2 * j + 1)));
+        uint32_t ka[W], kb[W];
+        att_words<W>(ka, entry_at(stage, 0, 8 * u + att_key(2 * j)));
+        att_words<W>(kb, entry_at(stage, 0, 8 * u + att_key(2 * j + 1)));
         F2 r0 = f2(0.f, 0.f), r1 = f2(0.f, 0.f);
 #pragma unroll
         for (int g = 0; g < W; ++g) {
-          const F2 step = f2(half_lo(x0[g]), half_lo(x1[g])), base = f2(half_hi(x0[g]), half_hi(x1[g]));
-          r0 = f2_fma(step, f2(acc[g][0], acc[g][1]), r0);
-          r1 = f2_fma(step, f2(acc[g][2], acc[g][3]), r1);
-          r0 = f2_fma(base, f2(qs0[g], qs0[g]), r0);
-          r1 = f2_fma(base, f2(qs1[g], qs1[g]), r1);
+          const F2 step = f2(half_lo(ka[g]), half_lo(kb[g])), base = f2(half_hi(ka[g]), half_hi(kb[g]));
+          r0 = f2_fma(base, f2(qs0[g], qs0[g]), f2_fma(step, f2(acc[g][0], acc[g][1]), r0));
+          if (R == 16) r1 = f2_fma(base, f2(qs1[g], qs1[g]), f2_fma(step, f2(acc[g][2], acc[g][3]), r1));
         }
         f2_get(r0, s[u][0], s[u][1]);
-        f2_get(r1, s[u][2], s[u][3]);
-      }
-      const bool cut = t_base + ST > lim_min;  // some query does not see all of the stage
-      if (cut) {
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
+        if (R == 16) f2_get(r1, s[u][2 % X], s[u][3 % X]);
+        if (cut) {
           const int ta = t_base + 8 * u + att_key(2 * j), tb = t_base + 8 * u + att_key(2 * j + 1);
           if (ta >= lim0) s[u][0] = -INFINITY;
           if (tb >= lim0) s[u][1] = -INFINITY;
-          if (ta >= lim1) s[u][2] = -INFINITY;
-          if (tb >= lim1) s[u][3] = -INFINITY;
+          if (R == 16 && ta >= lim1) s[u][2 % X] = -INFINITY;
+          if (R == 16 && tb >= lim1) s[u][3 % X] = -INFINITY;
         }
-      }
-      // ---- running maximum; the largest step of each group ----------------------------
-      // f may be negative (a negative scale): the maximum is taken after it
-      float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        if (cut) {
-          s[u][0] = s[u][0] == -INFINITY ? -INFINITY : s[u][0] * f0;
-          s[u][1] = s[u][1] == -INFINITY ? -INFINITY : s[u][1] * f0;
-          s[u][2] = s[u][2] == -INFINITY ? -INFINITY : s[u][2] * f1;
-          s[u][3] = s[u][3] == -INFINITY ? -INFINITY : s[u][3] * f1;
-        } else {
-          s[u][0] *= f0, s[u][1] *= f0, s[u][2] *= f1, s[u][3] *= f1;
-        }
-        x0 = fmaxf(x0, fmaxf(s[u][0], s[u][1]));
-        x1 = fmaxf(x1, fmaxf(s[u][2], s[u][3]));
+        x0 = max3(x0, s[u][0], s[u][1]);
+        if (R == 16) x1 = max3(x1, s[u][2 % X], s[u][3 % X]);
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+        if (R == 16) x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
       }
-      if (__any_sync(0xffffffffu, x0 > m0 + 14.f || x1 > m1 + 14.f)) {
+      x0 *= f0, x1 *= f1;
+      if (__any_sync(0xffffffffu, x0 > m0 + 14.f || (R == 16 && x1 > m1 + 14.f))) {
         const float n0 = fmaxf(m0, x0 - 6.f), n1 = fmaxf(m1, x1 - 6.f);
         const float a0 = n0 == m0 ? 1.f : ex2(m0 - n0), a1 = n1 == m1 ? 1.f : ex2(m1 - n1);
         m0 = n0, m1 = n1;
-        l0 *= a0, l1 *= a1;
+        l0 = f2_mul(l0, f2(a0, a0)), l1 = f2_mul(l1, f2(a1, a1));
+        if (R == 16) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) o_acc[i][0] *= a0, o_acc[i][1] *= a0, o_acc[i][2] *= a1, o_acc[i][3] *= a1;
+          for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] *= a0, o_acc[i][1] *= a0, o_acc[i][2] *= a1, o_acc[i][3] *= a1;
+        } else {  // columns 2j, 2j + 1 are the rows
+          const float ca = __shfl_sync(0xffffffffu, a0, 8 * j), cb = __shfl_sync(0xffffffffu, a0, 8 * j + 4);
+#pragma unroll
+          for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] *= ca, o_acc[i][1] *= cb, o_acc[i][2] *= ca, o_acc[i][3] *= cb;
+        }
       }
-      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+      const float r0 = m0 == -INFINITY ? 0.f : -m0, r1 = m1 == -INFINITY ? 0.f : -m1;
 
       // ---- probabilities and output, 16 keys at a time --------------------------------
 #pragma unroll
       for (int h = 0; h < NT / 2; ++h) {
-        uint32_t a[4], es[W][2], eb[W][2];  // P; (step, step), (base, base) of the key pairs
+        uint32_t a[X], es[W][2], eb[W][2];  // P; (step, step), (base, base) of the key pairs
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int u = 2 * h + half;
-          const float p00 = ex2(s[u][0] - r0), p01 = ex2(s[u][1] - r0);
-          const float p10 = ex2(s[u][2] - r1), p11 = ex2(s[u][3] - r1);
-          l0 += p00 + p01, l1 += p10 + p11;
-          a[2 * half] = pack_h2(p00, p01);
-          a[2 * half + 1] = pack_h2(p10, p11);
+          float pa, pb;
+          f2_get(f2_fma(f2(s[u][0], s[u][1]), f2(f0, f0), f2(r0, r0)), pa, pb);
+          pa = ex2(pa), pb = ex2(pb);
+          l0 = f2_add(l0, f2(pa, pb));
+          a[R == 16 ? 2 * half : half] = pack_h2(pa, pb);
+          if (R == 16) {
+            f2_get(f2_fma(f2(s[u][2 % X], s[u][3 % X]), f2(f1, f1), f2(r1, r1)), pa, pb);
+            pa = ex2(pa), pb = ex2(pb);
+            l1 = f2_add(l1, f2(pa, pb));
+            a[(2 * half + 1) % X] = pack_h2(pa, pb);
+          }
           const int ka = 8 * u + att_key(2 * j), kb = 8 * u + att_key(2 * j + 1);
           uint32_t wa[W], wb[W];
           att_words<W>(wa, entry_at(stage, 1, ka));
@@ -562,156 +624,183 @@ __global__ void __launch_bounds__(kAttThreads, 2) kv4_attend_mma(const __grid_co
           for (int half = 0; half < 2; ++half) {
             const uint32_t x = __byte_perm(w0[g], w1[g], half ? 0x7632 : 0x5410);
             const uint32_t y = __byte_perm(w2[g], w3[g], half ? 0x7632 : 0x5410);
-            const uint32_t xs = x >> 8, ys = y >> 8;
+            const uint32_t v00 = att_even(x, es[g][0], eb[g][0]), v01 = att_even(y, es[g][1], eb[g][1]);
+            const uint32_t v10 = att_odd(x, es[g][0], eb[g][0]), v11 = att_odd(y, es[g][1], eb[g][1]);
+            const uint32_t v20 = att_even(x >> 8, es[g][0], eb[g][0]), v21 = att_even(y >> 8, es[g][1], eb[g][1]);
+            const uint32_t v30 = att_odd(x >> 8, es[g][0], eb[g][0]), v31 = att_odd(y >> 8, es[g][1], eb[g][1]);
             const int o = 8 * g + 4 * half;
-            mma16816(o_acc[o], a[0], a[1], a[2], a[3], att_even(x, es[g][0], eb[g][0]), att_even(y, es[g][1], eb[g][1]));
-            mma16816(o_acc[o + 1], a[0], a[1], a[2], a[3], att_odd(x, es[g][0], eb[g][0]), att_odd(y, es[g][1], eb[g][1]));
-            mma16816(o_acc[o + 2], a[0], a[1], a[2], a[3], att_even(xs, es[g][0], eb[g][0]), att_even(ys, es[g][1], eb[g][1]));
-            mma16816(o_acc[o + 3], a[0], a[1], a[2], a[3], att_odd(xs, es[g][0], eb[g][0]), att_odd(ys, es[g][1], eb[g][1]));
+            if (R == 16) {
+              mma16816(o_acc[o % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v00, v01);
+              mma16816(o_acc[(o + 1) % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v10, v11);
+              mma16816(o_acc[(o + 2) % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v20, v21);
+              mma16816(o_acc[(o + 3) % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v30, v31);
+            } else {
+              mma16816(o_acc[o / 2], v00, v10, v01, v11, a[0], a[1]);
+              mma16816(o_acc[o / 2 + 1], v20, v30, v21, v31, a[0], a[1]);
+            }
           }
         }
       }
       __syncwarp();  // every lane is done with the slot
       if (issued < st_hi && !dead) {
         const int page = next;
-        next = page_of(issued + kAttWarps);
-        issue(issued, slot, page);
-        issued += kAttWarps;
+        next = page_of(cur, issued + NW);
+        issue(cur, issued, page);
+        issued += NW;
       }
       slot = slot + 1 == S::kSlots ? 0 : slot + 1;
     }
-    // the ring starts again at slot 0: all its copies of this piece have been waited for
+
+    // ---- the next piece's first stages on their way ----------------------------------------
+    if (cur.more) {
+      in = slot;  // every copy of this piece has been waited for
+      issued = warp;
+      next = page_of(s_piece[(turn & 1) ^ 1], issued);
+      fill(s_piece[(turn & 1) ^ 1], S::kAhead);
+    }
+
     // ---- this warp's part: outputs, maximum and sum of its keys -----------------------
+    float la, lb, l0s, l1s;
+    f2_get(l0, la, lb);
+    l0s = la + lb;
+    f2_get(l1, la, lb);
+    l1s = la + lb;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+      l0s += __shfl_xor_sync(0xffffffffu, l0s, o);
       nan0 |= __shfl_xor_sync(0xffffffffu, nan0, o);
-      nan1 |= __shfl_xor_sync(0xffffffffu, nan1, o);
+      if (R == 16) {
+        l1s += __shfl_xor_sync(0xffffffffu, l1s, o);
+        nan1 |= __shfl_xor_sync(0xffffffffu, nan1, o);
+      }
     }
-    __syncwarp();
+    // the ring's slots before the next to read, the last kScratch of them
+    const bool has = cur.st0 + warp < cur.st_hi;
+    auto scratch = [&](int w, int from, int i) -> float * {  // accumulator i of warp w's part
+      int k = from - 1 - i / S::kRegsSlot;
+      k += k < 0 ? S::kSlots : 0;
+      return reinterpret_cast<float *>(smem + w * S::kRing + k * S::kStage) + (i % S::kRegsSlot) * 32;
+    };
+    if (has) {
+      const float nan = __uint_as_float(0x7fc00000u);
+      uint32_t na = nan0, nb = nan1;
+      if (R == 8) na = __shfl_sync(0xffffffffu, nan0, 8 * j), nb = __shfl_sync(0xffffffffu, nan0, 8 * j + 4);
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+      for (int t = 0; t < D / 8; ++t)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        join[(i * 4 + k) * 32 + lane] = ((k < 2 ? nan0 : nan1) >> (i / 8) & 1u) ? __uint_as_float(0x7fc00000u) : o_acc[i][k];
-    if (j == 0) s_m[warp][n] = m0, s_m[warp][n + 8] = m1, s_l[warp][n] = l0, s_l[warp][n + 8] = l1;
+        for (int x = 0; x < X; ++x) {
+          const int i = S::reg(t, x);
+          const uint32_t mask = R == 16 ? (x < 2 ? na : nb) : (x ? nb : na);
+          scratch(warp, slot, i)[lane] = mask >> (t / 8) & 1u ? nan : o_acc[i / 4][i % 4];
+        }
+    }
+    if (j == 0) {
+      s_m[warp][n] = m0, s_l[warp][n] = l0s;
+      if (R == 16) s_m[warp][(n + 8) % R] = m1, s_l[warp][(n + 8) % R] = l1s;
+    }
+    if (lane == 0) s_scr[warp] = slot;
     __syncthreads();
 
-    // ---- join of the warps: warp w has the 8-channel tiles [w D / 32, (w + 1) D / 32) ------
-    constexpr int TW = D / 8 / kAttWarps;
-    float y[TW][4], M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < TW; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
-    {
-      float c0[kAttWarps], c1[kAttWarps];
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) M0 = fmaxf(M0, s_m[w][n]), M1 = fmaxf(M1, s_m[w][n + 8]);
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) {
-        c0[w] = s_m[w][n] == -INFINITY ? 0.f : ex2(s_m[w][n] - M0);
-        c1[w] = s_m[w][n + 8] == -INFINITY ? 0.f : ex2(s_m[w][n + 8] - M1);
-        // a NaN score leaves the maximum alone but not the sum
-        if (s_l[w][n] != s_l[w][n]) c0[w] = 1.f;
-        if (s_l[w][n + 8] != s_l[w][n + 8]) c1[w] = 1.f;
-        L0 = fmaf(s_l[w][n], c0[w], L0), L1 = fmaf(s_l[w][n + 8], c1[w], L1);
-      }
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) {
-        const float *src = reinterpret_cast<const float *>(smem + w * S::kRing);
-#pragma unroll
-        for (int i = 0; i < TW; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[i][k] = fmaf(src[((warp * TW + i) * 4 + k) * 32 + lane], k < 2 ? c0[w] : c1[w], y[i][k]);
-      }
-    }
-
-    // ---- the whole unit, or a part of it ------------------------------------------------
-    bool whole = unit_first >= at && unit_end <= at + (st1 - st0);
-    if (!whole) {
-      const long long c_first = ((unit_first + 1) * ctas - 1) / total, c_last = (unit_end * ctas - 1) / total;
-      float *part = parts + (size_t(c) * 2 + (c == c_first ? 1 : 0)) * att_part_floats<D>();
-#pragma unroll
-      for (int i = 0; i < TW; ++i)
-        *reinterpret_cast<float4 *>(part + ((warp * TW + i) * 32 + lane) * 4) = make_float4(y[i][0], y[i][1], y[i][2], y[i][3]);
-      if (warp == 0 && j == 0) {
-        part[S::kPart + n] = M0, part[S::kPart + n + 8] = M1;
-        part[S::kPart + 16 + n] = L0, part[S::kPart + 16 + n + 8] = L1;
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t need = uint32_t(c_last - c_first + 1);
-        const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
-        s_flag = done == need;
-        if (done == need) counters[c_first] = 0;  // ready for the next call
+    // ---- join of the warps, and of the CTAs if the unit is cut -------------------------
+    const int warps = min(NW, max(0, cur.st_hi - cur.st0));
+    const bool whole = cur.st0 == 0 && cur.st1 == cur.stages;
+    const int c_first = whole ? c : cta_of(cur.first), c_last = whole ? c : cta_of(cur.first + cur.stages - 1);
+    auto part_of = [&](int k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * att_part_floats<D, R>(); };
+    constexpr int kItems = (S::kQuads + S::kThreads - 1) / S::kThreads;
+    // item: 4 channels (g, eh) of value x; q: its group of lanes
+    auto weight = [](float m, float l, float M) { return l != l ? 1.f : m == -INFINITY ? 0.f : ex2(m - M); };
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass == 1) {
+        if (whole) break;
         __threadfence();
-      }
-      __syncthreads();
-      whole = s_flag != 0;
-      if (whole) {
-        M0 = M1 = -INFINITY;
-        for (long long k = c_first; k <= c_last; ++k) {
-          const float *src = parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * att_part_floats<D>();
-          M0 = fmaxf(M0, __ldcg(src + S::kPart + n)), M1 = fmaxf(M1, __ldcg(src + S::kPart + n + 8));
+        __syncthreads();
+        if (tid == 0) {
+          const uint32_t need = uint32_t(c_last - c_first + 1);
+          const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
+          s_flag = done == need;
+          if (done == need) counters[c_first] = 0;  // ready for the next call
+          __threadfence();
         }
-        L0 = L1 = 0.f;
+        __syncthreads();
+        if (!s_flag) break;
+      }
+#pragma unroll 1
+      for (int k = 0; k < kItems; ++k) {
+        const int item = k * S::kThreads + tid;
+        if (item >= S::kQuads) break;
+        const int ln = item & 31, quad = item >> 5, x = quad % X, t0 = quad / X * 4;  // channel tiles t0 .. t0 + 3
+        const int nn = ln >> 2, jj = ln & 3;
+        const int r = R == 16 ? nn + (x >> 1) * 8 : 2 * jj + x;
+        const int col = R == 16 ? 2 * jj + (x & 1) : nn;
+        float M = -INFINITY, L = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+        if (pass == 0) {
+#pragma unroll 4
+          for (int w = 0; w < warps; ++w) M = fmaxf(M, s_m[w][r]);
+#pragma unroll 2
+          for (int w = 0; w < warps; ++w) {
+            const float cw = weight(s_m[w][r], s_l[w][r], M);
+            L = fmaf(s_l[w][r], cw, L);
+            const int from = s_scr[w];
 #pragma unroll
-        for (int i = 0; i < TW; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
-        for (long long k = c_first; k <= c_last; ++k) {
-          const float *src = parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * att_part_floats<D>();
-          const float ma = __ldcg(src + S::kPart + n), mb = __ldcg(src + S::kPart + n + 8);
-          const float la = __ldcg(src + S::kPart + 16 + n), lb = __ldcg(src + S::kPart + 16 + n + 8);
-          const float c0 = la != la ? 1.f : ma == -INFINITY ? 0.f : ex2(ma - M0);
-          const float c1 = lb != lb ? 1.f : mb == -INFINITY ? 0.f : ex2(mb - M1);
-          L0 = fmaf(la, c0, L0), L1 = fmaf(lb, c1, L1);
-#pragma unroll
-          for (int i = 0; i < TW; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + ((warp * TW + i) * 32 + lane) * 4));
-            y[i][0] = fmaf(v.x, c0, y[i][0]), y[i][1] = fmaf(v.y, c0, y[i][1]);
-            y[i][2] = fmaf(v.z, c1, y[i][2]), y[i][3] = fmaf(v.w, c1, y[i][3]);
+            for (int e = 0; e < 4; ++e) y[e] = fmaf(scratch(w, from, S::reg(t0 + e, x))[ln], cw, y[e]);
+          }
+        } else {
+#pragma unroll 4
+          for (int q = c_first; q <= c_last; ++q) M = fmaxf(M, __ldcg(part_of(q) + S::kPart + r));
+#pragma unroll 4
+          for (int q = c_first; q <= c_last; ++q) {
+            const float *src = part_of(q);
+            const float lq = __ldcg(src + S::kPart + 16 + r), cq = weight(__ldcg(src + S::kPart + r), lq, M);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + item);
+            L = fmaf(lq, cq, L);
+            y[0] = fmaf(v.x, cq, y[0]), y[1] = fmaf(v.y, cq, y[1]), y[2] = fmaf(v.z, cq, y[2]), y[3] = fmaf(v.w, cq, y[3]);
+          }
+        }
+        if (pass == 0 && !whole) {
+          float *part = part_of(c);
+          *(reinterpret_cast<float4 *>(part) + item) = make_float4(y[0], y[1], y[2], y[3]);
+          if (t0 == 0 && (R == 16 ? jj == 0 && (x & 1) == 0 : nn == 0)) part[S::kPart + r] = M, part[S::kPart + 16 + r] = L;
+        } else {
+          const int rr = cur.tile * R + r, i = rr / G;
+          if (i < cur.row.span) {
+            const float v = L > 0.f ? 1.f / L : L;  // no key: 0; NaN stays
+            uint16_t *dst = p.out + (size_t(cur.row.start + i) * p.g.H_q + cur.hk * G + rr - i * G) * D + (col * W + t0 / 8) * 8 + t0 % 8;
+            const __nv_bfloat162 u0 = __floats2bfloat162_rn(y[0] * v, y[1] * v), u1 = __floats2bfloat162_rn(y[2] * v, y[3] * v);
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&u0), *reinterpret_cast<const uint32_t *>(&u1));
           }
         }
       }
     }
-    if (whole) {
-      // tile 8 g + e, column c: channel (c W + g) 8 + e; a warp holds TW (a
-      // multiple of 2) neighbouring channels of each column
-      const float v0 = L0 > 0.f ? 1.f / L0 : L0, v1 = L1 > 0.f ? 1.f / L1 : L1;  // no key: 0; NaN stays
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c8 = 2 * j + (k & 1), tok = k < 2 ? tok0 : tok1, head = k < 2 ? head0 : head1;
-        if (!(k < 2 ? in0 : in1)) continue;
-        const float v = k < 2 ? v0 : v1;
-        uint16_t *dst = p.out + (size_t(tok) * p.g.H_q + head) * D;
-#pragma unroll
-        for (int i = 0; i < TW; i += 2) {
-          const int t = warp * TW + i, ch = (c8 * W + t / 8) * 8 + t % 8;
-          const __nv_bfloat162 x = __floats2bfloat162_rn(y[i][k] * v, y[i + 1][k] * v);
-          *reinterpret_cast<__nv_bfloat162 *>(dst + ch) = x;
-        }
-      }
-    }
-    at += st1 - st0;
-    fence_proxy_async_shared();  // the join's writes before the next piece's copies
+    if (!cur.more) break;
+    ++turn;
+    fence_proxy_async_shared();  // the join's accesses before the copies that write over them
     __syncthreads();
+    fill(s_piece[turn & 1], S::kSlots - S::kAhead);
   }
 }
 
-template <int D>
+template <int D, int R>
 inline size_t att_mma_ws(int ctas) {
-  return 4096 + sizeof(float) * 2 * size_t(ctas) * att_part_floats<D>();
+  return 4096 + sizeof(float) * 2 * size_t(ctas) * att_part_floats<D, R>();
 }
 
-template <int D>
-cudaError_t launch_att_mma(const Kv4AttendParams &p, int ctas, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kv4_attend_mma<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttShape<D>::kSmem);
+template <int D, int R>
+cudaError_t launch_att_mma_r(const Kv4AttendParams &p, int ctas, cudaStream_t s) {
+  using S = AttShape<D, R>;
+  const cudaError_t e = cudaFuncSetAttribute(kv4_attend_mma<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_smem(kv4_attend_mma<D>, dim3(ctas), dim3(kAttThreads), AttShape<D>::kSmem, s, p);
+  return launch_pdl_smem(kv4_attend_mma<D, R>, dim3(ctas), dim3(S::kThreads), S::kSmem, s, p);
 }
 
-cudaError_t launch_att_mma_64(const Kv4AttendParams &p, int ctas, cudaStream_t s);
-cudaError_t launch_att_mma_128(const Kv4AttendParams &p, int ctas, cudaStream_t s);
-cudaError_t launch_att_mma_256(const Kv4AttendParams &p, int ctas, cudaStream_t s);
+// rows: query rows of a unit (8 or 16)
+template <int D>
+cudaError_t launch_att_mma(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s) {
+  return rows == 8 ? launch_att_mma_r<D, 8>(p, ctas, s) : launch_att_mma_r<D, 16>(p, ctas, s);
+}
+
+cudaError_t launch_att_mma_64(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s);
+cudaError_t launch_att_mma_128(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s);
+cudaError_t launch_att_mma_256(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s);
 
 }  // namespace gdn
