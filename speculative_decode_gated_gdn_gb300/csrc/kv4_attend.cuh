@@ -42,10 +42,10 @@ namespace gdn {
 template <int D, int R>
 struct AttShape {
   static constexpr int W = D / 64;               // groups of a head
-  static constexpr int ST = D == 64 ? 64 : 32;   // keys of a stage
-  static constexpr int NT = ST / 8;              // key tiles of a stage
-  // warps of a CTA, as many as the registers of a thread allow
-  static constexpr int NW = D == 256 ? (R == 8 ? 12 : 8) : D == 128 ? (R == 8 ? 16 : 12) : 16;
+  static constexpr int ST = D == 256 ? 32 : 64;  // keys of a stage: what a copy brings
+  static constexpr int CK = 32, NT = CK / 8;     // keys, and key tiles, taken at a time
+  // warps of a CTA, as the registers of a thread allow
+  static constexpr int NW = D == 256 ? (R == 8 ? 12 : 8) : D == 128 ? 12 : 16;
   static constexpr int kThreads = 32 * NW;
   static constexpr int kCodes = ST * D / 2, kEntries = ST * W * 4;
   static constexpr int kStage = 2 * (kCodes + kEntries);
@@ -55,7 +55,7 @@ struct AttShape {
   static constexpr int kScratch = (kRegs * 128 + kStage - 1) / kStage;  // slots a warp's part takes in the join
   static constexpr int kAhead = kSlots - kScratch;                      // slots the next unit may fill before it
   static constexpr int kRegsSlot = kRegs / kScratch;                    // accumulators a slot takes
-  static constexpr int kQuads = kRegs / 4 * 32;  // items of the join: 4 channels of a query row
+  static constexpr int kPairs = kRegs / 2 * 32;  // items of the join: 2 channels of a query row
   static constexpr int kPart = kRegs * 32;       // floats of a part
   static constexpr int kRing = kSlots * kStage;
   static constexpr int kSmem = NW * kRing + 128;
@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_full[NW][S::kSlots];
   __shared__ float s_m[NW][R], s_l[NW][R];
+  __shared__ float s_c[NW][R], s_sum[R], s_max[R], s_w[16][R], s_lw[16][R];
   __shared__ int s_scr[NW];
   __shared__ long long s_warp[NW];
-  __shared__ long long s_place[2];
   __shared__ AttPiece s_piece[2];
   __shared__ int s_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -264,14 +264,15 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   pdl_trigger();
 
   // ---- this CTA's piece of the line ----------------------------------------------
-  long long mine = 0, total;
-#pragma unroll 1
+  // rows beyond the CTA's threads are summed first and looked at again below
+  long long mine = 0, total, before = 0;
+  AttRow own{};
   for (int b = tid; b < p.g.B; b += S::kThreads) {
     const AttRow r = att_row<D, R>(p, b, blockIdx.x == 0);
-    mine += (long long)r.tiles * r.stages;
+    if (b == tid) own = r;
+    mine += (long long)r.tiles * r.stages * Hkv;
   }
-  att_scan<NW>(mine, s_warp, &total);
-  total *= Hkv;
+  before = att_scan<NW>(mine, s_warp, &total);
   if (total == 0) return;
   // a CTA wants a stage for each warp at least
   const int ctas = int(min((long long)gridDim.x, (total + NW - 1) / NW));
@@ -285,29 +286,6 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     const long long y = x - more * (per + 1);
     return int(y < 0 ? x / (per + 1) : more + y / per);
   };
-  // the row that holds `at`
-  long long before0 = 0;
-#pragma unroll 1
-  for (int b0 = 0; b0 < p.g.B; b0 += S::kThreads) {
-    long long v = 0, sum;
-    if (b0 + tid < p.g.B) {
-      const AttRow r = att_row<D, R>(p, b0 + tid, false);
-      v = (long long)r.tiles * r.stages * Hkv;
-    }
-    const long long before = before0 + att_scan<NW>(v, s_warp, &sum);
-    if (at >= before && at < before + v) s_place[0] = b0 + tid, s_place[1] = at - before;
-    before0 += sum;
-    if (at < before0) break;
-  }
-  __syncthreads();
-
-  uint8_t *ring = smem + warp * S::kRing;
-  float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
-  uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
-  uint32_t phases = 0;      // parity of each ring slot
-  int slot = 0, in = 0;     // next slot to read and to fill
-  bool dead = false;        // a copy never came: nothing more is issued
-
   // a piece's extent and limits, from its rows' queries
   auto close = [&](AttPiece &u, long long from) {
     u.stages = u.row.stages;
@@ -318,18 +296,36 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     u.lim_max = last >= first ? max(0, u.row.len - u.row.count + last + 1) : 0;
     u.st_hi = min(u.st1, (u.lim_max + ST - 1) / ST);
   };
-  if (tid == 0) {
-    AttPiece u;
-    u.b = int(s_place[0]);
-    u.row = att_row<D, R>(p, u.b, false);
-    const int x = int(s_place[1] / u.row.stages);
-    u.st0 = int(s_place[1] - (long long)x * u.row.stages);
-    u.hk = x / u.row.tiles, u.tile = x - u.hk * u.row.tiles;
-    close(u, at);
-    s_piece[0] = u;
+  // the first piece, by the thread of the row that holds `at`
+  long long before0 = 0;
+  for (int b0 = 0; b0 < p.g.B; b0 += S::kThreads) {
+    if (p.g.B > S::kThreads) {
+      if (b0 + tid < p.g.B) own = att_row<D, R>(p, b0 + tid, false);
+      else own.tiles = 0;
+      long long sum;
+      before = before0 + att_scan<NW>((long long)own.tiles * own.stages * Hkv, s_warp, &sum);
+      before0 += sum;
+    }
+    if (b0 + tid < p.g.B && at >= before && at - before < (long long)own.tiles * own.stages * Hkv) {
+      AttPiece u;
+      u.b = b0 + tid, u.row = own;
+      const int x = int((at - before) / own.stages);
+      u.st0 = int(at - before - (long long)x * own.stages);
+      u.hk = x / own.tiles, u.tile = x - u.hk * own.tiles;
+      close(u, at);
+      s_piece[0] = u;
+    }
+    if (p.g.B > S::kThreads && at < before0) break;
   }
   __syncthreads();
   uint32_t turn = 0;  // s_piece[turn & 1] is the current piece
+
+  uint8_t *ring = smem + warp * S::kRing;
+  float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
+  uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
+  uint32_t phases = 0;      // parity of each ring slot
+  int slot = 0, in = 0;     // next slot to read and to fill
+  bool dead = false;        // a copy never came: nothing more is issued
 
   // ---- copies: a page is one copy, as it lies in memory (copies are taken one in
   // about 70 cycles whatever their size); half of a page is four pieces ---------------
@@ -366,15 +362,13 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     }
     in = in + 1 == S::kSlots ? 0 : in + 1;
   };
-  // places of a stage's keys: `pt` keys (a page, or the half of one) a record
+  // places of a stage's keys: records of `pt` keys (a page, or the half of one);
+  // 16 keys always lie in one
   const int log2pt = min(p.g.log2P, ST == 32 ? 5 : 6), pt = 1 << log2pt;
   const int rec_c = pt * (D / 2), rec_e = pt * (W * 4), rec_s = 2 * (rec_c + rec_e);
-  auto code_at = [&](const uint8_t *stage, int which, int key) {
-    return stage + (key >> log2pt) * rec_s + which * rec_c + (key & (pt - 1)) * (D / 2);
-  };
-  auto entry_at = [&](const uint8_t *stage, int which, int key) {
-    return stage + (key >> log2pt) * rec_s + 2 * rec_c + which * rec_e + (key & (pt - 1)) * (W * 4);
-  };
+  const uint32_t lane_k = att_key(n) * (D / 2) + (D == 64 ? 8 : 16) * j;  // the lane's key of 8, its words
+  const uint32_t lane_v0 = att_key(2 * j) * (D / 2) + n * (4 * W), lane_v1 = att_key(2 * j + 1) * (D / 2) + n * (4 * W);
+  const uint32_t lane_e0 = att_key(2 * j) * (4 * W), lane_e1 = att_key(2 * j + 1) * (4 * W);
 
   int issued = s_piece[0].st0 + warp;  // next stage of the piece to issue
   int next = page_of(s_piece[0], issued);
@@ -493,9 +487,18 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
         dead = __any_sync(0xffffffffu, dead);
         phases ^= 1u << slot;
       }
-      const uint8_t *stage = ring + slot * S::kStage;
-      const int t_base = st * ST;
-      const bool cut = t_base + ST > lim_min;  // some query does not see all of the stage
+#pragma unroll 1
+     for (int ck = 0; ck < ST && st * ST + ck < lim_max; ck += S::CK) {
+      const int t_base = st * ST + ck;
+      // 16-key groups: K codes and K entries; the values' lie rec_c and rec_e behind
+      const uint8_t *codes[NT / 2], *entries[NT / 2];
+#pragma unroll
+      for (int h = 0; h < NT / 2; ++h) {
+        const int key = ck + 16 * h, off = key & (pt - 1);
+        const uint8_t *rec = ring + slot * S::kStage + (key >> log2pt) * rec_s;
+        codes[h] = rec + off * (D / 2), entries[h] = rec + 2 * rec_c + off * (W * 4);
+      }
+      const bool cut = t_base + S::CK > lim_min;  // some query does not see all of them
 
       // ---- scores, and their maximum ----------------------------------------------
       float s[NT][X];
@@ -505,15 +508,15 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
         float acc[W][4];
 #pragma unroll
         for (int g = 0; g < W; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-        const uint8_t *kr = code_at(stage, 0, 8 * u + att_key(n));
+        const uint8_t *kr = codes[u / 2] + lane_k + (u & 1) * (8 * (D / 2));
         uint32_t word[D / 32];
         if (D == 64) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(kr + 8 * j);
+          const uint2 x = *reinterpret_cast<const uint2 *>(kr);
           word[0] = x.x, word[1] = x.y;
         } else {
 #pragma unroll
           for (int i = 0; i < D / 128; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(kr + 64 * i + 16 * j);
+            const uint4 x = *reinterpret_cast<const uint4 *>(kr + 64 * i);
             word[4 * i] = x.x, word[4 * i + 1] = x.y, word[4 * i + 2] = x.z, word[4 * i + 3] = x.w;
           }
         }
@@ -530,8 +533,8 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
           }
         }
         uint32_t ka[W], kb[W];
-        att_words<W>(ka, entry_at(stage, 0, 8 * u + att_key(2 * j)));
-        att_words<W>(kb, entry_at(stage, 0, 8 * u + att_key(2 * j + 1)));
+        att_words<W>(ka, entries[u / 2] + lane_e0 + (u & 1) * (32 * W));
+        att_words<W>(kb, entries[u / 2] + lane_e1 + (u & 1) * (32 * W));
         F2 r0 = f2(0.f, 0.f), r1 = f2(0.f, 0.f);
 #pragma unroll
         for (int g = 0; g < W; ++g) {
@@ -593,8 +596,8 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
           }
           const int ka = 8 * u + att_key(2 * j), kb = 8 * u + att_key(2 * j + 1);
           uint32_t wa[W], wb[W];
-          att_words<W>(wa, entry_at(stage, 1, ka));
-          att_words<W>(wb, entry_at(stage, 1, kb));
+          att_words<W>(wa, entries[h] + rec_e + lane_e0 + half * (32 * W));
+          att_words<W>(wb, entries[h] + rec_e + lane_e1 + half * (32 * W));
           if (cut) {
             // a value that one query sees and another does not must not reach
             // the other as 0 * NaN: it is left out and remembered by the row
@@ -614,10 +617,10 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
           }
         }
         uint32_t w0[W], w1[W], w2[W], w3[W];
-        att_words<W>(w0, code_at(stage, 1, 16 * h + att_key(2 * j)) + n * (4 * W));
-        att_words<W>(w1, code_at(stage, 1, 16 * h + att_key(2 * j + 1)) + n * (4 * W));
-        att_words<W>(w2, code_at(stage, 1, 16 * h + 8 + att_key(2 * j)) + n * (4 * W));
-        att_words<W>(w3, code_at(stage, 1, 16 * h + 8 + att_key(2 * j + 1)) + n * (4 * W));
+        att_words<W>(w0, codes[h] + rec_c + lane_v0);
+        att_words<W>(w1, codes[h] + rec_c + lane_v1);
+        att_words<W>(w2, codes[h] + rec_c + lane_v0 + 8 * (D / 2));
+        att_words<W>(w3, codes[h] + rec_c + lane_v1 + 8 * (D / 2));
 #pragma unroll
         for (int g = 0; g < W; ++g) {
 #pragma unroll
@@ -641,6 +644,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
           }
         }
       }
+     }
       __syncwarp();  // every lane is done with the slot
       if (issued < st_hi && !dead) {
         const int page = next;
@@ -702,72 +706,115 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     __syncthreads();
 
     // ---- join of the warps, and of the CTAs if the unit is cut -------------------------
-    const int warps = min(NW, max(0, cur.st_hi - cur.st0));
+    const int warps = min(NW, max(0, st_hi - cur.st0));
     const bool whole = cur.st0 == 0 && cur.st1 == cur.stages;
+    // a part's weight against the common maximum M; a NaN sum keeps its NaN
+    auto weight = [](float m, float l, float M) { return l != l ? 1.f : m == -INFINITY ? 0.f : ex2(m - M); };
+    if (tid < NW * R) {
+      const int w = tid / R, r = tid % R;
+      float M = -INFINITY;
+      for (int k = 0; k < warps; ++k) M = fmaxf(M, s_m[k][r]);
+      s_c[w][r] = weight(s_m[w][r], s_l[w][r], M);
+      if (w == 0) {
+        float L = 0.f;
+        for (int k = 0; k < warps; ++k) L = fmaf(s_l[k][r], weight(s_m[k][r], s_l[k][r], M), L);
+        s_max[r] = M, s_sum[r] = L;
+      }
+    }
+    __syncthreads();
+    // items: the channels 8 g + e, 8 g + e + 1 of value x
+    auto place = [&](int item, int &ln, int &x, int &t, int &r, int &col) {
+      ln = item & 31, x = (item >> 5) % X, t = (item >> 5) / X * 2;
+      const int nn = ln >> 2, jj = ln & 3;
+      r = R == 16 ? nn + (x >> 1) * 8 : 2 * jj + x;
+      col = R == 16 ? 2 * jj + (x & 1) : nn;
+    };
+    auto put = [&](float y0, float y1, int t, int r, int col) {
+      const int rr = cur.tile * R + r, i = rr / G;
+      if (i >= cur.row.span) return;
+      const float L = s_sum[r], v = L > 0.f ? 1.f / L : L;  // no key: 0; NaN stays
+      uint16_t *dst = p.out + (size_t(cur.row.start + i) * p.g.H_q + cur.hk * G + rr - i * G) * D + (col * W + t / 8) * 8 + t % 8;
+      *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(y0 * v, y1 * v);
+    };
     const int c_first = whole ? c : cta_of(cur.first), c_last = whole ? c : cta_of(cur.first + cur.stages - 1);
     auto part_of = [&](int k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * att_part_floats<D, R>(); };
-    constexpr int kItems = (S::kQuads + S::kThreads - 1) / S::kThreads;
-    // item: 4 channels (g, eh) of value x; q: its group of lanes
-    auto weight = [](float m, float l, float M) { return l != l ? 1.f : m == -INFINITY ? 0.f : ex2(m - M); };
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      if (pass == 1) {
-        if (whole) break;
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          const uint32_t need = uint32_t(c_last - c_first + 1);
-          const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
-          s_flag = done == need;
-          if (done == need) counters[c_first] = 0;  // ready for the next call
-          __threadfence();
-        }
-        __syncthreads();
-        if (!s_flag) break;
+    for (int item = tid; item < S::kPairs; item += S::kThreads) {
+      int ln, x, t, r, col;
+      place(item, ln, x, t, r, col);
+      float y0 = 0.f, y1 = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < warps; ++w) {
+        const float cw = s_c[w][r];
+        const int from = s_scr[w];
+        y0 = fmaf(scratch(w, from, S::reg(t, x))[ln], cw, y0), y1 = fmaf(scratch(w, from, S::reg(t + 1, x))[ln], cw, y1);
       }
-#pragma unroll 1
-      for (int k = 0; k < kItems; ++k) {
-        const int item = k * S::kThreads + tid;
-        if (item >= S::kQuads) break;
-        const int ln = item & 31, quad = item >> 5, x = quad % X, t0 = quad / X * 4;  // channel tiles t0 .. t0 + 3
-        const int nn = ln >> 2, jj = ln & 3;
-        const int r = R == 16 ? nn + (x >> 1) * 8 : 2 * jj + x;
-        const int col = R == 16 ? 2 * jj + (x & 1) : nn;
-        float M = -INFINITY, L = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-        if (pass == 0) {
-#pragma unroll 4
-          for (int w = 0; w < warps; ++w) M = fmaxf(M, s_m[w][r]);
-#pragma unroll 2
-          for (int w = 0; w < warps; ++w) {
-            const float cw = weight(s_m[w][r], s_l[w][r], M);
-            L = fmaf(s_l[w][r], cw, L);
-            const int from = s_scr[w];
+      if (whole) put(y0, y1, t, r, col);
+      else *(reinterpret_cast<float2 *>(part_of(c)) + item) = make_float2(y0, y1);
+    }
+    if (!whole) {
+      if (tid < R) part_of(c)[S::kPart + tid] = s_max[tid], part_of(c)[S::kPart + 16 + tid] = s_sum[tid];
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const uint32_t need = uint32_t(c_last - c_first + 1);
+        const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
+        s_flag = done == need;
+        if (done == need) counters[c_first] = 0;  // ready for the next call
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_flag) {
+        // 16 parts at a time: their weights by 16 R threads, then the items
+        for (int r = tid; r < R; r += S::kThreads) s_sum[r] = 0.f;
+        float M = -INFINITY;  // of row tid % R
+        if (tid < 16 * R) {
+          for (int q = c_first + tid / R; q <= c_last; q += 16) M = fmaxf(M, __ldcg(part_of(q) + S::kPart + tid % R));
+          s_w[tid / R][tid % R] = M;
+        }
+        __syncthreads();
+        if (tid < 16 * R)
+          for (int q = 0; q < 16; ++q) M = fmaxf(M, s_w[q][tid % R]);
+        constexpr int kItems = (S::kPairs + S::kThreads - 1) / S::kThreads;
+        float2 y[kItems];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = fmaf(scratch(w, from, S::reg(t0 + e, x))[ln], cw, y[e]);
+        for (int k = 0; k < kItems; ++k) y[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int q0 = c_first; q0 <= c_last; q0 += 16) {
+          const int some = min(16, c_last + 1 - q0);
+          __syncthreads();
+          if (tid < 16 * R && tid / R < some) {
+            const float *src = part_of(q0 + tid / R) + S::kPart + tid % R;
+            const float l = __ldcg(src + 16), w = weight(__ldcg(src), l, M);
+            s_w[tid / R][tid % R] = w;
+            s_lw[tid / R][tid % R] = l * w;
           }
-        } else {
-#pragma unroll 4
-          for (int q = c_first; q <= c_last; ++q) M = fmaxf(M, __ldcg(part_of(q) + S::kPart + r));
-#pragma unroll 4
-          for (int q = c_first; q <= c_last; ++q) {
-            const float *src = part_of(q);
-            const float lq = __ldcg(src + S::kPart + 16 + r), cq = weight(__ldcg(src + S::kPart + r), lq, M);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src) + item);
-            L = fmaf(lq, cq, L);
-            y[0] = fmaf(v.x, cq, y[0]), y[1] = fmaf(v.y, cq, y[1]), y[2] = fmaf(v.z, cq, y[2]), y[3] = fmaf(v.w, cq, y[3]);
+          __syncthreads();
+          if (tid < R)
+            for (int q = 0; q < some; ++q) s_sum[tid] += s_lw[q][tid];
+#pragma unroll
+          for (int k = 0; k < kItems; ++k) {
+            const int item = k * S::kThreads + tid;
+            if (item < S::kPairs) {
+              int ln, x, t, r, col;
+              place(item, ln, x, t, r, col);
+#pragma unroll 8
+              for (int q = 0; q < some; ++q) {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q)) + item);
+                const float w = s_w[q][r];
+                y[k].x = fmaf(v.x, w, y[k].x), y[k].y = fmaf(v.y, w, y[k].y);
+              }
+            }
           }
         }
-        if (pass == 0 && !whole) {
-          float *part = part_of(c);
-          *(reinterpret_cast<float4 *>(part) + item) = make_float4(y[0], y[1], y[2], y[3]);
-          if (t0 == 0 && (R == 16 ? jj == 0 && (x & 1) == 0 : nn == 0)) part[S::kPart + r] = M, part[S::kPart + 16 + r] = L;
-        } else {
-          const int rr = cur.tile * R + r, i = rr / G;
-          if (i < cur.row.span) {
-            const float v = L > 0.f ? 1.f / L : L;  // no key: 0; NaN stays
-            uint16_t *dst = p.out + (size_t(cur.row.start + i) * p.g.H_q + cur.hk * G + rr - i * G) * D + (col * W + t0 / 8) * 8 + t0 % 8;
-            const __nv_bfloat162 u0 = __floats2bfloat162_rn(y[0] * v, y[1] * v), u1 = __floats2bfloat162_rn(y[2] * v, y[3] * v);
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&u0), *reinterpret_cast<const uint32_t *>(&u1));
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+          const int item = k * S::kThreads + tid;
+          if (item < S::kPairs) {
+            int ln, x, t, r, col;
+            place(item, ln, x, t, r, col);
+            put(y[k].x, y[k].y, t, r, col);
           }
         }
       }
