@@ -25,11 +25,12 @@
 // close behind; hence the AND-only unpacking of the keys, packed fp32
 // arithmetic and as many warps as the registers allow.
 //
-// The keys' stages of all units form one line, which the CTAs of a persistent
-// grid (one an SM) cut into equal pieces; the warps of a CTA take its stages in
-// turn, each with its own ring of bulk copies, and join in shared memory while
-// the next unit's first stages are on their way.  A unit cut between CTAs is
-// joined by whichever of them finishes last, in the order of the pieces, so the
+// The keys' stages of all units form one line, which the warps of a persistent
+// grid (one CTA an SM) cut into equal pieces, each with its own ring of bulk
+// copies that runs ahead into the next unit: a short unit costs its warp a load
+// of queries and a store, and nobody else waits.  A unit cut between warps is
+// joined at the end, in shared memory among the warps of a CTA, and by
+// whichever CTA finishes last among several, in the order of the pieces, so the
 // result does not depend on timing.
 #pragma once
 
@@ -52,14 +53,11 @@ struct AttShape {
   static constexpr int kSlots = (224 * 1024 / kStage) / NW;  // stages of a warp's ring
   static constexpr int X = R / 4;                // accumulators of a lane and channel tile
   static constexpr int kRegs = D / 8 * X;        // accumulators of a lane
-  static constexpr int kScratch = (kRegs * 128 + kStage - 1) / kStage;  // slots a warp's part takes in the join
-  static constexpr int kAhead = kSlots - kScratch;                      // slots the next unit may fill before it
-  static constexpr int kRegsSlot = kRegs / kScratch;                    // accumulators a slot takes
   static constexpr int kPairs = kRegs / 2 * 32;  // items of the join: 2 channels of a query row
   static constexpr int kPart = kRegs * 32;       // floats of a part
   static constexpr int kRing = kSlots * kStage;
   static constexpr int kSmem = NW * kRing + 128;
-  static_assert(kAhead >= 1 && kRegs % kScratch == 0 && kRegsSlot * 128 <= kStage, "ring");
+  static_assert(kSlots >= 2 && kPart * 4 <= kRing, "ring");
   // accumulator of channel tile 8 g + e: R = 16: one tile of 8 channels a product,
   // x the four values; R = 8: two tiles a product, x the two rows
   static __host__ __device__ constexpr int reg(int t, int x) { return R == 16 ? 4 * t + x : (t >> 1) * 4 + 2 * (t & 1) + x; }
@@ -67,7 +65,8 @@ struct AttShape {
 
 constexpr int kAttMaxRows = 16;
 
-// Floats of a part in the workspace: outputs, then maximum and sum of 16 rows.
+// Floats of a CTA's part of a cut unit in the workspace: outputs, then maximum
+// and sum of 16 rows.
 template <int D, int R>
 __host__ __device__ constexpr size_t att_part_floats() { return AttShape<D, R>::kPart + 32; }
 
@@ -232,13 +231,26 @@ __device__ __forceinline__ long long att_scan(long long v, long long *s_warp, lo
   return before + x - v;
 }
 
-// A unit, or the part of one that a CTA has: stages [st0, st1) of `stages`, of
-// which those below st_hi hold keys that a query sees.
+// A unit, or the part of one that a warp has: stages [st0, st1) of `stages`, of
+// which those below st_hi hold keys that a query sees.  On the line a unit is
+// one place (queries in, outputs out: about half a stage's time) and then two
+// places a stage; a stage belongs to the piece that holds its first.
 struct AttPiece {
   int b, hk, tile, st0, st1, stages, st_hi, lim_max;
-  int more;             // another piece follows
-  long long first, end; // the unit's first place on the line, the place behind the piece
+  int more;         // the warp has another piece
+  long long first;  // the unit's first place
   AttRow row;
+};
+
+// What the join needs in shared memory; it lies in the first warp's ring, behind
+// that warp's part.
+template <int D, int R>
+struct AttJoin {
+  static constexpr int NW = AttShape<D, R>::NW;
+  float c[2][NW][R];                   // weights of the warps' parts
+  float max[NW + 1][R], sum[NW + 1][R];
+  float w[16][R], lw[16][R];           // weights, and weighted sums, of 16 CTAs' parts
+  int from[NW + 1], to[NW + 1];        // warps of a cut unit; from > to: none
 };
 
 template <int D, int R>
@@ -247,85 +259,127 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   constexpr int W = S::W, ST = S::ST, NT = S::NT, NW = S::NW, X = S::X;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_full[NW][S::kSlots];
-  __shared__ float s_m[NW][R], s_l[NW][R];
-  __shared__ float s_c[NW][R], s_sum[R], s_max[R], s_w[16][R], s_lw[16][R];
-  __shared__ int s_scr[NW];
+  __shared__ AttPiece s_piece[NW][2], s_cut[2][NW];  // current and next pieces; cut pieces (0: begun before the warp's)
+  __shared__ int s_has[2][NW];                       // 1: a cut piece's part is in the ring, 2: in the workspace
+  __shared__ int s_none[NW];                         // the warp has no stage at all
+  __shared__ float s_m[2][NW][R], s_l[2][NW][R];
   __shared__ long long s_warp[NW];
-  __shared__ AttPiece s_piece[2];
   __shared__ int s_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = lane >> 2, j = lane & 3;
   const int G = p.g.H_q / p.g.H_kv, Hkv = p.g.H_kv;
   const int P = 1 << p.g.log2P;
-  if (lane == 0)
+  if (lane == 0) {
     for (int i = 0; i < S::kSlots; ++i) mbar_init(&s_full[warp][i], 1);
+    s_has[0][warp] = s_has[1][warp] = 0;
+  }
   fence_mbar_init();
   pdl_wait();
   pdl_trigger();
 
-  // ---- this CTA's piece of the line ----------------------------------------------
+  // ---- the line, and this CTA's pieces of it ------------------------------------------
   // rows beyond the CTA's threads are summed first and looked at again below
+  auto places = [&](const AttRow &r) -> long long { return (long long)r.tiles * (2 * r.stages + 1) * Hkv; };
   long long mine = 0, total, before = 0;
   AttRow own{};
   for (int b = tid; b < p.g.B; b += S::kThreads) {
     const AttRow r = att_row<D, R>(p, b, blockIdx.x == 0);
     if (b == tid) own = r;
-    mine += (long long)r.tiles * r.stages * Hkv;
+    mine += places(r);
   }
   before = att_scan<NW>(mine, s_warp, &total);
   if (total == 0) return;
-  // a CTA wants a stage for each warp at least
-  const int ctas = int(min((long long)gridDim.x, (total + NW - 1) / NW));
+  // a warp wants a stage at least
+  const int ctas = int(min((long long)gridDim.x, (total + 3 * NW - 1) / (3 * NW)));
   const int c = blockIdx.x;
   if (c >= ctas) return;
-  // pieces of `per` stages, the first `more` of one more
-  const long long per = total / ctas;
-  const int more = int(total - per * ctas);
-  const long long at = per * c + min(c, more), stop = at + per + (c < more);
+  // pieces of `per` places, the first `plus` of one more
+  const long long per = total / (ctas * NW);
+  const int plus = int(total - per * (ctas * NW));
+  auto start_of = [&](int w) -> long long { return per * w + min(w, plus); };  // of a warp of the grid
   auto cta_of = [&](long long x) -> int {
-    const long long y = x - more * (per + 1);
-    return int(y < 0 ? x / (per + 1) : more + y / per);
+    const long long y = x - plus * (per + 1);
+    return int(y < 0 ? x / (per + 1) : plus + y / per) / NW;
   };
-  // a piece's extent and limits, from its rows' queries
-  auto close = [&](AttPiece &u, long long from) {
+  const long long stop = start_of(c * NW + warp + 1);
+  // a piece from place x on, x in the unit, of the warp whose places end at `to`
+  auto close = [&](AttPiece &u, long long x, long long to) {
     u.stages = u.row.stages;
-    u.st1 = int(min((long long)u.stages, u.st0 + (stop - from)));
-    u.first = from - u.st0, u.end = from + (u.st1 - u.st0), u.more = u.end < stop;
+    u.st0 = int(min((long long)u.stages, (x - u.first) >> 1));
+    u.st1 = int(min((long long)u.stages, (to - u.first) >> 1));
     const int first = u.tile * R / G;
     const int last = min(((u.tile + 1) * R - 1) / G, u.row.count - 1);
     u.lim_max = last >= first ? max(0, u.row.len - u.row.count + last + 1) : 0;
     u.st_hi = min(u.st1, (u.lim_max + ST - 1) / ST);
   };
-  // the first piece, by the thread of the row that holds `at`
+  // each warp's first unit, by the thread of the row that holds it
   long long before0 = 0;
   for (int b0 = 0; b0 < p.g.B; b0 += S::kThreads) {
     if (p.g.B > S::kThreads) {
       if (b0 + tid < p.g.B) own = att_row<D, R>(p, b0 + tid, false);
       else own.tiles = 0;
       long long sum;
-      before = before0 + att_scan<NW>((long long)own.tiles * own.stages * Hkv, s_warp, &sum);
+      before = before0 + att_scan<NW>(places(own), s_warp, &sum);
       before0 += sum;
     }
-    if (b0 + tid < p.g.B && at >= before && at - before < (long long)own.tiles * own.stages * Hkv) {
-      AttPiece u;
-      u.b = b0 + tid, u.row = own;
-      const int x = int((at - before) / own.stages);
-      u.st0 = int(at - before - (long long)x * own.stages);
-      u.hk = x / own.tiles, u.tile = x - u.hk * own.tiles;
-      close(u, at);
-      s_piece[0] = u;
+#pragma unroll 1
+    for (int w = 0; w < NW; ++w) {
+      const long long x = start_of(c * NW + w) - before;
+      if (b0 + tid < p.g.B && x >= 0 && x < places(own)) {
+        AttPiece u;
+        u.b = b0 + tid, u.row = own;
+        const int k = int(x / (2 * own.stages + 1));
+        u.first = before + (long long)k * (2 * own.stages + 1);
+        u.hk = k / own.tiles, u.tile = k - u.hk * own.tiles;
+        close(u, before + x, start_of(c * NW + w + 1));
+        s_piece[w][0] = u;
+      }
     }
-    if (p.g.B > S::kThreads && at < before0) break;
   }
   __syncthreads();
-  uint32_t turn = 0;  // s_piece[turn & 1] is the current piece
 
   uint8_t *ring = smem + warp * S::kRing;
   float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
+  float *stash = parts + 2 * size_t(gridDim.x) * att_part_floats<D, R>() + (size_t(c) * NW) * S::kPart;
   uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
   uint32_t phases = 0;      // parity of each ring slot
   int slot = 0, in = 0;     // next slot to read and to fill
   bool dead = false;        // a copy never came: nothing more is issued
+  AttPiece *pieces = s_piece[warp];
+
+  // the first piece with a stage from u on; without a stage if there is none
+  auto seek = [&](AttPiece u) -> AttPiece {
+    while (u.st0 >= u.st1) {
+      const long long x = u.first + 2 * u.row.stages + 1;
+      if (x >= stop) break;
+      if (++u.tile == u.row.tiles) {
+        u.tile = 0;
+        if (++u.hk == Hkv) {
+          u.hk = 0;
+          do u.row = att_row<D, R>(p, ++u.b, false);
+          while (u.row.tiles == 0);
+        }
+      }
+      u.first = x;
+      close(u, x, stop);
+    }
+    return u;
+  };
+  // the piece behind u, into `to`; marks u as followed
+  auto follow = [&](AttPiece &u, AttPiece &to) {
+    AttPiece v = u;
+    v.st0 = v.st1;  // done with
+    v = seek(v);
+    u.more = v.st0 < v.st1;
+    if (u.more) to = v;
+  };
+  if (lane == 0) {
+    AttPiece &u = pieces[0];
+    if (start_of(c * NW + warp) < stop) u = seek(u);
+    else u.st0 = u.st1 = u.st_hi = 0;  // no place at all
+    s_none[warp] = u.st0 >= u.st1;
+  }
+  __syncwarp();
 
   // ---- copies: a page is one copy, as it lies in memory (copies are taken one in
   // about 70 cycles whatever their size); half of a page is four pieces ---------------
@@ -370,22 +424,35 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   const uint32_t lane_v0 = att_key(2 * j) * (D / 2) + n * (4 * W), lane_v1 = att_key(2 * j + 1) * (D / 2) + n * (4 * W);
   const uint32_t lane_e0 = att_key(2 * j) * (4 * W), lane_e1 = att_key(2 * j + 1) * (4 * W);
 
-  int issued = s_piece[0].st0 + warp;  // next stage of the piece to issue
-  int next = page_of(s_piece[0], issued);
-  auto fill = [&](const AttPiece &u, int most) {  // up to `most` stages
+  // the piece whose stages are being issued: the current one or the one behind it
+  int ahead = 0, issued = pieces[0].st0, next = page_of(pieces[0], issued);
+  int flight = 0;     // stages issued and not read yet
+  uint32_t turn = 0;  // pieces[turn & 1] is the current piece
+  auto refill = [&]() {
 #pragma unroll 1
-    for (int i = 0; i < most && issued < u.st_hi && !dead; ++i) {
-      const int page = next;
-      next = page_of(u, issued + NW);
-      issue(u, issued, page);
-      issued += NW;
+    while (flight < S::kSlots && !dead) {
+      if (issued < pieces[ahead].st_hi) {
+        const int page = next;
+        next = page_of(pieces[ahead], issued + 1);
+        issue(pieces[ahead], issued, page);
+        ++issued, ++flight;
+      } else if (ahead == int(turn & 1) && pieces[ahead].more) {  // on into the next piece
+        ahead ^= 1, issued = pieces[ahead].st0, next = page_of(pieces[ahead], issued);
+      } else {
+        break;
+      }
     }
   };
-  fill(s_piece[0], S::kSlots);
 
-  for (;;) {
-    const AttPiece &cur = s_piece[turn & 1];
-    const int lim_max = cur.lim_max, st_hi = cur.st_hi;
+#pragma unroll 1
+  for (bool any = !s_none[warp]; any; any = pieces[turn & 1].more != 0, ++turn) {
+    // (the loop's step reads `more` of the piece that is done)
+    const AttPiece &cur = pieces[turn & 1];
+    const int lim_max = cur.lim_max, st_hi = cur.st_hi, st_first = cur.st0;
+    __syncwarp();  // every lane is done with the piece before
+    if (lane == 0) follow(pieces[turn & 1], pieces[(turn & 1) ^ 1]);
+    __syncwarp();
+    refill();
     // ---- the tile's queries: rows n and (R = 16) n + 8 ---------------------------------
     const AttRow row = cur.row;
     const int R0 = cur.tile * R + n, R1 = R0 + 8;
@@ -453,23 +520,6 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
       }
     }
 
-    // the piece after this one, by the warp with the fewest stages
-    if (cur.more && tid == S::kThreads - 1) {
-      AttPiece u = cur;
-      u.st0 = 0;
-      if (++u.tile == u.row.tiles) {
-        u.tile = 0;
-        if (++u.hk == Hkv) {
-          u.hk = 0;
-          do u.row = att_row<D, R>(p, ++u.b, false);
-          while (u.row.tiles == 0);
-        }
-      }
-      close(u, cur.end);
-      s_piece[(turn & 1) ^ 1] = u;
-    }
-    __syncthreads();
-
     float o_acc[S::kRegs / 4][4];
 #pragma unroll
     for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.f;
@@ -478,8 +528,9 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     F2 l0 = f2(0.f, 0.f), l1 = f2(0.f, 0.f);
 
 #pragma unroll 1
-    for (int st = cur.st0 + warp; st < st_hi; st += NW) {
-      if (st < issued) {  // once a wait has run out nothing more is issued, and what is in flight still waited for
+    for (int st = st_first; st < st_hi; ++st) {
+      if (flight > 0) {  // once a wait has run out nothing more is issued, and what is in flight still waited for
+        --flight;
         if (!att_wait(&s_full[warp][slot], (phases >> slot) & 1)) {
           dead = true;
           atomicOr(p.status, GDN_STATUS_TIMEOUT);
@@ -646,24 +697,12 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
       }
      }
       __syncwarp();  // every lane is done with the slot
-      if (issued < st_hi && !dead) {
-        const int page = next;
-        next = page_of(cur, issued + NW);
-        issue(cur, issued, page);
-        issued += NW;
-      }
       slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+      refill();
     }
+    refill();  // a piece without copies has not gone on yet
 
-    // ---- the next piece's first stages on their way ----------------------------------------
-    if (cur.more) {
-      in = slot;  // every copy of this piece has been waited for
-      issued = warp;
-      next = page_of(s_piece[(turn & 1) ^ 1], issued);
-      fill(s_piece[(turn & 1) ^ 1], S::kAhead);
-    }
-
-    // ---- this warp's part: outputs, maximum and sum of its keys -----------------------
+    // ---- the piece's outputs ---------------------------------------------------------
     float la, lb, l0s, l1s;
     f2_get(l0, la, lb);
     l0s = la + lb;
@@ -678,158 +717,220 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
         nan1 |= __shfl_xor_sync(0xffffffffu, nan1, o);
       }
     }
-    // the ring's slots before the next to read, the last kScratch of them
-    const bool has = cur.st0 + warp < cur.st_hi;
-    auto scratch = [&](int w, int from, int i) -> float * {  // accumulator i of warp w's part
-      int k = from - 1 - i / S::kRegsSlot;
-      k += k < 0 ? S::kSlots : 0;
-      return reinterpret_cast<float *>(smem + w * S::kRing + k * S::kStage) + (i % S::kRegsSlot) * 32;
-    };
-    if (has) {
+    // of the lane's values' rows: R = 16: n, n + 8; R = 8: 2 j, 2 j + 1
+    uint32_t na = nan0, nb = nan1;
+    float sa = l0s, sb = l1s;
+    if (R == 8) {
+      na = __shfl_sync(0xffffffffu, nan0, 8 * j), nb = __shfl_sync(0xffffffffu, nan0, 8 * j + 4);
+      sa = __shfl_sync(0xffffffffu, l0s, 8 * j), sb = __shfl_sync(0xffffffffu, l0s, 8 * j + 4);
+    }
+    const bool starts = st_first == 0, ends = cur.st1 == cur.stages;
+    if (starts && ends) {  // the whole unit
+      const float va = sa > 0.f ? 1.f / sa : sa, vb = sb > 0.f ? 1.f / sb : sb;  // no key: 0; NaN stays
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        const bool second = R == 16 ? x >= 2 : x == 1;
+        const int rr = cur.tile * R + (R == 16 ? n + (second ? 8 : 0) : 2 * j + x), i = rr / G;
+        const int col = R == 16 ? 2 * j + (x & 1) : n;
+        const float v = second ? vb : va;
+        const uint32_t nan = second ? nb : na;
+        uint16_t *dst = p.out + (size_t(cur.row.start + i) * p.g.H_q + cur.hk * G + rr - i * G) * D + col * W * 8;
+        if (i < cur.row.span) {
+#pragma unroll
+          for (int g = 0; g < W; ++g) {
+            const float w = nan >> g & 1u ? __uint_as_float(0x7fc00000u) : v;
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int a = S::reg(8 * g + 2 * e, x), b = S::reg(8 * g + 2 * e + 1, x);
+              const __nv_bfloat162 y = __floats2bfloat162_rn(o_acc[a / 4][a % 4] * w, o_acc[b / 4][b % 4] * w);
+              h[e] = *reinterpret_cast<const uint32_t *>(&y);
+            }
+            *reinterpret_cast<uint4 *>(dst + 8 * g) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+      }
+    } else {
+      const int kind = starts ? 1 : 0;
+      const bool stay = !cur.more;  // the ring is free after the last piece
+      float *dst = stay ? reinterpret_cast<float *>(ring) : stash + size_t(warp) * S::kPart;
       const float nan = __uint_as_float(0x7fc00000u);
-      uint32_t na = nan0, nb = nan1;
-      if (R == 8) na = __shfl_sync(0xffffffffu, nan0, 8 * j), nb = __shfl_sync(0xffffffffu, nan0, 8 * j + 4);
 #pragma unroll
       for (int t = 0; t < D / 8; ++t)
 #pragma unroll
         for (int x = 0; x < X; ++x) {
           const int i = S::reg(t, x);
-          const uint32_t mask = R == 16 ? (x < 2 ? na : nb) : (x ? nb : na);
-          scratch(warp, slot, i)[lane] = mask >> (t / 8) & 1u ? nan : o_acc[i / 4][i % 4];
+          const uint32_t mask = (R == 16 ? x < 2 : x == 0) ? na : nb;
+          dst[i * 32 + lane] = mask >> (t / 8) & 1u ? nan : o_acc[i / 4][i % 4];
         }
-    }
-    if (j == 0) {
-      s_m[warp][n] = m0, s_l[warp][n] = l0s;
-      if (R == 16) s_m[warp][(n + 8) % R] = m1, s_l[warp][(n + 8) % R] = l1s;
-    }
-    if (lane == 0) s_scr[warp] = slot;
-    __syncthreads();
-
-    // ---- join of the warps, and of the CTAs if the unit is cut -------------------------
-    const int warps = min(NW, max(0, st_hi - cur.st0));
-    const bool whole = cur.st0 == 0 && cur.st1 == cur.stages;
-    // a part's weight against the common maximum M; a NaN sum keeps its NaN
-    auto weight = [](float m, float l, float M) { return l != l ? 1.f : m == -INFINITY ? 0.f : ex2(m - M); };
-    if (tid < NW * R) {
-      const int w = tid / R, r = tid % R;
-      float M = -INFINITY;
-      for (int k = 0; k < warps; ++k) M = fmaxf(M, s_m[k][r]);
-      s_c[w][r] = weight(s_m[w][r], s_l[w][r], M);
-      if (w == 0) {
-        float L = 0.f;
-        for (int k = 0; k < warps; ++k) L = fmaf(s_l[k][r], weight(s_m[k][r], s_l[k][r], M), L);
-        s_max[r] = M, s_sum[r] = L;
+      if (j == 0) {
+        s_m[kind][warp][n] = m0, s_l[kind][warp][n] = l0s;
+        if (R == 16) s_m[kind][warp][(n + 8) % R] = m1, s_l[kind][warp][(n + 8) % R] = l1s;
       }
+      if (lane == 0) s_has[kind][warp] = stay ? 1 : 2, s_cut[kind][warp] = cur;
     }
-    __syncthreads();
-    // items: the channels 8 g + e, 8 g + e + 1 of value x
-    auto place = [&](int item, int &ln, int &x, int &t, int &r, int &col) {
-      ln = item & 31, x = (item >> 5) % X, t = (item >> 5) / X * 2;
-      const int nn = ln >> 2, jj = ln & 3;
-      r = R == 16 ? nn + (x >> 1) * 8 : 2 * jj + x;
-      col = R == 16 ? 2 * jj + (x & 1) : nn;
-    };
-    auto put = [&](float y0, float y1, int t, int r, int col) {
-      const int rr = cur.tile * R + r, i = rr / G;
-      if (i >= cur.row.span) return;
-      const float L = s_sum[r], v = L > 0.f ? 1.f / L : L;  // no key: 0; NaN stays
-      uint16_t *dst = p.out + (size_t(cur.row.start + i) * p.g.H_q + cur.hk * G + rr - i * G) * D + (col * W + t / 8) * 8 + t % 8;
-      *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(y0 * v, y1 * v);
-    };
-    const int c_first = whole ? c : cta_of(cur.first), c_last = whole ? c : cta_of(cur.first + cur.stages - 1);
-    auto part_of = [&](int k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * att_part_floats<D, R>(); };
+  }
+
+  // ---- join of the cut units: entry 0 is one begun before this CTA, entry w + 1 one
+  // that begins with warp w -----------------------------------------------------------
+  static_assert(S::kPart * 4 + sizeof(AttJoin<D, R>) <= S::kRing, "join");
+  AttJoin<D, R> &join = *reinterpret_cast<AttJoin<D, R> *>(smem + S::kPart * 4);
+  __syncthreads();
+  if (tid <= NW) {
+    const int e = tid;
+    int from = NW, to = -1;
+    if (e == 0) {
+      int w = 0;
+      while (w < NW && s_none[w]) ++w;
+      if (w < NW && s_has[0][w]) from = to = w;
+    } else if (s_has[1][e - 1]) {
+      from = to = e - 1;
+    }
+    if (from <= to && !(e == 0 && s_cut[0][from].st1 == s_cut[0][from].stages))
+      for (int w = from + 1; w < NW; ++w) {
+        if (s_none[w]) continue;
+        if (!s_has[0][w]) break;
+        to = w;
+        if (s_cut[0][w].st1 == s_cut[0][w].stages) break;
+      }
+    join.from[e] = from, join.to[e] = to;
+  }
+  __syncthreads();
+  // a part's weight against the common maximum M; a NaN sum keeps its NaN
+  auto weight = [](float m, float l, float M) { return l != l ? 1.f : m == -INFINITY ? 0.f : ex2(m - M); };
+  auto kind_of = [&](int e, int w) { return e > 0 && w == join.from[e] ? 1 : 0; };
+  for (int k = tid; k < (NW + 1) * R; k += S::kThreads) {
+    const int e = k / R, r = k % R;
+    float M = -INFINITY, L = 0.f;
+    for (int w = join.from[e]; w <= join.to[e]; ++w)
+      if (s_has[kind_of(e, w)][w]) M = fmaxf(M, s_m[kind_of(e, w)][w][r]);
+    for (int w = join.from[e]; w <= join.to[e]; ++w) {
+      const int d = kind_of(e, w);
+      const float cw = s_has[d][w] ? weight(s_m[d][w][r], s_l[d][w][r], M) : 0.f;
+      join.c[d][w][r] = cw;
+      if (s_has[d][w]) L = fmaf(s_l[d][w][r], cw, L);
+    }
+    join.max[e][r] = M, join.sum[e][r] = L;
+  }
+  __syncthreads();
+  // items: the channels 8 g + e, 8 g + e + 1 of value x
+  auto place = [&](int item, int &ln, int &x, int &t, int &r, int &col) {
+    ln = item & 31, x = (item >> 5) % X, t = (item >> 5) / X * 2;
+    const int nn = ln >> 2, jj = ln & 3;
+    r = R == 16 ? nn + (x >> 1) * 8 : 2 * jj + x;
+    col = R == 16 ? 2 * jj + (x & 1) : nn;
+  };
+  auto put = [&](const AttPiece &u, float L, float y0, float y1, int t, int r, int col) {
+    const int rr = u.tile * R + r, i = rr / G;
+    if (i >= u.row.span) return;
+    const float v = L > 0.f ? 1.f / L : L;
+    uint16_t *dst = p.out + (size_t(u.row.start + i) * p.g.H_q + u.hk * G + rr - i * G) * D + (col * W + t / 8) * 8 + t % 8;
+    *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(y0 * v, y1 * v);
+  };
+  auto entry_piece = [&](int e) -> const AttPiece & { return s_cut[e > 0 ? 1 : 0][join.from[e]]; };
+  auto entry_whole = [&](int e) { return e > 0 && join.to[e] > join.from[e] && s_cut[0][join.to[e]].st1 == s_cut[0][join.to[e]].stages; };
+  auto part_of = [&](int k, int c_first) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * att_part_floats<D, R>(); };
+#pragma unroll 1
+  for (int e = 0; e <= NW; ++e) {
+    const int from = join.from[e], to = join.to[e];
+    if (from > to) continue;
+    const AttPiece &u = entry_piece(e);
+    const bool whole = entry_whole(e);
+    float *part = part_of(c, e > 0 ? c : -1);
 #pragma unroll 1
     for (int item = tid; item < S::kPairs; item += S::kThreads) {
       int ln, x, t, r, col;
       place(item, ln, x, t, r, col);
       float y0 = 0.f, y1 = 0.f;
 #pragma unroll 4
-      for (int w = 0; w < warps; ++w) {
-        const float cw = s_c[w][r];
-        const int from = s_scr[w];
-        y0 = fmaf(scratch(w, from, S::reg(t, x))[ln], cw, y0), y1 = fmaf(scratch(w, from, S::reg(t + 1, x))[ln], cw, y1);
+      for (int w = from; w <= to; ++w) {
+        const int d = kind_of(e, w), has = s_has[d][w];
+        if (!has) continue;
+        const float cw = join.c[d][w][r];
+        const float *src = has == 1 ? reinterpret_cast<const float *>(smem + w * S::kRing) : stash + size_t(w) * S::kPart;
+        y0 = fmaf(src[S::reg(t, x) * 32 + ln], cw, y0), y1 = fmaf(src[S::reg(t + 1, x) * 32 + ln], cw, y1);
       }
-      if (whole) put(y0, y1, t, r, col);
-      else *(reinterpret_cast<float2 *>(part_of(c)) + item) = make_float2(y0, y1);
+      if (whole) put(u, join.sum[e][r], y0, y1, t, r, col);
+      else *(reinterpret_cast<float2 *>(part) + item) = make_float2(y0, y1);
     }
-    if (!whole) {
-      if (tid < R) part_of(c)[S::kPart + tid] = s_max[tid], part_of(c)[S::kPart + 16 + tid] = s_sum[tid];
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t need = uint32_t(c_last - c_first + 1);
-        const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
-        s_flag = done == need;
-        if (done == need) counters[c_first] = 0;  // ready for the next call
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_flag) {
-        // 16 parts at a time: their weights by 16 R threads, then the items
-        for (int r = tid; r < R; r += S::kThreads) s_sum[r] = 0.f;
-        float M = -INFINITY;  // of row tid % R
-        if (tid < 16 * R) {
-          for (int q = c_first + tid / R; q <= c_last; q += 16) M = fmaxf(M, __ldcg(part_of(q) + S::kPart + tid % R));
-          s_w[tid / R][tid % R] = M;
-        }
-        __syncthreads();
-        if (tid < 16 * R)
-          for (int q = 0; q < 16; ++q) M = fmaxf(M, s_w[q][tid % R]);
-        constexpr int kItems = (S::kPairs + S::kThreads - 1) / S::kThreads;
-        float2 y[kItems];
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) y[k] = make_float2(0.f, 0.f);
+    if (!whole && tid < R) part[S::kPart + tid] = join.max[e][tid], part[S::kPart + 16 + tid] = join.sum[e][tid];
+  }
+  // ---- units cut between CTAs: two at most -----------------------------------------------
 #pragma unroll 1
-        for (int q0 = c_first; q0 <= c_last; q0 += 16) {
-          const int some = min(16, c_last + 1 - q0);
-          __syncthreads();
-          if (tid < 16 * R && tid / R < some) {
-            const float *src = part_of(q0 + tid / R) + S::kPart + tid % R;
-            const float l = __ldcg(src + 16), w = weight(__ldcg(src), l, M);
-            s_w[tid / R][tid % R] = w;
-            s_lw[tid / R][tid % R] = l * w;
-          }
-          __syncthreads();
-          if (tid < R)
-            for (int q = 0; q < some; ++q) s_sum[tid] += s_lw[q][tid];
+  for (int e = 0; e <= NW; ++e) {
+    if (join.from[e] > join.to[e] || entry_whole(e)) continue;
+    const AttPiece &u = entry_piece(e);
+    const int c_first = cta_of(u.first + 1), c_last = cta_of(u.first + 2 * u.stages - 1);
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t need = uint32_t(c_last - c_first + 1);
+      const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
+      s_flag = done == need;
+      if (done == need) counters[c_first] = 0;  // ready for the next call
+      __threadfence();
+    }
+    __syncthreads();
+    if (!s_flag) continue;
+    // 16 parts at a time: their weights by 16 R threads, then the items
+    float M = -INFINITY;  // of row tid % R
+    if (tid < 16 * R) {
+      for (int q = c_first + tid / R; q <= c_last; q += 16) M = fmaxf(M, __ldcg(part_of(q, c_first) + S::kPart + tid % R));
+      join.w[tid / R][tid % R] = M;
+    }
+    if (tid < R) join.sum[e][tid] = 0.f;
+    __syncthreads();
+    if (tid < 16 * R)
+      for (int q = 0; q < 16; ++q) M = fmaxf(M, join.w[q][tid % R]);
+    constexpr int kItems = (S::kPairs + S::kThreads - 1) / S::kThreads;
+    float2 y[kItems];
 #pragma unroll
-          for (int k = 0; k < kItems; ++k) {
-            const int item = k * S::kThreads + tid;
-            if (item < S::kPairs) {
-              int ln, x, t, r, col;
-              place(item, ln, x, t, r, col);
+    for (int k = 0; k < kItems; ++k) y[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int q0 = c_first; q0 <= c_last; q0 += 16) {
+      const int some = min(16, c_last + 1 - q0);
+      __syncthreads();
+      if (tid < 16 * R && tid / R < some) {
+        const float *src = part_of(q0 + tid / R, c_first) + S::kPart + tid % R;
+        const float l = __ldcg(src + 16), w = weight(__ldcg(src), l, M);
+        join.w[tid / R][tid % R] = w;
+        join.lw[tid / R][tid % R] = l * w;
+      }
+      __syncthreads();
+      if (tid < R)
+        for (int q = 0; q < some; ++q) join.sum[e][tid] += join.lw[q][tid];
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int item = k * S::kThreads + tid;
+        if (item < S::kPairs) {
+          int ln, x, t, r, col;
+          place(item, ln, x, t, r, col);
 #pragma unroll 8
-              for (int q = 0; q < some; ++q) {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q)) + item);
-                const float w = s_w[q][r];
-                y[k].x = fmaf(v.x, w, y[k].x), y[k].y = fmaf(v.y, w, y[k].y);
-              }
-            }
-          }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-          const int item = k * S::kThreads + tid;
-          if (item < S::kPairs) {
-            int ln, x, t, r, col;
-            place(item, ln, x, t, r, col);
-            put(y[k].x, y[k].y, t, r, col);
+          for (int q = 0; q < some; ++q) {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q, c_first)) + item);
+            const float w = join.w[q][r];
+            y[k].x = fmaf(v.x, w, y[k].x), y[k].y = fmaf(v.y, w, y[k].y);
           }
         }
       }
     }
-    if (!cur.more) break;
-    ++turn;
-    fence_proxy_async_shared();  // the join's accesses before the copies that write over them
     __syncthreads();
-    fill(s_piece[turn & 1], S::kSlots - S::kAhead);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int item = k * S::kThreads + tid;
+      if (item < S::kPairs) {
+        int ln, x, t, r, col;
+        place(item, ln, x, t, r, col);
+        put(u, join.sum[e][r], y[k].x, y[k].y, t, r, col);
+      }
+    }
   }
 }
 
 template <int D, int R>
 inline size_t att_mma_ws(int ctas) {
-  return 4096 + sizeof(float) * 2 * size_t(ctas) * att_part_floats<D, R>();
+  // counters; two parts a CTA; what a warp puts aside while its ring goes on
+  return 4096 + sizeof(float) * size_t(ctas) * (2 * att_part_floats<D, R>() + size_t(AttShape<D, R>::NW) * AttShape<D, R>::kPart);
 }
 
 template <int D, int R>
