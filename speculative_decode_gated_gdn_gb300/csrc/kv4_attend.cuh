@@ -234,7 +234,11 @@ __device__ __forceinline__ long long att_scan(long long v, long long *s_warp, lo
 // A unit, or the part of one that a warp has: stages [st0, st1) of `stages`, of
 // which those below st_hi hold keys that a query sees.  On the line a unit is
 // one place (queries in, outputs out: about half a stage's time) and then two
-// places a stage; a stage belongs to the piece that holds its first.
+// places a stage; a stage belongs to the piece that holds its first.  A unit of
+// kAttUncut stages or fewer is not cut: it belongs to the piece that holds its
+// first place, whole.
+constexpr int kAttUncut = 4;
+
 struct AttPiece {
   int b, hk, tile, st0, st1, stages, st_hi, lim_max;
   int more;         // the warp has another piece
@@ -294,11 +298,12 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   const int c = blockIdx.x;
   if (c >= ctas) return;
   // pieces of `per` places, the first `plus` of one more
-  const long long per = total / (ctas * NW);
+  const long long per = total < (1ll << 31) ? int(total) / (ctas * NW) : total / (ctas * NW);
   const int plus = int(total - per * (ctas * NW));
   auto start_of = [&](int w) -> long long { return per * w + min(w, plus); };  // of a warp of the grid
   auto cta_of = [&](long long x) -> int {
     const long long y = x - plus * (per + 1);
+    if (x < (1ll << 31)) return (y < 0 ? int(x) / int(per + 1) : plus + int(y) / int(per)) / NW;
     return int(y < 0 ? x / (per + 1) : plus + y / per) / NW;
   };
   const long long stop = start_of(c * NW + warp + 1);
@@ -307,13 +312,15 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     u.stages = u.row.stages;
     u.st0 = int(min((long long)u.stages, (x - u.first) >> 1));
     u.st1 = int(min((long long)u.stages, (to - u.first) >> 1));
+    if (u.stages <= kAttUncut) u.st0 = x > u.first ? u.stages : 0, u.st1 = u.stages;
     const int first = u.tile * R / G;
     const int last = min(((u.tile + 1) * R - 1) / G, u.row.count - 1);
     u.lim_max = last >= first ? max(0, u.row.len - u.row.count + last + 1) : 0;
     u.st_hi = min(u.st1, (u.lim_max + ST - 1) / ST);
   };
-  // each warp's first unit, by the thread of the row that holds it
+  // the row that holds each warp's first place, by that row's thread
   long long before0 = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.g.B; b0 += S::kThreads) {
     if (p.g.B > S::kThreads) {
       if (b0 + tid < p.g.B) own = att_row<D, R>(p, b0 + tid, false);
@@ -322,18 +329,11 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
       before = before0 + att_scan<NW>(places(own), s_warp, &sum);
       before0 += sum;
     }
+    const long long end = before + places(own);
 #pragma unroll 1
     for (int w = 0; w < NW; ++w) {
-      const long long x = start_of(c * NW + w) - before;
-      if (b0 + tid < p.g.B && x >= 0 && x < places(own)) {
-        AttPiece u;
-        u.b = b0 + tid, u.row = own;
-        const int k = int(x / (2 * own.stages + 1));
-        u.first = before + (long long)k * (2 * own.stages + 1);
-        u.hk = k / own.tiles, u.tile = k - u.hk * own.tiles;
-        close(u, before + x, start_of(c * NW + w + 1));
-        s_piece[w][0] = u;
-      }
+      const long long x = start_of(c * NW + w);
+      if (x >= before && x < end) s_piece[w][0].b = b0 + tid, s_piece[w][0].first = before, s_piece[w][0].row = own;
     }
   }
   __syncthreads();
@@ -374,9 +374,19 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     if (u.more) to = v;
   };
   if (lane == 0) {
-    AttPiece &u = pieces[0];
-    if (start_of(c * NW + warp) < stop) u = seek(u);
-    else u.st0 = u.st1 = u.st_hi = 0;  // no place at all
+    AttPiece u = pieces[0];
+    const long long x = start_of(c * NW + warp);
+    if (x < stop) {
+      const int len = 2 * u.row.stages + 1;  // a unit's places
+      const int k = x - u.first < (1ll << 31) ? int(x - u.first) / len : int((x - u.first) / len);
+      u.first += (long long)k * len;
+      u.hk = k / u.row.tiles, u.tile = k - u.hk * u.row.tiles;
+      close(u, x, stop);
+      u = seek(u);
+    } else {
+      u.st0 = u.st1 = u.st_hi = 0;  // no place at all
+    }
+    pieces[0] = u;
     s_none[warp] = u.st0 >= u.st1;
   }
   __syncwarp();
@@ -837,21 +847,38 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     const AttPiece &u = entry_piece(e);
     const bool whole = entry_whole(e);
     float *part = part_of(c, e > 0 ? c : -1);
+    constexpr int kItems = (S::kPairs + S::kThreads - 1) / S::kThreads;
 #pragma unroll 1
-    for (int item = tid; item < S::kPairs; item += S::kThreads) {
-      int ln, x, t, r, col;
-      place(item, ln, x, t, r, col);
-      float y0 = 0.f, y1 = 0.f;
-#pragma unroll 4
+    for (int k0 = 0; k0 < kItems; k0 += 4) {  // 4 items of a thread at a time
+      float2 y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
       for (int w = from; w <= to; ++w) {
         const int d = kind_of(e, w), has = s_has[d][w];
         if (!has) continue;
-        const float cw = join.c[d][w][r];
         const float *src = has == 1 ? reinterpret_cast<const float *>(smem + w * S::kRing) : stash + size_t(w) * S::kPart;
-        y0 = fmaf(src[S::reg(t, x) * 32 + ln], cw, y0), y1 = fmaf(src[S::reg(t + 1, x) * 32 + ln], cw, y1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int item = (k0 + k) * S::kThreads + tid;
+          if (k0 + k < kItems && item < S::kPairs) {
+            int ln, x, t, r, col;
+            place(item, ln, x, t, r, col);
+            const float cw = join.c[d][w][r];
+            y[k].x = fmaf(src[S::reg(t, x) * 32 + ln], cw, y[k].x), y[k].y = fmaf(src[S::reg(t + 1, x) * 32 + ln], cw, y[k].y);
+          }
+        }
       }
-      if (whole) put(u, join.sum[e][r], y0, y1, t, r, col);
-      else *(reinterpret_cast<float2 *>(part) + item) = make_float2(y0, y1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int item = (k0 + k) * S::kThreads + tid;
+        if (k0 + k < kItems && item < S::kPairs) {
+          int ln, x, t, r, col;
+          place(item, ln, x, t, r, col);
+          if (whole) put(u, join.sum[e][r], y[k].x, y[k].y, t, r, col);
+          else *(reinterpret_cast<float2 *>(part) + item) = y[k];
+        }
+      }
     }
     if (!whole && tid < R) part[S::kPart + tid] = join.max[e][tid], part[S::kPart + 16 + tid] = join.sum[e][tid];
   }
@@ -899,19 +926,28 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
       __syncthreads();
       if (tid < R)
         for (int q = 0; q < some; ++q) join.sum[e][tid] += join.lw[q][tid];
+      // the loads of four parts, all of a thread's items, are on their way together
+#pragma unroll 1
+      for (int q = 0; q < some; q += 4) {
+        float2 v[4][kItems];
 #pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        const int item = k * S::kThreads + tid;
-        if (item < S::kPairs) {
-          int ln, x, t, r, col;
-          place(item, ln, x, t, r, col);
-#pragma unroll 8
-          for (int q = 0; q < some; ++q) {
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q, c_first)) + item);
-            const float w = join.w[q][r];
-            y[k].x = fmaf(v.x, w, y[k].x), y[k].y = fmaf(v.y, w, y[k].y);
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+          for (int k = 0; k < kItems; ++k) {
+            const int item = k * S::kThreads + tid;
+            v[f][k] = item < S::kPairs && q + f < some ? __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q + f, c_first)) + item)
+                                                       : make_float2(0.f, 0.f);
           }
-        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+          for (int k = 0; k < kItems; ++k) {
+            const int item = k * S::kThreads + tid;
+            int ln, x, t, r, col;
+            place(item, ln, x, t, r, col);
+            const float w = q + f < some ? join.w[q + f][r] : 0.f;
+            y[k].x = fmaf(v[f][k].x, w, y[k].x), y[k].y = fmaf(v[f][k].y, w, y[k].y);
+          }
       }
     }
     __syncthreads();

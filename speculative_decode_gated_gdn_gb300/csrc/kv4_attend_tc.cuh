@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   constexpr int W = S::W, NK = S::NK;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t raw_full[kTcRing], raw_empty[kTcRing], unit_full[kTcUnits], unit_empty[kTcUnits];
-  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], m_full[2];
-  __shared__ uint64_t pv_done, q_full, joined, drained;
+  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], m_full[2], pv_done[2];
+  __shared__ uint64_t q_full, joined, drained;
   __shared__ TcUnit s_unit[kTcUnits];
   __shared__ uint32_t s_tmem;
   __shared__ long long s_warp[kTcThreads / 32];
@@ -277,9 +277,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128), mbar_init(&v_full[i], 128);
       mbar_init(&k_empty[i], 1), mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&m_full[i], 128);
+      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&m_full[i], 128), mbar_init(&pv_done[i], 1);
     }
-    mbar_init(&pv_done, 1), mbar_init(&q_full, 256), mbar_init(&joined, 256), mbar_init(&drained, 1);
+    mbar_init(&q_full, 256), mbar_init(&joined, 256), mbar_init(&drained, 1);
     s_dead = 0;
     fence_mbar_init();
   }
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (i < n) {
           const uint32_t it = base + i, buf = it & 1;
           // the P of two tiles ago that lies over them is used up
-          if (i > 1) ok = wait_warp(&pv_done, (it - 2) & 1);
+          if (i > 1) ok = wait_warp(&pv_done[buf], ((it - 2) >> 1) & 1);
           ok = ok && wait_warp(&k_full[buf], (it >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
             if (buf) tc_output<D, 1>(kv, i > 1);
             else tc_output<D, 0>(kv, i > 1);
             umma_commit(&v_empty[buf]);
-            umma_commit(&pv_done);
+            umma_commit(&pv_done[buf]);
           }
           __syncwarp();
         }
@@ -745,7 +745,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         }
         if (own != m) l *= own == -INFINITY ? 0.f : ex2(own - m);
         if (k > 0 && __any_sync(0xffffffffu, move)) {
-          ok = wait_warp(&pv_done, (it - 1) & 1);  // every product before this tile's is in O
+          // every product before this tile's is in O.  (A wait names a phase by its
+          // parity, so the one before has to be over: this tile's scores were let go
+          // after the product of three tiles ago.)
+          ok = wait_warp(&pv_done[wg ^ 1], ((it - 1) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -802,17 +805,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       if (!ok) break;
       // ---- the unit's rows, or a part of them: half of the words a group -----------------
       const uint32_t last_it = base + n - 1;
-      ok = wait_warp(&pv_done, last_it & 1);
+      // The group of the last tile waits for its product, which ends after all
+      // others; the other group learns of it at `joined`.
+      if ((last_it & 1) == wg) ok = wait_warp(&pv_done[wg], (last_it >> 1) & 1);
       if (!ok) break;
-      tc_fence_after();
-      if (n > 1 && ((base + n - 2) & 1) == wg) look(n - 2);
-      if ((last_it & 1) == wg) look(n - 1);
       s_sum[wg][r] = l, s_own[wg][r] = m;
       s_nan[wg * kTcRows + r] = nan;
       mbar_arrive(&joined);
       ok = wait_warp(&joined, joins++ & 1);
       if (!ok) break;
+      tc_fence_after();
       nan |= s_nan[(wg ^ 1) * kTcRows + r];
+      if (n > 1) look(n - 2);  // neither group has looked at these two
+      look(n - 1);
       {
         const float mo = s_own[wg ^ 1][r], lo = s_sum[wg ^ 1][r];
         const float M = fmaxf(m, mo);  // the later tile's reference

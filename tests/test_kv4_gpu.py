@@ -399,6 +399,19 @@ def test_attend_workspace_is_ready_again_and_repeatable(gdn):
             assert torch.equal(bits(out), bits(a))
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,T,n", [(8, 1, 128, 8, 200), (16, 2, 256, 40, 300), (4, 4, 64, 70, 500), (16, 2, 256, 2, 3000), (8, 2, 128, 1, 777)])
+def test_attend_gives_equal_bits_call_after_call(gdn, Hq, Hkv, d, T, n):
+    """Forty calls without a wait between them: the split and the joins leave nothing to timing."""
+    rows = [(T, T, T), (n, T, T), (n // 2, max(1, T - 1), T)]
+    cache, table, q_start, q_count, kv_len, q = attend_case(Hq, Hkv, d, 16, rows, seed=11)
+    a, ws, kd, args = run_attend(cache, table, q_start, q_count, kv_len, q, 0.09, T)
+    outs = [torch.empty_like(a) for _ in range(40)]
+    for o in outs:
+        L.gdn_kv4_attend(kd, *args, 0.09, o, ws, T)
+    torch.cuda.synchronize()
+    assert all(torch.equal(bits(o), bits(a)) for o in outs)
+
+
 def test_attend_on_another_stream_and_in_a_graph(gdn):
     rows = [(2000, 2, 2), (500, 1, 2)]
     cache, table, q_start, q_count, kv_len, q = attend_case(8, 2, 128, 32, rows, seed=8)
