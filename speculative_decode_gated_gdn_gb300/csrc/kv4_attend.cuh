@@ -36,6 +36,8 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "kv4.cuh"
 
 namespace gdn {
@@ -396,11 +398,20 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   const bool half_page = P > ST;
   const int n_sub = half_page ? 4 : ST >> p.g.log2P;
   const uint32_t rec_bytes = kv4_record_bytes(D, P);
-  auto page_of = [&](const AttPiece &u, int st) -> int {
-    const int t = st * ST + (half_page ? 0 : lane << p.g.log2P);
-    return lane < n_sub && t < u.lim_max && st < u.st_hi ? p.table[size_t(u.b) * p.g.max_pages + (t >> p.g.log2P)] : -2;
+  // Table cells of the stages ahead, a lane a cell: `look` loads those of kBatch
+  // stages from `st` on, so that a stage costs no round trip to the table.
+  const int n_cells = half_page ? 1 : n_sub;  // cells of a stage
+  constexpr int kBatch = 32 * 16 / ST > 32 ? 32 : 32 * 16 / ST;  // stages whose cells 32 lanes hold at any page size
+  int cells = -2, cells_st = 0;               // the lane's cell, the first stage they are of
+  auto look = [&](const AttPiece &u, int st) {
+    const int k = lane / n_cells, t = (st + k) * ST + ((lane - k * n_cells) << p.g.log2P);
+    cells_st = st;
+    cells = k < kBatch && st + k < u.st_hi && t < u.lim_max ? p.table[size_t(u.b) * p.g.max_pages + (t >> p.g.log2P)] : -2;
   };
-  auto issue = [&](const AttPiece &u, int st, int page) {
+  auto issue = [&](const AttPiece &u, int st) {
+    const int k = (st - cells_st) * n_cells + (half_page ? 0 : lane);
+    int page = __shfl_sync(0xffffffffu, cells, k & 31);
+    if (lane >= n_sub) page = -2;
     bool ok = page != -2;
     if (ok && (page < 0 || page >= p.g.n_pages)) {
       ok = false;
@@ -435,19 +446,20 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   const uint32_t lane_e0 = att_key(2 * j) * (4 * W), lane_e1 = att_key(2 * j + 1) * (4 * W);
 
   // the piece whose stages are being issued: the current one or the one behind it
-  int ahead = 0, issued = pieces[0].st0, next = page_of(pieces[0], issued);
+  int ahead = 0, issued = pieces[0].st0;
   int flight = 0;     // stages issued and not read yet
   uint32_t turn = 0;  // pieces[turn & 1] is the current piece
-  auto refill = [&]() {
+  look(pieces[0], issued);
+  auto refill = [&](bool go_on) {
 #pragma unroll 1
     while (flight < S::kSlots && !dead) {
       if (issued < pieces[ahead].st_hi) {
-        const int page = next;
-        next = page_of(pieces[ahead], issued + 1);
-        issue(pieces[ahead], issued, page);
+        if (issued - cells_st >= kBatch) look(pieces[ahead], issued);
+        issue(pieces[ahead], issued);
         ++issued, ++flight;
-      } else if (ahead == int(turn & 1) && pieces[ahead].more) {  // on into the next piece
-        ahead ^= 1, issued = pieces[ahead].st0, next = page_of(pieces[ahead], issued);
+      } else if (go_on && ahead == int(turn & 1) && pieces[ahead].more) {  // on into the next piece
+        ahead ^= 1, issued = pieces[ahead].st0;
+        look(pieces[ahead], issued);
       } else {
         break;
       }
@@ -459,10 +471,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     // (the loop's step reads `more` of the piece that is done)
     const AttPiece &cur = pieces[turn & 1];
     const int lim_max = cur.lim_max, st_hi = cur.st_hi, st_first = cur.st0;
-    __syncwarp();  // every lane is done with the piece before
-    if (lane == 0) follow(pieces[turn & 1], pieces[(turn & 1) ^ 1]);
-    __syncwarp();
-    refill();
+    refill(false);
     // ---- the tile's queries: rows n and (R = 16) n + 8 ---------------------------------
     const AttRow row = cur.row;
     const int R0 = cur.tile * R + n, R1 = R0 + 8;
@@ -533,6 +542,9 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     float o_acc[S::kRegs / 4][4];
 #pragma unroll
     for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] = o_acc[i][1] = o_acc[i][2] = o_acc[i][3] = 0.f;
+    __syncwarp();  // every lane is done with the piece before
+    if (lane == 0) follow(pieces[turn & 1], pieces[(turn & 1) ^ 1]);
+    __syncwarp();
     uint32_t nan0 = 0, nan1 = 0;  // groups in which the row has seen a value that is not finite
     float m0 = -INFINITY, m1 = -INFINITY;
     F2 l0 = f2(0.f, 0.f), l1 = f2(0.f, 0.f);
@@ -708,9 +720,9 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
      }
       __syncwarp();  // every lane is done with the slot
       slot = slot + 1 == S::kSlots ? 0 : slot + 1;
-      refill();
+      refill(true);
     }
-    refill();  // a piece without copies has not gone on yet
+    refill(true);  // a piece without copies has not gone on yet
 
     // ---- the piece's outputs ---------------------------------------------------------
     float la, lb, l0s, l1s;
@@ -899,37 +911,18 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     }
     __syncthreads();
     if (!s_flag) continue;
-    // 16 parts at a time: their weights by 16 R threads, then the items
-    float M = -INFINITY;  // of row tid % R
-    if (tid < 16 * R) {
-      for (int q = c_first + tid / R; q <= c_last; q += 16) M = fmaxf(M, __ldcg(part_of(q, c_first) + S::kPart + tid % R));
-      join.w[tid / R][tid % R] = M;
-    }
-    if (tid < R) join.sum[e][tid] = 0.f;
-    __syncthreads();
-    if (tid < 16 * R)
-      for (int q = 0; q < 16; ++q) M = fmaxf(M, join.w[q][tid % R]);
+    // 16 parts at a time: maxima and sums by 16 R threads, then the items, whose
+    // first loads are on their way meanwhile
     constexpr int kItems = (S::kPairs + S::kThreads - 1) / S::kThreads;
     float2 y[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) y[k] = make_float2(0.f, 0.f);
+    if (tid < R) join.max[e][tid] = -INFINITY, join.sum[e][tid] = 0.f;
 #pragma unroll 1
     for (int q0 = c_first; q0 <= c_last; q0 += 16) {
       const int some = min(16, c_last + 1 - q0);
-      __syncthreads();
-      if (tid < 16 * R && tid / R < some) {
-        const float *src = part_of(q0 + tid / R, c_first) + S::kPart + tid % R;
-        const float l = __ldcg(src + 16), w = weight(__ldcg(src), l, M);
-        join.w[tid / R][tid % R] = w;
-        join.lw[tid / R][tid % R] = l * w;
-      }
-      __syncthreads();
-      if (tid < R)
-        for (int q = 0; q < some; ++q) join.sum[e][tid] += join.lw[q][tid];
-      // the loads of four parts, all of a thread's items, are on their way together
-#pragma unroll 1
-      for (int q = 0; q < some; q += 4) {
-        float2 v[4][kItems];
+      float2 v[4][kItems];
+      auto load4 = [&](int q) {
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll
@@ -938,13 +931,56 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
             v[f][k] = item < S::kPairs && q + f < some ? __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q + f, c_first)) + item)
                                                        : make_float2(0.f, 0.f);
           }
+      };
+      float m = -INFINITY, l = 0.f;
+      if (tid < 16 * R && tid / R < some) {
+        const float *src = part_of(q0 + tid / R, c_first) + S::kPart + tid % R;
+        m = __ldcg(src), l = __ldcg(src + 16);
+      }
+      load4(0);
+      __syncthreads();
+      if (tid < 16 * R) join.w[tid / R][tid % R] = m;
+      __syncthreads();
+      float M = -INFINITY;
+      if (tid < 16 * R) {
+        M = join.max[e][tid % R];
+        for (int q = 0; q < 16; ++q) M = fmaxf(M, join.w[q][tid % R]);
+      }
+      __syncthreads();
+      if (tid < 16 * R) {
+        const float w = weight(m, l, M);
+        join.w[tid / R][tid % R] = w, join.lw[tid / R][tid % R] = tid / R < some ? l * w : 0.f;
+        if (tid < R) {
+          const float old = join.max[e][tid];
+          join.c[0][0][tid] = old == -INFINITY ? 0.f : ex2(old - M);  // of the batches before
+          join.max[e][tid] = M;
+        }
+      }
+      __syncthreads();
+      if (tid < R) {
+        float L = join.sum[e][tid];
+        L = L != L ? L : L * join.c[0][0][tid];
+        for (int q = 0; q < 16; ++q) L += join.lw[q][tid];
+        join.sum[e][tid] = L;
+      }
+      if (q0 > c_first) {
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+          int ln, x, t, r, col;
+          place(k * S::kThreads + tid, ln, x, t, r, col);
+          const float w = join.c[0][0][r];
+          y[k].x *= w, y[k].y *= w;
+        }
+      }
+#pragma unroll 1
+      for (int q = 0; q < some; q += 4) {
+        if (q > 0) load4(q);
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll
           for (int k = 0; k < kItems; ++k) {
-            const int item = k * S::kThreads + tid;
             int ln, x, t, r, col;
-            place(item, ln, x, t, r, col);
+            place(k * S::kThreads + tid, ln, x, t, r, col);
             const float w = q + f < some ? join.w[q + f][r] : 0.f;
             y[k].x = fmaf(v[f][k].x, w, y[k].x), y[k].y = fmaf(v[f][k].y, w, y[k].y);
           }
@@ -969,10 +1005,22 @@ inline size_t att_mma_ws(int ctas) {
   return 4096 + sizeof(float) * size_t(ctas) * (2 * att_part_floats<D, R>() + size_t(AttShape<D, R>::NW) * AttShape<D, R>::kPart);
 }
 
+// Raise a kernel's shared-memory limit, once per device.
+inline cudaError_t att_configure(const void *kernel, int smem, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 template <int D, int R>
 cudaError_t launch_att_mma_r(const Kv4AttendParams &p, int ctas, cudaStream_t s) {
   using S = AttShape<D, R>;
-  const cudaError_t e = cudaFuncSetAttribute(kv4_attend_mma<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  static std::atomic<bool> configured[64];
+  const cudaError_t e = att_configure(reinterpret_cast<const void *>(kv4_attend_mma<D, R>), S::kSmem, configured);
   if (e != cudaSuccess) return e;
   return launch_pdl_smem(kv4_attend_mma<D, R>, dim3(ctas), dim3(S::kThreads), S::kSmem, s, p);
 }

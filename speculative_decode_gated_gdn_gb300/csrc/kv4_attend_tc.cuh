@@ -932,7 +932,8 @@ inline size_t att_tc_ws(int ctas) {
 
 template <int D>
 cudaError_t launch_att_tc(const Kv4AttendParams &p, int ctas, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kv4_attend_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+  static std::atomic<bool> configured[64];
+  const cudaError_t e = att_configure(reinterpret_cast<const void *>(kv4_attend_tc<D>), TcShape<D>::kSmem, configured);
   if (e != cudaSuccess) return e;
   return launch_pdl_smem(kv4_attend_tc<D>, dim3(ctas), dim3(kTcThreads), TcShape<D>::kSmem, s, p);
 }

@@ -140,6 +140,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load (building first if missing or stale) and return the ctypes library."""
     global _lib
+    if path is None and _lib is not None:  # every call comes through here
+        return _lib
     with _lock:
         if _lib is None or path is not None:
             p = path or _build.build()
@@ -158,7 +160,7 @@ def _ptr(t, what, dtype=None):
     """Device pointer of a tensor (or a raw int pointer / None)."""
     if t is None or isinstance(t, int):
         return t
-    import torch
+    torch = _t()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch.Tensor or an int pointer")
     if not t.is_cuda:
@@ -172,8 +174,7 @@ def _ptr(t, what, dtype=None):
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _t().cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -184,9 +185,15 @@ def _check(rc, fn):
         raise GdnError(rc, fn, load().gdn_last_error().decode())
 
 
+_torch = None
+
+
 def _t():
-    import torch
-    return torch
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def gdn_version() -> str:
@@ -410,7 +417,10 @@ def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, fre
 
 def _cache(kd, pages):
     """Pointer of a cache; it may be larger than its dims say, never smaller."""
-    need = kd.n_pages * gdn_kv4_page_bytes(kd)
+    key = (kd.H_kv, kd.d, kd.page)
+    if kd.__dict__.get("_key") != key:  # the page's size is asked for once
+        kd._key, kd._page_bytes = key, gdn_kv4_page_bytes(kd)
+    need = kd.n_pages * kd._page_bytes
     p = _ptr(pages, "pages", _t().uint8)
     if pages.numel() < need:
         raise ValueError(f"pages: {pages.numel()} bytes, needs {need}")
