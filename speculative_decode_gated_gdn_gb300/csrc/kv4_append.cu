@@ -62,14 +62,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 template <int D>
 __device__ __forceinline__ void store_codes(const float (&y)[8], uint8_t *codes, uint8_t *entries, int chunk, bool store) {
   constexpr int W = D / 64;
-  float mn = y[0], mx = y[0];
-  bool fine = fabsf(y[0]) <= 3.402823466e38f;
+  float mn = y[0], mx = y[0], nil = y[0] * 0.f;
 #pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    mn = fminf(mn, y[e]), mx = fmaxf(mx, y[e]);
-    fine = fine && fabsf(y[e]) <= 3.402823466e38f;
-  }
-  int ok = fine;
+  for (int e = 1; e < 8; ++e) mn = fminf(mn, y[e]), mx = fmaxf(mx, y[e]), nil = fmaf(y[e], 0.f, nil);
+  int ok = nil == 0.f;  // an infinity or NaN leaves a NaN
 #pragma unroll
   for (int o = W; o < 8 * W; o <<= 1) {
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -82,10 +78,24 @@ __device__ __forceinline__ void store_codes(const float (&y)[8], uint8_t *codes,
   const float b = __half2float(base), s = __half2float(step);
   uint32_t word = 0;
   if (ok && s > 0.f) {
+    // (y - b) / s by a reciprocal, off by a few 2^-23 of at most 15: only next to
+    // a border between two codes can that matter, and there the division decides
+    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the sum's last bits are the nearest integer
+    const float inv = __fdividef(1.f, s);
+    bool near = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(y[e], b), s)), 0.f), 15.f);
-      word |= uint32_t(c) << (4 * e);
+      const float t = fminf(fmaxf(__fsub_rn(y[e], b) * inv, 0.f), 15.f), u = __fadd_rn(t, kMagic);
+      near = near || fabsf(t - __fsub_rn(u, kMagic)) > 0.4999f;
+      word |= (__float_as_uint(u) & 15u) << (4 * e);
+    }
+    if (near) {
+      word = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(y[e], b), s)), 0.f), 15.f);
+        word |= uint32_t(c) << (4 * e);
+      }
     }
   }
   if (!store) return;
@@ -138,68 +148,85 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4App
   const int per = (heads + splits - 1) / splits;
   const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
   const int partner = lane + (p.pairs || !turned ? 0 : (8 * chunk < half ? half / 8 : -half / 8));
-  const float sign = 8 * chunk < half ? -1.f : 1.f;
-  for (int hb = h0; hb < h1; hb += HPW) {
-    const int h = hb + sub;
-    const bool in = h < h1;
-    const int kind = h < p.H_q ? 0 : h < p.H_q + p.H_kv ? 1 : 2;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (in) {
-      const uint16_t *src = kind == 0   ? p.q + n * p.q_stride + size_t(h) * D
-                            : kind == 1 ? p.k + n * p.k_stride + size_t(h - p.H_q) * D
-                                        : p.v + n * p.v_stride + size_t(h - p.H_q - p.H_kv) * D;
-      raw = ld_stream_u4(src + 8 * chunk);
-    }
-    float y[8];
-    unpack8(raw, y);
-    if (p.rot) {  // every lane takes part in the exchange
-      if (p.pairs) {
-        if (turned && kind < 2) {
+  if (!p.pairs && 8 * chunk < half) {  // the lower half takes the partner's product away
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float a = y[e], b = y[e + 1];
-            y[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
-            y[e + 1] = __fadd_rn(__fmul_rn(b, cs[e + 1]), __fmul_rn(a, sn[e + 1]));
-          }
-        }
-      } else {
-        uint4 o;
-        o.x = __shfl_sync(0xffffffffu, raw.x, partner);
-        o.y = __shfl_sync(0xffffffffu, raw.y, partner);
-        o.z = __shfl_sync(0xffffffffu, raw.z, partner);
-        o.w = __shfl_sync(0xffffffffu, raw.w, partner);
-        if (turned && kind < 2) {
-          float z[8];
-          unpack8(o, z);
+    for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+  }
+  // the loads of kAhead heads are on their way together
+  constexpr int kAhead = 4;
+#pragma unroll 1
+  for (int hb = h0; hb < h1; hb += kAhead * HPW) {
+    uint4 raws[kAhead];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), sign * __fmul_rn(z[e], sn[e]));
-        }
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u * HPW + sub;
+      raws[u] = make_uint4(0, 0, 0, 0);
+      if (h < h1) {
+        const uint16_t *src = h < p.H_q              ? p.q + n * p.q_stride + size_t(h) * D
+                              : h < p.H_q + p.H_kv ? p.k + n * p.k_stride + size_t(h - p.H_q) * D
+                                                   : p.v + n * p.v_stride + size_t(h - p.H_q - p.H_kv) * D;
+        raws[u] = ld_stream_u4(src + 8 * chunk);
       }
     }
-    if (in && kind == 0)
-      *reinterpret_cast<uint4 *>(p.q_out + (size_t(n) * p.H_q + h) * D + 8 * chunk) = pack8(y);
-    // the groups' exchanges need every lane of a head, so the whole warp goes in
-    if (__any_sync(0xffffffffu, in && kind > 0)) {
-      const int hk = kind == 1 ? h - p.H_q : h - p.H_q - p.H_kv;
-      const bool store = in && kind > 0 && write;
-      uint8_t *rec = p.pages + (size_t(page) * p.H_kv + (store ? hk : 0)) * kv4_record_bytes(D, P);
-      const int w = kind == 2;
-      store_codes<D>(y, rec + w * kv4_code_bytes(D, P) + off * (D / 2),
-                     rec + 2 * kv4_code_bytes(D, P) + w * kv4_entry_bytes(D, P) + off * (W * 4), chunk, store);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u * HPW + sub;
+      if (hb + u * HPW >= h1) break;  // the whole warp
+      const bool in = h < h1;
+      const int kind = h < p.H_q ? 0 : h < p.H_q + p.H_kv ? 1 : 2;
+      const uint4 raw = raws[u];
+      float y[8];
+      unpack8(raw, y);
+      if (p.rot) {  // every lane takes part in the exchange
+        if (p.pairs) {
+          if (turned && kind < 2) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float a = y[e], b = y[e + 1];
+              y[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+              y[e + 1] = __fadd_rn(__fmul_rn(b, cs[e + 1]), __fmul_rn(a, sn[e + 1]));
+            }
+          }
+        } else {
+          uint4 o;
+          o.x = __shfl_sync(0xffffffffu, raw.x, partner);
+          o.y = __shfl_sync(0xffffffffu, raw.y, partner);
+          o.z = __shfl_sync(0xffffffffu, raw.z, partner);
+          o.w = __shfl_sync(0xffffffffu, raw.w, partner);
+          if (turned && kind < 2) {
+            float z[8];
+            unpack8(o, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), __fmul_rn(z[e], sn[e]));
+          }
+        }
+      }
+      if (in && kind == 0)
+        *reinterpret_cast<uint4 *>(p.q_out + (size_t(n) * p.H_q + h) * D + 8 * chunk) = turned ? pack8(y) : raw;
+      // the groups' exchanges need every lane of a head, so the whole warp goes in
+      if (__any_sync(0xffffffffu, in && kind > 0)) {
+        const int hk = kind == 1 ? h - p.H_q : h - p.H_q - p.H_kv;
+        const bool store = in && kind > 0 && write;
+        uint8_t *rec = p.pages + (size_t(page) * p.H_kv + (store ? hk : 0)) * kv4_record_bytes(D, P);
+        const int w = kind == 2;
+        store_codes<D>(y, rec + w * kv4_code_bytes(D, P) + off * (D / 2),
+                       rec + 2 * kv4_code_bytes(D, P) + w * kv4_entry_bytes(D, P) + off * (W * 4), chunk, store);
+      }
     }
   }
 }
 
+// Two words (16 channels) a thread.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(const Kv4ReadParams p) {
-  constexpr int LPH = D / 8, W = D / 64;
+  constexpr int LPH = D / 16, W = D / 64;
   pdl_wait();
   pdl_trigger();
   const long long item = (blockIdx.x * (long long)kAppendThreads + threadIdx.x) / LPH;  // (token, head, K or V)
-  const int chunk = threadIdx.x % LPH;
+  const int pair = threadIdx.x % LPH;
   const long long th = item >> 1;
   if (th >= (long long)p.N * p.H_kv) return;
-  const int w = int(item & 1), n = int(th / p.H_kv), h = int(th % p.H_kv);
+  const int w = int(item & 1), n = int(th / p.H_kv), h = int(th - (long long)n * p.H_kv);
   const int P = 1 << p.log2P;
   const int slot = p.slots[n];
   bool in = slot >= 0;
@@ -207,21 +234,28 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_read_kernel(const Kv4ReadP
     in = false;
     atomicOr(p.status, GDN_STATUS_BAD_INDEX);
   }
-  float y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = 0.f;
+  uint2 word = make_uint2(0, 0), entry = make_uint2(0, 0);
   if (in) {
     const int off = slot & (P - 1);
     const uint8_t *rec = p.pages + (size_t(slot >> p.log2P) * p.H_kv + h) * kv4_record_bytes(D, P);
-    const uint32_t word = *reinterpret_cast<const uint32_t *>(rec + w * kv4_code_bytes(D, P) + off * (D / 2) + 4 * chunk);
-    const uint32_t entry = *reinterpret_cast<const uint32_t *>(rec + 2 * kv4_code_bytes(D, P) + w * kv4_entry_bytes(D, P) +
-                                                               (off * W + chunk % W) * 4);
-    const float s = __half2float(__ushort_as_half(uint16_t(entry))), b = __half2float(__ushort_as_half(uint16_t(entry >> 16)));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = fmaf(s, float((word >> (4 * e)) & 15u), b);  // s * code is exact in fp32
+    word = *reinterpret_cast<const uint2 *>(rec + w * kv4_code_bytes(D, P) + off * (D / 2) + 8 * pair);
+    const uint8_t *e = rec + 2 * kv4_code_bytes(D, P) + w * kv4_entry_bytes(D, P) + off * (W * 4);
+    if (W == 1) {
+      entry.x = entry.y = *reinterpret_cast<const uint32_t *>(e);
+    } else {
+      entry = *reinterpret_cast<const uint2 *>(e + (2 * pair % W) * 4);
+    }
   }
-  uint16_t *dst = (w ? p.v : p.k) + (size_t(n) * p.H_kv + h) * D + 8 * chunk;
-  *reinterpret_cast<uint4 *>(dst) = pack8(y);
+  uint4 *dst = reinterpret_cast<uint4 *>((w ? p.v : p.k) + (size_t(n) * p.H_kv + h) * D + 16 * pair);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t c = k ? word.y : word.x, g = k ? entry.y : entry.x;
+    const float s = __half2float(__ushort_as_half(uint16_t(g))), b = __half2float(__ushort_as_half(uint16_t(g >> 16)));
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = fmaf(s, float((c >> (4 * e)) & 15u), b);  // s * code is exact in fp32
+    dst[k] = pack8(y);
+  }
 }
 
 template <int D>
@@ -245,7 +279,7 @@ cudaError_t launch_append(const Kv4AppendParams &p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_read(const Kv4ReadParams &p, cudaStream_t s) {
-  const long long threads = (long long)p.N * p.H_kv * 2 * (D / 8);
+  const long long threads = (long long)p.N * p.H_kv * 2 * (D / 16);
   return launch_pdl(kv4_read_kernel<D>, dim3(unsigned((threads + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), s, p);
 }
 
