@@ -107,7 +107,7 @@ __device__ __forceinline__ void store_codes(const float (&y)[8], uint8_t *codes,
 // One token a warp sub-group: D / 8 lanes hold a head, the warp's 32 / (D / 8)
 // heads at a time; blockIdx.y splits the heads of a token where tokens are few.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4AppendParams p, const int splits) {
+__global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const Kv4AppendParams p, const int splits) {
   constexpr int LPH = D / 8, HPW = 32 / LPH, W = D / 64;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = lane % LPH, sub = lane / LPH;
@@ -115,6 +115,27 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4App
   pdl_wait();
   pdl_trigger();
   if (n >= p.N) return;  // whole warps
+  const int heads = p.H_q + 2 * p.H_kv;
+  const int per = (heads + splits - 1) / splits;
+  const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
+  // the loads of kAhead heads are on their way together, the next ones' and the
+  // angles' while these are worked on
+  constexpr int kAhead = 2;
+  uint4 raws[kAhead];
+  auto load = [&](int hb) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u * HPW + sub;
+      raws[u] = make_uint4(0, 0, 0, 0);
+      if (h < h1) {
+        const uint16_t *src = h < p.H_q              ? p.q + n * p.q_stride + size_t(h) * D
+                              : h < p.H_q + p.H_kv ? p.k + n * p.k_stride + size_t(h - p.H_q) * D
+                                                   : p.v + n * p.v_stride + size_t(h - p.H_q - p.H_kv) * D;
+        raws[u] = ld_stream_u4(src + 8 * chunk);
+      }
+    }
+  };
+  load(h0);
   const int P = 1 << p.log2P;
   const int slot = p.slots[n];
   bool write = slot >= 0;
@@ -144,37 +165,24 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4App
   }
   write = __all_sync(0xffffffffu, write);
   const int page = write ? slot >> p.log2P : 0, off = write ? slot & (P - 1) : 0;
-  const int heads = p.H_q + 2 * p.H_kv;
-  const int per = (heads + splits - 1) / splits;
-  const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
   const int partner = lane + (p.pairs || !turned ? 0 : (8 * chunk < half ? half / 8 : -half / 8));
   if (!p.pairs && 8 * chunk < half) {  // the lower half takes the partner's product away
 #pragma unroll
     for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
   }
-  // the loads of kAhead heads are on their way together
-  constexpr int kAhead = 4;
 #pragma unroll 1
   for (int hb = h0; hb < h1; hb += kAhead * HPW) {
-    uint4 raws[kAhead];
+    uint4 now[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = hb + u * HPW + sub;
-      raws[u] = make_uint4(0, 0, 0, 0);
-      if (h < h1) {
-        const uint16_t *src = h < p.H_q              ? p.q + n * p.q_stride + size_t(h) * D
-                              : h < p.H_q + p.H_kv ? p.k + n * p.k_stride + size_t(h - p.H_q) * D
-                                                   : p.v + n * p.v_stride + size_t(h - p.H_q - p.H_kv) * D;
-        raws[u] = ld_stream_u4(src + 8 * chunk);
-      }
-    }
+    for (int u = 0; u < kAhead; ++u) now[u] = raws[u];
+    load(hb + kAhead * HPW);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int h = hb + u * HPW + sub;
       if (hb + u * HPW >= h1) break;  // the whole warp
       const bool in = h < h1;
       const int kind = h < p.H_q ? 0 : h < p.H_q + p.H_kv ? 1 : 2;
-      const uint4 raw = raws[u];
+      const uint4 raw = now[u];
       float y[8];
       unpack8(raw, y);
       if (p.rot) {  // every lane takes part in the exchange
