@@ -259,9 +259,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   __shared__ TcUnit s_unit[kTcUnits];
   __shared__ uint32_t s_tmem;
   __shared__ long long s_warp[kTcThreads / 32];
-  __shared__ long long s_place[2];
+  __shared__ struct {
+    int b;
+    TcRow row;
+    long long in_row, len;
+  } s_at;  // the row that holds the CTA's first place
   __shared__ float s_ref[kTcRows], s_sum[2][kTcRows], s_own[2][kTcRows];
-  __shared__ uint32_t s_nan[2 * kTcRows];
+  __shared__ uint32_t s_nan[2 * kTcRows], s_mx[2][kTcRows];
   __shared__ int s_flag, s_dead;
   // keys of a V tile with a value that is not finite, per group; of four tiles,
   // since the rows look two tiles later
@@ -288,52 +292,43 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   pdl_trigger();
 
   // ---- this CTA's piece of the line --------------------------------------------------
-  long long total = 0, mine = 0;
+  // rows beyond the CTA's threads are summed first and looked at again below
+  auto places = [&](const TcRow &r) -> long long { return tc_row_stages<NK>(r, TT) * Hkv; };
+  long long total = 0, mine = 0, before, len = 0;
+  TcRow own{};
 #pragma unroll 1
-  for (int b = tid; b < p.g.B; b += kTcThreads) mine += tc_row_stages<NK>(tc_row(p, b, TT, blockIdx.x == 0), TT);
-  tc_scan(mine, s_warp, &total);
-  total *= Hkv;
+  for (int b = tid; b < p.g.B; b += kTcThreads) {
+    const TcRow r = tc_row(p, b, TT, blockIdx.x == 0);
+    const long long x = places(r);
+    if (b == tid) own = r, len = x;
+    mine += x;
+  }
+  before = tc_scan(mine, s_warp, &total);
   // a piece is worth its fixed costs, or there are fewer
   const int ctas = int(min((long long)gridDim.x, (total + kTcUnitCost + 1) / (kTcUnitCost + 2)));
   const int c = blockIdx.x;
   if (c >= ctas) return;
   // pieces of `per` places, the first `more` of one more
-  const long long per = total / ctas;
+  const long long per = total < (1ll << 31) ? int(total) / ctas : total / ctas;
   const int more = int(total - per * ctas);
   const long long at0 = per * c + min(c, more), stop = at0 + per + (c < more);
   auto cta_of = [&](long long x) -> int {
     const long long y = x - more * (per + 1);
+    if (x < (1ll << 31)) return y < 0 ? int(x) / int(per + 1) : more + int(y) / int(per);
     return int(y < 0 ? x / (per + 1) : more + y / per);
   };
-  // the row, and in it the query tile, that hold at0: the same search twice
-  long long want = at0;
-  int b_at = 0, hk_at = 0, t_at = 0, st_at = 0;
-  TcRow row_at{};
+  // the row that holds at0, by its thread
+  long long before0 = 0;
 #pragma unroll 1
-  for (int level = 0; level < 2; ++level) {
-    const int n = level ? row_at.tiles : p.g.B;
-    long long before0 = 0;
-#pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += kTcThreads) {
-      const int i = i0 + tid;
-      long long v = 0, sum;
-      if (i < n) v = level ? tc_stages<NK>(row_at, i, TT) + kTcUnitCost : tc_row_stages<NK>(tc_row(p, i, TT, false), TT) * Hkv;
-      const long long before = before0 + tc_scan(v, s_warp, &sum);
-      if (want >= before && want < before + v) s_place[0] = i, s_place[1] = want - before;
+  for (int b0 = 0; b0 < p.g.B; b0 += kTcThreads) {
+    if (p.g.B > kTcThreads) {
+      long long sum;
+      len = 0;
+      if (b0 + tid < p.g.B) own = tc_row(p, b0 + tid, TT, false), len = places(own);
+      before = before0 + tc_scan(len, s_warp, &sum);
       before0 += sum;
-      if (want < before0) break;  // the same for every thread
     }
-    __syncthreads();
-    if (level == 0) {
-      b_at = int(s_place[0]);
-      row_at = tc_row(p, b_at, TT, false);
-      const long long head = tc_row_stages<NK>(row_at, TT);
-      want = s_place[1];
-      while (want >= head) want -= head, ++hk_at;
-    } else {
-      t_at = int(s_place[0]), st_at = int(s_place[1]);
-    }
-    __syncthreads();
+    if (at0 >= before && at0 < before + len) s_at.b = b0 + tid, s_at.row = own, s_at.in_row = at0 - before, s_at.len = len;
   }
 
   if (warp == 16) tmem_alloc(&s_tmem, S::kCols);
@@ -362,8 +357,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   if (warp == 18) {
     // ---- units ------------------------------------------------------------------------------
     long long at = at0;
-    int b = b_at, hk = hk_at, t = t_at, place = st_at;  // place in the unit, of stages + kTcUnitCost
-    TcRow row = row_at;
+    int b = s_at.b, hk = 0, t = 0, place;  // place in the unit, of stages + kTcUnitCost
+    TcRow row = s_at.row;
+    {
+      // the head, then the query tile: 32 at a time
+      const long long head = s_at.len / Hkv;
+      long long left = s_at.in_row;
+      while (left >= head) left -= head, ++hk;
+#pragma unroll 1
+      for (;;) {
+        const int v = t + lane < row.tiles ? tc_stages<NK>(row, t + lane, TT) + kTcUnitCost : 0;
+        int sum = v;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += u;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, sum > left);
+        if (past) {
+          const int f = __ffs(past) - 1;
+          t += f;
+          place = int(left) - __shfl_sync(0xffffffffu, sum - v, f);
+          break;
+        }
+        left -= __shfl_sync(0xffffffffu, sum, 31);
+        t += 32;
+      }
+    }
     bool ok = true;
     uint32_t k = 0;
 #pragma unroll 1
@@ -497,8 +517,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   } else if (warp >= 12) {
     // ---- V^T: 8 keys of one word (8 channels) at a time, 16 bytes of 8 rows ------------------
     const int vt = tid - 384;
-    constexpr int kWords = D / 8, kTasks = NK / 8 * kWords / 128;
+    constexpr int kWords = D / 8, kTasks = NK / 8 * kWords / 128, kChunkStep = 128 / kWords;
     uint32_t had = 0;  // bit kTasks * (tile % 4) + i: the thread noted keys of task i
+    // what a thread's tasks read and write, the same in every tile
+    const int word = vt % kWords, chunk0 = vt / kWords;  // task i has keys 8 (chunk0 + i kChunkStep) ..
+    // rows of two neighbouring chunks lie in the same banks: the odd ones read
+    // their key pairs the other way round
+    static_assert(kTasks == 1 || kChunkStep % 2 == 0, "chunks of a thread share their order");
+    const int swap = D == 256 ? 0 : chunk0 & 1;
+    const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
+    int code_at[kTasks], entry_at[kTasks], to[kTasks];
+#pragma unroll
+    for (int i = 0; i < kTasks; ++i) {
+      const int chunk = chunk0 + i * kChunkStep, off = (chunk * 8) & (P - 1);
+      const int rec = (chunk >> (p.g.log2P - 3)) * kv4_record_bytes(D, P);
+      code_at[i] = rec + kv4_code_bytes(D, P) + off * (D / 2) + word * 4;
+      entry_at[i] = rec + 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P) + (off * W + word % W) * 4;
+      to[i] = (chunk >> 3) * (D * 128) + word * 128 + (((chunk ^ word) & 7) << 4);
+    }
     uint32_t it = 0;
     bool ok = true;
     while (next_unit(ok)) {
@@ -511,35 +547,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         const uint8_t *raw = ring + slot * S::kRaw;
         uint8_t *vb = smem + (2 + buf) * S::kKBytes;
         uint32_t noted = 0;
-#pragma unroll 1
+        const bool tail = st * NK + NK > lim;
+#pragma unroll
         for (int i = 0; i < kTasks; ++i) {
-          const int id = i * 128 + vt, word = id % kWords, chunk = id / kWords;  // keys [8 chunk, 8 chunk + 8)
-          // rows of two neighbouring chunks lie in the same banks: the odd ones
-          // read their key pairs the other way round
-          const int swap = D == 256 ? 0 : chunk & 1;
-          const uint8_t *rec = raw + (chunk >> (p.g.log2P - 3)) * kv4_record_bytes(D, P);
-          const int off = (chunk * 8) & (P - 1);
-          const uint8_t *cp = rec + kv4_code_bytes(D, P) + off * (D / 2) + word * 4;
-          const uint8_t *ep = rec + 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P) + (off * W + word % W) * 4;
-          uint32_t c[8], e[8];
+          const int chunk = chunk0 + i * kChunkStep;  // keys [8 chunk, 8 chunk + 8)
+          const uint8_t *ce = raw + code_at[i] + swap * (D / 2), *co = raw + code_at[i] - swap * (D / 2);
+          const uint8_t *ee = raw + entry_at[i] + swap * (W * 4), *eo = raw + entry_at[i] - swap * (W * 4);
+          uint32_t c[8], e[8];  // of key k ^ swap
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            c[k] = *reinterpret_cast<const uint32_t *>(cp + (k ^ swap) * (D / 2));
-            e[k] = *reinterpret_cast<const uint32_t *>(ep + (k ^ swap) * (W * 4));
+            c[k] = *reinterpret_cast<const uint32_t *>((k & 1 ? co : ce) + k * (D / 2));
+            e[k] = *reinterpret_cast<const uint32_t *>((k & 1 ? eo : ee) + k * (W * 4));
           }
-          const int left = lim - st * NK - chunk * 8;  // keys that the row has
-          if (left < 8) {
+          if (tail) {  // keys that the row does not have
+            const int left = lim - st * NK - chunk * 8;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if ((k ^ swap) >= left) e[k] = 0;
           }
           // values that are not finite are left out here and put back by the rows
           // that see their key: the thread of the group's first word notes them
-          uint32_t odd = 0;
+          uint32_t nil = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) odd |= ((e[k] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+          for (int k = 0; k < 8; ++k) nil = h2_fma(e[k], 0u, nil);  // an infinity or NaN leaves a NaN
           const bool was = had >> ((it & 3) * kTasks + i) & 1u;
-          if (odd || was) {
+          if ((nil & 0x7fff7fffu) != 0 || was) {
             uint32_t bad = 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -550,15 +582,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
               if (bad) atomicOr(flag, bad << ((chunk & 3) * 8)), noted |= 1u << i;
             }
           }
-          const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
           uint32_t es[4], eb[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             es[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel0);
             eb[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel1);
           }
-          uint8_t *dst = vb + (chunk >> 3) * (D * 128) + word * 128 + (((chunk ^ word) & 7) << 4);
-#pragma unroll 1
+          uint8_t *dst = vb + to[i];
+#pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t x[4], y[4];
 #pragma unroll
@@ -583,7 +614,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   } else if (warp >= 8) {
     // ---- K: 4 words (32 channels) of a key at a time ----------------------------------------
     const int kt = tid - 256;
-    constexpr int kChunks = D / 32, kTasks = NK * kChunks / 128;
+    constexpr int kChunks = D / 32, kTasks = NK * kChunks / 128, kRowStep = 128 / kChunks;
+    // what a thread's tasks read and write, the same in every tile
+    const int c = kt % kChunks, r0 = kt / kChunks;  // chunk, first row; task i has row r0 + i kRowStep
+    int code_at[kTasks], entry_at[kTasks], to[4];
+#pragma unroll
+    for (int i = 0; i < kTasks; ++i) {
+      const int r = r0 + i * kRowStep, off = r & (P - 1);
+      const int rec = (r >> p.g.log2P) * kv4_record_bytes(D, P);
+      code_at[i] = rec + off * (D / 2) + c * 16;
+      entry_at[i] = rec + 2 * kv4_code_bytes(D, P) + off * (W * 4);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int u = tc_unit<D>(c, q);
+      to[q] = (u >> 3) * (NK * 128) + r0 * 128 + (((u ^ r0) & 7) << 4);  // kRowStep is a multiple of 8
+    }
+    static_assert(kRowStep % 8 == 0, "rows of a thread share their swizzle");
     uint32_t it = 0;
     bool ok = true;
     while (next_unit(ok)) {
@@ -595,22 +642,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (!ok) break;
         const uint8_t *raw = ring + slot * S::kRaw;
         uint8_t *kb = smem + buf * S::kKBytes;
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < kTasks; ++i) {
-          const int id = i * 128 + kt, c = id % kChunks, r = id / kChunks;
-          const uint8_t *rec = raw + (r >> p.g.log2P) * kv4_record_bytes(D, P);
-          const int off = r & (P - 1);
-          const uint4 x4 = *reinterpret_cast<const uint4 *>(rec + off * (D / 2) + c * 16);
-          uint32_t e[W];
-          att_words<W>(e, rec + 2 * kv4_code_bytes(D, P) + off * (W * 4));
+          const uint4 x4 = *reinterpret_cast<const uint4 *>(raw + code_at[i]);
+          uint32_t e[W], step[W], base[W];
+          att_words<W>(e, raw + entry_at[i]);
+#pragma unroll
+          for (int g = 0; g < W; ++g) step[g] = __byte_perm(e[g], e[g], 0x1010), base[g] = __byte_perm(e[g], e[g], 0x3232);
           const uint32_t wd[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint32_t step = __byte_perm(e[q % W], e[q % W], 0x1010), off = __byte_perm(e[q % W], e[q % W], 0x3232);
-            const uint32_t x = wd[q], y = x >> 8;
-            const int u = tc_unit<D>(c, q);
-            *reinterpret_cast<uint4 *>(kb + (u >> 3) * (NK * 128) + r * 128 + (((u ^ r) & 7) << 4)) =
-                make_uint4(att_even(x, step, off), att_odd(x, step, off), att_even(y, step, off), att_odd(y, step, off));
+            const uint32_t x = wd[q], y = x >> 8, sw = step[q % W], bw = base[q % W];
+            *reinterpret_cast<uint4 *>(kb + to[q] + i * (kRowStep * 128)) =
+                make_uint4(att_even(x, sw, bw), att_odd(x, sw, bw), att_even(y, sw, bw), att_odd(y, sw, bw));
           }
         }
         fence_proxy_async_shared();
@@ -644,40 +688,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         // the factor of a score is kept positive: the maximum is taken before it
         const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
         if (p.scale == 0.f) f = 1.f;
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(live ? tok : 0) * p.g.H_q + (live ? head : 0)) * D);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(live ? tok : 0) * p.g.H_q + (live ? head : 0)) * D) + wg * (D / 16);
+        uint4 x[D / 16];
         uint32_t mx = 0;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {  // the group's own half last: it stays in registers
-          uint4 x[D / 16];
-          const int half = wg ^ h ^ 1;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) x[k] = live ? __ldg(src + half * (D / 16) + k) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < D / 16; ++k) x[k] = live ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        for (int k = 0; k < D / 16; ++k) {
+          // the largest of both halves of a word: as unsigned pairs, signs away
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu), __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
+        }
+        mx = max(mx & 0xffffu, mx >> 16);
+        s_mx[wg][r] = mx;
+        mbar_arrive(&joined);
+        ok = wait_warp(&joined, joins++ & 1);
+        if (!ok) break;
+        mx = max(mx, s_mx[wg ^ 1][r]);
+        const int e = int(mx >> 7);
+        float up = sign;
+        if (mx != 0 && (e < 127 - 6 || e > 127 + 13)) {
+          const int k = min(max(e, 20), 240);
+          const float s2 = __uint_as_float(uint32_t(264 - k) << 23);
+          up *= s2;
+          f *= 1.f / s2;
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = max(mx, max(a[e] & 0x7fffu, (a[e] >> 16) & 0x7fffu));
-          }
-          if (h == 0) continue;
-          const int e = int(mx >> 7);
-          float up = sign;
-          if (mx != 0 && (e < 127 - 6 || e > 127 + 13)) {
-            const int k = min(max(e, 20), 240);
-            const float s2 = __uint_as_float(uint32_t(264 - k) << 23);
-            up *= s2;
-            f *= 1.f / s2;
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          float y[8];
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            float y[8];
-#pragma unroll
-            for (int h2 = 0; h2 < 4; ++h2)
-              y[2 * h2] = __uint_as_float(a[h2] << 16) * up, y[2 * h2 + 1] = __uint_as_float(a[h2] & 0xffff0000u) * up;
-            const int word = half * (D / 16) + k;
-            tmem_st4_async(lane_base + S::kColQ + 4 * tc_unit<D>(word >> 2, word & 3), pack_h2(y[0], y[4]), pack_h2(y[1], y[5]),
-                           pack_h2(y[2], y[6]), pack_h2(y[3], y[7]));
-          }
+          for (int h = 0; h < 4; ++h)
+            y[2 * h] = __uint_as_float(a[h] << 16) * up, y[2 * h + 1] = __uint_as_float(a[h] & 0xffff0000u) * up;
+          const int w = wg * (D / 16) + k;
+          tmem_st4_async(lane_base + S::kColQ + 4 * tc_unit<D>(w >> 2, w & 3), pack_h2(y[0], y[4]), pack_h2(y[1], y[5]),
+                         pack_h2(y[2], y[6]), pack_h2(y[3], y[7]));
         }
         tmem_wait_st();
         tc_fence_before();
