@@ -38,7 +38,11 @@
 namespace gdn {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 608;  // warps 0-7 softmax, 8-11 K, 12-15 V, 16 products, 17 copies, 18 units
+// Roles by `role` = (warp + 16) mod 20: 0-7 softmax, 8-11 K, 12-15 V, 16 products,
+// 17 copies, 18 units, 19 none.  The products' warp is the oldest of its
+// scheduler, which seems to favour the oldest ready one (a prompt of 4096 at
+// D = 256: 242 us with it as the youngest, 227 so).
+constexpr int kTcThreads = 640;
 constexpr int kTcRing = 4;       // tiles of codes in flight
 constexpr int kTcUnits = 4;      // units handed out ahead
 // What a unit costs besides its tiles of keys (queries in, outputs out), in
@@ -270,7 +274,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   // keys of a V tile with a value that is not finite, per group; of four tiles,
   // since the rows look two tiles later
   __shared__ __align__(16) uint32_t s_bad[4][NK / 32 * W];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int role = ((tid >> 5) + 16) % 20, rtid = role * 32 + lane;  // and the thread's place among the roles'
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *ring = smem + 4 * S::kKBytes;
   const int G = p.g.H_q / p.g.H_kv, Hkv = p.g.H_kv, TT = kTcRows / G;
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     if (at0 >= before && at0 < before + len) s_at.b = b0 + tid, s_at.row = own, s_at.in_row = at0 - before, s_at.len = len;
   }
 
-  if (warp == 16) tmem_alloc(&s_tmem, S::kCols);
+  if (role == 16) tmem_alloc(&s_tmem, S::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   };
   auto unit = [&]() -> const TcUnit & { return s_unit[(un - 1) % kTcUnits]; };
 
-  if (warp == 18) {
+  if (role == 18) {
     // ---- units ------------------------------------------------------------------------------
     long long at = at0;
     int b = s_at.b, hk = 0, t = 0, place;  // place in the unit, of stages + kTcUnitCost
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         }
       }
     }
-  } else if (warp == 17) {
+  } else if (role == 17) {
     // ---- copies -------------------------------------------------------------------------
     // A page is one copy, as it lies in memory: copies are taken one in about 70
     // cycles whatever their size, so 32 pieces of eight small pages took 2250
@@ -463,7 +468,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     if (!ok)
       for (uint32_t k = it < kTcRing ? 0 : it - kTcRing; k < it; ++k)
         att_wait(&raw_full[k % kTcRing], k / kTcRing & 1);
-  } else if (warp == 16) {
+  } else if (role == 16) {
     // ---- products -----------------------------------------------------------------------
     // The whole warp waits, one elected thread issues; the operands'
     // addresses are constants of each buffer's own code, so that they stand in
@@ -514,9 +519,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       __syncwarp();
       att_wait(&drained, 0);
     }
-  } else if (warp >= 12) {
+  } else if (role >= 12 && role < 16) {
     // ---- V^T: 8 keys of one word (8 channels) at a time, 16 bytes of 8 rows ------------------
-    const int vt = tid - 384;
+    const int vt = rtid - 384;
     constexpr int kWords = D / 8, kTasks = NK / 8 * kWords / 128, kChunkStep = 128 / kWords;
     uint32_t had = 0;  // bit kTasks * (tile % 4) + i: the thread noted keys of task i
     // what a thread's tasks read and write, the same in every tile
@@ -611,9 +616,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (lane == 0) mbar_arrive(&raw_empty[slot]);
       }
     }
-  } else if (warp >= 8) {
+  } else if (role >= 8 && role < 12) {
     // ---- K: 4 words (32 channels) of a key at a time ----------------------------------------
-    const int kt = tid - 256;
+    const int kt = rtid - 256;
     constexpr int kChunks = D / 32, kTasks = NK * kChunks / 128, kRowStep = 128 / kChunks;
     // what a thread's tasks read and write, the same in every tile
     const int c = kt % kChunks, r0 = kt / kChunks;  // chunk, first row; task i has row r0 + i kRowStep
@@ -663,11 +668,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (lane == 0) mbar_arrive(&raw_empty[slot]);
       }
     }
-  } else {
+  } else if (role < 8) {
     // ---- softmax: thread = query row, groups of 4 warps by the tile's parity -------------------
-    const uint32_t wg = warp >> 2;
-    const int r = tid & 127;
-    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t wg = role >> 2;
+    const int r = rtid & 127;
+    const uint32_t lane_base = uint32_t((role & 3) * 32) << 16;
     constexpr int kWords = D / 8;  // column e kWords + w of O is channel 8 w + e
     float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
     uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
@@ -891,7 +896,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         mbar_arrive(&joined);
         ok = wait_warp(&joined, joins++ & 1);
         if (!ok) break;
-        if (tid == 0) {
+        if (rtid == 0) {
           const uint32_t need = uint32_t(c_last - c_first + 1);
           const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
           s_flag = done == need;
@@ -966,7 +971,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(s_tmem, S::kCols);
+  if (role == 16) tmem_dealloc(s_tmem, S::kCols);
 }
 
 template <int D>
