@@ -531,15 +531,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     static_assert(kTasks == 1 || kChunkStep % 2 == 0, "chunks of a thread share their order");
     const int swap = D == 256 ? 0 : chunk0 & 1;
     const uint32_t sel0 = swap ? 0x1054u : 0x5410u, sel1 = swap ? 0x3276u : 0x7632u;
-    int code_at[kTasks], entry_at[kTasks], to[kTasks];
+    // (the second task's a fixed step behind the first's)
+    int code_at = 0, entry_at = 0, to = 0, code_step = 0, entry_step = 0, to_step = 0;
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
       const int chunk = chunk0 + i * kChunkStep, off = (chunk * 8) & (P - 1);
       const int rec = (chunk >> (p.g.log2P - 3)) * kv4_record_bytes(D, P);
-      code_at[i] = rec + kv4_code_bytes(D, P) + off * (D / 2) + word * 4;
-      entry_at[i] = rec + 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P) + (off * W + word % W) * 4;
-      to[i] = (chunk >> 3) * (D * 128) + word * 128 + (((chunk ^ word) & 7) << 4);
+      const int code = rec + kv4_code_bytes(D, P) + off * (D / 2) + word * 4;
+      const int entry = rec + 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P) + (off * W + word % W) * 4;
+      const int at = (chunk >> 3) * (D * 128) + word * 128 + (((chunk ^ word) & 7) << 4);
+      if (i == 0) code_at = code, entry_at = entry, to = at;
+      else code_step = code - code_at, entry_step = entry - entry_at, to_step = at - to;
     }
+    static_assert(kTasks <= 2, "two tasks at most");
     uint32_t it = 0;
     bool ok = true;
     while (next_unit(ok)) {
@@ -553,11 +557,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         uint8_t *vb = smem + (2 + buf) * S::kKBytes;
         uint32_t noted = 0;
         const bool tail = st * NK + NK > lim;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kTasks; ++i) {
           const int chunk = chunk0 + i * kChunkStep;  // keys [8 chunk, 8 chunk + 8)
-          const uint8_t *ce = raw + code_at[i] + swap * (D / 2), *co = raw + code_at[i] - swap * (D / 2);
-          const uint8_t *ee = raw + entry_at[i] + swap * (W * 4), *eo = raw + entry_at[i] - swap * (W * 4);
+          const uint8_t *codes = raw + code_at + i * code_step, *entries = raw + entry_at + i * entry_step;
+          const uint8_t *ce = codes + swap * (D / 2), *co = codes - swap * (D / 2);
+          const uint8_t *ee = entries + swap * (W * 4), *eo = entries - swap * (W * 4);
           uint32_t c[8], e[8];  // of key k ^ swap
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
             es[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel0);
             eb[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel1);
           }
-          uint8_t *dst = vb + to[i];
+          uint8_t *dst = vb + to + i * to_step;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t x[4], y[4];
@@ -622,14 +627,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     constexpr int kChunks = D / 32, kTasks = NK * kChunks / 128, kRowStep = 128 / kChunks;
     // what a thread's tasks read and write, the same in every tile
     const int c = kt % kChunks, r0 = kt / kChunks;  // chunk, first row; task i has row r0 + i kRowStep
-    int code_at[kTasks], entry_at[kTasks], to[4];
+    // (two at a time, the next two a fixed step behind: short code, above)
+    int code_at[2], entry_at[2], code_step = 0, entry_step = 0, to[4];
 #pragma unroll
-    for (int i = 0; i < kTasks; ++i) {
+    for (int i = 0; i < (kTasks > 2 ? 3 : 2); ++i) {
       const int r = r0 + i * kRowStep, off = r & (P - 1);
       const int rec = (r >> p.g.log2P) * kv4_record_bytes(D, P);
-      code_at[i] = rec + off * (D / 2) + c * 16;
-      entry_at[i] = rec + 2 * kv4_code_bytes(D, P) + off * (W * 4);
+      const int code = rec + off * (D / 2) + c * 16, entry = rec + 2 * kv4_code_bytes(D, P) + off * (W * 4);
+      if (i < 2) code_at[i % 2] = code, entry_at[i % 2] = entry;
+      else code_step = code - code_at[0], entry_step = entry - entry_at[0];
     }
+    static_assert(kTasks == 2 || kTasks == 4, "two pairs at most");
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int u = tc_unit<D>(c, q);
@@ -647,11 +655,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (!ok) break;
         const uint8_t *raw = ring + slot * S::kRaw;
         uint8_t *kb = smem + buf * S::kKBytes;
+#pragma unroll 1
+        for (int h = 0; h < kTasks / 2; ++h, kb += 2 * kRowStep * 128) {
+         const uint8_t *codes = raw + h * code_step, *entries = raw + h * entry_step;
 #pragma unroll
-        for (int i = 0; i < kTasks; ++i) {
-          const uint4 x4 = *reinterpret_cast<const uint4 *>(raw + code_at[i]);
+         for (int i = 0; i < 2; ++i) {
+          const uint4 x4 = *reinterpret_cast<const uint4 *>(codes + code_at[i]);
           uint32_t e[W], step[W], base[W];
-          att_words<W>(e, raw + entry_at[i]);
+          att_words<W>(e, entries + entry_at[i]);
 #pragma unroll
           for (int g = 0; g < W; ++g) step[g] = __byte_perm(e[g], e[g], 0x1010), base[g] = __byte_perm(e[g], e[g], 0x3232);
           const uint32_t wd[4] = {x4.x, x4.y, x4.z, x4.w};
@@ -661,6 +672,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
             *reinterpret_cast<uint4 *>(kb + to[q] + i * (kRowStep * 128)) =
                 make_uint4(att_even(x, sw, bw), att_odd(x, sw, bw), att_even(y, sw, bw), att_odd(y, sw, bw));
           }
+         }
         }
         fence_proxy_async_shared();
         mbar_arrive(&k_full[buf]);
