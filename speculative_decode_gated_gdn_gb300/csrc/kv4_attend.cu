@@ -7,10 +7,6 @@ namespace gdn {
 
 namespace {
 
-// CTAs of the persistent grids at most: the workspace has room for the parts of
-// so many, on whichever device it is used.
-constexpr int kMaxSms = 160;
-
 int att_sms() {
   static std::atomic<int> cached[64];  // per device, 0 until looked up
   int dev = 0, n = 0;
@@ -18,7 +14,7 @@ int att_sms() {
   n = cached[dev].load(std::memory_order_relaxed);
   if (!n) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    n = n < kMaxSms ? n : kMaxSms;
+    n = n < kAttMaxCtas ? n : kAttMaxCtas;
     cached[dev].store(n, std::memory_order_relaxed);
   }
   return n;
@@ -33,15 +29,15 @@ bool att_many_rows(const Kv4Geom &g, int max_q) { return (long long)max_q * (g.H
 size_t kv4_attend_workspace_bytes(const Kv4Geom &g, int, int max_q) {
   if (att_many_rows(g, max_q)) {
     switch (g.D) {
-      case 64: return att_tc_ws<64>(kMaxSms);
-      case 128: return att_tc_ws<128>(kMaxSms);
-      default: return att_tc_ws<256>(kMaxSms);
+      case 64: return att_tc_ws<64>(kAttMaxCtas);
+      case 128: return att_tc_ws<128>(kAttMaxCtas);
+      default: return att_tc_ws<256>(kAttMaxCtas);
     }
   }
   switch (g.D) {
-    case 64: return att_mma_ws<64, 16>(kMaxSms);
-    case 128: return att_mma_ws<128, 16>(kMaxSms);
-    default: return att_mma_ws<256, 16>(kMaxSms);
+    case 64: return att_mma_ws<64, 16>(kAttMaxCtas);
+    case 128: return att_mma_ws<128, 16>(kAttMaxCtas);
+    default: return att_mma_ws<256, 16>(kAttMaxCtas);
   }
 }
 

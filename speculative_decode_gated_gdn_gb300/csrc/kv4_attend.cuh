@@ -66,6 +66,9 @@ struct AttShape {
 };
 
 constexpr int kAttMaxRows = 16;
+// CTAs of the persistent grids at most: the workspace has room for the parts of
+// so many, on whichever device it is used.
+constexpr int kAttMaxCtas = 160;
 
 // Floats of a CTA's part of a cut unit in the workspace: outputs, then maximum
 // and sum of 16 rows.

@@ -49,6 +49,7 @@ constexpr int kTcUnits = 4;      // units handed out ahead
 // tiles: its place on the line is that much longer, so that the pieces of the
 // CTAs that have many short units are not the last to end.
 constexpr int kTcUnitCost = 6;
+constexpr int kTcJoin = 8;       // parts of a cut unit that are joined at a time
 
 template <int D>
 struct TcShape {
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     long long in_row, len;
   } s_at;  // the row that holds the CTA's first place
   __shared__ float s_ref[kTcRows], s_sum[2][kTcRows], s_own[2][kTcRows];
+  __shared__ float s_w[(kAttMaxCtas + kTcJoin - 1) / kTcJoin][kTcRows];  // weights of the parts of a join
   __shared__ uint32_t s_nan[2 * kTcRows], s_mx[2][kTcRows];
   __shared__ int s_flag, s_dead;
   // keys of a V tile with a value that is not finite, per group; of four tiles,
@@ -887,81 +889,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         m = M;
       }
       const bool whole = st0 == 0 && n == unit().stages;
-      bool last = whole;
-      int c_first = 0, c_last = 0;
-      auto part_of = [&](int k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>() + r; };
-      if (!whole) {
-        c_first = cta_of(unit().first + kTcUnitCost);
-        c_last = cta_of(unit().first + unit().stages + kTcUnitCost - 1);
-        float *part = part_of(c);
-#pragma unroll 1
-        for (int q = wg * (D / 64); q < (wg + 1) * (D / 64); ++q) {
-          uint32_t o[32];
-          tmem_ld32_async(lane_base + 32 * q, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            part[size_t(32 * q + e) * kTcRows] = nan >> ((32 * q + e) % kWords % W) & 1 ? __uint_as_float(0x7fc00000u) : __uint_as_float(o[e]);
-        }
-        if (wg == 0) part[size_t(D) * kTcRows] = m, part[size_t(D + 1) * kTcRows] = l;
-        __threadfence();
-        mbar_arrive(&joined);
-        ok = wait_warp(&joined, joins++ & 1);
-        if (!ok) break;
-        if (rtid == 0) {
-          const uint32_t need = uint32_t(c_last - c_first + 1);
-          const uint32_t done = atomicAdd(&counters[c_first], 1u) + 1u;
-          s_flag = done == need;
-          if (done == need) counters[c_first] = 0;  // ready for the next call
-          __threadfence();
-        }
-        __syncwarp();
-        mbar_arrive(&joined);
-        ok = wait_warp(&joined, joins++ & 1);
-        if (!ok) break;
-        last = *reinterpret_cast<volatile int *>(&s_flag) != 0;
-      }
-      if (last) {
-        float M = m, Ls = l;
-        if (!whole) {
-          M = -INFINITY, Ls = 0.f;
-#pragma unroll 1
-          for (int k = c_first; k <= c_last; ++k) M = fmaxf(M, __ldcg(part_of(k) + size_t(D) * kTcRows));
-#pragma unroll 1
-          for (int k = c_first; k <= c_last; ++k) {
-            const float mk = __ldcg(part_of(k) + size_t(D) * kTcRows), lk = __ldcg(part_of(k) + size_t(D + 1) * kTcRows);
-            Ls = fmaf(lk, lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M), Ls);
-          }
-        }
-        const float v = Ls > 0.f ? 1.f / Ls : Ls;  // no key: 0; NaN stays
+      if (whole) {
+        const float v = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
         uint16_t *dst = p.out + (size_t(tok) * p.g.H_q + head) * D;
 #pragma unroll 1
         for (int w = wg * (kWords / 2); w < (wg + 1) * (kWords / 2); w += 4) {  // 4 words of 8 channels
           float y[8][4];
-          if (whole) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) tmem_ld4_async(lane_base + e * kWords + w, y[e]);
-            tmem_wait_ld();
-            if (nan)
+          for (int e = 0; e < 8; ++e) tmem_ld4_async(lane_base + e * kWords + w, y[e]);
+          tmem_wait_ld();
+          if (nan)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (nan >> (k % W) & 1)
+            for (int k = 0; k < 4; ++k)
+              if (nan >> (k % W) & 1)
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e][k] = __uint_as_float(0x7fc00000u);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e][0] = y[e][1] = y[e][2] = y[e][3] = 0.f;
-#pragma unroll 1
-            for (int kc = c_first; kc <= c_last; ++kc) {
-              const float *src = part_of(kc);
-              const float mk = __ldcg(src + size_t(D) * kTcRows), lk = __ldcg(src + size_t(D + 1) * kTcRows);
-              const float ck = lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[e][k] = fmaf(__ldcg(src + size_t(e * kWords + w + k) * kTcRows), ck, y[e][k]);
-            }
-          }
+                for (int e = 0; e < 8; ++e) y[e][k] = __uint_as_float(0x7fc00000u);
           if (in) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -975,6 +917,122 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
             }
           }
         }
+      } else {
+        // A part of 32-row blocks that hold rows; then the parts are joined kTcJoin
+        // at a time by the CTA that brings the last of them, and what comes of that,
+        // in the place of the first, once more.  The order of a sum does not depend
+        // on who joins.
+        const int c_first = cta_of(unit().first + kTcUnitCost);
+        const int c_last = cta_of(unit().first + unit().stages + kTcUnitCost - 1);
+        const int rows = min(TT, unit().span - unit().tile * TT) * G, blocks = (rows + 31) >> 5;
+        auto part_of = [&](int k) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * tc_part_floats<D>(); };
+        if (r < blocks * 32) {
+          float *part = part_of(c) + r;
+#pragma unroll 1
+          for (int q = wg * (D / 64); q < (wg + 1) * (D / 64); ++q) {
+            uint32_t o[32];
+            tmem_ld32_async(lane_base + 32 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              part[size_t(32 * q + e) * kTcRows] = nan >> ((32 * q + e) % kWords % W) & 1 ? __uint_as_float(0x7fc00000u) : __uint_as_float(o[e]);
+          }
+          if (wg == 0) part[size_t(D) * kTcRows] = m, part[size_t(D + 1) * kTcRows] = l;
+        }
+        // a warp: one block of rows, the words from w0
+        const int splits = blocks == 1 ? 8 : blocks == 2 ? 4 : 2, words = kWords / splits;
+        const int jr = role / splits * 32 + lane, w0 = role % splits * words;
+        const int ji = unit().tile * TT + jr / G;
+        const bool there = jr < blocks * 32;
+        uint16_t *dst = p.out + (size_t(unit().start + ji) * p.g.H_q + unit().hk * G + jr % G) * D;
+        int from = c - (c - c_first) % kTcJoin, step = 1, some = min(kTcJoin, c_last + 1 - from);
+        uint32_t *count = counters + 256 + 2 * from + (from == c_first);
+        if (c_last - c_first < kTcJoin) count = counters + c_first;
+#pragma unroll 1
+        for (;;) {
+          __threadfence();
+          mbar_arrive(&joined);
+          ok = wait_warp(&joined, joins++ & 1);
+          if (!ok) break;
+          if (rtid == 0) {
+            const uint32_t done = atomicAdd(count, 1u) + 1u;
+            s_flag = done == uint32_t(some);
+            if (done == uint32_t(some)) *count = 0;  // ready for the next call
+            __threadfence();
+          }
+          __syncwarp();
+          mbar_arrive(&joined);
+          ok = wait_warp(&joined, joins++ & 1);
+          if (!ok || *reinterpret_cast<volatile int *>(&s_flag) == 0) break;
+          const bool final = count == counters + c_first;
+          // weights of the parts against the common maximum, by the block's first warp
+          float M = -INFINITY, L = 0.f;
+          if (there && w0 == 0) {
+#pragma unroll 4
+            for (int k = 0; k < some; ++k) M = fmaxf(M, __ldcg(part_of(from + k * step) + size_t(D) * kTcRows + jr));
+#pragma unroll 4
+            for (int k = 0; k < some; ++k) {
+              const float *src = part_of(from + k * step) + size_t(D) * kTcRows + jr;
+              const float mk = __ldcg(src), lk = __ldcg(src + kTcRows);
+              const float ck = lk != lk ? 1.f : mk == -INFINITY ? 0.f : ex2(mk - M);
+              s_w[k][jr] = ck;
+              L = fmaf(lk, ck, L);
+            }
+            s_sum[0][jr] = L;
+          }
+          mbar_arrive(&joined);
+          ok = wait_warp(&joined, joins++ & 1);
+          if (!ok) break;
+          if (there) {
+            const float Ls = s_sum[0][jr], v = Ls > 0.f ? 1.f / Ls : Ls;  // no key: 0; NaN stays
+#pragma unroll 1
+            for (int w = w0; w < w0 + words; ++w) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = 0.f;
+#pragma unroll 1
+              for (int k = 0; k < some; k += 4) {  // 4 parts' loads on their way
+                float x[4][8];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                  const float *src = part_of(from + (k + f) * step) + jr;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) x[f][e] = k + f < some ? __ldcg(src + size_t(e * kWords + w) * kTcRows) : 0.f;
+                }
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                  const float ck = k + f < some ? s_w[k + f][jr] : 0.f;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) y[e] = fmaf(x[f][e], ck, y[e]);
+                }
+              }
+              if (!final) {
+                float *part = part_of(from) + jr;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) part[size_t(e * kWords + w) * kTcRows] = y[e];
+              } else if (jr < rows) {
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * e] * v, y[2 * e + 1] * v);
+                  h[e] = *reinterpret_cast<const uint32_t *>(&b2);
+                }
+                *reinterpret_cast<uint4 *>(dst + 8 * w) = make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+          }
+          if (final) break;
+          mbar_arrive(&joined);  // every warp has read the parts' maxima and sums
+          ok = wait_warp(&joined, joins++ & 1);
+          if (!ok) break;
+          if (there && w0 == 0) {
+            float *part = part_of(from) + jr;
+            part[size_t(D) * kTcRows] = M, part[size_t(D + 1) * kTcRows] = L;
+          }
+          from = c_first, step = kTcJoin, some = (c_last - c_first) / kTcJoin + 1;
+          count = counters + c_first;
+        }
+        if (!ok) break;
       }
       base += n;
       tc_fence_before();
