@@ -1,7 +1,7 @@
 // kv4_attend.cuh -- causal attention of a few query rows over the paged 4-bit
 // cache: one pass over the keys, the codes as matrix operands.
 //
-// A unit is (row b, kv head, tile of R = 8 or 16 query rows); a query row is one
+// A unit is (row b, kv head, tile of 8 query rows); a query row is one
 // (token, head of the group), so the group's heads and a row's draft positions
 // share every byte that is read.  A warp takes stages of ST keys:
 //   scores   mma m16n8k16 (fp16, fp32 accumulators) of Q with the keys' codes.
@@ -16,8 +16,8 @@
 //            out exactly (1024 + code, less 1024, or 1024 + 16 code, / 16 - 64),
 //            then base + step * code in one fused multiply-add; P is rounded
 //            once to fp16, at most 2^14 and exact to 2^-11 down to 2^-20 of
-//            the largest.  With R = 8 the values are the first operand and P the
-//            second, which takes half the products and accumulators.
+//            the largest.  The values are the first operand and P the second, so that
+//            the eight rows fill a product.
 // q is scaled per row by a power of two before fp16, exactly.
 //
 // What bounds it: HBM for single tokens and drafts (144 bytes a token and
@@ -42,38 +42,32 @@
 
 namespace gdn {
 
-template <int D, int R>
+constexpr int kAttRows = 8;  // query rows of a unit
+
+template <int D>
 struct AttShape {
   static constexpr int W = D / 64;               // groups of a head
   static constexpr int ST = D == 256 ? 32 : 64;  // keys of a stage: what a copy brings
   static constexpr int CK = 32, NT = CK / 8;     // keys, and key tiles, taken at a time
-  // warps of a CTA, as the registers of a thread allow
-  static constexpr int NW = D == 256 ? (R == 8 ? 12 : 8) : D == 128 ? 12 : 16;
+  static constexpr int NW = D == 64 ? 16 : 12;   // warps of a CTA, as the registers of a thread allow
   static constexpr int kThreads = 32 * NW;
   static constexpr int kCodes = ST * D / 2, kEntries = ST * W * 4;
   static constexpr int kStage = 2 * (kCodes + kEntries);
   static constexpr int kSlots = (224 * 1024 / kStage) / NW;  // stages of a warp's ring
-  static constexpr int X = R / 4;                // accumulators of a lane and channel tile
-  static constexpr int kRegs = D / 8 * X;        // accumulators of a lane
-  static constexpr int kPairs = kRegs / 2 * 32;  // items of the join: 2 channels of a query row
-  static constexpr int kPart = kRegs * 32;       // floats of a part
+  static constexpr int kRegs = D / 4;            // accumulators of a lane: channel tiles x 2 rows
+  static constexpr int kPart = kRegs * 32;       // floats of a part: outputs [accumulator][lane]
+  static constexpr int kPartAll = kPart + 2 * kAttRows;  // a CTA's part in the workspace: with the rows' maxima and sums
   static constexpr int kRing = kSlots * kStage;
   static constexpr int kSmem = NW * kRing + 128;
-  static_assert(kSlots >= 2 && kPart * 4 <= kRing, "ring");
-  // accumulator of channel tile 8 g + e: R = 16: one tile of 8 channels a product,
-  // x the four values; R = 8: two tiles a product, x the two rows
-  static __host__ __device__ constexpr int reg(int t, int x) { return R == 16 ? 4 * t + x : (t >> 1) * 4 + 2 * (t & 1) + x; }
+  static_assert(kSlots >= 2, "ring");
+  // accumulator of channel tile t (channels 8 g + e: t = 8 g + e), row 2 j + x:
+  // two tiles a product
+  static __host__ __device__ constexpr int reg(int t, int x) { return (t >> 1) * 4 + 2 * (t & 1) + x; }
 };
 
-constexpr int kAttMaxRows = 16;
 // CTAs of the persistent grids at most: the workspace has room for the parts of
 // so many, on whichever device it is used.
 constexpr int kAttMaxCtas = 160;
-
-// Floats of a CTA's part of a cut unit in the workspace: outputs, then maximum
-// and sum of 16 rows.
-template <int D, int R>
-__host__ __device__ constexpr size_t att_part_floats() { return AttShape<D, R>::kPart + 32; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -191,7 +185,7 @@ struct AttRow {
   int tiles, stages;            // query tiles; stages of each
 };
 
-template <int D, int R>
+template <int D>
 __device__ __forceinline__ AttRow att_row(const Kv4AttendParams &p, int b, bool report) {
   AttRow r;
   r.start = p.q_start[b];
@@ -208,8 +202,8 @@ __device__ __forceinline__ AttRow att_row(const Kv4AttendParams &p, int b, bool 
   }
   r.span = span, r.count = count, r.len = min(max(len, 0), cap);
   const int G = p.g.H_q / p.g.H_kv;
-  r.tiles = int(((long long)span * G + R - 1) / R);
-  r.stages = count > 0 ? max(1, (r.len + AttShape<D, R>::ST - 1) / AttShape<D, R>::ST) : 1;
+  r.tiles = int(((long long)span * G + kAttRows - 1) / kAttRows);
+  r.stages = count > 0 ? max(1, (r.len + AttShape<D>::ST - 1) / AttShape<D>::ST) : 1;
   return r;
 }
 
@@ -253,25 +247,25 @@ struct AttPiece {
 
 // What the join needs in shared memory; it lies in the first warp's ring, behind
 // that warp's part.
-template <int D, int R>
+template <int D>
 struct AttJoin {
-  static constexpr int NW = AttShape<D, R>::NW;
-  float c[2][NW][R];                   // weights of the warps' parts
-  float max[NW + 1][R], sum[NW + 1][R];
-  float w[16][R], lw[16][R];           // weights, and weighted sums, of 16 CTAs' parts
+  static constexpr int NW = AttShape<D>::NW;
+  float c[2][NW][kAttRows];                   // weights of the warps' parts
+  float max[NW + 1][kAttRows], sum[NW + 1][kAttRows];
+  float w[16][kAttRows], lw[16][kAttRows];           // weights, and weighted sums, of 16 CTAs' parts
   int from[NW + 1], to[NW + 1];        // warps of a cut unit; from > to: none
 };
 
-template <int D, int R>
-__global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(const __grid_constant__ Kv4AttendParams p) {
-  using S = AttShape<D, R>;
-  constexpr int W = S::W, ST = S::ST, NT = S::NT, NW = S::NW, X = S::X;
+template <int D>
+__global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const __grid_constant__ Kv4AttendParams p) {
+  using S = AttShape<D>;
+  constexpr int W = S::W, ST = S::ST, NT = S::NT, NW = S::NW;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_full[NW][S::kSlots];
   __shared__ AttPiece s_piece[NW][2], s_cut[2][NW];  // current and next pieces; cut pieces (0: begun before the warp's)
   __shared__ int s_has[2][NW];                       // 1: a cut piece's part is in the ring, 2: in the workspace
   __shared__ int s_none[NW];                         // the warp has no stage at all
-  __shared__ float s_m[2][NW][R], s_l[2][NW][R];
+  __shared__ float s_m[2][NW][kAttRows], s_l[2][NW][kAttRows];
   __shared__ long long s_warp[NW];
   __shared__ int s_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -292,7 +286,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   long long mine = 0, total, before = 0;
   AttRow own{};
   for (int b = tid; b < p.g.B; b += S::kThreads) {
-    const AttRow r = att_row<D, R>(p, b, blockIdx.x == 0);
+    const AttRow r = att_row<D>(p, b, blockIdx.x == 0);
     if (b == tid) own = r;
     mine += places(r);
   }
@@ -318,8 +312,8 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     u.st0 = int(min((long long)u.stages, (x - u.first) >> 1));
     u.st1 = int(min((long long)u.stages, (to - u.first) >> 1));
     if (u.stages <= kAttUncut) u.st0 = x > u.first ? u.stages : 0, u.st1 = u.stages;
-    const int first = u.tile * R / G;
-    const int last = min(((u.tile + 1) * R - 1) / G, u.row.count - 1);
+    const int first = u.tile * kAttRows / G;
+    const int last = min(((u.tile + 1) * kAttRows - 1) / G, u.row.count - 1);
     u.lim_max = last >= first ? max(0, u.row.len - u.row.count + last + 1) : 0;
     u.st_hi = min(u.st1, (u.lim_max + ST - 1) / ST);
   };
@@ -328,7 +322,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll 1
   for (int b0 = 0; b0 < p.g.B; b0 += S::kThreads) {
     if (p.g.B > S::kThreads) {
-      if (b0 + tid < p.g.B) own = att_row<D, R>(p, b0 + tid, false);
+      if (b0 + tid < p.g.B) own = att_row<D>(p, b0 + tid, false);
       else own.tiles = 0;
       long long sum;
       before = before0 + att_scan<NW>(places(own), s_warp, &sum);
@@ -345,7 +339,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 
   uint8_t *ring = smem + warp * S::kRing;
   float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
-  float *stash = parts + 2 * size_t(gridDim.x) * att_part_floats<D, R>() + (size_t(c) * NW) * S::kPart;
+  float *stash = parts + 2 * size_t(gridDim.x) * S::kPartAll + (size_t(c) * NW) * S::kPart;
   uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
   uint32_t phases = 0;      // parity of each ring slot
   int slot = 0, in = 0;     // next slot to read and to fill
@@ -361,7 +355,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
         u.tile = 0;
         if (++u.hk == Hkv) {
           u.hk = 0;
-          do u.row = att_row<D, R>(p, ++u.b, false);
+          do u.row = att_row<D>(p, ++u.b, false);
           while (u.row.tiles == 0);
         }
       }
@@ -475,29 +469,23 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     const AttPiece &cur = pieces[turn & 1];
     const int lim_max = cur.lim_max, st_hi = cur.st_hi, st_first = cur.st0;
     refill(false);
-    // ---- the tile's queries: rows n and (R = 16) n + 8 ---------------------------------
+    // ---- the tile's queries: row n of a lane -------------------------------------------
     const AttRow row = cur.row;
-    const int R0 = cur.tile * R + n, R1 = R0 + 8;
-    const int i0 = R0 / G, i1 = R1 / G;
-    const bool in0 = i0 < row.span, in1 = R == 16 && i1 < row.span;
-    const bool live0 = in0 && i0 < row.count, live1 = in1 && i1 < row.count;
+    const int rn = cur.tile * kAttRows + n, at = rn / G;
+    const bool inside = at < row.span, live = inside && at < row.count;
     // keys that the row's query sees; rows past the span follow the others
-    const int lim0 = live0 ? max(0, row.len - row.count + i0 + 1) : in0 ? 0 : lim_max;
-    const int lim1 = live1 ? max(0, row.len - row.count + i1 + 1) : in1 ? 0 : lim_max;
-    const int lim_min = __reduce_min_sync(0xffffffffu, min(lim0, lim1));
+    const int lim = live ? max(0, row.len - row.count + at + 1) : inside ? 0 : lim_max;
+    const int lim_min = __reduce_min_sync(0xffffffffu, lim);
 
     // ---- Q as fp16 fragments, scaled by a power of two per row -------------------------
-    uint32_t qa[D / 16][R / 4];  // rows n (, n + 8) of columns 0-7, then of columns 8-15
-    float qs0[W], qs1[W];
-    float f0 = fabsf(p.scale) * 1.4426950408889634f * 16777216.f, f1 = f0;  // 2^24 of the subnormal codes
+    uint32_t qa[D / 16][2];  // columns 0-7, then 8-15
+    float qs[W];
+    float f = fabsf(p.scale) * 1.4426950408889634f * 16777216.f;  // 2^24 of the subnormal codes
     // the factor of a score is kept positive: the maximum is taken before it
     const float sign = p.scale > 0.f ? 1.f : p.scale < 0.f ? -1.f : 0.f;
-    if (p.scale == 0.f) f0 = f1 = 1.f;
-#pragma unroll
-    for (int h = 0; h < R / 8; ++h) {
-      const bool live = h ? live1 : live0;
-      const int tok = row.start + (h ? i1 : i0), head = cur.hk * G + (h ? R1 - i1 * G : R0 - i0 * G);
-      const uint16_t *src = p.q + (size_t(live ? tok : 0) * p.g.H_q + (live ? head : 0)) * D;
+    if (p.scale == 0.f) f = 1.f;
+    {
+      const uint16_t *src = p.q + (size_t(live ? row.start + at : 0) * p.g.H_q + (live ? cur.hk * G + rn - at * G : 0)) * D;
       uint4 raw[D / 32];
       uint32_t mx = 0;
 #pragma unroll
@@ -507,18 +495,16 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
         raw[w] = live ? *reinterpret_cast<const uint4 *>(src + ch) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const uint32_t a[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = max(mx, max(a[e] & 0x7fffu, (a[e] >> 16) & 0x7fffu));
-      }
+      for (int w = 0; w < D / 32; ++w)  // the largest of both halves of a word: as unsigned pairs, signs away
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(raw[w].x & 0x7fff7fffu, raw[w].y & 0x7fff7fffu),
+                                   __vmaxu2(raw[w].z & 0x7fff7fffu, raw[w].w & 0x7fff7fffu)));
+      mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       // the largest magnitude goes to [2^10, 2^11)
       const int e = min(max(int(mx >> 7), 20), 240);
       const float s2 = __uint_as_float(uint32_t(264 - e) << 23), up = s2 * sign;
-      (h ? f1 : f0) *= 1.f / s2;
-      float qs[W];
+      f *= 1.f / s2;
 #pragma unroll
       for (int g = 0; g < W; ++g) qs[g] = 0.f;
 #pragma unroll
@@ -531,14 +517,14 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll
         for (int k = 0; k < 8; ++k) qs[w % W] += x[k];
         // step 2w: columns (0, 4) and (1, 5) / 16; step 2w + 1: (2, 6) and (3, 7) / 16
-        qa[2 * w][h] = pack_h2(x[0], x[4]), qa[2 * w][R / 8 + h] = pack_h2(x[1] * 0.0625f, x[5] * 0.0625f);
-        qa[2 * w + 1][h] = pack_h2(x[2], x[6]), qa[2 * w + 1][R / 8 + h] = pack_h2(x[3] * 0.0625f, x[7] * 0.0625f);
+        qa[2 * w][0] = pack_h2(x[0], x[4]), qa[2 * w][1] = pack_h2(x[1] * 0.0625f, x[5] * 0.0625f);
+        qa[2 * w + 1][0] = pack_h2(x[2], x[6]), qa[2 * w + 1][1] = pack_h2(x[3] * 0.0625f, x[7] * 0.0625f);
       }
 #pragma unroll
       for (int g = 0; g < W; ++g) {
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], o);
-        (h ? qs1 : qs0)[g] = qs[g] * 5.9604644775390625e-08f;  // 2^-24, as the codes
+        qs[g] *= 5.9604644775390625e-08f;  // 2^-24, as the codes
       }
     }
 
@@ -548,9 +534,9 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     __syncwarp();  // every lane is done with the piece before
     if (lane == 0) follow(pieces[turn & 1], pieces[(turn & 1) ^ 1]);
     __syncwarp();
-    uint32_t nan0 = 0, nan1 = 0;  // groups in which the row has seen a value that is not finite
-    float m0 = -INFINITY, m1 = -INFINITY;
-    F2 l0 = f2(0.f, 0.f), l1 = f2(0.f, 0.f);
+    uint32_t nan = 0;  // groups in which the row has seen a value that is not finite
+    float m = -INFINITY;
+    F2 l2 = f2(0.f, 0.f);
 
 #pragma unroll 1
     for (int st = st_first; st < st_hi; ++st) {
@@ -577,8 +563,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
       const bool cut = t_base + S::CK > lim_min;  // some query does not see all of them
 
       // ---- scores, and their maximum ----------------------------------------------
-      float s[NT][X];
-      float x0 = -INFINITY, x1 = -INFINITY;
+      float s[NT][2], top = -INFINITY;
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         float acc[W][4];
@@ -599,77 +584,54 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           const uint32_t x = word[w], y = x >> 8;
-          if (R == 16) {
-            mma16816(acc[w % W], qa[2 * w][0], qa[2 * w][1], qa[2 * w][2 % X], qa[2 * w][3 % X], x & 0x000f000fu, x & 0x00f000f0u);
-            mma16816(acc[w % W], qa[2 * w + 1][0], qa[2 * w + 1][1], qa[2 * w + 1][2 % X], qa[2 * w + 1][3 % X], y & 0x000f000fu,
-                     y & 0x00f000f0u);
-          } else {
-            mma16816(acc[w % W], qa[2 * w][0], 0u, qa[2 * w][1], 0u, x & 0x000f000fu, x & 0x00f000f0u);
-            mma16816(acc[w % W], qa[2 * w + 1][0], 0u, qa[2 * w + 1][1], 0u, y & 0x000f000fu, y & 0x00f000f0u);
-          }
+          mma16816(acc[w % W], qa[2 * w][0], 0u, qa[2 * w][1], 0u, x & 0x000f000fu, x & 0x00f000f0u);
+          mma16816(acc[w % W], qa[2 * w + 1][0], 0u, qa[2 * w + 1][1], 0u, y & 0x000f000fu, y & 0x00f000f0u);
         }
         uint32_t ka[W], kb[W];
         att_words<W>(ka, entries[u / 2] + lane_e0 + (u & 1) * (32 * W));
         att_words<W>(kb, entries[u / 2] + lane_e1 + (u & 1) * (32 * W));
-        F2 r0 = f2(0.f, 0.f), r1 = f2(0.f, 0.f);
+        F2 sum = f2(0.f, 0.f);
 #pragma unroll
         for (int g = 0; g < W; ++g) {
           const F2 step = f2(half_lo(ka[g]), half_lo(kb[g])), base = f2(half_hi(ka[g]), half_hi(kb[g]));
-          r0 = f2_fma(base, f2(qs0[g], qs0[g]), f2_fma(step, f2(acc[g][0], acc[g][1]), r0));
-          if (R == 16) r1 = f2_fma(base, f2(qs1[g], qs1[g]), f2_fma(step, f2(acc[g][2], acc[g][3]), r1));
+          sum = f2_fma(base, f2(qs[g], qs[g]), f2_fma(step, f2(acc[g][0], acc[g][1]), sum));
         }
-        f2_get(r0, s[u][0], s[u][1]);
-        if (R == 16) f2_get(r1, s[u][2 % X], s[u][3 % X]);
+        f2_get(sum, s[u][0], s[u][1]);
         if (cut) {
           const int ta = t_base + 8 * u + att_key(2 * j), tb = t_base + 8 * u + att_key(2 * j + 1);
-          if (ta >= lim0) s[u][0] = -INFINITY;
-          if (tb >= lim0) s[u][1] = -INFINITY;
-          if (R == 16 && ta >= lim1) s[u][2 % X] = -INFINITY;
-          if (R == 16 && tb >= lim1) s[u][3 % X] = -INFINITY;
+          if (ta >= lim) s[u][0] = -INFINITY;
+          if (tb >= lim) s[u][1] = -INFINITY;
         }
-        x0 = max3(x0, s[u][0], s[u][1]);
-        if (R == 16) x1 = max3(x1, s[u][2 % X], s[u][3 % X]);
+        top = max3(top, s[u][0], s[u][1]);
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
-        if (R == 16) x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
-      x0 *= f0, x1 *= f1;
-      if (__any_sync(0xffffffffu, x0 > m0 + 14.f || (R == 16 && x1 > m1 + 14.f))) {
-        const float n0 = fmaxf(m0, x0 - 6.f), n1 = fmaxf(m1, x1 - 6.f);
-        const float a0 = n0 == m0 ? 1.f : ex2(m0 - n0), a1 = n1 == m1 ? 1.f : ex2(m1 - n1);
-        m0 = n0, m1 = n1;
-        l0 = f2_mul(l0, f2(a0, a0)), l1 = f2_mul(l1, f2(a1, a1));
-        if (R == 16) {
+      top *= f;
+      if (__any_sync(0xffffffffu, top > m + 14.f)) {
+        const float to = fmaxf(m, top - 6.f), a = to == m ? 1.f : ex2(m - to);
+        m = to;
+        l2 = f2_mul(l2, f2(a, a));
+        // columns 2j, 2j + 1 are the rows
+        const float ca = __shfl_sync(0xffffffffu, a, 8 * j), cb = __shfl_sync(0xffffffffu, a, 8 * j + 4);
 #pragma unroll
-          for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] *= a0, o_acc[i][1] *= a0, o_acc[i][2] *= a1, o_acc[i][3] *= a1;
-        } else {  // columns 2j, 2j + 1 are the rows
-          const float ca = __shfl_sync(0xffffffffu, a0, 8 * j), cb = __shfl_sync(0xffffffffu, a0, 8 * j + 4);
-#pragma unroll
-          for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] *= ca, o_acc[i][1] *= cb, o_acc[i][2] *= ca, o_acc[i][3] *= cb;
-        }
+        for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] *= ca, o_acc[i][1] *= cb, o_acc[i][2] *= ca, o_acc[i][3] *= cb;
       }
-      const float r0 = m0 == -INFINITY ? 0.f : -m0, r1 = m1 == -INFINITY ? 0.f : -m1;
+      const float r0 = m == -INFINITY ? 0.f : -m;
 
       // ---- probabilities and output, 16 keys at a time --------------------------------
 #pragma unroll
       for (int h = 0; h < NT / 2; ++h) {
-        uint32_t a[X], es[W][2], eb[W][2];  // P; (step, step), (base, base) of the key pairs
+        uint32_t a[2], es[W][2], eb[W][2];  // P; (step, step), (base, base) of the key pairs
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int u = 2 * h + half;
           float pa, pb;
-          f2_get(f2_fma(f2(s[u][0], s[u][1]), f2(f0, f0), f2(r0, r0)), pa, pb);
+          f2_get(f2_fma(f2(s[u][0], s[u][1]), f2(f, f), f2(r0, r0)), pa, pb);
           pa = ex2(pa), pb = ex2(pb);
-          l0 = f2_add(l0, f2(pa, pb));
-          a[R == 16 ? 2 * half : half] = pack_h2(pa, pb);
-          if (R == 16) {
-            f2_get(f2_fma(f2(s[u][2 % X], s[u][3 % X]), f2(f1, f1), f2(r1, r1)), pa, pb);
-            pa = ex2(pa), pb = ex2(pb);
-            l1 = f2_add(l1, f2(pa, pb));
-            a[(2 * half + 1) % X] = pack_h2(pa, pb);
-          }
+          l2 = f2_add(l2, f2(pa, pb));
+          a[half] = pack_h2(pa, pb);
           const int ka = 8 * u + att_key(2 * j), kb = 8 * u + att_key(2 * j + 1);
           uint32_t wa[W], wb[W];
           att_words<W>(wa, entries[h] + rec_e + lane_e0 + half * (32 * W));
@@ -680,8 +642,8 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll
             for (int g = 0; g < W; ++g) {
               const int ta = t_base + ka, tb = t_base + kb;
-              if (att_not_finite(wa[g])) nan0 |= uint32_t(ta < lim0) << g, nan1 |= uint32_t(ta < lim1) << g, wa[g] = 0;
-              if (att_not_finite(wb[g])) nan0 |= uint32_t(tb < lim0) << g, nan1 |= uint32_t(tb < lim1) << g, wb[g] = 0;
+              if (att_not_finite(wa[g])) nan |= uint32_t(ta < lim) << g, wa[g] = 0;
+              if (att_not_finite(wb[g])) nan |= uint32_t(tb < lim) << g, wb[g] = 0;
               if (ta >= lim_max) wa[g] = 0;
               if (tb >= lim_max) wb[g] = 0;
             }
@@ -708,15 +670,8 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
             const uint32_t v20 = att_even(x >> 8, es[g][0], eb[g][0]), v21 = att_even(y >> 8, es[g][1], eb[g][1]);
             const uint32_t v30 = att_odd(x >> 8, es[g][0], eb[g][0]), v31 = att_odd(y >> 8, es[g][1], eb[g][1]);
             const int o = 8 * g + 4 * half;
-            if (R == 16) {
-              mma16816(o_acc[o % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v00, v01);
-              mma16816(o_acc[(o + 1) % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v10, v11);
-              mma16816(o_acc[(o + 2) % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v20, v21);
-              mma16816(o_acc[(o + 3) % (S::kRegs / 4)], a[0], a[1], a[2 % X], a[3 % X], v30, v31);
-            } else {
-              mma16816(o_acc[o / 2], v00, v10, v01, v11, a[0], a[1]);
-              mma16816(o_acc[o / 2 + 1], v20, v30, v21, v31, a[0], a[1]);
-            }
+            mma16816(o_acc[o / 2], v00, v10, v01, v11, a[0], a[1]);
+            mma16816(o_acc[o / 2 + 1], v20, v30, v21, v31, a[0], a[1]);
           }
         }
       }
@@ -728,42 +683,32 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     refill(true);  // a piece without copies has not gone on yet
 
     // ---- the piece's outputs ---------------------------------------------------------
-    float la, lb, l0s, l1s;
-    f2_get(l0, la, lb);
-    l0s = la + lb;
-    f2_get(l1, la, lb);
-    l1s = la + lb;
+    float l;
+    {
+      float la, lb;
+      f2_get(l2, la, lb);
+      l = la + lb;
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-      l0s += __shfl_xor_sync(0xffffffffu, l0s, o);
-      nan0 |= __shfl_xor_sync(0xffffffffu, nan0, o);
-      if (R == 16) {
-        l1s += __shfl_xor_sync(0xffffffffu, l1s, o);
-        nan1 |= __shfl_xor_sync(0xffffffffu, nan1, o);
-      }
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      nan |= __shfl_xor_sync(0xffffffffu, nan, o);
     }
-    // of the lane's values' rows: R = 16: n, n + 8; R = 8: 2 j, 2 j + 1
-    uint32_t na = nan0, nb = nan1;
-    float sa = l0s, sb = l1s;
-    if (R == 8) {
-      na = __shfl_sync(0xffffffffu, nan0, 8 * j), nb = __shfl_sync(0xffffffffu, nan0, 8 * j + 4);
-      sa = __shfl_sync(0xffffffffu, l0s, 8 * j), sb = __shfl_sync(0xffffffffu, l0s, 8 * j + 4);
-    }
+    // of the rows of the lane's values: 2 j, 2 j + 1
+    const uint32_t nans[2] = {__shfl_sync(0xffffffffu, nan, 8 * j), __shfl_sync(0xffffffffu, nan, 8 * j + 4)};
+    const float sums[2] = {__shfl_sync(0xffffffffu, l, 8 * j), __shfl_sync(0xffffffffu, l, 8 * j + 4)};
     const bool starts = st_first == 0, ends = cur.st1 == cur.stages;
+    const float none = __uint_as_float(0x7fc00000u);
     if (starts && ends) {  // the whole unit
-      const float va = sa > 0.f ? 1.f / sa : sa, vb = sb > 0.f ? 1.f / sb : sb;  // no key: 0; NaN stays
 #pragma unroll
-      for (int x = 0; x < X; ++x) {
-        const bool second = R == 16 ? x >= 2 : x == 1;
-        const int rr = cur.tile * R + (R == 16 ? n + (second ? 8 : 0) : 2 * j + x), i = rr / G;
-        const int col = R == 16 ? 2 * j + (x & 1) : n;
-        const float v = second ? vb : va;
-        const uint32_t nan = second ? nb : na;
-        uint16_t *dst = p.out + (size_t(cur.row.start + i) * p.g.H_q + cur.hk * G + rr - i * G) * D + col * W * 8;
+      for (int x = 0; x < 2; ++x) {
+        const int rr = cur.tile * kAttRows + 2 * j + x, i = rr / G;
+        const float v = sums[x] > 0.f ? 1.f / sums[x] : sums[x];  // no key: 0; NaN stays
+        uint16_t *dst = p.out + (size_t(cur.row.start + i) * p.g.H_q + cur.hk * G + rr - i * G) * D + n * W * 8;
         if (i < cur.row.span) {
 #pragma unroll
           for (int g = 0; g < W; ++g) {
-            const float w = nan >> g & 1u ? __uint_as_float(0x7fc00000u) : v;
+            const float w = nans[x] >> g & 1u ? none : v;
             uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -779,27 +724,21 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
       const int kind = starts ? 1 : 0;
       const bool stay = !cur.more;  // the ring is free after the last piece
       float *dst = stay ? reinterpret_cast<float *>(ring) : stash + size_t(warp) * S::kPart;
-      const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
       for (int t = 0; t < D / 8; ++t)
 #pragma unroll
-        for (int x = 0; x < X; ++x) {
+        for (int x = 0; x < 2; ++x) {
           const int i = S::reg(t, x);
-          const uint32_t mask = (R == 16 ? x < 2 : x == 0) ? na : nb;
-          dst[i * 32 + lane] = mask >> (t / 8) & 1u ? nan : o_acc[i / 4][i % 4];
+          dst[i * 32 + lane] = nans[x] >> (t / 8) & 1u ? none : o_acc[i / 4][i % 4];
         }
-      if (j == 0) {
-        s_m[kind][warp][n] = m0, s_l[kind][warp][n] = l0s;
-        if (R == 16) s_m[kind][warp][(n + 8) % R] = m1, s_l[kind][warp][(n + 8) % R] = l1s;
-      }
+      if (j == 0) s_m[kind][warp][n] = m, s_l[kind][warp][n] = l;
       if (lane == 0) s_has[kind][warp] = stay ? 1 : 2, s_cut[kind][warp] = cur;
     }
   }
 
   // ---- join of the cut units: entry 0 is one begun before this CTA, entry w + 1 one
   // that begins with warp w -----------------------------------------------------------
-  static_assert(S::kPart * 4 + sizeof(AttJoin<D, R>) <= S::kRing, "join");
-  AttJoin<D, R> &join = *reinterpret_cast<AttJoin<D, R> *>(smem + S::kPart * 4);
+  AttJoin<D> &join = *reinterpret_cast<AttJoin<D> *>(smem + S::kPart * 4);
   __syncthreads();
   if (tid <= NW) {
     const int e = tid;
@@ -824,8 +763,8 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   // a part's weight against the common maximum M; a NaN sum keeps its NaN
   auto weight = [](float m, float l, float M) { return l != l ? 1.f : m == -INFINITY ? 0.f : ex2(m - M); };
   auto kind_of = [&](int e, int w) { return e > 0 && w == join.from[e] ? 1 : 0; };
-  for (int k = tid; k < (NW + 1) * R; k += S::kThreads) {
-    const int e = k / R, r = k % R;
+  for (int k = tid; k < (NW + 1) * kAttRows; k += S::kThreads) {
+    const int e = k / kAttRows, r = k % kAttRows;
     float M = -INFINITY, L = 0.f;
     for (int w = join.from[e]; w <= join.to[e]; ++w)
       if (s_has[kind_of(e, w)][w]) M = fmaxf(M, s_m[kind_of(e, w)][w][r]);
@@ -840,13 +779,11 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   __syncthreads();
   // items: the channels 8 g + e, 8 g + e + 1 of value x
   auto place = [&](int item, int &ln, int &x, int &t, int &r, int &col) {
-    ln = item & 31, x = (item >> 5) % X, t = (item >> 5) / X * 2;
-    const int nn = ln >> 2, jj = ln & 3;
-    r = R == 16 ? nn + (x >> 1) * 8 : 2 * jj + x;
-    col = R == 16 ? 2 * jj + (x & 1) : nn;
+    ln = item & 31, x = (item >> 5) & 1, t = (item >> 6) * 2;
+    r = 2 * (ln & 3) + x, col = ln >> 2;
   };
   auto put = [&](const AttPiece &u, float L, float y0, float y1, int t, int r, int col) {
-    const int rr = u.tile * R + r, i = rr / G;
+    const int rr = u.tile * kAttRows + r, i = rr / G;
     if (i >= u.row.span) return;
     const float v = L > 0.f ? 1.f / L : L;
     uint16_t *dst = p.out + (size_t(u.row.start + i) * p.g.H_q + u.hk * G + rr - i * G) * D + (col * W + t / 8) * 8 + t % 8;
@@ -854,7 +791,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   };
   auto entry_piece = [&](int e) -> const AttPiece & { return s_cut[e > 0 ? 1 : 0][join.from[e]]; };
   auto entry_whole = [&](int e) { return e > 0 && join.to[e] > join.from[e] && s_cut[0][join.to[e]].st1 == s_cut[0][join.to[e]].stages; };
-  auto part_of = [&](int k, int c_first) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * att_part_floats<D, R>(); };
+  auto part_of = [&](int k, int c_first) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * S::kPartAll; };
 #pragma unroll 1
   for (int e = 0; e <= NW; ++e) {
     const int from = join.from[e], to = join.to[e];
@@ -862,7 +799,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     const AttPiece &u = entry_piece(e);
     const bool whole = entry_whole(e);
     float *part = part_of(c, e > 0 ? c : -1);
-    constexpr int kItems = (S::kPairs + S::kThreads - 1) / S::kThreads;
+    constexpr int kItems = ((S::kPart / 2) + S::kThreads - 1) / S::kThreads;
 #pragma unroll 1
     for (int k0 = 0; k0 < kItems; k0 += 4) {  // 4 items of a thread at a time
       float2 y[4];
@@ -876,7 +813,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int item = (k0 + k) * S::kThreads + tid;
-          if (k0 + k < kItems && item < S::kPairs) {
+          if (k0 + k < kItems && item < (S::kPart / 2)) {
             int ln, x, t, r, col;
             place(item, ln, x, t, r, col);
             const float cw = join.c[d][w][r];
@@ -887,7 +824,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int item = (k0 + k) * S::kThreads + tid;
-        if (k0 + k < kItems && item < S::kPairs) {
+        if (k0 + k < kItems && item < (S::kPart / 2)) {
           int ln, x, t, r, col;
           place(item, ln, x, t, r, col);
           if (whole) put(u, join.sum[e][r], y[k].x, y[k].y, t, r, col);
@@ -895,7 +832,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
         }
       }
     }
-    if (!whole && tid < R) part[S::kPart + tid] = join.max[e][tid], part[S::kPart + 16 + tid] = join.sum[e][tid];
+    if (!whole && tid < kAttRows) part[S::kPart + tid] = join.max[e][tid], part[S::kPart + kAttRows + tid] = join.sum[e][tid];
   }
   // ---- units cut between CTAs: two at most -----------------------------------------------
 #pragma unroll 1
@@ -914,13 +851,13 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
     }
     __syncthreads();
     if (!s_flag) continue;
-    // 16 parts at a time: maxima and sums by 16 R threads, then the items, whose
+    // 16 parts at a time: maxima and sums by 16 * 8 threads, then the items, whose
     // first loads are on their way meanwhile
-    constexpr int kItems = (S::kPairs + S::kThreads - 1) / S::kThreads;
+    constexpr int kItems = ((S::kPart / 2) + S::kThreads - 1) / S::kThreads;
     float2 y[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) y[k] = make_float2(0.f, 0.f);
-    if (tid < R) join.max[e][tid] = -INFINITY, join.sum[e][tid] = 0.f;
+    if (tid < kAttRows) join.max[e][tid] = -INFINITY, join.sum[e][tid] = 0.f;
 #pragma unroll 1
     for (int q0 = c_first; q0 <= c_last; q0 += 16) {
       const int some = min(16, c_last + 1 - q0);
@@ -931,36 +868,36 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll
           for (int k = 0; k < kItems; ++k) {
             const int item = k * S::kThreads + tid;
-            v[f][k] = item < S::kPairs && q + f < some ? __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q + f, c_first)) + item)
+            v[f][k] = item < (S::kPart / 2) && q + f < some ? __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q + f, c_first)) + item)
                                                        : make_float2(0.f, 0.f);
           }
       };
       float m = -INFINITY, l = 0.f;
-      if (tid < 16 * R && tid / R < some) {
-        const float *src = part_of(q0 + tid / R, c_first) + S::kPart + tid % R;
-        m = __ldcg(src), l = __ldcg(src + 16);
+      if (tid < 16 * kAttRows && tid / kAttRows < some) {
+        const float *src = part_of(q0 + tid / kAttRows, c_first) + S::kPart + tid % kAttRows;
+        m = __ldcg(src), l = __ldcg(src + kAttRows);
       }
       load4(0);
       __syncthreads();
-      if (tid < 16 * R) join.w[tid / R][tid % R] = m;
+      if (tid < 16 * kAttRows) join.w[tid / kAttRows][tid % kAttRows] = m;
       __syncthreads();
       float M = -INFINITY;
-      if (tid < 16 * R) {
-        M = join.max[e][tid % R];
-        for (int q = 0; q < 16; ++q) M = fmaxf(M, join.w[q][tid % R]);
+      if (tid < 16 * kAttRows) {
+        M = join.max[e][tid % kAttRows];
+        for (int q = 0; q < 16; ++q) M = fmaxf(M, join.w[q][tid % kAttRows]);
       }
       __syncthreads();
-      if (tid < 16 * R) {
+      if (tid < 16 * kAttRows) {
         const float w = weight(m, l, M);
-        join.w[tid / R][tid % R] = w, join.lw[tid / R][tid % R] = tid / R < some ? l * w : 0.f;
-        if (tid < R) {
+        join.w[tid / kAttRows][tid % kAttRows] = w, join.lw[tid / kAttRows][tid % kAttRows] = tid / kAttRows < some ? l * w : 0.f;
+        if (tid < kAttRows) {
           const float old = join.max[e][tid];
           join.c[0][0][tid] = old == -INFINITY ? 0.f : ex2(old - M);  // of the batches before
           join.max[e][tid] = M;
         }
       }
       __syncthreads();
-      if (tid < R) {
+      if (tid < kAttRows) {
         float L = join.sum[e][tid];
         L = L != L ? L : L * join.c[0][0][tid];
         for (int q = 0; q < 16; ++q) L += join.lw[q][tid];
@@ -993,7 +930,7 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
       const int item = k * S::kThreads + tid;
-      if (item < S::kPairs) {
+      if (item < (S::kPart / 2)) {
         int ln, x, t, r, col;
         place(item, ln, x, t, r, col);
         put(u, join.sum[e][r], y[k].x, y[k].y, t, r, col);
@@ -1002,10 +939,10 @@ __global__ void __launch_bounds__(AttShape<D, R>::kThreads, 1) kv4_attend_mma(co
   }
 }
 
-template <int D, int R>
+template <int D>
 inline size_t att_mma_ws(int ctas) {
   // counters; two parts a CTA; what a warp puts aside while its ring goes on
-  return 4096 + sizeof(float) * size_t(ctas) * (2 * att_part_floats<D, R>() + size_t(AttShape<D, R>::NW) * AttShape<D, R>::kPart);
+  return 4096 + sizeof(float) * size_t(ctas) * (2 * AttShape<D>::kPartAll + AttShape<D>::NW * AttShape<D>::kPart);
 }
 
 // Raise a kernel's shared-memory limit, once per device.
@@ -1019,23 +956,18 @@ inline cudaError_t att_configure(const void *kernel, int smem, std::atomic<bool>
   return e;
 }
 
-template <int D, int R>
-cudaError_t launch_att_mma_r(const Kv4AttendParams &p, int ctas, cudaStream_t s) {
-  using S = AttShape<D, R>;
-  static std::atomic<bool> configured[64];
-  const cudaError_t e = att_configure(reinterpret_cast<const void *>(kv4_attend_mma<D, R>), S::kSmem, configured);
-  if (e != cudaSuccess) return e;
-  return launch_pdl_smem(kv4_attend_mma<D, R>, dim3(ctas), dim3(S::kThreads), S::kSmem, s, p);
-}
-
-// rows: query rows of a unit (8 or 16)
 template <int D>
-cudaError_t launch_att_mma(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s) {
-  return rows == 8 ? launch_att_mma_r<D, 8>(p, ctas, s) : launch_att_mma_r<D, 16>(p, ctas, s);
+cudaError_t launch_att_mma(const Kv4AttendParams &p, int ctas, cudaStream_t s) {
+  using S = AttShape<D>;
+  static_assert(S::kPart * 4 + sizeof(AttJoin<D>) <= S::kRing, "join");
+  static std::atomic<bool> configured[64];
+  const cudaError_t e = att_configure(reinterpret_cast<const void *>(kv4_attend_mma<D>), S::kSmem, configured);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_smem(kv4_attend_mma<D>, dim3(ctas), dim3(S::kThreads), S::kSmem, s, p);
 }
 
-cudaError_t launch_att_mma_64(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s);
-cudaError_t launch_att_mma_128(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s);
-cudaError_t launch_att_mma_256(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s);
+cudaError_t launch_att_mma_64(const Kv4AttendParams &p, int ctas, cudaStream_t s);
+cudaError_t launch_att_mma_128(const Kv4AttendParams &p, int ctas, cudaStream_t s);
+cudaError_t launch_att_mma_256(const Kv4AttendParams &p, int ctas, cudaStream_t s);
 
 }  // namespace gdn

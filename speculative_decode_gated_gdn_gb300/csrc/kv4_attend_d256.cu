@@ -3,8 +3,8 @@
 
 namespace gdn {
 
-cudaError_t launch_att_mma_256(const Kv4AttendParams &p, int rows, int ctas, cudaStream_t s) {
-  return launch_att_mma<256>(p, rows, ctas, s);
+cudaError_t launch_att_mma_256(const Kv4AttendParams &p, int ctas, cudaStream_t s) {
+  return launch_att_mma<256>(p, ctas, s);
 }
 
 }  // namespace gdn
