@@ -250,10 +250,12 @@ struct AttPiece {
 template <int D>
 struct AttJoin {
   static constexpr int NW = AttShape<D>::NW;
-  float c[2][NW][kAttRows];                   // weights of the warps' parts
+  const float *src[2 * NW];              // the warps' parts, those of entry e from at[e] on
+  float c[2 * NW][kAttRows];             // their weights
+  int at[NW + 2], whole[NW + 1], n;      // entries: parts, nothing of it elsewhere; how many
+  const AttPiece *piece[NW + 1];
   float max[NW + 1][kAttRows], sum[NW + 1][kAttRows];
-  float w[16][kAttRows], lw[16][kAttRows];           // weights, and weighted sums, of 16 CTAs' parts
-  int from[NW + 1], to[NW + 1];        // warps of a cut unit; from > to: none
+  float w[16][kAttRows], lw[16][kAttRows], old[kAttRows];  // weights, and weighted sums, of 16 CTAs' parts
 };
 
 template <int D>
@@ -736,48 +738,52 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
     }
   }
 
-  // ---- join of the cut units: entry 0 is one begun before this CTA, entry w + 1 one
-  // that begins with warp w -----------------------------------------------------------
+  // ---- join of the cut units: entry 0 is one begun before this CTA, the others those
+  // that begin in it.  A lane is a piece, in the order of the line: of warp lane / 2,
+  // the one begun before that warp and the one that begins in it. ---------------------
   AttJoin<D> &join = *reinterpret_cast<AttJoin<D> *>(smem + S::kPart * 4);
-  __syncthreads();
-  if (tid <= NW) {
-    const int e = tid;
-    int from = NW, to = -1;
-    if (e == 0) {
-      int w = 0;
-      while (w < NW && s_none[w]) ++w;
-      if (w < NW && s_has[0][w]) from = to = w;
-    } else if (s_has[1][e - 1]) {
-      from = to = e - 1;
-    }
-    if (from <= to && !(e == 0 && s_cut[0][from].st1 == s_cut[0][from].stages))
-      for (int w = from + 1; w < NW; ++w) {
-        if (s_none[w]) continue;
-        if (!s_has[0][w]) break;
-        to = w;
-        if (s_cut[0][w].st1 == s_cut[0][w].stages) break;
-      }
-    join.from[e] = from, join.to[e] = to;
-  }
   __syncthreads();
   // a part's weight against the common maximum M; a NaN sum keeps its NaN
   auto weight = [](float m, float l, float M) { return l != l ? 1.f : m == -INFINITY ? 0.f : ex2(m - M); };
-  auto kind_of = [&](int e, int w) { return e > 0 && w == join.from[e] ? 1 : 0; };
-  for (int k = tid; k < (NW + 1) * kAttRows; k += S::kThreads) {
-    const int e = k / kAttRows, r = k % kAttRows;
-    float M = -INFINITY, L = 0.f;
-    for (int w = join.from[e]; w <= join.to[e]; ++w)
-      if (s_has[kind_of(e, w)][w]) M = fmaxf(M, s_m[kind_of(e, w)][w][r]);
-    for (int w = join.from[e]; w <= join.to[e]; ++w) {
-      const int d = kind_of(e, w);
-      const float cw = s_has[d][w] ? weight(s_m[d][w][r], s_l[d][w][r], M) : 0.f;
-      join.c[d][w][r] = cw;
-      if (s_has[d][w]) L = fmaf(s_l[d][w][r], cw, L);
+  if (warp < kAttRows) {  // a row a warp
+    const int w = lane >> 1, kind = lane & 1, has = w < NW ? s_has[kind][w % NW] : 0;
+    const uint32_t all = __ballot_sync(0xffffffffu, has != 0), heads = __ballot_sync(0xffffffffu, has != 0 && kind == 1);
+    const uint32_t upto = 0xffffffffu >> (31 - lane), before_it = heads & upto, behind = heads & ~upto;
+    const int e = __popc(before_it);  // the entry, and its lanes
+    const int first = before_it ? 31 - __clz(before_it) : 0, last = behind ? __ffs(behind) - 2 : 31;
+    const float m = has ? s_m[kind][w % NW][warp] : -INFINITY, l = has ? s_l[kind][w % NW][warp] : 0.f;
+    float M = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_up_sync(0xffffffffu, M, o);
+      if (lane - o >= first) M = fmaxf(M, x);
     }
-    join.max[e][r] = M, join.sum[e][r] = L;
+    M = __shfl_sync(0xffffffffu, M, last);
+    const float cw = weight(m, l, M);
+    float L = l * cw;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_up_sync(0xffffffffu, L, o);
+      if (lane - o >= first) L += x;
+    }
+    const int pos = __popc(all & (upto >> 1));
+    if (has) join.c[pos][warp] = cw;
+    if (lane == last) join.max[e][warp] = M, join.sum[e][warp] = L;
+    if (warp == 0) {
+      if (has) {
+        join.src[pos] = has == 1 ? reinterpret_cast<const float *>(smem + w * S::kRing) : stash + size_t(w) * S::kPart;
+        if (lane == first || (e == 0 && pos == 0)) join.piece[e] = &s_cut[kind][w];
+        const uint32_t rest = all & ~upto;
+        if (!rest || __ffs(rest) - 1 > last)  // the entry's last piece
+          join.whole[e] = e > 0 && kind == 0 && s_cut[0][w].st1 == s_cut[0][w].stages;
+      }
+      if (lane == last) join.at[e + 1] = pos + (has != 0);
+      if (lane == 0) join.at[0] = 0, join.n = __popc(heads) + 1;
+    }
   }
   __syncthreads();
   // items: the channels 8 g + e, 8 g + e + 1 of value x
+  constexpr int kPairs = S::kPart / 2;
   auto place = [&](int item, int &ln, int &x, int &t, int &r, int &col) {
     ln = item & 31, x = (item >> 5) & 1, t = (item >> 6) * 2;
     r = 2 * (ln & 3) + x, col = ln >> 2;
@@ -789,56 +795,40 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
     uint16_t *dst = p.out + (size_t(u.row.start + i) * p.g.H_q + u.hk * G + rr - i * G) * D + (col * W + t / 8) * 8 + t % 8;
     *reinterpret_cast<__nv_bfloat162 *>(dst) = __floats2bfloat162_rn(y0 * v, y1 * v);
   };
-  auto entry_piece = [&](int e) -> const AttPiece & { return s_cut[e > 0 ? 1 : 0][join.from[e]]; };
-  auto entry_whole = [&](int e) { return e > 0 && join.to[e] > join.from[e] && s_cut[0][join.to[e]].st1 == s_cut[0][join.to[e]].stages; };
   auto part_of = [&](int k, int c_first) -> float * { return parts + (size_t(k) * 2 + (k == c_first ? 1 : 0)) * S::kPartAll; };
+  const int entries = join.n;
 #pragma unroll 1
-  for (int e = 0; e <= NW; ++e) {
-    const int from = join.from[e], to = join.to[e];
-    if (from > to) continue;
-    const AttPiece &u = entry_piece(e);
-    const bool whole = entry_whole(e);
-    float *part = part_of(c, e > 0 ? c : -1);
-    constexpr int kItems = ((S::kPart / 2) + S::kThreads - 1) / S::kThreads;
+  for (int i = tid; i < entries * kPairs; i += S::kThreads) {
+    const int e = i / kPairs, item = i % kPairs, k1 = join.at[e + 1];
+    int k = join.at[e], ln, x, t, r, col;
+    if (k == k1) continue;
+    place(item, ln, x, t, r, col);
+    const int at = S::reg(t, x) * 32 + ln;  // tile t + 1: two accumulators on
+    float y0 = 0.f, y1 = 0.f;
 #pragma unroll 1
-    for (int k0 = 0; k0 < kItems; k0 += 4) {  // 4 items of a thread at a time
-      float2 y[4];
+    for (; k < k1; k += 4) {  // 4 parts' loads on their way
+      float x0[4], x1[4], cw[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = make_float2(0.f, 0.f);
-#pragma unroll 1
-      for (int w = from; w <= to; ++w) {
-        const int d = kind_of(e, w), has = s_has[d][w];
-        if (!has) continue;
-        const float *src = has == 1 ? reinterpret_cast<const float *>(smem + w * S::kRing) : stash + size_t(w) * S::kPart;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int item = (k0 + k) * S::kThreads + tid;
-          if (k0 + k < kItems && item < (S::kPart / 2)) {
-            int ln, x, t, r, col;
-            place(item, ln, x, t, r, col);
-            const float cw = join.c[d][w][r];
-            y[k].x = fmaf(src[S::reg(t, x) * 32 + ln], cw, y[k].x), y[k].y = fmaf(src[S::reg(t + 1, x) * 32 + ln], cw, y[k].y);
-          }
-        }
+      for (int f = 0; f < 4; ++f) {
+        const int q = k + f < k1 ? k + f : k;
+        x0[f] = join.src[q][at], x1[f] = join.src[q][at + 64], cw[f] = join.c[q][r];
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int item = (k0 + k) * S::kThreads + tid;
-        if (k0 + k < kItems && item < (S::kPart / 2)) {
-          int ln, x, t, r, col;
-          place(item, ln, x, t, r, col);
-          if (whole) put(u, join.sum[e][r], y[k].x, y[k].y, t, r, col);
-          else *(reinterpret_cast<float2 *>(part) + item) = y[k];
-        }
-      }
+      for (int f = 0; f < 4; ++f)
+        if (k + f < k1) y0 = fmaf(x0[f], cw[f], y0), y1 = fmaf(x1[f], cw[f], y1);
     }
-    if (!whole && tid < kAttRows) part[S::kPart + tid] = join.max[e][tid], part[S::kPart + kAttRows + tid] = join.sum[e][tid];
+    if (join.whole[e]) put(*join.piece[e], join.sum[e][r], y0, y1, t, r, col);
+    else *(reinterpret_cast<float2 *>(part_of(c, e > 0 ? c : -1)) + item) = make_float2(y0, y1);
   }
   // ---- units cut between CTAs: two at most -----------------------------------------------
 #pragma unroll 1
-  for (int e = 0; e <= NW; ++e) {
-    if (join.from[e] > join.to[e] || entry_whole(e)) continue;
-    const AttPiece &u = entry_piece(e);
+  for (int e = 0; e < entries; ++e) {
+    if (join.at[e] == join.at[e + 1] || join.whole[e]) continue;
+    const AttPiece &u = *join.piece[e];
+    if (tid < kAttRows) {
+      float *part = part_of(c, e > 0 ? c : -1);
+      part[S::kPart + tid] = join.max[e][tid], part[S::kPart + kAttRows + tid] = join.sum[e][tid];
+    }
     const int c_first = cta_of(u.first + 1), c_last = cta_of(u.first + 2 * u.stages - 1);
     __threadfence();
     __syncthreads();
@@ -853,7 +843,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
     if (!s_flag) continue;
     // 16 parts at a time: maxima and sums by 16 * 8 threads, then the items, whose
     // first loads are on their way meanwhile
-    constexpr int kItems = ((S::kPart / 2) + S::kThreads - 1) / S::kThreads;
+    constexpr int kItems = (kPairs + S::kThreads - 1) / S::kThreads;
     float2 y[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) y[k] = make_float2(0.f, 0.f);
@@ -868,7 +858,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
 #pragma unroll
           for (int k = 0; k < kItems; ++k) {
             const int item = k * S::kThreads + tid;
-            v[f][k] = item < (S::kPart / 2) && q + f < some ? __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q + f, c_first)) + item)
+            v[f][k] = item < kPairs && q + f < some ? __ldcg(reinterpret_cast<const float2 *>(part_of(q0 + q + f, c_first)) + item)
                                                        : make_float2(0.f, 0.f);
           }
       };
@@ -892,14 +882,14 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
         join.w[tid / kAttRows][tid % kAttRows] = w, join.lw[tid / kAttRows][tid % kAttRows] = tid / kAttRows < some ? l * w : 0.f;
         if (tid < kAttRows) {
           const float old = join.max[e][tid];
-          join.c[0][0][tid] = old == -INFINITY ? 0.f : ex2(old - M);  // of the batches before
+          join.old[tid] = old == -INFINITY ? 0.f : ex2(old - M);  // of the batches before
           join.max[e][tid] = M;
         }
       }
       __syncthreads();
       if (tid < kAttRows) {
         float L = join.sum[e][tid];
-        L = L != L ? L : L * join.c[0][0][tid];
+        L = L != L ? L : L * join.old[tid];
         for (int q = 0; q < 16; ++q) L += join.lw[q][tid];
         join.sum[e][tid] = L;
       }
@@ -908,7 +898,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
         for (int k = 0; k < kItems; ++k) {
           int ln, x, t, r, col;
           place(k * S::kThreads + tid, ln, x, t, r, col);
-          const float w = join.c[0][0][r];
+          const float w = join.old[r];
           y[k].x *= w, y[k].y *= w;
         }
       }
@@ -930,7 +920,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
       const int item = k * S::kThreads + tid;
-      if (item < (S::kPart / 2)) {
+      if (item < kPairs) {
         int ln, x, t, r, col;
         place(item, ln, x, t, r, col);
         put(u, join.sum[e][r], y[k].x, y[k].y, t, r, col);
