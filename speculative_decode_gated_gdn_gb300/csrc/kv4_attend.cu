@@ -20,16 +20,20 @@ int att_sms() {
   return n;
 }
 
-// More query rows a kv head than a unit of eight: the tensor-core form, which
-// shares every formed key among up to 128 rows.  Both sides, us, 8 rows (few, many)
-// and 16 (in units of 16 rows, which were taken out, many), 2 kv heads:
-//                       D = 64                  D = 128                 D = 256
-//   1 row  of 32768     25 26 | 28 26           26 31 | 32 31           36 39 | 47 39
-//   2 rows of 100000    31 41 | 35 41           37 49 | 45 49           64 77 | 87 77
-//   16 rows of 2000     26 21 | 28 21           25 24 | 31 24           30 27 | 37 27
-//   48 rows of 4000     30 38 | 33 38           34 45 | 42 45           62 70 | 79 70
+// More query rows a kv head than a few units of eight: the tensor-core form, which
+// shares every formed key among up to 128 rows.  Both sides, us (units of eight,
+// tensor cores), 2 kv heads:
+//                       D = 64            D = 128           D = 256
+//   rows                16      24        16      24        8       16
+//   1 row  of 32768     20 26   20 26     23 31   26 30     33 38   38 38
+//   2 rows of 100000    31 41   37 41     42 48   56 48     61 77   93 77
+//   16 rows of 2000     18 21   18 20     21 23   22 24     26 27   31 27
+//   48 rows of 4000     29 38   36 38     42 45   54 45     58 69   89 69
+//   64 rows of 300      18 21   18 21     21 23   21 23     26 25   27 25
 // The lengths are not known on the host, so the choice is by rows alone.
-bool att_many_rows(const Kv4Geom &g, int max_q) { return (long long)max_q * (g.H_q / g.H_kv) > kAttRows; }
+bool att_many_rows(const Kv4Geom &g, int max_q) {
+  return (long long)max_q * (g.H_q / g.H_kv) > (g.D == 64 ? 3 * kAttRows : g.D == 128 ? 2 * kAttRows : kAttRows);
+}
 
 }  // namespace
 
