@@ -49,7 +49,10 @@ struct AttShape {
   static constexpr int W = D / 64;               // groups of a head
   static constexpr int ST = D == 256 ? 32 : 64;  // keys of a stage: what a copy brings
   static constexpr int CK = 32, NT = CK / 8;     // keys, and key tiles, taken at a time
-  static constexpr int NW = D == 64 ? 16 : 12;   // warps of a CTA, as the registers of a thread allow
+  // Warps of a CTA, as the registers of a thread allow, and a multiple of 4.  48 rows of
+  // 8000 keys at D = 256: 82.5 us with 12 (spills), 100 with 9, 71.9 with 8, 73.9 with 7;
+  // 64 ragged rows of 8192 at D = 128: 106 with 12, 119 with 10, 114 with 8.
+  static constexpr int NW = D == 64 ? 16 : D == 128 ? 12 : 8;
   static constexpr int kThreads = 32 * NW;
   static constexpr int kCodes = ST * D / 2, kEntries = ST * W * 4;
   static constexpr int kStage = 2 * (kCodes + kEntries);
