@@ -48,11 +48,14 @@ template <int D>
 struct AttShape {
   static constexpr int W = D / 64;               // groups of a head
   static constexpr int ST = D == 256 ? 32 : 64;  // keys of a stage: what a copy brings
-  static constexpr int CK = 32, NT = CK / 8;     // keys, and key tiles, taken at a time
+  // Keys, and key tiles, taken at a time.  64 at D = 128 spill with 12 warps (ragged rows
+  // below: 117 us); 16 at D = 256: 95.8 us for 71.9.
+  static constexpr int CK = D == 64 ? 64 : 32, NT = CK / 8;
   // Warps of a CTA, as the registers of a thread allow, and a multiple of 4.  48 rows of
   // 8000 keys at D = 256: 82.5 us with 12 (spills), 100 with 9, 71.9 with 8, 73.9 with 7;
-  // 64 ragged rows of 8192 at D = 128: 106 with 12, 119 with 10, 114 with 8.
-  static constexpr int NW = D == 64 ? 16 : D == 128 ? 12 : 8;
+  // 64 ragged rows of 8192 at D = 128: 106 with 12, 119 with 10, 114 with 8; at D = 64,
+  // 16 rows of 2000: 15.9 with 12, 17.6 with 16 (and 38.8, 39.1 for 48 rows of 16000).
+  static constexpr int NW = D == 256 ? 8 : 12;
   static constexpr int kThreads = 32 * NW;
   static constexpr int kCodes = ST * D / 2, kEntries = ST * W * 4;
   static constexpr int kStage = 2 * (kCodes + kEntries);
@@ -238,7 +241,8 @@ __device__ __forceinline__ long long att_scan(long long v, long long *s_warp, lo
 // one place (queries in, outputs out: about half a stage's time) and then two
 // places a stage; a stage belongs to the piece that holds its first.  A unit of
 // kAttUncut stages or fewer is not cut: it belongs to the piece that holds its
-// first place, whole.
+// first place, whole (40 rows of 100 keys at D = 64: 12.0 us, cut at every stage
+// 16.2; 64 of 300: 17.7, uncut up to 8 stages 19.3).
 constexpr int kAttUncut = 4;
 
 struct AttPiece {
@@ -297,7 +301,8 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
   }
   before = att_scan<NW>(mine, s_warp, &total);
   if (total == 0) return;
-  // a warp wants a stage at least
+  // a warp wants a stage at least (16 rows of 2000 keys at D = 128: 20.4 us, with two
+  // stages 24.6)
   const int ctas = int(min((long long)gridDim.x, (total + 3 * NW - 1) / (3 * NW)));
   const int c = blockIdx.x;
   if (c >= ctas) return;
