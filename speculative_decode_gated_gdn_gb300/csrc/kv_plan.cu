@@ -18,7 +18,7 @@ namespace gdn {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanOneCta = 8192;  // tokens up to which the bookkeeping CTA writes the slots itself
+constexpr int kPlanOneCta = 2048;  // tokens up to which the bookkeeping CTA writes the slots itself
 
 // Inclusive scan of v over the CTA; *total gets the sum of all threads.
 __device__ __forceinline__ long long block_scan(long long v, long long *s_warp, long long *total) {

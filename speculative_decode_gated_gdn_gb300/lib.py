@@ -390,8 +390,25 @@ def _tokens(t, what, heads, d):
 
 
 def _count(t, what, n):
+    if not isinstance(t, _t().Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
     if t.numel() != n:
         raise ValueError(f"{what}: expected {n} elements, got {t.numel()}")
+
+
+def _ptrs(*args):
+    """Device pointers of contiguous CUDA tensors, each (tensor, name, elements,
+    dtype).  What they are is asked for in one pass, because small calls wait
+    for the host; the checks that name what is wrong run when something is."""
+    try:
+        p = [t.data_ptr() for t, _, n, dtype in args if t.numel() == n and t.dtype is dtype and t.is_cuda and t.is_contiguous()]
+        if len(p) == len(args):
+            return p
+    except AttributeError:
+        pass
+    for t, what, n, _ in args:
+        _count(t, what, n)
+    return [_ptr(t, what, dtype) for t, what, _, dtype in args]
 
 
 def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, free_count, q_start, q_count, kv_len,
@@ -400,18 +417,12 @@ def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, fre
     gdn_kv_plan): int32 CUDA tensors, active uint8; N = slots.numel().  T > 0
     puts row b's tokens at b*T, T = 0 packs them."""
     torch = _t()
-    i32, B = torch.int32, kd.B
-    for t, what, n in ((lens, "lens", B), (add, "add", B), (active, "active", B), (held, "held", B),
-                       (table, "table", B * kd.max_pages), (free_list, "free_list", kd.n_pages),
-                       (free_count, "free_count", 1), (q_start, "q_start", B + 1), (q_count, "q_count", B),
-                       (kv_len, "kv_len", B), (positions, "positions", slots.numel())):
-        _count(t, what, n)
-    rc = load().gdn_kv_plan(
-        ctypes.byref(kd), T, slots.numel(), _ptr(lens, "lens", i32), _ptr(add, "add", i32),
-        _ptr(active, "active", torch.uint8), _ptr(held, "held", i32), _ptr(table, "table", i32),
-        _ptr(free_list, "free_list", i32), _ptr(free_count, "free_count", i32), _ptr(q_start, "q_start", i32),
-        _ptr(q_count, "q_count", i32), _ptr(kv_len, "kv_len", i32), _ptr(slots, "slots", i32),
-        _ptr(positions, "positions", i32), _stream(stream))
+    i32, B, N = torch.int32, kd.B, slots.numel()
+    p = _ptrs((lens, "lens", B, i32), (add, "add", B, i32), (active, "active", B, torch.uint8), (held, "held", B, i32),
+              (table, "table", B * kd.max_pages, i32), (free_list, "free_list", kd.n_pages, i32),
+              (free_count, "free_count", 1, i32), (q_start, "q_start", B + 1, i32), (q_count, "q_count", B, i32),
+              (kv_len, "kv_len", B, i32), (slots, "slots", N, i32), (positions, "positions", N, i32))
+    rc = load().gdn_kv_plan(ctypes.byref(kd), T, N, *p, _stream(stream))
     _check(rc, "gdn_kv_plan")
 
 
@@ -441,8 +452,7 @@ def gdn_kv4_append(kd: gdn_kv4_dims, q, k, v, positions, rope, axis, slots, page
     N = q.shape[0]
     if k.shape[0] != N or v.shape[0] != N:
         raise ValueError("q, k and v must have the same number of tokens")
-    _count(slots, "slots", N)
-    _count(q_out, "q_out", N * kd.H_q * kd.d)
+    sp, op = _ptrs((slots, "slots", N, torch.int32), (q_out, "q_out", N * kd.H_q * kd.d, torch.bfloat16))
     rot, max_pos, n_axes = 0, 0, 0
     if rope is not None:
         if rope.dim() != 3 or rope.shape[2] != 2:
@@ -455,7 +465,7 @@ def gdn_kv4_append(kd: gdn_kv4_dims, q, k, v, positions, rope, axis, slots, page
     rc = load().gdn_kv4_append(
         ctypes.byref(kd), N, qp, qs, kp, ks, vp, vs, _ptr(positions, "positions", torch.int32) if rot else None,
         n_axes, _ptr(rope, "rope", torch.float32), max_pos, rot, axis if rot else None, style,
-        _ptr(slots, "slots", torch.int32), _cache(kd, pages), _ptr(q_out, "q_out", torch.bfloat16), _stream(stream))
+        sp, _cache(kd, pages), op, _stream(stream))
     _check(rc, "gdn_kv4_append")
 
 
@@ -464,10 +474,9 @@ def gdn_kv4_read(kd: gdn_kv4_dims, slots, pages, k, v, stream=None):
     gdn_kv4_read): k and v [N][H_kv][d] bf16, written."""
     torch = _t()
     N = slots.numel()
-    _count(k, "k", N * kd.H_kv * kd.d)
-    _count(v, "v", N * kd.H_kv * kd.d)
-    rc = load().gdn_kv4_read(ctypes.byref(kd), N, _ptr(slots, "slots", torch.int32), _cache(kd, pages),
-                             _ptr(k, "k", torch.bfloat16), _ptr(v, "v", torch.bfloat16), _stream(stream))
+    size, bf16 = N * kd.H_kv * kd.d, torch.bfloat16
+    sp, kp, vp = _ptrs((slots, "slots", N, torch.int32), (k, "k", size, bf16), (v, "v", size, bf16))
+    rc = load().gdn_kv4_read(ctypes.byref(kd), N, sp, _cache(kd, pages), kp, vp, _stream(stream))
     _check(rc, "gdn_kv4_read")
 
 
@@ -481,16 +490,13 @@ def gdn_kv4_attend(kd: gdn_kv4_dims, q, pages, table, q_start, q_count, kv_len, 
     gdn_kv4_attend): q and out [N][H_q][d] bf16, pages uint8, table, q_start,
     q_count, kv_len as gdn_kv_plan leaves them, ws zero-filled once."""
     torch = _t()
-    i32, B = torch.int32, kd.B
-    N = q.shape[0]
-    for t, what, n in ((q, "q", N * kd.H_q * kd.d), (out, "out", N * kd.H_q * kd.d),
-                       (table, "table", B * kd.max_pages), (q_start, "q_start", B + 1), (q_count, "q_count", B),
-                       (kv_len, "kv_len", B)):
-        _count(t, what, n)
+    i32, bf16, B, N = torch.int32, torch.bfloat16, kd.B, q.shape[0]
+    size = N * kd.H_q * kd.d
+    qp, op, tp, sp, cp, lp = _ptrs((q, "q", size, bf16), (out, "out", size, bf16), (table, "table", B * kd.max_pages, i32),
+                                   (q_start, "q_start", B + 1, i32), (q_count, "q_count", B, i32), (kv_len, "kv_len", B, i32))
     rc = load().gdn_kv4_attend(
-        ctypes.byref(kd), N, max_q, _ptr(q, "q", torch.bfloat16), _cache(kd, pages), _ptr(table, "table", i32),
-        _ptr(q_start, "q_start", i32), _ptr(q_count, "q_count", i32), _ptr(kv_len, "kv_len", i32), scale,
-        _ptr(out, "out", torch.bfloat16), _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
+        ctypes.byref(kd), N, max_q, qp, _cache(kd, pages), tp, sp, cp, lp, scale, op, _ptr(ws, "ws"),
+        ws.numel() * ws.element_size(), _stream(stream))
     _check(rc, "gdn_kv4_attend")
 
 
