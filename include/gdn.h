@@ -588,7 +588,9 @@ size_t gdn_kv4_attend_workspace_bytes(const gdn_kv4_dims *dims, int N, int max_q
  *             next); one call at a time may use it
  * A row with kv_len outside [0, max_pages * page] is cut to that range, a span
  * longer than max_q to max_q (GDN_STATUS_BAD_LEN); a page outside the cache
- * leaves that row's outputs unspecified (GDN_STATUS_BAD_INDEX).
+ * leaves that row's outputs unspecified (GDN_STATUS_BAD_INDEX).  After a wait
+ * that gave up (GDN_STATUS_TIMEOUT) all outputs are unspecified and ws must be
+ * zero-filled again.
  */
 int gdn_kv4_attend(const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages,
                    const int32_t *table, const int32_t *q_start, const int32_t *q_count, const int32_t *kv_len,

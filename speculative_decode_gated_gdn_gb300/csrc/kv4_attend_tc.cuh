@@ -21,16 +21,26 @@
 // The loops over a tile are kept short in code (a chunk of 32 scores, a word of
 // codes at a time): unrolled whole, the roles' code passed what the SM's
 // instruction caches hold, and every instruction waited for its fetch (5.5 us a
-// tile of 64 keys at D = 256).
+// tile of 64 keys at D = 256, for 1.4).
 //
-// What bounds it: the tensor cores where rows are many (4 * 128 * NK * D
-// operations a tile), the dequant's instructions where a tile's rows are few.
+// What bounds it: a tile is a chain (scores, their maximum, exponentials, output)
+// whose steps wait for one another, and the roles share the issue slots, which
+// are 55 % busy; the tensor cores work 28 % of the time.  A tile of 128 keys at D =
+// 128 takes 2700 cycles where its products alone take 1090; with the dequant, the
+// exponentials and the maxima left out, 1790: what then is left is the products
+// and the barriers between them.  Neither separate columns for P (no
+// product waits for the softmax of the tile before last, 3 % slower), nor loads of
+// scores 16 at a time and one ahead (17 % slower), nor leaving out the softmax of
+// warps without rows (2 % slower) shortened it.
 // With Q and P in tensor memory the products read only K and V from shared
 // memory, so that a 64-key tile still feeds them at D = 256, where O takes half
 // of the tensor memory.
+// 2000 queries behind 16001 keys, 32 heads over 8 of 128: 617 us, 900 TFLOP/s of
+// the products; a prompt of 4096, 16 heads over 2 of 256: 189 us, 730 TFLOP/s.
 //
 // Units are laid on one line in tiles of keys and cut evenly over a persistent
 // grid as in kv4_attend.cuh; causal tiles count as far as their last query sees.
+// A unit that is cut leaves parts in the workspace.
 #pragma once
 
 #include "kv4_attend.cuh"
@@ -47,9 +57,13 @@ constexpr int kTcRing = 4;       // tiles of codes in flight
 constexpr int kTcUnits = 4;      // units handed out ahead
 // What a unit costs besides its tiles of keys (queries in, outputs out), in
 // tiles: its place on the line is that much longer, so that the pieces of the
-// CTAs that have many short units are not the last to end.
+// CTAs that have many short units are not the last to end.  The prompt of 4096
+// above: 329 us with 1, 241 with 3, 189 with 6, 193 with 10; 24 rows of 8 drafts
+// over 6001 keys, 32 heads over 4 of 128: 59.8, 49.8, 51.6, 55.1.
 constexpr int kTcUnitCost = 6;
-constexpr int kTcJoin = 8;       // parts of a cut unit that are joined at a time
+// Parts of a cut unit that are joined at a time: by one CTA, part after part, those of
+// 32768 keys with 24 rows at D = 256 (76 parts) made the call take 240 us, 39 so.
+constexpr int kTcJoin = 8;
 
 template <int D>
 struct TcShape {
