@@ -328,6 +328,14 @@ def test_attend_long_rows(gdn, Hq, Hkv, d):
     check_attend(Hq, Hkv, d, 64, [(9000, 1, 1), (5, 1, 1), (4099, 1, 1)], seed=2)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,T,n", [(8, 1, 256, 3, 12000), (8, 1, 128, 6, 20000), (8, 1, 64, 10, 20000), (8, 1, 128, 16, 20000),
+                                          (1, 1, 64, 1, 20000), (8, 1, 128, 1, 20000), (4, 1, 256, 2, 12000), (8, 2, 128, 3, 9000)])
+def test_attend_row_cut_among_many_ctas(gdn, Hq, Hkv, d, T, n):
+    """A line long enough that one unit's parts are joined in more than one step, of one to four blocks of query rows; a
+    short row on either side."""
+    check_attend(Hq, Hkv, d, 32, [(40, T, T), (n, T, T), (7, 1, T)], seed=T)
+
+
 def test_attend_sharp_and_flat(gdn):
     """Scores far apart (one key takes all) and all equal (gain 0)."""
     for gain in (0.0, 12.0):

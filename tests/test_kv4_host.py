@@ -164,3 +164,19 @@ def test_reference_attend_is_softmax():
     _, v = cache.read(range(5))
     for i in range(5):
         assert np.allclose(out[i], v[:i + 1].mean(0))
+
+
+@pytest.mark.parametrize("what", ["table", "q_start", "q_count", "kv_len", "out"])
+def test_attend_names_what_is_not_a_tensor(what):
+    """Anything but a tensor is refused by its name, whatever else is wrong."""
+    torch = pytest.importorskip("torch")
+    dims = L.kv4_dims(2, 4, 2, 64, 16, 3, 6)
+    z = lambda *s, dtype=torch.int32: torch.zeros(*s, dtype=dtype)
+    a = dict(q=z(5, 4, 64, dtype=torch.bfloat16), pages=z(6 * 2 * 2 * 16 * 36, dtype=torch.uint8), table=z(2, 3), q_start=z(3),
+             q_count=z(2), kv_len=z(2), scale=0.125, out=z(5, 4, 64, dtype=torch.bfloat16), ws=z(16, dtype=torch.uint8), max_q=3)
+    with pytest.raises(TypeError, match=what):
+        L.gdn_kv4_attend(dims, **{**a, what: None})
+    with pytest.raises(ValueError, match="expected"):
+        L.gdn_kv4_attend(dims, **{**a, what: a[what][..., :1]})
+    with pytest.raises(ValueError, match="CUDA"):
+        L.gdn_kv4_attend(dims, **a)
