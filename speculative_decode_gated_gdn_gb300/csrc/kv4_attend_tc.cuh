@@ -227,7 +227,7 @@ __device__ __forceinline__ void tc_output(uint64_t kv, bool acc) {
   using S = TcShape<D>;
 #pragma unroll
   for (int ks = 0; ks < S::NK / 16; ++ks)
-    umma_f16_ts(0, S::kColS + BUF * S::NK + ks * 8,
+    umma_f16_ts(0, S::kColS + BUF * S::NK + (ks < S::NK / 32 ? 0 : S::NK / 4) + ks * 8,  // each half of P over its scores
                 kv + (((2 + BUF) * S::kKBytes + (ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4), umma_idesc_f16(kTcRows, D),
                 acc || ks > 0);
 }
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   constexpr int W = S::W, NK = S::NK;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t raw_full[kTcRing], raw_empty[kTcRing], unit_full[kTcUnits], unit_empty[kTcUnits];
-  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], m_full[2], pv_done[2];
+  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], x_full[4], pv_done[2];
   __shared__ uint64_t q_full, joined, drained;
   __shared__ TcUnit s_unit[kTcUnits];
   __shared__ uint32_t s_tmem;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     TcRow row;
     long long in_row, len;
   } s_at;  // the row that holds the CTA's first place
-  __shared__ float s_ref[kTcRows], s_sum[2][kTcRows], s_own[2][kTcRows];
+  __shared__ float s_top[2][2][kTcRows], s_sum[2][kTcRows];
   __shared__ float s_w[(kAttMaxCtas + kTcJoin - 1) / kTcJoin][kTcRows];  // weights of the parts of a join
   __shared__ uint32_t s_nan[2 * kTcRows], s_mx[2][kTcRows];
   __shared__ int s_flag, s_dead;
@@ -303,8 +303,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128), mbar_init(&v_full[i], 128);
       mbar_init(&k_empty[i], 1), mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&m_full[i], 128), mbar_init(&pv_done[i], 1);
+      mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 256), mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&x_full[i], 64);
     mbar_init(&q_full, 256), mbar_init(&joined, 256), mbar_init(&drained, 1);
     s_dead = 0;
     fence_mbar_init();
@@ -698,11 +699,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       }
     }
   } else if (role < 8) {
-    // ---- softmax: thread = query row, groups of 4 warps by the tile's parity -------------------
+    // ---- softmax: two threads a query row, half of a tile's keys a group of 4 warps -------------
     const uint32_t wg = role >> 2;
     const int r = rtid & 127;
     const uint32_t lane_base = uint32_t((role & 3) * 32) << 16;
     constexpr int kWords = D / 8;  // column e kWords + w of O is channel 8 w + e
+    constexpr int kHalf = NK / 2;  // keys of a tile that a group has
     float *parts = reinterpret_cast<float *>(static_cast<char *>(p.ws) + 4096);
     uint32_t *counters = reinterpret_cast<uint32_t *>(p.ws);
     uint32_t base = 0, joins = 0;
@@ -781,17 +783,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         }
       };
 #pragma unroll 1
-      for (int k = (base ^ wg) & 1; ok && k < n; k += 2) {
-        const uint32_t it = base + k, ph = (it >> 1) & 1;  // it & 1 == wg
-        ok = wait_warp(&s_full[wg], ph);
+      for (int k = 0; k < n; ++k) {
+        const uint32_t it = base + k, buf = it & 1;
+        ok = wait_warp(&s_full[buf], (it >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sc = lane_base + S::kColS + wg * NK;
-        const int t0 = (st0 + k) * NK;
-        const bool cut = t0 + NK > lim_min;
+        const uint32_t sc = lane_base + S::kColS + buf * NK + wg * kHalf;
+        const int t0 = (st0 + k) * NK + wg * kHalf;
+        const bool cut = t0 + kHalf > lim_min;
         float x = -INFINITY;
 #pragma unroll 1
-        for (int q = 0; q < NK / 32; ++q) {
+        for (int q = 0; q < kHalf / 32; ++q) {
           uint32_t a[32];
           tmem_ld32_async(sc + 32 * q, a);
           tmem_wait_ld();
@@ -806,31 +808,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           for (int e = 0; e < 32; e += 2) xs[(e >> 1) & 3] = max3(xs[(e >> 1) & 3], __uint_as_float(a[e]), __uint_as_float(a[e + 1]));
           x = fmaxf(max3(xs[0], xs[1], xs[2]), xs[3]);
         }
-        x *= f;
-        // the reference as the tile before left it
-        const float own = m;
-        if (k > 0) {
-          ok = wait_warp(&m_full[wg ^ 1], ((it - 1) >> 1) & 1);
-          if (!ok) break;
-          m = s_ref[r];
-        }
+        // the row's other half, by the warp of the other group with the same rows
+        s_top[buf][wg][r] = x;
+        mbar_arrive(&x_full[role & 3]);
+        ok = wait_warp(&x_full[role & 3], it & 1);
+        if (!ok) break;
+        x = fmaxf(x, s_top[buf][wg ^ 1][r]) * f;
         const bool move = x > m + 14.f;
         float a = 1.f;
         if (move) {
           const float to = fmaxf(m, x - 6.f);
           a = m == -INFINITY ? 0.f : ex2(m - to);
           m = to;
+          l *= a;
         }
-        if (own != m) l *= own == -INFINITY ? 0.f : ex2(own - m);
         if (k > 0 && __any_sync(0xffffffffu, move)) {
-          // every product before this tile's is in O.  (A wait names a phase by its
-          // parity, so the one before has to be over: this tile's scores were let go
-          // after the product of three tiles ago.)
-          ok = wait_warp(&pv_done[wg ^ 1], ((it - 1) >> 1) & 1);
+          // every product before this tile's is in O, half of whose columns a group
+          // rescales.  (A wait names a phase by its parity, so the one before has to be
+          // over: this tile's scores were let go after the product of two tiles ago.)
+          ok = wait_warp(&pv_done[buf ^ 1], ((it - 1) >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
+          for (int q = wg * (D / 64); q < (wg + 1) * (D / 64); ++q) {
             uint32_t o[32];
             tmem_ld32_async(lane_base + 32 * q, o);
             tmem_wait_ld();
@@ -841,15 +841,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           }
           tmem_wait_st();
         }
-        s_ref[r] = m;
-        tc_fence_before();
-        mbar_arrive(&m_full[wg]);
         const float r0 = m == -INFINITY ? 0.f : m;
         const F2 ff = f2(f, f), rr = f2(-r0, -r0);
         F2 ls[2] = {f2(l, 0.f), f2(0.f, 0.f)};
         // P's 16 columns of a chunk lie over scores that are read already
 #pragma unroll 1
-        for (int q = 0; q < NK / 32; ++q) {
+        for (int q = 0; q < kHalf / 32; ++q) {
           uint32_t b[32], w[16];
           tmem_ld32_async(sc + 32 * q, b);
           tmem_wait_ld();
@@ -875,19 +872,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           l = la + lb;
         }
         // the scores of this tile were let go after the values of two tiles ago
-        if (k > 1) look(k - 2);
+        if (k > 1 && buf == wg) look(k - 2);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[wg]);
+        mbar_arrive(&p_full[buf]);
       }
       if (!ok) break;
       // ---- the unit's rows, or a part of them: half of the words a group -----------------
       const uint32_t last_it = base + n - 1;
-      // The group of the last tile waits for its product, which ends after all
-      // others; the other group learns of it at `joined`.
-      if ((last_it & 1) == wg) ok = wait_warp(&pv_done[wg], (last_it >> 1) & 1);
+      ok = wait_warp(&pv_done[last_it & 1], (last_it >> 1) & 1);  // ends after all others
       if (!ok) break;
-      s_sum[wg][r] = l, s_own[wg][r] = m;
+      s_sum[wg][r] = l;
       s_nan[wg * kTcRows + r] = nan;
       mbar_arrive(&joined);
       ok = wait_warp(&joined, joins++ & 1);
@@ -896,13 +891,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       nan |= s_nan[(wg ^ 1) * kTcRows + r];
       if (n > 1) look(n - 2);  // neither group has looked at these two
       look(n - 1);
-      {
-        const float mo = s_own[wg ^ 1][r], lo = s_sum[wg ^ 1][r];
-        const float M = fmaxf(m, mo);  // the later tile's reference
-        const float ca = m == M ? 1.f : ex2(m - M), cb = mo == M ? 1.f : ex2(mo - M);
-        l = (l != l || m != -INFINITY ? l * ca : 0.f) + (lo != lo || mo != -INFINITY ? lo * cb : 0.f);
-        m = M;
-      }
+      l += s_sum[wg ^ 1][r];
       const bool whole = st0 == 0 && n == unit().stages;
       if (whole) {
         const float v = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
