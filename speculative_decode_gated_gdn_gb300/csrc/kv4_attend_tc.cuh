@@ -38,9 +38,9 @@
 // With Q and P in tensor memory the products read only K and V from shared
 // memory, so that a 64-key tile still feeds them at D = 256, where O takes half
 // of the tensor memory.
-// 2000 queries behind 16001 keys, 32 heads over 8 of 128: 617 us, 900 TFLOP/s of
-// the products; a prompt of 4096, 16 heads over 2 of 256: 189 us, 730 TFLOP/s
-// (back to back; 622 and 196 us with other work between the calls).
+// 2000 queries behind 16001 keys, 32 heads over 8 of 128: 615 us, 905 TFLOP/s of
+// the products; a prompt of 4096, 16 heads over 2 of 256: 191 us, 720 TFLOP/s
+// (back to back; 619 and 196 us with other work between the calls).
 //
 // Units are laid on one line in tiles of keys and cut evenly over a persistent
 // grid as in kv4_attend.cuh; causal tiles count as far as their last query sees.
