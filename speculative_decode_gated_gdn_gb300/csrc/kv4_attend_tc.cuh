@@ -27,7 +27,7 @@
 //
 // What bounds it: a tile is a chain (scores, their maximum, exponentials, output)
 // whose steps wait for one another, and the roles share the issue slots, which
-// are 55 % busy; the tensor cores work 28 % of the time.  A tile of 128 keys at D =
+// are 58 % busy; the tensor cores work 28 % of the time.  A tile of 128 keys at D =
 // 128 takes 2700 cycles where its products alone take 1090; with the dequant, the
 // exponentials and the maxima left out, 1790: what then is left is the products
 // and the barriers between them.  Neither separate columns for P (no
