@@ -535,8 +535,8 @@ int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, con
  * the table in 64 bits and round it once.  The channels from rot on are kept.
  * Codes are formed from the rotated fp32 keys: per group base = fp16(min), step =
  * fp16((max - min) / 15), code = clamp(round((y - base) / step), 0, 15).
- * Magnitudes over 65504 are held there; a group with an infinity or NaN reads
- * back as NaN.
+ * base and step are held within 65504 each (a level base + step * code may lie up
+ * to 16 * 65504 from zero); a group with an infinity or NaN reads back as NaN.
  *  q, k, v    bf16, token n at n * stride elements (stride a multiple of 8, at
  *             least heads * d), its heads densely packed: slices of one fused
  *             projection serve
@@ -580,6 +580,8 @@ size_t gdn_kv4_attend_workspace_bytes(const gdn_kv4_dims *dims, int N, int max_q
  * [q_start[b], q_start[b+1]) from q_count[b] on, and queries that see no key,
  * get zeros; tokens in no span are not written.  Keys behind a query's
  * position and places that no row holds are never used, whatever they hold.
+ * Keys and values count as what their entries stand for, also where a level
+ * passes fp16's 65504 (such groups are slow).
  *  q, out     [N][H_q][d] bf16 (rotated queries; out may not overlap q)
  *  table, q_start, q_count, kv_len  as gdn_kv_plan leaves them
  *  max_q      the largest span of a row (the host's bound; 1 for plain decoding)

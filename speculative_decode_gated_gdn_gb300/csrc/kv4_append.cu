@@ -13,7 +13,8 @@
 //   code = clamp(round_half_even((y - base) / step), 0, 15), 0 where step is 0
 // from the fp32 rotated value; min, max and the step are exact or rounded once
 // in fp32 before fp16.  A group that holds an infinity or NaN reads back as
-// NaN; magnitudes over 65504 are held at 65504.
+// NaN; base and step are held within 65504 each, so that a level base + step *
+// code may lie up to 16 * 65504 from zero.
 //
 // Both kernels move each byte once: 8 channels a lane (16 bytes of bf16, one
 // 32-bit word of codes), a head on D / 8 lanes, the loads of the next heads on

@@ -176,6 +176,11 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -187,6 +192,58 @@ __device__ __forceinline__ uint32_t att_even(uint32_t x, uint32_t step, uint32_t
 }
 __device__ __forceinline__ uint32_t att_odd(uint32_t x, uint32_t step, uint32_t base) {
   return h2_fma(h2_fma((x & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u), step, base);
+}
+
+// Wide groups.  A step and a base are finite fp16 numbers, but the levels base + step *
+// code lie anywhere up to 16 * 65504, and one that passes fp16 would enter a product as
+// an infinity, which even a query that does not see the key would meet, as 0 * infinity.
+// So every entry's top level is formed (one product and sum for two entries), and the
+// groups that do not fit in fp16 go another way.  Ordinary caches pay 2 % for it on the
+// tensor cores and 2 to 3 % with few rows (64 ragged rows of 8192 keys at D = 128: 105.3
+// us without the look, 108.9 with it).
+constexpr uint32_t kH2Fifteen = 0x4b804b80u, kH2Sixteenth = 0x2c002c00u;
+
+// `nil` with the top levels of two entries looked at: what is not 0 (signs aside) in the
+// end tells that one of them is wide, or not finite.
+__device__ __forceinline__ uint32_t att_look(uint32_t steps, uint32_t bases, uint32_t nil) {
+  return h2_fma(h2_fma(steps, kH2Fifteen, bases), 0u, nil);  // an infinity or NaN leaves a NaN
+}
+__device__ __forceinline__ bool att_found(uint32_t nil) { return (nil & 0x7fff7fffu) != 0; }
+
+// The entry is wide, or not finite.
+__device__ __forceinline__ bool att_not_fp16(uint32_t entry) {
+  return att_found(att_look(__byte_perm(entry, entry, 0x1010), __byte_perm(entry, entry, 0x3232), 0u));
+}
+__device__ __forceinline__ bool att_wide(uint32_t entry) { return att_not_fp16(entry) && !att_not_finite(entry); }
+
+// Where the cache holds token t of row b for head hk, the record's part `off` bytes from
+// its start with `bytes` bytes a token; NULL where the page is outside the cache.  t is
+// less than the row's length.
+__device__ __forceinline__ const uint8_t *att_place(const Kv4AttendParams &p, int b, int hk, int t, int off, int bytes) {
+  const int page = p.table[size_t(b) * p.g.max_pages + (t >> p.g.log2P)];
+  if (page < 0 || page >= p.g.n_pages) return nullptr;
+  return p.pages + (size_t(page) * p.g.H_kv + hk) * kv4_record_bytes(p.g.D, 1 << p.g.log2P) + off +
+         (t & ((1 << p.g.log2P) - 1)) * bytes;
+}
+
+// q . k of token t in fp32.  Few tokens of few caches come here, so it is kept short, not
+// fast.
+template <int D>
+static __device__ __noinline__ float att_dot(const Kv4AttendParams &p, int b, int hk, int t, const uint16_t *q) {
+  constexpr int W = D / 64;
+  const int P = 1 << p.g.log2P;
+  const uint8_t *codes = att_place(p, b, hk, t, 0, D / 2), *entries = att_place(p, b, hk, t, 2 * kv4_code_bytes(D, P), W * 4);
+  if (!codes) return 0.f;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int w = 0; w < D / 8; ++w) {
+    const uint32_t e = reinterpret_cast<const uint32_t *>(entries)[w % W];
+    const uint32_t c = reinterpret_cast<const uint32_t *>(codes)[w];
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+      sum = fmaf(__uint_as_float(uint32_t(q[8 * w + i]) << 16), fmaf(half_lo(e), float(c >> (4 * i) & 15u), half_hi(e)), sum);
+  }
+  return sum;
 }
 
 // One row's part of the line of stages.
@@ -563,6 +620,27 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
         dead = __any_sync(0xffffffffu, dead);
         phases ^= 1u << slot;
       }
+      // ---- wide groups among the stage's keys (1) and values (2): a lane has kOwn of the
+      // entries of each -----------------------------------------------------------------
+      uint32_t wide;
+      {
+        constexpr int kOwn = ST * W / 32;
+        const int key = lane * kOwn / W, off = key & (pt - 1);
+        const uint8_t *at = ring + slot * S::kStage + (key >> log2pt) * rec_s + 2 * rec_c + off * (W * 4);
+        uint32_t ke[kOwn], ve[kOwn], kn = 0, vn = 0;
+        att_words<kOwn>(ke, at), att_words<kOwn>(ve, at + rec_e);
+        if (st * ST + ST > lim_max) {  // places behind the last key hold anything
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i)
+            if (st * ST + key + i / W >= lim_max) ke[i] = ve[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; i += 2) {
+          kn = att_look(__byte_perm(ke[i], ke[i + 1], 0x5410), __byte_perm(ke[i], ke[i + 1], 0x7632), kn);
+          vn = att_look(__byte_perm(ve[i], ve[i + 1], 0x5410), __byte_perm(ve[i], ve[i + 1], 0x7632), vn);
+        }
+        wide = (__any_sync(0xffffffffu, att_found(kn)) ? 1u : 0u) | (__any_sync(0xffffffffu, att_found(vn)) ? 2u : 0u);
+      }
 #pragma unroll 1
      for (int ck = 0; ck < ST && st * ST + ck < lim_max; ck += S::CK) {
       const int t_base = st * ST + ck;
@@ -575,6 +653,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
         codes[h] = rec + off * (D / 2), entries[h] = rec + 2 * rec_c + off * (W * 4);
       }
       const bool cut = t_base + S::CK > lim_min;  // some query does not see all of them
+      const bool care = cut || wide != 0;
 
       // ---- scores, and their maximum ----------------------------------------------
       float s[NT][2], top = -INFINITY;
@@ -618,12 +697,35 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
         }
         top = max3(top, s[u][0], s[u][1]);
       }
+      if (__builtin_expect(wide & 1, 0)) {
+        // of wide keys the two sums step * (q . code) and base * sum(q) may be so large that
+        // nothing is left of their difference in fp32: those scores are formed anew
+        const uint16_t *query = p.q + (size_t(row.start + at) * p.g.H_q + cur.hk * G + rn - at * G) * D;
+#pragma unroll 1
+        for (int i = 0; i < 2 * NT; ++i) {
+          const int key = ck + 8 * (i >> 1) + att_key(2 * j + (i & 1)), t = st * ST + key;
+          if (!live || t >= lim) continue;
+          uint32_t e[W];
+          att_words<W>(e, ring + slot * S::kStage + (key >> log2pt) * rec_s + 2 * rec_c + (key & (pt - 1)) * (W * 4));
+          bool any = false;
+#pragma unroll
+          for (int g = 0; g < W; ++g) any = any || att_wide(e[g]);
+          if (!any) continue;
+          const float x = att_dot<D>(p, cur.b, cur.hk, t, query) * (p.scale * 1.4426950408889634f / f);
+#pragma unroll
+          for (int k = 0; k < 2 * NT; ++k)
+            if (k == i) s[k >> 1][k & 1] = x;
+        }
+        top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) top = max3(top, s[u][0], s[u][1]);
+      }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
       top *= f;
-      if (__any_sync(0xffffffffu, top > m + 14.f)) {
+      if (__any_sync(0xffffffffu, top > m + (wide & 2 ? 10.f : 14.f))) {
         const float to = fmaxf(m, top - 6.f), a = to == m ? 1.f : ex2(m - to);
         m = to;
         l2 = f2_mul(l2, f2(a, a));
@@ -632,7 +734,11 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
 #pragma unroll
         for (int i = 0; i < S::kRegs / 4; ++i) o_acc[i][0] *= ca, o_acc[i][1] *= cb, o_acc[i][2] *= ca, o_acc[i][3] *= cb;
       }
-      const float r0 = m == -INFINITY ? 0.f : -m;
+      float r0 = m == -INFINITY ? 0.f : -m;
+      // wide values are formed as sixteenths, which always fit, and all values of their
+      // stage with them (they keep 16 * 2^-25 of absolute precision): sixteen times the
+      // probabilities, and the sums until the chunk's end
+      if (wide & 2) r0 += 4.f, l2 = f2_mul(l2, f2(16.f, 16.f));
 
       // ---- probabilities and output, 16 keys at a time --------------------------------
 #pragma unroll
@@ -650,16 +756,22 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
           uint32_t wa[W], wb[W];
           att_words<W>(wa, entries[h] + rec_e + lane_e0 + half * (32 * W));
           att_words<W>(wb, entries[h] + rec_e + lane_e1 + half * (32 * W));
-          if (cut) {
-            // a value that one query sees and another does not must not reach
-            // the other as 0 * NaN: it is left out and remembered by the row
+          if (care) {
+            if (cut) {
+              // a value that one query sees and another does not must not reach
+              // the other as 0 * NaN: it is left out and remembered by the row
 #pragma unroll
-            for (int g = 0; g < W; ++g) {
-              const int ta = t_base + ka, tb = t_base + kb;
-              if (att_not_finite(wa[g])) nan |= uint32_t(ta < lim) << g, wa[g] = 0;
-              if (att_not_finite(wb[g])) nan |= uint32_t(tb < lim) << g, wb[g] = 0;
-              if (ta >= lim_max) wa[g] = 0;
-              if (tb >= lim_max) wb[g] = 0;
+              for (int g = 0; g < W; ++g) {
+                const int ta = t_base + ka, tb = t_base + kb;
+                if (att_not_finite(wa[g])) nan |= uint32_t(ta < lim) << g, wa[g] = 0;
+                if (att_not_finite(wb[g])) nan |= uint32_t(tb < lim) << g, wb[g] = 0;
+                if (ta >= lim_max) wa[g] = 0;
+                if (tb >= lim_max) wb[g] = 0;
+              }
+            }
+            if (wide & 2) {
+#pragma unroll
+              for (int g = 0; g < W; ++g) wa[g] = h2_mul(wa[g], kH2Sixteenth), wb[g] = h2_mul(wb[g], kH2Sixteenth);
             }
           }
 #pragma unroll
@@ -689,6 +801,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
           }
         }
       }
+      if (wide & 2) l2 = f2_mul(l2, f2(0.0625f, 0.0625f));
      }
       __syncwarp();  // every lane is done with the slot
       slot = slot + 1 == S::kSlots ? 0 : slot + 1;

@@ -14,6 +14,10 @@
 //            for 50.6);
 //   output   O += P V, P from tensor memory; O is rescaled only when a
 //            probability passes 2^14.
+// Entries whose levels pass fp16 (kv4_attend.cuh, "Wide groups") are noted by their key.
+// In K they spoil the key's own column of scores, which is formed anew before the
+// maximum; from V they are left out, and the rows that see the key add them to O when
+// the unit's products are done.
 // A product does not see the order of its inner dimension, nor O's columns the
 // order they are kept in, so both follow what shared memory likes:
 //  - inside 8 channels 0 4 1 5 2 6 3 7 (the order masks take codes out of a word);
@@ -53,7 +57,7 @@ namespace gdn {
 
 constexpr int kTcRows = 128;
 // Roles by `role` = (warp + 16) mod 20: 0-7 softmax, 8-11 K, 12-15 V, 16 products,
-// 17 copies, 18 units, 19 none.  The products' warp is the oldest of its
+// 17 copies, 18 units, 19 wide keys.  The products' warp is the oldest of its
 // scheduler, which seems to favour the oldest ready one (a prompt of 4096 at
 // D = 256: 242 us with it as the youngest, 227 so).
 constexpr int kTcThreads = 640;
@@ -271,6 +275,83 @@ static __device__ __noinline__ long long tc_scan(long long v, long long *s_warp,
   return before + x - v;
 }
 
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  float v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr));
+  tmem_wait_ld();
+  return v;
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(v) : "memory");
+  tmem_wait_st();
+}
+
+// A softmax thread's query row: its query (NULL: none) and the keys it sees.
+struct TcQuery {
+  const uint16_t *q;
+  int lim;
+};
+template <int D>
+static __device__ TcQuery tc_query(const Kv4AttendParams &p, const TcUnit &u) {
+  const int G = p.g.H_q / p.g.H_kv, TT = kTcRows / G, r = (threadIdx.x - 128) & 127, i = u.tile * TT + r / G;
+  if (r >= TT * G || i >= u.count) return TcQuery{nullptr, 0};
+  return TcQuery{p.q + (size_t(u.start + i) * p.g.H_q + u.hk * G + r % G) * D, max(0, u.len - u.count + i + 1)};
+}
+
+// The scores of a tile's wide keys (bits), formed anew for a softmax warp's rows and half
+// of the tile, which starts with key t0; in the columns from sc on, in units of f.
+template <int D>
+static __device__ __noinline__ void tc_new_scores(const Kv4AttendParams &p, const TcUnit &u, const uint32_t *keys, int t0, float f,
+                                                  uint32_t sc) {
+  const TcQuery row = tc_query<D>(p, u);
+#pragma unroll 1
+  for (int e = 0; e < TcShape<D>::NK / 2; ++e) {
+    if (!(keys[e >> 5] >> (e & 31) & 1u)) continue;
+    const float x = row.q && t0 + e < row.lim ? att_dot<D>(p, u.b, u.hk, t0 + e, row.q) * (p.scale * 1.4426950408889634f / f) : 0.f;
+    __syncwarp();
+    tmem_st1(sc + e, x);
+  }
+}
+
+// The wide groups' part of O, of the unit's keys [t0, t1), weighted against a row's
+// reference m, for a softmax warp's rows: its half of the words of O's columns, or
+// (blocks) of the columns themselves.
+template <int D>
+static __device__ __noinline__ void tc_add_values(const Kv4AttendParams &p, const TcUnit &u, int t0, int t1, float m, bool blocks) {
+  constexpr int W = D / 64, kWords = D / 8;
+  const TcQuery row = tc_query<D>(p, u);
+  const int lane = threadIdx.x & 31, P = 1 << p.g.log2P, half = (threadIdx.x - 128) >> 7, b = u.b, hk = u.hk;
+  const uint32_t tmem = (threadIdx.x & 96) << 16;
+#pragma unroll 1
+  for (int t = t0; t < t1; t += 32) {
+    uint32_t groups = 0;  // wide ones of the lane's key
+    if (t + lane < t1) {
+      const uint8_t *e = att_place(p, b, hk, t + lane, 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P), W * 4);
+      for (int g = 0; e && g < W; ++g) groups |= uint32_t(att_wide(reinterpret_cast<const uint32_t *>(e)[g])) << g;
+    }
+    uint32_t keys = __ballot_sync(0xffffffffu, groups != 0);
+#pragma unroll 1
+    for (; keys; keys &= keys - 1) {
+      const int k = __ffs(keys) - 1;
+      const uint32_t of = __shfl_sync(0xffffffffu, groups, k);
+      const uint8_t *codes = att_place(p, b, hk, t + k, kv4_code_bytes(D, P), D / 2);
+      const uint8_t *entries = att_place(p, b, hk, t + k, 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P), W * 4);
+      float weight = 0.f;
+      if (row.q && t + k < row.lim && m != -INFINITY)
+        weight = ex2(att_dot<D>(p, b, hk, t + k, row.q) * (p.scale * 1.4426950408889634f) - m);
+      __syncwarp();
+#pragma unroll 1
+      for (int col = blocks ? half * (D / 2) : 0; col < (blocks ? (half + 1) * (D / 2) : D); ++col) {
+        const int w = col % kWords, e = col / kWords;  // channel 8 w + e
+        if (!(of >> (w % W) & 1u) || (!blocks && w / (kWords / 2) != half)) continue;
+        const uint32_t entry = reinterpret_cast<const uint32_t *>(entries)[w % W];
+        const float code = float(reinterpret_cast<const uint32_t *>(codes)[w] >> (4 * e) & 15u);
+        tmem_st1(tmem + col, fmaf(weight, fmaf(half_lo(entry), code, half_hi(entry)), tmem_ld1(tmem + col)));
+      }
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_constant__ Kv4AttendParams p) {
   using S = TcShape<D>;
@@ -291,9 +372,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   __shared__ float s_w[(kAttMaxCtas + kTcJoin - 1) / kTcJoin][kTcRows];  // weights of the parts of a join
   __shared__ uint32_t s_nan[2 * kTcRows], s_mx[2][kTcRows];
   __shared__ int s_flag, s_dead;
-  // keys of a V tile with a value that is not finite, per group; of four tiles,
-  // since the rows look two tiles later
+  // keys of a V tile with a group that is not finite or wide, per group; of four tiles,
+  // since the rows look two tiles later; and keys of a K tile with a wide group
   __shared__ __align__(16) uint32_t s_bad[4][NK / 32 * W];
+  __shared__ uint32_t s_keys[4][NK / 32], s_some[4];
   const int tid = threadIdx.x, lane = tid & 31;
   const int role = ((tid >> 5) + 16) % 20, rtid = role * 32 + lane;  // and the thread's place among the roles'
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -301,10 +383,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   const int G = p.g.H_q / p.g.H_kv, Hkv = p.g.H_kv, TT = kTcRows / G;
   const int P = 1 << p.g.log2P;
   if (tid == 0) {
-    for (int i = 0; i < kTcRing; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 8);
-    for (int i = 0; i < kTcUnits; ++i) mbar_init(&unit_full[i], 1), mbar_init(&unit_empty[i], 18);
+    for (int i = 0; i < kTcRing; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 9);
+    for (int i = 0; i < kTcUnits; ++i) mbar_init(&unit_full[i], 1), mbar_init(&unit_empty[i], 19);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 128), mbar_init(&v_full[i], 128);
+      mbar_init(&k_full[i], 129), mbar_init(&v_full[i], 128);
       mbar_init(&k_empty[i], 1), mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 256), mbar_init(&pv_done[i], 1);
     }
@@ -314,6 +396,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
     fence_mbar_init();
   }
   for (int i = tid; i < 4 * (NK / 32) * W; i += kTcThreads) (&s_bad[0][0])[i] = 0;
+  if (tid < 4) s_some[tid] = 0;
   pdl_wait();
   pdl_trigger();
 
@@ -596,28 +679,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
             for (int k = 0; k < 8; ++k)
               if ((k ^ swap) >= left) e[k] = 0;
           }
-          // values that are not finite are left out here and put back by the rows
-          // that see their key: the thread of the group's first word notes them
-          uint32_t nil = 0;
+          uint32_t es[4], eb[4], nil = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) nil = h2_fma(e[k], 0u, nil);  // an infinity or NaN leaves a NaN
+          for (int k = 0; k < 4; ++k) {
+            es[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel0);
+            eb[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel1);
+            nil = att_look(es[k], eb[k], nil);
+          }
+          // values that are not finite, or wide, are left out here and put back by the rows
+          // that see their key: the thread of the group's first word notes them
           const bool was = had >> ((it & 3) * kTasks + i) & 1u;
-          if ((nil & 0x7fff7fffu) != 0 || was) {
+          if (att_found(nil) || was) {
             uint32_t bad = 0;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              if (att_not_finite(e[k])) bad |= 1u << (k ^ swap), e[k] = 0;
+              if (att_not_fp16(e[k])) bad |= 1u << (k ^ swap), e[k] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              es[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel0);
+              eb[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel1);
+            }
             if (word < W) {
               uint32_t *flag = &s_bad[it & 3][(chunk >> 2) * W + word];
               atomicAnd(flag, ~(0xffu << ((chunk & 3) * 8)));
               if (bad) atomicOr(flag, bad << ((chunk & 3) * 8)), noted |= 1u << i;
             }
-          }
-          uint32_t es[4], eb[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            es[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel0);
-            eb[k] = __byte_perm(e[2 * k], e[2 * k + 1], sel1);
           }
           uint8_t *dst = vb + to + i * to_step;
 #pragma unroll
@@ -701,6 +787,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (lane == 0) mbar_arrive(&raw_empty[slot]);
       }
     }
+  } else if (role == 19) {
+    // ---- wide keys: the entries of NK / 32 keys a lane, noted as the tile's K is formed -------
+    constexpr int kKeys = NK / 32, kOwn = kKeys * W;
+    const int key = lane * kKeys, off = key & (P - 1);
+    const int at = (key >> p.g.log2P) * kv4_record_bytes(D, P) + 2 * kv4_code_bytes(D, P) + off * (W * 4);
+    uint32_t had = 0;  // bit tile % 4: some key is noted
+    uint32_t it = 0;
+    bool ok = true;
+    while (next_unit(ok)) {
+      const int st1 = unit().st1;
+#pragma unroll 1
+      for (int st = unit().st0; ok && st < st1; ++st, ++it) {
+        const uint32_t buf = it & 1, slot = it % kTcRing, of = 1u << (it & 3);
+        ok = wait_warp(&k_empty[buf], ((it >> 1) & 1) ^ 1) && wait_warp(&raw_full[slot], it / kTcRing & 1);
+        if (!ok) break;
+        const uint32_t *e = reinterpret_cast<const uint32_t *>(ring + slot * S::kRaw + at);
+        uint32_t nil = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; i += 4) {
+          uint32_t x[4];
+          att_words<4>(x, reinterpret_cast<const uint8_t *>(e + i));
+          nil = att_look(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632), nil);
+          nil = att_look(__byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632), nil);
+        }
+        if (__any_sync(0xffffffffu, att_found(nil)) || (had & of)) {
+          uint32_t keys = 0, any = 0;
+#pragma unroll 1
+          for (int i = 0; i < kOwn; ++i) keys |= uint32_t(att_wide(e[i])) << (i / W);
+#pragma unroll 1
+          for (int w = 0; w < NK / 32; ++w) {
+            const uint32_t note = __reduce_or_sync(0xffffffffu, key >> 5 == w ? keys << (key & 31) : 0u);
+            if (lane == 0) s_keys[it & 3][w] = note;
+            any |= note;
+          }
+          if (lane == 0) s_some[it & 3] = any;
+          had = any ? had | of : had & ~of;
+          __syncwarp();
+        }
+        if (lane == 0) {
+          mbar_arrive(&k_full[buf]);
+          mbar_arrive(&raw_empty[slot]);
+        }
+      }
+    }
   } else if (role < 8) {
     // ---- softmax: two threads a query row, half of a tile's keys a group of 4 warps -------------
     const uint32_t wg = role >> 2;
@@ -768,7 +898,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       }
       float m = -INFINITY, l = 0.f;
       uint32_t nan = 0;
-      // values that are not finite reach the rows that see their key
+      // values that are not finite reach the rows that see their key; wide ones (bit 31)
+      // are added to what the products leave in O
       auto look = [&](int k) {  // tile k of the unit
         const uint32_t *bad = s_bad[(base + k) & 3];
         uint32_t any = 0;
@@ -780,8 +911,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         if (any) {
 #pragma unroll 1
           for (int g = 0; g < NK / 32 * W; ++g) {
-            const int left = lim - (st0 + k) * NK - 32 * (g / W);
-            if (left > 0 && (bad[g] & (left >= 32 ? 0xffffffffu : (1u << left) - 1))) nan |= 1u << (g % W);
+            const int t = (st0 + k) * NK + 32 * (g / W), left = lim - t;
+            uint32_t seen = left <= 0 ? 0u : bad[g] & (left >= 32 ? 0xffffffffu : (1u << left) - 1);
+#pragma unroll 1
+            for (; seen; seen &= seen - 1) {
+              const uint8_t *e = att_place(p, unit().b, unit().hk, t + __ffs(seen) - 1, 2 * kv4_code_bytes(D, P) + kv4_entry_bytes(D, P), W * 4);
+              if (e) nan |= att_not_finite(reinterpret_cast<const uint32_t *>(e)[g % W]) ? 1u << (g % W) : 1u << 31;
+            }
           }
         }
       };
@@ -794,6 +930,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
         const uint32_t sc = lane_base + S::kColS + buf * NK + wg * kHalf;
         const int t0 = (st0 + k) * NK + wg * kHalf;
         const bool cut = t0 + kHalf > lim_min;
+        if (__builtin_expect(s_some[it & 3] != 0, 0))
+          tc_new_scores<D>(p, unit(), s_keys[it & 3] + wg * (kHalf / 32), t0, f, sc);
         float x = -INFINITY;
 #pragma unroll 1
         for (int q = 0; q < kHalf / 32; ++q) {
@@ -896,6 +1034,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       look(n - 1);
       l += s_sum[wg ^ 1][r];
       const bool whole = st0 == 0 && n == unit().stages;
+      if (__any_sync(0xffffffffu, nan >> 31)) {
+        tc_add_values<D>(p, unit(), st0 * NK, min(unit().st1 * NK, tile_lim), m, !whole);
+        nan &= 0x7fffffffu;
+      }
       if (whole) {
         const float v = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
         uint16_t *dst = p.out + (size_t(tok) * p.g.H_q + head) * D;
