@@ -79,6 +79,10 @@ struct AttShape {
 // so many, on whichever device it is used.
 constexpr int kAttMaxCtas = 160;
 
+// Least factor of a score: 0 would make NaN of a masked key's -infinity; with this one
+// every score that the products can give is as good as 0.
+constexpr float kLeastFactor = 1.17549435e-38f;
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
       // the largest magnitude goes to [2^10, 2^11)
       const int e = min(max(int(mx >> 7), 20), 240);
       const float s2 = __uint_as_float(uint32_t(264 - e) << 23), up = s2 * sign;
-      f *= 1.f / s2;
+      f = fmaxf(f * (1.f / s2), kLeastFactor);
 #pragma unroll
       for (int g = 0; g < W; ++g) qs[g] = 0.f;
 #pragma unroll

@@ -881,6 +881,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           up *= s2;
           f *= 1.f / s2;
         }
+        f = fmaxf(f, kLeastFactor);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t a[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
