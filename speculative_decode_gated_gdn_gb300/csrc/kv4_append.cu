@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const Kv4
   if (n >= p.N) return;  // whole warps
   const int heads = p.H_q + 2 * p.H_kv;
   const int per = (heads + splits - 1) / splits;
-  const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
+  const int h1 = min(heads, int(blockIdx.y + 1) * per);
+  int h0 = blockIdx.y * per;
   // the loads of kAhead heads are on their way together, the next ones' and the
   // angles' while these are worked on
   constexpr int kAhead = 2;
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const Kv4
   const int half = p.rot >> 1;
   const bool turned = 8 * chunk < p.rot;
   float cs[8], sn[8];
+  uint32_t still = 0;  // channels whose position is outside the table: they do not turn
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     cs[e] = 1.f, sn[e] = 0.f;
@@ -165,9 +167,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const Kv4
       if (pos >= 0 && pos < p.max_pos) {
         const float2 t = __ldg(p.rope + size_t(pos) * half + i);
         cs[e] = t.x, sn[e] = t.y;
-      } else if (slot >= 0) {
-        write = false;
-        atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+      } else {
+        still |= 1u << e;
+        if (slot >= 0) {
+          write = false;
+          atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+        }
       }
     }
   }
@@ -177,6 +182,49 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const Kv4
   if (!p.pairs && 8 * chunk < half) {  // the lower half takes the partner's product away
 #pragma unroll
     for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+  }
+  auto turn = [&](const uint4 raw, float (&y)[8], bool rotate) {  // the whole warp
+    if (p.pairs) {
+      if (rotate) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float a = y[e], b = y[e + 1];
+          y[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+          y[e + 1] = __fadd_rn(__fmul_rn(b, cs[e + 1]), __fmul_rn(a, sn[e + 1]));
+        }
+      }
+    } else {
+      uint4 o;
+      o.x = __shfl_sync(0xffffffffu, raw.x, partner);
+      o.y = __shfl_sync(0xffffffffu, raw.y, partner);
+      o.z = __shfl_sync(0xffffffffu, raw.z, partner);
+      o.w = __shfl_sync(0xffffffffu, raw.w, partner);
+      if (rotate) {
+        float z[8];
+        unpack8(o, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), __fmul_rn(z[e], sn[e]));
+      }
+    }
+  };
+  // A token some of whose positions are outside the table: its queries one load at a time.
+  // (Times 1 plus times 0 would not do: an infinity in the pair, a zero's sign.)
+  if (__any_sync(0xffffffffu, still != 0)) {
+#pragma unroll 1
+    for (; h0 < min(h1, p.H_q); h0 += HPW) {
+      const int h = h0 + sub;
+      const bool in = h < min(h1, p.H_q);
+      const uint4 raw = in ? ld_stream_u4(p.q + n * p.q_stride + size_t(h) * D + 8 * chunk) : make_uint4(0, 0, 0, 0);
+      float x[8], y[8];
+      unpack8(raw, x), unpack8(raw, y);
+      turn(raw, y, turned);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (still >> e & 1u) y[e] = x[e];
+      if (in) *reinterpret_cast<uint4 *>(p.q_out + (size_t(n) * p.H_q + h) * D + 8 * chunk) = turned ? pack8(y) : raw;
+    }
+    h0 = max(int(blockIdx.y) * per, min(h1, p.H_q));
+    load(h0);
   }
 #pragma unroll 1
   for (int hb = h0; hb < h1; hb += kAhead * HPW) {
@@ -193,30 +241,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv4_append_kernel(const Kv4
       const uint4 raw = now[u];
       float y[8];
       unpack8(raw, y);
-      if (p.rot) {  // every lane takes part in the exchange
-        if (p.pairs) {
-          if (turned && kind < 2) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float a = y[e], b = y[e + 1];
-              y[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
-              y[e + 1] = __fadd_rn(__fmul_rn(b, cs[e + 1]), __fmul_rn(a, sn[e + 1]));
-            }
-          }
-        } else {
-          uint4 o;
-          o.x = __shfl_sync(0xffffffffu, raw.x, partner);
-          o.y = __shfl_sync(0xffffffffu, raw.y, partner);
-          o.z = __shfl_sync(0xffffffffu, raw.z, partner);
-          o.w = __shfl_sync(0xffffffffu, raw.w, partner);
-          if (turned && kind < 2) {
-            float z[8];
-            unpack8(o, z);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), __fmul_rn(z[e], sn[e]));
-          }
-        }
-      }
+      if (p.rot) turn(raw, y, turned && kind < 2);
       if (in && kind == 0)
         *reinterpret_cast<uint4 *>(p.q_out + (size_t(n) * p.H_q + h) * D + 8 * chunk) = turned ? pack8(y) : raw;
       // the groups' exchanges need every lane of a head, so the whole warp goes in
