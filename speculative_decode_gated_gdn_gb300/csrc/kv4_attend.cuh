@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
   auto look = [&](const AttPiece &u, int st) {
     const int k = lane / n_cells, t = (st + k) * ST + ((lane - k * n_cells) << p.g.log2P);
     cells_st = st;
-    cells = k < kBatch && st + k < u.st_hi && t < u.lim_max ? p.table[size_t(u.b) * p.g.max_pages + (t >> p.g.log2P)] : -2;
+    // (-2: there is no such cell; a negative one of the table is -1)
+    cells = k < kBatch && st + k < u.st_hi && t < u.lim_max ? max(-1, p.table[size_t(u.b) * p.g.max_pages + (t >> p.g.log2P)]) : -2;
   };
   auto issue = [&](const AttPiece &u, int st) {
     const int k = (st - cells_st) * n_cells + (half_page ? 0 : lane);

@@ -544,9 +544,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       const int lim = tc_limit(unit(), unit().tile, TT), st1 = unit().st1;
       const int32_t *table = p.table + size_t(unit().b) * p.g.max_pages;
       const uint8_t *head = p.pages + size_t(unit().hk) * rec_bytes;
-      auto page_of = [&](int st) -> int {  // lane l: page l of the tile
+      auto page_of = [&](int st) -> int {  // lane l: page l of the tile, -2: none; a negative one is -1
         const int t = st * NK + (lane << p.g.log2P);
-        return lane < n_sub && st < st1 && t < lim ? table[t >> p.g.log2P] : -2;
+        return lane < n_sub && st < st1 && t < lim ? max(-1, table[t >> p.g.log2P]) : -2;
       };
       int next = page_of(unit().st0);
 #pragma unroll 1

@@ -5,7 +5,7 @@ import torch
 
 from speculative_decode_gated_gdn_gb300 import lib as L
 from tests import kv4_ref as R
-from tests.test_kv4_gpu import append_case, bits, run_append
+from tests.test_kv4_gpu import append_case, attend_case, bits, run_append, run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,16 @@ def test_position_outside_does_not_turn(gdn, d, rot, pairs):
     for c in (a, b):
         want[..., c[1::2]] = q[..., c[1::2]]
     assert torch.equal(bits(q_out), bits(R.bf16(want)))
+
+
+@pytest.mark.parametrize("T", [2, 70])
+@pytest.mark.parametrize("cell", [-1, -2, -3, -(1 << 31)])
+def test_attend_negative_cell_raises_status(gdn, T, cell):
+    """Any negative cell where a row has keys is a page outside the cache; not a bit of the other row changes."""
+    cache, table, q_start, q_count, kv_len, q = attend_case(8, 2, 128, 16, [(100, T, T), (80, T, T)], seed=1)
+    good, *_ = run_attend(cache, table, q_start, q_count, kv_len, q, 0.1, T)
+    assert L.gdn_get_status(clear=True) == 0
+    table[0, 3] = cell
+    out, *_ = run_attend(cache, table, q_start, q_count, kv_len, q, 0.1, T)
+    assert L.gdn_get_status(clear=True) == L.GDN_STATUS_BAD_INDEX
+    assert torch.equal(bits(out[T:]), bits(good[T:]))
