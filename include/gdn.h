@@ -154,8 +154,9 @@ typedef uint16_t gdn_bf16; /* bfloat16 bit pattern */
  * flagged verify also takes 32 tensor-memory columns per CTA before that
  * wait; so the kernel that precedes it on the stream must not be one that,
  * after letting its dependents start, allocates tensor memory and needs more
- * than 416 of an SM's 512 columns (no kernel of this library does).  It is
- * always safe to omit. */
+ * than 416 of an SM's 512 columns (no kernel of this library does: the
+ * prefill's state pass and gdn_kv4_attend take all 512, but before they let
+ * the next kernel start).  It is always safe to omit. */
 #define GDN_VERIFY_OVERLAP 0x100
 
 /* A weaker flag for the first layer of a cycle after a DEFERRED gdn_commit

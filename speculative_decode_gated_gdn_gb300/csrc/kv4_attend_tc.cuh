@@ -398,7 +398,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   for (int i = tid; i < 4 * (NK / 32) * W; i += kTcThreads) (&s_bad[0][0])[i] = 0;
   if (tid < 4) s_some[tid] = 0;
   pdl_wait();
-  pdl_trigger();
 
   // ---- this CTA's piece of the line --------------------------------------------------
   // rows beyond the CTA's threads are summed first and looked at again below
@@ -444,6 +443,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // The next kernel starts only now: a flagged verify takes tensor memory before its wait,
+  // and one that came before the allocation above would wait for this kernel and it for
+  // the verify.
+  pdl_trigger();
   // a bounded wait of the whole warp; false once any wait of the CTA has run out
   auto wait_warp = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;

@@ -958,10 +958,10 @@ __global__ void __launch_bounds__(kStThreads, 1) prefill_state_tc_kernel(const P
     s_fail = 0;
   }
   pdl_wait();
-  pdl_trigger();
   // tensor memory is taken only after the wait: no CTA holds it while it
   // waits for another grid, so an allocation never waits on a CTA that is
-  // itself waiting for the allocating grid
+  // itself waiting for the allocating grid; and the next kernel starts only
+  // when it is taken, since a flagged verify takes 32 columns before its wait
   if (warp == 0) tmem_alloc(&s_tmem, kStCols);
 
   auto load_wq = [&](int c) {
@@ -1005,6 +1005,7 @@ __global__ void __launch_bounds__(kStThreads, 1) prefill_state_tc_kernel(const P
   tc_fence_before();
   __syncthreads();  // barriers, TMEM address, first gates
   tc_fence_after();
+  pdl_trigger();
   const uint32_t tm = s_tmem;
   const uint32_t trow = tm + (uint32_t(32 * quarter) << 16);
   // 16x32bx2 loads and stores: the second half-warp 8 tokens or 16 columns on

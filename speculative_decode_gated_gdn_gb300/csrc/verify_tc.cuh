@@ -300,8 +300,10 @@ __global__ void __launch_bounds__(kVtThreads, 3)
   // tensor memory, so this is what lets further CTAs of this and the next
   // layer start beside a waiting one.  The 32 columns cannot starve the
   // preceding kernel: at most three verify CTAs fit on an SM (96 of 512
-  // columns), and the library's prefill kernels, the only others that take
-  // tensor memory, need more shared memory than can sit beside a verify CTA.
+  // columns), and of the other kernels that take tensor memory the prefill's
+  // chunk products need 256 columns, while its state pass and the cache
+  // attention's tensor-core form, which need all 512, let this kernel start
+  // only when they hold them.
   // An unflagged call has already waited, whatever the preceding kernel is.
   if (active && issuer) tmem_alloc(&sc.tmem, kVtTmemCols);
   if (tid == 0) {
