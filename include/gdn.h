@@ -622,6 +622,23 @@ int gdn_test_verify_timeout(const gdn_dims *dims, int mode, const gdn_bf16 *x, c
                             const int32_t *offsets, const uint8_t *active, gdn_bf16 *out, void *layer_ws,
                             size_t layer_ws_bytes, uint32_t wait_limit, void *stream);
 
+/*
+ * gdn_kv4_attend with its failure path forced, for tests of that path.  (The
+ * pages describe no such call.)  One barrier of the first CTA, that of its first
+ * copies, expects an arrival that never comes, and every bounded wait of the call
+ * gives up after wait_limit polls instead of the library's default (a poll lasts
+ * at most about a microsecond).  The copies land; that CTA sets
+ * GDN_STATUS_TIMEOUT, waits (bounded) for its copies and products in flight,
+ * frees its tensor memory and ends, and the other CTAs do their part.  As after
+ * any timeout, all outputs are unspecified and ws must be zero-filled before the
+ * next call.  Nothing is forced where no query sees a key.  Errors: as
+ * gdn_kv4_attend.
+ */
+int gdn_test_kv4_attend_timeout(const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages,
+                                const int32_t *table, const int32_t *q_start, const int32_t *q_count,
+                                const int32_t *kv_len, float scale, gdn_bf16 *out, void *ws, size_t ws_bytes,
+                                uint32_t wait_limit, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -639,11 +639,11 @@ __attribute__((visibility("default"))) size_t gdn_kv4_attend_workspace_bytes(con
   return kv4_attend_workspace_bytes(geom_of(dims), N, max_q);
 }
 
-__attribute__((visibility("default"))) int gdn_kv4_attend(
-    const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages, const int32_t *table,
-    const int32_t *q_start, const int32_t *q_count, const int32_t *kv_len, float scale, gdn_bf16 *out, void *ws,
-    size_t ws_bytes, void *stream) {
-  NvtxRange range("gdn_kv4_attend");
+namespace {
+
+int attend(const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages, const int32_t *table,
+           const int32_t *q_start, const int32_t *q_count, const int32_t *kv_len, float scale, gdn_bf16 *out, void *ws,
+           size_t ws_bytes, void *stream, uint32_t wait_limit = kWaitLimit, uint32_t test_hold = 0) {
   int rc = check_kv4(dims);
   if (rc) return rc;
   if ((rc = check_tokens(N))) return rc;
@@ -665,11 +665,31 @@ __attribute__((visibility("default"))) int gdn_kv4_attend(
   p.q = q, p.pages = static_cast<const uint8_t *>(pages), p.table = table;
   p.q_start = q_start, p.q_count = q_count, p.kv_len = kv_len, p.out = out, p.ws = ws;
   p.scale = scale, p.N = N, p.max_q = max_q, p.g = geom_of(dims);
+  p.wait_limit = wait_limit, p.test_hold = test_hold;
   p.status = status_word_address();
   if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   cudaError_t e = launch_kv4_attend(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gdn_kv4_attend launch");
   return ok();
+}
+
+}  // namespace
+
+__attribute__((visibility("default"))) int gdn_kv4_attend(
+    const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages, const int32_t *table,
+    const int32_t *q_start, const int32_t *q_count, const int32_t *kv_len, float scale, gdn_bf16 *out, void *ws,
+    size_t ws_bytes, void *stream) {
+  NvtxRange range("gdn_kv4_attend");
+  return attend(dims, N, max_q, q, pages, table, q_start, q_count, kv_len, scale, out, ws, ws_bytes, stream);
+}
+
+__attribute__((visibility("default"))) int gdn_test_kv4_attend_timeout(
+    const gdn_kv4_dims *dims, int N, int max_q, const gdn_bf16 *q, const void *pages, const int32_t *table,
+    const int32_t *q_start, const int32_t *q_count, const int32_t *kv_len, float scale, gdn_bf16 *out, void *ws,
+    size_t ws_bytes, uint32_t wait_limit, void *stream) {
+  NvtxRange range("gdn_test_kv4_attend_timeout");
+  if (wait_limit < 1) return fail(GDN_ERR_INVALID_ARG, "gdn_test_kv4_attend_timeout: wait_limit must be >= 1");
+  return attend(dims, N, max_q, q, pages, table, q_start, q_count, kv_len, scale, out, ws, ws_bytes, stream, wait_limit, 1);
 }
 
 // ---- verify without caller-provided workspace ---------------------------------

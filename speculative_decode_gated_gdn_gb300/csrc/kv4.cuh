@@ -72,6 +72,8 @@ struct Kv4AttendParams {
   uint32_t *status;
   float scale;
   int N, max_q;
+  uint32_t wait_limit;  // polls of a bounded wait (kWaitLimit)
+  uint32_t test_hold;   // 1: the first copies of CTA 0 never count as complete (a test hook)
   Kv4Geom g;
 };
 

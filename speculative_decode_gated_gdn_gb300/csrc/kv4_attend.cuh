@@ -143,9 +143,9 @@ __device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ush
 __device__ __forceinline__ int att_key(int c) { return c ^ ((c >> 1) & 1); }
 
 // As mbar_wait_spin, kept small: the roles wait in many places.
-__device__ __forceinline__ bool att_wait(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool att_wait(uint64_t *bar, uint32_t parity, uint32_t limit) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+  for (uint32_t i = 0; i < limit; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
@@ -154,6 +154,15 @@ __device__ __forceinline__ bool att_wait(uint64_t *bar, uint32_t parity) {
         : "memory");
     if (ok) return true;
   }
+  return false;
+}
+
+// The rest of a wait that did not end at once.  One that runs out is reported and begun
+// once more: what it waits for is a copy into memory that is given up afterwards.
+static __device__ __noinline__ bool att_wait_slow(uint64_t *bar, uint32_t parity, uint32_t *status, uint32_t limit) {
+  if (att_wait(bar, parity, limit)) return true;
+  atomicOr(status, GDN_STATUS_TIMEOUT);
+  att_wait(bar, parity, limit);
   return false;
 }
 
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
   const int G = p.g.H_q / p.g.H_kv, Hkv = p.g.H_kv;
   const int P = 1 << p.g.log2P;
   if (lane == 0) {
-    for (int i = 0; i < S::kSlots; ++i) mbar_init(&s_full[warp][i], 1);
+    for (int i = 0; i < S::kSlots; ++i) mbar_init(&s_full[warp][i], 1 + (blockIdx.x + warp + i == 0 ? p.test_hold : 0u));
     s_has[0][warp] = s_has[1][warp] = 0;
   }
   fence_mbar_init();
@@ -618,10 +627,8 @@ __global__ void __launch_bounds__(AttShape<D>::kThreads, 1) kv4_attend_mma(const
     for (int st = st_first; st < st_hi; ++st) {
       if (flight > 0) {  // once a wait has run out nothing more is issued, and what is in flight still waited for
         --flight;
-        if (!att_wait(&s_full[warp][slot], (phases >> slot) & 1)) {
-          dead = true;
-          atomicOr(p.status, GDN_STATUS_TIMEOUT);
-        }
+        if (!mbar_try_wait(&s_full[warp][slot], (phases >> slot) & 1))
+          dead = !att_wait_slow(&s_full[warp][slot], (phases >> slot) & 1, p.status, p.wait_limit) || dead;
         dead = __any_sync(0xffffffffu, dead);
         phases ^= 1u << slot;
       }

@@ -241,10 +241,10 @@ __device__ __forceinline__ void tc_output(uint64_t kv, bool acc) {
 
 // The rest of a wait that did not end at once; out of line to keep the roles'
 // code small.
-static __device__ __noinline__ bool tc_wait_slow(uint64_t *bar, uint32_t parity, volatile int *dead, uint32_t *status) {
+static __device__ __noinline__ bool tc_wait_slow(uint64_t *bar, uint32_t parity, volatile int *dead, uint32_t *status, uint32_t limit) {
   bool ok = false;
   if (!*dead) {
-    ok = att_wait(bar, parity);
+    ok = att_wait(bar, parity, limit);
     if (!ok && !*dead) {
       *dead = 1;
       atomicOr(status, GDN_STATUS_TIMEOUT);
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   const int G = p.g.H_q / p.g.H_kv, Hkv = p.g.H_kv, TT = kTcRows / G;
   const int P = 1 << p.g.log2P;
   if (tid == 0) {
-    for (int i = 0; i < kTcRing; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 9);
+    for (int i = 0; i < kTcRing; ++i) mbar_init(&raw_full[i], 1 + (blockIdx.x + i == 0 ? p.test_hold : 0u)), mbar_init(&raw_empty[i], 9);
     for (int i = 0; i < kTcUnits; ++i) mbar_init(&unit_full[i], 1), mbar_init(&unit_empty[i], 19);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 129), mbar_init(&v_full[i], 128);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
   // a bounded wait of the whole warp; false once any wait of the CTA has run out
   auto wait_warp = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return tc_wait_slow(bar, parity, &s_dead, p.status);
+    return tc_wait_slow(bar, parity, &s_dead, p.status, p.wait_limit);
   };
   uint32_t un = 0;  // units taken so far
   // the next unit, for a role's warp; false when there is none or a wait ran out
@@ -570,11 +570,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
           bulk_g2s(ring + slot * S::kRaw + lane * rec_bytes, head + size_t(page) * (Hkv * size_t(rec_bytes)), rec_bytes, &raw_full[slot]);
       }
     }
-    // nothing is in flight when the CTA ends: every copy is waited for by its
-    // readers, or here after a wait that ran out
-    if (!ok)
-      for (uint32_t k = it < kTcRing ? 0 : it - kTcRing; k < it; ++k)
-        att_wait(&raw_full[k % kTcRing], k / kTcRing & 1);
+    // no copy is in flight when the CTA ends, whichever role's wait may have run out: its
+    // readers have waited for it, or do no more
+    for (uint32_t k = it < kTcRing ? 0 : it - kTcRing; k < it; ++k)
+      att_wait(&raw_full[k % kTcRing], k / kTcRing & 1, p.wait_limit);
   } else if (role == 16) {
     // ---- products -----------------------------------------------------------------------
     // The whole warp waits, one elected thread issues; the operands'
@@ -621,11 +620,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_attend_tc(const __grid_cons
       }
       base += n;
     }
-    if (!ok) {  // a wait ran out: the products in flight end before the CTA does
-      if (elect_one()) umma_commit(&drained);
-      __syncwarp();
-      att_wait(&drained, 0);
-    }
+    // no product is in flight when the CTA ends, whichever role's wait may have run out
+    if (elect_one()) umma_commit(&drained);
+    __syncwarp();
+    att_wait(&drained, 0, p.wait_limit);
   } else if (role >= 12 && role < 16) {
     // ---- V^T: 8 keys of one word (8 channels) at a time, 16 bytes of 8 rows ------------------
     const int vt = rtid - 384;

@@ -42,7 +42,8 @@ EXPORTS = ("gdn_version", "gdn_last_error", "gdn_layer_workspace_bytes", "gdn_co
            "gdn_commit", "gdn_prefill_workspace_bytes", "gdn_prefill_chunked", "gdn_get_status",
            "gdn_conv_verify_noalloc", "gdn_flush", "gdn_accept_workspace_bytes", "gdn_accept_greedy",
            "gdn_conv_verify_gated", "gdn_move_rows", "gdn_kv4_page_bytes", "gdn_kv_plan", "gdn_kv4_append",
-           "gdn_kv4_read", "gdn_kv4_attend_workspace_bytes", "gdn_kv4_attend", "gdn_test_verify_timeout")
+           "gdn_kv4_read", "gdn_kv4_attend_workspace_bytes", "gdn_kv4_attend", "gdn_test_verify_timeout",
+           "gdn_test_kv4_attend_timeout")
 
 
 class GdnError(RuntimeError):
@@ -130,6 +131,8 @@ def _declare(lib):
     lib.gdn_kv4_attend_workspace_bytes.argtypes = [K, I, I]
     lib.gdn_kv4_attend.restype = ctypes.c_int
     lib.gdn_kv4_attend.argtypes = [K, I, I] + [_P] * 6 + [ctypes.c_float, _P, _P, ctypes.c_size_t, _P]
+    lib.gdn_test_kv4_attend_timeout.restype = ctypes.c_int
+    lib.gdn_test_kv4_attend_timeout.argtypes = lib.gdn_kv4_attend.argtypes[:-1] + [ctypes.c_uint32, _P]
 
 
 def library_path() -> str:
@@ -485,19 +488,29 @@ def gdn_kv4_attend_workspace_bytes(kd: gdn_kv4_dims, N: int, max_q: int) -> int:
     return int(load().gdn_kv4_attend_workspace_bytes(ctypes.byref(kd), N, max_q))
 
 
-def gdn_kv4_attend(kd: gdn_kv4_dims, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q, stream=None):
-    """Causal attention of the new tokens over the cache (gdn.h,
-    gdn_kv4_attend): q and out [N][H_q][d] bf16, pages uint8, table, q_start,
-    q_count, kv_len as gdn_kv_plan leaves them, ws zero-filled once."""
+def _attend_args(kd, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q):
     torch = _t()
     i32, bf16, B, N = torch.int32, torch.bfloat16, kd.B, q.shape[0]
     size = N * kd.H_q * kd.d
     qp, op, tp, sp, cp, lp = _ptrs((q, "q", size, bf16), (out, "out", size, bf16), (table, "table", B * kd.max_pages, i32),
                                    (q_start, "q_start", B + 1, i32), (q_count, "q_count", B, i32), (kv_len, "kv_len", B, i32))
-    rc = load().gdn_kv4_attend(
-        ctypes.byref(kd), N, max_q, qp, _cache(kd, pages), tp, sp, cp, lp, scale, op, _ptr(ws, "ws"),
-        ws.numel() * ws.element_size(), _stream(stream))
-    _check(rc, "gdn_kv4_attend")
+    return (ctypes.byref(kd), N, max_q, qp, _cache(kd, pages), tp, sp, cp, lp, scale, op, _ptr(ws, "ws"),
+            ws.numel() * ws.element_size())
+
+
+def gdn_kv4_attend(kd: gdn_kv4_dims, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q, stream=None):
+    """Causal attention of the new tokens over the cache (gdn.h,
+    gdn_kv4_attend): q and out [N][H_q][d] bf16, pages uint8, table, q_start,
+    q_count, kv_len as gdn_kv_plan leaves them, ws zero-filled once."""
+    args = _attend_args(kd, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q)
+    _check(load().gdn_kv4_attend(*args, _stream(stream)), "gdn_kv4_attend")
+
+
+def gdn_test_kv4_attend_timeout(kd: gdn_kv4_dims, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q,
+                                wait_limit=4000, stream=None):
+    """Test hook: gdn_kv4_attend with its bounded-wait failure path forced (gdn.h)."""
+    args = _attend_args(kd, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q)
+    _check(load().gdn_test_kv4_attend_timeout(*args, wait_limit, _stream(stream)), "gdn_test_kv4_attend_timeout")
 
 
 def gdn_get_status(clear: bool = False) -> int:
