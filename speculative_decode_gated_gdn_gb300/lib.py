@@ -433,7 +433,8 @@ def _cache(kd, pages):
     """Pointer of a cache; it may be larger than its dims say, never smaller."""
     key = (kd.H_kv, kd.d, kd.page)
     if kd.__dict__.get("_key") != key:  # the page's size is asked for once
-        kd._key, kd._page_bytes = key, gdn_kv4_page_bytes(kd)
+        kd._page_bytes = gdn_kv4_page_bytes(kd)
+        kd._key = key if kd._page_bytes else None  # (0: dims that the call will refuse, which says nothing of others)
     need = kd.n_pages * kd._page_bytes
     p = _ptr(pages, "pages", _t().uint8)
     if pages.numel() < need:
