@@ -392,13 +392,16 @@ def _tokens(t, what, heads, d):
     return t.data_ptr(), (s0 if t.shape[0] > 1 else max(heads * d, 8))
 
 
-def _need(t, what):
-    if not isinstance(t, _t().Tensor):
-        raise TypeError(f"{what}: expected a torch.Tensor")
+def _need(**args):
+    """Names the first argument that is no tensor; called where one turned out
+    to lack a tensor's methods, so that calls that are right do not wait for it."""
+    for what, t in args.items():
+        if not isinstance(t, _t().Tensor):
+            raise TypeError(f"{what}: expected a torch.Tensor")
 
 
 def _count(t, what, n):
-    _need(t, what)
+    _need(**{what: t})
     if t.numel() != n:
         raise ValueError(f"{what}: expected {n} elements, got {t.numel()}")
 
@@ -424,8 +427,11 @@ def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, fre
     gdn_kv_plan): int32 CUDA tensors, active uint8; N = slots.numel().  T > 0
     puts row b's tokens at b*T, T = 0 packs them."""
     torch = _t()
-    _need(slots, "slots")
-    i32, B, N = torch.int32, kd.B, slots.numel()
+    try:
+        i32, B, N = torch.int32, kd.B, slots.numel()
+    except AttributeError:
+        _need(slots=slots)
+        raise
     p = _ptrs((lens, "lens", B, i32), (add, "add", B, i32), (active, "active", B, torch.uint8), (held, "held", B, i32),
               (table, "table", B * kd.max_pages, i32), (free_list, "free_list", kd.n_pages, i32),
               (free_count, "free_count", 1, i32), (q_start, "q_start", B + 1, i32), (q_count, "q_count", B, i32),
@@ -441,10 +447,14 @@ def _cache(kd, pages):
         kd._page_bytes = gdn_kv4_page_bytes(kd)
         kd._key = key if kd._page_bytes else None  # (0: dims that the call will refuse, which says nothing of others)
     need = kd.n_pages * kd._page_bytes
-    _need(pages, "pages")
+    try:
+        size = pages.numel()
+    except AttributeError:
+        _need(pages=pages)
+        raise
     p = _ptr(pages, "pages", _t().uint8)
-    if pages.numel() < need:
-        raise ValueError(f"pages: {pages.numel()} bytes, needs {need}")
+    if size < need:
+        raise ValueError(f"pages: {size} bytes, needs {need}")
     return p
 
 
@@ -465,14 +475,16 @@ def gdn_kv4_append(kd: gdn_kv4_dims, q, k, v, positions, rope, axis, slots, page
     sp, op = _ptrs((slots, "slots", N, torch.int32), (q_out, "q_out", N * kd.H_q * kd.d, torch.bfloat16))
     rot, max_pos, n_axes = 0, 0, 0
     if rope is not None:
-        _need(rope, "rope")
-        _need(positions, "positions")
+        try:
+            if rope.dim() != 3 or rope.shape[2] != 2:
+                raise ValueError("rope: expected [max_pos][rot/2][2]")
+            if positions.dim() != 2 or positions.shape[1] != N:
+                raise ValueError("positions: expected [axes][N]")
+        except AttributeError:
+            _need(rope=rope, positions=positions)
+            raise
         if not isinstance(axis, (bytes, ctypes.Array)):
             raise TypeError("axis: expected bytes")
-        if rope.dim() != 3 or rope.shape[2] != 2:
-            raise ValueError("rope: expected [max_pos][rot/2][2]")
-        if positions.dim() != 2 or positions.shape[1] != N:
-            raise ValueError("positions: expected [axes][N]")
         max_pos, rot, n_axes = rope.shape[0], 2 * rope.shape[1], positions.shape[0]
         if len(axis) != rot // 2:
             raise ValueError(f"axis: expected {rot // 2} bytes, got {len(axis)}")
@@ -487,8 +499,11 @@ def gdn_kv4_read(kd: gdn_kv4_dims, slots, pages, k, v, stream=None):
     """The cached keys and values at the given slots in bf16 (gdn.h,
     gdn_kv4_read): k and v [N][H_kv][d] bf16, written."""
     torch = _t()
-    _need(slots, "slots")
-    N = slots.numel()
+    try:
+        N = slots.numel()
+    except AttributeError:
+        _need(slots=slots)
+        raise
     size, bf16 = N * kd.H_kv * kd.d, torch.bfloat16
     sp, kp, vp = _ptrs((slots, "slots", N, torch.int32), (k, "k", size, bf16), (v, "v", size, bf16))
     rc = load().gdn_kv4_read(ctypes.byref(kd), N, sp, _cache(kd, pages), kp, vp, _stream(stream))
@@ -502,14 +517,15 @@ def gdn_kv4_attend_workspace_bytes(kd: gdn_kv4_dims, N: int, max_q: int) -> int:
 
 def _attend_args(kd, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q):
     torch = _t()
-    _need(q, "q")
-    _need(ws, "ws")
-    i32, bf16, B, N = torch.int32, torch.bfloat16, kd.B, q.shape[0]
+    try:
+        i32, bf16, B, N, ws_bytes = torch.int32, torch.bfloat16, kd.B, q.shape[0], ws.numel() * ws.element_size()
+    except AttributeError:
+        _need(q=q, ws=ws)
+        raise
     size = N * kd.H_q * kd.d
     qp, op, tp, sp, cp, lp = _ptrs((q, "q", size, bf16), (out, "out", size, bf16), (table, "table", B * kd.max_pages, i32),
                                    (q_start, "q_start", B + 1, i32), (q_count, "q_count", B, i32), (kv_len, "kv_len", B, i32))
-    return (ctypes.byref(kd), N, max_q, qp, _cache(kd, pages), tp, sp, cp, lp, scale, op, _ptr(ws, "ws"),
-            ws.numel() * ws.element_size())
+    return ctypes.byref(kd), N, max_q, qp, _cache(kd, pages), tp, sp, cp, lp, scale, op, _ptr(ws, "ws"), ws_bytes
 
 
 def gdn_kv4_attend(kd: gdn_kv4_dims, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q, stream=None):
