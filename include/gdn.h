@@ -557,8 +557,8 @@ int gdn_kv4_append(const gdn_kv4_dims *dims, int N, const gdn_bf16 *q, long long
                    void *pages, gdn_bf16 *q_out, void *stream);
 
 /*
- * The keys and values that the cache stands for at the given slots, rounded
- * once to bf16: k, v [N][H_kv][d]; zeros for a negative slot or one outside
+ * The keys and values that the cache stands for at the given slots, formed in
+ * fp32 and rounded to bf16: k, v [N][H_kv][d]; zeros for a negative slot or one outside
  * the cache (GDN_STATUS_BAD_INDEX).  (The pages describe no such call; it
  * serves moves to a cache of another kind, and checks.)
  */
@@ -583,6 +583,14 @@ size_t gdn_kv4_attend_workspace_bytes(const gdn_kv4_dims *dims, int N, int max_q
  * position and places that no row holds are never used, whatever they hold.
  * Keys and values count as what their entries stand for, also where a level
  * passes fp16's 65504 (such groups are slow).
+ * Precision: scores, their maxima and sums, and outputs accumulate in fp32; a
+ * query is scaled by a power of two, and probabilities and formed values are
+ * rounded once to fp16 (values under 2^-14 keep 2^-25 of absolute precision,
+ * under a level that passes fp16 2^-21).  The form for many rows also rounds the
+ * formed keys once to fp16; with few rows a key's codes enter exactly, and step
+ * and base in fp32.  Outputs are rounded once to bf16.  Queries under 2^118 in
+ * magnitude and scores (scale * q . k) under 2^23 are supported: beyond, a row
+ * may come out as NaN.
  *  q, out     [N][H_q][d] bf16 (rotated queries; out may not overlap q)
  *  table, q_start, q_count, kv_len  as gdn_kv_plan leaves them
  *  max_q      the largest span of a row (the host's bound; 1 for plain decoding)

@@ -21,13 +21,13 @@
 // q is scaled per row by a power of two before fp16, exactly.
 //
 // What bounds it: the instructions that unpack 2 x D codes a token, before HBM (144
-// bytes a token and head pair at D = 128): 1700 a warp and 64 keys, at 57 % of the
+// bytes a token and head pair at D = 128): 1740 a warp and 64 keys, at 56 % of the
 // issue slots, with the halved rate of the logic instructions behind most stalls;
 // hence the AND-only unpacking of the keys, packed fp32 arithmetic and as many
 // warps as the registers allow.  Where the keys are few it is latency: 3 us until
 // the line is cut, 2 to the first keys, 5 to 8 for the joins.
-// 59 ragged rows of up to 8192 keys, 32 heads over 8 of 128: 106 us, 3.3 TB/s of the
-// cache's bytes; one row of 131001 keys: 53 us, 2.8 TB/s.
+// 59 ragged rows of up to 8192 keys, 32 heads over 8 of 128: 109 us, 3.3 TB/s of the
+// cache's bytes; one row of 131001 keys: 54.5 us, 2.8 TB/s.
 //
 // The keys' stages of all units form one line, which the warps of a persistent
 // grid (one CTA an SM) cut into equal pieces, each with its own ring of bulk
@@ -52,13 +52,15 @@ template <int D>
 struct AttShape {
   static constexpr int W = D / 64;               // groups of a head
   static constexpr int ST = D == 256 ? 32 : 64;  // keys of a stage: what a copy brings
-  // Keys, and key tiles, taken at a time.  64 at D = 128 spill with 12 warps (ragged rows
-  // below: 117 us); 16 at D = 256: 95.8 us for 71.9.
+  // Keys, and key tiles, taken at a time.  64 at D = 128 spill heavily with 12 warps
+  // (ragged rows below: 117 us for 106); 16 at D = 256: 95.8 us for 71.9.
   static constexpr int CK = D == 64 ? 64 : 32, NT = CK / 8;
-  // Warps of a CTA, as the registers of a thread allow, and a multiple of 4.  48 rows of
-  // 8000 keys at D = 256: 82.5 us with 12 (spills), 100 with 9, 71.9 with 8, 73.9 with 7;
-  // 64 ragged rows of 8192 at D = 128: 106 with 12, 119 with 10, 114 with 8; at D = 64,
-  // 16 rows of 2000: 15.9 with 12, 17.6 with 16 (and 38.8, 39.1 for 48 rows of 16000).
+  // Warps of a CTA, as the registers of a thread allow, and a multiple of 4 (the compiler
+  // spills 96 bytes a thread at D = 256 with 8, 8 at D = 128 with 12, none at D = 64).  48
+  // rows of 8000 keys at D = 256: 82.5 us with 12, which spill more, 100 with 9, 71.9 with
+  // 8, 73.9 with 7; 64 ragged rows of 8192 at D = 128: 106 with 12, 119 with 10, 114 with
+  // 8; at D = 64, 16 rows of 2000: 15.9 with 12, 17.6 with 16 (and 38.8, 39.1 for 48 rows
+  // of 16000).
   static constexpr int NW = D == 256 ? 8 : 12;
   static constexpr int kThreads = 32 * NW;
   static constexpr int kCodes = ST * D / 2, kEntries = ST * W * 4;

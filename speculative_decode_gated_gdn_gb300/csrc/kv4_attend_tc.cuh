@@ -32,7 +32,7 @@
 // What bounds it: a tile is a chain (scores, their maximum, exponentials, output)
 // whose steps wait for one another, and the roles share the issue slots, which
 // are 58 % busy; the tensor cores work 28 % of the time.  A tile of 128 keys at D =
-// 128 takes 2700 cycles where its products alone take 1090; with the dequant, the
+// 128 takes 2740 cycles where its products alone take 1090; with the dequant, the
 // exponentials and the maxima left out, 1790: what then is left is the products
 // and the barriers between them.  Neither separate columns for P (no
 // scores wait for the output of the tile before last, 3 % slower), nor loads of
@@ -42,9 +42,9 @@
 // With Q and P in tensor memory the products read only K and V from shared
 // memory, so that a 64-key tile still feeds them at D = 256, where O takes half
 // of the tensor memory.
-// 2000 queries behind 16001 keys, 32 heads over 8 of 128: 615 us, 905 TFLOP/s of
-// the products; a prompt of 4096, 16 heads over 2 of 256: 191 us, 720 TFLOP/s
-// (back to back; 619 and 196 us with other work between the calls).
+// 2000 queries behind 16001 keys, 32 heads over 8 of 128: 624 us, 893 TFLOP/s of
+// the products; a prompt of 4096, 16 heads over 2 of 256: 198 us, 690 TFLOP/s
+// (back to back; 628 and 202 us with other work between the calls).
 //
 // Units are laid on one line in tiles of keys and cut evenly over a persistent
 // grid as in kv4_attend.cuh; causal tiles count as far as their last query sees.
