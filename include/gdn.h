@@ -454,6 +454,65 @@ size_t gdn_accept_workspace_bytes(int B, int T, int V);
 int gdn_accept_greedy(int B, int T, int V, const gdn_bf16 *logits, const int32_t *draft, const uint8_t *active,
                       int32_t *keep, int32_t *next, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- sampled decoding -----------------------------------------------------------
+ * One token of every position of a verify drawn from its logits, and the accepted
+ * prefix of the drafts, on the device like gdn_accept_greedy ("Add request-owned
+ * eight-way MTP serving for Qwen 35B" takes the acceptance decision off the host).
+ * The row's own parameters filter a position's logits x, in this order (values
+ * descending, equal ones by index; NaN never takes part):
+ *   w_v = exp((x_v - max x) / temperature)
+ *   min_p  those with w_v >= min_p
+ *   top_k  of these the first top_k
+ *   top_p  of these the shortest beginning with top_p of their mass (one at least)
+ * and the token is the first of what is left whose running sum of weights passes
+ * u times their mass.  logp is the logarithm of the token's share of that mass.
+ * temperature <= 0 or NaN takes the first (logp 0); min_p <= 0 or NaN, top_k <= 0
+ * and top_p >= 1 or NaN filter nothing; min_p over 1 counts as 1, top_p below 0 as 0,
+ * u outside [0, 1) as the nearest number in it, NaN as 0.  A position with no number
+ * above -infinity gives what gdn_accept_greedy takes, with logp -infinity.
+ * Infinite logits share the mass among themselves.
+ * Precision: weights to 2^-37 of themselves and 2^-43 of the largest, their sums
+ * exact in integers; the same inputs give the same outputs on every run.
+ *  logits  position (b, t) at (b * T + t) * stride elements, bf16, stride >= V;
+ *          any 2-byte aligned address
+ *  active  [B] uint8, NULL: all.  Inactive rows get token -1 and logp 0
+ *  temperature, top_p, min_p [B] fp32, top_k [B] int32: NULL: 1, off, off, off
+ *  u       [B][T] fp32, uniform random numbers in [0, 1)
+ *  token   [B][T] int32, written; logp [B][T] fp32, written (each may be NULL in
+ *          gdn_accept_sampled, logp in gdn_sample)
+ * Supported: 1 <= V <= 2^20, 1 <= T <= 64, B * T <= 65535.
+ */
+
+/*
+ * One token a row: T = 1.  (The pages describe no such call; it samples a
+ * prompt's first token, and serves hosts without drafts.)
+ */
+int gdn_sample(int B, int V, const gdn_bf16 *logits, long long stride, const uint8_t *active,
+               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+               const float *u, int32_t *token, float *logp, void *stream);
+
+/*
+ * The tokens of T positions and, per active row,
+ *   keep[b]  = 1 + the number of leading t in 1..T-1 with draft[b][t] == token[b][t-1]
+ *   next[b]  = token[b][keep[b]-1]
+ * as gdn_accept_greedy has them of the arg max ("Add request-owned eight-way MTP
+ * serving for Qwen 35B", section 4: keep per row).  What is emitted, the accepted
+ * drafts and next, is distributed as tokens sampled one by one are, however the
+ * drafts were made, if u is fresh: a draft is kept when the draw equals it.
+ * Inactive rows get keep 0 and next -1.
+ *  ws  gdn_accept_sampled_workspace_bytes, 256-byte aligned, zero-filled once before
+ *      its first use (each call leaves it ready for the next); one call at a time
+ *      may use it
+ */
+int gdn_accept_sampled(int B, int T, int V, const gdn_bf16 *logits, long long stride, const int32_t *draft,
+                       const uint8_t *active, const float *temperature, const int32_t *top_k, const float *top_p,
+                       const float *min_p, const float *u, int32_t *keep, int32_t *next, int32_t *token,
+                       float *logp, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace gdn_accept_sampled needs; 0 for invalid sizes.  (The pages
+ * describe no such call.) */
+size_t gdn_accept_sampled_workspace_bytes(int B, int T, int V);
+
 /* ---- a paged 4-bit key/value cache for the attention layers --------------------
  * The hybrid models of the three pages have attention layers next to the GDN
  * layers, with a KV cache that is trimmed on rewind ("perf(qwen): full-context

@@ -20,6 +20,7 @@
 
 #include "gdn_common.cuh"
 #include "kv4.cuh"
+#include "sample.cuh"
 
 using namespace gdn;
 
@@ -480,6 +481,82 @@ __attribute__((visibility("default"))) int gdn_move_rows(
   if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   cudaError_t e = launch_move_rows(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gdn_move_rows launch");
+  return ok();
+}
+
+// ---- sampled decoding ----------------------------------------------------------
+namespace {
+
+int check_sample(int B, int T, int V, long long stride) {
+  if (B < 0 || T < 1 || V < 1) return fail(GDN_ERR_INVALID_ARG, "sample: B=%d T=%d V=%d", B, T, V);
+  if (T > kMaxAcceptT) return fail(GDN_ERR_UNSUPPORTED, "sample: T=%d above %d", T, kMaxAcceptT);
+  if ((long long)B * T > 65535) return fail(GDN_ERR_UNSUPPORTED, "sample: B*T=%lld above 65535", (long long)B * T);
+  if (V > kMaxSampleV) return fail(GDN_ERR_UNSUPPORTED, "sample: V=%d above %d", V, kMaxSampleV);
+  if (stride < V || stride > (1LL << 40)) return fail(GDN_ERR_INVALID_ARG, "sample: stride %lld below V=%d, or above 2^40", stride, V);
+  return GDN_OK;
+}
+
+// What both calls share; the optional arrays may be NULL, never misaligned.
+int fill_sample(SampleParams &p, int B, int T, int V, const gdn_bf16 *logits, long long stride, const uint8_t *active,
+                const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                const float *u, int32_t *token, float *logp) {
+  GDN_NEED_PTR(logits, 2);
+  GDN_NEED_PTR(u, 4);
+  const void *all[] = {temperature, top_k, top_p, min_p, token, logp};
+  for (const void *q : all)
+    if (!aligned(q, 4)) return fail(GDN_ERR_MISALIGNED, "sample: an array is not 4-byte aligned");
+  p.logits = logits, p.stride = stride, p.active = active;
+  p.temperature = temperature, p.top_k = top_k, p.top_p = top_p, p.min_p = min_p;
+  p.u = u, p.token = token, p.logp = logp;
+  p.B = B, p.T = T, p.V = V;
+  return GDN_OK;
+}
+
+}  // namespace
+
+__attribute__((visibility("default"))) int gdn_sample(int B, int V, const gdn_bf16 *logits, long long stride,
+                                                      const uint8_t *active, const float *temperature,
+                                                      const int32_t *top_k, const float *top_p, const float *min_p,
+                                                      const float *u, int32_t *token, float *logp, void *stream) {
+  NvtxRange range("gdn_sample");
+  int rc = check_sample(B, 1, V, stride);
+  if (rc) return rc;
+  if (B == 0) return ok();
+  GDN_NEED_PTR(token, 4);
+  SampleParams p{};
+  if ((rc = fill_sample(p, B, 1, V, logits, stride, active, temperature, top_k, top_p, min_p, u, token, logp))) return rc;
+  cudaError_t e = launch_sample(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_sample launch");
+  return ok();
+}
+
+__attribute__((visibility("default"))) size_t gdn_accept_sampled_workspace_bytes(int B, int T, int V) {
+  if (check_sample(B, T, V, V) != GDN_OK) return 0;
+  return accept_sampled_workspace_bytes(B, T);
+}
+
+__attribute__((visibility("default"))) int gdn_accept_sampled(
+    int B, int T, int V, const gdn_bf16 *logits, long long stride, const int32_t *draft, const uint8_t *active,
+    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+    int32_t *keep, int32_t *next, int32_t *token, float *logp, void *ws, size_t ws_bytes, void *stream) {
+  NvtxRange range("gdn_accept_sampled");
+  int rc = check_sample(B, T, V, stride);
+  if (rc) return rc;
+  if (B == 0) return ok();
+  GDN_NEED_PTR(draft, 4);
+  GDN_NEED_PTR(keep, 4);
+  GDN_NEED_PTR(next, 4);
+  GDN_NEED_PTR(ws, 256);
+  SampleParams p{};
+  if ((rc = fill_sample(p, B, T, V, logits, stride, active, temperature, top_k, top_p, min_p, u, token, logp))) return rc;
+  const size_t need = accept_sampled_workspace_bytes(B, T);
+  if (ws_bytes < need)
+    return fail(GDN_ERR_WORKSPACE, "sampled acceptance workspace has %zu bytes, needs %zu", ws_bytes, need);
+  p.draft = draft, p.keep = keep, p.next = next;
+  p.ws_token = static_cast<int32_t *>(ws);
+  p.ws_count = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + align256(size_t(B) * T * sizeof(int32_t)));
+  cudaError_t e = launch_sample(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_accept_sampled launch");
   return ok();
 }
 

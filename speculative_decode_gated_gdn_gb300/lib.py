@@ -42,7 +42,8 @@ EXPORTS = ("gdn_version", "gdn_last_error", "gdn_layer_workspace_bytes", "gdn_co
            "gdn_commit", "gdn_prefill_workspace_bytes", "gdn_prefill_chunked", "gdn_get_status",
            "gdn_conv_verify_noalloc", "gdn_flush", "gdn_accept_workspace_bytes", "gdn_accept_greedy",
            "gdn_conv_verify_gated", "gdn_move_rows", "gdn_kv4_page_bytes", "gdn_kv_plan", "gdn_kv4_append",
-           "gdn_kv4_read", "gdn_kv4_attend_workspace_bytes", "gdn_kv4_attend", "gdn_test_verify_timeout",
+           "gdn_kv4_read", "gdn_sample", "gdn_accept_sampled",
+           "gdn_accept_sampled_workspace_bytes", "gdn_kv4_attend_workspace_bytes", "gdn_kv4_attend", "gdn_test_verify_timeout",
            "gdn_test_kv4_attend_timeout")
 
 
@@ -118,6 +119,12 @@ def _declare(lib):
     lib.gdn_accept_workspace_bytes.argtypes = [ctypes.c_int] * 3
     lib.gdn_accept_greedy.restype = ctypes.c_int
     lib.gdn_accept_greedy.argtypes = [ctypes.c_int] * 3 + [_P] * 6 + [ctypes.c_size_t, _P]
+    lib.gdn_sample.restype = ctypes.c_int
+    lib.gdn_sample.argtypes = [ctypes.c_int] * 2 + [_P, ctypes.c_longlong] + [_P] * 9
+    lib.gdn_accept_sampled_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_accept_sampled_workspace_bytes.argtypes = [ctypes.c_int] * 3
+    lib.gdn_accept_sampled.restype = ctypes.c_int
+    lib.gdn_accept_sampled.argtypes = ([ctypes.c_int] * 3 + [_P, ctypes.c_longlong] + [_P] * 12 + [ctypes.c_size_t, _P])
     K, I, LL = ctypes.POINTER(gdn_kv4_dims), ctypes.c_int, ctypes.c_longlong
     lib.gdn_kv4_page_bytes.restype = ctypes.c_size_t
     lib.gdn_kv4_page_bytes.argtypes = [K]
@@ -369,6 +376,83 @@ def gdn_accept_greedy(logits, draft, active, keep, nxt, ws, stream=None):
                                   _ptr(nxt, "next", torch.int32), _ptr(ws, "ws"),
                                   ws.numel() * ws.element_size(), _stream(stream))
     _check(rc, "gdn_accept_greedy")
+
+
+def _logits(t, dims):
+    """Pointer and position stride of [B][V] or [B][T][V] bf16 logits whose
+    positions lie at equal distances (a slice of a padded vocabulary serves)."""
+    _need(logits=t)
+    if not t.is_cuda:
+        raise ValueError("logits: tensor must be on a CUDA device")
+    if t.dtype != _t().bfloat16:
+        raise TypeError(f"logits: expected {_t().bfloat16}, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"logits: expected {dims} dimensions, got {tuple(t.shape)}")
+    *shape, V = t.shape
+    *strides, one = t.stride()
+    n = 1  # positions at and behind a dimension
+    s = max(V, 1)
+    for size, stride in zip(reversed(shape), reversed(strides)):
+        if size > 1:
+            if n == 1:
+                s = stride
+            elif stride != n * s:
+                raise ValueError("logits: positions must lie at equal distances")
+            n *= size
+    if one != 1 and V > 1:
+        raise ValueError("logits: a position's logits must be densely packed")
+    return t.data_ptr(), s
+
+
+def _per_row(t, what, n, dtype):
+    return None if t is None else _ptrs((t, what, n, dtype))[0]
+
+
+def _filters(B, temperature, top_k, top_p, min_p):
+    f32 = _t().float32
+    return (_per_row(temperature, "temperature", B, f32), _per_row(top_k, "top_k", B, _t().int32),
+            _per_row(top_p, "top_p", B, f32), _per_row(min_p, "min_p", B, f32))
+
+
+def gdn_sample(logits, u, token, logp=None, temperature=None, top_k=None, top_p=None, min_p=None, active=None,
+               stream=None):
+    """One token a row from its logits (gdn.h, gdn_sample): logits [B][V] bf16
+    (row stride free), u [B] fp32 -> token [B] int32, logp [B] fp32, written in
+    place.  temperature, top_p, min_p [B] fp32, top_k [B] int32, active [B]
+    uint8; None: 1, off, off, off, all."""
+    torch = _t()
+    lp, stride = _logits(logits, 2)
+    B, V = logits.shape
+    up, tp = _ptrs((u, "u", B, torch.float32), (token, "token", B, torch.int32))
+    rc = load().gdn_sample(B, V, lp, stride, _per_row(active, "active", B, torch.uint8),
+                           *_filters(B, temperature, top_k, top_p, min_p), up, tp,
+                           _per_row(logp, "logp", B, torch.float32), _stream(stream))
+    _check(rc, "gdn_sample")
+
+
+def gdn_accept_sampled_workspace_bytes(B: int, T: int, V: int) -> int:
+    """Bytes of workspace gdn_accept_sampled needs (0 for invalid sizes)."""
+    return int(load().gdn_accept_sampled_workspace_bytes(B, T, V))
+
+
+def gdn_accept_sampled(logits, draft, active, u, keep, nxt, token, logp, ws, temperature=None, top_k=None, top_p=None,
+                       min_p=None, stream=None):
+    """Sampled acceptance on the device (gdn.h, gdn_accept_sampled): logits
+    [B][T][V] bf16 (position stride free), draft [B][T] int32, active [B] uint8
+    (None: all), u [B][T] fp32 -> keep [B], nxt [B] int32, token [B][T] int32 and
+    logp [B][T] fp32 (each may be None), written in place.  ws:
+    gdn_accept_sampled_workspace_bytes(B, T, V) bytes, zero-filled once."""
+    torch = _t()
+    lp, stride = _logits(logits, 3)
+    B, T, V = logits.shape
+    i32, f32 = torch.int32, torch.float32
+    dp, up, kp, np_ = _ptrs((draft, "draft", B * T, i32), (u, "u", B * T, f32), (keep, "keep", B, i32), (nxt, "next", B, i32))
+    _need(ws=ws)
+    rc = load().gdn_accept_sampled(
+        B, T, V, lp, stride, dp, _per_row(active, "active", B, torch.uint8),
+        *_filters(B, temperature, top_k, top_p, min_p), up, kp, np_, _per_row(token, "token", B * T, i32),
+        _per_row(logp, "logp", B * T, f32), _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
+    _check(rc, "gdn_accept_sampled")
 
 
 def gdn_kv4_page_bytes(kd: gdn_kv4_dims) -> int:
