@@ -184,7 +184,8 @@ typedef uint16_t gdn_bf16; /* bfloat16 bit pattern */
                                   wrote no output, capture or state for that
                                   (row, head) after the wait */
 #define GDN_STATUS_BAD_ROW 4u  /* gdn_move_rows got a row index outside its
-                                  cohort; that pair was not copied */
+                                  cohort, or gdn_kv_fork one that does not serve;
+                                  that pair was not copied */
 
 #define GDN_STATUS_NO_PAGES 8u /* gdn_kv_plan found no page, or no place for
                                   its tokens, for a row */
@@ -586,6 +587,78 @@ int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, con
                 const uint8_t *active, int32_t *held, int32_t *table, int32_t *free_list, int32_t *free_count,
                 int32_t *q_start, int32_t *q_count, int32_t *kv_len, int32_t *slots, int32_t *positions,
                 void *stream);
+
+/*
+ * gdn_kv_plan for a cache whose pages several rows may hold ("Add request-owned
+ * eight-way MTP serving for Qwen 35B", section 2: per-row committed offsets; rows
+ * forked from one prompt keep its pages in common).  As gdn_kv_plan, with
+ *  refs [n_pages] int32 in/out: the rows that hold each page, 0 where none does
+ * A page taken gets one holder.  A page given back loses one, and goes onto the stack
+ * when it has none left, at the place (in row order, each row's in column order) of
+ * the last of its releases in the call.  A page outside the cache, or one that had no
+ * holder, is dropped (GDN_STATUS_BAD_INDEX).  A row's length never falls below what it
+ * shares, except to 0: rows write behind their committed length, and what is shared
+ * lies before it.  Supported: B * max_pages < 2^31.
+ */
+int gdn_kv_plan_shared(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, const int32_t *add,
+                       const uint8_t *active, int32_t *held, int32_t *table, int32_t *free_list,
+                       int32_t *free_count, int32_t *refs, int32_t *q_start, int32_t *q_count, int32_t *kv_len,
+                       int32_t *slots, int32_t *positions, void *stream);
+
+/*
+ * Rows that continue other rows' sequences: for each pair i < n, the first lens[i]
+ * tokens of row src_rows[i] become those of row dst_rows[i] as well, for every layer
+ * that the table serves.  (The pages describe no such call; it is to the attention
+ * layers what gdn_move_rows is to the GDN layers, which copies the state and the
+ * committed offset of such a row.)  Full pages get one holder more; the rest, if any,
+ * gets a page from the stack's end, in the order of the pairs, and a copy for
+ * gdn_kv_copy_pages, to be made before either row's next append.
+ *  lens       [n] int32; src_rows, dst_rows [n] int32
+ *  held, table, free_list, free_count  as for gdn_kv_plan; refs as for gdn_kv_plan_shared
+ *  copy_src, copy_dst  [n] int32 out: pages; -1 where the pair needs no copy, -2 where
+ *             it was not made.  A pair of length 0 needs nothing
+ * Not made are: a pair with a row outside the cohort, with equal rows, or whose
+ * destination holds pages already, also from an earlier pair of the call
+ * (GDN_STATUS_BAD_ROW); one with a negative length, or longer than its source's pages
+ * before the call (GDN_STATUS_BAD_LEN); one that needs a page when none is left, and
+ * then every later one that needs one (GDN_STATUS_NO_PAGES).  n = 0 does nothing.
+ */
+int gdn_kv_fork(const gdn_kv4_dims *dims, int n, const int32_t *src_rows, const int32_t *dst_rows,
+                const int32_t *lens, int32_t *held, int32_t *table, int32_t *free_list, int32_t *free_count,
+                int32_t *refs, int32_t *copy_src, int32_t *copy_dst, void *stream);
+
+/*
+ * Move the pages in use (refs > 0), U of them, to the cache's first U places: those
+ * behind move, in ascending order, to the free ones among the first U, in ascending
+ * order.  (The pages describe no such call; a cache that is to be saved, or to give
+ * memory back, wants its pages together.)  The pages themselves are moved by
+ * gdn_kv_copy_pages.
+ *  held [B], table [B][max_pages], refs [n_pages]  int32, as gdn_kv_plan_shared leaves them
+ *  new_table, new_refs  out, as table and refs; each may be its input itself.  Cells
+ *             behind a row's held pages are copied
+ *  new_free_list [n_pages], new_free_count [1]  int32 out: a stack of the places from
+ *             U on whose end is place U; entries behind the count get -1
+ *  page_map   [n_pages] int32 out: the new place of each page, -1 for free ones
+ *  copy_src, copy_dst  [n_pages / 2, at least 1] int32 out, copy_count [1] int32 out:
+ *             the moves; entries from copy_count on are not written
+ * As sources lie behind place U and destinations before it, the old tables stay valid
+ * until pages are appended through the new ones.  A cell that holds no page in use
+ * becomes -1 (GDN_STATUS_BAD_INDEX).
+ */
+int gdn_kv_compact(const gdn_kv4_dims *dims, const int32_t *held, const int32_t *table, const int32_t *refs,
+                   int32_t *new_table, int32_t *new_refs, int32_t *new_free_list, int32_t *new_free_count,
+                   int32_t *page_map, int32_t *copy_src, int32_t *copy_dst, int32_t *copy_count, void *stream);
+
+/*
+ * Copy page src[i] to page dst[i], whole, in every layer's cache, i < min(n, *count).
+ * (The pages describe no such call.)  Pairs with a negative page are skipped, pairs
+ * with one outside the cache too (GDN_STATUS_BAD_INDEX).  Destinations are distinct,
+ * and none is a source.
+ *  pages     HOST array [n_layers] of device pointers to the layers' caches
+ *  src, dst  [n] int32 device; count [1] int32 device, NULL: all n
+ */
+int gdn_kv_copy_pages(const gdn_kv4_dims *dims, int n_layers, void *const *pages, int n, const int32_t *src,
+                      const int32_t *dst, const int32_t *count, void *stream);
 
 /*
  * Rotate q and k by positions of several axes and write k and v into the cache

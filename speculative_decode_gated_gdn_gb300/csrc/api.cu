@@ -600,17 +600,21 @@ __attribute__((visibility("default"))) size_t gdn_kv4_page_bytes(const gdn_kv4_d
   return size_t(dims->H_kv) * kv4_record_bytes(dims->d, dims->page);
 }
 
-__attribute__((visibility("default"))) int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens,
-                                                       const int32_t *add, const uint8_t *active, int32_t *held,
-                                                       int32_t *table, int32_t *free_list, int32_t *free_count,
-                                                       int32_t *q_start, int32_t *q_count, int32_t *kv_len,
-                                                       int32_t *slots, int32_t *positions, void *stream) {
-  NvtxRange range("gdn_kv_plan");
+namespace {
+
+// Both forms of the plan; `shared`: with holder counts.
+int plan_call(const char *name, const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, const int32_t *add,
+              const uint8_t *active, int32_t *held, int32_t *table, int32_t *free_list, int32_t *free_count,
+              bool shared, int32_t *refs, int32_t *q_start, int32_t *q_count, int32_t *kv_len, int32_t *slots,
+              int32_t *positions, void *stream) {
+  NvtxRange range(name);
   int rc = check_kv4(dims);
   if (rc) return rc;
   if ((rc = check_tokens(N))) return rc;
   if (T < 0 || (T > 0 && (long long)dims->B * T > N))
     return fail(GDN_ERR_INVALID_ARG, "plan: need T >= 0 and, where T > 0, N (%d) >= B * T (%d * %d)", N, dims->B, T);
+  if (shared && (long long)dims->B * dims->max_pages >= (1LL << 31))
+    return fail(GDN_ERR_UNSUPPORTED, "need B * max_pages (%d * %d) < 2^31", dims->B, dims->max_pages);
   if (dims->B == 0) return ok();
   GDN_NEED_PTR(lens, 4);
   GDN_NEED_PTR(add, 4);
@@ -619,6 +623,7 @@ __attribute__((visibility("default"))) int gdn_kv_plan(const gdn_kv4_dims *dims,
   GDN_NEED_PTR(table, 4);
   GDN_NEED_PTR(free_list, 4);
   GDN_NEED_PTR(free_count, 4);
+  if (shared) GDN_NEED_PTR(refs, 4);
   GDN_NEED_PTR(q_start, 4);
   GDN_NEED_PTR(q_count, 4);
   GDN_NEED_PTR(kv_len, 4);
@@ -628,14 +633,126 @@ __attribute__((visibility("default"))) int gdn_kv_plan(const gdn_kv4_dims *dims,
   }
   KvPlanParams p{};
   p.lens = lens, p.add = add, p.active = active;
-  p.held = held, p.table = table, p.free_list = free_list, p.free_count = free_count;
+  p.held = held, p.table = table, p.free_list = free_list, p.free_count = free_count, p.refs = refs;
   p.q_start = q_start, p.q_count = q_count, p.kv_len = kv_len, p.slots = slots, p.positions = positions;
   p.B = dims->B, p.T = T, p.N = N;
   p.log2P = log2_page(dims), p.max_pages = dims->max_pages, p.n_pages = dims->n_pages;
   p.status = status_word_address();
   if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
   cudaError_t e = launch_kv_plan(p, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv_plan launch");
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
+  return ok();
+}
+
+}  // namespace
+
+__attribute__((visibility("default"))) int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens,
+                                                       const int32_t *add, const uint8_t *active, int32_t *held,
+                                                       int32_t *table, int32_t *free_list, int32_t *free_count,
+                                                       int32_t *q_start, int32_t *q_count, int32_t *kv_len,
+                                                       int32_t *slots, int32_t *positions, void *stream) {
+  return plan_call("gdn_kv_plan", dims, T, N, lens, add, active, held, table, free_list, free_count, false, nullptr,
+                   q_start, q_count, kv_len, slots, positions, stream);
+}
+
+__attribute__((visibility("default"))) int gdn_kv_plan_shared(
+    const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, const int32_t *add, const uint8_t *active,
+    int32_t *held, int32_t *table, int32_t *free_list, int32_t *free_count, int32_t *refs, int32_t *q_start,
+    int32_t *q_count, int32_t *kv_len, int32_t *slots, int32_t *positions, void *stream) {
+  return plan_call("gdn_kv_plan_shared", dims, T, N, lens, add, active, held, table, free_list, free_count, true, refs,
+                   q_start, q_count, kv_len, slots, positions, stream);
+}
+
+__attribute__((visibility("default"))) int gdn_kv_fork(const gdn_kv4_dims *dims, int n, const int32_t *src_rows,
+                                                       const int32_t *dst_rows, const int32_t *lens, int32_t *held,
+                                                       int32_t *table, int32_t *free_list, int32_t *free_count,
+                                                       int32_t *refs, int32_t *copy_src, int32_t *copy_dst,
+                                                       void *stream) {
+  NvtxRange range("gdn_kv_fork");
+  int rc = check_kv4(dims);
+  if (rc) return rc;
+  if (n < 0 || n > 65535) return fail(GDN_ERR_UNSUPPORTED, "fork: n=%d outside [0, 65535]", n);
+  if (n == 0) return ok();
+  GDN_NEED_PTR(src_rows, 4);
+  GDN_NEED_PTR(dst_rows, 4);
+  GDN_NEED_PTR(lens, 4);
+  GDN_NEED_PTR(held, 4);
+  GDN_NEED_PTR(table, 4);
+  GDN_NEED_PTR(free_list, 4);
+  GDN_NEED_PTR(free_count, 4);
+  GDN_NEED_PTR(refs, 4);
+  GDN_NEED_PTR(copy_src, 4);
+  GDN_NEED_PTR(copy_dst, 4);
+  KvForkParams p{};
+  p.src_rows = src_rows, p.dst_rows = dst_rows, p.lens = lens, p.held = held, p.table = table;
+  p.free_list = free_list, p.free_count = free_count, p.refs = refs, p.copy_src = copy_src, p.copy_dst = copy_dst;
+  p.n = n, p.B = dims->B, p.log2P = log2_page(dims), p.max_pages = dims->max_pages, p.n_pages = dims->n_pages;
+  p.status = status_word_address();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  cudaError_t e = launch_kv_fork(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv_fork launch");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int gdn_kv_compact(
+    const gdn_kv4_dims *dims, const int32_t *held, const int32_t *table, const int32_t *refs, int32_t *new_table,
+    int32_t *new_refs, int32_t *new_free_list, int32_t *new_free_count, int32_t *page_map, int32_t *copy_src,
+    int32_t *copy_dst, int32_t *copy_count, void *stream) {
+  NvtxRange range("gdn_kv_compact");
+  int rc = check_kv4(dims);
+  if (rc) return rc;
+  if (dims->B > 0) {
+    GDN_NEED_PTR(held, 4);
+    GDN_NEED_PTR(table, 4);
+    GDN_NEED_PTR(new_table, 4);
+  }
+  GDN_NEED_PTR(refs, 4);
+  GDN_NEED_PTR(new_refs, 4);
+  GDN_NEED_PTR(new_free_list, 4);
+  GDN_NEED_PTR(new_free_count, 4);
+  GDN_NEED_PTR(page_map, 4);
+  GDN_NEED_PTR(copy_src, 4);
+  GDN_NEED_PTR(copy_dst, 4);
+  GDN_NEED_PTR(copy_count, 4);
+  KvCompactParams p{};
+  p.held = held, p.table = table, p.refs = refs, p.new_table = new_table, p.new_refs = new_refs;
+  p.new_free_list = new_free_list, p.new_free_count = new_free_count, p.page_map = page_map;
+  p.copy_src = copy_src, p.copy_dst = copy_dst, p.copy_count = copy_count;
+  p.B = dims->B, p.max_pages = dims->max_pages, p.n_pages = dims->n_pages;
+  p.status = status_word_address();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  cudaError_t e = launch_kv_compact(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv_compact launch");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int gdn_kv_copy_pages(const gdn_kv4_dims *dims, int n_layers,
+                                                             void *const *pages, int n, const int32_t *src,
+                                                             const int32_t *dst, const int32_t *count, void *stream) {
+  NvtxRange range("gdn_kv_copy_pages");
+  int rc = check_kv4(dims);
+  if (rc) return rc;
+  if (n_layers < 1 || n_layers > kMaxCopyLayers)
+    return fail(GDN_ERR_INVALID_ARG, "n_layers=%d outside [1, %d]", n_layers, kMaxCopyLayers);
+  if (n < 0) return fail(GDN_ERR_INVALID_ARG, "copy_pages: n=%d", n);
+  if (!pages) return fail(GDN_ERR_INVALID_ARG, "pages is NULL");
+  KvCopyParams p{};
+  for (int l = 0; l < n_layers; ++l) {
+    if (!pages[l]) return fail(GDN_ERR_INVALID_ARG, "layer %d: NULL pages", l);
+    if (!aligned(pages[l], 16)) return fail(GDN_ERR_MISALIGNED, "layer %d: pages not 16-byte aligned", l);
+    p.pages[l] = static_cast<uint8_t *>(pages[l]);
+  }
+  if (n == 0) return ok();
+  GDN_NEED_PTR(src, 4);
+  GDN_NEED_PTR(dst, 4);
+  if (!aligned(count, 4)) return fail(GDN_ERR_MISALIGNED, "count is not 4-byte aligned");
+  p.src = src, p.dst = dst, p.count = count;
+  p.n = n, p.n_layers = n_layers, p.n_pages = dims->n_pages;
+  p.page_bytes = dims->H_kv * kv4_record_bytes(dims->d, dims->page);
+  p.status = status_word_address();
+  if (!p.status) return fail(GDN_ERR_CUDA, "cannot resolve the device status word");
+  cudaError_t e = launch_kv_copy(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gdn_kv_copy_pages launch");
   return ok();
 }
 

@@ -34,9 +34,34 @@ struct KvPlanParams {
   const uint8_t *active;
   int32_t *held, *table, *free_list, *free_count;
   int32_t *q_start, *q_count, *kv_len, *slots, *positions;
+  int32_t *refs;  // [n_pages] rows that hold a page; NULL: one at most
   uint32_t *status;
   int B, T, N;  // T > 0: row b's tokens at b * T; T == 0: packed
   int log2P, max_pages, n_pages;
+};
+
+struct KvForkParams {
+  const int32_t *src_rows, *dst_rows, *lens;  // [n]
+  int32_t *held, *table, *free_list, *free_count, *refs;
+  int32_t *copy_src, *copy_dst;  // [n]
+  uint32_t *status;
+  int n, B, log2P, max_pages, n_pages;
+};
+
+struct KvCompactParams {
+  const int32_t *held, *table, *refs;
+  int32_t *new_table, *new_refs, *new_free_list, *new_free_count, *page_map, *copy_src, *copy_dst, *copy_count;
+  uint32_t *status;
+  int B, max_pages, n_pages;
+};
+
+constexpr int kMaxCopyLayers = 256;
+
+struct KvCopyParams {
+  uint8_t *pages[kMaxCopyLayers];
+  const int32_t *src, *dst, *count;  // count NULL: all n
+  uint32_t *status;
+  int n, n_layers, n_pages, page_bytes;
 };
 
 constexpr int kMaxRopePairs = 128;  // rot / 2 <= D / 2
@@ -78,6 +103,9 @@ struct Kv4AttendParams {
 };
 
 cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t s);
+cudaError_t launch_kv_fork(const KvForkParams &p, cudaStream_t s);
+cudaError_t launch_kv_compact(const KvCompactParams &p, cudaStream_t s);
+cudaError_t launch_kv_copy(const KvCopyParams &p, cudaStream_t s);
 cudaError_t launch_kv4_append(const Kv4AppendParams &p, int D, cudaStream_t s);
 cudaError_t launch_kv4_read(const Kv4ReadParams &p, int D, cudaStream_t s);
 size_t kv4_attend_workspace_bytes(const Kv4Geom &g, int N, int max_q);

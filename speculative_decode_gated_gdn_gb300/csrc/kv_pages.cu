@@ -1,0 +1,292 @@
+// kv_pages.cu -- pages of the attention cache between rows: forks that share them,
+// compaction, and copies in all layers.
+//
+// A fork's row gets the source's full pages as they are (a holder more each) and a
+// page of its own for the last, partly filled one.  Rows only write behind their own
+// length, so nobody writes a shared page.
+#include "kv4.cuh"
+#include "scan.cuh"
+
+namespace gdn {
+
+namespace {
+
+// ---- forks --------------------------------------------------------------------------
+struct ForkPair {
+  int src, dst, len, want;
+  bool rows;  // two rows of the cohort
+};
+enum { kAsks, kNothing, kBadRow, kBadLen };
+
+__device__ __forceinline__ ForkPair fork_pair(const KvForkParams &p, int i) {
+  ForkPair r;
+  r.src = p.src_rows[i], r.dst = p.dst_rows[i], r.len = p.lens[i];
+  const int P = 1 << p.log2P;
+  r.want = int(((long long)r.len + P - 1) >> p.log2P);
+  r.rows = r.src >= 0 && r.src < p.B && r.dst >= 0 && r.dst < p.B && r.src != r.dst;
+  return r;
+}
+
+// Which pairs hold, and their last pages.  An empty row goes to the first pair that
+// asks for it: each leaves its index less n in the row's count, and the least stays.
+__global__ void __launch_bounds__(kScanThreads) kv_fork_kernel(const KvForkParams p) {
+  __shared__ long long s_warp[32];
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int count0 = min(max(*p.free_count, 0), p.n_pages);
+  // a pair's verdict stands in copy_src until its page does; its thread is the same both times
+  for (int i = tid; i < p.n; i += kScanThreads) {
+    const ForkPair r = fork_pair(p, i);
+    int verdict = kBadRow;
+    if (r.len < 0 || r.want > p.max_pages) {
+      verdict = kBadLen;
+    } else if (r.rows) {
+      const int held = *(volatile int32_t *)(p.held + r.src), taken = *(volatile int32_t *)(p.held + r.dst);
+      if (held < r.want || held > p.max_pages) {
+        if (r.want > 0) verdict = kBadLen;
+        else if (taken <= 0) verdict = kNothing;
+      } else if (taken <= 0) {
+        verdict = r.len ? kAsks : kNothing;
+        if (r.len) atomicMin(p.held + r.dst, i - p.n);
+      }
+    }
+    p.copy_src[i] = verdict;
+  }
+  __syncthreads();
+  long long taken = 0;
+  for (int i0 = 0; i0 < p.n; i0 += kScanThreads) {
+    const int i = i0 + tid;
+    ForkPair r{};
+    int verdict = kNothing;
+    bool won = false;
+    if (i < p.n) {
+      r = fork_pair(p, i);
+      verdict = p.copy_src[i];
+      won = verdict == kAsks && *(volatile int32_t *)(p.held + r.dst) == i - p.n;
+    }
+    const int whole = r.len >> p.log2P, need = won && r.want > whole;
+    long long all;
+    const long long end = taken + block_scan(need, s_warp, &all);
+    if (i < p.n) {
+      int from = -2, to = -2;
+      if (won) {
+        const bool fits = !need || end <= count0;
+        if (fits) {
+          from = to = -1;
+          if (need) {
+            int32_t *cells = p.table + size_t(r.dst) * p.max_pages;
+            from = p.table[size_t(r.src) * p.max_pages + whole];
+            to = p.free_list[count0 - end];
+            cells[whole] = to;
+            if (to >= 0 && to < p.n_pages) p.refs[to] = 1;
+            else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+          }
+        } else {
+          atomicOr(p.status, GDN_STATUS_NO_PAGES);
+        }
+        p.held[r.dst] = fits ? r.want : 0;
+      } else if (verdict == kNothing) {
+        from = to = -1;
+      } else {
+        atomicOr(p.status, verdict == kBadLen ? GDN_STATUS_BAD_LEN : GDN_STATUS_BAD_ROW);
+      }
+      p.copy_src[i] = from, p.copy_dst[i] = to;
+    }
+    taken += all;
+    __syncthreads();
+  }
+  if (tid == 0) *p.free_count = count0 - int(min(taken, (long long)count0));
+}
+
+constexpr int kForkThreads = 256;
+
+// The shared pages' cells and counts, of the pairs that held.
+__global__ void __launch_bounds__(kForkThreads) kv_share_kernel(const KvForkParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x;
+  if (p.copy_src[i] == -2) return;
+  const ForkPair r = fork_pair(p, i);
+  const int whole = r.len >> p.log2P;
+  const int32_t *from = p.table + size_t(r.src) * p.max_pages;
+  int32_t *to = p.table + size_t(r.dst) * p.max_pages;
+  for (int c = blockIdx.y * kForkThreads + threadIdx.x; c < whole; c += gridDim.y * kForkThreads) {
+    const int page = from[c];
+    to[c] = page;
+    if (page >= 0 && page < p.n_pages) atomicAdd(p.refs + page, 1);
+    else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+  }
+}
+
+// ---- compaction ---------------------------------------------------------------------
+// Counts in one CTA: each warp has a stretch of the pages, four a lane and step.
+struct Stretch {
+  int begin, end;
+};
+__device__ __forceinline__ Stretch stretch_of(int warp, int n) {
+  const int steps = (n + 127) / 128, each = (steps + 31) / 32;
+  return Stretch{min(n, warp * each * 128), min(n, (warp + 1) * each * 128)};
+}
+// Which of the four pages from `at` on are in use, as bits.
+__device__ __forceinline__ uint32_t used_of(const int32_t *refs, int at, int end) {
+  if (at + 4 <= end && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+    const int4 x = *reinterpret_cast<const int4 *>(refs + at);
+    return (x.x > 0) | (x.y > 0) << 1 | (x.z > 0) << 2 | (x.w > 0) << 3;
+  }
+  uint32_t m = 0;
+  for (int j = 0; j < 4 && at + j < end; ++j) m |= uint32_t(refs[at + j] > 0) << j;
+  return m;
+}
+
+__global__ void __launch_bounds__(kScanThreads) kv_compact_kernel(const KvCompactParams p) {
+  __shared__ long long s_warp[32];
+  __shared__ int s_before[32], s_below;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const int n = p.n_pages;
+  const Stretch s = stretch_of(warp, n);
+  int count = 0;
+#pragma unroll 4
+  for (int at = s.begin + 4 * lane; at < s.end; at += 128) count += __popc(used_of(p.refs, at, s.end));
+  long long U_;
+  const long long upto = block_scan(count, s_warp, &U_);
+  if (lane == 31) s_before[warp] = int(upto);
+  __syncthreads();
+  const int U = int(U_);
+  int before = warp ? s_before[warp - 1] : 0;
+  // pages in use below place U: those behind it move into the gaps
+  if (U >= s.begin && U < s.end) {
+    int below = 0;
+    for (int at = s.begin + 4 * lane; at < U; at += 128) below += __popc(used_of(p.refs, at, U));
+    below = __reduce_add_sync(0xffffffffu, below);
+    if (lane == 0) s_below = before + below;
+  }
+  if (U == n && tid == 0) s_below = U;
+  __syncthreads();
+  const int below = s_below;
+  for (int base = s.begin; base < s.end; base += 128) {
+    const int at = base + 4 * lane;
+    const uint32_t m = at < s.end ? used_of(p.refs, at, s.end) : 0;
+    int mine = __popc(m), sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    int k = before + sum - mine;  // pages in use before place at + j
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = at + j;
+      if (i >= s.end) break;
+      const bool used = m >> j & 1;
+      p.page_map[i] = used ? i : -1;
+      if (used && i >= U) p.copy_src[k - below] = i;
+      if (!used && i < U) p.copy_dst[i - k] = i;
+      k += used;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  __syncthreads();
+  const int moves = U - below;
+  for (int j = tid; j < moves; j += kScanThreads) p.page_map[p.copy_src[j]] = p.copy_dst[j];
+  if (tid == 0) *p.copy_count = moves, *p.new_free_count = n - U;
+}
+
+constexpr int kRemapThreads = 256;
+
+// Tables, counts and the free stack by the map.  Where an output is the input itself,
+// each entry is read and written by one thread, or stands for the same either way.
+__global__ void __launch_bounds__(kRemapThreads) kv_remap_kernel(const KvCompactParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = p.n_pages, U = n - *p.new_free_count, moves = *p.copy_count;
+  const size_t step = size_t(gridDim.x) * kRemapThreads, first = size_t(blockIdx.x) * kRemapThreads + threadIdx.x;
+  for (size_t i = first; i < size_t(p.B) * p.max_pages; i += step) {
+    const int b = int(i / p.max_pages), c = int(i - size_t(b) * p.max_pages);
+    int page = p.table[i];
+    if (c < p.held[b]) {
+      page = page >= 0 && page < n ? p.page_map[page] : -1;
+      if (page < 0) atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+    }
+    p.new_table[i] = page;
+  }
+  for (size_t i = first; i < size_t(n); i += step) {
+    p.new_free_list[i] = i < size_t(n - U) ? n - 1 - int(i) : -1;
+    const int r = p.refs[i];
+    if ((r > 0) == (i < size_t(U))) p.new_refs[i] = max(r, 0);
+  }
+  for (size_t j = first; j < size_t(moves); j += step) {
+    const int from = p.copy_src[j];
+    const int r = p.refs[from];
+    p.new_refs[p.copy_dst[j]] = r;
+    p.new_refs[from] = 0;
+  }
+}
+
+// ---- copies -------------------------------------------------------------------------
+constexpr int kCopyThreads = 256, kCopyLoads = 4;
+constexpr int kCopyUnit = kCopyThreads * kCopyLoads * 16;  // bytes of a CTA's step
+
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_constant__ KvCopyParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = p.count ? min(max(*p.count, 0), p.n) : p.n;
+  const int units = (p.page_bytes + kCopyUnit - 1) / kCopyUnit;
+  const size_t total = size_t(n) * p.n_layers * units;
+  for (size_t u = blockIdx.x; u < total; u += gridDim.x) {
+    const size_t q = u / units;
+    const int part = int(u - q * units), layer = int(q / n), i = int(q - size_t(layer) * n);
+    const int from = p.src[i], to = p.dst[i];
+    if (from < 0 || to < 0) continue;
+    if (from >= p.n_pages || to >= p.n_pages) {
+      if (threadIdx.x == 0) atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+      continue;
+    }
+    const uint4 *s = reinterpret_cast<const uint4 *>(p.pages[layer] + size_t(from) * p.page_bytes);
+    uint4 *d = reinterpret_cast<uint4 *>(p.pages[layer] + size_t(to) * p.page_bytes);
+    const int words = p.page_bytes / 16, w0 = part * (kCopyUnit / 16) + threadIdx.x;
+    uint4 x[kCopyLoads];
+#pragma unroll
+    for (int j = 0; j < kCopyLoads; ++j)
+      if (w0 + j * kCopyThreads < words) x[j] = s[w0 + j * kCopyThreads];
+#pragma unroll
+    for (int j = 0; j < kCopyLoads; ++j)
+      if (w0 + j * kCopyThreads < words) d[w0 + j * kCopyThreads] = x[j];
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n > 0 ? n : 152;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const KvForkParams &p, cudaStream_t s) {
+  const cudaError_t e = launch_pdl(kv_fork_kernel, dim3(1), dim3(kScanThreads), s, p);
+  if (e != cudaSuccess) return e;
+  const int y = (p.max_pages + kForkThreads - 1) / kForkThreads;
+  return launch_pdl(kv_share_kernel, dim3(p.n, y < 16 ? y : 16), dim3(kForkThreads), s, p);
+}
+
+cudaError_t launch_kv_compact(const KvCompactParams &p, cudaStream_t s) {
+  const cudaError_t e = launch_pdl(kv_compact_kernel, dim3(1), dim3(kScanThreads), s, p);
+  if (e != cudaSuccess) return e;
+  const size_t items = size_t(p.B) * p.max_pages > size_t(p.n_pages) ? size_t(p.B) * p.max_pages : size_t(p.n_pages);
+  size_t grid = (items + kRemapThreads - 1) / kRemapThreads;
+  const size_t most = size_t(sm_count()) * 8;
+  if (grid > most) grid = most;
+  return launch_pdl(kv_remap_kernel, dim3(unsigned(grid)), dim3(kRemapThreads), s, p);
+}
+
+cudaError_t launch_kv_copy(const KvCopyParams &p, cudaStream_t s) {
+  const size_t units = size_t(p.n) * p.n_layers * ((p.page_bytes + kCopyUnit - 1) / kCopyUnit);
+  size_t grid = size_t(sm_count()) * 8;
+  if (grid > units) grid = units;
+  return launch_pdl(kv_copy_kernel, dim3(unsigned(grid)), dim3(kCopyThreads), s, p);
+}
+
+}  // namespace gdn

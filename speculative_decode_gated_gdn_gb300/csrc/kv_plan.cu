@@ -11,42 +11,24 @@
 // one CTA does the bookkeeping of all rows (scans in shared memory, pages
 // moved one a thread by a search in the scan, whichever row they belong to),
 // and, where the tokens are few, writes their slots too.
+//
+// Shared pages (refs): a page given back loses a holder, and goes onto the stack when
+// it has none left, at the place of the last of the cycle's releases of it.  Three
+// passes over the releases in their order: the counts go down; where a count has
+// reached zero, the releases of that page leave their least negative mark there, which
+// is the last one's; the release that finds its own mark pushes the page.
 #include "kv4.cuh"
+#include "scan.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = kScanThreads;
 // Tokens up to which the bookkeeping CTA writes the slots itself; a kernel of their own
 // behind it costs 16 tokens 5.8 us for 4.7, and 2048 5.6 for 5.3, but 8192 take 5.5 for
 // 7.3 and 65536 5.6 for 26.5.
 constexpr int kPlanOneCta = 2048;
-
-// Inclusive scan of v over the CTA; *total gets the sum of all threads.
-__device__ __forceinline__ long long block_scan(long long v, long long *s_warp, long long *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();  // s_warp may still be read by an earlier scan
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = s_warp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  *total = s_warp[31];
-  return v + (warp ? s_warp[warp - 1] : 0);
-}
 
 struct PlanRow {
   int len, a, held, want;
@@ -67,17 +49,6 @@ __device__ __forceinline__ PlanRow plan_row(const KvPlanParams &p, int b) {
   return r;
 }
 
-// First index i in [0, n) with ends[i] > x (ends ascending, ends[n - 1] > x).
-__device__ __forceinline__ int find_row(const int *ends, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (ends[m] > x) hi = m;
-    else lo = m + 1;
-  }
-  return lo;
-}
-
 // Slot and position of token i, -1 where no row has it.
 __device__ __forceinline__ void plan_token(const KvPlanParams &p, int i) {
   const int b = p.T > 0 ? i / p.T : find_row(p.q_start + 1, p.B, i);
@@ -94,6 +65,7 @@ __device__ __forceinline__ void plan_token(const KvPlanParams &p, int i) {
   p.positions[i] = pos;
 }
 
+template <bool SHARED>
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParams p, const int write_slots) {
   __shared__ long long s_warp[32];
   __shared__ int s_ends[kPlanThreads];   // pages that the chunk's rows move, summed up to each row
@@ -106,27 +78,70 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
 
   // ---- pages given back --------------------------------------------------------
   long long released = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-    const int b = b0 + tid, rows = min(kPlanThreads, p.B - b0);
-    PlanRow r{};
-    if (b < p.B) r = plan_row(p, b);
-    if (b < p.B && r.bad) atomicOr(p.status, GDN_STATUS_BAD_LEN);
-    const int rel = max(r.held - r.want, 0);
-    long long total;
-    const long long end = block_scan(rel, s_warp, &total);
-    if (total == 0) continue;  // the same for every thread
-    s_ends[tid] = int(end);
-    s_from[tid] = r.want;
-    __syncthreads();
-    for (int i = tid; i < int(total); i += kPlanThreads) {
-      const int w = find_row(s_ends, rows, i);
-      int32_t *cell = p.table + size_t(b0 + w) * p.max_pages + s_from[w] + i - (w ? s_ends[w - 1] : 0);
-      const long long at = count0 + released + i;
-      if (at < n_pages) p.free_list[at] = *cell;
-      else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
-      *cell = -1;
+  const int passes = SHARED ? 3 : 1;
+#pragma unroll 1
+  for (int pass = 0; pass < passes; ++pass) {
+    long long index0 = 0;  // releases of the rows before the chunk
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+      const int b = b0 + tid, rows = min(kPlanThreads, p.B - b0);
+      PlanRow r{};
+      if (b < p.B) r = plan_row(p, b);
+      if (pass == 0 && b < p.B && r.bad) atomicOr(p.status, GDN_STATUS_BAD_LEN);
+      const int rel = max(r.held - r.want, 0);
+      long long total;
+      const long long end = block_scan(rel, s_warp, &total);
+      if (total == 0) continue;  // the same for every thread
+      s_ends[tid] = int(end);
+      s_from[tid] = r.want;
+      __syncthreads();
+      for (int i0 = 0; i0 < int(total); i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int32_t *cell = nullptr;
+        int page = -1;
+        if (i < int(total)) {
+          const int w = find_row(s_ends, rows, i);
+          cell = p.table + size_t(b0 + w) * p.max_pages + s_from[w] + i - (w ? s_ends[w - 1] : 0);
+          page = *cell;
+        }
+        if (!SHARED) {
+          if (!cell) continue;
+          const long long at = count0 + released + i;
+          if (at < n_pages) p.free_list[at] = page;
+          else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+          *cell = -1;
+          continue;
+        }
+        const bool known = cell && page >= 0 && page < n_pages;
+        const int mark = -1 - int(index0 + i);
+        if (pass == 0) {
+          if (cell && !known) *cell = -1, atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+          if (known && atomicSub(p.refs + page, 1) <= 0) {  // nobody held it: not given back
+            atomicAdd(p.refs + page, 1);
+            *cell = -1;
+            atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+          }
+        } else if (pass == 1) {
+          if (known && *(volatile int32_t *)(p.refs + page) <= 0) atomicMin(p.refs + page, mark);
+        } else {
+          const bool push = known && *(volatile int32_t *)(p.refs + page) == mark;
+          long long pushed;
+          const long long place = count0 + released + block_scan(push, s_warp, &pushed) - 1;
+          if (push) {
+            if (place < n_pages) p.free_list[place] = page;
+            else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+            p.refs[page] = 0;
+          }
+          if (known) *cell = -1;
+          released += pushed;
+        }
+      }
+      if (!SHARED) released += total;
+      index0 += total;
     }
-    released += total;
+    if (SHARED) {
+      if (index0 == 0) break;  // the same for every thread
+      __syncthreads();
+    }
   }
   const long long avail = min((long long)n_pages, count0 + released);
   __syncthreads();  // the pushed pages are visible to the whole CTA
@@ -164,7 +179,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     for (int i = tid; i < int(got_total); i += kPlanThreads) {
       const int w = find_row(s_ends, rows, i);
       const long long from = avail - 1 - (taken0 + i);
-      p.table[size_t(b0 + w) * p.max_pages + s_from[w] + i - (w ? s_ends[w - 1] : 0)] = p.free_list[from];
+      const int page = p.free_list[from];
+      p.table[size_t(b0 + w) * p.max_pages + s_from[w] + i - (w ? s_ends[w - 1] : 0)] = page;
+      if (SHARED) {
+        if (page >= 0 && page < n_pages) p.refs[page] = 1;
+        else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+      }
     }
     taken0 += need_total;
     tokens0 += tok_total;
@@ -204,7 +224,7 @@ cudaError_t launch_kv_plan(const KvPlanParams &p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kv_plan_kernel), args);
+  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(p.refs ? kv_plan_kernel<true> : kv_plan_kernel<false>), args);
   if (e != cudaSuccess || one) return e;
   return launch_pdl(kv_slots_kernel, dim3((p.N + 255) / 256), dim3(256), s, p);
 }

@@ -41,7 +41,8 @@ GDN_NOALLOC_WS_BYTES = 4 << 20
 EXPORTS = ("gdn_version", "gdn_last_error", "gdn_layer_workspace_bytes", "gdn_conv_verify",
            "gdn_commit", "gdn_prefill_workspace_bytes", "gdn_prefill_chunked", "gdn_get_status",
            "gdn_conv_verify_noalloc", "gdn_flush", "gdn_accept_workspace_bytes", "gdn_accept_greedy",
-           "gdn_conv_verify_gated", "gdn_move_rows", "gdn_kv4_page_bytes", "gdn_kv_plan", "gdn_kv4_append",
+           "gdn_conv_verify_gated", "gdn_move_rows", "gdn_kv4_page_bytes", "gdn_kv_plan", "gdn_kv_plan_shared",
+           "gdn_kv_fork", "gdn_kv_compact", "gdn_kv_copy_pages", "gdn_kv4_append",
            "gdn_kv4_read", "gdn_sample", "gdn_accept_sampled",
            "gdn_accept_sampled_workspace_bytes", "gdn_kv4_attend_workspace_bytes", "gdn_kv4_attend", "gdn_test_verify_timeout",
            "gdn_test_kv4_attend_timeout")
@@ -130,6 +131,14 @@ def _declare(lib):
     lib.gdn_kv4_page_bytes.argtypes = [K]
     lib.gdn_kv_plan.restype = ctypes.c_int
     lib.gdn_kv_plan.argtypes = [K, I, I] + [_P] * 13
+    lib.gdn_kv_plan_shared.restype = ctypes.c_int
+    lib.gdn_kv_plan_shared.argtypes = [K, I, I] + [_P] * 14
+    lib.gdn_kv_fork.restype = ctypes.c_int
+    lib.gdn_kv_fork.argtypes = [K, I] + [_P] * 11
+    lib.gdn_kv_compact.restype = ctypes.c_int
+    lib.gdn_kv_compact.argtypes = [K] + [_P] * 12
+    lib.gdn_kv_copy_pages.restype = ctypes.c_int
+    lib.gdn_kv_copy_pages.argtypes = [K, I, PP, I] + [_P] * 4
     lib.gdn_kv4_append.restype = ctypes.c_int
     lib.gdn_kv4_append.argtypes = [K, I, _P, LL, _P, LL, _P, LL, _P, I, _P, I, I, ctypes.c_char_p, I, _P, _P, _P, _P]
     lib.gdn_kv4_read.restype = ctypes.c_int
@@ -522,6 +531,81 @@ def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, fre
               (kv_len, "kv_len", B, i32), (slots, "slots", N, i32), (positions, "positions", N, i32))
     rc = load().gdn_kv_plan(ctypes.byref(kd), T, N, *p, _stream(stream))
     _check(rc, "gdn_kv_plan")
+
+
+def gdn_kv_plan_shared(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, free_count, refs, q_start, q_count,
+                       kv_len, slots, positions, T=0, stream=None):
+    """gdn_kv_plan for a cache whose pages several rows may hold (gdn.h,
+    gdn_kv_plan_shared): refs [n_pages] int32, the holders of each page."""
+    torch = _t()
+    try:
+        i32, B, N = torch.int32, kd.B, slots.numel()
+    except AttributeError:
+        _need(slots=slots)
+        raise
+    p = _ptrs((lens, "lens", B, i32), (add, "add", B, i32), (active, "active", B, torch.uint8), (held, "held", B, i32),
+              (table, "table", B * kd.max_pages, i32), (free_list, "free_list", kd.n_pages, i32),
+              (free_count, "free_count", 1, i32), (refs, "refs", kd.n_pages, i32), (q_start, "q_start", B + 1, i32),
+              (q_count, "q_count", B, i32), (kv_len, "kv_len", B, i32), (slots, "slots", N, i32),
+              (positions, "positions", N, i32))
+    rc = load().gdn_kv_plan_shared(ctypes.byref(kd), T, N, *p, _stream(stream))
+    _check(rc, "gdn_kv_plan_shared")
+
+
+def gdn_kv_fork(kd: gdn_kv4_dims, src_rows, dst_rows, lens, held, table, free_list, free_count, refs, copy_src, copy_dst,
+                stream=None):
+    """Rows dst_rows continue the first lens tokens of rows src_rows (gdn.h,
+    gdn_kv_fork): int32 CUDA tensors; copy_src and copy_dst [n] are written, for
+    gdn_kv_copy_pages."""
+    i32 = _t().int32
+    try:
+        n, B = src_rows.numel(), kd.B
+    except AttributeError:
+        _need(src_rows=src_rows)
+        raise
+    p = _ptrs((src_rows, "src_rows", n, i32), (dst_rows, "dst_rows", n, i32), (lens, "lens", n, i32),
+              (held, "held", B, i32), (table, "table", B * kd.max_pages, i32), (free_list, "free_list", kd.n_pages, i32),
+              (free_count, "free_count", 1, i32), (refs, "refs", kd.n_pages, i32), (copy_src, "copy_src", n, i32),
+              (copy_dst, "copy_dst", n, i32))
+    _check(load().gdn_kv_fork(ctypes.byref(kd), n, *p, _stream(stream)), "gdn_kv_fork")
+
+
+def gdn_kv_compact(kd: gdn_kv4_dims, held, table, refs, new_table, new_refs, new_free_list, new_free_count, page_map,
+                   copy_src, copy_dst, copy_count, stream=None):
+    """Places for the pages in use at the cache's front (gdn.h, gdn_kv_compact):
+    int32 CUDA tensors; new_table and new_refs may be table and refs, copy_src and
+    copy_dst have n_pages / 2 elements or more."""
+    i32, B, n = _t().int32, kd.B, kd.n_pages
+    try:
+        size = copy_src.numel()
+    except AttributeError:
+        _need(copy_src=copy_src)
+        raise
+    if size < max(n // 2, 1):
+        raise ValueError(f"copy_src: {size} elements, needs {max(n // 2, 1)}")
+    p = _ptrs((held, "held", B, i32), (table, "table", B * kd.max_pages, i32), (refs, "refs", n, i32),
+              (new_table, "new_table", B * kd.max_pages, i32), (new_refs, "new_refs", n, i32),
+              (new_free_list, "new_free_list", n, i32), (new_free_count, "new_free_count", 1, i32),
+              (page_map, "page_map", n, i32), (copy_src, "copy_src", size, i32), (copy_dst, "copy_dst", size, i32),
+              (copy_count, "copy_count", 1, i32))
+    _check(load().gdn_kv_compact(ctypes.byref(kd), *p, _stream(stream)), "gdn_kv_compact")
+
+
+def gdn_kv_copy_pages(kd: gdn_kv4_dims, caches, src, dst, count=None, stream=None):
+    """Page src[i] to page dst[i] in every layer's cache (gdn.h,
+    gdn_kv_copy_pages): caches, a sequence of uint8 CUDA tensors; src, dst [n]
+    int32; count [1] int32, or None for all n."""
+    i32 = _t().int32
+    try:
+        n = src.numel()
+    except AttributeError:
+        _need(src=src)
+        raise
+    sp, dp = _ptrs((src, "src", n, i32), (dst, "dst", n, i32))
+    layers = (_P * max(len(caches), 1))(*[_cache(kd, t) for t in caches])
+    rc = load().gdn_kv_copy_pages(ctypes.byref(kd), len(caches), layers, n, sp, dp,
+                                  None if count is None else _ptrs((count, "count", 1, i32))[0], _stream(stream))
+    _check(rc, "gdn_kv_copy_pages")
 
 
 def _cache(kd, pages):
