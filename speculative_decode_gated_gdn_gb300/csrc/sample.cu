@@ -2,44 +2,88 @@
 // top-k and top-p from a given random number, and the accepted prefix of a verify's
 // drafts.
 //
-// One CTA a position.  A row's values are taken in windows of 2048 places of the
-// order, from the largest down: the CTA counts the row's logits in the window in
-// shared memory, sums counts and masses over it, and stops where the question at hand
-// is answered: which value ends the first k, which ends the first p of the mass, which
-// one u falls on.  Windows begin at the next value that the row has.
+// A position belongs to a cluster of C CTAs, each with a slice of its logits, which are
+// read once:
+//   1. From its slice's first 8192 logits each CTA bounds what can matter: nothing
+//      whose weight rounds to 0 or is below min_p, and, with top_k, nothing below a
+//      value that the first k reach for sure (each warp's ceil(k / warps)-th largest of
+//      its granules' maxima, the least of them).
+//   2. The logits that pass are counted by value in shared memory: 2048 magnitudes, the
+//      16 binades below the largest, of either sign, in the order of the row.  What lies
+//      between the two signs' magnitudes, near zero, is rare and goes to a list.
+//   3. The CTAs add up their counts, each a part of the values, and form counts and
+//      masses of groups of 16 values for the first CTA, which asks them where the first
+//      k end, where p of the mass ends, and where u falls.
+//   4. It finds that value's logit in the slice that has it.
+// A logit above all of the 16 binades makes the counting begin again with others; an
+// answer near zero is looked for in windows of 2048 values over the row.
+#include <cooperative_groups.h>
+
 #include "sample.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kWindow = 2048;
-constexpr int kPer = kWindow / kThreads;  // places of a thread
+namespace cg = cooperative_groups;
 
 typedef unsigned long long u64;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kLoads = 4;                     // granules of a thread and tile
+constexpr int kTile = kThreads * kLoads;      // granules of a tile
+constexpr int kMagnitudes = 2048;             // of each sign: 16 binades
+constexpr int kBins = 2 * kMagnitudes;        // in the order of the row
+constexpr int kGroup = 16;                    // bins of a group
+static_assert(kBins / kGroup == kThreads, "a group a thread");
+constexpr int kNear = 512;                    // places of the list of values near zero
+constexpr int kWindow = 2048;                 // values of a window, and logits of one value found
 
 struct Found {
   int place;       // the value
   uint32_t n;      // logits of that value up to the one that was asked for, it included
-  uint32_t count;  // logits before that value
   u64 w, mass;     // its weight; the mass before that value
-  int hit;         // 0: not within what the row has; count and mass are of all
+  int hit;
+};
+
+// What a CTA tells the others of its cluster.
+struct Told {
+  float top, low, bound;  // largest and least number, bound of what matters
+  int beyond;             // largest magnitude that had no bin, 0 if none
 };
 
 struct Shared {
-  uint32_t hist[kWindow];
+  uint32_t hist[kBins];
+  uint32_t sum[kBins];      // the cluster's (where it has more than one CTA); first CTA
+  uint32_t window[kWindow];
+  uint16_t near[kNear];
   u64 table[32];
-  u64 warp_mass[kWarps];
-  uint32_t warp_count[kWarps];
-  int low;     // least place behind the window
-  int place;   // least place of the row
+  u64 group_mass[kThreads];
+  uint32_t group_count[kThreads];
+  u64 near_mass, warp_mass[kWarps];
+  uint32_t near_count, warp_count[kWarps];  // near_count: of the cluster, first CTA
+  float warp_top[kWarps], warp_low[kWarps], warp_bound[kWarps];
+  Told told[2][8];          // by rank: before and after the counts
+  Scale scale;
+  u64 least;
+  uint32_t near_n;          // of this CTA's list
+  int beyond, next, at, last;
+  uint32_t matches;
+  u64 before_mass;
+  uint32_t before_count;
   Found found;
-  int last;
 };
 
 enum Question { kCount, kMassReaches, kMassPasses };
+
+__device__ __forceinline__ bool answers(Question what, u64 target, u64 count, u64 count1, u64 mass, u64 mass1) {
+  return what == kCount ? count < target && target <= count1
+                        : what == kMassReaches ? mass < target && target <= mass1 : mass <= target && target < mass1;
+}
+__device__ __forceinline__ uint32_t number_of(Question what, u64 target, u64 count, u64 mass, u64 w) {
+  return what == kCount ? uint32_t(target - count) : what == kMassReaches ? uint32_t((target - mass + w - 1) / w) : uint32_t((target - mass) / w) + 1;
+}
 
 // Inclusive sums over the CTA of (count, mass).
 __device__ __forceinline__ void scan(uint32_t &count, u64 &mass, Shared &s) {
@@ -50,96 +94,83 @@ __device__ __forceinline__ void scan(uint32_t &count, u64 &mass, Shared &s) {
     const u64 b = __shfl_up_sync(0xffffffffu, mass, o);
     if (lane >= o) count += a, mass += b;
   }
+  __syncthreads();
   if (lane == 31) s.warp_count[warp] = count, s.warp_mass[warp] = mass;
   __syncthreads();
   for (int w = 0; w < warp; ++w) count += s.warp_count[w], mass += s.warp_mass[w];
 }
 
-// The first value, among those with weight >= least, at which the number of logits (kCount) or
-// their mass reaches the target, or their mass passes it.
-__device__ Found find(const SampleRow &row, int top, Scale c, u64 least, Question what, u64 target, Shared &s) {
+// The answer among the values at places [from, end), in windows over the row, with count0 and
+// mass0 before them.  Rare, and as slow as windows are many.
+__device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int end, int top, uint32_t count0, u64 mass0, Question what,
+                                             u64 target, Shared &s) {
   const int tid = threadIdx.x;
-  int from = top;
-  uint32_t count0 = 0;
-  u64 mass0 = 0;
-  for (;;) {
+  constexpr int kPer = kWindow / kThreads;
+  while (from < end) {
     __syncthreads();
-    for (int i = tid; i < kWindow; i += kThreads) s.hist[i] = 0;
-    if (tid == 0) s.low = kPlaceEnd, s.found.hit = 0;
+    for (int i = tid; i < kWindow; i += kThreads) s.window[i] = 0;
+    if (tid == 0) s.next = end, s.found.hit = 0;
     __syncthreads();
-    int low = kPlaceEnd;
+    int next = end;
     for (int g = tid; g < row.granules; g += kThreads) {
       const uint4 q = row.load(g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = place_of(half_of(q, j)) - from;
-        if (at >= 0 && at < kWindow) atomicAdd(&s.hist[at], 1u);
-        else if (at >= kWindow) low = min(low, at + from);
+        const int place = place_of(half_of(q, j));
+        if (place < from || place >= end) continue;
+        if (place - from < kWindow) atomicAdd(&s.window[place - from], 1u);
+        else next = min(next, place);
       }
     }
-    if (low < kPlaceEnd) atomicMin(&s.low, low);
+    if (next < end) atomicMin(&s.next, next);
     __syncthreads();
-    u64 w[kPer];
-    uint32_t n[kPer], count = 0;
+    uint32_t count = 0;
     u64 mass = 0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
-      const int place = from + tid * kPer + i;
-      n[i] = place < kPlaceEnd ? s.hist[tid * kPer + i] : 0;
-      w[i] = n[i] ? weight_of(place, top, c, s.table) : 0;
-      if (w[i] < least) n[i] = 0;
-      count += n[i], mass += n[i] * w[i];
+      const uint32_t n = s.window[tid * kPer + i];
+      const u64 w = n ? weight_of(from + tid * kPer + i, top, s.scale, s.table) : 0;
+      if (w >= s.least) count += n, mass += n * w;
     }
     uint32_t count1 = count;
     u64 mass1 = mass;
     scan(count1, mass1, s);
     count1 += count0, mass1 += mass0;
     count = count1 - count, mass = mass1 - mass;  // before this thread's places
-    const bool here = what == kCount ? count < target && target <= count1
-                                     : what == kMassReaches ? mass < target && target <= mass1 : mass <= target && target < mass1;
-    if (here) {
+    if (answers(what, target, count, count1, mass, mass1)) {
 #pragma unroll 1
       for (int i = 0; i < kPer; ++i) {
-        const u64 m = mass + n[i] * w[i];
-        if (n[i] && (what == kCount ? target <= count + n[i] : what == kMassReaches ? target <= m : target < m)) {
-          Found f;
-          f.place = from + tid * kPer + i, f.count = count, f.w = w[i], f.mass = mass, f.hit = 1;
-          f.n = what == kCount ? uint32_t(target - count)
-                               : what == kMassReaches ? uint32_t((target - mass + w[i] - 1) / w[i]) : uint32_t((target - mass) / w[i]) + 1;
-          s.found = f;
+        const int place = from + tid * kPer + i;
+        uint32_t n = s.window[tid * kPer + i];
+        const u64 w = n ? weight_of(place, top, s.scale, s.table) : 0;
+        if (w < s.least) n = 0;
+        if (n && answers(what, target, count, count + n, mass, mass + n * w)) {
+          s.found = Found{place, number_of(what, target, count, mass, w), w, mass, 1};
           break;
         }
-        count += n[i], mass = m;
+        count += n, mass += n * w;
       }
     }
-    if (tid == kThreads - 1) s.warp_count[0] = count1, s.warp_mass[0] = mass1;
+    if (tid == kThreads - 1) s.before_count = count1, s.before_mass = mass1;
     __syncthreads();
-    count0 = s.warp_count[0], mass0 = s.warp_mass[0];
-    from = s.low;
-    if (s.found.hit) return s.found;
-    // behind the least weight nothing counts any more
-    const u64 next = from < kPlaceEnd ? weight_of(from, top, c, s.table) : 0;
-    if (next < least || next == 0) {
-      Found f{};
-      f.count = count0, f.mass = mass0;
-      return f;
-    }
+    if (s.found.hit) return;
+    count0 = s.before_count, mass0 = s.before_mass;
+    from = s.next;
   }
 }
 
-// Index of the n-th logit (from 1) with the given place.
-__device__ int locate(const SampleRow &row, int place, uint32_t n, Shared &s) {
+// Index of the n-th logit (from 1) with the given place among granules [g0, g1), tile after tile.
+__device__ __noinline__ int locate_in_order(const SampleRow &row, int g0, int g1, int place, uint32_t n, Shared &s) {
   const int tid = threadIdx.x;
   uint32_t before = 0;
-  for (int g0 = 0; g0 < row.granules; g0 += kThreads) {
+  for (; g0 < g1; g0 += kThreads) {
     const int g = g0 + tid;
     uint32_t mask = 0;
-    if (g < row.granules) {
+    if (g < g1) {
       const uint4 q = row.load(g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) mask |= uint32_t(place_of(half_of(q, j)) == place) << j;
     }
-    __syncthreads();
     uint32_t end = __popc(mask);
     u64 none = 0;
     scan(end, none, s);
@@ -148,78 +179,413 @@ __device__ int locate(const SampleRow &row, int place, uint32_t n, Shared &s) {
       uint32_t left = n - (end - __popc(mask)), j = 0;
       for (;; ++j)
         if ((mask >> j & 1) && --left == 0) break;
-      s.last = row.first(g) + int(j);
+      s.at = row.first(g) + int(j);
     }
     __syncthreads();
     uint32_t all = 0;
     for (int w = 0; w < kWarps; ++w) all += s.warp_count[w];
     before += all;
-    if (before >= n) return s.last;
+    if (before >= n) return s.at;
   }
   return 0;
 }
 
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
-  __shared__ Shared s;
+// The same for a value that few logits have: they are listed, and counted against one another.
+__device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t n, uint32_t all, Shared &s) {
+  if (all > uint32_t(kWindow)) return locate_in_order(row, g0, g1, place, n, s);
   const int tid = threadIdx.x;
-  const int bt = blockIdx.x, b = bt / p.T;
+  __syncthreads();
+  if (tid == 0) s.matches = 0, s.at = 0;
+  __syncthreads();
+  // equal as numbers: -0 as 0, NaN never
+  const __nv_bfloat162 v = __float2bfloat162_rn(value_at(place));
+  auto same = [&](uint32_t w) { return __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w), v); };
+  for (int g = g0 + tid; g < g1; g += kTile) {
+    uint4 q[kLoads];
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r)
+      q[r] = g + r * kThreads < g1 ? row.load(g + r * kThreads) : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r) {
+      if (same(q[r].x) | same(q[r].y) | same(q[r].z) | same(q[r].w)) {
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j)
+          if (place_of(half_of(q[r], j)) == place) {
+            const uint32_t i = atomicAdd(&s.matches, 1u);
+            if (i < uint32_t(kWindow)) s.window[i] = uint32_t(row.first(g + r * kThreads) + j);
+          }
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t m = min(s.matches, uint32_t(kWindow));
+  for (uint32_t i = tid; i < m; i += kThreads) {
+    const uint32_t x = s.window[i];
+    uint32_t below = 0;
+    for (uint32_t j = 0; j < m; ++j) below += s.window[j] < x;
+    if (below + 1 == n) s.at = int(x);
+  }
+  __syncthreads();
+  return s.at;
+}
+
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ __nv_bfloat162 b2(const uint32_t &w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
+__device__ __forceinline__ float max_of(const uint4 &q) {
+  const __nv_bfloat162 m = __hmax2(__hmax2(b2(q.x), b2(q.y)), __hmax2(b2(q.z), b2(q.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float min_of(const uint4 &q) {
+  const __nv_bfloat162 m = __hmin2(__hmin2(b2(q.x), b2(q.y)), __hmin2(b2(q.z), b2(q.w)));
+  return fminf(__low2float(m), __high2float(m));
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_min(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+constexpr uint32_t kNoNumbers = 0x7fff7fffu;
+
+template <int C>
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams p) {
+  __shared__ Shared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = C > 1 ? int(cluster.block_rank()) : 0;
+  const int bt = blockIdx.x / C, b = bt / p.T;
+  auto together = [&] {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
   pdl_wait();
   pdl_trigger();
-  if (tid < 32) s.table[tid] = kExp2Table[tid];
-  if (tid == 0) s.place = 0xffff;
-  __syncthreads();
-  const bool active = !p.active || p.active[b];
+  const bool active = !p.active || p.active[b];  // the cluster agrees
   int token = -1;
   float logp = 0.f;
   if (active) {
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
     const SampleRow row(p.logits + size_t(bt) * p.stride, p.V);
-    int top = 0xffff;
-    for (int g = tid; g < row.granules; g += kThreads) {
-      const uint4 q = row.load(g);
+    const int each = (row.granules + C - 1) / C;
+    const int g0 = min(row.granules, rank * each), g1 = min(row.granules, g0 + each);
+    auto load = [&](uint4(&q)[kLoads], int g) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = min(top, place_of(half_of(q, j)));
+      for (int r = 0; r < kLoads; ++r)
+        q[r] = g + r * kThreads < g1 ? row.load(g + r * kThreads) : make_uint4(kNoNumbers, kNoNumbers, kNoNumbers, kNoNumbers);
+    };
+    uint4 first[kLoads];
+    load(first, g0 + tid);
+    for (int i = 4 * tid; i < kBins; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+
+    // ---- the row's parameters ----------------------------------------------------------
+    float temperature = p.temperature ? p.temperature[b] : 1.f;
+    float min_p = p.min_p ? p.min_p[b] : 0.f, top_p = p.top_p ? p.top_p[b] : 1.f;
+    int top_k = p.top_k ? p.top_k[b] : 0;
+    if (!(temperature > 0.f)) temperature = 0.f, min_p = 0.f, top_p = 1.f, top_k = 1;
+    min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
+    if (top_k <= 0 || top_k > p.V) top_k = p.V;
+    if (tid == 0) {
+      s.scale = temperature > 0.f ? scale_of(temperature) : Scale{0.f, 0.f};
+      s.least = u64(ceil(double(min_p) * double(kWeightOne)));
+      s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0;
     }
-    atomicMin(&s.place, top);
-    __syncthreads();
-    top = s.place;
-    __syncthreads();
-    const float temperature = p.temperature ? p.temperature[b] : 1.f;
-    if (top >= kPlaceEnd) {  // nothing above -infinity: what greedy acceptance takes, and no probability
-      token = top == kPlaceEnd ? locate(row, top, 1, s) : 0;
-      logp = -INFINITY;
-    } else if (!(temperature > 0.f)) {
-      token = locate(row, top, 1, s);
-    } else {
-      const Scale c = scale_of(temperature);
-      const float min_p = p.min_p ? p.min_p[b] : 0.f, top_p = p.top_p ? p.top_p[b] : 1.f;
-      const int top_k = p.top_k ? p.top_k[b] : 0;
-      const u64 least = min_p > 0.f ? u64(ceil(fmin(double(min_p), 1.0) * double(kWeightOne))) : 0;
-      Found f = find(row, top, c, least, kCount, top_k > 0 && top_k < p.V ? u64(top_k) : u64(p.V) + 1, s);
-      u64 mass = f.hit ? f.mass + f.n * f.w : f.mass;
-      if (top_p < 1.f) {
-        const u64 want = max(u64(1), min(mass, u64(ceil(double(fmaxf(top_p, 0.f)) * double(mass)))));
-        f = find(row, top, c, least, kMassReaches, want, s);
-        mass = f.mass + f.n * f.w;
+    if (tid < 32) s.table[tid] = kExp2Table[tid];
+
+    // ---- what can matter ----------------------------------------------------------------
+    float top = -INFINITY, low = INFINITY, bound = -INFINITY;
+    {
+      int place[kLoads];
+#pragma unroll
+      for (int r = 0; r < kLoads; ++r) {
+        const float x = max_of(first[r]);
+        top = fmaxf(top, x), low = fminf(low, min_of(first[r]));
+        place[r] = place_of(__float_as_uint(x) >> 16);
       }
-      const float u = p.u[bt];
-      const u64 at = u > 0.f ? min(mass - 1, u64(double(fminf(u, 1.f)) * double(mass))) : 0;
-      f = find(row, top, c, least, kMassPasses, at, s);
-      token = locate(row, f.place, f.n, s);
-      logp = -log1pf(float(mass - f.w) / float(f.w));
+      const int mine = (top_k + kWarps * C - 1) / (kWarps * C);
+      if (top_k < p.V && mine <= 32 * kLoads) {
+        // the least place that so many of the warp's granules reach
+        int lo = 0, hi = kPlaceEnd;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          int n = 0;
+#pragma unroll
+          for (int r = 0; r < kLoads; ++r) n += place[r] <= mid;
+          if (int(__reduce_add_sync(0xffffffffu, unsigned(n))) >= mine) hi = mid;
+          else lo = mid + 1;
+        }
+        if (lo < kPlaceEnd) bound = value_at(lo);
+      }
+      top = warp_max(top), low = warp_min(low);
+      if (lane == 0) s.warp_top[warp] = top, s.warp_low[warp] = low, s.warp_bound[warp] = bound;
     }
+    __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all of them do
+    if (tid < C) {
+      Told t{s.warp_top[0], s.warp_low[0], s.warp_bound[0], 0};
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w)
+        t.top = fmaxf(t.top, s.warp_top[w]), t.low = fminf(t.low, s.warp_low[w]), t.bound = fminf(t.bound, s.warp_bound[w]);
+      (C > 1 ? cluster.map_shared_rank(s.told[0], tid) : s.told[0])[rank] = t;
+    }
+    together();
+    top = s.told[0][0].top, low = s.told[0][0].low, bound = s.told[0][0].bound;
+#pragma unroll
+    for (int i = 1; i < C; ++i) top = fmaxf(top, s.told[0][i].top), low = fminf(low, s.told[0][i].low), bound = fminf(bound, s.told[0][i].bound);
+    // Weights under 2^-44 count as 0: 46 ln 2 temperatures below the largest.  Rounding moves these
+    // bounds by far less than a step of bf16, and never above the largest.
+    if (top > -INFINITY && top < INFINITY) {
+      bound = fmaxf(bound, top - 31.9f * temperature);
+      if (min_p > 0.f) bound = fmaxf(bound, top + temperature * __logf(min_p) - (1e-3f * temperature + 1e-6f * fabsf(top)));
+    } else if (top == INFINITY) {
+      bound = INFINITY;
+    }
+    bound = fmaxf(bound, -3.3895314e38f);  // the least finite number
+    // the largest magnitude that may come; where more is read than was looked at, of twice that
+    uint32_t magnitude = (__float_as_uint(fmaxf(fabsf(top), fabsf(fmaxf(low, bound)))) >> 16);
+    if (!(top > -INFINITY)) magnitude = 0;
+    int binade = int(magnitude >> 7) + (each > kTile);
+
+    // ---- counts by value ------------------------------------------------------------------
+    int base;
+    for (;;) {
+      base = max(0, ((min(binade, 255) + 1) << 7) - kMagnitudes);
+      const uint32_t from = uint32_t(base);
+      auto take = [&](const uint4 &q) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float f = (j & 1) ? hi_of(w[j >> 1]) : lo_of(w[j >> 1]);
+          if (f >= bound) {
+            const uint32_t bits = __float_as_uint(f) >> 16, a = bits & 0x7fffu, off = a - from;
+            const bool minus = bits > 0x8000u;
+            if (off < uint32_t(kMagnitudes)) {
+              atomicAdd(&s.hist[minus ? kMagnitudes + off : kMagnitudes - 1 - off], 1u);
+            } else if (a < from) {
+              const uint32_t i = atomicAdd(&s.near_n, 1u);
+              if (i < uint32_t(kNear)) s.near[i] = uint16_t(place_of(bits));
+            } else {
+              atomicMax(&s.beyond, int(a));
+            }
+          }
+        }
+      };
+      float most = -INFINITY;
+      auto look = [&](const uint4(&q)[kLoads]) {
+#pragma unroll
+        for (int r = 0; r < kLoads; ++r) {
+          const float x = max_of(q[r]);
+          most = fmaxf(most, x);
+          if (x >= bound) take(q[r]);
+        }
+      };
+      uint4 next[kLoads];
+      int g = g0 + tid + kTile;
+      if (g - tid < g1) load(next, g);
+      look(first);
+      for (; g - tid < g1; g += kTile) {
+        uint4 q[kLoads];
+#pragma unroll
+        for (int r = 0; r < kLoads; ++r) q[r] = next[r];
+        if (g - tid + kTile < g1) load(next, g + kTile);
+        look(q);
+      }
+      most = warp_max(most);
+      if (lane == 0) s.warp_top[warp] = most;
+      __syncthreads();
+      if (tid < C) {
+        Told t{s.warp_top[0], 0.f, 0.f, s.beyond};
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) t.top = fmaxf(t.top, s.warp_top[w]);
+        (C > 1 ? cluster.map_shared_rank(s.told[1], tid) : s.told[1])[rank] = t;
+      }
+      together();
+      top = s.told[1][0].top;
+      int beyond = s.told[1][0].beyond;
+#pragma unroll
+      for (int i = 1; i < C; ++i) top = fmaxf(top, s.told[1][i].top), beyond = max(beyond, s.told[1][i].beyond);
+      if (!beyond) break;
+      // once more, with the bins that hold the largest of all
+      binade = beyond >> 7;
+      together();  // everybody has read what was told
+      for (int i = 4 * tid; i < kBins; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+      if (tid == 0) s.near_n = 0, s.beyond = 0;
+      __syncthreads();
+    }
+
+    if (!(top > -INFINITY)) {  // nothing above -infinity: what greedy acceptance takes, and no probability
+      if (rank == 0) token = locate_in_order(row, 0, row.granules, kPlaceEnd, 1, s);
+      logp = -INFINITY;
+    } else {
+      const int best = place_of(__float_as_uint(top) >> 16);
+      const Scale scale = s.scale;
+      const u64 least = s.least;
+      auto place_at = [&](int bin) { return bin < kMagnitudes ? kPlaceZero - base - (kMagnitudes - 1 - bin) : 0x8000 + base + bin - kMagnitudes; };
+      Shared &s0 = C > 1 ? *cluster.map_shared_rank(&s, 0) : s;
+
+      // ---- the cluster's counts, and its groups' counts and masses ---------------------------
+      uint32_t *sum = C > 1 ? s.sum : s.hist;  // in the first CTA
+      {
+        constexpr int kMine = kGroup / C;  // bins of a thread
+        const int bin = rank * (kBins / C) + tid * kMine;
+        uint32_t n[kMine] = {};
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          const uint32_t *h = (C > 1 ? cluster.map_shared_rank(s.hist, i) : s.hist) + bin;
+          if (kMine == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(h);
+            n[0] += x.x, n[1 % kMine] += x.y;
+          } else {
+#pragma unroll
+            for (int j = 0; j < kMine / 4; ++j) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(h + 4 * j);
+              n[4 * j % kMine] += x.x, n[(4 * j + 1) % kMine] += x.y, n[(4 * j + 2) % kMine] += x.z, n[(4 * j + 3) % kMine] += x.w;
+            }
+          }
+        }
+        uint32_t count = 0;
+        u64 mass = 0;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+          if (n[j]) {
+            const u64 w = weight_of(place_at(bin + j), best, scale, s.table);
+            if (w < least) n[j] = 0;
+            count += n[j], mass += n[j] * w;
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < C; o <<= 1) count += __shfl_xor_sync(0xffffffffu, count, o), mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        if (tid % C == 0) s0.group_count[bin / kGroup] = count, s0.group_mass[bin / kGroup] = mass;
+        if (C > 1) {
+#pragma unroll
+          for (int j = 0; j < kMine; ++j) s0.sum[bin + j] = n[j];
+        } else if (least) {
+#pragma unroll
+          for (int j = 0; j < kMine; ++j) s.hist[bin + j] = n[j];
+        }
+      }
+      // values near zero: from the list, or, where it was too short, from the slice once more
+      const uint32_t near_n = s.near_n;
+      if (near_n) {
+        uint32_t count = 0;
+        u64 mass = 0;
+        auto add = [&](int place) {
+          const u64 w = weight_of(place, best, scale, s.table);
+          if (w >= least) ++count, mass += w;
+        };
+        if (near_n <= uint32_t(kNear)) {
+          for (uint32_t i = tid; i < near_n; i += kThreads) add(s.near[i]);
+        } else {
+          for (int g = g0 + tid; g < g1; g += kThreads) {
+            const uint4 q = row.load(g);
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t bits = half_of(q, j);
+              if (int(bits & 0x7fffu) < base && bf2f(uint16_t(bits)) >= bound) add(place_of(bits));
+            }
+          }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o), mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        if (lane == 0 && count) atomicAdd(&s0.near_count, count), atomicAdd(&s0.near_mass, mass);
+      }
+      together();
+
+      if (rank == 0) {
+        // ---- three questions ------------------------------------------------------------------
+        const uint32_t count = s.group_count[tid];
+        const u64 mass = s.group_mass[tid];
+        uint32_t count1 = count;
+        u64 mass1 = mass;
+        scan(count1, mass1, s);
+        if (tid == kThreads / 2 - 1) s.before_count = count1, s.before_mass = mass1;  // before the values near zero
+        if (tid >= kThreads / 2) count1 += s.near_count, mass1 += s.near_mass;
+        if (tid == kThreads - 1) s.warp_count[0] = count1, s.warp_mass[0] = mass1;
+        __syncthreads();
+        const uint32_t near_at = s.before_count, total_count = s.warp_count[0];
+        const u64 near_mass_at = s.before_mass, total = s.warp_mass[0];
+        __syncthreads();
+        auto find = [&](Question what, u64 target) -> Found {
+          if (tid == 0) s.at = -1, s.found = Found{best, 1, kWeightOne, 0, 0};
+          __syncthreads();
+          if (answers(what, target, count1 - count, count1, mass1 - mass, mass1))
+            s.at = tid, s.before_count = count1 - count, s.before_mass = mass1 - mass;
+          __syncthreads();
+          const int at = s.at;
+          if (at < 0) {
+            find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, near_at, near_mass_at, what, target, s);
+          } else if (warp == 0) {
+            const int bin = at * kGroup + (lane & 15), place = place_at(bin);
+            const uint32_t n = lane < 16 ? sum[bin] : 0;
+            const u64 w = n ? weight_of(place, best, scale, s.table) : 0;
+            uint32_t c1 = n;
+            u64 m1 = n * w;
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) {
+              const uint32_t x = __shfl_up_sync(0xffffffffu, c1, o);
+              const u64 y = __shfl_up_sync(0xffffffffu, m1, o);
+              if (lane >= o) c1 += x, m1 += y;
+            }
+            c1 += s.before_count, m1 += s.before_mass;
+            if (n && answers(what, target, c1 - n, c1, m1 - n * w, m1))
+              s.found = Found{place, number_of(what, target, c1 - n, m1 - n * w, w), w, m1 - n * w, 1};
+          }
+          __syncthreads();
+          return s.found;
+        };
+        u64 rest = total;
+        if (u64(top_k) < total_count) {
+          const Found f = find(kCount, u64(top_k));
+          rest = f.mass + f.n * f.w;
+          __syncthreads();
+        }
+        if (top_p < 1.f) {
+          const Found f = find(kMassReaches, max(u64(1), min(rest, u64(ceil(double(fmaxf(top_p, 0.f)) * double(rest))))));
+          rest = f.mass + f.n * f.w;
+          __syncthreads();
+        }
+        const float u = p.u[bt];
+        const Found f = find(kMassPasses, u > 0.f ? min(rest - 1, u64(double(fminf(u, 1.f)) * double(rest))) : 0);
+        __syncthreads();
+        logp = -log1pf(float(rest - f.w) / float(f.w));
+
+        // ---- the logit ---------------------------------------------------------------------------
+        const int a = f.place <= kPlaceZero ? kPlaceZero - f.place : f.place - 0x8000;
+        if (a < base) {
+          token = locate_in_order(row, 0, row.granules, f.place, f.n, s);
+        } else {
+          const int bin = f.place <= kPlaceZero ? kMagnitudes - 1 - (a - base) : kMagnitudes + a - base;
+          uint32_t n = f.n, all = s.hist[bin];
+          int q = 0;
+          if (C > 1) {
+            while (q < C - 1 && n > all) n -= all, ++q, all = cluster.map_shared_rank(s.hist, q)[bin];
+          }
+          const int from = min(row.granules, q * each);
+          token = locate(row, from, min(row.granules, from + each), f.place, n, all, s);
+        }
+      }
+    }
+    if (C > 1) cluster.sync();  // the first CTA has read what it needs of the others
   }
+  if (rank != 0) return;
   if (tid == 0) {
     if (p.token) p.token[bt] = token;
     if (p.logp) p.logp[bt] = logp;
   }
   if (!p.draft) return;
 
-  // ---- acceptance: the row's last CTA decides -------------------------------------------
+  // ---- acceptance: the row's last position decides ------------------------------------------
   if (tid == 0) {
     p.ws_token[bt] = token;
     __threadfence();  // the token is visible before it is counted
-    s.last = atomicAdd(&p.ws_count[b], 1u) + 1u == uint32_t(p.T);
-    if (s.last) {
+    if (atomicAdd(&p.ws_count[b], 1u) + 1u == uint32_t(p.T)) {
       __threadfence();
       int k = 0;
       if (active) {
@@ -233,6 +599,22 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   }
 }
 
+template <int C>
+cudaError_t launch(const SampleParams &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.B) * unsigned(p.T) * C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<C>, p);
+}
+
 }  // namespace
 
 size_t accept_sampled_workspace_bytes(int B, int T) {
@@ -240,7 +622,15 @@ size_t accept_sampled_workspace_bytes(int B, int T) {
 }
 
 cudaError_t launch_sample(const SampleParams &p, cudaStream_t s) {
-  return launch_pdl(sample_kernel, dim3(p.B * p.T), dim3(kThreads), s, p);
+  const int rows = p.B * p.T;
+  int C = 8;
+  while (C > 1 && (rows * C > 608 || p.V < 2048 * C)) C /= 2;
+  switch (C) {
+    case 8: return launch<8>(p, s);
+    case 4: return launch<4>(p, s);
+    case 2: return launch<2>(p, s);
+    default: return launch<1>(p, s);
+  }
 }
 
 }  // namespace gdn
