@@ -35,10 +35,10 @@ constexpr int kLoads = 4;                     // granules of a thread and tile
 constexpr int kTile = kThreads * kLoads;      // granules of a tile
 constexpr int kMagnitudes = 2048;             // of each sign: 16 binades
 constexpr int kBins = 2 * kMagnitudes;        // in the order of the row
-constexpr int kGroup = 16;                    // bins of a group
-static_assert(kBins / kGroup == kThreads, "a group a thread");
+constexpr int kGroups = kBins / 32;           // of 32 bins, a warp's
+constexpr int kFewGranules = 512;             // of a slice: counted without a bound of top_k
 constexpr int kNear = 512;                    // places of the list of values near zero
-constexpr int kWindow = 2048;                 // values of a window, and logits of one value found
+constexpr int kWindow = 1024;                 // values of a window, and logits of one value found
 
 struct Found {
   int place;       // the value
@@ -53,26 +53,31 @@ struct Told {
   int beyond;             // largest magnitude that had no bin, 0 if none
 };
 
+// A question about the values near zero; what = -1: there are no more.
+struct Asked {
+  int what;
+  u64 target;
+};
+
 struct Shared {
-  uint32_t hist[kBins];
+  alignas(16) uint32_t hist[kBins];
   uint32_t sum[kBins];      // the cluster's (where it has more than one CTA); first CTA
   uint32_t window[kWindow];
   uint16_t near[kNear];
   u64 table[32];
-  u64 group_mass[kThreads];
-  uint32_t group_count[kThreads];
+  u64 group_mass[kGroups];
+  uint32_t group_count[kGroups];
   u64 near_mass, warp_mass[kWarps];
   uint32_t near_count, warp_count[kWarps];  // near_count: of the cluster, first CTA
   float warp_top[kWarps], warp_low[kWarps], warp_bound[kWarps];
   Told told[2][8];          // by rank: before and after the counts
-  Scale scale;
-  u64 least;
   uint32_t near_n;          // of this CTA's list
-  int beyond, next, at, last;
+  int beyond, next, at;
   uint32_t matches;
   u64 before_mass;
   uint32_t before_count;
   Found found;
+  Asked asked;
 };
 
 enum Question { kCount, kMassReaches, kMassPasses };
@@ -82,7 +87,7 @@ __device__ __forceinline__ bool answers(Question what, u64 target, u64 count, u6
                         : what == kMassReaches ? mass < target && target <= mass1 : mass <= target && target < mass1;
 }
 __device__ __forceinline__ uint32_t number_of(Question what, u64 target, u64 count, u64 mass, u64 w) {
-  return what == kCount ? uint32_t(target - count) : what == kMassReaches ? uint32_t((target - mass + w - 1) / w) : uint32_t((target - mass) / w) + 1;
+  return what == kCount ? uint32_t(target - count) : few_in(target - mass - (what == kMassReaches), w) + 1;
 }
 
 // Inclusive sums over the CTA of (count, mass).
@@ -97,13 +102,21 @@ __device__ __forceinline__ void scan(uint32_t &count, u64 &mass, Shared &s) {
   __syncthreads();
   if (lane == 31) s.warp_count[warp] = count, s.warp_mass[warp] = mass;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) count += s.warp_count[w], mass += s.warp_mass[w];
+#pragma unroll
+  for (int w = 0; w < kWarps - 1; ++w)
+    if (w < warp) count += s.warp_count[w], mass += s.warp_mass[w];
+}
+
+// Sum over a warp of numbers under 2^63.
+__device__ __forceinline__ u64 warp_sum(u64 x) {
+  const uint32_t a = uint32_t(x) & 0x7ffffffu, b = uint32_t(x >> 27) & 0x7ffffffu, c = uint32_t(x >> 54);
+  return u64(__reduce_add_sync(0xffffffffu, a)) + (u64(__reduce_add_sync(0xffffffffu, b)) << 27) + (u64(__reduce_add_sync(0xffffffffu, c)) << 54);
 }
 
 // The answer among the values at places [from, end), in windows over the row, with count0 and
 // mass0 before them.  Rare, and as slow as windows are many.
-__device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int end, int top, uint32_t count0, u64 mass0, Question what,
-                                             u64 target, Shared &s) {
+__device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int end, int top, Scale scale, u64 least, uint32_t count0,
+                                             u64 mass0, Question what, u64 target, Shared &s) {
   const int tid = threadIdx.x;
   constexpr int kPer = kWindow / kThreads;
   while (from < end) {
@@ -129,8 +142,8 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
       const uint32_t n = s.window[tid * kPer + i];
-      const u64 w = n ? weight_of(from + tid * kPer + i, top, s.scale, s.table) : 0;
-      if (w >= s.least) count += n, mass += n * w;
+      const u64 w = n ? weight_of(from + tid * kPer + i, top, scale, s.table) : 0;
+      if (w >= least) count += n, mass += n * w;
     }
     uint32_t count1 = count;
     u64 mass1 = mass;
@@ -142,8 +155,8 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
       for (int i = 0; i < kPer; ++i) {
         const int place = from + tid * kPer + i;
         uint32_t n = s.window[tid * kPer + i];
-        const u64 w = n ? weight_of(place, top, s.scale, s.table) : 0;
-        if (w < s.least) n = 0;
+        const u64 w = n ? weight_of(place, top, scale, s.table) : 0;
+        if (w < least) n = 0;
         if (n && answers(what, target, count, count + n, mass, mass + n * w)) {
           s.found = Found{place, number_of(what, target, count, mass, w), w, mass, 1};
           break;
@@ -153,9 +166,11 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
     }
     if (tid == kThreads - 1) s.before_count = count1, s.before_mass = mass1;
     __syncthreads();
-    if (s.found.hit) return;
+    const bool hit = s.found.hit;
     count0 = s.before_count, mass0 = s.before_mass;
     from = s.next;
+    __syncthreads();  // everybody has read them
+    if (hit) return;
   }
 }
 
@@ -200,29 +215,35 @@ __device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t 
   // equal as numbers: -0 as 0, NaN never
   const __nv_bfloat162 v = __float2bfloat162_rn(value_at(place));
   auto same = [&](uint32_t w) { return __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w), v); };
-  for (int g = g0 + tid; g < g1; g += kTile) {
+  for (int g = g0 + tid; g - tid < g1; g += kTile) {  // the warp's lanes together
     uint4 q[kLoads];
 #pragma unroll
     for (int r = 0; r < kLoads; ++r)
       q[r] = g + r * kThreads < g1 ? row.load(g + r * kThreads) : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
 #pragma unroll
     for (int r = 0; r < kLoads; ++r) {
-      if (same(q[r].x) | same(q[r].y) | same(q[r].z) | same(q[r].w)) {
-#pragma unroll 1
-        for (int j = 0; j < 8; ++j)
-          if (place_of(half_of(q[r], j)) == place) {
-            const uint32_t i = atomicAdd(&s.matches, 1u);
-            if (i < uint32_t(kWindow)) s.window[i] = uint32_t(row.first(g + r * kThreads) + j);
-          }
+      const uint32_t m0 = same(q[r].x), m1 = same(q[r].y), m2 = same(q[r].z), m3 = same(q[r].w);
+      if (m0 | m1 | m2 | m3) {
+        uint32_t bits = (m0 & 0x10001u) | (m1 & 0x10001u) << 2 | (m2 & 0x10001u) << 4 | (m3 & 0x10001u) << 6;
+        bits = (bits | bits >> 15) & 0xffu;  // logit j at bit j
+        const uint32_t i = atomicAdd(&s.matches, uint32_t(__popc(bits)));
+        const int at = row.first(g + r * kThreads);
+        for (uint32_t k = i; bits && k < uint32_t(kWindow); ++k, bits &= bits - 1) s.window[k] = uint32_t(at + __ffs(bits) - 1);
       }
+      __syncwarp();
     }
   }
   __syncthreads();
   const uint32_t m = min(s.matches, uint32_t(kWindow));
+  if (tid < 4 && m + tid < uint32_t(kWindow)) s.window[m + tid] = 0xffffffffu;
+  __syncthreads();
   for (uint32_t i = tid; i < m; i += kThreads) {
     const uint32_t x = s.window[i];
     uint32_t below = 0;
-    for (uint32_t j = 0; j < m; ++j) below += s.window[j] < x;
+    for (uint32_t j = 0; j < m; j += 4) {
+      const uint4 y = *reinterpret_cast<const uint4 *>(s.window + j);
+      below += (y.x < x) + (y.y < x) + (y.z < x) + (y.w < x);
+    }
     if (below + 1 == n) s.at = int(x);
   }
   __syncthreads();
@@ -255,6 +276,24 @@ __device__ __forceinline__ float warp_min(float x) {
 
 constexpr uint32_t kNoNumbers = 0x7fff7fffu;
 
+// One more in the bin of f, if f >= bound and its magnitude has one.  Returns, where f >=
+// bound, its magnitude beyond the least that has one, in the upper half, else 0.  `bins`
+// is the address of the first bin of a negative value; positive ones lie before it, in
+// the other direction.
+__device__ __forceinline__ uint32_t count_value(float f, float bound, uint32_t least_magnitude, uint32_t bins) {
+  const int x = __float_as_int(f + 0.f);  // -0 as 0
+  const uint32_t off = (uint32_t(x) & 0x7fffffffu) - least_magnitude;
+  const uint32_t at = bins + ((off >> 14) ^ (~uint32_t(x >> 31) & ~3u));
+  uint32_t far;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ge.f32 p, %1, %2;\n setp.lt.and.u32 q, %3, %4, p;\n @q red.shared.add.u32 [%5], 1;\n"
+      " selp.u32 %0, %3, 0, p;\n}"
+      : "=r"(far)
+      : "f"(f), "f"(bound), "r"(off), "r"(uint32_t(kMagnitudes) << 16), "r"(at)
+      : "memory");
+  return far;
+}
+
 template <int C>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams p) {
   __shared__ Shared s;
@@ -283,21 +322,15 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
     };
     uint4 first[kLoads];
     load(first, g0 + tid);
-    for (int i = 4 * tid; i < kBins; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
-
-    // ---- the row's parameters ----------------------------------------------------------
     float temperature = p.temperature ? p.temperature[b] : 1.f;
     float min_p = p.min_p ? p.min_p[b] : 0.f, top_p = p.top_p ? p.top_p[b] : 1.f;
     int top_k = p.top_k ? p.top_k[b] : 0;
+    for (int i = 4 * tid; i < kBins; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+    if (tid < 32) s.table[tid] = kExp2Table[tid];
+    if (tid == 0) s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0;
     if (!(temperature > 0.f)) temperature = 0.f, min_p = 0.f, top_p = 1.f, top_k = 1;
     min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
     if (top_k <= 0 || top_k > p.V) top_k = p.V;
-    if (tid == 0) {
-      s.scale = temperature > 0.f ? scale_of(temperature) : Scale{0.f, 0.f};
-      s.least = u64(ceil(double(min_p) * double(kWeightOne)));
-      s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0;
-    }
-    if (tid < 32) s.table[tid] = kExp2Table[tid];
 
     // ---- what can matter ----------------------------------------------------------------
     float top = -INFINITY, low = INFINITY, bound = -INFINITY;
@@ -310,18 +343,18 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
         place[r] = place_of(__float_as_uint(x) >> 16);
       }
       const int mine = (top_k + kWarps * C - 1) / (kWarps * C);
-      if (top_k < p.V && mine <= 32 * kLoads) {
-        // the least place that so many of the warp's granules reach
-        int lo = 0, hi = kPlaceEnd;
+      if (each > kFewGranules && mine <= 32 * kLoads) {
+        // a place that so many of the warp's granules reach, the least but for its last five bits
+        int lo = 0, hi = kPlaceEnd >> 5;
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
           int n = 0;
 #pragma unroll
-          for (int r = 0; r < kLoads; ++r) n += place[r] <= mid;
+          for (int r = 0; r < kLoads; ++r) n += place[r] < (mid + 1) << 5;
           if (int(__reduce_add_sync(0xffffffffu, unsigned(n))) >= mine) hi = mid;
           else lo = mid + 1;
         }
-        if (lo < kPlaceEnd) bound = value_at(lo);
+        if (lo < kPlaceEnd >> 5) bound = value_at((lo << 5) + 31);
       }
       top = warp_max(top), low = warp_min(low);
       if (lane == 0) s.warp_top[warp] = top, s.warp_low[warp] = low, s.warp_bound[warp] = bound;
@@ -355,35 +388,37 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
 
     // ---- counts by value ------------------------------------------------------------------
     int base;
+    const uint32_t bins = smem_u32(s.hist + kMagnitudes);
     for (;;) {
       base = max(0, ((min(binade, 255) + 1) << 7) - kMagnitudes);
-      const uint32_t from = uint32_t(base);
-      auto take = [&](const uint4 &q) {
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float f = (j & 1) ? hi_of(w[j >> 1]) : lo_of(w[j >> 1]);
-          if (f >= bound) {
-            const uint32_t bits = __float_as_uint(f) >> 16, a = bits & 0x7fffu, off = a - from;
-            const bool minus = bits > 0x8000u;
-            if (off < uint32_t(kMagnitudes)) {
-              atomicAdd(&s.hist[minus ? kMagnitudes + off : kMagnitudes - 1 - off], 1u);
-            } else if (a < from) {
-              const uint32_t i = atomicAdd(&s.near_n, 1u);
-              if (i < uint32_t(kNear)) s.near[i] = uint16_t(place_of(bits));
-            } else {
-              atomicMax(&s.beyond, int(a));
-            }
-          }
-        }
-      };
+      const uint32_t least_magnitude = uint32_t(base) << 16;
       float most = -INFINITY;
       auto look = [&](const uint4(&q)[kLoads]) {
 #pragma unroll
         for (int r = 0; r < kLoads; ++r) {
           const float x = max_of(q[r]);
           most = fmaxf(most, x);
-          if (x >= bound) take(q[r]);
+          // branches are the warp's, so that it stays together
+          if (!__any_sync(0xffffffffu, x >= bound)) continue;
+          const uint32_t w[4] = {q[r].x, q[r].y, q[r].z, q[r].w};
+          uint32_t far = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            far = max(far, max(count_value(lo_of(w[j]), bound, least_magnitude, bins), count_value(hi_of(w[j]), bound, least_magnitude, bins)));
+          if (!__any_sync(0xffffffffu, far >= uint32_t(kMagnitudes) << 16)) continue;
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j) {  // some that matter have no bin
+            const uint32_t bits = half_of(q[r], j), a = bits & 0x7fffu;
+            if (bf2f(uint16_t(bits)) >= bound && a - uint32_t(base) >= uint32_t(kMagnitudes)) {
+              if (a < uint32_t(base)) {
+                const uint32_t i = atomicAdd(&s.near_n, 1u);
+                if (i < uint32_t(kNear)) s.near[i] = uint16_t(place_of(bits));
+              } else {
+                atomicMax(&s.beyond, int(a));
+              }
+            }
+            __syncwarp();
+          }
         }
       };
       uint4 next[kLoads];
@@ -425,51 +460,30 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
       logp = -INFINITY;
     } else {
       const int best = place_of(__float_as_uint(top) >> 16);
-      const Scale scale = s.scale;
-      const u64 least = s.least;
+      const Scale scale = temperature > 0.f ? scale_of(temperature) : Scale{0.f, 0.f};
+      const u64 least = __float2ull_ru(min_p * float(kWeightOne));  // exact before it is rounded up
       auto place_at = [&](int bin) { return bin < kMagnitudes ? kPlaceZero - base - (kMagnitudes - 1 - bin) : 0x8000 + base + bin - kMagnitudes; };
       Shared &s0 = C > 1 ? *cluster.map_shared_rank(&s, 0) : s;
 
       // ---- the cluster's counts, and its groups' counts and masses ---------------------------
       uint32_t *sum = C > 1 ? s.sum : s.hist;  // in the first CTA
-      {
-        constexpr int kMine = kGroup / C;  // bins of a thread
-        const int bin = rank * (kBins / C) + tid * kMine;
-        uint32_t n[kMine] = {};
+#pragma unroll 2
+      for (int group = rank * kWarps + warp; group < kGroups; group += C * kWarps) {
+        const int bin = group * 32 + lane;
+        uint32_t n = 0;
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-          const uint32_t *h = (C > 1 ? cluster.map_shared_rank(s.hist, i) : s.hist) + bin;
-          if (kMine == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(h);
-            n[0] += x.x, n[1 % kMine] += x.y;
-          } else {
-#pragma unroll
-            for (int j = 0; j < kMine / 4; ++j) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(h + 4 * j);
-              n[4 * j % kMine] += x.x, n[(4 * j + 1) % kMine] += x.y, n[(4 * j + 2) % kMine] += x.z, n[(4 * j + 3) % kMine] += x.w;
-            }
-          }
-        }
+        for (int i = 0; i < C; ++i) n += (C > 1 ? cluster.map_shared_rank(s.hist, i) : s.hist)[bin];
         uint32_t count = 0;
         u64 mass = 0;
-#pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          if (n[j]) {
-            const u64 w = weight_of(place_at(bin + j), best, scale, s.table);
-            if (w < least) n[j] = 0;
-            count += n[j], mass += n[j] * w;
-          }
+        if (__any_sync(0xffffffffu, n != 0)) {
+          const u64 w = weight_of(place_at(bin), best, scale, s.table);
+          if (w < least) n = 0;
+          count = __reduce_add_sync(0xffffffffu, n);
+          mass = warp_sum(n * w);
         }
-#pragma unroll
-        for (int o = 1; o < C; o <<= 1) count += __shfl_xor_sync(0xffffffffu, count, o), mass += __shfl_xor_sync(0xffffffffu, mass, o);
-        if (tid % C == 0) s0.group_count[bin / kGroup] = count, s0.group_mass[bin / kGroup] = mass;
-        if (C > 1) {
-#pragma unroll
-          for (int j = 0; j < kMine; ++j) s0.sum[bin + j] = n[j];
-        } else if (least) {
-#pragma unroll
-          for (int j = 0; j < kMine; ++j) s.hist[bin + j] = n[j];
-        }
+        if (C > 1) s0.sum[bin] = n;
+        else if (least) s.hist[bin] = n;
+        if (lane == 0) s0.group_count[group] = count, s0.group_mass[group] = mass;
       }
       // values near zero: from the list, or, where it was too short, from the slice once more
       const uint32_t near_n = s.near_n;
@@ -492,71 +506,101 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
             }
           }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o), mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        count = __reduce_add_sync(0xffffffffu, count), mass = warp_sum(mass);
         if (lane == 0 && count) atomicAdd(&s0.near_count, count), atomicAdd(&s0.near_mass, mass);
       }
       together();
 
       if (rank == 0) {
-        // ---- three questions ------------------------------------------------------------------
-        const uint32_t count = s.group_count[tid];
-        const u64 mass = s.group_mass[tid];
-        uint32_t count1 = count;
-        u64 mass1 = mass;
-        scan(count1, mass1, s);
-        if (tid == kThreads / 2 - 1) s.before_count = count1, s.before_mass = mass1;  // before the values near zero
-        if (tid >= kThreads / 2) count1 += s.near_count, mass1 += s.near_mass;
-        if (tid == kThreads - 1) s.warp_count[0] = count1, s.warp_mass[0] = mass1;
-        __syncthreads();
-        const uint32_t near_at = s.before_count, total_count = s.warp_count[0];
-        const u64 near_mass_at = s.before_mass, total = s.warp_mass[0];
-        __syncthreads();
-        auto find = [&](Question what, u64 target) -> Found {
-          if (tid == 0) s.at = -1, s.found = Found{best, 1, kWeightOne, 0, 0};
-          __syncthreads();
-          if (answers(what, target, count1 - count, count1, mass1 - mass, mass1))
-            s.at = tid, s.before_count = count1 - count, s.before_mass = mass1 - mass;
-          __syncthreads();
-          const int at = s.at;
-          if (at < 0) {
-            find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, near_at, near_mass_at, what, target, s);
-          } else if (warp == 0) {
-            const int bin = at * kGroup + (lane & 15), place = place_at(bin);
-            const uint32_t n = lane < 16 ? sum[bin] : 0;
-            const u64 w = n ? weight_of(place, best, scale, s.table) : 0;
+        // ---- three questions, asked by the first warp -------------------------------------------
+        if (warp == 0) {
+          constexpr int kMine = kGroups / 32;  // groups of a lane
+          uint32_t count[kMine], before = 0;
+          u64 mass[kMine], mass_before = 0;
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            count[i] = s.group_count[lane * kMine + i], mass[i] = s.group_mass[lane * kMine + i];
+            before += count[i], mass_before += mass[i];
+          }
+          const uint32_t own_count = before;
+          const u64 own_mass = mass_before;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
+            const u64 y = __shfl_up_sync(0xffffffffu, mass_before, o);
+            if (lane >= o) before += x, mass_before += y;
+          }
+          const uint32_t near_at = __shfl_sync(0xffffffffu, before, 15);  // before the values near zero
+          const u64 near_mass_at = __shfl_sync(0xffffffffu, mass_before, 15);
+          if (lane >= 16) before += s.near_count, mass_before += s.near_mass;
+          const uint32_t total_count = __shfl_sync(0xffffffffu, before, 31);
+          const u64 total = __shfl_sync(0xffffffffu, mass_before, 31);
+          before -= own_count, mass_before -= own_mass;
+          auto find = [&](Question what, u64 target) -> Found {
+            int group = -1;
+            uint32_t c0 = before, c = 0;
+            u64 m0 = mass_before, m = 0;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+              if (answers(what, target, c0, c0 + count[i], m0, m0 + mass[i])) group = lane * kMine + i, c = c0, m = m0;
+              c0 += count[i], m0 += mass[i];
+            }
+            const uint32_t who = __ballot_sync(0xffffffffu, group >= 0);
+            Found f{best, 1, kWeightOne, 0, 0};
+            if (!who) {  // among the values near zero: the whole CTA looks
+              if (lane == 0) s.asked = Asked{what, target}, s.found = f, s.before_count = near_at, s.before_mass = near_mass_at;
+              __syncthreads();
+              find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, near_at, near_mass_at, what, target, s);
+              return s.found;
+            }
+            const int lead = __ffs(who) - 1;
+            group = __shfl_sync(0xffffffffu, group, lead);
+            c = __shfl_sync(0xffffffffu, c, lead), m = __shfl_sync(0xffffffffu, m, lead);
+            const int bin = group * 32 + lane, place = place_at(bin);
+            const uint32_t n = sum[bin];
+            const u64 w = weight_of(place, best, scale, s.table);
             uint32_t c1 = n;
             u64 m1 = n * w;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) {
+            for (int o = 1; o < 32; o <<= 1) {
               const uint32_t x = __shfl_up_sync(0xffffffffu, c1, o);
               const u64 y = __shfl_up_sync(0xffffffffu, m1, o);
               if (lane >= o) c1 += x, m1 += y;
             }
-            c1 += s.before_count, m1 += s.before_mass;
-            if (n && answers(what, target, c1 - n, c1, m1 - n * w, m1))
-              s.found = Found{place, number_of(what, target, c1 - n, m1 - n * w, w), w, m1 - n * w, 1};
+            c1 += c, m1 += m;
+            const bool here = n && answers(what, target, c1 - n, c1, m1 - n * w, m1);
+            if (here) f = Found{place, number_of(what, target, c1 - n, m1 - n * w, w), w, m1 - n * w, 1};
+            const uint32_t whose = __ballot_sync(0xffffffffu, here);
+            const int from = whose ? __ffs(whose) - 1 : 0;
+            f.place = __shfl_sync(0xffffffffu, f.place, from), f.n = __shfl_sync(0xffffffffu, f.n, from);
+            f.w = __shfl_sync(0xffffffffu, f.w, from), f.mass = __shfl_sync(0xffffffffu, f.mass, from);
+            return f;
+          };
+          u64 rest = total;
+          if (uint32_t(top_k) < total_count) {
+            const Found f = find(kCount, u64(top_k));
+            rest = f.mass + f.n * f.w;
           }
+          if (top_p < 1.f) {
+            const Found f = find(kMassReaches, max(u64(1), share_of(fmaxf(top_p, 0.f), rest, true)));
+            rest = f.mass + f.n * f.w;
+          }
+          const float u = p.u[bt];
+          const Found f = find(kMassPasses, u > 0.f ? (u < 1.f ? share_of(u, rest, false) : rest - 1) : 0);
+          logp = -log1pf(float(rest - f.w) / float(f.w));
+          if (lane == 0) s.asked.what = -1, s.found = f;
           __syncthreads();
-          return s.found;
-        };
-        u64 rest = total;
-        if (u64(top_k) < total_count) {
-          const Found f = find(kCount, u64(top_k));
-          rest = f.mass + f.n * f.w;
-          __syncthreads();
+        } else {
+          for (;;) {
+            __syncthreads();
+            const Asked a = s.asked;
+            if (a.what < 0) break;
+            find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, s.before_count, s.before_mass, Question(a.what), a.target, s);
+          }
         }
-        if (top_p < 1.f) {
-          const Found f = find(kMassReaches, max(u64(1), min(rest, u64(ceil(double(fmaxf(top_p, 0.f)) * double(rest))))));
-          rest = f.mass + f.n * f.w;
-          __syncthreads();
-        }
-        const float u = p.u[bt];
-        const Found f = find(kMassPasses, u > 0.f ? min(rest - 1, u64(double(fminf(u, 1.f)) * double(rest))) : 0);
-        __syncthreads();
-        logp = -log1pf(float(rest - f.w) / float(f.w));
 
         // ---- the logit ---------------------------------------------------------------------------
+        const Found f = s.found;
         const int a = f.place <= kPlaceZero ? kPlaceZero - f.place : f.place - 0x8000;
         if (a < base) {
           token = locate_in_order(row, 0, row.granules, f.place, f.n, s);
@@ -624,7 +668,7 @@ size_t accept_sampled_workspace_bytes(int B, int T) {
 cudaError_t launch_sample(const SampleParams &p, cudaStream_t s) {
   const int rows = p.B * p.T;
   int C = 8;
-  while (C > 1 && (rows * C > 608 || p.V < 2048 * C)) C /= 2;
+  while (C > 1 && (rows * C > (C > 2 ? 608 : 1216) || p.V < 2048 * C)) C /= 2;
   switch (C) {
     case 8: return launch<8>(p, s);
     case 4: return launch<4>(p, s);

@@ -66,12 +66,35 @@ struct Scale {
   float hi, lo;  // 2 / (temperature * ln 2); 0: every weight is 1
 };
 
+// The quotient's remainder is exact by fma, so hi + lo is within 2^-46 of it.
 __device__ __forceinline__ Scale scale_of(float temperature) {
-  const double c = 2.8853900817779268147 / double(temperature);
+  constexpr float k = 2.88539004f, k_lo = 3.851926067e-8f;  // 2 / ln 2
   Scale s;
-  s.hi = float(c);
-  s.lo = isinf(s.hi) ? 0.f : float(c - double(s.hi));
+  s.hi = __fdiv_rn(k, temperature);
+  s.lo = isinf(s.hi) ? 0.f : __fdiv_rn(fmaf(-s.hi, temperature, k) + k_lo, temperature);
   return s;
+}
+
+// x * mass for 0 <= x < 1, rounded down or up, exactly.
+__device__ __forceinline__ unsigned long long share_of(float x, unsigned long long mass, bool up) {
+  const uint32_t bits = __float_as_uint(x);
+  const uint32_t e = max(bits >> 23, 1u), m = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
+  const unsigned long long lo = m * mass, hi = __umul64hi(m, mass);
+  const uint32_t shift = 150 - e;  // 24 .. 149
+  if (shift >= 128) return up && m && mass;
+  unsigned long long q, rest;
+  if (shift >= 64) q = hi >> (shift - 64), rest = lo | (shift > 64 ? hi << (128 - shift) : 0);
+  else q = hi << (64 - shift) | lo >> shift, rest = lo << (64 - shift);
+  return q + (up && rest);
+}
+
+// floor(a / b) where it is at most 2^20; 0 < b, a < 2^63.  The quotient of the rounded
+// numbers is within 2^-21 of itself, so less than one off.
+__device__ __forceinline__ uint32_t few_in(unsigned long long a, unsigned long long b) {
+  uint32_t q = uint32_t(__fdividef(__ull2float_rn(a), __ull2float_rn(b)));
+  if (q * b > a) --q;
+  else if ((q + 1ull) * b <= a) ++q;
+  return q;
 }
 
 // exp((value_at(place) - value_at(top)) / temperature) in units of 2^-43, rounded; top <= place.
