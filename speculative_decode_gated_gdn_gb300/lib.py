@@ -191,9 +191,22 @@ def _ptr(t, what, dtype=None):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
+    """The stream's handle; by default torch's current stream of the current
+    device, asked for without making a Stream object (2.9 us of a small call's
+    10, 0.2 this way)."""
+    global _raw_stream
     if stream is None:
-        return _t().cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            torch = _t()
+            handle = torch.cuda.current_stream().cuda_stream  # initialises CUDA, or says why it cannot
+            device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+            _raw_stream = lambda: raw(device())
+            return handle
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -390,37 +403,44 @@ def gdn_accept_greedy(logits, draft, active, keep, nxt, ws, stream=None):
 def _logits(t, dims):
     """Pointer and position stride of [B][V] or [B][T][V] bf16 logits whose
     positions lie at equal distances (a slice of a padded vocabulary serves)."""
-    _need(logits=t)
-    if not t.is_cuda:
-        raise ValueError("logits: tensor must be on a CUDA device")
-    if t.dtype != _t().bfloat16:
-        raise TypeError(f"logits: expected {_t().bfloat16}, got {t.dtype}")
-    if t.dim() != dims:
-        raise ValueError(f"logits: expected {dims} dimensions, got {tuple(t.shape)}")
-    *shape, V = t.shape
-    *strides, one = t.stride()
-    n = 1  # positions at and behind a dimension
-    s = max(V, 1)
-    for size, stride in zip(reversed(shape), reversed(strides)):
-        if size > 1:
-            if n == 1:
-                s = stride
-            elif stride != n * s:
-                raise ValueError("logits: positions must lie at equal distances")
-            n *= size
-    if one != 1 and V > 1:
+    torch = _t()
+    try:
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"logits: expected {torch.bfloat16}, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError("logits: tensor must be on a CUDA device")
+        shape, stride = t.shape, t.stride()
+    except AttributeError:
+        _need(logits=t)
+        raise
+    if len(shape) != dims:
+        raise ValueError(f"logits: expected {dims} dimensions, got {tuple(shape)}")
+    V = shape[-1]
+    if stride[-1] != 1 and V > 1:
         raise ValueError("logits: a position's logits must be densely packed")
+    B, T = shape[0], shape[1] if dims == 3 else 1
+    s = stride[1] if T > 1 else stride[0] if B > 1 else max(V, 1)
+    if T > 1 and B > 1 and stride[0] != T * s:
+        raise ValueError("logits: positions must lie at equal distances")
     return t.data_ptr(), s
 
 
-def _per_row(t, what, n, dtype):
-    return None if t is None else _ptrs((t, what, n, dtype))[0]
-
-
-def _filters(B, temperature, top_k, top_p, min_p):
-    f32 = _t().float32
-    return (_per_row(temperature, "temperature", B, f32), _per_row(top_k, "top_k", B, _t().int32),
-            _per_row(top_p, "top_p", B, f32), _per_row(min_p, "min_p", B, f32))
+def _some_ptrs(*args):
+    """_ptrs of arguments that may be None, which stays None."""
+    p = []
+    for t, what, n, dtype in args:
+        if t is None:
+            p.append(None)
+        else:
+            try:
+                if t.numel() == n and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+                    p.append(t.data_ptr())
+                    continue
+            except AttributeError:
+                pass
+            _count(t, what, n)
+            p.append(_ptr(t, what, dtype))
+    return p
 
 
 def gdn_sample(logits, u, token, logp=None, temperature=None, top_k=None, top_p=None, min_p=None, active=None,
@@ -430,13 +450,15 @@ def gdn_sample(logits, u, token, logp=None, temperature=None, top_k=None, top_p=
     place.  temperature, top_p, min_p [B] fp32, top_k [B] int32, active [B]
     uint8; None: 1, off, off, off, all."""
     torch = _t()
+    f32, i32 = torch.float32, torch.int32
     lp, stride = _logits(logits, 2)
     B, V = logits.shape
-    up, tp = _ptrs((u, "u", B, torch.float32), (token, "token", B, torch.int32))
-    rc = load().gdn_sample(B, V, lp, stride, _per_row(active, "active", B, torch.uint8),
-                           *_filters(B, temperature, top_k, top_p, min_p), up, tp,
-                           _per_row(logp, "logp", B, torch.float32), _stream(stream))
-    _check(rc, "gdn_sample")
+    up, tp = _ptrs((u, "u", B, f32), (token, "token", B, i32))
+    a, t, k, p, m, lg = _some_ptrs((active, "active", B, torch.uint8), (temperature, "temperature", B, f32), (top_k, "top_k", B, i32),
+                                   (top_p, "top_p", B, f32), (min_p, "min_p", B, f32), (logp, "logp", B, f32))
+    rc = load().gdn_sample(B, V, lp, stride, a, t, k, p, m, up, tp, lg, _stream(stream))
+    if rc:
+        _check(rc, "gdn_sample")
 
 
 def gdn_accept_sampled_workspace_bytes(B: int, T: int, V: int) -> int:
@@ -452,16 +474,20 @@ def gdn_accept_sampled(logits, draft, active, u, keep, nxt, token, logp, ws, tem
     logp [B][T] fp32 (each may be None), written in place.  ws:
     gdn_accept_sampled_workspace_bytes(B, T, V) bytes, zero-filled once."""
     torch = _t()
+    f32, i32 = torch.float32, torch.int32
     lp, stride = _logits(logits, 3)
     B, T, V = logits.shape
-    i32, f32 = torch.int32, torch.float32
-    dp, up, kp, np_ = _ptrs((draft, "draft", B * T, i32), (u, "u", B * T, f32), (keep, "keep", B, i32), (nxt, "next", B, i32))
+    N = B * T
+    dp, up, kp, np_ = _ptrs((draft, "draft", N, i32), (u, "u", N, f32), (keep, "keep", B, i32), (nxt, "next", B, i32))
+    a, t, k, p, m, tp, lg = _some_ptrs((active, "active", B, torch.uint8), (temperature, "temperature", B, f32),
+                                       (top_k, "top_k", B, i32), (top_p, "top_p", B, f32), (min_p, "min_p", B, f32),
+                                       (token, "token", N, i32), (logp, "logp", N, f32))
+    wp = _ptr(ws, "ws")
     _need(ws=ws)
-    rc = load().gdn_accept_sampled(
-        B, T, V, lp, stride, dp, _per_row(active, "active", B, torch.uint8),
-        *_filters(B, temperature, top_k, top_p, min_p), up, kp, np_, _per_row(token, "token", B * T, i32),
-        _per_row(logp, "logp", B * T, f32), _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
-    _check(rc, "gdn_accept_sampled")
+    rc = load().gdn_accept_sampled(B, T, V, lp, stride, dp, a, t, k, p, m, up, kp, np_, tp, lg, wp,
+                                   ws.numel() * ws.element_size(), _stream(stream))
+    if rc:
+        _check(rc, "gdn_accept_sampled")
 
 
 def gdn_kv4_page_bytes(kd: gdn_kv4_dims) -> int:
@@ -602,19 +628,30 @@ def gdn_kv_copy_pages(kd: gdn_kv4_dims, caches, src, dst, count=None, stream=Non
         _need(src=src)
         raise
     sp, dp = _ptrs((src, "src", n, i32), (dst, "dst", n, i32))
-    layers = (_P * max(len(caches), 1))(*[_cache(kd, t) for t in caches])
-    rc = load().gdn_kv_copy_pages(ctypes.byref(kd), len(caches), layers, n, sp, dp,
+    u8, need = _t().uint8, _cache_bytes(kd)
+    try:  # one pass, as in _ptrs
+        p = [t.data_ptr() for t in caches if t.dtype is u8 and t.is_cuda and t.is_contiguous() and t.numel() >= need]
+    except AttributeError:
+        p = ()
+    if len(p) != len(caches):
+        p = [_cache(kd, t) for t in caches]
+    rc = load().gdn_kv_copy_pages(ctypes.byref(kd), len(p), (_P * max(len(p), 1))(*p), n, sp, dp,
                                   None if count is None else _ptrs((count, "count", 1, i32))[0], _stream(stream))
     _check(rc, "gdn_kv_copy_pages")
 
 
-def _cache(kd, pages):
-    """Pointer of a cache; it may be larger than its dims say, never smaller."""
+def _cache_bytes(kd):
+    """Bytes of a cache of these dims; a page's size is asked for once."""
     key = (kd.H_kv, kd.d, kd.page)
-    if kd.__dict__.get("_key") != key:  # the page's size is asked for once
+    if kd.__dict__.get("_key") != key:
         kd._page_bytes = gdn_kv4_page_bytes(kd)
         kd._key = key if kd._page_bytes else None  # (0: dims that the call will refuse, which says nothing of others)
-    need = kd.n_pages * kd._page_bytes
+    return kd.n_pages * kd._page_bytes
+
+
+def _cache(kd, pages):
+    """Pointer of a cache; it may be larger than its dims say, never smaller."""
+    need = _cache_bytes(kd)
     try:
         size = pages.numel()
     except AttributeError:
