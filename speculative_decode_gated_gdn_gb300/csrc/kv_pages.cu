@@ -4,12 +4,23 @@
 // A fork's row gets the source's full pages as they are (a holder more each) and a
 // page of its own for the last, partly filled one.  Rows only write behind their own
 // length, so nobody writes a shared page.
+//
+// The bookkeeping is a few dependent trips to L2, so it is latency that counts: one
+// kernel of one cluster does it where it is small, whose CTAs wait for the first one's
+// decisions and then share the cells; where it is large, a second kernel of many CTAs
+// does the cells.  Copies are bound by HBM.
+#include <cooperative_groups.h>
+
 #include "kv4.cuh"
 #include "scan.cuh"
 
 namespace gdn {
 
 namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kCluster = 8;
 
 // ---- forks --------------------------------------------------------------------------
 struct ForkPair {
@@ -29,11 +40,8 @@ __device__ __forceinline__ ForkPair fork_pair(const KvForkParams &p, int i) {
 
 // Which pairs hold, and their last pages.  An empty row goes to the first pair that
 // asks for it: each leaves its index less n in the row's count, and the least stays.
-__global__ void __launch_bounds__(kScanThreads) kv_fork_kernel(const KvForkParams p) {
-  __shared__ long long s_warp[32];
+__device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
   const int tid = threadIdx.x;
-  pdl_wait();
-  pdl_trigger();
   const int count0 = min(max(*p.free_count, 0), p.n_pages);
   // a pair's verdict stands in copy_src until its page does; its thread is the same both times
   for (int i = tid; i < p.n; i += kScanThreads) {
@@ -99,19 +107,14 @@ __global__ void __launch_bounds__(kScanThreads) kv_fork_kernel(const KvForkParam
   if (tid == 0) *p.free_count = count0 - int(min(taken, (long long)count0));
 }
 
-constexpr int kForkThreads = 256;
-
-// The shared pages' cells and counts, of the pairs that held.
-__global__ void __launch_bounds__(kForkThreads) kv_share_kernel(const KvForkParams p) {
-  pdl_wait();
-  pdl_trigger();
-  const int i = blockIdx.x;
-  if (p.copy_src[i] == -2) return;
+// The shared pages' cells and counts of pair i, if it holds: cells first, first + step, ...
+__device__ __forceinline__ void share_cells(const KvForkParams &p, int i, int first, int step) {
+  if (__ldcg(p.copy_src + i) == -2) return;
   const ForkPair r = fork_pair(p, i);
   const int whole = r.len >> p.log2P;
   const int32_t *from = p.table + size_t(r.src) * p.max_pages;
   int32_t *to = p.table + size_t(r.dst) * p.max_pages;
-  for (int c = blockIdx.y * kForkThreads + threadIdx.x; c < whole; c += gridDim.y * kForkThreads) {
+  for (int c = first; c < whole; c += step) {
     const int page = from[c];
     to[c] = page;
     if (page >= 0 && page < p.n_pages) atomicAdd(p.refs + page, 1);
@@ -119,14 +122,43 @@ __global__ void __launch_bounds__(kForkThreads) kv_share_kernel(const KvForkPara
   }
 }
 
+__global__ void __launch_bounds__(kScanThreads) kv_fork_kernel(const KvForkParams p) {
+  __shared__ long long s_warp[32];
+  pdl_wait();
+  pdl_trigger();
+  decide_forks(p, s_warp);
+}
+
+// Both in one cluster; a warp has a pair, or a part of one.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads) kv_fork_cluster_kernel(const KvForkParams p) {
+  __shared__ long long s_warp[32];
+  cg::cluster_group cluster = cg::this_cluster();
+  pdl_wait();
+  pdl_trigger();
+  if (cluster.block_rank() == 0) decide_forks(p, s_warp);
+  cluster.sync();
+  constexpr int kWarps = kCluster * kScanThreads / 32;
+  const int g = int(cluster.block_rank()) * (kScanThreads / 32) + int(threadIdx.x >> 5);
+  const int parts = p.n < kWarps ? kWarps / p.n : 1;
+  for (int i = g / parts; i < p.n; i += kWarps / parts) share_cells(p, i, (g % parts) * 32 + int(threadIdx.x & 31), parts * 32);
+}
+
+constexpr int kForkThreads = 256;
+
+__global__ void __launch_bounds__(kForkThreads) kv_share_kernel(const KvForkParams p) {
+  pdl_wait();
+  pdl_trigger();
+  share_cells(p, blockIdx.x, blockIdx.y * kForkThreads + threadIdx.x, gridDim.y * kForkThreads);
+}
+
 // ---- compaction ---------------------------------------------------------------------
-// Counts in one CTA: each warp has a stretch of the pages, four a lane and step.
+// Counts in one cluster: each warp has a stretch of the pages, four a lane and step.
 struct Stretch {
   int begin, end;
 };
-__device__ __forceinline__ Stretch stretch_of(int warp, int n) {
-  const int steps = (n + 127) / 128, each = (steps + 31) / 32;
-  return Stretch{min(n, warp * each * 128), min(n, (warp + 1) * each * 128)};
+__device__ __forceinline__ Stretch stretch_of(int warp, int warps, int n) {
+  const long long steps = (n + 127) / 128, each = (steps + warps - 1) / warps;
+  return Stretch{int(min((long long)n, warp * each * 128)), int(min((long long)n, (warp + 1) * each * 128))};
 }
 // Which of the four pages from `at` on are in use, as bits.
 __device__ __forceinline__ uint32_t used_of(const int32_t *refs, int at, int end) {
@@ -139,32 +171,68 @@ __device__ __forceinline__ uint32_t used_of(const int32_t *refs, int at, int end
   return m;
 }
 
-__global__ void __launch_bounds__(kScanThreads) kv_compact_kernel(const KvCompactParams p) {
+// Tables, counts and the free stack by the map; item i of `step` threads.  Where an output
+// is the input itself, each entry is read and written by one thread, or stands for the
+// same either way.
+__device__ __forceinline__ void remap(const KvCompactParams &p, int U, int moves, size_t first, size_t step) {
+  const int n = p.n_pages;
+  for (size_t i = first; i < size_t(p.B) * p.max_pages; i += step) {
+    const int b = int(i / p.max_pages), c = int(i - size_t(b) * p.max_pages);
+    int page = p.table[i];
+    if (c < p.held[b]) {
+      page = page >= 0 && page < n ? __ldcg(p.page_map + page) : -1;
+      if (page < 0) atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+    }
+    p.new_table[i] = page;
+  }
+  for (size_t i = first; i < size_t(n); i += step) {
+    p.new_free_list[i] = i < size_t(n - U) ? n - 1 - int(i) : -1;
+    const int r = p.refs[i];
+    if ((r > 0) == (i < size_t(U))) p.new_refs[i] = max(r, 0);
+  }
+  for (size_t j = first; j < size_t(moves); j += step) {
+    const int from = __ldcg(p.copy_src + j);
+    const int r = p.refs[from];
+    p.new_refs[__ldcg(p.copy_dst + j)] = r;
+    p.new_refs[from] = 0;
+  }
+}
+
+// In C CTAs; ALL: the tables too.
+template <int C, bool ALL>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kScanThreads) kv_compact_kernel(const KvCompactParams p) {
   __shared__ long long s_warp[32];
-  __shared__ int s_before[32], s_below;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int s_before[32], s_used[C], s_below;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = C > 1 ? int(cluster.block_rank()) : 0;
+  auto together = [&] {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
   pdl_wait();
   pdl_trigger();
   const int n = p.n_pages;
-  const Stretch s = stretch_of(warp, n);
+  const Stretch s = stretch_of(rank * (kScanThreads / 32) + warp, C * (kScanThreads / 32), n);
   int count = 0;
 #pragma unroll 4
   for (int at = s.begin + 4 * lane; at < s.end; at += 128) count += __popc(used_of(p.refs, at, s.end));
-  long long U_;
-  const long long upto = block_scan(count, s_warp, &U_);
+  long long used;
+  const long long upto = block_scan(count, s_warp, &used);
   if (lane == 31) s_before[warp] = int(upto);
-  __syncthreads();
-  const int U = int(U_);
-  int before = warp ? s_before[warp - 1] : 0;
+  if (C > 1) cluster.sync();  // every CTA runs
+  if (tid < C) (C > 1 ? cluster.map_shared_rank(s_used, tid) : s_used)[rank] = int(used);
+  together();
+  int U = 0, before = warp ? s_before[warp - 1] : 0;  // pages in use: all, before the stretch
+  for (int q = 0; q < C; ++q) U += s_used[q], before += q < rank ? s_used[q] : 0;
   // pages in use below place U: those behind it move into the gaps
-  if (U >= s.begin && U < s.end) {
+  if ((U >= s.begin && U < s.end) || (U == n && rank == 0 && warp == 0)) {
     int below = 0;
-    for (int at = s.begin + 4 * lane; at < U; at += 128) below += __popc(used_of(p.refs, at, U));
-    below = __reduce_add_sync(0xffffffffu, below);
-    if (lane == 0) s_below = before + below;
+    if (U < n)
+      for (int at = s.begin + 4 * lane; at < U; at += 128) below += __popc(used_of(p.refs, at, U));
+    below = U < n ? before + __reduce_add_sync(0xffffffffu, below) : U;
+    if (lane < C) *(C > 1 ? cluster.map_shared_rank(&s_below, lane) : &s_below) = below;
   }
-  if (U == n && tid == 0) s_below = U;
-  __syncthreads();
+  together();
   const int below = s_below;
   for (int base = s.begin; base < s.end; base += 128) {
     const int at = base + 4 * lane;
@@ -179,50 +247,31 @@ __global__ void __launch_bounds__(kScanThreads) kv_compact_kernel(const KvCompac
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int i = at + j;
-      if (i >= s.end) break;
-      const bool used = m >> j & 1;
-      p.page_map[i] = used ? i : -1;
-      if (used && i >= U) p.copy_src[k - below] = i;
-      if (!used && i < U) p.copy_dst[i - k] = i;
-      k += used;
+      if (i < s.end) {
+        const bool in_use = m >> j & 1;
+        if (!in_use || i < U) p.page_map[i] = in_use ? i : -1;  // the others' below
+        if (in_use && i >= U) p.copy_src[k - below] = i;
+        if (!in_use && i < U) p.copy_dst[i - k] = i;
+        k += in_use;
+      }
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
-  __syncthreads();
+  together();
   const int moves = U - below;
-  for (int j = tid; j < moves; j += kScanThreads) p.page_map[p.copy_src[j]] = p.copy_dst[j];
-  if (tid == 0) *p.copy_count = moves, *p.new_free_count = n - U;
+  for (int j = rank * kScanThreads + tid; j < moves; j += C * kScanThreads) p.page_map[__ldcg(p.copy_src + j)] = __ldcg(p.copy_dst + j);
+  if (rank == 0 && tid == 0) *p.copy_count = moves, *p.new_free_count = n - U;
+  if (!ALL) return;
+  together();
+  remap(p, U, moves, size_t(rank) * kScanThreads + tid, size_t(C) * kScanThreads);
 }
 
 constexpr int kRemapThreads = 256;
 
-// Tables, counts and the free stack by the map.  Where an output is the input itself,
-// each entry is read and written by one thread, or stands for the same either way.
 __global__ void __launch_bounds__(kRemapThreads) kv_remap_kernel(const KvCompactParams p) {
   pdl_wait();
   pdl_trigger();
-  const int n = p.n_pages, U = n - *p.new_free_count, moves = *p.copy_count;
-  const size_t step = size_t(gridDim.x) * kRemapThreads, first = size_t(blockIdx.x) * kRemapThreads + threadIdx.x;
-  for (size_t i = first; i < size_t(p.B) * p.max_pages; i += step) {
-    const int b = int(i / p.max_pages), c = int(i - size_t(b) * p.max_pages);
-    int page = p.table[i];
-    if (c < p.held[b]) {
-      page = page >= 0 && page < n ? p.page_map[page] : -1;
-      if (page < 0) atomicOr(p.status, GDN_STATUS_BAD_INDEX);
-    }
-    p.new_table[i] = page;
-  }
-  for (size_t i = first; i < size_t(n); i += step) {
-    p.new_free_list[i] = i < size_t(n - U) ? n - 1 - int(i) : -1;
-    const int r = p.refs[i];
-    if ((r > 0) == (i < size_t(U))) p.new_refs[i] = max(r, 0);
-  }
-  for (size_t j = first; j < size_t(moves); j += step) {
-    const int from = p.copy_src[j];
-    const int r = p.refs[from];
-    p.new_refs[p.copy_dst[j]] = r;
-    p.new_refs[from] = 0;
-  }
+  remap(p, p.n_pages - *p.new_free_count, *p.copy_count, size_t(blockIdx.x) * kRemapThreads + threadIdx.x, size_t(gridDim.x) * kRemapThreads);
 }
 
 // ---- copies -------------------------------------------------------------------------
@@ -257,6 +306,11 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
   }
 }
 
+// Cells up to which one cluster does all: four a thread.
+constexpr long long kOneClusterCells = 4ll * kCluster * kScanThreads;
+
+constexpr int kOneCtaCells = 4 * kScanThreads;  // and one CTA
+
 int sm_count() {
   int dev = 0, n = 152;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
@@ -266,6 +320,7 @@ int sm_count() {
 }  // namespace
 
 cudaError_t launch_kv_fork(const KvForkParams &p, cudaStream_t s) {
+  if ((long long)p.n * p.max_pages <= kOneClusterCells) return launch_pdl(kv_fork_cluster_kernel, dim3(kCluster), dim3(kScanThreads), s, p);
   const cudaError_t e = launch_pdl(kv_fork_kernel, dim3(1), dim3(kScanThreads), s, p);
   if (e != cudaSuccess) return e;
   const int y = (p.max_pages + kForkThreads - 1) / kForkThreads;
@@ -273,9 +328,11 @@ cudaError_t launch_kv_fork(const KvForkParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_compact(const KvCompactParams &p, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(kv_compact_kernel, dim3(1), dim3(kScanThreads), s, p);
+  const size_t cells = size_t(p.B) * p.max_pages, items = cells > size_t(p.n_pages) ? cells : size_t(p.n_pages);
+  if (items <= size_t(kOneCtaCells)) return launch_pdl(kv_compact_kernel<1, true>, dim3(1), dim3(kScanThreads), s, p);
+  if (items <= size_t(kOneClusterCells)) return launch_pdl(kv_compact_kernel<kCluster, true>, dim3(kCluster), dim3(kScanThreads), s, p);
+  const cudaError_t e = launch_pdl(kv_compact_kernel<kCluster, false>, dim3(kCluster), dim3(kScanThreads), s, p);
   if (e != cudaSuccess) return e;
-  const size_t items = size_t(p.B) * p.max_pages > size_t(p.n_pages) ? size_t(p.B) * p.max_pages : size_t(p.n_pages);
   size_t grid = (items + kRemapThreads - 1) / kRemapThreads;
   const size_t most = size_t(sm_count()) * 8;
   if (grid > most) grid = most;
