@@ -95,6 +95,10 @@ __device__ __forceinline__ long long release_shared(const KvPlanParams &p, int c
     else __syncthreads();
   };
   long long released = 0, total = 0;
+  // kBatch releases of a thread at a time, so that their trips to memory overlap; where that is
+  // all, they stay from pass to pass
+  int32_t *cell[kBatch];
+  int page[kBatch];  // -1: none, or outside the cache
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     long long index0 = 0;  // releases of the rows before the chunk
@@ -112,10 +116,9 @@ __device__ __forceinline__ long long release_shared(const KvPlanParams &p, int c
       if (total == 0) continue;  // the same for every thread of the cluster
       const PlanChunk chunk{s_ends, s_from, b0, rows};
       const int lo = int(total * rank / C), hi = int(total * (rank + 1) / C);
-      // kBatch releases of a thread at a time, so that their trips to memory overlap
-      int32_t *cell[kBatch];
-      int page[kBatch];  // -1: none, or outside the cache
+      const bool again = pass > 0 && p.B <= kPlanThreads && total <= C * kBatch * kPlanThreads;
       auto gather = [&](int i0) {
+        if (again) return;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int i = i0 + k * kPlanThreads + tid;
@@ -148,7 +151,7 @@ __device__ __forceinline__ long long release_shared(const KvPlanParams &p, int c
             for (int k = 0; k < kBatch; ++k)
               if (cell[k] && c[k] <= 0) {  // no page, or nobody held it: not given back
                 if (page[k] >= 0) atomicAdd(p.refs + page[k], 1);
-                *cell[k] = -1;
+                *cell[k] = -1, page[k] = -1;
                 atomicOr(p.status, GDN_STATUS_BAD_INDEX);
               }
           }
