@@ -6,18 +6,21 @@
 // read once:
 //   1. From its slice's first 8192 logits each CTA bounds what can matter: nothing
 //      whose weight rounds to 0 or is below min_p, and, with top_k, nothing below a
-//      value that the first k reach for sure (each warp's ceil(k / warps)-th largest of
+//      value that the first k reach for sure (each warp's ceil(k / 8)-th largest of
 //      its granules' maxima, the least of them).
 //   2. The logits that pass are counted by value in shared memory: 2048 magnitudes, the
-//      16 binades below the largest, of either sign, in the order of the row.  What lies
-//      between the two signs' magnitudes, near zero, is rare and goes to a list.
+//      16 binades below the slice's largest, of either sign, in the order of the row.
+//      What lies between the two signs' magnitudes, near zero, is rare and goes to a
+//      list.
 //   3. The CTAs add up their counts, each a part of the values, and form counts and
-//      masses of groups of 16 values for the first CTA, which asks them where the first
-//      k end, where p of the mass ends, and where u falls.
+//      masses of groups of 32 values for the first CTA, whose first warp asks them where
+//      the first k end, where p of the mass ends, and where u falls.
 //   4. It finds that value's logit in the slice that has it.
-// A logit above all of the 16 binades makes the counting begin again with others; an
-// answer near zero is looked for in windows of 2048 values over the row.
+// A logit above all of the 16 binades makes a CTA's counting begin again with others; an
+// answer near zero is looked for in windows of 1024 values over the row.
 #include <cooperative_groups.h>
+
+#include <atomic>
 
 #include "sample.cuh"
 
@@ -29,16 +32,20 @@ namespace cg = cooperative_groups;
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kLoads = 4;                     // granules of a thread and tile
-constexpr int kTile = kThreads * kLoads;      // granules of a tile
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kLoads = 4;                     // granules of a thread in flight
 constexpr int kMagnitudes = 2048;             // of each sign: 16 binades
 constexpr int kBins = 2 * kMagnitudes;        // in the order of the row
+// Where the counts stand: those of positive values, largest first, a gap as large, those of
+// negative ones, and behind each side 32 words, one a lane, for what has no bin.  So a
+// bin's word is its magnitude's number in 12 bits, the sign's bit xored with the rest.
+constexpr int kMinusWords = 2 * kMagnitudes, kWords = kMinusWords + kMagnitudes + 32;
+__device__ __forceinline__ int word_of(int bin) { return bin < kMagnitudes ? bin : bin + kMagnitudes; }
 constexpr int kGroups = kBins / 32;           // of 32 bins, a warp's
-constexpr int kFewGranules = 512;             // of a slice: counted without a bound of top_k
+constexpr int kFewLanes = 12;                 // of a warp that have something to count: one by one
 constexpr int kNear = 512;                    // places of the list of values near zero
-constexpr int kWindow = 1024;                 // values of a window, and logits of one value found
+constexpr int kWindow = 1024;                 // values of a window
+static_assert(kWindow + kNear / 2 <= kMagnitudes - 32, "they lie in the gap of the counts");
 
 struct Found {
   int place;       // the value
@@ -49,28 +56,30 @@ struct Found {
 
 // What a CTA tells the others of its cluster.
 struct Told {
-  float top, low, bound;  // largest and least number, bound of what matters
-  int beyond;             // largest magnitude that had no bin, 0 if none
+  float top, bound;  // its largest number; what matters is not below this
+  int base;          // its least magnitude that has a bin
 };
 
-// A question about the values near zero; what = -1: there are no more.
+// A question about the values near zero: by count (0) or by mass; -1: there are no more.
 struct Asked {
   int what;
   u64 target;
 };
 
 struct Shared {
-  alignas(16) uint32_t hist[kBins];
-  uint32_t sum[kBins];      // the cluster's (where it has more than one CTA); first CTA
-  uint32_t window[kWindow];
-  uint16_t near[kNear];
+  alignas(16) uint32_t hist[kWords];
+  uint32_t sum[kBins];      // the cluster's counts, up to each bin of a group; then indices of one value; first CTA
+  u64 mass[kBins];          // masses likewise
+  __device__ __forceinline__ uint32_t *window() { return hist + kMagnitudes; }  // in the gap
+  __device__ __forceinline__ uint16_t *near() { return reinterpret_cast<uint16_t *>(hist + kMagnitudes + kWindow); }
+
   u64 table[32];
   u64 group_mass[kGroups];
   uint32_t group_count[kGroups];
-  u64 near_mass, warp_mass[kWarps];
-  uint32_t near_count, warp_count[kWarps];  // near_count: of the cluster, first CTA
-  float warp_top[kWarps], warp_low[kWarps], warp_bound[kWarps];
-  Told told[2][8];          // by rank: before and after the counts
+  u64 near_mass, warp_mass[32];
+  uint32_t near_count, warp_count[32];  // near_count: of the cluster, first CTA
+  float warp_top[32], warp_low[32], warp_bound[32];
+  Told told[8];             // by rank
   uint32_t near_n;          // of this CTA's list
   int beyond, next, at;
   uint32_t matches;
@@ -80,25 +89,20 @@ struct Shared {
   Asked asked;
 };
 
-enum Question { kCount, kMassReaches, kMassPasses };
-
-__device__ __forceinline__ bool answers(Question what, u64 target, u64 count, u64 count1, u64 mass, u64 mass1) {
-  return what == kCount ? count < target && target <= count1
-                        : what == kMassReaches ? mass < target && target <= mass1 : mass <= target && target < mass1;
-}
-__device__ __forceinline__ uint32_t number_of(Question what, u64 target, u64 count, u64 mass, u64 w) {
-  return what == kCount ? uint32_t(target - count) : few_in(target - mass - (what == kMassReaches), w) + 1;
-}
-
-// Inclusive sums over the CTA of (count, mass).
-__device__ __forceinline__ void scan(uint32_t &count, u64 &mass, Shared &s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sums over a warp of (count, mass).
+__device__ __forceinline__ void sum_up_to(uint32_t &count, u64 &mass) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t a = __shfl_up_sync(0xffffffffu, count, o);
     const u64 b = __shfl_up_sync(0xffffffffu, mass, o);
-    if (lane >= o) count += a, mass += b;
+    if (int(threadIdx.x & 31) >= o) count += a, mass += b;
   }
+}
+
+// The same over the CTA.
+__device__ __forceinline__ void scan(uint32_t &count, u64 &mass, Shared &s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sum_up_to(count, mass);
   __syncthreads();
   if (lane == 31) s.warp_count[warp] = count, s.warp_mass[warp] = mass;
   __syncthreads();
@@ -116,12 +120,12 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
 // The answer among the values at places [from, end), in windows over the row, with count0 and
 // mass0 before them.  Rare, and as slow as windows are many.
 __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int end, int top, Scale scale, u64 least, uint32_t count0,
-                                             u64 mass0, Question what, u64 target, Shared &s) {
+                                             u64 mass0, bool by_count, u64 target, Shared &s) {
   const int tid = threadIdx.x;
   constexpr int kPer = kWindow / kThreads;
   while (from < end) {
     __syncthreads();
-    for (int i = tid; i < kWindow; i += kThreads) s.window[i] = 0;
+    for (int i = tid; i < kWindow; i += kThreads) s.window()[i] = 0;
     if (tid == 0) s.next = end, s.found.hit = 0;
     __syncthreads();
     int next = end;
@@ -131,7 +135,7 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
       for (int j = 0; j < 8; ++j) {
         const int place = place_of(half_of(q, j));
         if (place < from || place >= end) continue;
-        if (place - from < kWindow) atomicAdd(&s.window[place - from], 1u);
+        if (place - from < kWindow) atomicAdd(&s.window()[place - from], 1u);
         else next = min(next, place);
       }
     }
@@ -141,7 +145,7 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
     u64 mass = 0;
 #pragma unroll 1
     for (int i = 0; i < kPer; ++i) {
-      const uint32_t n = s.window[tid * kPer + i];
+      const uint32_t n = s.window()[tid * kPer + i];
       const u64 w = n ? weight_of(from + tid * kPer + i, top, scale, s.table) : 0;
       if (w >= least) count += n, mass += n * w;
     }
@@ -150,15 +154,16 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
     scan(count1, mass1, s);
     count1 += count0, mass1 += mass0;
     count = count1 - count, mass = mass1 - mass;  // before this thread's places
-    if (answers(what, target, count, count1, mass, mass1)) {
+    const u64 lo = by_count ? u64(count) : mass, hi = by_count ? u64(count1) : mass1;
+    if (lo < target && target <= hi) {
 #pragma unroll 1
       for (int i = 0; i < kPer; ++i) {
         const int place = from + tid * kPer + i;
-        uint32_t n = s.window[tid * kPer + i];
+        uint32_t n = s.window()[tid * kPer + i];
         const u64 w = n ? weight_of(place, top, scale, s.table) : 0;
         if (w < least) n = 0;
-        if (n && answers(what, target, count, count + n, mass, mass + n * w)) {
-          s.found = Found{place, number_of(what, target, count, mass, w), w, mass, 1};
+        if (n && target <= (by_count ? u64(count + n) : mass + n * w)) {
+          s.found = Found{place, by_count ? uint32_t(target) - count : few_in(target - 1 - mass, w) + 1, w, mass, 1};
           break;
         }
         count += n, mass += n * w;
@@ -205,43 +210,16 @@ __device__ __noinline__ int locate_in_order(const SampleRow &row, int g0, int g1
   return 0;
 }
 
-// The same for a value that few logits have: they are listed, and counted against one another.
-__device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t n, uint32_t all, Shared &s) {
-  if (all > uint32_t(kWindow)) return locate_in_order(row, g0, g1, place, n, s);
+// The n-th least of the first m of s.sum.
+__device__ __forceinline__ int pick(uint32_t m, uint32_t n, Shared &s) {
   const int tid = threadIdx.x;
-  __syncthreads();
-  if (tid == 0) s.matches = 0, s.at = 0;
-  __syncthreads();
-  // equal as numbers: -0 as 0, NaN never
-  const __nv_bfloat162 v = __float2bfloat162_rn(value_at(place));
-  auto same = [&](uint32_t w) { return __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w), v); };
-  for (int g = g0 + tid; g - tid < g1; g += kTile) {  // the warp's lanes together
-    uint4 q[kLoads];
-#pragma unroll
-    for (int r = 0; r < kLoads; ++r)
-      q[r] = g + r * kThreads < g1 ? row.load(g + r * kThreads) : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-#pragma unroll
-    for (int r = 0; r < kLoads; ++r) {
-      const uint32_t m0 = same(q[r].x), m1 = same(q[r].y), m2 = same(q[r].z), m3 = same(q[r].w);
-      if (m0 | m1 | m2 | m3) {
-        uint32_t bits = (m0 & 0x10001u) | (m1 & 0x10001u) << 2 | (m2 & 0x10001u) << 4 | (m3 & 0x10001u) << 6;
-        bits = (bits | bits >> 15) & 0xffu;  // logit j at bit j
-        const uint32_t i = atomicAdd(&s.matches, uint32_t(__popc(bits)));
-        const int at = row.first(g + r * kThreads);
-        for (uint32_t k = i; bits && k < uint32_t(kWindow); ++k, bits &= bits - 1) s.window[k] = uint32_t(at + __ffs(bits) - 1);
-      }
-      __syncwarp();
-    }
-  }
-  __syncthreads();
-  const uint32_t m = min(s.matches, uint32_t(kWindow));
-  if (tid < 4 && m + tid < uint32_t(kWindow)) s.window[m + tid] = 0xffffffffu;
+  if (tid < 4 && m + tid < uint32_t(kBins)) s.sum[m + tid] = 0xffffffffu;
   __syncthreads();
   for (uint32_t i = tid; i < m; i += kThreads) {
-    const uint32_t x = s.window[i];
+    const uint32_t x = s.sum[i];
     uint32_t below = 0;
     for (uint32_t j = 0; j < m; j += 4) {
-      const uint4 y = *reinterpret_cast<const uint4 *>(s.window + j);
+      const uint4 y = *reinterpret_cast<const uint4 *>(s.sum + j);
       below += (y.x < x) + (y.y < x) + (y.z < x) + (y.w < x);
     }
     if (below + 1 == n) s.at = int(x);
@@ -250,8 +228,44 @@ __device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t 
   return s.at;
 }
 
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// The same for a value that few logits have: they are listed, tile after tile until there are
+// n, and counted against one another.
+__device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t n, uint32_t all, Shared &s) {
+  if (all > uint32_t(kBins)) return locate_in_order(row, g0, g1, place, n, s);
+  const int tid = threadIdx.x;
+  // equal as numbers: -0 as 0, NaN never
+  const __nv_bfloat162 v = __float2bfloat162_rn(value_at(place));
+  auto same = [&](uint32_t w) { return __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w), v); };
+  uint4 next[kLoads];
+  auto load = [&](int g) {
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r)
+      next[r] = g + r * kThreads < g1 ? row.load(g + r * kThreads) : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+  };
+  load(g0 + tid);
+  uint32_t found = 0;
+  for (int g = g0 + tid; g - tid < g1 && found < n; g += kThreads * kLoads) {  // the same for every thread
+    uint4 q[kLoads];
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r) q[r] = next[r];
+    if (g - tid + kThreads * kLoads < g1) load(g + kThreads * kLoads);
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r) {
+      const uint32_t m0 = same(q[r].x), m1 = same(q[r].y), m2 = same(q[r].z), m3 = same(q[r].w);
+      if (m0 | m1 | m2 | m3) {
+        uint32_t bits = (m0 & 0x10001u) | (m1 & 0x10001u) << 2 | (m2 & 0x10001u) << 4 | (m3 & 0x10001u) << 6;
+        bits = (bits | bits >> 15) & 0xffu;  // logit j at bit j
+        uint32_t k = atomicAdd(&s.matches, uint32_t(__popc(bits)));
+        const int at = row.first(g + r * kThreads);
+        for (; bits && k < uint32_t(kBins); ++k, bits &= bits - 1) s.sum[k] = uint32_t(at + __ffs(bits) - 1);
+      }
+    }
+    __syncthreads();
+    found = s.matches;
+    __syncthreads();
+  }
+  return pick(min(found, uint32_t(kBins)), n, s);
+}
 
 __device__ __forceinline__ __nv_bfloat162 b2(const uint32_t &w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
 __device__ __forceinline__ float max_of(const uint4 &q) {
@@ -276,27 +290,29 @@ __device__ __forceinline__ float warp_min(float x) {
 
 constexpr uint32_t kNoNumbers = 0x7fff7fffu;
 
-// One more in the bin of f, if f >= bound and its magnitude has one.  Returns, where f >=
-// bound, its magnitude beyond the least that has one, in the upper half, else 0.  `bins`
-// is the address of the first bin of a negative value; positive ones lie before it, in
-// the other direction.
-__device__ __forceinline__ uint32_t count_value(float f, float bound, uint32_t least_magnitude, uint32_t bins) {
-  const int x = __float_as_int(f + 0.f);  // -0 as 0
-  const uint32_t off = (uint32_t(x) & 0x7fffffffu) - least_magnitude;
-  const uint32_t at = bins + ((off >> 14) ^ (~uint32_t(x >> 31) & ~3u));
-  uint32_t far;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ge.f32 p, %1, %2;\n setp.lt.and.u32 q, %3, %4, p;\n @q red.shared.add.u32 [%5], 1;\n"
-      " selp.u32 %0, %3, 0, p;\n}"
-      : "=r"(far)
-      : "f"(f), "f"(bound), "r"(off), "r"(uint32_t(kMagnitudes) << 16), "r"(at)
-      : "memory");
-  return far;
+// One more in the bins of two logits, 16 bits each, where their magnitudes have one;
+// returns their magnitudes' numbers, from kMagnitudes on where they have none.
+// less_base: -base twice; most: the lane's word for what has no bin, twice.
+__device__ __forceinline__ uint32_t count_two(uint32_t w, uint32_t less_base, uint32_t most, uint32_t hist) {
+  const uint32_t off = __viaddmin_u16x2(w & 0x7fff7fffu, less_base, most);
+  uint32_t minus;  // each sign 16 times
+  asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(minus) : "r"(w));
+  const uint32_t at = off << 2 ^ ((minus & 4 * kMinusWords * 0x10001u) | (~minus & 4 * (kMagnitudes - 1) * 0x10001u));
+  asm volatile("red.shared.add.u32 [%0], 1;\n red.shared.add.u32 [%1], 1;" ::"r"(hist + (at & 0xffffu)), "r"(hist + (at >> 16)) : "memory");
+  return off;
+}
+
+// Which of a granule's logits reach the bound, logit j as bit j.
+__device__ __forceinline__ uint32_t reaching(const uint4 &q, __nv_bfloat162 bound) {
+  const uint32_t m = (__hge2_mask(b2(q.x), bound) & 0x10001u) | (__hge2_mask(b2(q.y), bound) & 0x10001u) << 2 |
+                     (__hge2_mask(b2(q.z), bound) & 0x10001u) << 4 | (__hge2_mask(b2(q.w), bound) & 0x10001u) << 6;
+  return (m | m >> 15) & 0xffu;
 }
 
 template <int C>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams p) {
-  __shared__ Shared s;
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+  extern __shared__ __align__(16) unsigned char memory[];
+  Shared &s = *reinterpret_cast<Shared *>(memory);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = C > 1 ? int(cluster.block_rank()) : 0;
@@ -307,25 +323,26 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
   };
   pdl_wait();
   pdl_trigger();
+  const SampleRow row(p.logits + size_t(bt) * p.stride, p.V);
+  const int each = (row.granules + C - 1) / C;
+  const int g0 = min(row.granules, rank * each), g1 = min(row.granules, g0 + each);
+      auto load = [&](int g) { return g < g1 ? row.load(g) : make_uint4(kNoNumbers, kNoNumbers, kNoNumbers, kNoNumbers); };
+      uint4 ahead[kLoads];  // this thread's next granules, kThreads apart
+      auto start = [&] {
+  #pragma unroll
+        for (int r = 0; r < kLoads; ++r) ahead[r] = load(g0 + tid + r * kThreads);
+      };
+      start();
+      float temperature = p.temperature ? p.temperature[b] : 1.f;
+      float min_p = p.min_p ? p.min_p[b] : 0.f, top_p = p.top_p ? p.top_p[b] : 1.f;
+      int top_k = p.top_k ? p.top_k[b] : 0;
+      const float u = p.u[bt];
   const bool active = !p.active || p.active[b];  // the cluster agrees
   int token = -1;
   float logp = 0.f;
   if (active) {
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
-    const SampleRow row(p.logits + size_t(bt) * p.stride, p.V);
-    const int each = (row.granules + C - 1) / C;
-    const int g0 = min(row.granules, rank * each), g1 = min(row.granules, g0 + each);
-    auto load = [&](uint4(&q)[kLoads], int g) {
-#pragma unroll
-      for (int r = 0; r < kLoads; ++r)
-        q[r] = g + r * kThreads < g1 ? row.load(g + r * kThreads) : make_uint4(kNoNumbers, kNoNumbers, kNoNumbers, kNoNumbers);
-    };
-    uint4 first[kLoads];
-    load(first, g0 + tid);
-    float temperature = p.temperature ? p.temperature[b] : 1.f;
-    float min_p = p.min_p ? p.min_p[b] : 0.f, top_p = p.top_p ? p.top_p[b] : 1.f;
-    int top_k = p.top_k ? p.top_k[b] : 0;
-    for (int i = 4 * tid; i < kBins; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+    for (int i = 4 * tid; i < kWords; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
     if (tid < 32) s.table[tid] = kExp2Table[tid];
     if (tid == 0) s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0;
     if (!(temperature > 0.f)) temperature = 0.f, min_p = 0.f, top_p = 1.f, top_k = 1;
@@ -334,44 +351,22 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
 
     // ---- what can matter ----------------------------------------------------------------
     float top = -INFINITY, low = INFINITY, bound = -INFINITY;
-    {
-      int place[kLoads];
 #pragma unroll
-      for (int r = 0; r < kLoads; ++r) {
-        const float x = max_of(first[r]);
-        top = fmaxf(top, x), low = fminf(low, min_of(first[r]));
-        place[r] = place_of(__float_as_uint(x) >> 16);
-      }
-      const int mine = (top_k + kWarps * C - 1) / (kWarps * C);
-      if (each > kFewGranules && mine <= 32 * kLoads) {
-        // a place that so many of the warp's granules reach, the least but for its last five bits
-        int lo = 0, hi = kPlaceEnd >> 5;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          int n = 0;
+    for (int r = 0; r < kLoads; ++r) top = fmaxf(top, max_of(ahead[r])), low = fminf(low, min_of(ahead[r]));
+    // so many lanes' maxima that the CTA has top_k groups or more; the least of the groups'
+    const int lanes = top_k <= kWarps ? 32 : top_k <= kThreads ? 1 << (31 - __clz(kThreads / top_k)) : 0;
+    bound = lanes == 1 ? top : bound;
 #pragma unroll
-          for (int r = 0; r < kLoads; ++r) n += place[r] < (mid + 1) << 5;
-          if (int(__reduce_add_sync(0xffffffffu, unsigned(n))) >= mine) hi = mid;
-          else lo = mid + 1;
-        }
-        if (lo < kPlaceEnd >> 5) bound = value_at((lo << 5) + 31);
-      }
-      top = warp_max(top), low = warp_min(low);
-      if (lane == 0) s.warp_top[warp] = top, s.warp_low[warp] = low, s.warp_bound[warp] = bound;
+    for (int o = 1; o < 32; o <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      bound = lanes == 2 * o ? top : bound;
     }
+    bound = warp_min(bound), low = warp_min(low);
+    if (lane == 0) s.warp_top[warp] = top, s.warp_low[warp] = low, s.warp_bound[warp] = bound;
     __syncthreads();
-    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all of them do
-    if (tid < C) {
-      Told t{s.warp_top[0], s.warp_low[0], s.warp_bound[0], 0};
+    top = s.warp_top[0], low = s.warp_low[0], bound = s.warp_bound[0];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w)
-        t.top = fmaxf(t.top, s.warp_top[w]), t.low = fminf(t.low, s.warp_low[w]), t.bound = fminf(t.bound, s.warp_bound[w]);
-      (C > 1 ? cluster.map_shared_rank(s.told[0], tid) : s.told[0])[rank] = t;
-    }
-    together();
-    top = s.told[0][0].top, low = s.told[0][0].low, bound = s.told[0][0].bound;
-#pragma unroll
-    for (int i = 1; i < C; ++i) top = fmaxf(top, s.told[0][i].top), low = fminf(low, s.told[0][i].low), bound = fminf(bound, s.told[0][i].bound);
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s.warp_top[w]), low = fminf(low, s.warp_low[w]), bound = fminf(bound, s.warp_bound[w]);
     // Weights under 2^-44 count as 0: 46 ln 2 temperatures below the largest.  Rounding moves these
     // bounds by far less than a step of bf16, and never above the largest.
     if (top > -INFINITY && top < INFINITY) {
@@ -380,80 +375,87 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
     } else if (top == INFINITY) {
       bound = INFINITY;
     }
-    bound = fmaxf(bound, -3.3895314e38f);  // the least finite number
+    // the least number of bf16 that reaches it, and a finite one
+    bound = __bfloat162float(__float2bfloat16_ru(fmaxf(bound, -3.3895314e38f)));
     // the largest magnitude that may come; where more is read than was looked at, of twice that
     uint32_t magnitude = (__float_as_uint(fmaxf(fabsf(top), fabsf(fmaxf(low, bound)))) >> 16);
     if (!(top > -INFINITY)) magnitude = 0;
-    int binade = int(magnitude >> 7) + (each > kTile);
+    int binade = int(magnitude >> 7) + (each > kThreads * kLoads);
 
     // ---- counts by value ------------------------------------------------------------------
     int base;
-    const uint32_t bins = smem_u32(s.hist + kMagnitudes);
+    const __nv_bfloat162 bound2 = __float2bfloat162_rn(bound);
+    const uint32_t hist = smem_u32(s.hist), most = (kMagnitudes + lane) * 0x10001u;
     for (;;) {
-      base = max(0, ((min(binade, 255) + 1) << 7) - kMagnitudes);
-      const uint32_t least_magnitude = uint32_t(base) << 16;
-      float most = -INFINITY;
-      auto look = [&](const uint4(&q)[kLoads]) {
-#pragma unroll
-        for (int r = 0; r < kLoads; ++r) {
-          const float x = max_of(q[r]);
-          most = fmaxf(most, x);
-          // branches are the warp's, so that it stays together
-          if (!__any_sync(0xffffffffu, x >= bound)) continue;
-          const uint32_t w[4] = {q[r].x, q[r].y, q[r].z, q[r].w};
-          uint32_t far = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            far = max(far, max(count_value(lo_of(w[j]), bound, least_magnitude, bins), count_value(hi_of(w[j]), bound, least_magnitude, bins)));
-          if (!__any_sync(0xffffffffu, far >= uint32_t(kMagnitudes) << 16)) continue;
-#pragma unroll 1
-          for (int j = 0; j < 8; ++j) {  // some that matter have no bin
-            const uint32_t bits = half_of(q[r], j), a = bits & 0x7fffu;
-            if (bf2f(uint16_t(bits)) >= bound && a - uint32_t(base) >= uint32_t(kMagnitudes)) {
-              if (a < uint32_t(base)) {
-                const uint32_t i = atomicAdd(&s.near_n, 1u);
-                if (i < uint32_t(kNear)) s.near[i] = uint16_t(place_of(bits));
-              } else {
-                atomicMax(&s.beyond, int(a));
-              }
-            }
-            __syncwarp();
+      base = max(0, min((binade + 1) << 7, 0x7f81) - kMagnitudes);  // infinity is the last that has one
+      const uint32_t less_base = (-uint32_t(base) & 0xffffu) * 0x10001u;
+      float largest = -INFINITY;
+      auto count = [&](const uint4 &q) {
+        const float x = max_of(q);
+        largest = fmaxf(largest, x);
+        // branches are the warp's, so that it stays together
+        const uint32_t who = __ballot_sync(0xffffffffu, x >= bound);
+        if (!who) return;
+        uint32_t odd;  // logits to look at one by one, as bits
+        bool counted = false;
+        if (__popc(who) <= kFewLanes) {
+          odd = reaching(q, bound2);
+        } else {  // also what lies below the bound: it is behind all that matters
+          const uint32_t off = count_two(q.x, less_base, most, hist) | count_two(q.y, less_base, most, hist) |
+                               count_two(q.z, less_base, most, hist) | count_two(q.w, less_base, most, hist);
+          const bool some = off & kMagnitudes * 0x10001u;
+          if (!__any_sync(0xffffffffu, some)) return;
+          odd = some ? reaching(q, bound2) : 0;
+          counted = true;
+        }
+        for (; odd; odd &= odd - 1) {
+          const uint32_t bits = half_of(q, __ffs(odd) - 1), a = bits & 0x7fffu, off = a - uint32_t(base);
+          if (off < uint32_t(kMagnitudes)) {
+            if (!counted) atomicAdd(&s.hist[bits > 0x8000u ? kMinusWords + off : kMagnitudes - 1 - off], 1u);
+          } else if (a < uint32_t(base)) {
+            const uint32_t i = atomicAdd(&s.near_n, 1u);
+            if (i < uint32_t(kNear)) s.near()[i] = uint16_t(place_of(bits));
+          } else {
+            atomicMax(&s.beyond, int(a));
           }
         }
+        __syncwarp();
       };
-      uint4 next[kLoads];
-      int g = g0 + tid + kTile;
-      if (g - tid < g1) load(next, g);
-      look(first);
-      for (; g - tid < g1; g += kTile) {
-        uint4 q[kLoads];
-#pragma unroll
-        for (int r = 0; r < kLoads; ++r) q[r] = next[r];
-        if (g - tid + kTile < g1) load(next, g + kTile);
-        look(q);
+#pragma unroll 1
+      for (int g = g0 + tid; g - tid < g1; g += 2 * kThreads) {
+        const uint4 q0 = ahead[0], q1 = ahead[1];
+        ahead[0] = ahead[2], ahead[1] = ahead[3];
+        ahead[2] = load(g + 4 * kThreads), ahead[3] = load(g + 5 * kThreads);
+        count(q0);
+        count(q1);
       }
-      most = warp_max(most);
-      if (lane == 0) s.warp_top[warp] = most;
+      largest = warp_max(largest);
+      if (lane == 0) s.warp_top[warp] = largest;
       __syncthreads();
-      if (tid < C) {
-        Told t{s.warp_top[0], 0.f, 0.f, s.beyond};
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) t.top = fmaxf(t.top, s.warp_top[w]);
-        (C > 1 ? cluster.map_shared_rank(s.told[1], tid) : s.told[1])[rank] = t;
-      }
-      together();
-      top = s.told[1][0].top;
-      int beyond = s.told[1][0].beyond;
-#pragma unroll
-      for (int i = 1; i < C; ++i) top = fmaxf(top, s.told[1][i].top), beyond = max(beyond, s.told[1][i].beyond);
+      const int beyond = s.beyond;
       if (!beyond) break;
       // once more, with the bins that hold the largest of all
       binade = beyond >> 7;
-      together();  // everybody has read what was told
-      for (int i = 4 * tid; i < kBins; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+      for (int i = 4 * tid; i < kWords; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
       if (tid == 0) s.near_n = 0, s.beyond = 0;
+      start();
       __syncthreads();
     }
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all of them run
+    if (tid < C) {
+      Told t{s.warp_top[0], bound, base};
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) t.top = fmaxf(t.top, s.warp_top[w]);
+      (C > 1 ? cluster.map_shared_rank(s.told, tid) : s.told)[rank] = t;
+    }
+    if (tid == 32 && base == 0) s.hist[kMagnitudes - 1] += s.hist[kMinusWords], s.hist[kMinusWords] = 0;  // -0 is 0
+    together();
+    const int own_base = base;
+    const float own_bound = bound;
+    top = s.told[0].top, bound = s.told[0].bound, base = s.told[0].base;
+#pragma unroll
+    for (int i = 1; i < C; ++i) top = fmaxf(top, s.told[i].top), bound = fmaxf(bound, s.told[i].bound), base = max(base, s.told[i].base);
 
     if (!(top > -INFINITY)) {  // nothing above -infinity: what greedy acceptance takes, and no probability
       if (rank == 0) token = locate_in_order(row, 0, row.granules, kPlaceEnd, 1, s);
@@ -464,47 +466,61 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
       const u64 least = __float2ull_ru(min_p * float(kWeightOne));  // exact before it is rounded up
       auto place_at = [&](int bin) { return bin < kMagnitudes ? kPlaceZero - base - (kMagnitudes - 1 - bin) : 0x8000 + base + bin - kMagnitudes; };
       Shared &s0 = C > 1 ? *cluster.map_shared_rank(&s, 0) : s;
+      // a bin of the cluster's in a CTA with another base: nearer the middle, or none
+      auto count_of = [&](int i, int bin) -> uint32_t {
+        if (C == 1) return s.hist[word_of(bin)];
+        const int shift = base - s.told[i].base, at = bin < kMagnitudes ? bin - shift : bin + shift;
+        return at >= 0 && at < kBins ? cluster.map_shared_rank(s.hist, i)[word_of(at)] : 0;
+      };
 
       // ---- the cluster's counts, and its groups' counts and masses ---------------------------
-      uint32_t *sum = C > 1 ? s.sum : s.hist;  // in the first CTA
+      {
+        constexpr int kMine = kGroups / (C * kWarps);  // groups of a warp
 #pragma unroll 2
-      for (int group = rank * kWarps + warp; group < kGroups; group += C * kWarps) {
-        const int bin = group * 32 + lane;
-        uint32_t n = 0;
+        for (int k = 0; k < kMine; ++k) {
+          const int group = (rank + k * C) * kWarps + warp, bin = group * 32 + lane;
+          uint32_t count = 0;
+          u64 mass = 0;
+          if (value_at(place_at(group * 32)) >= bound) {  // its largest; where it is not there, the rest does not matter
 #pragma unroll
-        for (int i = 0; i < C; ++i) n += (C > 1 ? cluster.map_shared_rank(s.hist, i) : s.hist)[bin];
-        uint32_t count = 0;
-        u64 mass = 0;
-        if (__any_sync(0xffffffffu, n != 0)) {
-          const u64 w = weight_of(place_at(bin), best, scale, s.table);
-          if (w < least) n = 0;
-          count = __reduce_add_sync(0xffffffffu, n);
-          mass = warp_sum(n * w);
+            for (int i = 0; i < C; ++i) count += count_of(i, bin);
+            if (__any_sync(0xffffffffu, count != 0)) {
+              const u64 w = weight_of(place_at(bin), best, scale, s.table);
+              if (w < least) count = 0;
+              mass = count * w;
+              sum_up_to(count, mass);
+              s0.sum[bin] = count, s0.mass[bin] = mass;
+            }
+          }
+          if (lane == 31) s0.group_count[group] = count, s0.group_mass[group] = mass;
         }
-        if (C > 1) s0.sum[bin] = n;
-        else if (least) s.hist[bin] = n;
-        if (lane == 0) s0.group_count[group] = count, s0.group_mass[group] = mass;
       }
-      // values near zero: from the list, or, where it was too short, from the slice once more
+      // values near zero: from the list, or, where it was too short, from the slice once more,
+      // and from the bins of this CTA that the cluster has none for
       const uint32_t near_n = s.near_n;
-      if (near_n) {
+      if (near_n || base > own_base) {
         uint32_t count = 0;
         u64 mass = 0;
-        auto add = [&](int place) {
+        auto add = [&](int place, uint32_t n) {
           const u64 w = weight_of(place, best, scale, s.table);
-          if (w >= least) ++count, mass += w;
+          if (w >= least) count += n, mass += n * w;
         };
         if (near_n <= uint32_t(kNear)) {
-          for (uint32_t i = tid; i < near_n; i += kThreads) add(s.near[i]);
+          for (uint32_t i = tid; i < near_n; i += kThreads) add(s.near()[i], 1);
         } else {
           for (int g = g0 + tid; g < g1; g += kThreads) {
             const uint4 q = row.load(g);
 #pragma unroll 1
             for (int j = 0; j < 8; ++j) {
               const uint32_t bits = half_of(q, j);
-              if (int(bits & 0x7fffu) < base && bf2f(uint16_t(bits)) >= bound) add(place_of(bits));
+              if (int(bits & 0x7fffu) < own_base && bf2f(uint16_t(bits)) >= own_bound) add(place_of(bits), 1);
             }
           }
+        }
+        for (int i = tid; i < 2 * min(base - own_base, kMagnitudes); i += kThreads) {
+          const int off = i >> 1;
+          const uint32_t n = s.hist[i & 1 ? kMinusWords + off : kMagnitudes - 1 - off];
+          if (n) add(i & 1 ? 0x8000 + own_base + off : kPlaceZero - own_base - off, n);
         }
         count = __reduce_add_sync(0xffffffffu, count), mass = warp_sum(mass);
         if (lane == 0 && count) atomicAdd(&s0.near_count, count), atomicAdd(&s0.near_mass, mass);
@@ -513,80 +529,74 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
 
       if (rank == 0) {
         // ---- three questions, asked by the first warp -------------------------------------------
+        if (tid == 32) s.matches = 0, s.at = 0;
         if (warp == 0) {
-          constexpr int kMine = kGroups / 32;  // groups of a lane
-          uint32_t count[kMine], before = 0;
-          u64 mass[kMine], mass_before = 0;
+          // group sums up to each group, the values near zero before the 65th; a lane has four
+          constexpr int kMine = kGroups / 32;
+          uint32_t count[kMine], counts = 0;
+          u64 mass[kMine], masses = 0;
 #pragma unroll
           for (int i = 0; i < kMine; ++i) {
-            count[i] = s.group_count[lane * kMine + i], mass[i] = s.group_mass[lane * kMine + i];
-            before += count[i], mass_before += mass[i];
+            count[i] = counts += s.group_count[lane * kMine + i];
+            mass[i] = masses += s.group_mass[lane * kMine + i];
           }
-          const uint32_t own_count = before;
-          const u64 own_mass = mass_before;
+          const uint32_t own_count = counts;
+          const u64 own_mass = masses;
+          sum_up_to(counts, masses);
+          const uint32_t near_at = __shfl_sync(0xffffffffu, counts, 15), near_to = near_at + s.near_count;
+          const u64 near_mass_at = __shfl_sync(0xffffffffu, masses, 15), near_mass_to = near_mass_at + s.near_mass;
+          if (lane >= 16) counts += s.near_count, masses += s.near_mass;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
-            const u64 y = __shfl_up_sync(0xffffffffu, mass_before, o);
-            if (lane >= o) before += x, mass_before += y;
+          for (int i = 0; i < kMine; ++i) {
+            s.group_count[lane * kMine + i] = counts - own_count + count[i];
+            s.group_mass[lane * kMine + i] = masses - own_mass + mass[i];
           }
-          const uint32_t near_at = __shfl_sync(0xffffffffu, before, 15);  // before the values near zero
-          const u64 near_mass_at = __shfl_sync(0xffffffffu, mass_before, 15);
-          if (lane >= 16) before += s.near_count, mass_before += s.near_mass;
-          const uint32_t total_count = __shfl_sync(0xffffffffu, before, 31);
-          const u64 total = __shfl_sync(0xffffffffu, mass_before, 31);
-          before -= own_count, mass_before -= own_mass;
-          auto find = [&](Question what, u64 target) -> Found {
-            int group = -1;
-            uint32_t c0 = before, c = 0;
-            u64 m0 = mass_before, m = 0;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-              if (answers(what, target, c0, c0 + count[i], m0, m0 + mass[i])) group = lane * kMine + i, c = c0, m = m0;
-              c0 += count[i], m0 += mass[i];
+          __syncwarp();
+          const uint32_t total_count = __shfl_sync(0xffffffffu, counts, 31);
+          u64 rest = __shfl_sync(0xffffffffu, masses, 31);
+          Found f{best, 1, kWeightOne, 0, 0};
+          // each question: the first value up to which there are `target` logits, or as much mass
+#pragma unroll 1
+          for (int step = 0; step < 3; ++step) {
+            u64 target;
+            if (step == 0) {
+              if (uint32_t(top_k) >= total_count) continue;
+              target = u64(top_k);
+            } else if (step == 1) {
+              if (!(top_p < 1.f)) continue;
+              target = max(u64(1), share_of(fmaxf(top_p, 0.f), rest, true));
+            } else {  // to pass a share is to reach one more
+              target = u > 0.f ? (u < 1.f ? share_of(u, rest, false) + 1 : rest) : 1;
             }
-            const uint32_t who = __ballot_sync(0xffffffffu, group >= 0);
-            Found f{best, 1, kWeightOne, 0, 0};
-            if (!who) {  // among the values near zero: the whole CTA looks
-              if (lane == 0) s.asked = Asked{what, target}, s.found = f, s.before_count = near_at, s.before_mass = near_mass_at;
+            const bool by_count = step == 0;
+            const uint32_t lead = __ffs(__ballot_sync(0xffffffffu, (by_count ? u64(counts) : masses) >= target)) - 1;
+            if (lead == 16 && target <= (by_count ? u64(near_to) : near_mass_to)) {  // near zero: the whole CTA looks
+              if (lane == 0) s.asked = Asked{step, target}, s.found = f, s.before_count = near_at, s.before_mass = near_mass_at;
               __syncthreads();
-              find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, near_at, near_mass_at, what, target, s);
-              return s.found;
+              find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, near_at, near_mass_at, step == 0, target, s);
+              f = s.found;
+            } else if (lead < 32) {
+              const int mine = lead * kMine + (lane & (kMine - 1));
+              const uint32_t c = s.group_count[mine];
+              const u64 m = s.group_mass[mine];
+              const int group = lead * kMine + __ffs(__ballot_sync(0xffffffffu, (by_count ? u64(c) : m) >= target)) - 1;
+              const int bin = group * 32 + lane;
+              // before the group: what is up to it less what it has
+              const uint32_t c0 = s.group_count[group] - s.sum[group * 32 + 31], c1 = c0 + s.sum[bin];
+              const u64 m0 = s.group_mass[group] - s.mass[group * 32 + 31], m1 = m0 + s.mass[bin];
+              const int at = __ffs(__ballot_sync(0xffffffffu, (by_count ? u64(c1) : m1) >= target)) - 1;
+              const uint32_t to = __shfl_sync(0xffffffffu, c1, at), up = __shfl_sync(0xffffffffu, c1, at - 1), n = to - (at ? up : c0);
+              const u64 mass_to = __shfl_sync(0xffffffffu, m1, at), mass_up = __shfl_sync(0xffffffffu, m1, at - 1);
+              f.place = place_at(group * 32 + at);
+              f.mass = at ? mass_up : m0;
+              f.w = mass_to - f.mass, f.n = 1;
+              if (n > 1) {
+                f.w = weight_of(f.place, best, scale, s.table);
+                f.n = by_count ? uint32_t(target) - (to - n) : few_in(target - 1 - f.mass, f.w) + 1;
+              }
             }
-            const int lead = __ffs(who) - 1;
-            group = __shfl_sync(0xffffffffu, group, lead);
-            c = __shfl_sync(0xffffffffu, c, lead), m = __shfl_sync(0xffffffffu, m, lead);
-            const int bin = group * 32 + lane, place = place_at(bin);
-            const uint32_t n = sum[bin];
-            const u64 w = weight_of(place, best, scale, s.table);
-            uint32_t c1 = n;
-            u64 m1 = n * w;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const uint32_t x = __shfl_up_sync(0xffffffffu, c1, o);
-              const u64 y = __shfl_up_sync(0xffffffffu, m1, o);
-              if (lane >= o) c1 += x, m1 += y;
-            }
-            c1 += c, m1 += m;
-            const bool here = n && answers(what, target, c1 - n, c1, m1 - n * w, m1);
-            if (here) f = Found{place, number_of(what, target, c1 - n, m1 - n * w, w), w, m1 - n * w, 1};
-            const uint32_t whose = __ballot_sync(0xffffffffu, here);
-            const int from = whose ? __ffs(whose) - 1 : 0;
-            f.place = __shfl_sync(0xffffffffu, f.place, from), f.n = __shfl_sync(0xffffffffu, f.n, from);
-            f.w = __shfl_sync(0xffffffffu, f.w, from), f.mass = __shfl_sync(0xffffffffu, f.mass, from);
-            return f;
-          };
-          u64 rest = total;
-          if (uint32_t(top_k) < total_count) {
-            const Found f = find(kCount, u64(top_k));
-            rest = f.mass + f.n * f.w;
+            if (step < 2) rest = f.mass + f.n * f.w;
           }
-          if (top_p < 1.f) {
-            const Found f = find(kMassReaches, max(u64(1), share_of(fmaxf(top_p, 0.f), rest, true)));
-            rest = f.mass + f.n * f.w;
-          }
-          const float u = p.u[bt];
-          const Found f = find(kMassPasses, u > 0.f ? (u < 1.f ? share_of(u, rest, false) : rest - 1) : 0);
           logp = -log1pf(float(rest - f.w) / float(f.w));
           if (lane == 0) s.asked.what = -1, s.found = f;
           __syncthreads();
@@ -595,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
             __syncthreads();
             const Asked a = s.asked;
             if (a.what < 0) break;
-            find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, s.before_count, s.before_mass, Question(a.what), a.target, s);
+            find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, s.before_count, s.before_mass, a.what == 0, a.target, s);
           }
         }
 
@@ -606,11 +616,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
           token = locate_in_order(row, 0, row.granules, f.place, f.n, s);
         } else {
           const int bin = f.place <= kPlaceZero ? kMagnitudes - 1 - (a - base) : kMagnitudes + a - base;
-          uint32_t n = f.n, all = s.hist[bin];
+          uint32_t n = f.n, has[C];
+#pragma unroll
+          for (int i = 0; i < C; ++i) has[i] = count_of(i, bin);
           int q = 0;
-          if (C > 1) {
-            while (q < C - 1 && n > all) n -= all, ++q, all = cluster.map_shared_rank(s.hist, q)[bin];
-          }
+          uint32_t all = has[0];
+#pragma unroll
+          for (int i = 1; i < C; ++i)
+            if (q == i - 1 && n > all) n -= all, q = i, all = has[i];
           const int from = min(row.granules, q * each);
           token = locate(row, from, min(row.granules, from + each), f.place, n, all, s);
         }
@@ -646,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleParams 
 template <int C>
 cudaError_t launch(const SampleParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.gridDim = dim3(unsigned(p.B) * unsigned(p.T) * C);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
@@ -655,7 +669,7 @@ cudaError_t launch(const SampleParams &p, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = C, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = C > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, sample_kernel<C>, p);
 }
 
@@ -665,10 +679,31 @@ size_t accept_sampled_workspace_bytes(int B, int T) {
   return align256(size_t(B) * T * sizeof(int32_t)) + align256(size_t(B) * sizeof(uint32_t));
 }
 
+// CTAs of a position: as many as the GPU holds at once (two an SM) for all of them, where
+// each has 4096 logits at least.  Both sides, us of GPU time with 1, 2, 4, 8 CTAs:
+//   1 row of 32000, top-k 40, top-p, min-p        8.6   8.9   7.7   8.0
+//   16 of 151936, top-k 20, top-p                31.0  20.2  15.4  14.0
+//   64 of 151936, mixed                          32.6  24.5  20.7  28.8
+//   256 of 151936, unfiltered                    49.0  56.5  75.2   117
+//   480 of 151936, top-p                         90.8   104   140   232
 cudaError_t launch_sample(const SampleParams &p, cudaStream_t s) {
-  const int rows = p.B * p.T;
+  static std::atomic<int> cached[64];  // SMs by device, 0 until looked up
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
+  if (!sms) {
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    // more than the 48 KB of shared memory that need no asking
+    const void *kernels[] = {reinterpret_cast<const void *>(sample_kernel<1>), reinterpret_cast<const void *>(sample_kernel<2>),
+                             reinterpret_cast<const void *>(sample_kernel<4>), reinterpret_cast<const void *>(sample_kernel<8>)};
+    for (const void *k : kernels)
+      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Shared)))) != cudaSuccess) return e;
+    if (dev < 64) cached[dev].store(sms, std::memory_order_relaxed);
+  }
+  const long long rows = (long long)p.B * p.T;
   int C = 8;
-  while (C > 1 && (rows * C > (C > 2 ? 608 : 1216) || p.V < 2048 * C)) C /= 2;
+  while (C > 1 && (rows * C > 2 * sms || p.V < 4096 * C)) C /= 2;
   switch (C) {
     case 8: return launch<8>(p, s);
     case 4: return launch<4>(p, s);

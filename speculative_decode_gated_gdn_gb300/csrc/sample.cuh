@@ -100,9 +100,10 @@ __device__ __forceinline__ uint32_t few_in(unsigned long long a, unsigned long l
 // exp((value_at(place) - value_at(top)) / temperature) in units of 2^-43, rounded; top <= place.
 // The exponent t (base 2) is a sum of two floats, 2^-46 exact; 2^t = 2^n 2^(m/32) 2^r with the middle
 // factor from the table and the last, |r| <= 1/64, by its series: 2^-38 exact in all.
-__device__ __forceinline__ unsigned long long weight_of(int place, int top, Scale c, const unsigned long long *table) {
-  if (place == top || c.hi == 0.f) return kWeightOne;
+static __device__ __noinline__ unsigned long long weight_of(int place, int top, Scale c, const unsigned long long *table) {
+  if (place == top) return kWeightOne;
   if (top == kPlaceInf) return 0;
+  if (c.hi == 0.f) return kWeightOne;
   const float z = 0.5f * value_at(place), z0 = 0.5f * value_at(top);  // halves: their difference is finite
   const float s = z - z0, back = s - z;
   const float err = (z - (s - back)) + (-z0 - back);
