@@ -1,6 +1,6 @@
 """Speculative decoding of a two-layer hybrid model: one GDN layer, one attention layer over the paged 4-bit cache.
 
-    python examples/hybrid_decode.py [--rows 8] [--prompt 500] [--cycles 64] [--draft 1]
+    python examples/hybrid_decode.py [--rows 8] [--prompt 500] [--cycles 64] [--draft 1] [--samples 1] [--temperature 0.8]
 
 The weights are random, so the tokens mean nothing; what the script shows is how the calls go together.  The committed
 offsets that gdn_commit advances are the attention layer's lengths as well.  A prompt:
@@ -16,6 +16,13 @@ and a cycle of T tokens a row (the last accepted one and T - 1 drafts), captured
     gdn_conv_verify, gdn_kv4_append, gdn_kv4_attend
     gdn_accept_greedy        keep, and the next token
     gdn_commit               the GDN state of the accepted prefix; offsets += keep
+
+With --samples N every prompt goes on in N rows.  They share its full pages, and their tokens are drawn:
+
+    gdn_kv_fork, gdn_kv_copy_pages, gdn_move_rows    the prompt's pages and GDN state for its other rows
+    gdn_sample               each row's first token
+    gdn_kv_plan_shared, gdn_accept_sampled           in place of gdn_kv_plan and gdn_accept_greedy
+    gdn_kv_compact, gdn_kv_copy_pages                when rows have ended, what is left moves to the cache's front
 """
 import argparse
 import os
@@ -33,7 +40,7 @@ MODE = L.GDN_COMMIT_RECOMPUTE
 class Model:
     """B rows of the model with their GDN state, conv ring and cache pages."""
 
-    def __init__(self, B, T, max_len, vocab=512, width=256, H_k=2, H_v=4, d_gdn=64, H_q=8, H_kv=2, d=128, rot=64, page=32,
+    def __init__(self, B, T, max_len, samples=1, temperature=0.8, top_p=0.95, vocab=512, width=256, H_k=2, H_v=4, d_gdn=64, H_q=8, H_kv=2, d=128, rot=64, page=32,
                  seed=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *s, scale=1.0: (torch.randn(*s, generator=gen, device="cuda") * scale).bfloat16()
@@ -59,6 +66,10 @@ class Model:
         self.held, self.table = zeros(B), torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
         self.free_list = torch.arange(n_pages, dtype=torch.int32, device="cuda")
         self.free_count = torch.full((1,), n_pages, dtype=torch.int32, device="cuda")
+        # several rows a prompt: holders of each page, the rows' ways of sampling, and random numbers for a cycle
+        self.prompts, self.refs = B // samples, zeros(n_pages) if samples > 1 else None
+        self.ways = dict(temperature=torch.full((B,), temperature, device="cuda"), top_p=torch.full((B,), top_p, device="cuda"))
+        self.u = zeros(B, T, dtype=torch.float32)
         self.q_start, self.q_count, self.kv_len = zeros(B + 1), zeros(B), zeros(B)
         # text: the three axes of a position are the same, and the pairs of a head take them in turn
         t = torch.arange(max_len + T, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(rot // 2, dtype=torch.float64) / (rot // 2))
@@ -68,6 +79,7 @@ class Model:
         self.add = torch.full((B,), T, dtype=torch.int32, device="cuda")
         self.tokens, self.keep, self.next = zeros(B, T), zeros(B), zeros(B)
         self.accept_ws = zeros(L.gdn_accept_workspace_bytes(B, T, vocab), dtype=torch.uint8)
+        self.sample_ws = zeros(L.gdn_accept_sampled_workspace_bytes(B, T, vocab), dtype=torch.uint8)
         self.step = self._buffers(B * T, T)
 
     def _buffers(self, N, max_q):
@@ -78,8 +90,12 @@ class Model:
                     ws=z(L.gdn_kv4_attend_workspace_bytes(self.kd, N, max_q), dtype=torch.uint8))
 
     def _plan(self, buf, add, T):
-        L.gdn_kv_plan(self.kd, self.offsets, add, self.active, self.held, self.table, self.free_list, self.free_count,
-                      self.q_start, self.q_count, self.kv_len, buf["slots"], buf["positions"][0], T=T)
+        rows = (self.offsets, add, self.active, self.held, self.table, self.free_list, self.free_count)
+        out = (self.q_start, self.q_count, self.kv_len, buf["slots"], buf["positions"][0])
+        if self.refs is None:
+            L.gdn_kv_plan(self.kd, *rows, *out, T=T)
+        else:
+            L.gdn_kv_plan_shared(self.kd, *rows, self.refs, *out, T=T)
         buf["positions"][1:] = buf["positions"][0]
 
     def _attention(self, h, buf):
@@ -92,23 +108,60 @@ class Model:
         return buf["o"].flatten(1)
 
     def _gdn_inputs(self, h, n):
-        x = (h @ self.w_gdn).view(self.B, n, -1).contiguous()
-        g, beta = (h @ self.w_gate).float().view(self.B, n, 2, self.H_v).unbind(2)
+        rows = h.shape[0] // n
+        x = (h @ self.w_gdn).view(rows, n, -1).contiguous()
+        g, beta = (h @ self.w_gate).float().view(rows, n, 2, self.H_v).unbind(2)
         return x, -torch.nn.functional.softplus(g).contiguous(), beta.sigmoid().contiguous()
 
     def prompt(self, tokens):
-        """tokens [B][n]: fills state and cache, and puts the first token to verify in place."""
-        n = tokens.shape[1]
-        buf = self._buffers(self.B * n, n)
-        self._plan(buf, torch.full_like(self.add, n), 0)
+        """tokens [prompts][n]: fills state and cache, and puts every row's first token to verify in place."""
+        P, n = tokens.shape
+        buf = self._buffers(P * n, n)
+        add = torch.zeros_like(self.add)
+        add[:P] = n
+        self._plan(buf, add, 0)
         h = self.embed[tokens.reshape(-1)]
         x, g, beta = self._gdn_inputs(h, n)
-        o = torch.empty(self.B, n, self.H_v, self.d_gdn, dtype=torch.bfloat16, device="cuda")
-        ws = torch.empty(max(L.gdn_prefill_workspace_bytes(self.gdims, n), 16), dtype=torch.uint8, device="cuda")
+        o = torch.empty(P, n, self.H_v, self.d_gdn, dtype=torch.bfloat16, device="cuda")
+        dims = L.dims(B=P, T=self.T, H_k=self.gdims.H_k, H_v=self.H_v, d=self.d_gdn)  # the first P rows
+        ws = torch.empty(max(L.gdn_prefill_workspace_bytes(dims, n), 16), dtype=torch.uint8, device="cuda")
         a = self._attention(h, buf)
-        L.gdn_prefill_chunked(self.gdims, n, x, self.conv_w, g, beta, self.state, self.ring, self.offsets, o, ws)
-        last = torch.cat((o[:, -1].flatten(1), a.view(self.B, n, -1)[:, -1]), 1) @ self.w_out
-        self._feed(last.argmax(1).int())
+        L.gdn_prefill_chunked(dims, n, x, self.conv_w, g, beta, self.state[:P], self.ring[:P], self.offsets[:P], o, ws)
+        last = torch.cat((o[:, -1].flatten(1), a.view(P, n, -1)[:, -1]), 1) @ self.w_out
+        if self.refs is None:
+            self._feed(last.argmax(1).int())
+            return
+        self._fork(n)
+        self.u.uniform_()
+        L.gdn_sample(last.repeat(self.B // P, 1), self.u[:, 0].contiguous(), self.next, **self.ways)
+        self._feed(self.next)
+
+    def _fork(self, n):
+        """Rows from `prompts` on continue the prompts of n tokens in turn."""
+        dst = torch.arange(self.prompts, self.B, dtype=torch.int32, device="cuda")
+        src = dst % self.prompts
+        copies = torch.empty_like(src), torch.empty_like(src)
+        L.gdn_kv_fork(self.kd, src, dst, torch.full_like(src, n), self.held, self.table, self.free_list, self.free_count, self.refs,
+                      *copies)
+        L.gdn_kv_copy_pages(self.kd, [self.pages], *copies)
+        L.gdn_move_rows(self.gdims, self.gdims, MODE, [self.state], [self.ring], self.offsets, [self.state], [self.ring],
+                        self.offsets, None, src, dst)
+
+    def end(self, rows):
+        """The given rows end: their pages go back, those that others hold stay."""
+        self.offsets[rows] = 0
+        self.active[rows] = 0
+        self._plan(self.step, torch.zeros_like(self.add), self.T)
+
+    def compact(self):
+        """Moves the pages in use to the cache's front; returns how many there are."""
+        z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+        n = self.kd.n_pages
+        src, dst, count = z(max(n // 2, 1)), z(max(n // 2, 1)), z(1)
+        L.gdn_kv_compact(self.kd, self.held, self.table, self.refs, self.table, self.refs, self.free_list, self.free_count, z(n), src,
+                         dst, count)
+        L.gdn_kv_copy_pages(self.kd, [self.pages], src, dst, count=count)
+        return n - self.free_count.item()
 
     def _feed(self, nxt):
         """The next cycle's tokens: the accepted one, and drafts of it by a rule in place of a draft model."""
@@ -126,14 +179,18 @@ class Model:
         L.gdn_conv_verify(self.gdims, MODE, x, self.conv_w, g, beta, self.state, self.ring, self.offsets, self.active, o,
                           self.gdn_ws)
         logits = (torch.cat((o.flatten(2).flatten(0, 1), self._attention(h, buf)), 1) @ self.w_out).view(self.B, T, -1)
-        L.gdn_accept_greedy(logits, self.tokens, self.active, self.keep, self.next, self.accept_ws)
+        if self.refs is None:
+            L.gdn_accept_greedy(logits, self.tokens, self.active, self.keep, self.next, self.accept_ws)
+        else:
+            self.u.uniform_()
+            L.gdn_accept_sampled(logits, self.tokens, self.active, self.u, self.keep, self.next, None, None, self.sample_ws, **self.ways)
         L.gdn_commit(self.gdims, MODE, [self.state], [self.ring], [self.gdn_ws], self.keep, self.active, self.offsets)
         self._feed(self.next)
 
 
-def run(rows=8, prompt=500, cycles=64, draft=1, seed=0):
+def run(rows=8, prompt=500, cycles=64, draft=1, seed=0, samples=1, temperature=0.8):
     """Decodes and returns the model and the seconds a cycle took."""
-    m = Model(rows, draft + 1, prompt + (cycles + 3) * (draft + 1), seed=seed)
+    m = Model(rows * samples, draft + 1, prompt + (cycles + 3) * (draft + 1), samples, temperature, seed=seed)
     m.prompt(torch.randint(0, m.vocab, (rows, prompt), device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed + 1)))
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
@@ -161,12 +218,17 @@ def main():
     ap.add_argument("--prompt", type=int, default=500)
     ap.add_argument("--cycles", type=int, default=64)
     ap.add_argument("--draft", type=int, default=1)
+    ap.add_argument("--samples", type=int, default=1, help="rows that continue each prompt, by sampling if more than one")
+    ap.add_argument("--temperature", type=float, default=0.8)
     a = ap.parse_args()
-    m, dt = run(a.rows, a.prompt, a.cycles, a.draft)
+    m, dt = run(a.rows, a.prompt, a.cycles, a.draft, samples=a.samples, temperature=a.temperature)
     done = (m.offsets - a.prompt).float().mean().item()
     used = m.kd.n_pages - m.free_count.item()
-    print(f"{a.rows} rows, prompt {a.prompt}: {done:.1f} tokens a row in {a.cycles + 1} cycles of {a.draft + 1}, "
+    print(f"{a.rows} prompts of {a.prompt}, {m.B} rows: {done:.1f} tokens a row in {a.cycles + 1} cycles of {a.draft + 1}, "
           f"{dt * 1e6:.0f} us a cycle, {used} pages of {m.kd.page} tokens held ({used * L.gdn_kv4_page_bytes(m.kd)} bytes)")
+    if a.samples > 1:
+        m.end(torch.arange(a.rows, m.B, device="cuda"))
+        print(f"one row a prompt left: {m.compact()} pages, at the cache's front")
 
 
 if __name__ == "__main__":
