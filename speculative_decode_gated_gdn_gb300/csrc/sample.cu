@@ -228,27 +228,34 @@ __device__ __forceinline__ int pick(uint32_t m, uint32_t n, Shared &s) {
   return s.at;
 }
 
-// The same for a value that few logits have: they are listed, tile after tile until there are
-// n, and counted against one another.
+// The same for a value that `all` logits have, few: they are listed, tile after tile until there are
+// n, and counted against one another.  From the end, where it is nearer: a quarter of the slice
+// on average.
 __device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t n, uint32_t all, Shared &s) {
   if (all > uint32_t(kBins)) return locate_in_order(row, g0, g1, place, n, s);
   const int tid = threadIdx.x;
+  constexpr int kTile = kThreads * kLoads;
+  const bool back = n > all - n;
+  const uint32_t want = back ? all - n + 1 : n;
+  const int tiles = (g1 - g0 + kTile - 1) / kTile;
   // equal as numbers: -0 as 0, NaN never
   const __nv_bfloat162 v = __float2bfloat162_rn(value_at(place));
   auto same = [&](uint32_t w) { return __heq2_mask(*reinterpret_cast<const __nv_bfloat162 *>(&w), v); };
+  auto start_of = [&](int tile) { return g0 + (back ? tiles - 1 - tile : tile) * kTile + tid; };
   uint4 next[kLoads];
   auto load = [&](int g) {
 #pragma unroll
     for (int r = 0; r < kLoads; ++r)
       next[r] = g + r * kThreads < g1 ? row.load(g + r * kThreads) : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
   };
-  load(g0 + tid);
+  load(start_of(0));
   uint32_t found = 0;
-  for (int g = g0 + tid; g - tid < g1 && found < n; g += kThreads * kLoads) {  // the same for every thread
+  for (int tile = 0; tile < tiles && found < want; ++tile) {  // the same for every thread
+    const int g = start_of(tile);
     uint4 q[kLoads];
 #pragma unroll
     for (int r = 0; r < kLoads; ++r) q[r] = next[r];
-    if (g - tid + kThreads * kLoads < g1) load(g + kThreads * kLoads);
+    if (tile + 1 < tiles) load(start_of(tile + 1));
 #pragma unroll
     for (int r = 0; r < kLoads; ++r) {
       const uint32_t m0 = same(q[r].x), m1 = same(q[r].y), m2 = same(q[r].z), m3 = same(q[r].w);
@@ -264,7 +271,8 @@ __device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t 
     found = s.matches;
     __syncthreads();
   }
-  return pick(min(found, uint32_t(kBins)), n, s);
+  const uint32_t m = min(found, uint32_t(kBins));
+  return pick(m, back ? m - want + 1 : want, s);
 }
 
 __device__ __forceinline__ __nv_bfloat162 b2(const uint32_t &w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
