@@ -120,6 +120,61 @@ def test_equal_values_go_by_index(gdn):
         check(bits_of(x), rng.random(6), **kw)
 
 
+def test_the_largest_vocabulary_of_equal_values(gdn):
+    """2^20 logits of weight 1: the mass is 2^63 units."""
+    v = 1 << 20
+    x = torch.full((3, v), -2.5, dtype=torch.bfloat16, device="cuda")
+    u = torch.tensor([0.0, 0.5, 1 - 2 ** -24], device="cuda")
+    token, logp = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(3, device="cuda")
+    L.gdn_sample(x, u, token, logp)
+    assert token.tolist() == [0, v // 2, v - 1]
+    assert (logp.double() + math.log(v)).abs().max() <= 2 ** -22 * (1 + math.log(v))
+    L.gdn_sample(x, u, token, top_p=torch.full((3,), 0.75, device="cuda"), top_k=torch.full((3,), v - 4, dtype=torch.int32, device="cuda"))
+    n = (v - 4) * 3 // 4
+    assert token.tolist() == [0, n // 2, int((1 - 2 ** -24) * n)]
+
+
+def test_most_rows(gdn):
+    rng = np.random.default_rng(11)
+    bits = bits_of(rng.standard_normal((65535, 40)) * 3)
+    u = rng.random(65535).astype(np.float32)
+    token = torch.zeros(65535, dtype=torch.int32, device="cuda")
+    L.gdn_sample(logits_on(bits), torch.from_numpy(u).cuda(), token)
+    got, x = token.cpu().numpy(), R.values(bits)
+    for i in range(0, 65535, 331):
+        assert got[i] == R.draw(x[i], u[i])[0]
+
+
+def test_threads_and_repeats(gdn):
+    """Calls at once on streams of their own give what one call gives, every time."""
+    import threading
+    wrong = []
+
+    def work(seed):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                gen = torch.Generator(device="cuda").manual_seed(seed)
+                x = (torch.randn(20, 30011, device="cuda", generator=gen) * 2).bfloat16()
+                u = torch.rand(20, device="cuda", generator=gen)
+                first = torch.zeros(20, dtype=torch.int32, device="cuda"), torch.zeros(20, device="cuda")
+                L.gdn_sample(x, u, *first)
+                outs = [(torch.zeros_like(first[0]), torch.zeros_like(first[1])) for _ in range(30)]
+                for o in outs:
+                    L.gdn_sample(x, u, *o)
+                stream.synchronize()
+                assert all(torch.equal(a, b) for o in outs for a, b in zip(o, first))
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+
+
 def test_masks(gdn):
     """Forbidden tokens, rows with one allowed token or none, NaN and infinities."""
     rng = np.random.default_rng(2)
