@@ -189,6 +189,15 @@ __device__ __forceinline__ void tma_store_2d(const TmaDesc *map, int x, int y, c
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// The CTA's barrier where it stands in a loop or branch that depends on what is in memory.  That
+// all threads go the same way is not known to the compiler there, and it may leave a warp split
+// by a loop before; a split warp arrives more than once, and every barrier from then on ends
+// before the last warp is there.  So the warp's lanes meet first.
+__device__ __forceinline__ void sync_cta() {
+  __syncwarp();
+  __syncthreads();
+}
+
 template <typename Kernel, typename Params>
 inline cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, cudaStream_t stream, const Params &p) {
   cudaLaunchConfig_t cfg = {};

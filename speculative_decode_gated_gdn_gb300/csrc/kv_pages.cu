@@ -65,7 +65,7 @@ __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
     }
     p.copy_src[i] = verdict;
   }
-  __syncthreads();
+  sync_cta();
   long long taken = 0;
   for (int i0 = 0; i0 < p.n; i0 += kScanThreads) {
     const int i = i0 + tid;
@@ -106,7 +106,7 @@ __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
       p.copy_src[i] = from, p.copy_dst[i] = to;
     }
     taken += all;
-    __syncthreads();
+    sync_cta();
   }
   if (tid == 0) *p.free_count = count0 - int(min(taken, (long long)count0));
 }
@@ -140,6 +140,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   pdl_wait();
   pdl_trigger();
   if (cluster.block_rank() == 0) decide_forks(p, s_warp);
+  __syncwarp();
   cluster.sync();
   constexpr int kWarps = kCluster * kScanThreads / 32;
   const int g = int(cluster.block_rank()) * (kScanThreads / 32) + int(threadIdx.x >> 5);
@@ -210,6 +211,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kScanThreads) kv_com
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = C > 1 ? int(cluster.block_rank()) : 0;
   auto together = [&] {
+    __syncwarp();  // a warp that a loop has split would arrive more than once
     if (C > 1) cluster.sync();
     else __syncthreads();
   };
@@ -223,6 +225,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kScanThreads) kv_com
   long long used;
   const long long upto = block_scan(count, s_warp, &used);
   if (lane == 31) s_before[warp] = int(upto);
+  __syncwarp();
   if (C > 1) cluster.sync();  // every CTA runs
   if (tid < C) (C > 1 ? cluster.map_shared_rank(s_used, tid) : s_used)[rank] = int(used);
   together();

@@ -95,6 +95,7 @@ __device__ __forceinline__ long long release_shared(const KvPlanParams &p, int c
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = C > 1 ? int(cluster.block_rank()) : 0, tid = threadIdx.x, n_pages = p.n_pages;
   auto together = [&] {
+    __syncwarp();  // a warp that a loop has split would arrive more than once
     if (C > 1) cluster.sync();
     else __syncthreads();
   };
@@ -115,7 +116,7 @@ __device__ __forceinline__ long long release_shared(const KvPlanParams &p, int c
         if (pass == 0 && rank == 0 && b < p.B && r.bad) atomicOr(p.status, GDN_STATUS_BAD_LEN);
         const long long end = block_scan(max(r.held - r.want, 0), s_warp, &total);
         s_ends[tid] = int(end), s_from[tid] = r.want;
-        __syncthreads();
+        sync_cta();
       }
       if (total == 0) continue;  // the same for every thread of the cluster
       const PlanChunk chunk{s_ends, s_from, b0, rows};
@@ -169,7 +170,10 @@ __device__ __forceinline__ long long release_shared(const KvPlanParams &p, int c
             gather(i0);
             counts(c);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) mine += __syncthreads_count(page[k] >= 0 && c[k] == mark(i0, k));
+            for (int k = 0; k < kBatch; ++k) {
+              __syncwarp();
+              mine += __syncthreads_count(page[k] >= 0 && c[k] == mark(i0, k));
+            }
           }
           if (tid < C) cluster.map_shared_rank(s_pushed, tid)[rank] = mine;
           together();
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     released = release_shared<C>(p, count0, s_ends, s_from, s_warp, s_pushed);
     if (C > 1) {
       cg::cluster_group cluster = cg::this_cluster();
+      __syncwarp();
       cluster.sync();  // the rows are read, the pushed pages visible
       if (cluster.block_rank() != 0) return;
     }
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
       if (total == 0) continue;  // the same for every thread
       s_ends[tid] = int(end);
       s_from[tid] = r.want;
-      __syncthreads();
+      sync_cta();
       const PlanChunk chunk{s_ends, s_from, b0, rows};
       for (int i = tid; i < int(total); i += kPlanThreads) {
         int32_t *cell = chunk.cell(p, i);
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     }
   }
   const long long avail = min((long long)n_pages, count0 + released);
-  __syncthreads();  // the pushed pages are visible to the whole CTA
+  sync_cta();  // the pushed pages are visible to the whole CTA
 
   // ---- pages taken, in row order -----------------------------------------------
   long long taken0 = 0, tokens0 = 0, granted = 0, got_sum = 0;
@@ -288,7 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
       if (b == p.B - 1) p.q_start[p.B] = p.T > 0 ? p.B * p.T : int(granted + a_end);
       p.held[b] = r.held - max(r.held - r.want, 0) + got;
     }
-    __syncthreads();
+    sync_cta();
     for (int i = tid; i < int(got_total); i += kPlanThreads) {
       const int w = find_row(s_ends, rows, i);
       const long long from = avail - 1 - (taken0 + i);
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     tokens0 += tok_total;
     granted += a_total;
     got_sum += got_total;
-    __syncthreads();  // s_ends is free for the next chunk, and the rows' results are visible
+    sync_cta();  // s_ends is free for the next chunk, and the rows' results are visible
   }
   if (tid == 0) *p.free_count = int(avail - got_sum);
   if (!write_slots) return;

@@ -114,9 +114,9 @@ __device__ __forceinline__ void sum_up_to(uint32_t &count, u64 &mass) {
 __device__ __forceinline__ void scan(uint32_t &count, u64 &mass, Shared &s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   sum_up_to(count, mass);
-  __syncthreads();
+  sync_cta();
   if (lane == 31) s.warp_count[warp] = count, s.warp_mass[warp] = mass;
-  __syncthreads();
+  sync_cta();
 #pragma unroll
   for (int w = 0; w < kWarps - 1; ++w)
     if (w < warp) count += s.warp_count[w], mass += s.warp_mass[w];
@@ -135,10 +135,10 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
   const int tid = threadIdx.x;
   constexpr int kPer = kWindow / kThreads;
   while (from < end) {
-    __syncthreads();
+    sync_cta();
     for (int i = tid; i < kWindow; i += kThreads) s.window()[i] = 0;
     if (tid == 0) s.next = end, s.found.hit = 0;
-    __syncthreads();
+    sync_cta();
     int next = end;
     for (int g = tid; g < row.granules; g += kThreads) {
       const uint4 q = row.load(g);
@@ -151,7 +151,7 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
       }
     }
     if (next < end) atomicMin(&s.next, next);
-    __syncthreads();
+    sync_cta();
     uint32_t count = 0;
     u64 mass = 0;
 #pragma unroll 1
@@ -181,11 +181,11 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
       }
     }
     if (tid == kThreads - 1) s.before_count = count1, s.before_mass = mass1;
-    __syncthreads();
+    sync_cta();
     const bool hit = s.found.hit;
     count0 = s.before_count, mass0 = s.before_mass;
     from = s.next;
-    __syncthreads();  // everybody has read them
+    sync_cta();  // everybody has read them
     if (hit) return;
   }
 }
@@ -212,7 +212,7 @@ __device__ __noinline__ int locate_in_order(const SampleRow &row, int g0, int g1
         if ((mask >> j & 1) && --left == 0) break;
       s.at = row.first(g) + int(j);
     }
-    __syncthreads();
+    sync_cta();
     uint32_t all = 0;
     for (int w = 0; w < kWarps; ++w) all += s.warp_count[w];
     before += all;
@@ -225,7 +225,7 @@ __device__ __noinline__ int locate_in_order(const SampleRow &row, int g0, int g1
 __device__ __forceinline__ int pick(uint32_t m, uint32_t n, Shared &s) {
   const int tid = threadIdx.x;
   if (tid < 4 && m + tid < uint32_t(kBins)) s.sum[m + tid] = 0xffffffffu;
-  __syncthreads();
+  sync_cta();
   for (uint32_t i = tid; i < m; i += kThreads) {
     const uint32_t x = s.sum[i];
     uint32_t below = 0;
@@ -235,7 +235,7 @@ __device__ __forceinline__ int pick(uint32_t m, uint32_t n, Shared &s) {
     }
     if (below + 1 == n) s.at = int(x);
   }
-  __syncthreads();
+  sync_cta();
   return s.at;
 }
 
@@ -278,9 +278,9 @@ __device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t 
         for (; bits && k < uint32_t(kBins); ++k, bits &= bits - 1) s.sum[k] = uint32_t(at + __ffs(bits) - 1);
       }
     }
-    __syncthreads();
+    sync_cta();
     found = s.matches;
-    __syncthreads();
+    sync_cta();
   }
   const uint32_t m = min(found, uint32_t(kBins));
   return pick(m, back ? m - want + 1 : want, s);
@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const int rank = C > 1 ? int(cluster.block_rank()) : 0;
   const int bt = blockIdx.x / C, b = bt / p.T;
   auto together = [&] {
+    __syncwarp();
     if (C > 1) cluster.sync();
     else __syncthreads();
   };
@@ -360,8 +361,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   int token = -1;
   float logp = 0.f;
   if (active) {
+    __syncwarp();
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
-    for (int i = 4 * tid; i < kWords; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+    auto clear = [&] {  // as many rounds for every thread
+#pragma unroll
+      for (int i = 4 * tid; i - 4 * tid < kWords; i += 4 * kThreads)
+        if (i < kWords) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+    };
+    clear();
     if (tid < 32) s.table[tid] = kExp2Table[tid];
     if (tid == 0) s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0;
     if (!(temperature > 0.f)) temperature = 0.f, min_p = 0.f, top_p = 1.f, top_k = 1;
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     bound = warp_min(bound), low = warp_min(low);
     if (lane == 0) s.warp_top[warp] = top, s.warp_low[warp] = low, s.warp_bound[warp] = bound;
-    __syncthreads();
+    sync_cta();
     top = s.warp_top[0], low = s.warp_low[0], bound = s.warp_bound[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s.warp_top[w]), low = fminf(low, s.warp_low[w]), bound = fminf(bound, s.warp_bound[w]);
@@ -450,17 +457,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       }
       largest = warp_max(largest);
       if (lane == 0) s.warp_top[warp] = largest;
-      __syncthreads();
+      sync_cta();
       const int beyond = s.beyond;
-      if (!beyond) break;
+      __syncwarp();
+      if (!__syncthreads_or(beyond)) break;
       // once more, with the bins that hold the largest of all
       binade = beyond >> 7;
-      __syncthreads();
-      for (int i = 4 * tid; i < kWords; i += 4 * kThreads) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+      clear();
       if (tid == 0) s.near_n = 0, s.beyond = 0;
       start();
-      __syncthreads();
+      sync_cta();
     }
+    __syncwarp();
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all of them run
     if (tid < C) {
       Told t{s.warp_top[0], bound, base};
@@ -591,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const uint32_t lead = __ffs(__ballot_sync(0xffffffffu, (by_count ? u64(counts) : masses) >= target)) - 1;
             if (lead == 16 && target <= (by_count ? u64(near_to) : near_mass_to)) {  // near zero: the whole CTA looks
               if (lane == 0) s.asked = Asked{step, target}, s.found = f, s.before_count = near_at, s.before_mass = near_mass_at;
-              __syncthreads();
+              sync_cta();
               find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, near_at, near_mass_at, step == 0, target, s);
               f = s.found;
             } else if (lead < 32) {
@@ -618,10 +626,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           }
           logp = -log1pf(float(rest - f.w) / float(f.w));
           if (lane == 0) s.asked.what = -1, s.found = f;
-          __syncthreads();
+          sync_cta();
         } else {
           for (;;) {
-            __syncthreads();
+            sync_cta();
             const Asked a = s.asked;
             if (a.what < 0) break;
             find_in_windows(row, kPlaceZero - base + 1, 0x8000 + base, best, scale, least, s.before_count, s.before_mass, a.what == 0, a.target, s);
@@ -648,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
       }
     }
+    __syncwarp();
     if (C > 1) cluster.sync();  // the first CTA has read what it needs of the others
   }
   if (rank != 0) return;

@@ -15,9 +15,9 @@ __device__ __forceinline__ long long block_scan(long long v, long long *s_warp, 
     const long long u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
-  __syncthreads();  // s_warp may still be read by an earlier scan
+  sync_cta();  // s_warp may still be read by an earlier scan
   if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
+  sync_cta();
   if (warp == 0) {
     long long w = s_warp[lane];
 #pragma unroll
@@ -27,7 +27,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long *s_warp, 
     }
     s_warp[lane] = w;
   }
-  __syncthreads();
+  sync_cta();
   *total = s_warp[31];
   return v + (warp ? s_warp[warp - 1] : 0);
 }

@@ -228,6 +228,35 @@ def test_values_far_from_usual(gdn, name):
         check(bits, rng.random(4), **kw)
 
 
+@pytest.mark.parametrize("rows,v", [(160, 40001), (80, 60003), (40, 100003), (3, 200003)])
+@pytest.mark.parametrize("name", ["forbidden", "late", "late infinity", "late negative", "every slice its own"])
+def test_counts_begin_again(gdn, name, rows, v):
+    """Logits far above what a slice's first 16384 show, in slices of one, two, four and eight a row: the counts begin again
+    with other bins, in some CTAs and not in others."""
+    rng = np.random.default_rng(v)
+    x = rng.standard_normal((rows, v))
+    kw = dict(temperature=1.0, top_p=0.9)
+    if name == "forbidden":  # few allowed, small ones first
+        x *= 2.2
+        x[rng.random((rows, v)) < 0.99] = -INF
+        x[:, 17] = 1.0
+        kw = dict(min_p=0.2, top_k=1231, top_p=0.99)
+    elif name == "late":
+        x[:, :v // 2] *= 1e-3
+        x[:, -90:] += 40
+        kw = dict(temperature=2.0, top_k=rng.choice([0, 5, 60, 700], rows))
+    elif name == "late infinity":
+        x[::2, -7] = INF
+        x[1::2, -1] = 3e38
+    elif name == "late negative":
+        x[:, -5000:] = -1e6 * (1 + rng.random((rows, 5000)))
+        kw = dict(temperature=1e7)
+    else:
+        x *= np.exp2(rng.integers(-6, 7, v // 1000 + 1)).repeat(1000)[:v]
+        kw = dict(temperature=30.0)
+    check(bits_of(x), rng.random(rows), **kw)
+
+
 def run_accept(logits, draft, active, u, ws=None, outputs=True, **kw):
     B, T, V = logits.shape
     z = lambda *s, dtype=torch.int32: torch.full(s, -9, dtype=dtype, device="cuda")
