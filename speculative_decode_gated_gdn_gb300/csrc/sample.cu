@@ -92,7 +92,7 @@ struct Shared {
   float warp_top[32], warp_low[32], warp_bound[32];
   Told told[8];             // by rank
   uint32_t near_n;          // of this CTA's list
-  int beyond, next, at;
+  int beyond, next, at, dust;
   uint32_t matches;
   u64 before_mass;
   uint32_t before_count;
@@ -158,7 +158,7 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
     for (int i = 0; i < kPer; ++i) {
       const uint32_t n = s.window()[tid * kPer + i];
       const u64 w = n ? weight_of(from + tid * kPer + i, top, scale, s.table) : 0;
-      if (w >= least) count += n, mass += n * w;
+      if (w && w >= least) count += n, mass += n * w;
     }
     uint32_t count1 = count;
     u64 mass1 = mass;
@@ -172,7 +172,7 @@ __device__ __noinline__ void find_in_windows(const SampleRow &row, int from, int
         const int place = from + tid * kPer + i;
         uint32_t n = s.window()[tid * kPer + i];
         const u64 w = n ? weight_of(place, top, scale, s.table) : 0;
-        if (w < least) n = 0;
+        if (!w || w < least) n = 0;
         if (n && target <= (by_count ? u64(count + n) : mass + n * w)) {
           s.found = Found{place, by_count ? uint32_t(target) - count : few_in(target - 1 - mass, w) + 1, w, mass, 1};
           break;
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     };
     clear();
     if (tid < 32) s.table[tid] = kExp2Table[tid];
-    if (tid == 0) s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0;
+    if (tid == 0) s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0, s.dust = 0;
     if (!(temperature > 0.f)) temperature = 0.f, min_p = 0.f, top_p = 1.f, top_k = 1;
     min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
     if (top_k <= 0 || top_k > p.V) top_k = p.V;
@@ -393,10 +393,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     top = s.warp_top[0], low = s.warp_low[0], bound = s.warp_bound[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s.warp_top[w]), low = fminf(low, s.warp_low[w]), bound = fminf(bound, s.warp_bound[w]);
-    // Weights under 2^-44 count as 0: 46 ln 2 temperatures below the largest.  Rounding moves these
-    // bounds by far less than a step of bf16, and never above the largest.
+    // Weights under 2^-44 round to 0 and are dust (below), those under 2^-53 are nothing: 54 ln 2
+    // temperatures below the largest.  Rounding moves these bounds by far less than a step of bf16,
+    // and never above the largest.
     if (top > -INFINITY && top < INFINITY) {
-      bound = fmaxf(bound, top - 31.9f * temperature);
+      bound = fmaxf(bound, top - 37.4f * temperature);
       if (min_p > 0.f) bound = fmaxf(bound, top + temperature * __logf(min_p) - (1e-3f * temperature + 1e-6f * fabsf(top)));
     } else if (top == INFINITY) {
       bound = INFINITY;
@@ -500,6 +501,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return at >= 0 && at < kBins ? cluster.map_shared_rank(s.hist, i)[word_of(at)] : 0;
       };
 
+      // Dust: weights too small for the units of the masses.  It is told, because where the rest meets
+      // a border exactly (two equal logits share the mass, top_p is 0.5) any more than nothing decides.
+      const float dust_from = top - 36.7f * temperature;
+      auto is_dust = [&](int place, u64 w) { return !w && !least && value_at(place) >= dust_from; };
+
       // ---- the cluster's counts, and its groups' counts and masses ---------------------------
       {
         constexpr int kMine = kGroups / (C * kWarps);  // groups of a warp
@@ -513,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             for (int i = 0; i < C; ++i) count += count_of(i, bin);
             if (__any_sync(0xffffffffu, count != 0)) {
               const u64 w = weight_of(place_at(bin), best, scale, s.table);
-              if (w < least) count = 0;
+              if (count && is_dust(place_at(bin), w)) s0.dust = 1;
+              if (!w || w < least) count = 0;
               mass = count * w;
               sum_up_to(count, mass);
               s0.sum[bin] = count, s0.mass[bin] = mass;
@@ -530,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         u64 mass = 0;
         auto add = [&](int place, uint32_t n) {
           const u64 w = weight_of(place, best, scale, s.table);
-          if (w >= least) count += n, mass += n * w;
+          if (is_dust(place, w)) s0.dust = 1;
+          if (w && w >= least) count += n, mass += n * w;
         };
         if (near_n <= uint32_t(kNear)) {
           for (uint32_t i = tid; i < near_n; i += kThreads) add(s.near()[i], 1);
@@ -587,11 +595,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           for (int step = 0; step < 3; ++step) {
             u64 target;
             if (step == 0) {
-              if (uint32_t(top_k) >= total_count) continue;
+              if (uint32_t(top_k) >= total_count) continue;  // all that has weight
               target = u64(top_k);
             } else if (step == 1) {
               if (!(top_p < 1.f)) continue;
-              target = max(u64(1), share_of(fmaxf(top_p, 0.f), rest, true));
+              const bool dust = s.dust && uint32_t(top_k) > total_count;
+              target = dust ? share_of(fmaxf(top_p, 0.f), rest, false) + 1 : max(u64(1), share_of(fmaxf(top_p, 0.f), rest, true));
             } else {  // to pass a share is to reach one more
               target = u > 0.f ? (u < 1.f ? share_of(u, rest, false) + 1 : rest) : 1;
             }

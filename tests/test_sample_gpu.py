@@ -175,6 +175,21 @@ def test_threads_and_repeats(gdn):
     assert not wrong, wrong
 
 
+def test_borders_that_the_mass_meets_exactly(gdn):
+    """Two, or four, equal maxima and top_p a half: the first are half of the mass, so they are kept alone only if nothing else
+    has any; what is 2^-47 of the largest, and less than a unit of the masses, still decides."""
+    for tops, others, v in ((2, 0, 40), (2, 3, 40), (4, 5, 5000), (2, 900, 20000)):
+        x = np.full((8, v), -INF)
+        x[:, 1:1 + tops] = 3.0
+        x[:, 10:10 + others] = 3.0 - 47 * math.log(2) * 0.25  # weights of 2^-47 at a quarter's temperature
+        u = np.linspace(0.05, 0.95, 8)
+        got = check(bits_of(x), u, temperature=0.25, top_p=0.5)
+        assert len(set(got.tolist())) == (tops // 2 + 1 if others else tops // 2)
+        check(bits_of(x), u, temperature=0.25, top_p=0.5, top_k=tops)  # only the maxima
+        check(bits_of(x), u, temperature=0.25, top_p=0.5, top_k=tops + 1)
+        check(bits_of(x), u, temperature=0.25, top_p=0.5, min_p=0.1)
+
+
 def test_masks(gdn):
     """Forbidden tokens, rows with one allowed token or none, NaN and infinities."""
     rng = np.random.default_rng(2)
