@@ -191,6 +191,28 @@ def _ptr(t, what, dtype=None):
     return t.data_ptr()
 
 
+_device_number = None
+
+
+def _here():
+    """The current CUDA device's number: what get_device() of a call's tensors
+    has to be (-1 is the host); -2 where there is none."""
+    global _device_number
+    if _device_number is None:
+        _device_number = _t()._C._cuda_getDevice
+    try:
+        return _device_number()
+    except RuntimeError:
+        return -2
+
+
+def _elsewhere(t, what):
+    """Refuses a tensor that is on another CUDA device than the current one,
+    whose address the call's kernels could not follow."""
+    if t.get_device() != _here():
+        raise ValueError(f"{what}: tensor is on {t.device}, the current CUDA device is {_here()}")
+
+
 _raw_stream = None
 
 
@@ -400,7 +422,7 @@ def gdn_accept_greedy(logits, draft, active, keep, nxt, ws, stream=None):
     _check(rc, "gdn_accept_greedy")
 
 
-def _logits(t, dims):
+def _logits(t, dims, here):
     """Pointer and position stride of [B][V] or [B][T][V] bf16 logits whose
     positions lie at equal distances (a slice of a padded vocabulary serves)."""
     torch = _t()
@@ -409,6 +431,8 @@ def _logits(t, dims):
             raise TypeError(f"logits: expected {torch.bfloat16}, got {t.dtype}")
         if not t.is_cuda:
             raise ValueError("logits: tensor must be on a CUDA device")
+        if t.get_device() != here:
+            _elsewhere(t, "logits")
         shape, stride = t.shape, t.stride()
     except AttributeError:
         _need(logits=t)
@@ -425,7 +449,7 @@ def _logits(t, dims):
     return t.data_ptr(), s
 
 
-def _some_ptrs(*args):
+def _some_ptrs(here, *args):
     """_ptrs of arguments that may be None, which stays None."""
     p = []
     for t, what, n, dtype in args:
@@ -433,13 +457,14 @@ def _some_ptrs(*args):
             p.append(None)
         else:
             try:
-                if t.numel() == n and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+                if t.numel() == n and t.dtype is dtype and t.get_device() == here and t.is_contiguous():
                     p.append(t.data_ptr())
                     continue
             except AttributeError:
                 pass
             _count(t, what, n)
             p.append(_ptr(t, what, dtype))
+            _elsewhere(t, what)
     return p
 
 
@@ -450,13 +475,12 @@ def gdn_sample(logits, u, token, logp=None, temperature=None, top_k=None, top_p=
     place.  temperature, top_p, min_p [B] fp32, top_k [B] int32, active [B]
     uint8; None: 1, off, off, off, all."""
     torch = _t()
-    f32, i32 = torch.float32, torch.int32
-    lp, stride = _logits(logits, 2)
+    f32, i32, here = torch.float32, torch.int32, _here()
+    lp, stride = _logits(logits, 2, here)
     B, V = logits.shape
-    up, tp = _ptrs((u, "u", B, f32), (token, "token", B, i32))
-    a, t, k, p, m, lg = _some_ptrs((active, "active", B, torch.uint8), (temperature, "temperature", B, f32), (top_k, "top_k", B, i32),
-                                   (top_p, "top_p", B, f32), (min_p, "min_p", B, f32), (logp, "logp", B, f32))
-    rc = load().gdn_sample(B, V, lp, stride, a, t, k, p, m, up, tp, lg, _stream(stream))
+    p = _some_ptrs(here, (active, "active", B, torch.uint8), (temperature, "temperature", B, f32), (top_k, "top_k", B, i32),
+                   (top_p, "top_p", B, f32), (min_p, "min_p", B, f32), (u, "u", B, f32), (token, "token", B, i32), (logp, "logp", B, f32))
+    rc = load().gdn_sample(B, V, lp, stride, *p, _stream(stream))
     if rc:
         _check(rc, "gdn_sample")
 
@@ -474,18 +498,19 @@ def gdn_accept_sampled(logits, draft, active, u, keep, nxt, token, logp, ws, tem
     logp [B][T] fp32 (each may be None), written in place.  ws:
     gdn_accept_sampled_workspace_bytes(B, T, V) bytes, zero-filled once."""
     torch = _t()
-    f32, i32 = torch.float32, torch.int32
-    lp, stride = _logits(logits, 3)
+    f32, i32, here = torch.float32, torch.int32, _here()
+    lp, stride = _logits(logits, 3, here)
     B, T, V = logits.shape
     N = B * T
-    dp, up, kp, np_ = _ptrs((draft, "draft", N, i32), (u, "u", N, f32), (keep, "keep", B, i32), (nxt, "next", B, i32))
-    a, t, k, p, m, tp, lg = _some_ptrs((active, "active", B, torch.uint8), (temperature, "temperature", B, f32),
-                                       (top_k, "top_k", B, i32), (top_p, "top_p", B, f32), (min_p, "min_p", B, f32),
-                                       (token, "token", N, i32), (logp, "logp", N, f32))
-    wp = _ptr(ws, "ws")
-    _need(ws=ws)
-    rc = load().gdn_accept_sampled(B, T, V, lp, stride, dp, a, t, k, p, m, up, kp, np_, tp, lg, wp,
-                                   ws.numel() * ws.element_size(), _stream(stream))
+    try:
+        bytes_ = ws.numel() * ws.element_size()
+    except AttributeError:
+        _need(ws=ws)
+        raise
+    p = _some_ptrs(here, (draft, "draft", N, i32), (active, "active", B, torch.uint8), (temperature, "temperature", B, f32),
+                   (top_k, "top_k", B, i32), (top_p, "top_p", B, f32), (min_p, "min_p", B, f32), (u, "u", N, f32), (keep, "keep", B, i32),
+                   (nxt, "next", B, i32), (token, "token", N, i32), (logp, "logp", N, f32), (ws, "ws", ws.numel(), ws.dtype))
+    rc = load().gdn_accept_sampled(B, T, V, lp, stride, *p, bytes_, _stream(stream))
     if rc:
         _check(rc, "gdn_accept_sampled")
 
@@ -529,15 +554,19 @@ def _ptrs(*args):
     """Device pointers of contiguous CUDA tensors, each (tensor, name, elements,
     dtype).  What they are is asked for in one pass, because small calls wait
     for the host; the checks that name what is wrong run when something is."""
+    here = _here()
     try:
-        p = [t.data_ptr() for t, _, n, dtype in args if t.numel() == n and t.dtype is dtype and t.is_cuda and t.is_contiguous()]
+        p = [t.data_ptr() for t, _, n, dtype in args if t.numel() == n and t.dtype is dtype and t.get_device() == here and t.is_contiguous()]
         if len(p) == len(args):
             return p
     except AttributeError:
         pass
     for t, what, n, _ in args:
         _count(t, what, n)
-    return [_ptr(t, what, dtype) for t, what, _, dtype in args]
+    p = [_ptr(t, what, dtype) for t, what, _, dtype in args]
+    for t, what, _, _ in args:
+        _elsewhere(t, what)
+    return p
 
 
 def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, free_count, q_start, q_count, kv_len,
@@ -630,11 +659,14 @@ def gdn_kv_copy_pages(kd: gdn_kv4_dims, caches, src, dst, count=None, stream=Non
     sp, dp = _ptrs((src, "src", n, i32), (dst, "dst", n, i32))
     u8, need = _t().uint8, _cache_bytes(kd)
     try:  # one pass, as in _ptrs
-        p = [t.data_ptr() for t in caches if t.dtype is u8 and t.is_cuda and t.is_contiguous() and t.numel() >= need]
+        here = _here()
+        p = [t.data_ptr() for t in caches if t.dtype is u8 and t.get_device() == here and t.is_contiguous() and t.numel() >= need]
     except AttributeError:
         p = ()
     if len(p) != len(caches):
         p = [_cache(kd, t) for t in caches]
+        for i, t in enumerate(caches):
+            _elsewhere(t, f"caches[{i}]")
     rc = load().gdn_kv_copy_pages(ctypes.byref(kd), len(p), (_P * max(len(p), 1))(*p), n, sp, dp,
                                   None if count is None else _ptrs((count, "count", 1, i32))[0], _stream(stream))
     _check(rc, "gdn_kv_copy_pages")

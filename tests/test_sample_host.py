@@ -68,6 +68,35 @@ def test_binding_refuses():
         L.gdn_accept_sampled(7, i, i, f, i, i, i, f, i)
 
 
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    """A fake tensor of device 1 where device 0 is the current one, in the place of each argument."""
+    torch = pytest.importorskip("torch")
+
+    class Fake:
+        def __init__(self, shape, dtype, device):
+            self.shape, self.dtype, self.at, self.device, self.is_cuda = shape, dtype, device, f"cuda:{device}", True
+
+        numel = lambda self: math.prod(self.shape)
+        element_size = lambda self: 4
+        get_device = lambda self: self.at
+        is_contiguous = lambda self: True
+        data_ptr = lambda self: G
+        stride = lambda self: tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    monkeypatch.setattr(L, "_here", lambda: 0)
+    monkeypatch.setattr(L, "_need", lambda **a: None)
+    monkeypatch.setattr(L, "_ptr", lambda t, what, dtype=None: G)
+    B, T, V = 3, 2, 50
+    i32, f32 = torch.int32, torch.float32
+    sizes = dict(u=((B, T), f32), keep=((B,), i32), nxt=((B,), i32), token=((B, T), i32), logp=((B, T), f32), ws=((4096,), torch.uint8),
+                 temperature=((B,), f32), top_k=((B,), i32), top_p=((B,), f32), min_p=((B,), f32), logits=((B, T, V), torch.bfloat16),
+                 draft=((B, T), i32), active=((B,), torch.uint8))
+    for bad in sizes:
+        args = {k: Fake(shape, dtype, int(k == bad)) for k, (shape, dtype) in sizes.items()}
+        with pytest.raises(ValueError, match="cuda:1"):
+            L.gdn_accept_sampled(**args)
+
+
 def test_reference_in_small():
     x = np.log(np.array([0.1, 0.4, 0.1, 0.3, 0.1]))
     assert [R.draw(x, u)[0] for u in (0.0, 0.39, 0.41, 0.69, 0.71, 0.79, 0.81, 0.95)] == [1, 1, 3, 3, 0, 0, 2, 4]
