@@ -56,7 +56,9 @@ constexpr int kGroups = kBins / 32;           // of 32 bins, a warp's
 constexpr int kFewLanes = 12;                 // of a warp that have something to count: one by one
 constexpr int kNear = 512;                    // places of the list of values near zero
 constexpr int kWindow = 1024;                 // values of a window
-static_assert(kWindow + kNear / 2 <= kMagnitudes - 32, "they lie in the gap of the counts");
+constexpr int kListed = 480;                  // logits of the list of what passed
+static_assert(kListed <= kThreads, "a thread each");
+static_assert(kWindow + kNear / 2 + kListed + kListed / 2 <= kMagnitudes - 32, "they lie in the gap of the counts");
 
 struct Found {
   int place;       // the value
@@ -83,6 +85,9 @@ struct Shared {
   u64 mass[kBins];          // masses likewise
   __device__ __forceinline__ uint32_t *window() { return hist + kMagnitudes; }  // in the gap
   __device__ __forceinline__ uint16_t *near() { return reinterpret_cast<uint16_t *>(hist + kMagnitudes + kWindow); }
+  // what passed the bound and has a bin: index and place, if no warp took all of its logits
+  __device__ __forceinline__ uint32_t *index() { return hist + kMagnitudes + kWindow + kNear / 2; }
+  __device__ __forceinline__ uint16_t *place() { return reinterpret_cast<uint16_t *>(index() + kListed); }
 
   u64 table[32];
   u64 group_mass[kGroups];
@@ -91,7 +96,8 @@ struct Shared {
   uint32_t near_count, warp_count[32];  // near_count: of the cluster, first CTA
   float warp_top[32], warp_low[32], warp_bound[32];
   Told told[8];             // by rank
-  uint32_t near_n;          // of this CTA's list
+  uint32_t near_n, listed;  // of this CTA's lists
+  int unlisted;             // some passed that are not listed
   int beyond, next, at, dust;
   uint32_t matches;
   u64 before_mass;
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     };
     clear();
     if (tid < 32) s.table[tid] = kExp2Table[tid];
-    if (tid == 0) s.near_n = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0, s.dust = 0;
+    if (tid == 0) s.near_n = 0, s.listed = 0, s.unlisted = 0, s.near_count = 0, s.near_mass = 0, s.beyond = 0, s.dust = 0;
     if (!(temperature > 0.f)) temperature = 0.f, min_p = 0.f, top_p = 1.f, top_k = 1;
     min_p = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
     if (top_k <= 0 || top_k > p.V) top_k = p.V;
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       base = max(0, min((binade + 1) << 7, 0x7f81) - kMagnitudes);  // infinity is the last that has one
       const uint32_t less_base = (-uint32_t(base) & 0xffffu) * 0x10001u;
       float largest = -INFINITY;
-      auto count = [&](const uint4 &q) {
+      auto count = [&](const uint4 &q, int g) {
         const float x = max_of(q);
         largest = fmaxf(largest, x);
         // branches are the warp's, so that it stays together
@@ -431,14 +437,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           const uint32_t off = count_two(q.x, less_base, most, hist) | count_two(q.y, less_base, most, hist) |
                                count_two(q.z, less_base, most, hist) | count_two(q.w, less_base, most, hist);
           const bool some = off & kMagnitudes * 0x10001u;
+          if (lane == 0) s.unlisted = 1;
           if (!__any_sync(0xffffffffu, some)) return;
           odd = some ? reaching(q, bound2) : 0;
           counted = true;
         }
         for (; odd; odd &= odd - 1) {
-          const uint32_t bits = half_of(q, __ffs(odd) - 1), a = bits & 0x7fffu, off = a - uint32_t(base);
+          const int j = __ffs(odd) - 1;
+          const uint32_t bits = half_of(q, j), a = bits & 0x7fffu, off = a - uint32_t(base);
           if (off < uint32_t(kMagnitudes)) {
-            if (!counted) atomicAdd(&s.hist[bits > 0x8000u ? kMinusWords + off : kMagnitudes - 1 - off], 1u);
+            if (!counted) {
+              atomicAdd(&s.hist[bits > 0x8000u ? kMinusWords + off : kMagnitudes - 1 - off], 1u);
+              const uint32_t i = atomicAdd(&s.listed, 1u);
+              if (i < uint32_t(kListed)) s.index()[i] = uint32_t(row.first(g) + j), s.place()[i] = uint16_t(place_of(bits));
+            }
           } else if (a < uint32_t(base)) {
             const uint32_t i = atomicAdd(&s.near_n, 1u);
             if (i < uint32_t(kNear)) s.near()[i] = uint16_t(place_of(bits));
@@ -453,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const uint4 q0 = ahead[0], q1 = ahead[1];
         ahead[0] = ahead[2], ahead[1] = ahead[3];
         ahead[2] = load(g + 4 * kThreads), ahead[3] = load(g + 5 * kThreads);
-        count(q0);
-        count(q1);
+        count(q0, g);
+        count(q1, g + kThreads);
       }
       largest = warp_max(largest);
       if (lane == 0) s.warp_top[warp] = largest;
@@ -465,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       // once more, with the bins that hold the largest of all
       binade = beyond >> 7;
       clear();
-      if (tid == 0) s.near_n = 0, s.beyond = 0;
+      if (tid == 0) s.near_n = 0, s.listed = 0, s.unlisted = 0, s.beyond = 0;
       start();
       sync_cta();
     }
@@ -660,8 +672,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
           for (int i = 1; i < C; ++i)
             if (q == i - 1 && n > all) n -= all, q = i, all = has[i];
-          const int from = min(row.granules, q * each);
-          token = locate(row, from, min(row.granules, from + each), f.place, n, all, s);
+          Shared &sq = C > 1 ? *cluster.map_shared_rank(&s, q) : s;
+          const uint32_t listed = sq.listed;
+          if (!sq.unlisted && listed <= uint32_t(kListed)) {
+            if (tid < int(listed) && sq.place()[tid] == f.place) s.sum[atomicAdd(&s.matches, 1u)] = sq.index()[tid];
+            sync_cta();
+            token = pick(s.matches, n, s);
+          } else {
+            const int from = min(row.granules, q * each);
+            token = locate(row, from, min(row.granules, from + each), f.place, n, all, s);
+          }
         }
       }
     }
