@@ -47,18 +47,20 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kLoads = 4;                     // granules of a thread in flight
 constexpr int kMagnitudes = 2048;             // of each sign: 16 binades
 constexpr int kBins = 2 * kMagnitudes;        // in the order of the row
-// Where the counts stand: those of positive values, largest first, a gap as large, those of
-// negative ones, and behind each side 32 words, one a lane, for what has no bin.  So a
-// bin's word is its magnitude's number in 12 bits, the sign's bit xored with the rest.
-constexpr int kMinusWords = 2 * kMagnitudes, kWords = kMinusWords + kMagnitudes + 32;
-__device__ __forceinline__ int word_of(int bin) { return bin < kMagnitudes ? bin : bin + kMagnitudes; }
+// Where the counts stand: a positive value's at its magnitude's number, a negative one's 32 KB
+// behind, where its sign's bit points in 16 bits of address; behind each side 32 words, one
+// a lane, for what has no bin; other arrays between the two.
+constexpr int kSideWords = kMagnitudes + 32, kMinusWords = 8192, kWords = kMinusWords + kSideWords;
+__device__ __forceinline__ int word_of(int bin) { return bin < kMagnitudes ? kMagnitudes - 1 - bin : kMinusWords + bin - kMagnitudes; }
 constexpr int kGroups = kBins / 32;           // of 32 bins, a warp's
 constexpr int kFewLanes = 12;                 // of a warp that have something to count: one by one
 constexpr int kNear = 512;                    // places of the list of values near zero
 constexpr int kWindow = 1024;                 // values of a window
 constexpr int kListed = 480;                  // logits of the list of what passed
 static_assert(kListed <= kThreads, "a thread each");
-static_assert(kWindow + kNear / 2 + kListed + kListed / 2 <= kMagnitudes - 32, "they lie in the gap of the counts");
+static_assert(kSideWords + kBins + kWindow + kNear / 2 + kListed + kListed / 2 <= kMinusWords, "they lie between the counts");
+static_assert(kSideWords % 4 == 0, "in vectors");
+static_assert(4 * kSideWords <= 0x8000 && 4 * kMinusWords == 0x8000, "offsets fit 16 bits, the sign's bit apart");
 
 struct Found {
   int place;       // the value
@@ -81,12 +83,14 @@ struct Asked {
 
 struct Shared {
   alignas(16) uint32_t hist[kWords];
-  uint32_t sum[kBins];      // the cluster's counts, up to each bin of a group; then indices of one value; first CTA
-  u64 mass[kBins];          // masses likewise
-  __device__ __forceinline__ uint32_t *window() { return hist + kMagnitudes; }  // in the gap
-  __device__ __forceinline__ uint16_t *near() { return reinterpret_cast<uint16_t *>(hist + kMagnitudes + kWindow); }
+  u64 mass[kBins];  // the cluster's masses, up to each bin of a group; first CTA
+  // Between the counts of the two signs:
+  // the cluster's counts, up to each bin of a group; then indices of one value; first CTA
+  __device__ __forceinline__ uint32_t *sum() { return hist + kSideWords; }
+  __device__ __forceinline__ uint32_t *window() { return sum() + kBins; }
+  __device__ __forceinline__ uint16_t *near() { return reinterpret_cast<uint16_t *>(window() + kWindow); }
   // what passed the bound and has a bin: index and place, if no warp took all of its logits
-  __device__ __forceinline__ uint32_t *index() { return hist + kMagnitudes + kWindow + kNear / 2; }
+  __device__ __forceinline__ uint32_t *index() { return window() + kWindow + kNear / 2; }
   __device__ __forceinline__ uint16_t *place() { return reinterpret_cast<uint16_t *>(index() + kListed); }
 
   u64 table[32];
@@ -227,16 +231,16 @@ __device__ __noinline__ int locate_in_order(const SampleRow &row, int g0, int g1
   return 0;
 }
 
-// The n-th least of the first m of s.sum.
+// The n-th least of the first m of s.sum().
 __device__ __forceinline__ int pick(uint32_t m, uint32_t n, Shared &s) {
   const int tid = threadIdx.x;
-  if (tid < 4 && m + tid < uint32_t(kBins)) s.sum[m + tid] = 0xffffffffu;
+  if (tid < 4 && m + tid < uint32_t(kBins)) s.sum()[m + tid] = 0xffffffffu;
   sync_cta();
   for (uint32_t i = tid; i < m; i += kThreads) {
-    const uint32_t x = s.sum[i];
+    const uint32_t x = s.sum()[i];
     uint32_t below = 0;
     for (uint32_t j = 0; j < m; j += 4) {
-      const uint4 y = *reinterpret_cast<const uint4 *>(s.sum + j);
+      const uint4 y = *reinterpret_cast<const uint4 *>(s.sum() + j);
       below += (y.x < x) + (y.y < x) + (y.z < x) + (y.w < x);
     }
     if (below + 1 == n) s.at = int(x);
@@ -281,7 +285,7 @@ __device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t 
         bits = (bits | bits >> 15) & 0xffu;  // logit j at bit j
         uint32_t k = atomicAdd(&s.matches, uint32_t(__popc(bits)));
         const int at = row.first(g + r * kThreads);
-        for (; bits && k < uint32_t(kBins); ++k, bits &= bits - 1) s.sum[k] = uint32_t(at + __ffs(bits) - 1);
+        for (; bits && k < uint32_t(kBins); ++k, bits &= bits - 1) s.sum()[k] = uint32_t(at + __ffs(bits) - 1);
       }
     }
     sync_cta();
@@ -293,8 +297,11 @@ __device__ int locate(const SampleRow &row, int g0, int g1, int place, uint32_t 
 }
 
 __device__ __forceinline__ __nv_bfloat162 b2(const uint32_t &w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
+__device__ __forceinline__ __nv_bfloat162 max2_of(const uint4 &q) {
+  return __hmax2(__hmax2(b2(q.x), b2(q.y)), __hmax2(b2(q.z), b2(q.w)));
+}
 __device__ __forceinline__ float max_of(const uint4 &q) {
-  const __nv_bfloat162 m = __hmax2(__hmax2(b2(q.x), b2(q.y)), __hmax2(b2(q.z), b2(q.w)));
+  const __nv_bfloat162 m = max2_of(q);
   return fmaxf(__low2float(m), __high2float(m));
 }
 __device__ __forceinline__ float min_of(const uint4 &q) {
@@ -317,12 +324,11 @@ constexpr uint32_t kNoNumbers = 0x7fff7fffu;
 
 // One more in the bins of two logits, 16 bits each, where their magnitudes have one;
 // returns their magnitudes' numbers, from kMagnitudes on where they have none.
-// less_base: -base twice; most: the lane's word for what has no bin, twice.
+// less_base: -base twice; most: the lane's word for what has no bin, twice.  The offsets fit 16
+// bits; the counts' address does not (in a cluster it holds the CTA's rank) and is added in 32.
 __device__ __forceinline__ uint32_t count_two(uint32_t w, uint32_t less_base, uint32_t most, uint32_t hist) {
   const uint32_t off = __viaddmin_u16x2(w & 0x7fff7fffu, less_base, most);
-  uint32_t minus;  // each sign 16 times
-  asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(minus) : "r"(w));
-  const uint32_t at = off << 2 ^ ((minus & 4 * kMinusWords * 0x10001u) | (~minus & 4 * (kMagnitudes - 1) * 0x10001u));
+  const uint32_t at = off << 2 | (w & 0x80008000u);
   asm volatile("red.shared.add.u32 [%0], 1;\n red.shared.add.u32 [%1], 1;" ::"r"(hist + (at & 0xffffu)), "r"(hist + (at >> 16)) : "memory");
   return off;
 }
@@ -371,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
     auto clear = [&] {  // as many rounds for every thread
 #pragma unroll
-      for (int i = 4 * tid; i - 4 * tid < kWords; i += 4 * kThreads)
-        if (i < kWords) *reinterpret_cast<uint4 *>(s.hist + i) = make_uint4(0, 0, 0, 0);
+      for (int i = 4 * tid; i - 4 * tid < 2 * kSideWords; i += 4 * kThreads)
+        if (i < 2 * kSideWords) *reinterpret_cast<uint4 *>(s.hist + (i < kSideWords ? i : i - kSideWords + kMinusWords)) = make_uint4(0, 0, 0, 0);
     };
     clear();
     if (tid < 32) s.table[tid] = kExp2Table[tid];
@@ -422,12 +428,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     for (;;) {
       base = max(0, min((binade + 1) << 7, 0x7f81) - kMagnitudes);  // infinity is the last that has one
       const uint32_t less_base = (-uint32_t(base) & 0xffffu) * 0x10001u;
-      float largest = -INFINITY;
+      __nv_bfloat162 largest2 = __float2bfloat162_rn(-INFINITY);
       auto count = [&](const uint4 &q, int g) {
-        const float x = max_of(q);
-        largest = fmaxf(largest, x);
+        const __nv_bfloat162 x = max2_of(q);
+        largest2 = __hmax2(largest2, x);
         // branches are the warp's, so that it stays together
-        const uint32_t who = __ballot_sync(0xffffffffu, x >= bound);
+        const uint32_t who = __ballot_sync(0xffffffffu, __hge2_mask(x, bound2) != 0);
         if (!who) return;
         uint32_t odd;  // logits to look at one by one, as bits
         bool counted = false;
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           const uint32_t bits = half_of(q, j), a = bits & 0x7fffu, off = a - uint32_t(base);
           if (off < uint32_t(kMagnitudes)) {
             if (!counted) {
-              atomicAdd(&s.hist[bits > 0x8000u ? kMinusWords + off : kMagnitudes - 1 - off], 1u);
+              atomicAdd(&s.hist[bits > 0x8000u ? kMinusWords + off : off], 1u);
               const uint32_t i = atomicAdd(&s.listed, 1u);
               if (i < uint32_t(kListed)) s.index()[i] = uint32_t(row.first(g) + j), s.place()[i] = uint16_t(place_of(bits));
             }
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         count(q0, g);
         count(q1, g + kThreads);
       }
-      largest = warp_max(largest);
+      const float largest = warp_max(fmaxf(__low2float(largest2), __high2float(largest2)));
       if (lane == 0) s.warp_top[warp] = largest;
       sync_cta();
       const int beyond = s.beyond;
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       for (int w = 1; w < kWarps; ++w) t.top = fmaxf(t.top, s.warp_top[w]);
       (C > 1 ? cluster.map_shared_rank(s.told, tid) : s.told)[rank] = t;
     }
-    if (tid == 32 && base == 0) s.hist[kMagnitudes - 1] += s.hist[kMinusWords], s.hist[kMinusWords] = 0;  // -0 is 0
+    if (tid == 32 && base == 0) s.hist[0] += s.hist[kMinusWords], s.hist[kMinusWords] = 0;  // -0 is 0
     together();
     const int own_base = base;
     const float own_bound = bound;
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
               if (!w || w < least) count = 0;
               mass = count * w;
               sum_up_to(count, mass);
-              s0.sum[bin] = count, s0.mass[bin] = mass;
+              s0.sum()[bin] = count, s0.mass[bin] = mass;
             }
           }
           if (lane == 31) s0.group_count[group] = count, s0.group_mass[group] = mass;
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         for (int i = tid; i < 2 * min(base - own_base, kMagnitudes); i += kThreads) {
           const int off = i >> 1;
-          const uint32_t n = s.hist[i & 1 ? kMinusWords + off : kMagnitudes - 1 - off];
+          const uint32_t n = s.hist[i & 1 ? kMinusWords + off : off];
           if (n) add(i & 1 ? 0x8000 + own_base + off : kPlaceZero - own_base - off, n);
         }
         count = __reduce_add_sync(0xffffffffu, count), mass = warp_sum(mass);
@@ -630,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
               const int group = lead * kMine + __ffs(__ballot_sync(0xffffffffu, (by_count ? u64(c) : m) >= target)) - 1;
               const int bin = group * 32 + lane;
               // before the group: what is up to it less what it has
-              const uint32_t c0 = s.group_count[group] - s.sum[group * 32 + 31], c1 = c0 + s.sum[bin];
+              const uint32_t c0 = s.group_count[group] - s.sum()[group * 32 + 31], c1 = c0 + s.sum()[bin];
               const u64 m0 = s.group_mass[group] - s.mass[group * 32 + 31], m1 = m0 + s.mass[bin];
               const int at = __ffs(__ballot_sync(0xffffffffu, (by_count ? u64(c1) : m1) >= target)) - 1;
               const uint32_t to = __shfl_sync(0xffffffffu, c1, at), up = __shfl_sync(0xffffffffu, c1, at - 1), n = to - (at ? up : c0);
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           Shared &sq = C > 1 ? *cluster.map_shared_rank(&s, q) : s;
           const uint32_t listed = sq.listed;
           if (!sq.unlisted && listed <= uint32_t(kListed)) {
-            if (tid < int(listed) && sq.place()[tid] == f.place) s.sum[atomicAdd(&s.matches, 1u)] = sq.index()[tid];
+            if (tid < int(listed) && sq.place()[tid] == f.place) s.sum()[atomicAdd(&s.matches, 1u)] = sq.index()[tid];
             sync_cta();
             token = pick(s.matches, n, s);
           } else {
