@@ -651,7 +651,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             }
             if (step < 2) rest = f.mass + f.n * f.w;
           }
-          logp = -log1pf(float(rest - f.w) / float(f.w));
+          // A weight under 2^24 units is off by more than 2^-25 of itself: its logarithm from the logits.
+          if (f.w < (1u << 24)) {
+            const float x = value_at(f.place), d = x - top;
+            logp = (isinf(d) ? __fdiv_rn(.5f * x - .5f * top, .5f * temperature) : __fdiv_rn(d, temperature)) -
+                   logf(float(rest) / float(kWeightOne));
+          } else {
+            logp = -log1pf(float(rest - f.w) / float(f.w));
+          }
           if (lane == 0) s.asked.what = -1, s.found = f;
           sync_cta();
         } else {

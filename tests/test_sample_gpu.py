@@ -272,6 +272,27 @@ def test_counts_begin_again(gdn, name, rows, v):
     check(bits_of(x), rng.random(rows), **kw)
 
 
+@pytest.mark.parametrize("temperature,below", [(1.0, 20.0), (1.0, 24.0), (0.25, 5.5), (8.0, 184.0)])
+@pytest.mark.parametrize("v", [3001, 60003])
+def test_logp_of_a_rare_token(gdn, v, temperature, below):
+    """A token whose weight is a few units of the masses: logp is as near as any other's.  From the logits
+    it is (x - max) / temperature - log(mass): two roundings of the first (2^-23 of it), log's of the second
+    (2^-23 of it; it is half of |logp| at most), one of the mass (2^-24; the units are 2^-24 of it too)
+    and the last one (2^-24 |logp|): below 2^-22 (1 + |logp|)."""
+    x = np.full((2, v), 8.0 - below, np.float64)
+    x[0, 5], x[1, v - 2] = 8.0, 8.0
+    bits = bits_of(x)
+    u = np.array([1 - 2.0 ** -23, 1 - 2.0 ** -23], np.float32)
+    if not v * math.exp(-below / temperature) > 2.0 ** -22:
+        u[:] = 1.0  # the last one
+    token, logp = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, device="cuda")
+    L.gdn_sample(logits_on(bits), torch.from_numpy(u).cuda(), token, logp, temperature=torch.full((2,), temperature, device="cuda"))
+    for i in range(2):
+        assert R.values(bits[i])[int(token[i])] < 8.0
+        lp = -below / temperature - math.log1p((v - 1) * math.exp(-below / temperature))
+        assert abs(float(logp[i]) - lp) <= 2 ** -22 * (1 + abs(lp)), (i, float(logp[i]), lp)
+
+
 def run_accept(logits, draft, active, u, ws=None, outputs=True, **kw):
     B, T, V = logits.shape
     z = lambda *s, dtype=torch.int32: torch.full(s, -9, dtype=dtype, device="cuda")
