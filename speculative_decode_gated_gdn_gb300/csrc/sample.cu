@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
               const bool dust = s.dust && uint32_t(top_k) > total_count;
               target = dust ? share_of(fmaxf(top_p, 0.f), rest, false) + 1 : max(u64(1), share_of(fmaxf(top_p, 0.f), rest, true));
             } else {  // to pass a share is to reach one more
-              target = u > 0.f ? (u < 1.f ? share_of(u, rest, false) + 1 : rest) : 1;
+              target = u > 0.f ? share_of(fminf(u, 0x1.fffffep-1f), rest, false) + 1 : 1;
             }
             const bool by_count = step == 0;
             const uint32_t lead = __ffs(__ballot_sync(0xffffffffu, (by_count ? u64(counts) : masses) >= target)) - 1;

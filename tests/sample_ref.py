@@ -41,7 +41,7 @@ def draw(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         w = w[:n]
     run = np.cumsum(w)
     u = np.float64(np.float32(u))
-    at = min(max(u, 0.0) if u == u else 0.0, 1.0) * run[-1]
+    at = min(max(u, 0.0) if u == u else 0.0, 1 - 2.0 ** -24) * run[-1]  # the nearest fp32 in [0, 1)
     j = min(int((run <= at).sum()), int(np.flatnonzero(w > 0)[-1]))
     border = float(np.min(np.abs(run - at))) / run[-1]
     return int(order[j]), -math.log1p((run[-1] - w[j]) / w[j]), border

@@ -227,6 +227,17 @@ def test_parameters_out_of_their_range(gdn):
     check(bits[:6], np.array([-1, 1, 2, NAN, INF, -INF], np.float32), top_p=0.9)
 
 
+def test_u_of_one_and_more_is_the_nearest_below(gdn):
+    """The largest fp32 below 1 leaves 2^-24 of the mass behind it: a token of 2^-36 is not drawn, one of 2^-20 is."""
+    for below, want in ((25.0, 7), (14.0, 40)):
+        x = np.full((4, 100), -INF)
+        x[:, 7], x[:, 40] = 8.0, 8.0 - below
+        check(bits_of(x), np.array([1, 2, INF, 1 - 2.0 ** -24], np.float32))
+        token, logp = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, device="cuda")
+        L.gdn_sample(logits_on(bits_of(x)), torch.tensor([1, 2, INF, 1 - 2.0 ** -24], device="cuda"), token, logp)
+        assert token.tolist() == [want] * 4
+
+
 @pytest.mark.parametrize("name", ["tiny", "huge", "wide", "mixed magnitudes", "far", "near the largest number", "late maximum"])
 def test_values_far_from_usual(gdn, name):
     """Logits whose magnitudes are far apart: the values between take more than one look."""
