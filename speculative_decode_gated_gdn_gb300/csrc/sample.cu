@@ -12,23 +12,24 @@
 //      below the slice's largest, of either sign, in the order of the row.  Where a
 //      warp's 256 logits have few above the bound, these one by one, else all of them,
 //      two in a 32-bit register: what is below the bound is behind all that matters, so
-//      it does no harm.  What lies between the two signs' magnitudes, near zero, is
-//      rare and goes to a list.
+//      it does no harm.  What was taken one by one is also listed, with its index.  What
+//      lies between the two signs' magnitudes, near zero, is rare and goes to a list.
 //   3. The CTAs add up their counts, each a part of the values, and form counts and
 //      masses up to each value of a group of 32 for the first CTA, whose first warp
 //      asks them where the first k end, where p of the mass ends, and where u falls.
-//   4. It finds that value's logit in the slice that has it, from the nearer end.
+//   4. It finds that value's logit in the slice that has it: among the listed ones, or,
+//      where the list does not hold all, in the slice, from the nearer end.
 // A logit above all of the 16 binades makes a CTA's counting begin again with others; an
 // answer near zero is looked for in windows of 1024 values over the row.
 //
-// What bounds it.  Few rows: latency, 8 us for one row of 32000: 2 to the first logits,
+// What bounds it.  Few rows: latency, 7.7 us for one row of 32000: 2 to the first logits,
 // 1 to 2 for the counts, 0.7 for each of three cluster barriers, 2 for the questions (a
-// share of the mass, three ballots, a weight and a quotient each), 1 for the search.
-// Many unfiltered rows: the shared-memory atomics, one a logit: 32 random bins take 3.5
-// cycles of the banks, 15 us of 45.6 for 256 rows of 151936 (77.8 MB, 11.6 us of HBM), and
-// instructions: 29 million, 0.6 an issue slot on the SMs with two rows; about a third
-// of them weights (128 groups a row), a tenth the search.  256 rows leave 48 SMs with
-// one row and 104 with two.  480 rows of 151936 with top-p: 88 us.
+// share of the mass, three ballots, a weight and a quotient each), 0.5 for the logit.
+// Many unfiltered rows: the counts, 30 us of 45.8 for 256 rows of 151936 (77.8 MB, 11.6 us
+// of HBM).  Of these the atomics, one a logit, take 15: 32 random bins cost 3.4 cycles of
+// the banks.  The rest is instructions: 29 million in all, 0.6 an issue slot, 0.8 on the
+// SMs with two rows.  Then the groups' weights, 7, and the search, 5.  256 rows
+// leave 48 SMs with one row and 104 with two.  480 rows of 151936 with top-p: 89 us.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -358,17 +359,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const SampleRow row(p.logits + size_t(bt) * p.stride, p.V);
   const int each = (row.granules + C - 1) / C;
   const int g0 = min(row.granules, rank * each), g1 = min(row.granules, g0 + each);
-      auto load = [&](int g) { return g < g1 ? row.load(g) : make_uint4(kNoNumbers, kNoNumbers, kNoNumbers, kNoNumbers); };
-      uint4 ahead[kLoads];  // this thread's next granules, kThreads apart
-      auto start = [&] {
-  #pragma unroll
-        for (int r = 0; r < kLoads; ++r) ahead[r] = load(g0 + tid + r * kThreads);
-      };
-      start();
-      float temperature = p.temperature ? p.temperature[b] : 1.f;
-      float min_p = p.min_p ? p.min_p[b] : 0.f, top_p = p.top_p ? p.top_p[b] : 1.f;
-      int top_k = p.top_k ? p.top_k[b] : 0;
-      const float u = p.u[bt];
+  auto load = [&](int g) { return g < g1 ? row.load(g) : make_uint4(kNoNumbers, kNoNumbers, kNoNumbers, kNoNumbers); };
+  uint4 ahead[kLoads];  // this thread's next granules, kThreads apart
+  auto start = [&] {
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r) ahead[r] = load(g0 + tid + r * kThreads);
+  };
+  start();
+  float temperature = p.temperature ? p.temperature[b] : 1.f;
+  float min_p = p.min_p ? p.min_p[b] : 0.f, top_p = p.top_p ? p.top_p[b] : 1.f;
+  int top_k = p.top_k ? p.top_k[b] : 0;
+  const float u = p.u[bt];
   const bool active = !p.active || p.active[b];  // the cluster agrees
   int token = -1;
   float logp = 0.f;
@@ -751,11 +752,11 @@ size_t accept_sampled_workspace_bytes(int B, int T) {
 
 // CTAs of a position: as many as the GPU holds at once (two an SM) for all of them, where
 // each has 4096 logits at least.  Both sides, us of GPU time with 1, 2, 4, 8 CTAs:
-//   1 row of 32000, top-k 40, top-p, min-p        8.6   8.9   7.7   8.0
-//   16 of 151936, top-k 20, top-p                31.0  20.2  15.4  14.0
-//   64 of 151936, mixed                          32.6  24.5  20.7  28.8
-//   256 of 151936, unfiltered                    49.0  56.5  75.2   117
-//   480 of 151936, top-p                         90.8   104   140   232
+//   1 row of 32000, top-k 40, top-p, min-p        7.8   8.3   7.6   7.8
+//   16 of 151936, top-k 20, top-p                30.1  21.6  14.6  13.9
+//   64 of 151936, mixed                          34.0  25.1  21.4  29.0
+//   256 of 151936, unfiltered                    45.8  57.5  79.1   123
+//   480 of 151936, top-p                         89.1   107   147   241
 cudaError_t launch_sample(const SampleParams &p, cudaStream_t s) {
   static std::atomic<int> cached[64];  // SMs by device, 0 until looked up
   int dev = 0;
