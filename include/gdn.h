@@ -503,8 +503,8 @@ int gdn_sample(int B, int V, const gdn_bf16 *logits, long long stride, const uin
  * drafts were made, if u is fresh: a draft is kept when the draw equals it.
  * Inactive rows get keep 0 and next -1.
  *  ws  gdn_accept_sampled_workspace_bytes, 256-byte aligned, zero-filled once before
- *      its first use (each call leaves it ready for the next); one call at a time
- *      may use it
+ *      its first use (each call leaves it ready for the next, also of other sizes); one
+ *      call at a time may use it
  */
 int gdn_accept_sampled(int B, int T, int V, const gdn_bf16 *logits, long long stride, const int32_t *draft,
                        const uint8_t *active, const float *temperature, const int32_t *top_k, const float *top_p,

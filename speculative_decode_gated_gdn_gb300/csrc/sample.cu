@@ -722,7 +722,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       }
       p.keep[b] = k;
       p.next[b] = k ? __ldcg(p.ws_token + size_t(b) * p.T + k - 1) : -1;
-      p.ws_count[b] = 0;  // ready for the next call
+      // ready for the next call, also one of other sizes, whose counts lie elsewhere
+      p.ws_count[b] = 0;
+      for (int t = 0; t < p.T; ++t) p.ws_token[size_t(b) * p.T + t] = 0;
     }
   }
 }

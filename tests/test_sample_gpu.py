@@ -346,6 +346,26 @@ def test_accept(gdn, shape):
     assert torch.equal(one.view(B, T), token)
 
 
+def test_one_workspace_for_calls_of_other_sizes(gdn):
+    """Zeroed once, then used with other B and T, as a host that varies its drafts' depth does; all zero after each call."""
+    rng = np.random.default_rng(12)
+    ws = torch.zeros(max(L.gdn_accept_sampled_workspace_bytes(B, T, 1003) for B, T in ((200, 8), (700, 1), (3, 64))), dtype=torch.uint8, device="cuda")
+    for B, T in ((4, 2), (200, 8), (4, 2), (3, 64), (700, 1), (70, 2), (200, 8), (4, 3)):
+        x = torch.from_numpy(bell(rng, B * T, 1003)).bfloat16().cuda().view(B, T, 1003)
+        draft = torch.full((B, T), -1, dtype=torch.int32, device="cuda")
+        active = torch.from_numpy((rng.random(B) < 0.8).astype(np.uint8)).cuda()
+        u = torch.rand(B, T, device="cuda")
+        first = torch.zeros(B * T, dtype=torch.int32, device="cuda")
+        L.gdn_sample(x.view(B * T, 1003), u.view(-1), first)
+        draft[:, 1:] = first.view(B, T)[:, :-1]  # all of them kept
+        keep, nxt = (torch.full((B,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+        L.gdn_accept_sampled(x, draft, active, u, keep, nxt, None, None, ws)
+        on = active.bool()
+        assert torch.equal(keep, torch.where(on, T, 0).int()), (B, T)
+        assert torch.equal(nxt, torch.where(on, first.view(B, T)[:, -1], -1)), (B, T)
+        assert not ws.any(), (B, T)
+
+
 def test_accept_at_temperature_0_is_the_greedy_one(gdn):
     B, T, V = 6, 4, 5003
     rng = np.random.default_rng(9)
