@@ -99,7 +99,9 @@ struct Shared {
   uint32_t group_count[kGroups];
   u64 near_mass, warp_mass[32];
   uint32_t near_count, warp_count[32];  // near_count: of the cluster, first CTA
-  float warp_top[32], warp_low[32], warp_bound[32];
+  // Written once each: of the first granules, behind the bound's barrier; of the whole slice, read behind
+  // the counts' barrier, while others may still be at the bound's.
+  float warp_top[32], warp_low[32], warp_bound[32], warp_largest[32];
   Told told[8];             // by rank
   uint32_t near_n, listed;  // of this CTA's lists
   int unlisted;             // some passed that are not listed
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         count(q1, g + kThreads);
       }
       const float largest = warp_max(fmaxf(__low2float(largest2), __high2float(largest2)));
-      if (lane == 0) s.warp_top[warp] = largest;
+      if (lane == 0) s.warp_largest[warp] = largest;
       sync_cta();
       const int beyond = s.beyond;
       __syncwarp();
@@ -491,9 +493,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     __syncwarp();
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all of them run
     if (tid < C) {
-      Told t{s.warp_top[0], bound, base};
+      Told t{s.warp_largest[0], bound, base};
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) t.top = fmaxf(t.top, s.warp_top[w]);
+      for (int w = 1; w < kWarps; ++w) t.top = fmaxf(t.top, s.warp_largest[w]);
       (C > 1 ? cluster.map_shared_rank(s.told, tid) : s.told)[rank] = t;
     }
     if (tid == 32 && base == 0) s.hist[0] += s.hist[kMinusWords], s.hist[kMinusWords] = 0;  // -0 is 0
