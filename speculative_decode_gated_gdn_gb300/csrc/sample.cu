@@ -423,13 +423,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     uint32_t magnitude = (__float_as_uint(fmaxf(fabsf(top), fabsf(fmaxf(low, bound)))) >> 16);
     if (!(top > -INFINITY)) magnitude = 0;
     int binade = int(magnitude >> 7) + (each > kThreads * kLoads);
+    // -infinity has no bin, so no weight either: only where +infinity is there, beside which nothing
+    // has any, do the bins go up to the magnitude of infinity
+    if (top < INFINITY) binade = min(binade, 254);
 
     // ---- counts by value ------------------------------------------------------------------
     int base;
     const __nv_bfloat162 bound2 = __float2bfloat162_rn(bound);
     const uint32_t hist = smem_u32(s.hist), most = (kMagnitudes + lane) * 0x10001u;
     for (;;) {
-      base = max(0, min((binade + 1) << 7, 0x7f81) - kMagnitudes);  // infinity is the last that has one
+      base = max(0, min((binade + 1) << 7, 0x7f81) - kMagnitudes);  // +infinity is the last that has one
       const uint32_t less_base = (-uint32_t(base) & 0xffffu) * 0x10001u;
       __nv_bfloat162 largest2 = __float2bfloat162_rn(-INFINITY);
       auto count = [&](const uint4 &q, int g) {

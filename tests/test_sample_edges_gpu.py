@@ -29,3 +29,42 @@ def test_largest_logit_behind_the_first_granules(gdn, rows, v):
     for o in outs:
         L.gdn_sample(logits, uu, *o, **ways)
     assert all(torch.equal(a, b) for o in outs for a, b in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("rows,v", [(1, 151936), (3, 60003), (160, 40001), (300, 16500), (6, 3001)])
+@pytest.mark.parametrize("temperature", [INF, 1e38, 3e4])
+@pytest.mark.parametrize("mask", [0.5, 0.99])
+def test_forbidden_tokens_are_never_drawn(gdn, rows, v, temperature, mask):
+    """Half of the tokens or nearly all forbidden, at temperatures at which all others weigh the same, in slices longer than
+    their first granules and shorter ones: -infinity has no weight, and decides no border either."""
+    rng = np.random.default_rng(v)
+    n = min(rows, 6)
+    x = rng.standard_normal((n, v)) * 2
+    x[rng.random((n, v)) < mask] = -INF
+    bits = bits_of(x)
+    allowed = np.isfinite(x)
+    for kw in (dict(), dict(top_p=0.5), dict(top_k=7), dict(min_p=0.5)):
+        u = np.linspace(0.03, 0.999, n)
+        check(bits, u, temperature=temperature, **kw)
+    # all rows of the launch, every place of u
+    logits = logits_on(np.tile(bits, (-(-rows // n), 1))[:rows])
+    token, logp = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.zeros(rows, device="cuda")
+    for u in np.linspace(0, 1, 9):
+        L.gdn_sample(logits, torch.full((rows,), float(u), device="cuda"), token, logp, temperature=torch.full((rows,), temperature, device="cuda"))
+        t, lp = token.cpu().numpy(), logp.double().cpu().numpy()
+        for i in range(rows):
+            assert allowed[i % n, t[i]]
+            if temperature == INF:
+                assert abs(lp[i] + math.log(allowed[i % n].sum())) <= 2 ** -22 * (1 + math.log(v))
+
+
+def test_forbidden_tokens_do_not_decide_an_exact_border(gdn):
+    """Two equal maxima, top_p a half, the rest forbidden: one of them is half of the mass, so it is kept alone, whatever the
+    temperature; slices whose bins reach the largest magnitudes."""
+    x = np.full((6, 151936), -INF)
+    x[:, [9, 33000]] = 3.0
+    x[3:] = -INF
+    x[3:, [9, 33000]] = -2e38
+    for temperature in (INF, 1e38, 1.0):
+        got = check(bits_of(x), np.linspace(0.05, 0.95, 6), temperature=temperature, top_p=0.5)
+        assert set(got.tolist()) == {9}
