@@ -473,8 +473,8 @@ int gdn_accept_greedy(int B, int T, int V, const gdn_bf16 *logits, const int32_t
  * above -infinity gives what gdn_accept_greedy takes, with logp -infinity.
  * Infinite logits share the mass among themselves.
  * Precision: weights to 2^-37 of themselves and 2^-43 of the largest (down to 2^-53 of it
- * what is smaller still decides where the rest meets top_p exactly), their sums exact in
- * integers; logp to 2^-22 (1 + |logp|); the same inputs give the same outputs on every run.
+ * what is smaller, and left by min_p, still decides where the rest meets top_p exactly), their
+ * sums exact in integers; logp to 2^-22 (1 + |logp|); the same inputs give the same outputs on every run.
  *  logits  position (b, t) at (b * T + t) * stride elements, bf16, stride >= V;
  *          any 2-byte aligned address
  *  active  [B] uint8, NULL: all.  Inactive rows get token -1 and logp 0

@@ -68,3 +68,26 @@ def test_forbidden_tokens_do_not_decide_an_exact_border(gdn):
     for temperature in (INF, 1e38, 1.0):
         got = check(bits_of(x), np.linspace(0.05, 0.95, 6), temperature=temperature, top_p=0.5)
         assert set(got.tolist()) == {9}
+
+
+@pytest.mark.parametrize("min_p,kept", [(1e-15, True), (7.0e-15, True), (1e-30, True), (7.3e-15, False), (1e-13, False), (0.1, False)])
+@pytest.mark.parametrize("tops,others,v", [(2, 3, 40), (4, 5, 5000), (2, 900, 20000), (2, 40, 151936)])
+def test_min_p_below_the_masses_units(gdn, tops, others, v, min_p, kept):
+    """Equal maxima, others of 2^-47 = 7.1e-15 of them, top_p a half: where min_p leaves the others, one maximum more than half of
+    them is kept."""
+    x = np.full((8, v), -INF)
+    x[:, 1:1 + tops] = 3.0
+    x[:, 20:20 + others] = -5.0
+    temperature = np.float32(8.0 / (47 * math.log(2)))
+    got = check(bits_of(x), np.linspace(0.05, 0.95, 8), temperature=temperature, top_p=0.5, min_p=min_p)
+    assert len(set(got.tolist())) == (tops // 2 + 1 if kept else tops // 2)
+    check(bits_of(x), np.linspace(0.05, 0.95, 8), temperature=temperature, top_p=0.5, min_p=min_p, top_k=tops)
+    check(bits_of(x), np.linspace(0.05, 0.95, 8), temperature=temperature, top_p=0.5, min_p=min_p, top_k=tops + 1)
+
+
+def test_far_below_the_units_is_nothing_at_any_scale(gdn):
+    """Two equal maxima near the largest number, another 2^-98 of them: nothing, so top_p of a half keeps one maximum."""
+    x = np.full((4, 5000), -INF)
+    x[:, [3, 9]], x[:, 40] = 3.3e38, -3.3e38
+    got = check(bits_of(x), np.linspace(0.05, 0.95, 4), temperature=1e37, top_p=0.5)
+    assert set(got.tolist()) == {3}
