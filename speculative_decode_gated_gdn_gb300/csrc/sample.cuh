@@ -99,7 +99,8 @@ __device__ __forceinline__ uint32_t few_in(unsigned long long a, unsigned long l
 
 // exp((value_at(place) - value_at(top)) / temperature) in units of 2^-43, rounded; top <= place.
 // The exponent t (base 2) is a sum of two floats, 2^-46 exact; 2^t = 2^n 2^(m/32) 2^r with the middle
-// factor from the table and the last, |r| <= 1/64, by its series: 2^-38 exact in all.
+// factor from the table and the last, |r| <= 1/64, by its series: 2^-38 of the weight in all, half
+// a unit aside.
 static __device__ __noinline__ unsigned long long weight_of(int place, int top, Scale c, const unsigned long long *table) {
   if (place == top) return kWeightOne;
   if (top == kPlaceInf) return 0;
@@ -116,9 +117,11 @@ static __device__ __noinline__ unsigned long long weight_of(int place, int top, 
   constexpr float kLn2 = 0.693147182464599609f, kLn2Lo = -1.9046542121259336e-9f;
   const float y = r * kLn2, y_lo = fmaf(r, kLn2, -y) + fmaf(r, kLn2Lo, t_lo * kLn2);
   const float hi = y + y_lo, lo = y_lo - (hi - y);
-  const float q = hi * hi * fmaf(hi, fmaf(hi, fmaf(hi, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f);
+  // 1 + hi + hi^2 / 2 + ..: the first two in a sum of two floats, the square with its remainder
+  const float sq = hi * hi, half = 0.5f * sq, first = hi + half;
+  const float rest = fmaf(0.5f, fmaf(hi, hi, -sq), fmaf(sq * hi, fmaf(hi, fmaf(hi, 1.f / 120, 1.f / 24), 1.f / 6), fmaf(lo, hi, lo) + (half - (first - hi))));
   const float unit = 1125899906842624.f;  // 2^50
-  const unsigned long long f = (1ull << 50) + (unsigned long long)(__float2ll_rn(hi * unit) + __float2ll_rn((fmaf(lo, hi, lo) + q) * unit));
+  const unsigned long long f = (1ull << 50) + (unsigned long long)(__float2ll_rn(first * unit) + __float2ll_rn(rest * unit));
   const unsigned long long w = __umul64hi(table[k & 31], f << 13);  // in units of 2^(n - 61)
   const int shift = 61 - kWeightBits - (k >> 5);
   if (shift > 62) return 0;
