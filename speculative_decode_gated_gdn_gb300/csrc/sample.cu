@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       logp = -INFINITY;
     } else {
       const int best = place_of(__float_as_uint(top) >> 16);
-      const Scale scale = temperature > 0.f ? scale_of(temperature) : Scale{0.f, 0.f};
+      const Scale scale = temperature > 0.f ? scale_of(temperature) : Scale{0.f, 0.f, 1.f};
       const u64 least = __float2ull_ru(min_p * float(kWeightOne));  // exact before it is rounded up
       auto place_at = [&](int bin) { return bin < kMagnitudes ? kPlaceZero - base - (kMagnitudes - 1 - bin) : 0x8000 + base + bin - kMagnitudes; };
       Shared &s0 = C > 1 ? *cluster.map_shared_rank(&s, 0) : s;

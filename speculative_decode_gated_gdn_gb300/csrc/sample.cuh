@@ -63,15 +63,19 @@ __device__ const unsigned long long kExp2Table[32] = {
 };
 
 struct Scale {
-  float hi, lo;  // 2 / (temperature * ln 2); 0: every weight is 1
+  float hi, lo;  // 2 / (temperature * unit * ln 2); 0: every weight is 1
+  float unit;    // a power of two that keeps the quotient and its remainder among the normal numbers
 };
 
 // The quotient's remainder is exact by fma, so hi + lo is within 2^-46 of it.
 __device__ __forceinline__ Scale scale_of(float temperature) {
   constexpr float k = 2.88539004f, k_lo = 3.851926067e-8f;  // 2 / ln 2
+  constexpr float large = 18446744073709551616.f;           // 2^64
   Scale s;
+  s.unit = temperature >= large ? 1.f / large : temperature < 1.f / large ? large : 1.f;
+  temperature *= s.unit;
   s.hi = __fdiv_rn(k, temperature);
-  s.lo = isinf(s.hi) ? 0.f : __fdiv_rn(fmaf(-s.hi, temperature, k) + k_lo, temperature);
+  s.lo = __fdiv_rn(fmaf(-s.hi, temperature, k) + k_lo, temperature);
   return s;
 }
 
@@ -106,8 +110,8 @@ static __device__ __noinline__ unsigned long long weight_of(int place, int top, 
   if (top == kPlaceInf) return 0;
   if (c.hi == 0.f) return kWeightOne;
   const float z = 0.5f * value_at(place), z0 = 0.5f * value_at(top);  // halves: their difference is finite
-  const float s = z - z0, back = s - z;
-  const float err = (z - (s - back)) + (-z0 - back);
+  const float d = z - z0, back = d - z;
+  const float s = d * c.unit, err = ((z - (d - back)) + (-z0 - back)) * c.unit;
   const float t = s * c.hi;
   if (!(t > -46.f)) return 0;
   const float t_lo = fmaf(s, c.hi, -t) + fmaf(s, c.lo, err * c.hi);

@@ -91,3 +91,13 @@ def test_far_below_the_units_is_nothing_at_any_scale(gdn):
     x[:, [3, 9]], x[:, 40] = 3.3e38, -3.3e38
     got = check(bits_of(x), np.linspace(0.05, 0.95, 4), temperature=1e37, top_p=0.5)
     assert set(got.tolist()) == {3}
+
+
+@pytest.mark.parametrize("temperature", [2e-42, 9e-41, 1.2e-39, 9e-39, 1.2e-38, 1e-20, 1e19, 2e19, 3e37, 3e38])
+def test_temperatures_of_any_size(gdn, temperature):
+    """Logits some temperatures apart, at temperatures below the normal numbers and near the largest."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((4, 9001)) * 3 * np.float64(np.float32(temperature))
+    bits = bits_of(np.clip(x, -3.3e38, 3.3e38))
+    for kw in (dict(), dict(top_p=0.8), dict(top_k=30), dict(min_p=0.1)):
+        check(bits, rng.random(4), temperature=temperature, **kw)

@@ -98,3 +98,19 @@ def test_weights_to_half_a_unit_and_their_38th_bit(tmp_path):
     low part, under 2^-18, two or three roundings to 2^-43; the series' terms from the cube on, under 2^-22, a few roundings to 2^-45, the
     first two with their remainders; what the series leaves out 2^-48: 2^-39.5 in all."""
     assert run_on_host(tmp_path) < -38
+
+
+@pytest.mark.skipif(not shutil.which("g++"), reason="needs g++")
+@pytest.mark.parametrize("lo,hi", [(-103, -87), (-90, -40), (40, 75), (70, 88.7)])
+def test_weights_at_every_temperature(tmp_path, lo, hi):
+    """The same for temperatures from the least positive number to the largest, with logits some temperatures apart."""
+    assert run_on_host(tmp_path, f"""
+  worst = 0;
+  int seen = 0;
+  for (int i = 0; i < 1000000; ++i) {{
+    const float t = float(exp({lo} + ({hi} - {lo}) * uniform()));
+    const double a = (uniform() - 0.5) * 60 * t, b = a - 25 * t * uniform();
+    const int p = place_near(float(std::max(-3.3e38, std::min(3.3e38, a)))), q = place_near(float(std::max(-3.3e38, b)));
+    if (t > 0 && p < q) look(q, p, t), ++seen;
+  }}
+  if (seen < 10000) return 1;""") < -38
