@@ -622,7 +622,10 @@ int gdn_kv_plan_shared(const gdn_kv4_dims *dims, int T, int N, const int32_t *le
  * destination holds pages already, also from an earlier pair of the call
  * (GDN_STATUS_BAD_ROW); one with a negative length, or longer than its source's pages
  * before the call (GDN_STATUS_BAD_LEN); one that needs a page when none is left, and
- * then every later one that needs one (GDN_STATUS_NO_PAGES).  n = 0 does nothing.
+ * then every later one that needs one (GDN_STATUS_NO_PAGES); one that needs a page and
+ * whose source's last page, or the stack's, is outside the cache (GDN_STATUS_BAD_INDEX;
+ * the stack's entry is dropped).  Full pages outside the cache are passed on as they
+ * are (GDN_STATUS_BAD_INDEX).  n = 0 does nothing.
  */
 int gdn_kv_fork(const gdn_kv4_dims *dims, int n, const int32_t *src_rows, const int32_t *dst_rows,
                 const int32_t *lens, int32_t *held, int32_t *table, int32_t *free_list, int32_t *free_count,

@@ -31,7 +31,7 @@ struct ForkPair {
   int src, dst, len, want;
   bool rows;  // two rows of the cohort
 };
-enum { kAsks, kNothing, kBadRow, kBadLen };
+enum { kAsks, kNothing, kBadRow, kBadLen, kBadPage };
 
 __device__ __forceinline__ ForkPair fork_pair(const KvForkParams &p, int i) {
   ForkPair r;
@@ -55,12 +55,13 @@ __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
       verdict = kBadLen;
     } else if (r.rows) {
       const int held = *(volatile int32_t *)(p.held + r.src), taken = *(volatile int32_t *)(p.held + r.dst);
+      const int whole = r.len >> p.log2P, last = r.want > whole ? p.table[size_t(r.src) * p.max_pages + whole] : 0;
       if (held < r.want || held > p.max_pages) {
         if (r.want > 0) verdict = kBadLen;
         else if (taken <= 0) verdict = kNothing;
       } else if (taken <= 0) {
-        verdict = r.len ? kAsks : kNothing;
-        if (r.len) atomicMin(p.held + r.dst, i - p.n);
+        verdict = !r.len ? kNothing : last < 0 || last >= p.n_pages ? kBadPage : kAsks;
+        if (verdict == kAsks) atomicMin(p.held + r.dst, i - p.n);
       }
     }
     p.copy_src[i] = verdict;
@@ -83,25 +84,26 @@ __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
     if (i < p.n) {
       int from = -2, to = -2;
       if (won) {
-        const bool fits = !need || end <= count0;
-        if (fits) {
-          from = to = -1;
-          if (need) {
-            int32_t *cells = p.table + size_t(r.dst) * p.max_pages;
-            from = p.table[size_t(r.src) * p.max_pages + whole];
-            to = p.free_list[count0 - end];
-            cells[whole] = to;
-            if (to >= 0 && to < p.n_pages) p.refs[to] = 1;
-            else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+        bool made = !need || end <= count0;
+        if (!made) atomicOr(p.status, GDN_STATUS_NO_PAGES);
+        if (made && need) {
+          const int page = p.free_list[count0 - end];
+          made = page >= 0 && page < p.n_pages;
+          if (made) {
+            from = p.table[size_t(r.src) * p.max_pages + whole], to = page;
+            p.table[size_t(r.dst) * p.max_pages + whole] = page;
+            p.refs[page] = 1;
+          } else {
+            atomicOr(p.status, GDN_STATUS_BAD_INDEX);
           }
-        } else {
-          atomicOr(p.status, GDN_STATUS_NO_PAGES);
+        } else if (made) {
+          from = to = -1;
         }
-        p.held[r.dst] = fits ? r.want : 0;
+        p.held[r.dst] = made ? r.want : 0;
       } else if (verdict == kNothing) {
         from = to = -1;
       } else {
-        atomicOr(p.status, verdict == kBadLen ? GDN_STATUS_BAD_LEN : GDN_STATUS_BAD_ROW);
+        atomicOr(p.status, verdict == kBadLen ? GDN_STATUS_BAD_LEN : verdict == kBadPage ? GDN_STATUS_BAD_INDEX : GDN_STATUS_BAD_ROW);
       }
       p.copy_src[i] = from, p.copy_dst[i] = to;
     }
