@@ -597,7 +597,8 @@ int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, con
  * A page taken gets one holder.  A page given back loses one, and goes onto the stack
  * when it has none left, at the place (in row order, each row's in column order) of
  * the last of its releases in the call.  A page outside the cache, or one that had no
- * holder, is dropped (GDN_STATUS_BAD_INDEX).  A row's length never falls below what it
+ * holder, is dropped (GDN_STATUS_BAD_INDEX).  A stack entry outside the cache gives
+ * its row a cell of -1, and the tokens there no slots (GDN_STATUS_BAD_INDEX).  A row's length never falls below what it
  * shares, except to 0: rows write behind their committed length, and what is shared
  * lies before it.  Supported: B * max_pages < 2^31.
  */

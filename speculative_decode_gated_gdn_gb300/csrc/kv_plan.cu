@@ -297,12 +297,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     for (int i = tid; i < int(got_total); i += kPlanThreads) {
       const int w = find_row(s_ends, rows, i);
       const long long from = avail - 1 - (taken0 + i);
-      const int page = SHARED ? __ldcg(p.free_list + from) : p.free_list[from];
-      p.table[size_t(b0 + w) * p.max_pages + s_from[w] + i - (w ? s_ends[w - 1] : 0)] = page;
+      int page = SHARED ? __ldcg(p.free_list + from) : p.free_list[from];
       if (SHARED) {
         if (page >= 0 && page < n_pages) p.refs[page] = 1;
-        else atomicOr(p.status, GDN_STATUS_BAD_INDEX);
+        else page = -1, atomicOr(p.status, GDN_STATUS_BAD_INDEX);
       }
+      p.table[size_t(b0 + w) * p.max_pages + s_from[w] + i - (w ? s_ends[w - 1] : 0)] = page;
     }
     taken0 += need_total;
     tokens0 += tok_total;

@@ -57,3 +57,21 @@ def test_fork_where_the_stack_holds_no_page(gdn):
             refs[p] = 3
         refs[g.table[0, 2].item()] = refs[want] = 1
         assert g.refs.tolist() == refs
+
+
+@pytest.mark.parametrize("M", [4, 2000])
+@pytest.mark.parametrize("bad", [-1, -7, 20, (1 << 27) + 3, 1 << 30])
+def test_plan_where_the_stack_holds_no_page(gdn, bad, M):
+    """A stack entry outside the cache: its place in the table gets -1, its tokens no slots; the row beside is served."""
+    st = State(3, 16, M, 20)
+    g = Device(st)
+    g.free[18] = bad  # the second page taken: row 0's places 16 .. 31
+    z = lambda n: torch.full((n,), -5, dtype=torch.int32, device="cuda")
+    out = dict(q_start=z(4), q_count=z(3), kv_len=z(3), slots=z(60), positions=z(60))
+    L.gdn_kv_plan_shared(g.kd, dev([0] * 3), dev([40, 0, 10]), dev(ones(3), torch.uint8), g.held, g.table, g.free, g.count, g.refs, **out)
+    assert L.gdn_get_status(clear=True) == BAD_INDEX
+    assert g.table[:, :4].tolist() == [[19, -1, 17, -1], [-1] * 4, [16, -1, -1, -1]] and g.held.tolist() == [3, 0, 1]
+    assert g.refs.tolist() == [0] * 16 + [1, 1, 0, 1] and g.count.item() == 16
+    slots = [19 * 16 + i for i in range(16)] + [-1] * 16 + [17 * 16 + i for i in range(8)] + [16 * 16 + i for i in range(10)]
+    assert out["slots"].tolist() == slots + [-1] * 10
+    assert out["positions"].tolist() == list(range(40)) + list(range(10)) + [-1] * 10
