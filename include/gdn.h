@@ -620,8 +620,8 @@ int gdn_kv_plan_shared(const gdn_kv4_dims *dims, int T, int N, const int32_t *le
  *  copy_src, copy_dst  [n] int32 out: pages; -1 where the pair needs no copy, -2 where
  *             it was not made.  A pair of length 0 needs nothing
  * Not made are: a pair with a row outside the cohort, with equal rows, or whose
- * destination holds pages already, also from an earlier pair of the call
- * (GDN_STATUS_BAD_ROW); one with a negative length, or longer than its source's pages
+ * destination holds pages already, also from an earlier pair of the call that was
+ * made (GDN_STATUS_BAD_ROW); one with a negative length, or longer than its source's pages
  * before the call (GDN_STATUS_BAD_LEN); one that needs a page when none is left, and
  * then every later one that needs one (GDN_STATUS_NO_PAGES); one that needs a page and
  * whose source's last page, or the stack's, is outside the cache (GDN_STATUS_BAD_INDEX;

@@ -671,7 +671,7 @@ __attribute__((visibility("default"))) int gdn_kv_fork(const gdn_kv4_dims *dims,
   NvtxRange range("gdn_kv_fork");
   int rc = check_kv4(dims);
   if (rc) return rc;
-  if (n < 0 || n > 65535) return fail(GDN_ERR_UNSUPPORTED, "fork: n=%d outside [0, 65535]", n);
+  if (n < 0 || n > kMaxForks) return fail(GDN_ERR_UNSUPPORTED, "fork: n=%d outside [0, %d]", n, kMaxForks);
   if (n == 0) return ok();
   GDN_NEED_PTR(src_rows, 4);
   GDN_NEED_PTR(dst_rows, 4);

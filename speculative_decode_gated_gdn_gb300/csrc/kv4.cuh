@@ -40,6 +40,8 @@ struct KvPlanParams {
   int log2P, max_pages, n_pages;
 };
 
+constexpr int kMaxForks = 65535;
+
 struct KvForkParams {
   const int32_t *src_rows, *dst_rows, *lens;  // [n]
   int32_t *held, *table, *free_list, *free_count, *refs;

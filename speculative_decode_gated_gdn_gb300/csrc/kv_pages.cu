@@ -15,6 +15,8 @@
 // 133 us, 6.5 TB/s read and written, 0.97 of a plain copy.
 #include <cooperative_groups.h>
 
+#include <climits>
+
 #include "kv4.cuh"
 #include "scan.cuh"
 
@@ -42,32 +44,40 @@ __device__ __forceinline__ ForkPair fork_pair(const KvForkParams &p, int i) {
   return r;
 }
 
-// Which pairs hold, and their last pages.  An empty row goes to the first pair that
-// asks for it: each leaves its index less n in the row's count, and the least stays.
+// What a pair leaves in the count of an empty row that it asks for: below what else stands there, the least for
+// the first pair.
+__device__ __forceinline__ int claim(int i) { return INT_MIN + i; }
+__device__ __forceinline__ bool is_empty(int held) { return held == 0 || held < claim(kMaxForks); }
+
+// Which pairs hold, and their last pages.  An empty row goes to the first pair that asks for it and, if that one
+// gets no page, to the first later one that needs none.
 __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
   const int tid = threadIdx.x;
   const int count0 = min(max(*p.free_count, 0), p.n_pages);
-  // a pair's verdict stands in copy_src until its page does; its thread is the same both times
+  auto held_of = [&](int row) { return *(volatile int32_t *)(p.held + row); };
+  // a pair's verdict stands in copy_src until its page does; its thread is the same every time
   for (int i = tid; i < p.n; i += kScanThreads) {
     const ForkPair r = fork_pair(p, i);
     int verdict = kBadRow;
     if (r.len < 0 || r.want > p.max_pages) {
       verdict = kBadLen;
     } else if (r.rows) {
-      const int held = *(volatile int32_t *)(p.held + r.src), taken = *(volatile int32_t *)(p.held + r.dst);
+      const int held = held_of(r.src);
+      const bool empty = is_empty(held_of(r.dst));
       const int whole = r.len >> p.log2P, last = r.want > whole ? p.table[size_t(r.src) * p.max_pages + whole] : 0;
       if (held < r.want || held > p.max_pages) {
         if (r.want > 0) verdict = kBadLen;
-        else if (taken <= 0) verdict = kNothing;
-      } else if (taken <= 0) {
+        else if (empty) verdict = kNothing;
+      } else if (empty) {
         verdict = !r.len ? kNothing : last < 0 || last >= p.n_pages ? kBadPage : kAsks;
-        if (verdict == kAsks) atomicMin(p.held + r.dst, i - p.n);
+        if (verdict == kAsks) atomicMin(p.held + r.dst, claim(i));
       }
     }
     p.copy_src[i] = verdict;
   }
   sync_cta();
-  long long taken = 0;
+  constexpr int kLate = -3;  // in copy_dst: another pair asked first
+  long long taken = 0, late = 0;
   for (int i0 = 0; i0 < p.n; i0 += kScanThreads) {
     const int i = i0 + tid;
     ForkPair r{};
@@ -76,11 +86,11 @@ __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
     if (i < p.n) {
       r = fork_pair(p, i);
       verdict = p.copy_src[i];
-      won = verdict == kAsks && *(volatile int32_t *)(p.held + r.dst) == i - p.n;
+      won = verdict == kAsks && held_of(r.dst) == claim(i);
     }
     const int whole = r.len >> p.log2P, need = won && r.want > whole;
     long long all;
-    const long long end = taken + block_scan(need, s_warp, &all);
+    const long long end = taken + (block_scan(need | (long long)(verdict == kAsks && !won) << 32, s_warp, &all) & 0xffffffff);
     if (i < p.n) {
       int from = -2, to = -2;
       if (won) {
@@ -100,6 +110,8 @@ __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
           from = to = -1;
         }
         p.held[r.dst] = made ? r.want : 0;
+      } else if (verdict == kAsks) {
+        to = kLate;
       } else if (verdict == kNothing) {
         from = to = -1;
       } else {
@@ -107,10 +119,30 @@ __device__ void decide_forks(const KvForkParams &p, long long *s_warp) {
       }
       p.copy_src[i] = from, p.copy_dst[i] = to;
     }
-    taken += all;
+    taken += all & 0xffffffff, late += all >> 32;
     sync_cta();
   }
   if (tid == 0) *p.free_count = count0 - int(min(taken, (long long)count0));
+  if (late == 0) return;  // the same for every thread
+
+  // the pairs that came late, where the first one's page was missing
+  for (int i = tid; i < p.n; i += kScanThreads) {
+    const ForkPair r = fork_pair(p, i);
+    if (p.copy_dst[i] == kLate && r.want == r.len >> p.log2P && is_empty(held_of(r.dst))) atomicMin(p.held + r.dst, claim(i));
+  }
+  sync_cta();
+  for (int i = tid; i < p.n; i += kScanThreads) {
+    if (p.copy_dst[i] != kLate) continue;
+    const int held = held_of(p.dst_rows[i]);  // pages, or what the row's pair left, or 0
+    const bool made = held == claim(i), before = held > 0 || (held < 0 && held < claim(i));
+    if (!made) atomicOr(p.status, before || taken <= count0 ? GDN_STATUS_BAD_ROW : GDN_STATUS_NO_PAGES);
+    p.copy_src[i] = p.copy_dst[i] = made ? -1 : -2;
+  }
+  sync_cta();
+  for (int i = tid; i < p.n; i += kScanThreads) {
+    const ForkPair r = fork_pair(p, i);
+    if (p.copy_src[i] == -1 && r.len > 0 && held_of(r.dst) == claim(i)) p.held[r.dst] = r.want;
+  }
 }
 
 // The shared pages' cells and counts of pair i, if it holds: cells first, first + step, ...

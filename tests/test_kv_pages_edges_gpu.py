@@ -75,3 +75,74 @@ def test_plan_where_the_stack_holds_no_page(gdn, bad, M):
     slots = [19 * 16 + i for i in range(16)] + [-1] * 16 + [17 * 16 + i for i in range(8)] + [16 * 16 + i for i in range(10)]
     assert out["slots"].tolist() == slots + [-1] * 10
     assert out["positions"].tolist() == list(range(40)) + list(range(10)) + [-1] * 10
+
+
+def forks_in_order(st, src, dst, lens):
+    """The pairs one after the other, as gdn.h has them: a destination is taken once a pair of it is made."""
+    before, status, out, P = list(st.held), 0, [], st.P
+    for s, d, n in zip(src, dst, lens):
+        want, need = -(-n // P), n % P > 0
+        rows = 0 <= s < st.B and 0 <= d < st.B and s != d
+        pair = (-2, -2)
+        if n < 0 or want > st.M or (rows and before[s] < want):
+            status |= BAD_LEN
+        elif not rows or before[d] or (n and st.held[d]):
+            status |= BAD_ROW
+        elif n == 0:
+            pair = (-1, -1)
+        elif need and st.count == 0:
+            status |= NO_PAGES
+        else:
+            pair = (-1, -1)
+            for c in range(n // P):
+                st.table[d][c] = st.table[s][c]
+                st.refs[st.table[s][c]] += 1
+            if need:
+                st.count -= 1
+                pair = (st.table[s][n // P], st.free[st.count])
+                st.table[d][n // P] = pair[1]
+                st.refs[pair[1]] = 1
+            st.held[d] = want
+        out.append(pair)
+    return [a for a, _ in out], [b for _, b in out], status
+
+
+@pytest.mark.parametrize("B,M,n,spare", [(6, 6, 2, 0), (6, 6, 5, 1), (6, 6, 9, 2), (40, 8, 60, 7), (40, 8, 400, 0), (300, 12, 1500, 90), (2000, 20, 4000, 300)])
+def test_a_destination_goes_to_the_first_pair_that_is_made(gdn, B, M, n, spare):
+    """Destinations that several pairs ask for, while pages run out: one whose page is missing leaves its row to a later pair
+    that needs none."""
+    rng = np.random.default_rng(n)
+    for turn in range(4):
+        sources = max(2, B // 10)
+        need = [int(rng.integers(17, 16 * M + 1)) if b < sources else 0 for b in range(B)]
+        used = sum(-(-x // 16) for x in need)
+        st = State(B, 16, M, used + spare, rng.permutation(used + spare).tolist())
+        g = Device(st)
+        g.plan(0, sum(need), [0] * B, need, ones(B))
+        src = rng.integers(0, sources + 1, n).tolist()
+        dst = rng.integers(sources - 1, min(B, sources + 1 + n // 2), n).tolist()
+        lens = [int(rng.choice([need[s], need[s] // 16 * 16, 16, 0, int(rng.integers(0, need[s] + 20))])) for s in src]
+        want = forks_in_order(st, src, dst, lens)
+        assert fork(g, src, dst, lens) == want
+        g.same()
+        st.check()
+
+
+def test_whole_pages_after_the_last_page(gdn):
+    """No page is left: a pair of 33 tokens is not made, one of 32 for the same row is, and later ones find the row taken."""
+    st = State(5, 16, 4, 3)
+    g = Device(st)
+    g.plan(0, 40, [0] * 5, [33, 0, 0, 0, 0], ones(5))
+    a, b, status = fork(g, [0] * 6, [3, 3, 3, 3, 4, 3], [33, 32, 32, 33, 1, 0])
+    assert (a, b) == ([-2, -1, -2, -2, -2, -1],) * 2 and status == NO_PAGES | BAD_ROW
+    assert g.held.tolist() == [3, 0, 0, 2, 0] and g.table[3].tolist() == g.table[0].tolist()[:2] + [-1, -1]
+    assert g.refs.tolist() == [2 if p in g.table[3].tolist() else 1 for p in range(3)]
+
+
+def test_a_row_of_a_negative_count_is_not_empty(gdn):
+    st = State(4, 16, 4, 20)
+    g = Device(st)
+    g.plan(0, 40, [0] * 4, [33, 0, 0, 0], ones(4))
+    g.held[1], g.held[2] = -1, -100
+    a, b, status = fork(g, [0] * 4, [1, 2, 2, 3], [32] * 4)
+    assert (a, b) == ([-2, -2, -2, -1],) * 2 and status == BAD_ROW and g.held.tolist() == [3, -1, -100, 2]
