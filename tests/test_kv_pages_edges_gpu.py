@@ -146,3 +146,39 @@ def test_a_row_of_a_negative_count_is_not_empty(gdn):
     g.held[1], g.held[2] = -1, -100
     a, b, status = fork(g, [0] * 4, [1, 2, 2, 3], [32] * 4)
     assert (a, b) == ([-2, -2, -2, -1],) * 2 and status == BAD_ROW and g.held.tolist() == [3, -1, -100, 2]
+
+
+@pytest.mark.parametrize("B,M,lo,bad", [(120, 400, 60, False), (120, 400, 60, True), (100, 700, 690, False), (100, 700, 690, True), (3, 1400, 1, True), (1024, 8, 1, True), (1030, 40, 33, True)])
+def test_releases_of_large_tables(gdn, B, M, lo, bad):
+    """Pages given back where the table has thousands of cells, up to 4 x 8 x 1024 releases in a call (they stay in registers)
+    and more (they do not): rows of one prompt, cut to any length and ended, with cells outside the cache and pages that
+    nobody holds among them."""
+    rng = np.random.default_rng(B * M)
+    P, prompts = 16, max(1, B // 5)
+    need = [int(rng.integers(lo * P, M * P + 1)) if b < prompts else 0 for b in range(B)]
+    n = sum(-(-x // P) for x in need) + B + 10
+    st = State(B, P, M, n, rng.permutation(n).tolist())
+    g = Device(st)
+    g.plan(0, sum(need), [0] * B, need, ones(B))
+    dst = list(range(prompts, B))
+    src = [d % prompts for d in dst]
+    lens = need[:prompts] + [max(1, need[s] - int(rng.integers(0, need[s] // 3 + 1))) for s in src]
+    g.fork(src, dst, lens[prompts:])
+    st.check()
+    if bad:
+        for b in rng.permutation(B)[: max(3, B // 9)].tolist():
+            st.table[b][int(rng.integers(0, st.held[b]))] = int(rng.choice([-1, -9, n, n + 1000, 1 << 30]))
+        for b in rng.permutation(B)[: max(3, B // 9)].tolist():
+            page = st.table[b][int(rng.integers(0, st.held[b]))]
+            if 0 <= page < n:
+                st.refs[page] = 0
+        g.upload()
+    some = rng.permutation(B)[: B // 2].tolist()
+    held = list(st.held)
+    for b in some:
+        lens[b] = int(rng.choice([0, int(rng.integers(0, lens[b] + 1)), lens[b]]))
+    status = lambda new: BAD_INDEX if any(not 0 <= p < n or st.refs[p] == 0 for b in range(B) for p in st.table[b][-(-new[b] // P): st.held[b]]) else 0
+    g.plan(1, B, lens, [0] * B, ones(B), status=status(lens))
+    assert sum(held) > sum(st.held) or B < 5
+    g.plan(1, B, [0] * B, [0] * B, ones(B), status=status([0] * B))
+    assert not any(st.held) and (bad or st.count == n)
