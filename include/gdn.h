@@ -598,9 +598,12 @@ int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, con
  * when it has none left, at the place (in row order, each row's in column order) of
  * the last of its releases in the call.  A page outside the cache, or one that had no
  * holder, is dropped (GDN_STATUS_BAD_INDEX).  A stack entry outside the cache gives
- * its row a cell of -1, and the tokens there no slots (GDN_STATUS_BAD_INDEX).  A row's length never falls below what it
- * shares, except to 0: rows write behind their committed length, and what is shared
- * lies before it.  Supported: B * max_pages < 2^31.
+ * its row a cell of -1, and the tokens there no slots (GDN_STATUS_BAD_INDEX).
+ * Rows write behind their committed length, and what is shared has to lie before it:
+ * a row whose first new token would stand in a page that another row holds after the
+ * call's releases (it was cut to less than it shares, begins anew at 0 while it still
+ * holds such pages, or was forked behind its committed length) gives back what it holds
+ * too much and gets no tokens (GDN_STATUS_BAD_LEN).  Supported: B * max_pages < 2^31.
  */
 int gdn_kv_plan_shared(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, const int32_t *add,
                        const uint8_t *active, int32_t *held, int32_t *table, int32_t *free_list,

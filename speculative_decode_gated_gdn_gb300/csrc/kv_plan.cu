@@ -62,6 +62,15 @@ __device__ __forceinline__ PlanRow plan_row(const KvPlanParams &p, int b) {
   return r;
 }
 
+// Whether the row's first new token would stand in a page that another row holds too.  Where it
+// does not, no later one does: rows share beginnings, and give pages back from their ends.
+__device__ __forceinline__ bool writes_shared(const KvPlanParams &p, int b, const PlanRow &r) {
+  const int c = r.len >> p.log2P;
+  if (r.a == 0 || c >= r.held) return false;
+  const int page = p.table[size_t(b) * p.max_pages + c];
+  return page >= 0 && page < p.n_pages && __ldcg(p.refs + page) > 1;
+}
+
 // Slot and position of token i, -1 where no row has it.
 __device__ __forceinline__ void plan_token(const KvPlanParams &p, int i) {
   const int b = p.T > 0 ? i / p.T : find_row(p.q_start + 1, p.B, i);
@@ -270,6 +279,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanParam
     const int b = b0 + tid, rows = min(kPlanThreads, p.B - b0);
     PlanRow r{};
     if (b < p.B) r = plan_row(p, b);
+    if (SHARED && b < p.B && writes_shared(p, b, r)) {
+      r.a = 0, r.want = min(r.want, r.held);
+      atomicOr(p.status, GDN_STATUS_BAD_LEN);
+    }
     const int need = max(r.want - r.held, 0);
     long long need_total, tok_total;
     const long long need_end = taken0 + block_scan(need, s_warp, &need_total);

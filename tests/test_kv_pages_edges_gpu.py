@@ -182,3 +182,96 @@ def test_releases_of_large_tables(gdn, B, M, lo, bad):
     assert sum(held) > sum(st.held) or B < 5
     g.plan(1, B, [0] * B, [0] * B, ones(B), status=status([0] * B))
     assert not any(st.held) and (bad or st.count == n)
+
+
+def plan(g, T, N, lens, add, active=None):
+    z = lambda n: torch.full((n,), -5, dtype=torch.int32, device="cuda")
+    B = g.st.B
+    out = dict(q_start=z(B + 1), q_count=z(B), kv_len=z(B), slots=z(N), positions=z(N))
+    L.gdn_kv_plan_shared(g.kd, dev(lens), dev(add), dev(active or ones(B), torch.uint8), g.held, g.table, g.free, g.count, g.refs, **out, T=T)
+    return {k: v.tolist() for k, v in out.items()}, L.gdn_get_status(clear=True)
+
+
+@pytest.mark.parametrize("M", [8, 1500])
+@pytest.mark.parametrize("T", [0, 4])
+def test_no_row_writes_into_a_page_that_another_holds(gdn, M, T):
+    """A row whose next token would stand in a shared page gets no tokens, and a status; the others get theirs.  Row 0 has 70
+    tokens, row 1 continues them, row 2 the first 40, row 3 is alone."""
+    def start():
+        g = Device(State(4, 16, M, 40))
+        g.plan(0, 200, [0] * 4, [70, 0, 0, 33], ones(4))
+        g.fork([0, 0], [1, 2], [70, 40])
+        return g
+
+    # as the header has it: behind what is shared
+    g = start()
+    g.plan(T, 16, [70, 70, 40, 33], [4] * 4, ones(4))
+    g.st.check()
+    # rows 0 and 1 both cut: row 1 gives its third page back, so row 0 may go on in it; row 1's second is also row 0's
+    g = start()
+    out, status = plan(g, T, 16, [34, 20, 40, 33], [4] * 4)
+    assert status == BAD_LEN and out["q_count"] == [4, 0, 4, 4] and out["kv_len"] == [38, 20, 44, 37]
+    assert g.held.tolist() == [3, 2, 3, 3]
+    # row 0 at 34 while row 1 stays
+    g = start()
+    out, status = plan(g, T, 16, [34, 70, 40, 33], [4] * 4)
+    assert status == BAD_LEN and out["q_count"] == [0, 4, 4, 4] and out["kv_len"] == [34, 74, 44, 37] and g.held.tolist() == [3, 5, 3, 3]
+    at = out["q_start"][1]
+    assert out["slots"][at] == g.table[1, 4].item() * 16 + 70 % 16 and (T == 0 or out["slots"][:4] == [-1] * 4)
+    # a row that begins anew while it still holds what it shared; nothing to write, nothing wrong
+    g = start()
+    out, status = plan(g, T, 16, [0, 70, 40, 33], [4] * 4)
+    assert status == BAD_LEN and out["q_count"] == [0, 4, 4, 4]
+    out, status = plan(g, T, 16, [0, 74, 44, 37], [0, 4, 4, 4])
+    assert status == 0 and g.held.tolist() == [0, 5, 3, 3]
+    out, status = plan(g, T, 16, [0, 78, 48, 41], [4, 0, 0, 0])
+    assert status == 0 and out["q_count"] == [4, 0, 0, 0] and g.refs[g.table[0, 0]].item() == 1
+    # the other holders end in the same call: nobody shares it any more
+    g = start()
+    out, status = plan(g, T, 16, [34, 0, 0, 33], [4, 0, 0, 4])
+    assert status == 0 and out["q_count"] == [4, 0, 0, 4]
+    # a fork of more than the source has committed
+    g = start()
+    out, status = plan(g, T, 16, [70, 70, 0, 20], [0] * 4)  # row 3: 20 committed, in two pages
+    assert status == 0 and g.held.tolist() == [5, 5, 0, 2]
+    assert fork(g, [3], [2], [32]) == ([-1], [-1], 0)
+    out, status = plan(g, T, 16, [70, 70, 32, 20], [0, 0, 4, 4])
+    assert status == BAD_LEN and out["q_count"] == [0, 0, 4, 0]
+    # inactive rows and rows without new tokens may be of any length
+    out, status = plan(g, T, 16, [34, 20, 33, 3], [4, 0, 0, 4], [0, 1, 1, 0])
+    assert status == 0
+
+
+@pytest.mark.parametrize("B", [1030, 2500])
+def test_shared_rows_of_many_chunks(gdn, B):
+    """The same where rows take more than one look, in the fixed and the packed layout, against a row-by-row reading."""
+    rng = np.random.default_rng(B)
+    g = Device(State(B, 16, 6, 4 * B))
+    need = [int(rng.integers(1, 80)) if b % 3 == 0 else 0 for b in range(B)]
+    g.plan(0, sum(need), [0] * B, need, ones(B))
+    lens = list(need)
+    pairs = [(b - b % 3, b, int(rng.integers(1, need[b - b % 3] + 1))) for b in range(B) if b % 3]
+    g.fork(*map(list, zip(*pairs)))
+    for s, d, n in pairs:
+        lens[d] = n
+    cut = [int(rng.integers(1, n + 1)) if rng.random() < 0.3 else n for n in lens]
+    add = rng.integers(0, 4, B).tolist()
+    st = g.st
+    held = [min(st.held[b], -(-(cut[b] + add[b]) // 16)) for b in range(B)]
+    left = [0] * st.n
+    for b in range(B):
+        for c in range(held[b]):
+            left[st.table[b][c]] += 1
+    bad = [add[b] > 0 and cut[b] // 16 < held[b] and left[st.table[b][cut[b] // 16]] > 1 for b in range(B)]
+    assert 20 < sum(bad) < B // 2
+    for T in (3, 0):
+        g.upload()
+        out, status = plan(g, T, 3 * B, cut, add)
+        assert status == BAD_LEN
+        assert out["q_count"] == [0 if x else a for x, a in zip(bad, add)]
+        assert g.held.tolist() == [held[b] if bad[b] else -(-(cut[b] + add[b]) // 16) for b in range(B)]
+        seen = [0] * st.n
+        for b, (row, k) in enumerate(zip(g.table.tolist(), g.held.tolist())):
+            for p in row[:k]:
+                seen[p] += 1
+        assert seen == g.refs.tolist()
