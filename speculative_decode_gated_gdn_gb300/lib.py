@@ -209,8 +209,16 @@ def _here():
 def _elsewhere(t, what):
     """Refuses a tensor that is on another CUDA device than the current one,
     whose address the call's kernels could not follow."""
-    if t.get_device() != _here():
+    if t.is_cuda and t.get_device() != _here():
         raise ValueError(f"{what}: tensor is on {t.device}, the current CUDA device is {_here()}")
+
+
+def _ptr_here(t, what, dtype=None):
+    """_ptr of a tensor that has to be on the current device."""
+    p = _ptr(t, what, dtype)
+    if p is not t:  # (not a raw pointer, or None)
+        _elsewhere(t, what)
+    return p
 
 
 _raw_stream = None
@@ -415,9 +423,9 @@ def gdn_accept_greedy(logits, draft, active, keep, nxt, ws, stream=None):
     ws: gdn_accept_workspace_bytes(B, T, V) bytes, zero-filled once."""
     torch = _t()
     B, T, V = logits.shape
-    rc = load().gdn_accept_greedy(B, T, V, _ptr(logits, "logits", torch.bfloat16), _ptr(draft, "draft", torch.int32),
-                                  _ptr(active, "active", torch.uint8), _ptr(keep, "keep", torch.int32),
-                                  _ptr(nxt, "next", torch.int32), _ptr(ws, "ws"),
+    rc = load().gdn_accept_greedy(B, T, V, _ptr_here(logits, "logits", torch.bfloat16), _ptr_here(draft, "draft", torch.int32),
+                                  _ptr_here(active, "active", torch.uint8), _ptr_here(keep, "keep", torch.int32),
+                                  _ptr_here(nxt, "next", torch.int32), _ptr_here(ws, "ws"),
                                   ws.numel() * ws.element_size(), _stream(stream))
     _check(rc, "gdn_accept_greedy")
 
@@ -463,8 +471,7 @@ def _some_ptrs(here, *args):
             except AttributeError:
                 pass
             _count(t, what, n)
-            p.append(_ptr(t, what, dtype))
-            _elsewhere(t, what)
+            p.append(_ptr_here(t, what, dtype))
     return p
 
 
@@ -526,6 +533,7 @@ def _tokens(t, what, heads, d):
     torch = _t()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
+    _elsewhere(t, what)
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{what}: expected {torch.bfloat16}, got {t.dtype}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
@@ -563,10 +571,7 @@ def _ptrs(*args):
         pass
     for t, what, n, _ in args:
         _count(t, what, n)
-    p = [_ptr(t, what, dtype) for t, what, _, dtype in args]
-    for t, what, _, _ in args:
-        _elsewhere(t, what)
-    return p
+    return [_ptr_here(t, what, dtype) for t, what, _, dtype in args]
 
 
 def gdn_kv_plan(kd: gdn_kv4_dims, lens, add, active, held, table, free_list, free_count, q_start, q_count, kv_len,
@@ -664,9 +669,7 @@ def gdn_kv_copy_pages(kd: gdn_kv4_dims, caches, src, dst, count=None, stream=Non
     except AttributeError:
         p = ()
     if len(p) != len(caches):
-        p = [_cache(kd, t) for t in caches]
-        for i, t in enumerate(caches):
-            _elsewhere(t, f"caches[{i}]")
+        p = [_cache(kd, t, f"caches[{i}]") for i, t in enumerate(caches)]
     rc = load().gdn_kv_copy_pages(ctypes.byref(kd), len(p), (_P * max(len(p), 1))(*p), n, sp, dp,
                                   None if count is None else _ptrs((count, "count", 1, i32))[0], _stream(stream))
     _check(rc, "gdn_kv_copy_pages")
@@ -681,17 +684,17 @@ def _cache_bytes(kd):
     return kd.n_pages * kd._page_bytes
 
 
-def _cache(kd, pages):
+def _cache(kd, pages, what="pages"):
     """Pointer of a cache; it may be larger than its dims say, never smaller."""
     need = _cache_bytes(kd)
     try:
         size = pages.numel()
     except AttributeError:
-        _need(pages=pages)
+        _need(**{what: pages})
         raise
-    p = _ptr(pages, "pages", _t().uint8)
+    p = _ptr_here(pages, what, _t().uint8)
     if size < need:
-        raise ValueError(f"pages: {size} bytes, needs {need}")
+        raise ValueError(f"{what}: {size} bytes, needs {need}")
     return p
 
 
@@ -726,8 +729,8 @@ def gdn_kv4_append(kd: gdn_kv4_dims, q, k, v, positions, rope, axis, slots, page
         if len(axis) != rot // 2:
             raise ValueError(f"axis: expected {rot // 2} bytes, got {len(axis)}")
     rc = load().gdn_kv4_append(
-        ctypes.byref(kd), N, qp, qs, kp, ks, vp, vs, _ptr(positions, "positions", torch.int32) if rot else None,
-        n_axes, _ptr(rope, "rope", torch.float32), max_pos, rot, axis if rot else None, style,
+        ctypes.byref(kd), N, qp, qs, kp, ks, vp, vs, _ptr_here(positions, "positions", torch.int32) if rot else None,
+        n_axes, _ptr_here(rope, "rope", torch.float32), max_pos, rot, axis if rot else None, style,
         sp, _cache(kd, pages), op, _stream(stream))
     _check(rc, "gdn_kv4_append")
 
@@ -762,7 +765,7 @@ def _attend_args(kd, q, pages, table, q_start, q_count, kv_len, scale, out, ws, 
     size = N * kd.H_q * kd.d
     qp, op, tp, sp, cp, lp = _ptrs((q, "q", size, bf16), (out, "out", size, bf16), (table, "table", B * kd.max_pages, i32),
                                    (q_start, "q_start", B + 1, i32), (q_count, "q_count", B, i32), (kv_len, "kv_len", B, i32))
-    return ctypes.byref(kd), N, max_q, qp, _cache(kd, pages), tp, sp, cp, lp, scale, op, _ptr(ws, "ws"), ws_bytes
+    return ctypes.byref(kd), N, max_q, qp, _cache(kd, pages), tp, sp, cp, lp, scale, op, _ptr_here(ws, "ws"), ws_bytes
 
 
 def gdn_kv4_attend(kd: gdn_kv4_dims, q, pages, table, q_start, q_count, kv_len, scale, out, ws, max_q, stream=None):
