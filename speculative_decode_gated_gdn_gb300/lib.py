@@ -198,11 +198,12 @@ def _here():
     """The current CUDA device's number: what get_device() of a call's tensors
     has to be (-1 is the host); -2 where there is none."""
     global _device_number
-    if _device_number is None:
-        _device_number = _t()._C._cuda_getDevice
+    if _device_number is None:  # torch's own question behind current_device, without its look at the state of CUDA
+        torch = _t()
+        _device_number = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
     try:
         return _device_number()
-    except RuntimeError:
+    except (RuntimeError, AssertionError):
         return -2
 
 
@@ -233,8 +234,8 @@ def _stream(stream):
         if _raw_stream is None:
             torch = _t()
             handle = torch.cuda.current_stream().cuda_stream  # initialises CUDA, or says why it cannot
-            device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-            _raw_stream = lambda: raw(device())
+            device, raw = (getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+            _raw_stream = (lambda: raw(device())) if device and raw else (lambda: torch.cuda.current_stream().cuda_stream)
             return handle
         return _raw_stream()
     if isinstance(stream, int):

@@ -59,3 +59,33 @@ def test_tensors_of_another_device_are_refused(monkeypatch, name, bad):
     kd = () if name in ("gdn_accept_greedy", "gdn_sample") else (L.kv4_dims(**KD),)
     with pytest.raises(ValueError, match="cuda:1"):
         getattr(L, name)(*kd, **args, **rest)
+
+
+@pytest.fixture
+def bare_torch(monkeypatch):
+    """torch without the private names that make the two questions of every call cheap."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    for name in ("_device_number", "_raw_stream"):
+        monkeypatch.setattr(L, name, None)
+    return monkeypatch
+
+
+def test_public_device_and_stream_serve_where_the_private_names_are_gone(bare_torch):
+    class Stream:
+        cuda_stream = 5
+
+    bare_torch.setattr(torch.cuda, "current_device", lambda: 3)
+    bare_torch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    assert L._here() == 3 and [L._stream(None), L._stream(None)] == [5, 5]
+    Stream.cuda_stream = 7
+    assert L._stream(None) == 7 and L._stream(9) == 9 and L._stream(Stream) == 7
+
+
+@pytest.mark.parametrize("error", [RuntimeError, AssertionError])
+def test_no_device_is_none(bare_torch, error):
+    def none():
+        raise error("no CUDA")
+
+    bare_torch.setattr(torch.cuda, "current_device", none)
+    assert L._here() == -2
