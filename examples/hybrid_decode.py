@@ -17,7 +17,8 @@ and a cycle of T tokens a row (the last accepted one and T - 1 drafts), captured
     gdn_accept_greedy        keep, and the next token
     gdn_commit               the GDN state of the accepted prefix; offsets += keep
 
-With --samples N every prompt goes on in N rows.  They share its full pages, and their tokens are drawn:
+With --samples N every prompt goes on in N rows, which share its full pages.  Their tokens are drawn, as those of one row a
+prompt are where --temperature is given:
 
     gdn_kv_fork, gdn_kv_copy_pages, gdn_move_rows    the prompt's pages and GDN state for its other rows
     gdn_sample               each row's first token
@@ -40,7 +41,7 @@ MODE = L.GDN_COMMIT_RECOMPUTE
 class Model:
     """B rows of the model with their GDN state, conv ring and cache pages."""
 
-    def __init__(self, B, T, max_len, samples=1, temperature=0.8, top_p=0.95, vocab=512, width=256, H_k=2, H_v=4, d_gdn=64, H_q=8, H_kv=2, d=128, rot=64, page=32,
+    def __init__(self, B, T, max_len, samples=1, temperature=None, top_p=0.95, vocab=512, width=256, H_k=2, H_v=4, d_gdn=64, H_q=8, H_kv=2, d=128, rot=64, page=32,
                  seed=0):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *s, scale=1.0: (torch.randn(*s, generator=gen, device="cuda") * scale).bfloat16()
@@ -66,8 +67,9 @@ class Model:
         self.held, self.table = zeros(B), torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
         self.free_list = torch.arange(n_pages, dtype=torch.int32, device="cuda")
         self.free_count = torch.full((1,), n_pages, dtype=torch.int32, device="cuda")
-        # several rows a prompt: holders of each page, the rows' ways of sampling, and random numbers for a cycle
-        self.prompts, self.refs = B // samples, zeros(n_pages) if samples > 1 else None
+        # drawn tokens: holders of each page, the rows' ways of sampling, and random numbers for a cycle
+        self.prompts, self.refs = B // samples, zeros(n_pages) if samples > 1 or temperature is not None else None
+        temperature = 0.8 if temperature is None else temperature
         self.ways = dict(temperature=torch.full((B,), temperature, device="cuda"), top_p=torch.full((B,), top_p, device="cuda"))
         self.u = zeros(B, T, dtype=torch.float32)
         self.q_start, self.q_count, self.kv_len = zeros(B + 1), zeros(B), zeros(B)
@@ -131,7 +133,8 @@ class Model:
         if self.refs is None:
             self._feed(last.argmax(1).int())
             return
-        self._fork(n)
+        if P < self.B:
+            self._fork(n)
         self.u.uniform_()
         L.gdn_sample(last.repeat(self.B // P, 1), self.u[:, 0].contiguous(), self.next, **self.ways)
         self._feed(self.next)
@@ -188,8 +191,8 @@ class Model:
         self._feed(self.next)
 
 
-def run(rows=8, prompt=500, cycles=64, draft=1, seed=0, samples=1, temperature=0.8):
-    """Decodes and returns the model and the seconds a cycle took."""
+def run(rows=8, prompt=500, cycles=64, draft=1, seed=0, samples=1, temperature=None):
+    """Decodes and returns the model and the seconds a cycle took; tokens are drawn where samples > 1 or temperature is given."""
     m = Model(rows * samples, draft + 1, prompt + (cycles + 3) * (draft + 1), samples, temperature, seed=seed)
     m.prompt(torch.randint(0, m.vocab, (rows, prompt), device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed + 1)))
     stream = torch.cuda.Stream()
@@ -218,8 +221,8 @@ def main():
     ap.add_argument("--prompt", type=int, default=500)
     ap.add_argument("--cycles", type=int, default=64)
     ap.add_argument("--draft", type=int, default=1)
-    ap.add_argument("--samples", type=int, default=1, help="rows that continue each prompt, by sampling if more than one")
-    ap.add_argument("--temperature", type=float, default=0.8)
+    ap.add_argument("--samples", type=int, default=1, help="rows that continue each prompt")
+    ap.add_argument("--temperature", type=float, help="draw the tokens, also of one row a prompt (several rows: 0.8 by default)")
     a = ap.parse_args()
     m, dt = run(a.rows, a.prompt, a.cycles, a.draft, samples=a.samples, temperature=a.temperature)
     done = (m.offsets - a.prompt).float().mean().item()
