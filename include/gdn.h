@@ -472,9 +472,10 @@ int gdn_accept_greedy(int B, int T, int V, const gdn_bf16 *logits, const int32_t
  * u outside [0, 1) as the nearest number in it, NaN as 0.  A position with no number
  * above -infinity gives what gdn_accept_greedy takes, with logp -infinity.
  * Infinite logits share the mass among themselves.
- * Precision: weights to 2^-37 of themselves and 2^-43 of the largest (down to 2^-53 of it
- * what is smaller, and left by min_p, still decides where the rest meets top_p exactly), their
- * sums exact in integers; logp to 2^-22 (1 + |logp|); the same inputs give the same outputs on every run.
+ * Precision: weights, also where min_p meets them, to 2^-37 of themselves and 2^-43 of
+ * the largest (down to 2^-53 of it what is smaller, and left by min_p, still decides where
+ * the rest meets top_p exactly), their sums exact in integers; logp to 2^-22 (1 + |logp|);
+ * the same inputs give the same outputs on every run.
  *  logits  position (b, t) at (b * T + t) * stride elements, bf16, stride >= V;
  *          any 2-byte aligned address
  *  active  [B] uint8, NULL: all.  Inactive rows get token -1 and logp 0
@@ -597,7 +598,8 @@ int gdn_kv_plan(const gdn_kv4_dims *dims, int T, int N, const int32_t *lens, con
  * A page taken gets one holder.  A page given back loses one, and goes onto the stack
  * when it has none left, at the place (in row order, each row's in column order) of
  * the last of its releases in the call.  A page outside the cache, or one that had no
- * holder, is dropped (GDN_STATUS_BAD_INDEX).  A stack entry outside the cache gives
+ * holder, is dropped (GDN_STATUS_BAD_INDEX; where more rows give a page back than it
+ * counts, it goes back once, at the place of one of them).  A stack entry outside the cache gives
  * its row a cell of -1, and the tokens there no slots (GDN_STATUS_BAD_INDEX).
  * Rows write behind their committed length, and what is shared has to lie before it:
  * a row whose first new token would stand in a page that another row holds after the

@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       // Dust: weights too small for the units of the masses.  It is told, because where the rest meets
       // a border exactly (two equal logits share the mass, top_p is 0.5) any more than nothing decides.
       // Only what min_p leaves is any: log(min_p) is as near here as 2^-22 of itself.  Halves of the logits, whose
-      // differences are finite.
-      const float half_top = 0.5f * top, dust_from = fmaxf(-18.35f * temperature, min_p > 0.f ? 0.5f * temperature * logf(min_p) : -INFINITY);
+      // differences are finite; 36.8 temperatures are 2^-53.1.
+      const float half_top = 0.5f * top, dust_from = fmaxf(-18.4f * temperature, min_p > 0.f ? 0.5f * temperature * logf(min_p) : -INFINITY);
       auto is_dust = [&](int place, u64 w) { return !w && 0.5f * value_at(place) - half_top >= dust_from; };
 
       // ---- the cluster's counts, and its groups' counts and masses ---------------------------

@@ -101,3 +101,14 @@ def test_temperatures_of_any_size(gdn, temperature):
     bits = bits_of(np.clip(x, -3.3e38, 3.3e38))
     for kw in (dict(), dict(top_p=0.8), dict(top_k=30), dict(min_p=0.1)):
         check(bits, rng.random(4), temperature=temperature, **kw)
+
+
+@pytest.mark.parametrize("bits,decides", [(52.97, True), (50.0, True), (54.5, False)])
+def test_dust_down_to_its_border(gdn, bits, decides):
+    """Two equal maxima, top_p a half, others of 2^-bits of them: down to 2^-53 they make the half less than half."""
+    x = np.full((8, 300), -INF)
+    x[:, [4, 9]], x[:, 20:200] = 3.0, -5.0
+    token = torch.zeros(8, dtype=torch.int32, device="cuda")
+    full = lambda a: torch.full((8,), a, device="cuda")
+    L.gdn_sample(logits_on(bits_of(x)), torch.linspace(0.05, 0.95, 8, device="cuda"), token, temperature=full(8 / (bits * math.log(2))), top_p=full(0.5))
+    assert set(token.tolist()) == ({4, 9} if decides else {4})
