@@ -8,11 +8,10 @@
 // The bookkeeping is a few dependent trips to L2, so it is latency that counts: one
 // kernel of one cluster does it where it is small, whose CTAs wait for the first one's
 // decisions and then share the cells; where it is large, a second kernel of many CTAs
-// does the cells.  Eight forks of 207 pages take 7.3 us (two kernels 5.3 + 3.8), 256
-// of 62 8.7 (5.7 + 4.3); a compaction of 11,818 pages and 16,500 cells takes 13.4 us in
-// a cluster, 10.8 + 5.3 in a CTA and a second kernel; one of 90 pages 6.8 in a CTA
-// alone, 10.5 in a cluster.  Copies are bound by HBM: 11,820 pages of 36,864 bytes in
-// 133 us, 6.5 TB/s read and written, 0.97 of a plain copy.
+// does the cells.  Behind other kernels eight forks of 207 pages take 4.9 us, 256 of 62
+// 5.8; a compaction of 90 pages 4.8, of 11,818 pages and cells 10.7.  Copies are bound by
+// HBM: 11,820 pages of 36,864 bytes in 133 us, 6.5 TB/s read and written, 0.97 of a plain
+// copy.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -347,10 +346,15 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const __grid_cons
   }
 }
 
-// Cells up to which one cluster does all: four a thread.
+// Cells up to which one cluster does all: four a thread.  It saves a launch, 2 us of the caller's time, and on the GPU
+// costs less than that, us behind other kernels in one cluster and in two kernels:
+//   forks of 1,656 cells 4.9 / 4.2, 15,872 5.8 / 5.4, 32,768 6.2 / 5.1, 51,200 8.0 / 6.0, 131,072 10.9 / 8.6;
+//   by the clock, with the caller, 13.0 / 14.7, 13.1 / 15.2, 13.0 / 14.2
+//   compactions of 8,192 pages and cells 9.5 / 8.9, 32,768 11.4 / 9.5, 50,000 16.1 / 12.1
 constexpr long long kOneClusterCells = 4ll * kCluster * kScanThreads;
 
-constexpr int kOneCtaCells = 4 * kScanThreads;  // and one CTA
+// And one CTA: compactions of 1,000 pages and cells 5.0 us, in a cluster 7.3; 4,096 8.2 / 9.6; 6,000 10.3 / 9.1.
+constexpr int kOneCtaCells = 4 * kScanThreads;
 
 int sm_count() {
   int dev = 0, n = 152;

@@ -19,8 +19,10 @@
 // is the last one's; the release that finds its own mark pushes the page.  Each pass
 // is a few dependent trips to L2 a release, so where there may be many, a cluster of
 // kPlanCluster CTAs shares them, and up to four of a thread stay in its registers from
-// pass to pass: a plan with 24,000 releases of 122 rows takes 107 us in one CTA, 33 in
-// eight that look each up in every pass, 22.5 so.
+// pass to pass: 24,400 releases of 122 rows take 66.8 us in one CTA, 20.2 in eight that look
+// each up in every pass, 15.1 so.
+//
+// Whether a row writes into a shared page is two dependent reads a row more, 0.3 us of a plan's 5.
 #include <cooperative_groups.h>
 
 #include "kv4.cuh"
@@ -34,9 +36,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kPlanThreads = kScanThreads;
 constexpr int kPlanCluster = 8, kBatch = 4;
-// Cells of the table from which on shared releases go to a cluster, whose barriers cost a
-// plan without releases half a microsecond (8.4 us, 8.9).  1656 releases of 8 rows in one
-// CTA: 11 us.
+// Cells of the table from which on shared releases go to a cluster.  One CTA keeps 4096 releases in registers:
+// 4000 take 10.7 us there, 12.0 in the cluster; 4800 17.3 and 12.1; 16000 41.5 and 13.3.  A plan without releases
+// takes 4.7 and 5.1.
 constexpr long long kPlanCells = 4096;
 // Tokens up to which the bookkeeping CTA writes the slots itself; a kernel of their own
 // behind it costs 16 tokens 5.8 us for 4.7, and 2048 5.6 for 5.3, but 8192 take 5.5 for

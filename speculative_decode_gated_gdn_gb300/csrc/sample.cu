@@ -22,14 +22,18 @@
 // A logit above all of the 16 binades makes a CTA's counting begin again with others; an
 // answer near zero is looked for in windows of 1024 values over the row.
 //
-// What bounds it.  Few rows: latency, 7.7 us for one row of 32000: 2 to the first logits,
-// 1 to 2 for the counts, 0.7 for each of three cluster barriers, 2 for the questions (a
-// share of the mass, three ballots, a weight and a quotient each), 0.5 for the logit.
-// Many unfiltered rows: the counts, 30 us of 45.8 for 256 rows of 151936 (77.8 MB, 11.6 us
-// of HBM).  Of these the atomics, one a logit, take 15: 32 random bins cost 3.4 cycles of
-// the banks.  The rest is instructions: 29 million in all, 0.6 an issue slot, 0.8 on the
-// SMs with two rows.  Then the groups' weights, 7, and the search, 5.  256 rows
-// leave 48 SMs with one row and 104 with two.  480 rows of 151936 with top-p: 89 us.
+// What bounds it.  Few rows: latency.  One row of 32000 takes 7.8 us: 1.4 to the first logits, 0.4 the bound, 0.9
+// the counts, 1.2 the groups, 1.6 the questions (a share of the mass, three ballots, a weight and a quotient each),
+// 1.1 the logit, 1.2 in three cluster barriers.  Sixteen of 151936, twelve of them live, 14.3: 1.8 between two
+// kernels, 1.5 to the first logits, 0.3, 2.6 the counts (a slice is 14 % longer than what the first loads hold, so
+// there is one more trip to memory), 0.8, 2.1, 1.3, 2.1 in barriers, and 1.8 that the slowest slice takes longer.
+// Many unfiltered rows: instructions.  256 rows of 151936 (77.8 MB, 11.6 us of HBM) take 46.3 us and 29.2 million
+// warp instructions, 0.60 an issue slot while an SM is active, 0.79 on the fullest: 1.4 million to the bound, 15.3 in
+// the counts (6.3 loads with their bounds and maxima, 5.4 the bins' addresses and branches, 3.6 the atomics and
+// what waits for them, 1.25 million atomics whose 32 random bins cost 3.4 cycles of the banks), 8.2 in the groups'
+// weights, 0.8 in the questions, 3.5 in the search.  Ended after each of these the kernel takes 3.1, 27.6 (21.6
+// without the atomics, 13.0 with loads and maxima alone), 39.7, 41.6 and 46.3 us.  256 rows leave 48 SMs with one
+// row and 104 with two.  480 rows of 151936 with top-p: 90 us.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -761,11 +765,12 @@ size_t accept_sampled_workspace_bytes(int B, int T) {
 
 // CTAs of a position: as many as the GPU holds at once (two an SM) for all of them, where
 // each has 4096 logits at least.  Both sides, us of GPU time with 1, 2, 4, 8 CTAs:
-//   1 row of 32000, top-k 40, top-p, min-p        7.8   8.3   7.6   7.8
-//   16 of 151936, top-k 20, top-p                30.1  21.6  14.6  13.9
-//   64 of 151936, mixed                          34.0  25.1  21.4  29.0
-//   256 of 151936, unfiltered                    45.8  57.5  79.1   123
-//   480 of 151936, top-p                         89.1   107   147   241
+//   1 row of 32000, top-k 40, top-p, min-p        8.0   8.3   7.8   7.9
+//   7 of 100003, 0.9 forbidden, top-p            36.0  24.8  17.6  13.9
+//   16 of 151936, top-k 20, top-p                30.4  21.6  14.8  14.2
+//   64 of 151936, mixed                          34.3  25.2  21.4  29.1
+//   256 of 151936, unfiltered                    46.1  57.9  79.2   123
+//   480 of 151936, top-p                         89.8   108   148   242
 cudaError_t launch_sample(const SampleParams &p, cudaStream_t s) {
   static std::atomic<int> cached[64];  // SMs by device, 0 until looked up
   int dev = 0;
