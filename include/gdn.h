@@ -43,6 +43,8 @@
  *    a DEVICE pointer on the current CUDA device, owned by the caller, 16-byte
  *    aligned, to densely packed row-major storage in the layout stated.
  *    The library never allocates device memory and never frees caller memory.
+ *  - Arrays that a call writes overlap none of its other arrays, except where the
+ *    call says that they may.
  *  - bf16 tensors are passed as gdn_bf16 (the raw 16-bit pattern).
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream).  Every call
  *    only enqueues work; none synchronises the host except gdn_get_status.

@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstring>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -115,6 +116,25 @@ int fill_layers(CommitParams &p, int n_layers, float *const *state, gdn_bf16 *co
     if (!aligned((ptr), (align)))                                                            \
       return fail(GDN_ERR_MISALIGNED, "%s is not %d-byte aligned", #ptr, int(align));        \
   } while (0)
+
+// An array of a call, and whether the call writes it.
+struct Span {
+  const char *name;
+  const void *p;
+  size_t bytes;
+  bool written;
+};
+
+// Refuses an array that is written and lies over another one.
+int check_apart(const char *call, std::initializer_list<Span> spans) {
+  for (const Span *a = spans.begin(); a != spans.end(); ++a)
+    for (const Span *b = spans.begin(); b != a; ++b) {
+      const char *x = static_cast<const char *>(a->p), *y = static_cast<const char *>(b->p);
+      if ((a->written || b->written) && x && y && x < y + b->bytes && y < x + a->bytes)
+        return fail(GDN_ERR_INVALID_ARG, "%s: %s and %s overlap", call, b->name, a->name);
+    }
+  return GDN_OK;
+}
 
 int cuda_fail(cudaError_t e, const char *what) {
   return fail(GDN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -552,6 +572,11 @@ __attribute__((visibility("default"))) int gdn_accept_sampled(
   const size_t need = accept_sampled_workspace_bytes(B, T);
   if (ws_bytes < need)
     return fail(GDN_ERR_WORKSPACE, "sampled acceptance workspace has %zu bytes, needs %zu", ws_bytes, need);
+  // what a row's last position compares with the drafts, and the drafts
+  const size_t rows = size_t(B) * 4;
+  if ((rc = check_apart("gdn_accept_sampled", {{"draft", draft, rows * T, false}, {"keep", keep, rows, true}, {"next", next, rows, true},
+                                               {"token", token, rows * T, true}, {"ws", ws, need, true}})))
+    return rc;
   p.draft = draft, p.keep = keep, p.next = next;
   p.ws_token = static_cast<int32_t *>(ws);
   p.ws_count = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + align256(size_t(B) * T * sizeof(int32_t)));
@@ -631,6 +656,9 @@ int plan_call(const char *name, const gdn_kv4_dims *dims, int T, int N, const in
     GDN_NEED_PTR(slots, 4);
     GDN_NEED_PTR(positions, 4);
   }
+  // slots follow from the lengths after kv_len is written
+  const size_t rows = size_t(dims->B) * 4;
+  if (shared && (rc = check_apart(name, {{"lens", lens, rows, false}, {"kv_len", kv_len, rows, true}}))) return rc;
   KvPlanParams p{};
   p.lens = lens, p.add = add, p.active = active;
   p.held = held, p.table = table, p.free_list = free_list, p.free_count = free_count, p.refs = refs;
@@ -683,6 +711,13 @@ __attribute__((visibility("default"))) int gdn_kv_fork(const gdn_kv4_dims *dims,
   GDN_NEED_PTR(refs, 4);
   GDN_NEED_PTR(copy_src, 4);
   GDN_NEED_PTR(copy_dst, 4);
+  // what is written before the pairs' rows are read for the last time, and all else
+  const size_t pairs = size_t(n) * 4, pages = size_t(dims->n_pages) * 4, rows = size_t(dims->B) * 4;
+  if ((rc = check_apart("gdn_kv_fork", {{"src_rows", src_rows, pairs, false}, {"dst_rows", dst_rows, pairs, false}, {"lens", lens, pairs, false},
+                                        {"held", held, rows, true}, {"table", table, rows * dims->max_pages, true}, {"free_list", free_list, pages, false},
+                                        {"free_count", free_count, 4, true}, {"refs", refs, pages, true}, {"copy_src", copy_src, pairs, true},
+                                        {"copy_dst", copy_dst, pairs, true}})))
+    return rc;
   KvForkParams p{};
   p.src_rows = src_rows, p.dst_rows = dst_rows, p.lens = lens, p.held = held, p.table = table;
   p.free_list = free_list, p.free_count = free_count, p.refs = refs, p.copy_src = copy_src, p.copy_dst = copy_dst;
@@ -714,6 +749,16 @@ __attribute__((visibility("default"))) int gdn_kv_compact(
   GDN_NEED_PTR(copy_src, 4);
   GDN_NEED_PTR(copy_dst, 4);
   GDN_NEED_PTR(copy_count, 4);
+  // in place, or apart
+  const size_t pages = size_t(dims->n_pages) * 4, rows = size_t(dims->B) * 4, cells = rows * dims->max_pages;
+  const size_t moves = size_t(dims->n_pages > 1 ? dims->n_pages / 2 : 1) * 4;
+  const bool same_table = new_table == table, same_refs = new_refs == refs;
+  if ((rc = check_apart("gdn_kv_compact", {{"held", held, rows, false}, {"table", table, cells, same_table}, {"refs", refs, pages, same_refs},
+                                           {"new_table", same_table ? nullptr : new_table, cells, true}, {"new_refs", same_refs ? nullptr : new_refs, pages, true},
+                                           {"new_free_list", new_free_list, pages, true}, {"new_free_count", new_free_count, 4, true},
+                                           {"page_map", page_map, pages, true}, {"copy_src", copy_src, moves, true}, {"copy_dst", copy_dst, moves, true},
+                                           {"copy_count", copy_count, 4, true}})))
+    return rc;
   KvCompactParams p{};
   p.held = held, p.table = table, p.refs = refs, p.new_table = new_table, p.new_refs = new_refs;
   p.new_free_list = new_free_list, p.new_free_count = new_free_count, p.page_map = page_map;
